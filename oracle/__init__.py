@@ -13,10 +13,11 @@ Modules
   codebook  Lloyd iteration on the N(0,1) density -> centroids, thresholds, distortion
   hadamard  Sylvester / Paley Hadamard matrices, Kronecker H_K, SplitMix64 signs, rotation
   encode    rotate -> group RMS -> fp16 scale -> snap -> pack (bits or trits), unpack, dequant
+  attention rotary positions, attention over cached keys and values
   ops       qmv, gather_qmv, multi_gather_qmv, gather_qmm by their definitions
 
 Parity pins live in ``tests/test_oracle_*.py``. Every function here is pinned by at least
 one check that does not re-use its own formula; see the test files for which.
 """
 
-from . import codebook, hadamard, encode, ops  # noqa: F401
+from . import attention, codebook, hadamard, encode, ops  # noqa: F401

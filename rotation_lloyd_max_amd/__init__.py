@@ -21,7 +21,8 @@ __all__ = [
     "TqError", "QWeight", "lib", "codebook", "words_per_row", "signs", "encode", "fwht",
     "qmv", "gather_qmv", "multi_gather_qmv", "gather_qmm", "workspace_bytes", "dequant",
     "encode_stream", "multi_gather_qmv_static", "ExpertCache", "kv_fetch", "rotate_dense",
-    "encode_dense",
+    "encode_dense", "Rope", "rope_frequencies", "rope", "KVCache", "kv_cache", "kv_store",
+    "kv_load", "kv_attend", "kv_attend_workspace",
     "F32", "BF16", "F16", "X_ROTATED",
 ]
 
@@ -99,7 +100,7 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -m rotation_lloyd_max_amd.build`")
         handle = ctypes.CDLL(LIB_PATH)
-        for name, res, args in SIGNATURES:
+        for name, res, args in SIGNATURES + kv.SIGNATURES:
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args
@@ -555,3 +556,8 @@ class ExpertCache:
     def multi_gather_qmv(self, ids, X, **kw):
         sid, _ = self.fetch(ids)
         return multi_gather_qmv(self.pool, sid, X, **kw)
+
+
+from . import kv  # noqa: E402  (uses the names above)
+from .kv import (KVCache, Rope, kv_attend, kv_attend_workspace, kv_cache,  # noqa: E402
+                 kv_load, kv_store, rope, rope_frequencies)

@@ -106,6 +106,53 @@ hipError_t launch_gather_qmm(const WeightArgs& w, const void* x, int xdt, int64_
 bool kv_fetch_supported(int K, int levels);
 hipError_t launch_kv_fetch(const WeightArgs& w, int64_t rows, void* out, int odt, hipStream_t s);
 
+// A paged KV cache (tq_kv_cache), resolved on the host.
+struct KvHalf {
+  uint32_t* codes;
+  uint16_t* scales;
+  const uint32_t* signs;
+  int levels, bits, group, wpr;  // wpr: words per row
+};
+struct KvCacheArgs {
+  KvHalf k, v;
+  int D, heads, page;  // page: tokens of a page
+  int64_t pages;
+};
+struct RopeArgs {
+  const double* inv_freq;  // null: no rotary positions
+  const int32_t* positions;
+  int rot;
+  bool interleaved;
+  double gain;
+};
+hipError_t launch_rope(const void* x, int dt, int64_t tokens, int heads, int D, int64_t xts,
+                       int64_t xhs, const RopeArgs& r, bool transposed, void* out, int64_t ots,
+                       int64_t ohs, hipStream_t s);
+hipError_t launch_kv_store(const KvCacheArgs& c, const void* k, const void* v, int dt,
+                           int64_t tokens, const int64_t (&strides)[4], const int64_t* slots,
+                           const RopeArgs& r, hipStream_t s);
+hipError_t launch_kv_load(const KvCacheArgs& c, const int64_t* slots, int64_t tokens, void* k_out,
+                          void* v_out, int odt, hipStream_t s);
+struct AttendArgs {
+  KvCacheArgs c;
+  const void* q;
+  int qdt, q_heads;
+  int64_t q_stride;
+  int B;
+  const int32_t* q_offsets;
+  int64_t M;
+  const int32_t *kv_lens, *page_table;
+  int table_width;
+  const uint32_t* tree;
+  int tree_words;
+  float scale;
+  void* out;
+  int odt;
+  void* ws;
+};
+size_t kv_attend_workspace(const KvCacheArgs& c, int q_heads, int B, int64_t M);
+hipError_t launch_kv_attend(const AttendArgs& a, hipStream_t s);
+
 // Up to kMaxSlotIds int32 values passed by value to a kernel (tq_expert_cache_fetch).
 constexpr int kMaxSlotIds = 512;
 struct SlotIds {

@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "../../include/tq.h"
+#include "../../include/tq_kv.h"
 #include "internal.hpp"
 
 namespace tq {
@@ -262,6 +263,75 @@ int check_io(const void* x, int xdt, const void* y, int ydt, bool need) {
   if (!x || !y) return fail(TQ_ERR_ARG, "x and y must be non-NULL");
   if (!aligned(x, 16)) return fail(TQ_ERR_ALIGN, "x must be 16-byte aligned");
   if (!aligned(y, dtype_size(ydt))) return fail(TQ_ERR_ALIGN, "y misaligned for its dtype");
+  return TQ_OK;
+}
+
+// The two halves of a paged cache: their own limits on levels, group, head dimension and
+// pages (tq_kv_cache), the rest as any weight.
+int check_half(const tq_qweight& w, const char* name, int64_t rows, KvHalf* out) {
+  if (w.n_levels != 4 && w.n_levels != 8 && w.n_levels != 16 && w.n_levels != 256)
+    return fail(TQ_ERR_UNSUPPORTED, "cache %s: n_levels must be 4, 8, 16 or 256 (got %d)", name,
+                w.n_levels);
+  if (w.K != 64 && w.K != 128 && w.K != 256)
+    return fail(TQ_ERR_UNSUPPORTED, "cache %s: the head dimension must be 64, 128 or 256 (got %lld)",
+                name, static_cast<long long>(w.K));
+  if ((w.group != 32 && w.group != 64 && w.group != 128) || w.K % w.group != 0)
+    return fail(TQ_ERR_UNSUPPORTED,
+                "cache %s: group must be 32, 64 or 128 and divide the head dimension (got %d)",
+                name, w.group);
+  if (w.N != rows)
+    return fail(TQ_ERR_ARG, "cache %s: N must be heads * page_tokens = %lld (got %lld)", name,
+                static_cast<long long>(rows), static_cast<long long>(w.N));
+  if (w.E < 1 || w.E > 0x7fffffffll) return fail(TQ_ERR_ARG, "cache %s: pages out of range", name);
+  if (!w.codes || !w.scales || !w.signs)
+    return fail(TQ_ERR_ARG, "cache %s: codes, scales and signs must be non-NULL", name);
+  if (!aligned(w.codes, 16) || !aligned(w.scales, 8) || !aligned(w.signs, 4))
+    return fail(TQ_ERR_ALIGN, "cache %s: codes must be 16-byte, scales 8-byte and signs 4-byte aligned",
+                name);
+  out->codes = const_cast<uint32_t*>(w.codes);
+  out->scales = const_cast<uint16_t*>(w.scales);
+  out->signs = w.signs;
+  out->levels = w.n_levels;
+  out->bits = w.n_levels == 256 ? 8 : w.n_levels == 16 ? 4 : w.n_levels == 8 ? 3 : 2;
+  out->group = w.group;
+  out->wpr = static_cast<int>(w.K) * out->bits / 32;
+  return TQ_OK;
+}
+
+int check_cache(const tq_kv_cache* c, KvCacheArgs* out) {
+  if (!c) return fail(TQ_ERR_ARG, "cache descriptor is NULL");
+  if (c->heads < 1 || c->heads > 1024) return fail(TQ_ERR_ARG, "cache heads must be in [1, 1024]");
+  if (c->page_tokens < 16 || c->page_tokens > 65536 || c->page_tokens % 16 != 0)
+    return fail(TQ_ERR_ARG, "page_tokens must be a multiple of 16 in [16, 65536] (got %d)",
+                c->page_tokens);
+  const int64_t rows = static_cast<int64_t>(c->heads) * c->page_tokens;
+  int rc = check_half(c->k, "keys", rows, &out->k);
+  if (rc != TQ_OK) return rc;
+  rc = check_half(c->v, "values", rows, &out->v);
+  if (rc != TQ_OK) return rc;
+  if (c->k.K != c->v.K || c->k.E != c->v.E)
+    return fail(TQ_ERR_ARG, "cache keys and values differ in head dimension or pages");
+  out->D = static_cast<int>(c->k.K);
+  out->heads = c->heads;
+  out->page = c->page_tokens;
+  out->pages = c->k.E;
+  return TQ_OK;
+}
+
+int check_rope(const tq_rope_params* r, const int32_t* positions, int head_dim, RopeArgs* out) {
+  if (!r) return fail(TQ_ERR_ARG, "rope is NULL");
+  if (r->rot_dim < 2 || r->rot_dim > head_dim || r->rot_dim % 2 != 0)
+    return fail(TQ_ERR_ARG, "rot_dim must be even and in [2, head_dim] (got %d)", r->rot_dim);
+  if (r->interleaved != 0 && r->interleaved != 1)
+    return fail(TQ_ERR_ARG, "interleaved must be 0 or 1");
+  if (!r->inv_freq || !positions) return fail(TQ_ERR_ARG, "inv_freq and positions must be non-NULL");
+  if (!aligned(r->inv_freq, 8) || !aligned(positions, 4))
+    return fail(TQ_ERR_ALIGN, "inv_freq or positions misaligned");
+  out->inv_freq = r->inv_freq;
+  out->positions = positions;
+  out->rot = r->rot_dim;
+  out->interleaved = r->interleaved != 0;
+  out->gain = r->gain;
   return TQ_OK;
 }
 
@@ -718,6 +788,160 @@ int tq_gather_qmm_pair(const tq_qweight* w1, const tq_qweight* w2, const void* x
   return hip_status(launch_gather_qmm(a, x, x_dtype, T, row_token, expert_offsets, M, rotated, y,
                                       y_dtype, ws, static_cast<hipStream_t>(stream), &b),
                     "tq_gather_qmm_pair");
+}
+
+int tq_rope_frequencies(int32_t rot_dim, double base, int32_t scaling, double stretch,
+                        double original, double* inv_freq, double* gain) {
+  if (rot_dim < 2 || rot_dim > 1024 || rot_dim % 2 != 0)
+    return fail(TQ_ERR_ARG, "rot_dim must be even and in [2, 1024] (got %d)", rot_dim);
+  if (!(base > 0.0) || !std::isfinite(base)) return fail(TQ_ERR_ARG, "base must be positive");
+  if (!(stretch >= 1.0) || !std::isfinite(stretch)) return fail(TQ_ERR_ARG, "stretch must be at least 1");
+  if (scaling < TQ_ROPE_NONE || scaling > TQ_ROPE_YARN)
+    return fail(TQ_ERR_UNSUPPORTED, "unknown rope scaling %d", scaling);
+  if (scaling == TQ_ROPE_YARN && (!(original > 0.0) || !std::isfinite(original)))
+    return fail(TQ_ERR_ARG, "original must be positive");
+  if (scaling == TQ_ROPE_NTK && rot_dim == 2)
+    return fail(TQ_ERR_UNSUPPORTED, "NTK scaling needs rot_dim above 2");
+  if (!inv_freq || !gain) return fail(TQ_ERR_ARG, "inv_freq and gain must be non-NULL");
+  const double d = rot_dim;
+  const double b = scaling == TQ_ROPE_NTK ? base * std::pow(stretch, d / (d - 2.0)) : base;
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(b, -2.0 * i / d);
+    if (scaling == TQ_ROPE_LINEAR) f /= stretch;
+    if (scaling == TQ_ROPE_YARN) {
+      const double turns = original * f / (2.0 * M_PI);
+      const double g = std::fmin(std::fmax((turns - 1.0) / 31.0, 0.0), 1.0);
+      f *= g + (1.0 - g) / stretch;
+    }
+    inv_freq[i] = f;
+  }
+  *gain = scaling == TQ_ROPE_YARN ? 0.1 * std::log(stretch) + 1.0 : 1.0;
+  return TQ_OK;
+}
+
+int tq_rope(const void* x, tq_dtype dtype, int64_t tokens, int32_t heads, int32_t head_dim,
+            int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions,
+            const tq_rope_params* rope, uint32_t flags, void* out, int64_t out_token_stride,
+            int64_t out_head_stride, void* stream) {
+  if (!valid_dtype(dtype)) return fail(TQ_ERR_ARG, "bad dtype");
+  if (head_dim < 2 || head_dim > 1024 || head_dim % 2 != 0)
+    return fail(TQ_ERR_UNSUPPORTED, "head_dim must be even and in [2, 1024] (got %d)", head_dim);
+  if (tokens < 0 || tokens > (1 << 30) || heads < 0 || heads > 65536)
+    return fail(TQ_ERR_ARG, "tokens must be in [0, 2^30] and heads in [0, 65536]");
+  if (flags & ~static_cast<uint32_t>(TQ_ROPE_TRANSPOSED)) return fail(TQ_ERR_ARG, "unknown flags");
+  if (tokens == 0 || heads == 0) return TQ_OK;
+  if (!x || !out) return fail(TQ_ERR_ARG, "x and out must be non-NULL");
+  if (!aligned(x, dtype_size(dtype)) || !aligned(out, dtype_size(dtype)))
+    return fail(TQ_ERR_ALIGN, "x or out misaligned for its dtype");
+  if (x == out && (x_token_stride != out_token_stride || x_head_stride != out_head_stride))
+    return fail(TQ_ERR_ARG, "in place, x and out must have the same strides");
+  if ((tokens > 1 && out_token_stride == 0) || (heads > 1 && out_head_stride == 0))
+    return fail(TQ_ERR_ARG, "out must not overlap itself");
+  RopeArgs r{};
+  const int rc = check_rope(rope, positions, head_dim, &r);
+  if (rc != TQ_OK) return rc;
+  return hip_status(launch_rope(x, dtype, tokens, heads, head_dim, x_token_stride, x_head_stride, r,
+                                (flags & TQ_ROPE_TRANSPOSED) != 0, out, out_token_stride,
+                                out_head_stride, static_cast<hipStream_t>(stream)),
+                    "tq_rope");
+}
+
+int tq_kv_store(const tq_kv_cache* cache, const void* k, const void* v, tq_dtype dtype,
+                int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,
+                const tq_rope_params* rope, const int32_t* positions, void* stream) {
+  KvCacheArgs c{};
+  int rc = check_cache(cache, &c);
+  if (rc != TQ_OK) return rc;
+  if (!valid_dtype(dtype)) return fail(TQ_ERR_ARG, "bad dtype");
+  if (tokens < 0 || tokens > (1 << 30)) return fail(TQ_ERR_ARG, "tokens must be in [0, 2^30]");
+  if (tokens == 0) return TQ_OK;
+  if (!k || !v || !slots) return fail(TQ_ERR_ARG, "k, v and slots must be non-NULL");
+  if (!aligned(k, dtype_size(dtype)) || !aligned(v, dtype_size(dtype)) || !aligned(slots, 8))
+    return fail(TQ_ERR_ALIGN, "k, v or slots misaligned");
+  RopeArgs r{};
+  if (rope) {
+    rc = check_rope(rope, positions, c.D, &r);
+    if (rc != TQ_OK) return rc;
+  }
+  const int64_t strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
+  return hip_status(launch_kv_store(c, k, v, dtype, tokens, strides, slots, r,
+                                    static_cast<hipStream_t>(stream)),
+                    "tq_kv_store");
+}
+
+int tq_kv_load(const tq_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k_out,
+               void* v_out, tq_dtype dtype, void* stream) {
+  KvCacheArgs c{};
+  const int rc = check_cache(cache, &c);
+  if (rc != TQ_OK) return rc;
+  if (!valid_dtype(dtype)) return fail(TQ_ERR_ARG, "bad dtype");
+  if (tokens < 0 || tokens > (1 << 30)) return fail(TQ_ERR_ARG, "tokens must be in [0, 2^30]");
+  if (tokens == 0 || (!k_out && !v_out)) return TQ_OK;
+  if (!slots) return fail(TQ_ERR_ARG, "slots is NULL");
+  if (!aligned(slots, 8)) return fail(TQ_ERR_ALIGN, "slots misaligned");
+  if (!aligned(k_out, 16) || !aligned(v_out, 16))
+    return fail(TQ_ERR_ALIGN, "k_out and v_out must be 16-byte aligned");
+  return hip_status(launch_kv_load(c, slots, tokens, k_out, v_out, dtype,
+                                   static_cast<hipStream_t>(stream)),
+                    "tq_kv_load");
+}
+
+namespace {
+int check_attend_shape(const KvCacheArgs& c, int32_t q_heads, int32_t B, int64_t M) {
+  if (q_heads < 1 || q_heads > 65536 || q_heads % c.heads != 0)
+    return fail(TQ_ERR_ARG, "q_heads must be a multiple of the cache's %d heads, at most 65536 (got %d)",
+                c.heads, q_heads);
+  if (B < 0 || B > 65536) return fail(TQ_ERR_ARG, "B must be in [0, 65536]");
+  if (M < 0 || M > (1 << 24)) return fail(TQ_ERR_ARG, "M must be in [0, 2^24]");
+  return TQ_OK;
+}
+}  // namespace
+
+size_t tq_kv_attend_workspace(const tq_kv_cache* cache, int32_t q_heads, int32_t B, int64_t M) {
+  KvCacheArgs c{};
+  if (check_cache(cache, &c) != TQ_OK || check_attend_shape(c, q_heads, B, M) != TQ_OK)
+    return SIZE_MAX;
+  return kv_attend_workspace(c, q_heads, B, M);
+}
+
+int tq_kv_attend(const tq_kv_cache* cache, const void* q, tq_dtype q_dtype, int32_t q_heads,
+                 int64_t q_token_stride, int32_t B, const int32_t* q_offsets, int64_t M,
+                 const int32_t* kv_lens, const int32_t* page_table, int32_t table_width,
+                 const uint32_t* tree, int32_t tree_words, float scale, void* out,
+                 tq_dtype out_dtype, void* ws, size_t ws_bytes, void* stream) {
+  AttendArgs a{};
+  int rc = check_cache(cache, &a.c);
+  if (rc != TQ_OK) return rc;
+  rc = check_attend_shape(a.c, q_heads, B, M);
+  if (rc != TQ_OK) return rc;
+  if ((q_dtype != TQ_BF16 && q_dtype != TQ_F16) || (out_dtype != TQ_BF16 && out_dtype != TQ_F16))
+    return fail(TQ_ERR_UNSUPPORTED, "tq_kv_attend takes bf16 or fp16 queries and outputs");
+  if (table_width < 0) return fail(TQ_ERR_ARG, "table_width must be >= 0");
+  if (tree ? tree_words < 1 || tree_words > 65536 : tree_words != 0)
+    return fail(TQ_ERR_ARG, "tree_words must be in [1, 65536] with a tree and 0 without");
+  if (static_cast<int64_t>(table_width) * a.c.page > 0x7fffffffll - 65536)
+    return fail(TQ_ERR_ARG, "table_width * page_tokens must be below 2^31 - 65536");
+  if (B == 0 || M == 0) return TQ_OK;
+  if (!q || !out || !kv_lens || (table_width > 0 && !page_table))
+    return fail(TQ_ERR_ARG, "q, out, kv_lens and page_table must be non-NULL");
+  if (!q_offsets && M % B != 0)
+    return fail(TQ_ERR_ARG, "without q_offsets B must divide M");
+  if (!std::isfinite(scale)) return fail(TQ_ERR_ARG, "scale must be finite");
+  if (!aligned(q, 16) || q_token_stride % 8 != 0 || !aligned(out, 16))
+    return fail(TQ_ERR_ALIGN, "q and its rows, and out, must be 16-byte aligned");
+  if (!aligned(kv_lens, 4) || (page_table && !aligned(page_table, 4)) ||
+      (q_offsets && !aligned(q_offsets, 4)) || (tree && !aligned(tree, 4)))
+    return fail(TQ_ERR_ALIGN, "kv_lens, page_table, q_offsets or tree misaligned");
+  const size_t need = kv_attend_workspace(a.c, q_heads, B, M);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(TQ_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", need, ws_bytes);
+  if (need > 0 && !aligned(ws, 256)) return fail(TQ_ERR_ALIGN, "workspace must be 256-byte aligned");
+  a.q = q; a.qdt = q_dtype; a.q_heads = q_heads; a.q_stride = q_token_stride; a.B = B;
+  a.q_offsets = q_offsets; a.M = M; a.kv_lens = kv_lens; a.page_table = page_table;
+  a.table_width = table_width; a.tree = tree; a.tree_words = tree_words; a.scale = scale;
+  a.out = out; a.odt = out_dtype; a.ws = ws;
+  return hip_status(launch_kv_attend(a, static_cast<hipStream_t>(stream)), "tq_kv_attend");
 }
 
 // ---- expert cache ------------------------------------------------------------------------

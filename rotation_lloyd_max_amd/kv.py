@@ -1,0 +1,290 @@
+"""Binding of include/tq_kv.h: rotary positions, and the paged compressed KV cache with its
+write, read-back and attention. Argument marshalling only, like the package's other calls.
+
+These calls run once per layer and decoded token, so what a call does on the host is kept
+short: the cache's descriptor is checked and built once, in KVCache, and the device guard
+is entered only where the tensors' device is not the current one.
+"""
+
+import ctypes
+from dataclasses import dataclass
+
+import numpy as np
+import torch
+
+import rotation_lloyd_max_amd as _tq
+
+_P, _I32, _I64, _U32, _SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32,
+                             ctypes.c_size_t)
+_INT, _F32, _F64 = ctypes.c_int, ctypes.c_float, ctypes.c_double
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = [("k", _tq._QWeight), ("v", _tq._QWeight),
+                ("heads", ctypes.c_int32), ("page_tokens", ctypes.c_int32)]
+
+
+class _RopeParams(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("gain", ctypes.c_double)]
+
+
+_KV, _RP = ctypes.POINTER(_KVCache), ctypes.POINTER(_RopeParams)
+
+# (name, restype, argtypes) for every function declared in include/tq_kv.h
+SIGNATURES = [
+    ("tq_rope_frequencies", _INT, [_I32, _F64, _I32, _F64, _F64, _P, _P]),
+    ("tq_rope", _INT, [_P, _INT, _I64, _I32, _I32, _I64, _I64, _P, _RP, _U32, _P, _I64, _I64, _P]),
+    ("tq_kv_store", _INT, [_KV, _P, _P, _INT, _I64, _I64, _I64, _I64, _I64, _P, _RP, _P, _P]),
+    ("tq_kv_load", _INT, [_KV, _P, _I64, _P, _P, _INT, _P]),
+    ("tq_kv_attend", _INT, [_KV, _P, _INT, _I32, _I64, _I32, _P, _I64, _P, _P, _I32, _P, _I32, _F32,
+                            _P, _INT, _P, _SZ, _P]),
+    ("tq_kv_attend_workspace", _SZ, [_KV, _I32, _I32, _I64]),
+]
+
+ROPE_SCALING = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}
+_TRANSPOSED = 1
+_BITS = {4: 2, 8: 3, 16: 4, 256: 8}
+
+
+def _call(device, fn, *args):
+    """fn(*args, stream) on `device`'s current stream, with that device current."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be on a GPU, not on {device}")
+    if device.index == torch.cuda.current_device():
+        _tq._check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _tq._check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+def _as(t, dtype, device, name, shape=None):
+    """t as a contiguous tensor of dtype on device (the call's index arrays)."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        if t.dtype.is_floating_point or t.dtype.is_complex or t.dtype == torch.bool:
+            raise TypeError(f"{name} must hold integers, got {t.dtype}")
+        t = t.to(dtype)
+    return t if t.is_contiguous() else t.contiguous()
+
+
+@dataclass
+class Rope:
+    """Rotary positions: inv_freq float64 [rot_dim / 2] on the device (radians per position),
+    pairs (i, i + rot_dim / 2) or, interleaved, (2i, 2i + 1), the turned pair scaled by gain."""
+    inv_freq: torch.Tensor
+    rot_dim: int
+    interleaved: bool = False
+    gain: float = 1.0
+
+    def desc(self, device):
+        f = self.inv_freq
+        if f.dtype != torch.float64 or f.numel() * 2 != self.rot_dim or not f.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous float64 tensor of rot_dim / 2 elements")
+        if f.device != device:
+            raise ValueError(f"inv_freq is on {f.device}, the call runs on {device}")
+        return _RopeParams(f.data_ptr(), self.rot_dim, 1 if self.interleaved else 0, self.gain)
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling=None, stretch=1.0, original=4096,
+                     interleaved=False, device="cuda"):
+    """A Rope of the frequencies base^(-2i / rot_dim), stretched for texts `stretch` times as
+    long as `original` positions: scaling None, "linear", "ntk" or "yarn" (see tq_kv.h)."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {list(ROPE_SCALING)}")
+    f = np.zeros(max(1, rot_dim // 2), dtype=np.float64)
+    gain = ctypes.c_double(1.0)
+    _tq._check(_tq.lib().tq_rope_frequencies(rot_dim, base, ROPE_SCALING[scaling], stretch,
+                                             original, f.ctypes.data, ctypes.addressof(gain)))
+    return Rope(torch.from_numpy(f).to(device), rot_dim, interleaved, gain.value)
+
+
+def _head_strides(t, name):
+    """(token, head) strides of a [tokens, heads, dim] tensor with contiguous heads."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    s = t.stride()
+    if s[2] != 1 and t.shape[2] > 1:
+        raise ValueError(f"the elements of a head of {name} must be contiguous")
+    return s[0], s[1]
+
+
+def _overlaps_itself(t):
+    """Whether two (token, head) vectors of t can share an element."""
+    (n, h, d), (a, b, _) = t.shape, t.stride()
+    if n * h <= 1:
+        return False
+    if n == 1:
+        return b < d
+    if h == 1:
+        return a < d
+    inner, outer, count = (b, a, h) if b <= a else (a, b, n)
+    return inner < d or outer < inner * (count - 1) + d
+
+
+def rope(x, positions, rope, transposed=False, out=None):
+    """x ([tokens, heads, head_dim], the elements of a head contiguous, any token and head
+    strides) with rotary positions applied. out=x turns it in place; another out= must not
+    overlap x. transposed: the negative angle (the gradient of the call)."""
+    xs = _head_strides(x, "x")
+    dev = x.device
+    positions = _as(positions, torch.int32, dev, "positions", (x.shape[0],))
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev:
+        raise ValueError("out= must have x's shape, dtype and device")
+    elif _overlaps_itself(out):
+        raise ValueError("out= must not overlap itself")
+    os_ = _head_strides(out, "out")
+    r = rope.desc(dev)
+    _call(dev, _tq.lib().tq_rope, x.data_ptr(), _tq._dt(x), x.shape[0], x.shape[1], x.shape[2],
+          xs[0], xs[1], positions.data_ptr(), r, _TRANSPOSED if transposed else 0, out.data_ptr(),
+          os_[0], os_[1])
+    return out
+
+
+class KVCache:
+    """A paged compressed cache: k and v are QWeights of E = pages experts of N = heads *
+    page_tokens rows of head_dim K; row h * page_tokens + t of a page is its token t of head h.
+    Slot page * page_tokens + t names a token's place. The handle is of the tensors that k
+    and v held when it was made."""
+
+    def __init__(self, k, v, heads, page_tokens):
+        # the library reads and writes E * N rows through a half's pointers: its tensors must
+        # hold them, on one device
+        self.device = dev = k.codes.device
+        self._keep = (k.codes, k.scales, k.signs, v.codes, v.scales, v.signs)
+        for name, w in (("k", k), ("v", v)):
+            rows, codes, scales, sg = w.E * w.N, w.codes, w.scales, w.signs
+            if (codes.dtype != torch.int32 or codes.numel() * 32 != rows * w.K * _BITS.get(w.levels, 0)
+                    or not codes.is_contiguous()):
+                raise ValueError(f"{name}.codes must be a contiguous int32 tensor of {rows} packed rows")
+            if (scales.dtype != torch.float16 or scales.numel() * w.group != rows * w.K
+                    or not scales.is_contiguous()):
+                raise ValueError(f"{name}.scales must be a contiguous float16 tensor of {rows} rows "
+                                 "of K / group scales")
+            if sg.dtype != torch.int32 or sg.numel() * 32 < w.K or not sg.is_contiguous():
+                raise ValueError(f"{name}.signs must hold {w.K} sign bits")
+            if codes.device != dev or scales.device != dev or sg.device != dev:
+                raise ValueError(f"the tensors of a cache must be on one device ({name} is not on {dev})")
+        self.k, self.v, self.heads, self.page_tokens = k, v, heads, page_tokens
+        self.head_dim = k.K
+        self.desc = _KVCache(k.desc(), v.desc(), heads, page_tokens)
+
+
+def kv_cache(pages, heads, head_dim, page_tokens=64, k_levels=256, v_levels=8, k_group=64,
+             v_group=64, k_seed=0, v_seed=0, device="cuda"):
+    """A KVCache of zero rows."""
+    halves = []
+    for levels, group, seed in ((k_levels, k_group, k_seed), (v_levels, v_group, v_seed)):
+        rows = heads * page_tokens
+        codes = torch.zeros((pages, rows, _tq.words_per_row(head_dim, levels)), dtype=torch.int32,
+                            device=device)
+        scales = torch.zeros((pages, rows, head_dim // group), dtype=torch.float16, device=device)
+        with torch.cuda.device(codes.device):
+            sg = _tq.signs(seed, head_dim, codes.device)
+        halves.append(_tq.QWeight(codes, scales, sg, levels, group, head_dim, rows, pages, seed))
+    return KVCache(halves[0], halves[1], heads, page_tokens)
+
+
+def kv_store(cache, k, v, slots, rope=None, positions=None):
+    """Quantize the new tokens' keys and values ([tokens, heads, head_dim], the elements of a
+    head contiguous) into their slots of the cache (a slot outside it, such as -1, is skipped;
+    each other one at most once); with rope, the keys are turned at `positions` first."""
+    dev = cache.device
+    n = k.shape[0]
+    shape = (n, cache.heads, cache.head_dim)
+    if tuple(k.shape) != shape or tuple(v.shape) != shape or v.dtype != k.dtype:
+        raise ValueError(f"k and v must be [tokens, {cache.heads}, {cache.head_dim}] of one dtype")
+    if k.device != dev or v.device != dev:
+        raise ValueError(f"k and v must be on the cache's device {dev}")
+    ks, vs = _head_strides(k, "k"), _head_strides(v, "v")
+    slots = _as(slots, torch.int64, dev, "slots", (n,))
+    r = pos = None
+    if rope is not None:
+        if positions is None:
+            raise ValueError("rope needs the tokens' positions")
+        positions = _as(positions, torch.int32, dev, "positions", (n,))
+        r, pos = rope.desc(dev), positions.data_ptr()
+    _call(dev, _tq.lib().tq_kv_store, cache.desc, k.data_ptr(), v.data_ptr(), _tq._dt(k), n, ks[0],
+          ks[1], vs[0], vs[1], slots.data_ptr(), r, pos)
+
+
+def kv_load(cache, slots, out_dtype=torch.bfloat16, k_out=None, v_out=None, keys=True, values=True):
+    """(keys, values) of the tokens in `slots`, [tokens, heads, head_dim] each, dequantized and
+    rotated back; a slot outside the cache gives NaN rows. keys=False or values=False leaves
+    that half out (None)."""
+    dev = cache.device
+    slots = _as(slots, torch.int64, dev, "slots", (slots.numel(),))
+    shape = (slots.numel(), cache.heads, cache.head_dim)
+    for o in (k_out, v_out):
+        if o is not None and o.dtype != out_dtype:
+            raise ValueError(f"k_out= and v_out= must be {out_dtype}")
+    k = _tq._out(k_out, shape, out_dtype, dev) if keys else None
+    v = _tq._out(v_out, shape, out_dtype, dev) if values else None
+    if out_dtype not in _tq._DT:
+        raise TypeError(f"unsupported dtype {out_dtype}")
+    _call(dev, _tq.lib().tq_kv_load, cache.desc, slots.data_ptr(), shape[0],
+          k.data_ptr() if keys else None, v.data_ptr() if values else None, _tq._DT[out_dtype])
+    return k, v
+
+
+def kv_attend_workspace(cache, q_heads, seqs, rows):
+    """Bytes of workspace kv_attend needs for `rows` queries of `seqs` sequences."""
+    n = _tq.lib().tq_kv_attend_workspace(cache.desc, q_heads, seqs, rows)
+    if n == ctypes.c_size_t(-1).value:
+        raise _tq.TqError(-1, _tq.lib().tq_last_error().decode())
+    return n
+
+
+def kv_attend(cache, q, kv_lens, page_table, q_offsets=None, tree=None, scale=None,
+              out_dtype=None, out=None, ws=None):
+    """Attention of q ([M, q_heads, head_dim], bf16 or fp16, the heads of a row contiguous)
+    over the cache: sequence b has kv_lens[b] tokens in the pages page_table[b], the last of
+    them its queries' own; q_offsets [B + 1] bounds the sequences' rows of q (None: M / B rows
+    each). Causal, or with tree (int32 words [M, words]) bit j of a row's mask for each of the
+    sequence's own tokens j. scale: 1 / sqrt(head_dim) by default. Returns [M, q_heads,
+    head_dim] in out_dtype (q's by default)."""
+    dev = cache.device
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q must be [M, q_heads, {cache.head_dim}]")
+    M, H, D = q.shape
+    stride = q.stride()
+    if stride[2] != 1 or (H > 1 and stride[1] != D):
+        raise ValueError("the heads of a query row must be contiguous")
+    if q.device != dev:
+        raise ValueError(f"q is on {q.device}, the cache on {dev}")
+    B = kv_lens.numel()
+    kv_lens = _as(kv_lens, torch.int32, dev, "kv_lens", (B,))
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [sequences, pages of a sequence]")
+    width = page_table.shape[1]
+    page_table = _as(page_table, torch.int32, dev, "page_table", (B, width))
+    if q_offsets is not None:
+        q_offsets = _as(q_offsets, torch.int32, dev, "q_offsets", (B + 1,))
+    words = 0
+    if tree is not None:
+        if tree.dim() != 2 or tree.dtype != torch.int32:
+            raise ValueError("tree must be int32 words [M, words]")
+        words = tree.shape[1]
+        tree = _as(tree, torch.int32, dev, "tree", (M, words))
+    if out is None:
+        out = torch.empty((M, H, D), dtype=out_dtype or q.dtype, device=dev)
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out= must be {out_dtype}")
+        out = _tq._out(out, (M, H, D), out.dtype, dev)
+    nbytes = kv_attend_workspace(cache, H, B, M)
+    if ws is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    elif ws.device != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < nbytes:
+        raise ValueError(f"ws= must be a contiguous tensor of at least {nbytes} bytes on {dev}")
+    _call(dev, _tq.lib().tq_kv_attend, cache.desc, q.data_ptr(), _tq._dt(q), H,
+          stride[0] if M > 1 else H * D, B, q_offsets.data_ptr() if q_offsets is not None else None, M,
+          kv_lens.data_ptr(), page_table.data_ptr(), width,
+          tree.data_ptr() if tree is not None else None, words, D ** -0.5 if scale is None else scale,
+          out.data_ptr(), _tq._dt(out), ws.data_ptr() if ws is not None else None, nbytes)
+    return out
