@@ -15,7 +15,8 @@ LIB = os.path.join(HERE, "libtq.so")
 SOURCES = ["tq_api.cpp", "rotate.hip", "encode.hip", "encode_p2.hip", "encode_m.hip", "qmv.hip", "qmv_16.hip", "qmv_8.hip",
            "qmv_4.hip", "qmv_3.hip", "rot16.hip", "multi_gather.hip", "gather_qmm.hip",
            "dequant.hip", "slot_ids.hip", "kv_fetch.hip", "dense.hip", "rope.hip",
-           "kv_store.hip", "kv_load.hip", "kv_attend.hip"]
+           "kv_store.hip", "kv_load.hip", "kv_attend.hip", "kv_attend_2.hip",
+           "kv_attend_3.hip", "kv_attend_4.hip", "kv_attend_8.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++20", "-fPIC",

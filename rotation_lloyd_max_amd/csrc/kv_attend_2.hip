@@ -1,0 +1,8 @@
+// Attention kernels for keys of 2 bits.
+#include "kv_attend.hpp"
+
+namespace tq {
+
+template hipError_t at_launch_k<2>(const AttendParams& p, int R, hipStream_t s);
+
+}  // namespace tq

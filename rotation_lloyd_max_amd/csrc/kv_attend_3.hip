@@ -1,0 +1,8 @@
+// Attention kernels for keys of 3 bits.
+#include "kv_attend.hpp"
+
+namespace tq {
+
+template hipError_t at_launch_k<3>(const AttendParams& p, int R, hipStream_t s);
+
+}  // namespace tq

@@ -1,0 +1,8 @@
+// Attention kernels for keys of 4 bits.
+#include "kv_attend.hpp"
+
+namespace tq {
+
+template hipError_t at_launch_k<4>(const AttendParams& p, int R, hipStream_t s);
+
+}  // namespace tq

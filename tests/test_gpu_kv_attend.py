@@ -3,8 +3,9 @@ fp64, from the codes that the GPU stored.
 
 Bound per query row and head, in the 2-norm (the rotations keep it), with u = 2^-11, half a step
 of fp16, the type of the matrix cores' operands:
-  scores    rotated q and the centroid rounded to fp16, fp32 sums: |ds_j| <= E_j = |scale| ((2 u +
-            (D + 16) 2^-24) sum_d |q'_d k'_jd| + 2^-19 max|q'| sum_d |k'_jd|) + 2^-21 |s_j|
+  scores    rotated q, the key's centroid and its product with the scale rounded to fp16, fp32
+            sums: |ds_j| <= E_j = |scale| ((3 u + (D + 16) 2^-24) sum_d |q'_d k'_jd| +
+            2^-19 max|q'| sum_d |k'_jd|) + 2^-21 |s_j|
             (the last terms: the fp32 transform of q and the exponent's argument)
   weights   p_j off by a factor within e^(2 max E), and u + 2^-19 from the rounding of p and exp
   values    the centroid and its product with the scale rounded to fp16: 2 u
@@ -99,7 +100,7 @@ def check(got, bt, q, counts, scale, tree=None, only=None):
                         continue
                     kk, vv, pp = kp[mask], vp[mask], p[mask]
                     s = scale * (kk @ qr[m, h])
-                    E = abs(scale) * ((2 * U + (D + 16) * 2.0 ** -24) * (np.abs(kk) @ np.abs(qr[m, h]))
+                    E = abs(scale) * ((3 * U + (D + 16) * 2.0 ** -24) * (np.abs(kk) @ np.abs(qr[m, h]))
                                       + 2.0 ** -19 * np.abs(qr[m, h]).max() * np.abs(kk).sum(1)) + 2.0 ** -21 * np.abs(s)
                     rel = np.expm1(2 * E.max()) + 3 * U + 2.0 ** -18 + len(s) * 2.0 ** -24
                     room = rel * np.linalg.norm(pp @ np.abs(vv)) + HALF_STEP[got.dtype] * np.linalg.norm(want) * 1.01 + 1e-7
