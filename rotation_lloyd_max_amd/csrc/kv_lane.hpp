@@ -5,7 +5,9 @@
 // Lane L of a row holds chunk  c = L ^ 3 * ((L >> 2) & 1).  With that order the partner of a
 // Sylvester stage on chunk bit 0, 1, 2, 3 is the lane L ^ 1, L ^ 2, L ^ 7, L ^ 8, and each of
 // those moves is one DPP operand (quad permutations, half-row mirror, row rotation by 8), no
-// LDS traffic; only bit 4 (D = 256) goes through a swizzle. Lanes whose chunks share a group of 32,
+// LDS traffic; bits 4 and 5 are the row and half-wave swaps of gfx950 (v_permlane16_swap and
+// v_permlane32_swap: with both operands x they give the lower rows' x in one result and the upper
+// rows' in the other, for both partners). Lanes whose chunks share a group of 32,
 // 64 or 128 elements are closed under {1, 2}, {1, 2, 7}, {1, 2, 7, 8}.
 #pragma once
 
@@ -15,15 +17,11 @@ namespace tq {
 
 __device__ __forceinline__ int kv_chunk(int L) { return L ^ (3 * ((L >> 2) & 1)); }
 
-// x of the partner lane for chunk bit B.
+// x of the partner lane for chunk bit B < 4.
 template <int B>
 __device__ __forceinline__ int kv_swap(int x) {
-  if constexpr (B == 4) {
-    return __builtin_amdgcn_ds_swizzle(x, 0x401f);  // lane ^ 16
-  } else {
-    constexpr int ctrl = B == 0 ? 0xB1 : B == 1 ? 0x4E : B == 2 ? 0x141 : 0x128;
-    return __builtin_amdgcn_update_dpp(0, x, ctrl, 0xf, 0xf, true);
-  }
+  constexpr int ctrl = B == 0 ? 0xB1 : B == 1 ? 0x4E : B == 2 ? 0x141 : 0x128;
+  return __builtin_amdgcn_update_dpp(0, x, ctrl, 0xf, 0xf, true);
 }
 template <int B>
 __device__ __forceinline__ float kv_swap(float x) {
@@ -33,6 +31,29 @@ template <int B>
 __device__ __forceinline__ double kv_swap(double x) {
   return __hiloint2double(kv_swap<B>(__double2hiint(x)), kv_swap<B>(__double2loint(x)));
 }
+// x of the lower and of the upper partner for chunk bit B = 4, 5, in both of them.
+template <int B>
+__device__ __forceinline__ void kv_both(uint32_t x, uint32_t& lower, uint32_t& upper) {
+  const auto r = B == 4 ? __builtin_amdgcn_permlane16_swap(x, x, false, false)
+                        : __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  lower = r[0];
+  upper = r[1];
+}
+template <int B>
+__device__ __forceinline__ void kv_both(float x, float& lower, float& upper) {
+  uint32_t a, b;
+  kv_both<B>(__float_as_uint(x), a, b);
+  lower = __uint_as_float(a);
+  upper = __uint_as_float(b);
+}
+template <int B>
+__device__ __forceinline__ void kv_both(double x, double& lower, double& upper) {
+  uint32_t a, b, c, d;
+  kv_both<B>(static_cast<uint32_t>(__double2loint(x)), a, b);
+  kv_both<B>(static_cast<uint32_t>(__double2hiint(x)), c, d);
+  lower = __hiloint2double(static_cast<int>(c), static_cast<int>(a));
+  upper = __hiloint2double(static_cast<int>(d), static_cast<int>(b));
+}
 
 __device__ __forceinline__ float kv_flip(float x, uint32_t m) {
   return __uint_as_float(__float_as_uint(x) ^ m);
@@ -41,15 +62,54 @@ __device__ __forceinline__ double kv_flip(double x, uint32_t m) {
   return __hiloint2double(__double2hiint(x) ^ static_cast<int>(m), __double2loint(x));
 }
 
-// One stage across lanes: the lower chunk keeps the sum, the upper partner - own.
-template <int B, typename T>
-__device__ __forceinline__ void kv_stage(T (&v)[8], int c) {
+// One stage across lanes: the lower chunk keeps the sum, the upper lower - upper.
+template <int B, int N, typename T>
+__device__ __forceinline__ void kv_stage(T (&v)[N], int c) {
   const uint32_t m = (c >> B) & 1 ? 0x80000000u : 0u;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const T o = kv_swap<B>(v[j]);
-    v[j] = o + kv_flip(v[j], m);
+  for (int j = 0; j < N; ++j) {
+    if constexpr (B < 4) {
+      const T o = kv_swap<B>(v[j]);
+      v[j] = o + kv_flip(v[j], m);
+    } else {
+      T lower, upper;
+      kv_both<B>(v[j], lower, upper);
+      v[j] = lower + kv_flip(upper, m);
+    }
   }
+}
+
+// The maximum over the wave, in every lane.
+__device__ __forceinline__ float kv_wave_max(float x) {
+  x = fmaxf(x, kv_swap<0>(x));
+  x = fmaxf(x, kv_swap<1>(x));
+  x = fmaxf(x, kv_swap<2>(x));
+  x = fmaxf(x, kv_swap<3>(x));
+  float a, b;
+  kv_both<4>(x, a, b);
+  kv_both<5>(fmaxf(a, b), a, b);
+  return fmaxf(a, b);
+}
+
+// The unnormalized Sylvester transform of a row of 64 N elements on a whole wave, lane L holding
+// elements N kv_chunk(L) + j.
+template <int N>
+__device__ __forceinline__ void kv_wave_transform(float (&v)[N], int c) {
+#pragma unroll
+  for (int s = 1; s < N; s <<= 1)
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (j & s) continue;
+      const float a = v[j], b = v[j | s];
+      v[j] = a + b;
+      v[j | s] = a - b;
+    }
+  kv_stage<0>(v, c);
+  kv_stage<1>(v, c);
+  kv_stage<2>(v, c);
+  kv_stage<3>(v, c);
+  kv_stage<4>(v, c);
+  kv_stage<5>(v, c);
 }
 
 // The unnormalized Sylvester transform of the row.
