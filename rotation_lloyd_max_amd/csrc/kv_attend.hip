@@ -5,42 +5,61 @@
 
 namespace tq {
 
-extern template hipError_t at_launch_k<2>(const AttendParams& p, int R, hipStream_t s);
-extern template hipError_t at_launch_k<3>(const AttendParams& p, int R, hipStream_t s);
-extern template hipError_t at_launch_k<4>(const AttendParams& p, int R, hipStream_t s);
-extern template hipError_t at_launch_k<8>(const AttendParams& p, int R, hipStream_t s);
+extern template hipError_t at_launch_k<2>(const AttendParams& p, int vbits, int D, int R, hipStream_t s);
+extern template hipError_t at_launch_k<3>(const AttendParams& p, int vbits, int D, int R, hipStream_t s);
+extern template hipError_t at_launch_k<4>(const AttendParams& p, int vbits, int D, int R, hipStream_t s);
+extern template hipError_t at_launch_k<8>(const AttendParams& p, int vbits, int D, int R, hipStream_t s);
 
 namespace {
 
 constexpr size_t kMetaBytes = sizeof(AttendMeta) * kAtMaxGrid;
 
-// 16-row blocks of a tile.
-int workgroups(int D, int R) { return (R == 1 && D <= 128 ? 3 : 2) * kAtCus; }
+// 16-row blocks of a tile, and the workgroups of a launch.
 int tile_blocks(int D, int share, int B, int64_t M) {
-  const int64_t rows = (M * share + B - 1) / (B > 0 ? B : 1);  // query rows per key head and sequence
+  const int64_t rows = (M * share + B - 1) / B;  // query rows per key head and sequence
   return rows <= 16 ? 1 : D == 256 ? 2 : 4;
 }
+int workgroups(int D, int R) { return (R == 1 && D <= 128 ? 3 : 2) * kAtCus; }
 
-// One wave per query row of a unit whose parts lie in several workgroups' slots, in the
+// What the join needs of the arguments.
+struct JoinParams {
+  const AttendMeta* meta;
+  const float* parts;
+  const uint32_t* vsigns;
+  uint16_t* out;
+  int q_heads, odt, rows;
+  uint32_t hb_mul;
+  int hb;
+  float inv_sqrt_d;
+};
+
+// One wave per query row of a unit whose parts lie in several workgroups' slots, added in the
 // order of the tokens.
 template <int D>
-__global__ __launch_bounds__(256) void k_attend_join(AttendParams p, int rows) {
+__global__ __launch_bounds__(256) void k_attend_join(JoinParams p) {
   constexpr int EL = D / 64;
   __shared__ float wt[4][kAtMaxGrid];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const AttendMeta m = p.meta[blockIdx.x];
   if (m.parts == 0) return;
-  const int r = blockIdx.y * 4 + wave, tk = r / p.hb, hd = r - tk * p.hb;
-  if (tk >= m.nrows || hd >= m.hb) return;
-  const int n = m.parts + 1;
-  const int64_t slot = static_cast<int64_t>(rows) * (D + 2);
-  auto part = [&](int i) { return p.parts + (2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * slot; };
-  float top = -__builtin_inff(), l = 0.f;
-  for (int i = lane; i < n; i += 64) top = fmaxf(top, part(i)[rows * D + r]);
+  const int r = blockIdx.y * 4 + wave, tk = (static_cast<uint32_t>(r) * p.hb_mul) >> 16, hd = r - tk * p.hb;
+  if (tk >= m.nrows || hd >= m.nh) return;
+  const int n = m.parts + 1, d0 = kv_chunk(lane) * EL;
+  const uint32_t sg = p.vsigns[d0 >> 5] >> (d0 & 31);
+  const int64_t slot = static_cast<int64_t>(p.rows) * (D + 2);
+  // part 0 is the second slot of its workgroup, the others the first of theirs
+  const float* const base = p.parts + 2 * static_cast<int64_t>(blockIdx.x) * slot;
+  auto part = [&](int i) { return base + (i == 0 ? slot : 2 * i * slot); };
+  float top = kAtNone, l = 0.f;
+  for (int i = lane; i < n; i += 64) {
+    const float a = part(i)[p.rows * D + r];
+    wt[wave][i] = a;
+    top = fmaxf(top, a);
+  }
   top = kv_wave_max(top);
   for (int i = lane; i < n; i += 64) {
-    const float a = part(i)[rows * D + r], b = part(i)[rows * D + rows + r];
-    const float f = a == -__builtin_inff() ? 0.f : at_exp2(a - top);
+    const float a = wt[wave][i], b = part(i)[p.rows * D + p.rows + r];
+    const float f = a == kAtNone ? 0.f : at_exp2(a - top);
     wt[wave][i] = f;
     l += b != b ? b : b * f;
   }
@@ -48,14 +67,20 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendParams p, int rows) {
   for (int x = 1; x < 64; x <<= 1) l += __shfl_xor(l, x);
   wave_lds_sync();
   float v[EL] = {};
-  for (int i = 0; i < n; ++i) {
-    const float f = wt[wave][i];
-    const float* s = part(i) + r * D + kv_chunk(lane) * EL;
+  const float* s = base + slot + r * D + d0;
 #pragma unroll
-    for (int e = 0; e < EL; ++e) v[e] += f == 0.f ? 0.f : f * s[e];
+  for (int e = 0; e < EL; ++e) v[e] = wt[wave][0] * s[e];
+  s = base + r * D + d0;
+#pragma unroll 8
+  for (int i = 1; i < n; ++i) {
+    const float f = wt[wave][i];
+#pragma unroll
+    for (int e = 0; e < EL; ++e) v[e] = __builtin_fmaf(f, s[2 * i * slot + e], v[e]);
   }
-  at_finish<D>(p, v, l, m.row0 + tk, m.head0 + hd, lane);
+  at_finish<D>(&p, v, l, static_cast<int64_t>(m.row0) + tk, m.head0 + hd, sg, lane);
 }
+
+uint32_t div_mul(uint32_t d) { return d == 1 ? 0 : static_cast<uint32_t>((0x100000000ull + d - 1) / d); }
 
 }  // namespace
 
@@ -68,17 +93,32 @@ size_t kv_attend_workspace(const KvCacheArgs& c, int q_heads, int B, int64_t M) 
 
 hipError_t launch_kv_attend(const AttendArgs& a, hipStream_t s) {
   AttendParams p{};
-  p.a = a;
+  const int D = a.c.D;
+  p.kcodes = a.c.k.codes; p.vcodes = a.c.v.codes; p.ksigns = a.c.k.signs; p.vsigns = a.c.v.signs;
+  p.kscales = a.c.k.scales; p.vscales = a.c.v.scales;
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.out = static_cast<uint16_t*>(a.out);
+  p.q_offsets = a.q_offsets; p.kv_lens = a.kv_lens; p.page_table = a.page_table; p.tree = a.tree;
+  p.q_stride = a.q_stride; p.qdt = a.qdt; p.odt = a.odt; p.q_heads = a.q_heads; p.B = a.B;
+  p.M = static_cast<int>(a.M); p.table_width = a.table_width; p.tree_words = a.tree_words;
+  p.heads = a.c.heads; p.pages = static_cast<int>(a.c.pages); p.page = a.c.page;
+  p.page16 = a.c.page / 16;
+  p.page_mul = div_mul(p.page16);
+  p.lg_kg = __builtin_ctz(a.c.k.group); p.lg_vg = __builtin_ctz(a.c.v.group);
+  p.lg_gk = __builtin_ctz(D / a.c.k.group); p.lg_gv = __builtin_ctz(D / a.c.v.group);
   p.share = a.q_heads / a.c.heads;
-  const int R = tile_blocks(a.c.D, p.share, a.B, a.M), rows = 16 * R;
+  const int R = tile_blocks(D, p.share, a.B, a.M), rows = 16 * R;
   p.hb = p.share < rows ? p.share : rows;
   p.nhb = (p.share + p.hb - 1) / p.hb;
   p.a_tok = rows / p.hb;
-  p.grid = workgroups(a.c.D, R);
+  p.hb_mul = (65536 + p.hb - 1) / p.hb;  // rows below 64: the product is exact
+  p.a_mul = div_mul(p.a_tok);
+  p.hu_n = a.c.heads * p.nhb;
+  p.cap = a.table_width * a.c.page;
   p.n_each = static_cast<int>(a.M / a.B);
-  p.inv_sqrt_d = static_cast<float>(1.0 / __builtin_sqrt(static_cast<double>(a.c.D)));
-  p.page16 = a.c.page / 16;
-  p.page_mul = p.page16 == 1 ? 0 : static_cast<uint32_t>((0x100000000ull + p.page16 - 1) / p.page16);
+  p.negate = a.scale < 0.f;
+  p.inv_sqrt_d = static_cast<float>(1.0 / __builtin_sqrt(static_cast<double>(D)));
+  p.c1 = __builtin_fabsf(a.scale) * 1.44269504f * p.inv_sqrt_d;
   p.meta = static_cast<AttendMeta*>(a.ws);
   p.parts = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kMetaBytes);
   for (int i = 0; i < 2; ++i) {
@@ -88,16 +128,17 @@ hipError_t launch_kv_attend(const AttendArgs& a, hipStream_t s) {
   }
   hipError_t e;
   switch (a.c.k.bits) {
-    case 2: e = at_launch_k<2>(p, R, s); break;
-    case 3: e = at_launch_k<3>(p, R, s); break;
-    case 4: e = at_launch_k<4>(p, R, s); break;
-    default: e = at_launch_k<8>(p, R, s); break;
+    case 2: e = at_launch_k<2>(p, a.c.v.bits, D, R, s); break;
+    case 3: e = at_launch_k<3>(p, a.c.v.bits, D, R, s); break;
+    case 4: e = at_launch_k<4>(p, a.c.v.bits, D, R, s); break;
+    default: e = at_launch_k<8>(p, a.c.v.bits, D, R, s); break;
   }
   if (e != hipSuccess) return e;
-  const dim3 grid(p.grid, rows / 4);
-  if (a.c.D == 64) hipLaunchKernelGGL((k_attend_join<64>), grid, dim3(256), 0, s, p, rows);
-  else if (a.c.D == 128) hipLaunchKernelGGL((k_attend_join<128>), grid, dim3(256), 0, s, p, rows);
-  else hipLaunchKernelGGL((k_attend_join<256>), grid, dim3(256), 0, s, p, rows);
+  JoinParams j{p.meta, p.parts, p.vsigns, p.out, p.q_heads, p.odt, rows, p.hb_mul, p.hb, p.inv_sqrt_d};
+  const dim3 grid(workgroups(D, R), rows / 4);
+  if (D == 64) hipLaunchKernelGGL((k_attend_join<64>), grid, dim3(256), 0, s, j);
+  else if (D == 128) hipLaunchKernelGGL((k_attend_join<128>), grid, dim3(256), 0, s, j);
+  else hipLaunchKernelGGL((k_attend_join<256>), grid, dim3(256), 0, s, j);
   return hipGetLastError();
 }
 

@@ -5,10 +5,11 @@
 //
 // Work. A unit is (sequence, key head, tile of up to 16 R query rows that share the head). All
 // units lie on one line of work, each as long as the tokens it reads plus a constant for its
-// set-up, cut into equal shares, one per workgroup: uneven lengths balance, and a few long
-// sequences still fill the chip. A share boundary inside a unit leaves partial sums in the
-// workspace, which k_attend_join adds up in a fixed order. Workgroups are small (four waves), so
-// that two or three share a CU and one's set-up hides behind another's stream.
+// set-up, cut into shares, one per workgroup: uneven lengths balance, and a few long sequences
+// still fill the chip. With few units each is cut evenly into its own workgroups (AtPlan). A cut
+// inside a unit leaves partial sums in the workspace, which k_attend_join adds up in a fixed
+// order. Workgroups are small (four waves), so that two or three share a CU and one's set-up
+// hides behind another's stream.
 //
 // A wave takes blocks of 32 tokens. Scores come as S^T = K Q^T on v_mfma_f32_16x16x32_f16: lane l
 // supplies a quarter row of token l % 16 (elements D / 4 * (l / 16) + ..., one contiguous load and
@@ -36,25 +37,45 @@ namespace tq {
 constexpr int kAtCus = 256;
 constexpr int kAtMaxGrid = 3 * kAtCus;  // workgroups of a launch, at most
 constexpr int kAtUnit = 256;            // a unit's set-up in tokens of work
-constexpr int kAtMinShare = 512;        // least work of a share
-constexpr float kAtLazy = 8.f;      // log2 of how far a score may pass the reference
+constexpr int kAtMinShare = 384;        // least work of a share
+constexpr float kAtLazy = 8.f;          // log2 of how far a score may pass the reference
+constexpr float kAtNone = -3e38f;       // reference of a row that has seen nothing
 
 struct AttendMeta {                 // of a workgroup whose last unit goes on in the next ones
   int32_t parts;                    // following workgroups that hold a part; 0: nothing to join
-  int32_t row0, nrows;              // first query row (of M) of the unit, rows per (token, head)
-  int32_t head0, hb, pad[3];        // first query head, heads per token of the tile
+  int32_t row0, nrows;              // first query row (of M) of the unit, tokens of the tile
+  int32_t head0, nh, pad[3];        // first query head, heads per token
 };
 
 struct AttendParams {
-  AttendArgs a;
-  int share, hb, nhb, a_tok;  // query heads per key head; heads, head blocks, tokens of a tile
-  int grid, n_each;           // workgroups; queries of a sequence without q_offsets
-  float inv_sqrt_d;
-  uint32_t page16, page_mul;  // page_tokens / 16 and ceil(2^32 / page16) (0 for 1)
+  const uint32_t *kcodes, *vcodes, *ksigns, *vsigns;
+  const uint16_t *kscales, *vscales;
+  const uint16_t* q;
+  uint16_t* out;
+  const int32_t *q_offsets, *kv_lens, *page_table;
+  const uint32_t* tree;
   AttendMeta* meta;
   float* parts;
-  uint16_t hk[256], hv[256];  // fp16 centroids
+  int64_t q_stride;
+  int qdt, odt, q_heads, B, M, table_width, tree_words;
+  int heads, pages, page;
+  uint32_t page16, page_mul;        // page_tokens / 16 and ceil(2^32 / page16) (0 for 1)
+  int lg_gk, lg_gv, lg_kg, lg_vg;   // log2 of scales per row and of the groups
+  int share, hb, nhb, a_tok;        // query heads per key head; heads, head blocks, tokens of a tile
+  uint32_t hb_mul, a_mul;           // ceil(2^16 / hb), ceil(2^32 / a_tok) (0 for 1)
+  int hu_n, cap, n_each, negate;    // heads * nhb; tokens of a table row; queries without q_offsets
+  float inv_sqrt_d, c1;             // c1: |scale| log2(e) / sqrt(D); 0 for scale 0
+  uint16_t hk[256], hv[256];        // fp16 centroids
 };
+
+// The arguments are read where they are used, by scalar loads of the kernel's argument block:
+// held in registers from the start they would not fit beside the block loop's scalars. at_again
+// makes a point before which no read may be moved.
+typedef const __attribute__((address_space(4))) AttendParams* AtArgs;
+__device__ __forceinline__ AtArgs at_again(AtArgs p) {
+  asm volatile("" : "+s"(p));
+  return p;
+}
 
 template <int KB, int VB, int D, int R>
 struct AtCfg {
@@ -70,10 +91,11 @@ struct AtCfg {
   static constexpr int KS = D == 256 ? 2 : 1;                 // key scales of a quarter row, at most
   static constexpr int VW = (VB * CH + 31) / 32;              // words of a value piece
   static constexpr int WGS = R == 1 && D <= 128 ? 3 : 2;      // workgroups per CU
+  static constexpr int GRID = WGS * kAtCus;
   // LDS; the joined sums take the place of q
   static constexpr int WIDE = (KWIDE || VWIDE) ? 32768 : 0;
   static constexpr int TK = WIDE, TV = TK + 1024;
-  static constexpr int C1 = TV + 1024, ML = C1 + ROWS * 4, SC = ML + W * ROWS * 8, QS = SC + 64;
+  static constexpr int C1 = TV + 1024, LIM = C1 + ROWS * 4, ML = LIM + ROWS * 4, QS = ML + W * ROWS * 8;
   static constexpr int QP = D * 2 + 16;                       // padded row of q
   static constexpr int PER_N = W * ROWS * 16 * 4;             // bytes of one O block of all waves
   static constexpr int NL = PER_N >= 16384 ? 1 : 16384 / PER_N;  // O blocks joined per round
@@ -121,24 +143,32 @@ __device__ __forceinline__ T at_load(AtPtr base, uint32_t off) {
   return *(const __attribute__((address_space(1))) U*)(base + off);
 }
 
-// Normalises, rotates back and stores one output row held as in kv_wave_transform.
-template <int D>
-__device__ __forceinline__ void at_finish(const AttendParams& p, float (&v)[D / 64], float l, int64_t m,
-                                          int head, int lane) {
+// x / d for 0 <= x < 2^31 with mul = ceil(2^32 / d) (0 for d = 1): the product is at most one too
+// large while d <= 2^12 (x (mul d - 2^32) < 2^31 d), put right by one step.
+__device__ __forceinline__ int at_div(int x, int d, uint32_t mul) {
+  const uint32_t u = static_cast<uint32_t>(x);
+  uint32_t y = mul ? __umulhi(u, mul) : u;
+  y -= static_cast<uint64_t>(y) * d > u ? 1u : 0u;
+  return static_cast<int>(y);
+}
+
+// Normalises, rotates back and stores one output row held as in kv_wave_transform; sg: the lane's
+// sign bits.
+template <int D, typename P>
+__device__ __forceinline__ void at_finish(P p, float (&v)[D / 64], float l, int64_t m, int head, uint32_t sg, int lane) {
   constexpr int EL = D / 64;
-  const float f = l == 0.f ? 0.f : p.inv_sqrt_d / l;
+  const float f = p->inv_sqrt_d / l;
 #pragma unroll
   for (int e = 0; e < EL; ++e) v[e] = l == 0.f ? 0.f : v[e] * f;
-  const int c = kv_chunk(lane), d0 = c * EL;
-  const uint32_t sg = p.a.c.v.signs[d0 >> 5] >> (d0 & 31);
+  const int c = kv_chunk(lane);
   kv_wave_transform<EL>(v, c);
-  const int64_t o = (m * p.a.q_heads + head) * D + d0;
-  uint16_t* dst = static_cast<uint16_t*>(p.a.out) + o;
+  const int odt = p->odt;
+  uint16_t* dst = p->out + (m * p->q_heads + head) * D + c * EL;
   uint16_t x[EL];
 #pragma unroll
   for (int e = 0; e < EL; ++e) {
     const float y = (sg >> e) & 1u ? -v[e] : v[e];
-    x[e] = p.a.odt == 1 ? float_to_bf16_rne(y) : float_to_half_rne(y);
+    x[e] = odt == 1 ? float_to_bf16_rne(y) : float_to_half_rne(y);
   }
   __builtin_memcpy(__builtin_assume_aligned(dst, 2 * EL), x, 2 * EL);
 }
@@ -148,7 +178,7 @@ __device__ __forceinline__ void at_finish(const AttendParams& p, float (&v)[D / 
 // kAtUnit; block k of it lies kAtUnit + 32 k from the unit's begin on the line.
 struct AtSeq {
   int row0, n, len, tiles;
-  bool flat;         // every tile reads the whole length (trees; more queries than tokens)
+  int flat;          // 1: every tile reads the whole length (trees; more queries than tokens)
   int64_t per_head;  // cost of all tiles of one head
 };
 
@@ -161,42 +191,60 @@ __device__ __forceinline__ int at_reads(const AtSeq& s, int a, int t) {
   const int q = (t + 1) * a < s.n ? (t + 1) * a : s.n;
   return s.len - s.n + q;
 }
-// U: b is the same in every lane of the wave, and so is what comes of it.
-template <bool U>
-__device__ __forceinline__ AtSeq at_seq(const AttendParams& p, int b) {
-  AtSeq s;
-  const int M = static_cast<int>(p.a.M);
-  int len = p.a.kv_lens[b];
-  if constexpr (U) len = at_uniform(len);
-  if (p.a.q_offsets) {
-    int lo = p.a.q_offsets[b], hi = p.a.q_offsets[b + 1];
-    if constexpr (U) {
-      lo = at_uniform(lo);
-      hi = at_uniform(hi);
-    }
-    lo = lo < 0 ? 0 : lo > M ? M : lo;
-    hi = hi < lo ? lo : hi > M ? M : hi;
-    s.row0 = lo;
-    s.n = hi - lo;
+// What the schedule reads of a sequence: length and query rows [lo, hi).
+struct AtRaw {
+  int len, lo, hi;
+};
+__device__ __forceinline__ AtRaw at_raw(AtArgs p, int b) {
+  AtRaw r;
+  r.len = p->kv_lens[b];
+  if (p->q_offsets) {
+    r.lo = p->q_offsets[b];
+    r.hi = p->q_offsets[b + 1];
   } else {
-    s.n = p.n_each;
-    s.row0 = b * s.n;
+    r.lo = b * p->n_each;
+    r.hi = r.lo + p->n_each;
   }
-  const int cap = p.a.table_width * p.a.c.page;
-  s.len = len < 0 ? 0 : len < cap ? len : cap;
-  s.tiles = s.n <= p.a_tok ? (s.n > 0 ? 1 : 0) : (s.n + p.a_tok - 1) / p.a_tok;
-  s.flat = p.a.tree != nullptr || s.n > s.len;
-  s.per_head = s.tiles == 0 ? 0 : at_before(s, p.a_tok, s.tiles - 1) + at_reads(s, p.a_tok, s.tiles - 1) + kAtUnit;
+  return r;
+}
+__device__ __forceinline__ AtRaw at_uniform(AtRaw r) {
+  return AtRaw{at_uniform(r.len), at_uniform(r.lo), at_uniform(r.hi)};
+}
+__device__ __forceinline__ AtSeq at_seq(AtArgs p, const AtRaw& r) {
+  AtSeq s;
+  const int M = p->M, a = p->a_tok;
+  s.row0 = r.lo < 0 ? 0 : r.lo > M ? M : r.lo;
+  const int hi = r.hi < s.row0 ? s.row0 : r.hi > M ? M : r.hi;
+  s.n = hi - s.row0;
+  s.len = r.len < 0 ? 0 : r.len < p->cap ? r.len : p->cap;
+  s.tiles = at_div(s.n + a - 1, a, p->a_mul);
+  s.flat = p->tree != nullptr || s.n > s.len ? 1 : 0;
+  s.per_head = s.tiles == 0 ? 0 : at_before(s, a, s.tiles - 1) + at_reads(s, a, s.tiles - 1) + kAtUnit;
   return s;
 }
 
-// Page of token j (a multiple of 16): a product estimate, at most one too large because j / 16 < 2^27
-// and page16 <= 2^12, put right by one step.
-__device__ __forceinline__ int at_page(const AttendParams& p, int j) {
-  const uint32_t u = static_cast<uint32_t>(j) >> 4;
-  uint32_t x = p.page_mul ? __umulhi(u, p.page_mul) : u;
-  x -= x * p.page16 > u ? 1u : 0u;
-  return static_cast<int>(x);
+template <int V>
+struct AtInt {
+  static constexpr int value = V;
+};
+// Inclusive sum over the lanes of a wave (row shifts, then the rows' last lanes broadcast).
+__device__ __forceinline__ int64_t at_scan(int64_t x) {
+  auto step = [&](auto ctrl, auto rows) {
+    const int lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(x), decltype(ctrl)::value, decltype(rows)::value, 0xf, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(x >> 32), decltype(ctrl)::value, decltype(rows)::value, 0xf, false);
+    x += static_cast<int64_t>(hi) << 32 | static_cast<uint32_t>(lo);
+  };
+  step(AtInt<0x111>{}, AtInt<0xf>{});
+  step(AtInt<0x112>{}, AtInt<0xf>{});
+  step(AtInt<0x114>{}, AtInt<0xf>{});
+  step(AtInt<0x118>{}, AtInt<0xf>{});
+  step(AtInt<0x142>{}, AtInt<0xa>{});
+  step(AtInt<0x143>{}, AtInt<0xc>{});
+  return x;
+}
+__device__ __forceinline__ int64_t at_lane(int64_t x, int lane) {
+  return static_cast<int64_t>(__builtin_amdgcn_readlane(static_cast<int>(x >> 32), lane)) << 32 |
+         static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), lane));
 }
 
 // ---- decoding -----------------------------------------------------------------------------
@@ -252,6 +300,11 @@ __device__ __forceinline__ uint32_t at_pair_at(uint32_t x, int q, uint32_t lane4
   }
 }
 
+// the larger of each half, as unsigned numbers (scales are not negative)
+__device__ __forceinline__ uint32_t at_max_u16(uint32_t a, uint32_t b) {
+  typedef uint16_t V __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b)));
+}
 __device__ __forceinline__ uint32_t at_mul(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, a) * __builtin_bit_cast(half2_t, b));
 }
@@ -265,28 +318,39 @@ __device__ __forceinline__ f32x4_t at_mfma(const uint32_t (&a)[4], const uint32_
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, x), __builtin_bit_cast(f16x8_t, y), c, 0, 0, 0);
 }
 
+// A block's codes and scales as loaded: a quarter row of token l % 16 of each half for the scores,
+// a piece of eight tokens' rows for the sums.
+template <typename C>
+struct AtBlock {
+  uint32_t k[2][C::KW], v[8][C::VW], ks[2][C::KS], vs[4];
+  uint32_t bad;  // uniform; bit x: the page of half x is none
+};
+
 template <int KB, int VB, int D, int R>
-__global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS)) void k_attend(AttendParams p) {
+__global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS)) void k_attend(AttendParams) {
   using C = AtCfg<KB, VB, D, R>;
   constexpr int W = C::W, T = C::T, ROWS = C::ROWS, NS = C::NS, CH = C::CH, EL = D / 64;
   extern __shared__ __attribute__((aligned(16))) char smem[];
+  AtArgs p = (AtArgs)__builtin_amdgcn_kernarg_segment_ptr();
   const int tid = threadIdx.x, lane = tid & 63, wave = at_uniform(tid >> 6);
   const int col = lane & 15, h = lane >> 4;
   const uint32_t lane4 = (lane & 31) * 4;
+  const int wg = blockIdx.x;
 
-  // this workgroup's share of the work: a scan over the sequences' costs, each thread taking
-  // neighbouring ones; the thread that holds the share's begin finds its unit
-  const int hu_n = p.a.c.heads * p.nhb;
-  const int per = (p.a.B + T - 1) / T;
-  const int b0 = tid * per, b1 = b0 + per < p.a.B ? b0 + per : p.a.B;
-  int64_t sum = 0;
-  for (int b = b0; b < b1; ++b) sum += at_seq<false>(p, b).per_head * hu_n;
+  // ---- this workgroup's part of the work, found by every wave for itself: a scan over the
+  // sequences' costs, a lane taking `per` neighbouring ones ----
+  const int per = (p->B + 63) >> 6;
+  const int b0 = lane * per;
+  AtRaw raw0{0, 0, 0};
+  if (b0 < p->B) raw0 = at_raw(p, b0);
+  const int ch = kv_chunk(lane), d0 = ch * EL;
+  const uint32_t ksg = p->ksigns[d0 >> 5] >> (d0 & 31), vsg = p->vsigns[d0 >> 5] >> (d0 & 31);
 
-  // centroid tables
+  // centroid tables, while those loads are on their way. A wave's entries are uniform: scalar
+  // loads of the arguments, two 128-byte rows per store.
   if constexpr (C::WIDE > 0) {
-    // a wave's entries are uniform: scalar loads of the arguments, two 128-byte rows per store
     constexpr int TB = KB == 8 || VB == 8 ? 8 : 4;
-    const uint16_t* hc = KB == TB ? p.hk : p.hv;
+    const __attribute__((address_space(4))) uint16_t* hc = KB == TB ? p->hk : p->hv;
     constexpr int PW = 256 / W;
 #pragma unroll
     for (int k = 0; k < PW; k += 2) {
@@ -299,71 +363,98 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
   if constexpr (KB < 8 && !C::KWIDE)
     for (int e = tid; e < (1 << (2 * KB)); e += T)
       *reinterpret_cast<uint32_t*>(smem + C::TK + 4 * e) =
-          p.hk[e & ((1 << KB) - 1)] | static_cast<uint32_t>(p.hk[e >> KB]) << 16;
+          p->hk[e & ((1 << KB) - 1)] | static_cast<uint32_t>(p->hk[e >> KB]) << 16;
   if constexpr (VB < 8 && !C::VWIDE)
     for (int e = tid; e < (1 << (2 * VB)); e += T)
       *reinterpret_cast<uint32_t*>(smem + C::TV + 4 * e) =
-          p.hv[e & ((1 << VB) - 1)] | static_cast<uint32_t>(p.hv[e >> VB]) << 16;
+          p->hv[e & ((1 << VB) - 1)] | static_cast<uint32_t>(p->hv[e >> VB]) << 16;
 
-  int64_t* sc = reinterpret_cast<int64_t*>(smem + C::SC);  // [W] wave sums, then the begin
-  int64_t incl = sum;
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const int64_t o = __shfl_up(incl, m);
-    incl += lane >= m ? o : 0;
+  const int a_tok = p->a_tok, hu_n = p->hu_n;
+  if (tid == 0) p->meta[wg].parts = 0;
+  const AtSeq seq0 = at_seq(p, raw0);
+  const int b1 = b0 + per < p->B ? b0 + per : p->B;
+  // cost and units of the lane's sequences; even: every tile of a head costs the same
+  int64_t sum = 0, units = 0;
+  bool even = true;
+  for (int b = b0; b < b1; ++b) {
+    const AtSeq x = b == b0 ? seq0 : at_seq(p, at_raw(p, b));
+    sum += x.per_head * hu_n;
+    units += static_cast<int64_t>(x.tiles) * hu_n;
+    even = even && (x.flat || x.tiles <= 1);
   }
-  if (lane == 63) sc[wave] = incl;
-  if (tid == 0) p.meta[blockIdx.x].parts = 0;
-  __syncthreads();
-  int64_t total = 0, base = incl - sum;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    const int64_t x = sc[w];
-    base += w < wave ? x : 0;
-    total += x;
-  }
-  total = at_uniform(total);
-  int64_t q = total / p.grid + 1;
+  int64_t incl = at_scan(sum);
+  int64_t total = at_lane(incl, 63);
+  const int64_t all_units = at_lane(at_scan(units), 63);
+  // with few units, each is cut into parts of about q of work, one part per workgroup:
+  // q = total / (GRID - units) gives at most GRID parts. Otherwise the line is cut every q.
+  const bool own = !__any(!even) && all_units <= C::GRID / 2;
+  int64_t q = own ? static_cast<int64_t>(static_cast<double>(total) / static_cast<double>(C::GRID - all_units)) + 1
+                  : total / C::GRID + 1;
   q = at_uniform(q < kAtMinShare ? kAtMinShare : q);
-  const int64_t w0 = q * blockIdx.x, w1 = w0 + q < total ? w0 + q : total;
-  if (w0 >= total) return;
-  if (w0 >= base && w0 < base + sum) {
-    int64_t rem = w0 - base;
-    int b = b0;
-    AtSeq x = at_seq<false>(p, b);
-    while (rem >= x.per_head * hu_n) {
-      rem -= x.per_head * hu_n;
-      x = at_seq<false>(p, ++b);
+  const int q32 = static_cast<int>(q < 0x7fffffff ? q : 0x7fffffff);
+  auto parts_of = [&](const AtSeq& x) {  // of a unit of an even sequence
+    const int c = (x.len > 1 ? x.len : 1) + kAtUnit;
+    int y = static_cast<int>(static_cast<float>(c) / static_cast<float>(q32));
+    while (static_cast<int64_t>(y) * q32 < c) ++y;
+    return y;
+  };
+  if (own) {  // the same scan in parts
+    sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      const AtSeq x = b == b0 ? seq0 : at_seq(p, at_raw(p, b));
+      if (x.tiles > 0) sum += static_cast<int64_t>(x.tiles) * hu_n * parts_of(x);
     }
-    // head and tile: rem < 2^53, so the quotient in fp64 is at most one off
-    int64_t hd = static_cast<int64_t>(static_cast<double>(rem) / static_cast<double>(x.per_head));
-    hd -= hd * x.per_head > rem ? 1 : 0;
-    hd += (hd + 1) * x.per_head <= rem ? 1 : 0;
-    rem -= hd * x.per_head;
-    int lo = 0, hi = x.tiles - 1;  // last tile with at_before <= rem
+    incl = at_scan(sum);
+    total = at_lane(incl, 63);
+  }
+  const int64_t w0 = own ? wg : q * wg;
+  const int64_t w1 = own ? w0 + 1 : w0 + q < total ? w0 + q : total;
+  if (w0 >= total) return;
+  // the lane that holds w0, then the sequence among its own
+  const int src = __builtin_ctzll(__ballot(incl > w0));
+  int64_t rem = at_uniform(w0 - at_lane(incl - sum, src));
+  int b = src * per;
+  AtSeq sq = at_seq(p, AtRaw{__builtin_amdgcn_readlane(raw0.len, src), __builtin_amdgcn_readlane(raw0.lo, src),
+                             __builtin_amdgcn_readlane(raw0.hi, src)});
+  auto work_of = [&](const AtSeq& x) {
+    return x.tiles == 0 ? int64_t{0} : own ? static_cast<int64_t>(x.tiles) * hu_n * parts_of(x) : x.per_head * hu_n;
+  };
+  for (int64_t x = work_of(sq); rem >= x; x = work_of(sq)) {
+    rem = at_uniform(rem - x);
+    ++b;
+    sq = at_seq(p, at_uniform(at_raw(p, b)));
+  }
+  int hu, t, part = 0, np = 1;
+  int64_t u0 = 0;  // the unit's begin on the line
+  if (own) {
+    np = at_uniform(parts_of(sq));
+    const int r32 = static_cast<int>(rem);  // below GRID
+    const int unit = r32 / np;
+    part = r32 - unit * np;
+    hu = unit / sq.tiles;
+    t = unit - hu * sq.tiles;
+  } else {
+    // rem < 2^53, so the quotient in fp64 is at most one off
+    hu = static_cast<int>(static_cast<double>(rem) / static_cast<double>(sq.per_head));
+    hu -= hu * sq.per_head > rem ? 1 : 0;
+    hu += (hu + 1) * sq.per_head <= rem ? 1 : 0;
+    rem -= hu * sq.per_head;
+    int lo = 0, hi = sq.tiles - 1;  // last tile with at_before <= rem
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (at_before(x, p.a_tok, mid) <= rem) lo = mid;
+      if (at_before(sq, a_tok, mid) <= rem) lo = mid;
       else hi = mid - 1;
     }
-    sc[4] = static_cast<int64_t>(hd) << 32 | b;
-    sc[5] = lo;
-    sc[6] = w0 - (rem - at_before(x, p.a_tok, lo));
+    t = lo;
+    u0 = w0 - (rem - at_before(sq, a_tok, t));
   }
-  __syncthreads();
-  int b = at_uniform(static_cast<int>(sc[4])), hu = at_uniform(static_cast<int>(sc[4] >> 32));
-  int t = at_uniform(static_cast<int>(sc[5]));
-  int64_t u0 = at_uniform(sc[6]);  // the unit's begin
-  AtSeq sq = at_seq<true>(p, b);
 
-  const int page = p.a.c.page;
-  const int kg = p.a.c.k.group, vg = p.a.c.v.group;
-  const int gk = D / kg, gv = D / vg;
   const uint32_t koff = col * C::KROW + (C::KROW / 4) * h;
-  // scales of the quarter row's first and (D = 256) second half
-  const uint32_t ksoff = (col * gk + (D / 4 * h) / kg) * 2, ksoff2 = (col * gk + (D / 4 * h + D / 8) / kg) * 2;
   const uint32_t voff = 4 * h * C::VROW + (VB * CH * col) / 8;
-  const uint32_t vsoff = 4 * h * gv * 2 + ((col * CH) / vg) * 2;
+  // scales of the quarter row's first and (D = 256) second half, and of the value piece
+  const uint32_t ksoff = ((col << p->lg_gk) + ((D / 4 * h) >> p->lg_kg)) * 2;
+  const uint32_t ksoff2 = ((col << p->lg_gk) + ((D / 4 * h + D / 8) >> p->lg_kg)) * 2;
+  const uint32_t vsoff = ((4 * h << p->lg_gv) + ((col * CH) >> p->lg_vg)) * 2;
 
   for (int64_t w = w0; w < w1;) {
     // what steers the wave is the same in all its lanes; said so, it lives in scalar registers
@@ -376,151 +467,178 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
     sq.n = at_uniform(sq.n);
     sq.len = at_uniform(sq.len);
     sq.tiles = at_uniform(sq.tiles);
-    sq.flat = at_uniform(sq.flat ? 1 : 0) != 0;
-    const int reads = at_reads(sq, p.a_tok, t);
-    const int64_t x0 = w - u0 - kAtUnit, x1 = w1 - u0 - kAtUnit < reads ? w1 - u0 - kAtUnit : reads;
-    const int k0 = x0 <= 0 ? 0 : static_cast<int>((x0 + 31) >> 5);
-    const int k1 = x1 <= 0 ? 0 : static_cast<int>((x1 + 31) >> 5);
+    sq.flat = at_uniform(sq.flat);
+    p = at_again(p);
+    const int reads = at_reads(sq, a_tok, t);
     const int nblk = (reads + 31) >> 5;
+    int k0, k1;
+    if (own) {
+      k0 = static_cast<int>(static_cast<int64_t>(nblk) * part / np);
+      k1 = static_cast<int>(static_cast<int64_t>(nblk) * (part + 1) / np);
+    } else {
+      const int64_t x0 = w - u0 - kAtUnit, x1 = w1 - u0 - kAtUnit < reads ? w1 - u0 - kAtUnit : reads;
+      k0 = x0 <= 0 ? 0 : static_cast<int>((x0 + 31) >> 5);
+      k1 = x1 <= 0 ? 0 : static_cast<int>((x1 + 31) >> 5);
+    }
+    k0 = at_uniform(k0);
+    k1 = at_uniform(k1);
     if (k0 < k1) {
-      const int kh = hu / p.nhb, hblk = hu - kh * p.nhb;
-      const int head0 = kh * p.share + hblk * p.hb;
-      const int nh = p.share - hblk * p.hb < p.hb ? p.share - hblk * p.hb : p.hb;
-      const int tok0 = t * p.a_tok;
-      const int ntok = sq.n - tok0 < p.a_tok ? sq.n - tok0 : p.a_tok;
+      const int kh = p->nhb == 1 ? hu : hu / p->nhb, hblk = hu - kh * p->nhb;
+      const int hb = p->hb, head0 = kh * p->share + hblk * hb;
+      const int nh = p->share - hblk * hb < hb ? p->share - hblk * hb : hb;
+      const int tok0 = t * a_tok;
+      const int ntok = sq.n - tok0 < a_tok ? sq.n - tok0 : a_tok;
       const int before = sq.len - sq.n;
+      const int len = sq.len;
 
-      // ---- blocks of 32 tokens ----
-      uint32_t kraw[2][C::KW] = {}, vraw[8][C::VW] = {}, ksr[2][C::KS] = {}, vsr[4] = {};
-      const int32_t* table = p.a.page_table + static_cast<int64_t>(b) * p.a.table_width;
-      const int64_t khead = static_cast<int64_t>(kh) * page, prow = static_cast<int64_t>(p.a.c.heads) * page;
-      int64_t row_of[2] = {};
-      bool bad[2] = {};
+      // ---- the stream of blocks ----
+      const int page = p->page, pages = p->pages;
+      const uint32_t page16 = p->page16, page_mul = p->page_mul;
+      const uint32_t prow = static_cast<uint32_t>(p->heads) * page;
+      const int lgk = p->lg_gk, lgv = p->lg_gv;
+      const char* const kcodes = reinterpret_cast<const char*>(p->kcodes) + static_cast<int64_t>(kh) * page * C::KROW;
+      const char* const vcodes = reinterpret_cast<const char*>(p->vcodes) + static_cast<int64_t>(kh) * page * C::VROW;
+      const char* const kscales = reinterpret_cast<const char*>(p->kscales) + ((static_cast<int64_t>(kh) * page) << (lgk + 1));
+      const char* const vscales = reinterpret_cast<const char*>(p->vscales) + ((static_cast<int64_t>(kh) * page) << (lgv + 1));
       // page ids of a block's halves (a half past the end stands for the first one), read one
       // block ahead; constant memory, so that they come by scalar loads
       typedef const int32_t __attribute__((address_space(4))) * ConstIds;
-      const ConstIds ids = (ConstIds)reinterpret_cast<uintptr_t>(table);
+      const ConstIds ids = (ConstIds)reinterpret_cast<uintptr_t>(p->page_table + static_cast<int64_t>(b) * p->table_width);
       int id[2] = {}, in[2] = {};
       auto look = [&](int blk) {
-        const int j = blk * 32, j2 = j + 16 < sq.len ? j + 16 : j;
-        const int pi = at_page(p, j), pi2 = at_page(p, j2);
+        const int j = blk * 32, j2 = j + 16 < len ? j + 16 : j;
+        const int pi = at_div(j >> 4, page16, page_mul), pi2 = at_div(j2 >> 4, page16, page_mul);
         in[0] = j - pi * page;
         in[1] = j2 - pi2 * page;
-        id[0] = sq.len > 0 ? ids[pi] : -1;
-        id[1] = sq.len > 0 ? ids[pi2] : -1;
+        id[0] = len > 0 ? ids[pi] : -1;
+        id[1] = len > 0 ? ids[pi2] : -1;
       };
-      auto locate = [&]() {
+      int64_t row_of[2] = {};
+      auto locate = [&](AtBlock<C>& x) {
+        x.bad = 0;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          bad[x] = id[x] < 0 || id[x] >= p.a.c.pages;
-          row_of[x] = (bad[x] ? 0 : id[x]) * prow + khead + in[x];
+        for (int y = 0; y < 2; ++y) {
+          const bool none = static_cast<uint32_t>(id[y]) >= static_cast<uint32_t>(pages);
+          x.bad |= none ? 1u << y : 0u;
+          row_of[y] = static_cast<int64_t>(static_cast<uint64_t>(none ? 0u : static_cast<uint32_t>(id[y])) * prow) + in[y];
         }
       };
-      auto load_k = [&]() {
+      auto load_k = [&](AtBlock<C>& x) {
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb) {
-          const AtPtr kc = at_base(p.a.c.k.codes, row_of[sb] * C::KROW);
+          const AtPtr kc = at_base(kcodes, row_of[sb] * C::KROW);
           constexpr int L = C::KW % 4 == 0 ? 4 : C::KW % 3 == 0 ? 3 : C::KW % 2 == 0 ? 2 : 1;  // words of a load
           if constexpr (C::KROW % 16 != 0) {  // six bytes
-            kraw[sb][0] = at_load<uint32_t>(kc, koff);
-            kraw[sb][1] = at_load<uint16_t>(kc, koff + 4);
+            x.k[sb][0] = at_load<uint32_t>(kc, koff);
+            x.k[sb][1] = at_load<uint16_t>(kc, koff + 4);
           } else {
 #pragma unroll
-          for (int k = 0; k < C::KW; k += L) {
-            if constexpr (L == 4) {
-              const u32x4_t x = at_get<u32x4_t>(kc, koff + 4 * k);
-              kraw[sb][k] = x.x; kraw[sb][k + 1] = x.y; kraw[sb][k + 2] = x.z; kraw[sb][k + 3] = x.w;
-            } else if constexpr (L == 3) {
-              const u32x3_t x = at_get<u32x3_t>(kc, koff + 4 * k);
-              kraw[sb][k] = x.x; kraw[sb][k + 1] = x.y; kraw[sb][k + 2] = x.z;
-            } else if constexpr (L == 2) {
-              const u32x2_t x = at_get<u32x2_t>(kc, koff + 4 * k);
-              kraw[sb][k] = x.x; kraw[sb][k + 1] = x.y;
-            } else {
-              kraw[sb][k] = at_get<uint32_t>(kc, koff + 4 * k);
+            for (int k = 0; k < C::KW; k += L) {
+              if constexpr (L == 4) {
+                const u32x4_t y = at_get<u32x4_t>(kc, koff + 4 * k);
+                x.k[sb][k] = y.x; x.k[sb][k + 1] = y.y; x.k[sb][k + 2] = y.z; x.k[sb][k + 3] = y.w;
+              } else if constexpr (L == 3) {
+                const u32x3_t y = at_get<u32x3_t>(kc, koff + 4 * k);
+                x.k[sb][k] = y.x; x.k[sb][k + 1] = y.y; x.k[sb][k + 2] = y.z;
+              } else if constexpr (L == 2) {
+                const u32x2_t y = at_get<u32x2_t>(kc, koff + 4 * k);
+                x.k[sb][k] = y.x; x.k[sb][k + 1] = y.y;
+              } else {
+                x.k[sb][k] = at_get<uint32_t>(kc, koff + 4 * k);
+              }
             }
           }
-          }
-          const AtPtr sp = at_base(p.a.c.k.scales, row_of[sb] * gk * 2);
-          ksr[sb][0] = at_get<uint16_t>(sp, ksoff);
-          if constexpr (C::KS == 2) ksr[sb][1] = at_get<uint16_t>(sp, ksoff2);
+          const AtPtr sp = at_base(kscales, row_of[sb] << (lgk + 1));
+          x.ks[sb][0] = at_get<uint16_t>(sp, ksoff);
+          if constexpr (C::KS == 2) x.ks[sb][1] = at_get<uint16_t>(sp, ksoff2);
         }
       };
-      auto load_v = [&]() {
+      auto load_v = [&](AtBlock<C>& x) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int sb = i >> 2;
-          const AtPtr vc = at_base(p.a.c.v.codes, row_of[sb] * C::VROW);
-          const uint32_t off = voff + (i & 3) * C::VROW;
-          if constexpr (VB == 3) {
-            if constexpr (CH == 4) {
-              vraw[i][0] = at_load<uint16_t>(vc, off) >> (4 * (col & 1));
-            } else if constexpr (CH == 8) {
-              const uint32_t back = col == 15 ? 1 : 0;
-              vraw[i][0] = at_load<uint32_t>(vc, off - back) >> (8 * back);
+        for (int sb = 0; sb < 2; ++sb) {
+          const AtPtr vc = at_base(vcodes, row_of[sb] * C::VROW);
+          const AtPtr sp = at_base(vscales, row_of[sb] << (lgv + 1));
+#pragma unroll
+          for (int i = 4 * sb; i < 4 * sb + 4; ++i) {
+            const uint32_t off = voff + (i & 3) * C::VROW;
+            if constexpr (VB == 3) {
+              // a piece of 12, 24 or 48 bits; of 24, the row's last one is read one byte earlier,
+              // inside the row (shifted down where it is used)
+              if constexpr (CH == 4) {
+                x.v[i][0] = at_load<uint16_t>(vc, off);
+              } else if constexpr (CH == 8) {
+                x.v[i][0] = at_load<uint32_t>(vc, off - (col == 15 ? 1 : 0));
+              } else {
+                x.v[i][0] = at_load<uint32_t>(vc, off);
+                x.v[i][1] = at_load<uint16_t>(vc, off + 4);
+              }
+            } else if constexpr (VB * CH == 8) {
+              x.v[i][0] = at_get<uint8_t>(vc, off);
+            } else if constexpr (VB * CH == 16) {
+              x.v[i][0] = at_get<uint16_t>(vc, off);
+            } else if constexpr (C::VW == 4) {
+              const u32x4_t y = at_get<u32x4_t>(vc, off);
+              x.v[i][0] = y.x; x.v[i][1] = y.y; x.v[i][2] = y.z; x.v[i][3] = y.w;
+            } else if constexpr (C::VW == 2) {
+              const u32x2_t y = at_get<u32x2_t>(vc, off);
+              x.v[i][0] = y.x; x.v[i][1] = y.y;
             } else {
-              const uint32_t a = at_load<uint32_t>(vc, off), c = at_load<uint16_t>(vc, off + 4);
-              vraw[i][0] = a;
-              vraw[i][1] = (a >> 24) | (c << 8);
+              x.v[i][0] = at_get<uint32_t>(vc, off);
             }
-          } else if constexpr (VB * CH == 8) {
-            vraw[i][0] = at_get<uint8_t>(vc, off);
-          } else if constexpr (VB * CH == 16) {
-            vraw[i][0] = at_get<uint16_t>(vc, off);
+          }
+          // scales of the piece's group for the four tokens, in pairs
+          if (lgv == 0) {
+            const u32x2_t y = at_get<u32x2_t>(sp, 8 * h);
+            x.vs[2 * sb] = y.x;
+            x.vs[2 * sb + 1] = y.y;
           } else {
 #pragma unroll
-            for (int k = 0; k < C::VW; ++k) vraw[i][k] = at_get<uint32_t>(vc, off + 4 * k);
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t off = vsoff + ((2 * i) << (lgv + 1));
+              x.vs[2 * sb + i] = at_get<uint16_t>(sp, off) | static_cast<uint32_t>(at_get<uint16_t>(sp, off + (1 << (lgv + 1)))) << 16;
+            }
           }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const AtPtr sp = at_base(p.a.c.v.scales, row_of[i >> 1] * gv * 2);
-          const uint32_t off = vsoff + (2 * (i & 1)) * gv * 2;
-          const uint32_t a = at_get<uint16_t>(sp, off);
-          const uint32_t c = at_get<uint16_t>(sp, off + gv * 2);
-          vsr[i] = a | (c << 16);
-        }
       };
-
+      AtBlock<C> buf[2] = {};
       int blk = k0 + wave;
-      bool kbad[2] = {false, false};
       if (blk < k1) {
         look(blk);
-        locate();
-        load_k();
-        load_v();
-        kbad[0] = bad[0];
-        kbad[1] = bad[1];
+        locate(buf[0]);
+        load_k(buf[0]);
+        load_v(buf[0]);
         if (blk + W < k1) look(blk + W);
       }
+
       // ---- q: rotated, scaled by a power of two to fp16's upper range, into LDS ----
       __syncthreads();  // the last unit's readers of this memory are done
       {
         constexpr int RW = ROWS / W < 4 ? ROWS / W : 4;  // rows of a wave at a time
-        const int ch = kv_chunk(lane), d0 = ch * EL;
-        const uint32_t sg = p.a.c.k.signs[d0 >> 5] >> (d0 & 31);
+        const uint32_t neg = p->negate ? 0xffffffffu : 0u, hb_mul = p->hb_mul;
+        const float c1 = p->c1;
+        const int qdt = p->qdt;
 #pragma unroll 1
         for (int r0 = wave * (ROWS / W); r0 < (wave + 1) * (ROWS / W); r0 += RW) {
           float v[RW][EL];
+          uint16_t raw[RW][EL];
+          bool ok[RW];
 #pragma unroll
           for (int x = 0; x < RW; ++x) {
-            const int tk = (r0 + x) / p.hb, hd = r0 + x - tk * p.hb;
-            const bool ok = tk < ntok && hd < nh && p.a.scale != 0.f;
-            const uint16_t* src = static_cast<const uint16_t*>(p.a.q) +
-                                  (static_cast<int64_t>(sq.row0) + tok0 + (ok ? tk : 0)) * p.a.q_stride +
-                                  static_cast<int64_t>(head0 + (ok ? hd : 0)) * D + d0;
-            uint16_t raw[EL];
-            __builtin_memcpy(raw, __builtin_assume_aligned(src, 2 * EL), 2 * EL);
-#pragma unroll
-            for (int e = 0; e < EL; ++e) {
-              const float y = p.a.qdt == 1 ? bf16_bits_to_float(raw[e]) : half_bits_to_float(raw[e]);
-              v[x][e] = !ok ? 0.f : ((sg >> e) & 1u) != (p.a.scale < 0.f ? 1u : 0u) ? -y : y;
-            }
+            const int tk = (static_cast<uint32_t>(r0 + x) * hb_mul) >> 16, hd = r0 + x - tk * hb;
+            ok[x] = tk < ntok && hd < nh && c1 != 0.f;
+            const uint16_t* src = p->q + (static_cast<int64_t>(sq.row0) + tok0 + (ok[x] ? tk : 0)) * p->q_stride +
+                                  static_cast<int64_t>(head0 + (ok[x] ? hd : 0)) * D + d0;
+            __builtin_memcpy(raw[x], __builtin_assume_aligned(src, 2 * EL), 2 * EL);
           }
 #pragma unroll
           for (int x = 0; x < RW; ++x) {
-            kv_wave_transform<EL>(v[x], ch);
             float mx = 0.f;
+#pragma unroll
+            for (int e = 0; e < EL; ++e) {
+              const float y = qdt == 1 ? bf16_bits_to_float(raw[x][e]) : half_bits_to_float(raw[x][e]);
+              v[x][e] = !ok[x] ? 0.f : (((ksg ^ neg) >> e) & 1u) ? -y : y;
+            }
+            kv_wave_transform<EL>(v[x], ch);
 #pragma unroll
             for (int e = 0; e < EL; ++e) mx = fmaxf(mx, fabsf(v[x][e]));
             mx = kv_wave_max(mx);
@@ -533,36 +651,29 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
 #pragma unroll
             for (int e = 0; e < EL; ++e) y[e] = static_cast<_Float16>(v[x][e] * f);
             __builtin_memcpy(__builtin_assume_aligned(smem + C::QS + (r0 + x) * C::QP + 2 * d0, 2 * EL), y, 2 * EL);
-            if (lane == 0)
-              *reinterpret_cast<float*>(smem + C::C1 + 4 * (r0 + x)) =
-                  p.a.scale == 0.f ? 1.f : fabsf(p.a.scale) * 1.44269504f * p.inv_sqrt_d *
-                                               __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+            if (lane == 0) {
+              const int r = r0 + x, tk = (static_cast<uint32_t>(r) * hb_mul) >> 16, hd = r - tk * hb;
+              *reinterpret_cast<float*>(smem + C::C1 + 4 * r) =
+                  c1 == 0.f ? 1.f : c1 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+              int lim = p->tree ? before : before + tok0 + tk + 1;
+              lim = lim < 0 ? 0 : lim;
+              *reinterpret_cast<int*>(smem + C::LIM + 4 * r) = !(tk < ntok && hd < nh) || lim > len ? len : lim;
+            }
           }
         }
       }
       __syncthreads();
-      float c1[R];
-      int lim[R], tok_row[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int row = 16 * r + col, tk = row / p.hb, hd = row - tk * p.hb;
-        c1[r] = *reinterpret_cast<const float*>(smem + C::C1 + 4 * row);  // times 2^kexp
-        const bool ok = tk < ntok && hd < nh;
-        tok_row[r] = sq.row0 + tok0 + (ok ? tk : 0);
-        int x = p.a.tree ? before : before + tok0 + tk + 1;
-        x = x < 0 ? 0 : x;
-        lim[r] = !ok || x > sq.len ? sq.len : x;
-      }
       // from this token on some row's mask may cut
-      int cut = p.a.tree ? before : before + tok0 + 1;
+      int cut = p->tree ? before : before + tok0 + 1;
       cut = cut < 0 ? 0 : cut;
+      const uint32_t* const tree = p->tree;
 
-      float mref[R], mo[R], l[R];
+      float c1[R], mo[R], l[R];  // score factor; reference - 7; sum
       f32x4_t o[R][CH];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        mref[r] = -__builtin_inff();
-        mo[r] = 0.f;
+        c1[r] = *reinterpret_cast<const float*>(smem + C::C1 + 4 * (16 * r + col));  // times 2^kexp
+        mo[r] = kAtNone;
         l[r] = 0.f;
 #pragma unroll
         for (int n = 0; n < CH; ++n) o[r][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -571,37 +682,33 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
       // its scales are small (below 2^-4), and grow when one passes 2^13.
       int kexp = 0, vexp = 0;
 
-      for (; blk < k1; blk += W) {
-        const bool more = blk + W < k1;
-        const bool b0_ = kbad[0], b1_ = kbad[1];
-        // ---- scores ----
-        f32x4_t s[R][2];
-        uint32_t kd[2][C::KS];  // scales times 2^-kexp, in both halves; no number for a bad page
+      auto scores = [&](const AtBlock<C>& x, bool first, f32x4_t (&s)[R][2]) {
+        uint32_t kd[2][C::KS];  // scales times 2^-kexp, in both halves
         auto key_scales = [&]() {
           uint32_t big = 0;
 #pragma unroll
           for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
-            for (int x = 0; x < C::KS; ++x) {
-              uint32_t y = ksr[sb][x] | (ksr[sb][x] << 16);
-              if (sb ? b1_ : b0_) y = 0;
-              kd[sb][x] = at_mul(y, at_pow2(kexp));
-              big = kd[sb][x] > big ? kd[sb][x] : big;
+            for (int y = 0; y < C::KS; ++y) {
+              uint32_t z = x.ks[sb][y] | (x.ks[sb][y] << 16);
+              if ((x.bad >> sb) & 1u) z = 0;
+              kd[sb][y] = at_mul(z, at_pow2(kexp));
+              big = kd[sb][y] > big ? kd[sb][y] : big;
             }
           return big;
         };
-        const uint32_t kbig = key_scales();
-        if (__any(kbig > 0x7000ffffu) || (blk == k0 + wave && !__any(kbig > 0x2c00ffffu))) {  // beyond 2^13, no number, or small
+        const uint32_t big = key_scales();
+        if (__any(big > 0x7000ffffu) || (first && !__any(big > 0x2c00ffffu))) {  // beyond 2^13, no number, or small
           float top = 0.f;
 #pragma unroll
           for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
-            for (int x = 0; x < C::KS; ++x)
-              if ((ksr[sb][x] & 0x7c00u) != 0x7c00u && !(sb ? b1_ : b0_))
-                top = fmaxf(top, fabsf(half_bits_to_float(static_cast<uint16_t>(ksr[sb][x]))));
+            for (int y = 0; y < C::KS; ++y)
+              if ((x.ks[sb][y] & 0x7c00u) != 0x7c00u && !((x.bad >> sb) & 1u))
+                top = fmaxf(top, fabsf(half_bits_to_float(static_cast<uint16_t>(x.ks[sb][y]))));
           int ne = static_cast<int>(__float_as_uint(kv_wave_max(top)) >> 23) - 127;
           ne = at_uniform(ne < -15 ? -15 : ne);
-          if (ne > kexp || blk == k0 + wave) {
+          if (ne > kexp || first) {
             const float f = at_exp2(static_cast<float>(ne - kexp));
             kexp = ne;
 #pragma unroll
@@ -616,7 +723,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
 #pragma unroll
           for (int st = 0; st < NS; ++st) {
             uint32_t a[4];
-            at_decode_k<C, KB>(kraw[sb], st, lane4, a);
+            at_decode_k<C, KB>(x.k[sb], st, lane4, a);
 #pragma unroll
             for (int k = 0; k < 4; ++k) a[k] = at_mul(a[k], kd[sb][C::KS == 2 ? st / (NS / 2) : 0]);
 #pragma unroll
@@ -625,49 +732,45 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
               const uint32_t qb[4] = {qv.x, qv.y, qv.z, qv.w};
               s[r][sb] = at_mfma(a, qb, s[r][sb]);
             }
-            __builtin_amdgcn_sched_barrier(0);
+            if (R > 1 || (st & 1)) __builtin_amdgcn_sched_barrier(0);
           }
-          if (sb ? b1_ : b0_) {
+          if ((x.bad >> sb) & 1u) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
               for (int i = 0; i < 4; ++i) s[r][sb][i] = __builtin_nanf("");
           }
         }
-        if (more) {
-          locate();
-          load_k();
-          kbad[0] = bad[0];
-          kbad[1] = bad[1];
-          if (blk + 2 * W < k1) look(blk + 2 * W);
-        }
-        // ---- masks ----
+      };
+      auto softmax = [&](int blk, f32x4_t (&s)[R][2], uint32_t (&pb)[R][4]) {
+        // masks
         const int j0 = blk * 32 + 4 * h;
         if (blk * 32 + 32 > cut) {
 #pragma unroll
-          for (int r = 0; r < R; ++r)
+          for (int r = 0; r < R; ++r) {
+            const int row = 16 * r + col, lim = *reinterpret_cast<const int*>(smem + C::LIM + 4 * row);
+            const int tk = (static_cast<uint32_t>(row) * p->hb_mul) >> 16;
+            const uint32_t* bits = tree + static_cast<int64_t>(sq.row0 + tok0 + (tk < ntok ? tk : 0)) * p->tree_words;
 #pragma unroll
-            for (int sb = 0; sb < 2; ++sb)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int j = j0 + 16 * sb + i;
-                bool see = j < lim[r];
-                if (p.a.tree && !see && j < sq.len) {
-                  const int x = j - before;
-                  if (x >= 0 && x < p.a.tree_words * 32)
-                    see = (p.a.tree[static_cast<int64_t>(tok_row[r]) * p.a.tree_words + (x >> 5)] >> (x & 31)) & 1u;
-                }
-                s[r][sb][i] = see ? s[r][sb][i] : -__builtin_inff();
+            for (int i = 0; i < 8; ++i) {
+              const int j = j0 + 16 * (i >> 2) + (i & 3);
+              bool see = j < lim;
+              if (tree && !see && j < len) {
+                const int x = j - before;
+                if (x >= 0 && x < p->tree_words * 32) see = (bits[x >> 5] >> (x & 31)) & 1u;
               }
+              s[r][i >> 2][i & 3] = see ? s[r][i >> 2][i & 3] : -__builtin_inff();
+            }
+          }
         }
-        // ---- softmax against a lazily moved reference ----
+        // against a lazily moved reference
         float mx[R];
         bool move = false;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           mx[r] = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
                         fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3]))) * c1[r];
-          move = move || mx[r] > mref[r] + kAtLazy;
+          move = move || mx[r] > mo[r] + (7.f + kAtLazy);
         }
         if (__any(move)) {
 #pragma unroll
@@ -676,9 +779,8 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
             kv_both<4>(mx[r], x, y);
             kv_both<5>(fmaxf(x, y), x, y);
             x = fmaxf(x, y);
-            if (x > mref[r] + kAtLazy) {  // the same in the four lanes of a row
-              const float f = at_exp2(mref[r] - x);
-              mref[r] = x;
+            if (x > mo[r] + (7.f + kAtLazy)) {  // the same in the four lanes of a row
+              const float f = at_exp2(mo[r] + 7.f - x);
               mo[r] = x - 7.f;
               l[r] *= f;
 #pragma unroll
@@ -686,53 +788,47 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
             }
           }
         }
-        uint32_t pb[R][4];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           float e[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            e[i] = at_exp2(__builtin_fmaf(s[r][i >> 2][i & 3], c1[r], -mo[r]));
-            l[r] += e[i];
-          }
+          for (int i = 0; i < 8; ++i) e[i] = at_exp2(__builtin_fmaf(s[r][i >> 2][i & 3], c1[r], -mo[r]));
+          l[r] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const half2_t x{static_cast<_Float16>(e[2 * i]), static_cast<_Float16>(e[2 * i + 1])};
             pb[r][i] = __builtin_bit_cast(uint32_t, x);
           }
         }
-        // ---- value scales: dead tokens and bad pages to zero, held times 2^-vexp ----
-        uint32_t vs[4];
-        if (blk * 32 + 32 > sq.len || b0_ || b1_) {
+      };
+      auto values = [&](AtBlock<C>& x, int blk, bool first, const f32x4_t (&s)[R][2], const uint32_t (&pb)[R][4]) {
+        // scales: dead tokens and bad pages to zero, held times 2^-vexp
+        const int j0 = blk * 32 + 4 * h;
+        if (blk * 32 + 32 > len || x.bad) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int j = j0 + 16 * (i >> 1) + 2 * (i & 1);
-            const bool dead = i < 2 ? b0_ : b1_;
-            const uint32_t m = (dead || j >= sq.len ? 0u : 0xffffu) | (dead || j + 1 >= sq.len ? 0u : 0xffff0000u);
-            vsr[i] &= m;
+            const bool dead = (x.bad >> (i >> 1)) & 1u;
+            x.vs[i] &= (dead || j >= len ? 0u : 0xffffu) | (dead || j + 1 >= len ? 0u : 0xffff0000u);
           }
         }
+        uint32_t vs[4];
         uint32_t big = 0;
-        {
-          const uint32_t sc2 = at_pow2(vexp);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            vs[i] = at_mul(vsr[i], sc2);
-            const uint32_t a = vs[i] & 0xffffu, c = vs[i] >> 16;
-            big = a > big ? a : big;
-            big = c > big ? c : big;
-          }
+        for (int i = 0; i < 4; ++i) {
+          vs[i] = at_mul(x.vs[i], at_pow2(vexp));
+          big = at_max_u16(vs[i], big);
         }
-        if (__any(big > 0x7000u) || (blk == k0 + wave && !__any(big > 0x2c00u))) {
+        big = big > (big << 16) ? big : big << 16;
+        if (__any(big > 0x7000ffffu) || (first && !__any(big > 0x2c00ffffu))) {
           float top = 0.f;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint32_t bits = (vsr[i >> 1] >> (16 * (i & 1))) & 0xffffu;
-            const bool none = (bits & 0x7c00u) == 0x7c00u;
-            const uint64_t who = __ballot(none);
+            const uint32_t bits = (x.vs[i >> 1] >> (16 * (i & 1))) & 0xffffu;
+            const uint64_t who = __ballot((bits & 0x7c00u) == 0x7c00u);
             if ((who >> (16 * h)) & 0xffffu) {
               // this token's value is no number: rows that see it become NaN, others stay
-              vsr[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
+              x.vs[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
 #pragma unroll
               for (int r = 0; r < R; ++r)
                 if (s[r][i >> 2][i & 3] != -__builtin_inff()) l[r] = __builtin_nanf("");
@@ -742,7 +838,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
           }
           int ne = static_cast<int>(__float_as_uint(kv_wave_max(top)) >> 23) - 127;
           ne = at_uniform(ne < -15 ? -15 : ne);
-          if (ne > vexp || blk == k0 + wave) {
+          if (ne > vexp || first) {
             const float f = at_exp2(static_cast<float>(vexp - ne));
             vexp = ne;
 #pragma unroll
@@ -751,41 +847,97 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
               for (int n = 0; n < CH; ++n) o[r][n] *= f;
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) vs[i] = at_mul(vsr[i], at_pow2(vexp));
+          for (int i = 0; i < 4; ++i) vs[i] = at_mul(x.vs[i], at_pow2(vexp));
         }
-        // ---- values ----
+        if constexpr (VB == 3) {
 #pragma unroll
-        for (int half = 0; half < (VB == 8 ? 1 : VB == 3 && CH == 16 ? 2 : C::VW); ++half) {
-          constexpr int PN = VB == 8 ? CH : VB == 3 ? (CH == 16 ? 8 : CH) : (CH < 32 / VB ? CH : 32 / VB);
+          for (int i = 0; i < 8; ++i) {
+            if constexpr (CH == 4) x.v[i][0] >>= 4 * (col & 1);
+            else if constexpr (CH == 8) x.v[i][0] >>= col == 15 ? 8 : 0;
+            else x.v[i][1] = (x.v[i][0] >> 24) | (x.v[i][1] << 8);
+          }
+        }
+#pragma unroll
+        for (int half = 0; half < (VB == 8 ? 1 : C::VW); ++half) {
+          constexpr int PN = VB == 8 ? CH : CH / C::VW;
           uint32_t ev[4], od[4];
           if constexpr (VB < 8) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) at_pair<VB>(vraw[2 * i][half], vraw[2 * i + 1][half], ev[i], od[i]);
+            for (int i = 0; i < 4; ++i) at_pair<VB>(x.v[2 * i][half], x.v[2 * i + 1][half], ev[i], od[i]);
           }
 #pragma unroll
           for (int n = 0; n < PN; ++n) {
             uint32_t a[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              uint32_t x;
+              uint32_t y;
               if constexpr (VB == 8) {
-                const uint32_t y = at_lds(at_byte<128>(vraw[2 * i][n >> 2], n & 3, lane4));
-                const uint32_t z = at_lds(at_byte<128>(vraw[2 * i + 1][n >> 2], n & 3, lane4));
-                x = at_pack(y, z);
+                const uint32_t y0 = at_lds(at_byte<128>(x.v[2 * i][n >> 2], n & 3, lane4));
+                const uint32_t y1 = at_lds(at_byte<128>(x.v[2 * i + 1][n >> 2], n & 3, lane4));
+                y = at_pack(y0, y1);
               } else {
-                x = at_pair_at<C, VB>((n & 1) ? od[i] : ev[i], n >> 1, lane4);
+                y = at_pair_at<C, VB>((n & 1) ? od[i] : ev[i], n >> 1, lane4);
               }
-              a[i] = at_mul(x, vs[i]);
+              a[i] = at_mul(y, vs[i]);
             }
 #pragma unroll
             for (int r = 0; r < R; ++r) o[r][half * PN + n] = at_mfma(a, pb[r], o[r][half * PN + n]);
             if (n & 1) __builtin_amdgcn_sched_barrier(0);
           }
         }
-        if (more) load_v();
+      };
+
+      bool first = true;
+      if constexpr (R == 1) {
+        // the next block's codes are loaded while this one is used
+        auto step = [&](AtBlock<C>& cur, AtBlock<C>& nxt) {
+          if (blk + W < k1) {
+            locate(nxt);
+            load_k(nxt);
+            load_v(nxt);
+            if (blk + 2 * W < k1) look(blk + 2 * W);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          f32x4_t s[R][2];
+          uint32_t pb[R][4];
+          scores(cur, first, s);
+          softmax(blk, s, pb);
+          values(cur, blk, first, s, pb);
+          first = false;
+          blk += W;
+        };
+        while (blk < k1) {
+          step(buf[0], buf[1]);
+          if (blk >= k1) break;
+          step(buf[1], buf[0]);
+        }
+      } else {
+        // the registers hold one block: its keys' make room for the next keys after the scores, its
+        // values' after the sums
+        for (; blk < k1; blk += W) {
+          const bool more = blk + W < k1;
+          AtBlock<C>& x = buf[0];
+          f32x4_t s[R][2];
+          uint32_t pb[R][4];
+          const uint32_t bad = x.bad;
+          scores(x, first, s);
+          if (more) {
+            locate(x);
+            load_k(x);
+            if (blk + 2 * W < k1) look(blk + 2 * W);
+          }
+          const uint32_t nbad = x.bad;
+          softmax(blk, s, pb);
+          x.bad = bad;
+          values(x, blk, first, s, pb);
+          x.bad = nbad;
+          if (more) load_v(x);
+          first = false;
+        }
       }
 
       // ---- join the waves ----
+      p = at_again(p);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float x, y;
@@ -793,16 +945,16 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
         kv_both<5>(x + y, x, y);
         l[r] = x + y;
         if (h == 0)
-          *reinterpret_cast<float2*>(smem + C::ML + 8 * (wave * ROWS + 16 * r + col)) = make_float2(mref[r], l[r]);
+          *reinterpret_cast<float2*>(smem + C::ML + 8 * (wave * ROWS + 16 * r + col)) = make_float2(mo[r], l[r]);
       }
       __syncthreads();
       float f[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        float top = -__builtin_inff();
+        float top = kAtNone;
 #pragma unroll
         for (int x = 0; x < W; ++x) top = fmaxf(top, *reinterpret_cast<const float*>(smem + C::ML + 8 * (x * ROWS + 16 * r + col)));
-        f[r] = mref[r] == -__builtin_inff() ? 0.f : at_exp2(mref[r] - top + static_cast<float>(vexp));
+        f[r] = mo[r] == kAtNone ? 0.f : at_exp2(mo[r] - top + static_cast<float>(vexp));
       }
       constexpr int OUT = C::NL * 16 * ROWS / T;  // sums of a thread per round
       constexpr int RND = CH / C::NL;
@@ -838,26 +990,29 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
         }
       __syncthreads();
       const bool whole = k0 == 0 && k1 == nblk;
-      float* slot = p.parts + static_cast<int64_t>(2 * blockIdx.x + (k0 > 0 ? 0 : 1)) * ROWS * (D + 2);
+      float* slot = p->parts + static_cast<int64_t>(2 * wg + (k0 > 0 ? 0 : 1)) * ROWS * (D + 2);
+#pragma unroll 1
       for (int r = wave; r < ROWS; r += W) {
-        const int tk = r / p.hb, hd = r - tk * p.hb;
+        const int tk = (static_cast<uint32_t>(r) * p->hb_mul) >> 16, hd = r - tk * hb;
         if (tk >= ntok || hd >= nh) continue;
-        float top = -__builtin_inff(), ls = 0.f;
-#pragma unroll
-        for (int x = 0; x < W; ++x) top = fmaxf(top, *reinterpret_cast<const float*>(smem + C::ML + 8 * (x * ROWS + r)));
+        float2 ml[W];
+        float top = kAtNone, ls = 0.f;
 #pragma unroll
         for (int x = 0; x < W; ++x) {
-          const float2 ml = *reinterpret_cast<const float2*>(smem + C::ML + 8 * (x * ROWS + r));
-          ls += ml.x == -__builtin_inff() ? (ml.y != ml.y ? ml.y : 0.f) : ml.y * at_exp2(ml.x - top);
+          ml[x] = *reinterpret_cast<const float2*>(smem + C::ML + 8 * (x * ROWS + r));
+          top = fmaxf(top, ml[x].x);
         }
+#pragma unroll
+        for (int x = 0; x < W; ++x)  // a wave that saw nothing adds nothing, unless its sum is no number
+          ls += ml[x].x == kAtNone ? (ml[x].y != ml[x].y ? ml[x].y : 0.f) : ml[x].y * at_exp2(ml[x].x - top);
         float v[EL];
 #pragma unroll
-        for (int e = 0; e < EL; ++e) v[e] = red[r * C::FP + kv_chunk(lane) * EL + e];
+        for (int e = 0; e < EL; ++e) v[e] = red[r * C::FP + d0 + e];
         if (whole) {
-          at_finish<D>(p, v, ls, sq.row0 + tok0 + tk, head0 + hd, lane);
+          at_finish<D>(p, v, ls, static_cast<int64_t>(sq.row0) + tok0 + tk, head0 + hd, vsg, lane);
         } else {
 #pragma unroll
-          for (int e = 0; e < EL; ++e) slot[r * D + kv_chunk(lane) * EL + e] = v[e];
+          for (int e = 0; e < EL; ++e) slot[r * D + d0 + e] = v[e];
           if (lane == 0) {
             slot[ROWS * D + r] = top;
             slot[ROWS * D + ROWS + r] = ls;
@@ -865,18 +1020,19 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
         }
       }
       if (!whole && k0 == 0 && tid == 0) {
-        // the workgroups that go on with this unit: shares that hold the start of one of its blocks
-        const int64_t last = u0 + kAtUnit + static_cast<int64_t>(nblk - 1) * 32;  // the last block's place on the line
+        // the workgroups that go on with this unit: its other parts, or the shares of the line
+        // that hold the begin of one of its blocks
         AttendMeta m{};
-        m.parts = static_cast<int>(last / q) - static_cast<int>(blockIdx.x);
+        m.parts = own ? np - 1 : static_cast<int>((u0 + kAtUnit + static_cast<int64_t>(nblk - 1) * 32) / q) - wg;
         m.row0 = sq.row0 + tok0;
         m.nrows = ntok;
         m.head0 = head0;
-        m.hb = nh;
-        p.meta[blockIdx.x] = m;
+        m.nh = nh;
+        p->meta[wg] = m;
       }
     }
     // ---- next unit ----
+    if (own) break;
     u0 += reads + kAtUnit;
     w = u0;
     if (w >= w1) break;
@@ -886,7 +1042,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
         hu = 0;
         do {
           ++b;
-          sq = at_seq<true>(p, b);
+          sq = at_seq(p, at_uniform(at_raw(p, b)));
         } while (sq.tiles == 0);
       }
     }
@@ -899,13 +1055,13 @@ hipError_t at_launch(const AttendParams& p, hipStream_t s) {
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend<KB, VB, D, R>),
                                      hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_attend<KB, VB, D, R>), dim3(p.grid), dim3(C::T), C::LDS, s, p);
+  hipLaunchKernelGGL((k_attend<KB, VB, D, R>), dim3(C::GRID), dim3(C::T), C::LDS, s, p);
   return hipGetLastError();
 }
 
 template <int KB, int VB>
-hipError_t at_launch_d(const AttendParams& p, int R, hipStream_t s) {
-  switch (p.a.c.D) {
+hipError_t at_launch_d(const AttendParams& p, int D, int R, hipStream_t s) {
+  switch (D) {
     case 64: return R == 1 ? at_launch<KB, VB, 64, 1>(p, s) : at_launch<KB, VB, 64, 4>(p, s);
     case 128: return R == 1 ? at_launch<KB, VB, 128, 1>(p, s) : at_launch<KB, VB, 128, 4>(p, s);
     default: return R == 1 ? at_launch<KB, VB, 256, 1>(p, s) : at_launch<KB, VB, 256, 2>(p, s);
@@ -914,12 +1070,12 @@ hipError_t at_launch_d(const AttendParams& p, int R, hipStream_t s) {
 
 // One key format's kernels.
 template <int KB>
-hipError_t at_launch_k(const AttendParams& p, int R, hipStream_t s) {
-  switch (p.a.c.v.bits) {
-    case 2: return at_launch_d<KB, 2>(p, R, s);
-    case 3: return at_launch_d<KB, 3>(p, R, s);
-    case 4: return at_launch_d<KB, 4>(p, R, s);
-    default: return at_launch_d<KB, 8>(p, R, s);
+hipError_t at_launch_k(const AttendParams& p, int vbits, int D, int R, hipStream_t s) {
+  switch (vbits) {
+    case 2: return at_launch_d<KB, 2>(p, D, R, s);
+    case 3: return at_launch_d<KB, 3>(p, D, R, s);
+    case 4: return at_launch_d<KB, 4>(p, D, R, s);
+    default: return at_launch_d<KB, 8>(p, D, R, s);
   }
 }
 

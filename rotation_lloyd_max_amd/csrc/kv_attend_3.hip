@@ -3,6 +3,6 @@
 
 namespace tq {
 
-template hipError_t at_launch_k<3>(const AttendParams& p, int R, hipStream_t s);
+template hipError_t at_launch_k<3>(const AttendParams& p, int vbits, int D, int R, hipStream_t s);
 
 }  // namespace tq
