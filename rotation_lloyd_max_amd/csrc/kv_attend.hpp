@@ -248,22 +248,41 @@ __device__ __forceinline__ int64_t at_lane(int64_t x, int lane) {
 }
 
 // ---- decoding -----------------------------------------------------------------------------
-// Eight key codes (number st of the lane's quarter row) as four fp16 pairs.
+// the larger of each half, as unsigned numbers (scales are not negative)
+__device__ __forceinline__ uint32_t at_max_u16(uint32_t a, uint32_t b) {
+  typedef uint16_t V __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b)));
+}
+__device__ __forceinline__ uint32_t at_mul(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, a) * __builtin_bit_cast(half2_t, b));
+}
+// 2^-e in both halves, -15 <= e <= 14; 2^-15 as the subnormal it is
+__device__ __forceinline__ uint32_t at_pow2(int e) {
+  const uint32_t x = e < 15 ? static_cast<uint32_t>(15 - e) << 10 : 0x0200u;
+  return x | (x << 16);
+}
+__device__ __forceinline__ f32x4_t at_mfma(const uint32_t (&a)[4], const uint32_t (&b)[4], f32x4_t c) {
+  const u32x4_t x{a[0], a[1], a[2], a[3]}, y{b[0], b[1], b[2], b[3]};
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, x), __builtin_bit_cast(f16x8_t, y), c, 0, 0, 0);
+}
+
+// The table reads for eight key codes (number st of the lane's quarter row): one per code of 8
+// bits, one per pair of smaller ones.
+template <int KB>
+struct AtLook {
+  static constexpr int N = KB == 8 ? 8 : 4;
+  uint32_t t[N];
+};
 template <typename C, int KB>
-__device__ __forceinline__ void at_decode_k(const uint32_t* w, int st, uint32_t lane4, uint32_t (&o)[4]) {
+__device__ __forceinline__ void at_look_k(const uint32_t* w, int st, uint32_t lane4, AtLook<KB>& o) {
   if constexpr (KB == 8) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t x = w[2 * st + (k >> 1)];
-      const uint32_t a = at_lds(at_byte<128>(x, 2 * (k & 1), lane4));
-      const uint32_t b = at_lds(at_byte<128>(x, 2 * (k & 1) + 1, lane4));
-      o[k] = at_pack(a, b);
-    }
+    for (int k = 0; k < 8; ++k) o.t[k] = at_lds(at_byte<128>(w[2 * st + (k >> 2)], k & 3, lane4));
   } else if constexpr (KB == 4) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if constexpr (C::KWIDE) o[k] = at_lds(at_byte<128>(w[st], k, lane4));
-      else o[k] = at_lds(C::TK + (at_byte<4>(w[st], k, 0)));
+      if constexpr (C::KWIDE) o.t[k] = at_lds(at_byte<128>(w[st], k, lane4));
+      else o.t[k] = at_lds(C::TK + at_byte<4>(w[st], k, 0));
     }
   } else {
     // pairs of 2 KB bits of the bitstream; a table index times four
@@ -274,9 +293,15 @@ __device__ __forceinline__ void at_decode_k(const uint32_t* w, int st, uint32_t 
       uint32_t x;
       if (sh + 2 * KB > 32) x = static_cast<uint32_t>((static_cast<uint64_t>(w[wi + 1]) << 32 | w[wi]) >> (sh - 2));
       else x = sh < 2 ? w[wi] << (2 - sh) : w[wi] >> (sh - 2);
-      o[k] = at_lds(C::TK + (x & M));
+      o.t[k] = at_lds(C::TK + (x & M));
     }
   }
+}
+// What was read as four fp16 pairs, times the scale.
+template <int KB>
+__device__ __forceinline__ void at_pairs_k(const AtLook<KB>& x, uint32_t scale, uint32_t (&o)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) o[k] = at_mul(KB == 8 ? at_pack(x.t[(2 * k) % AtLook<KB>::N], x.t[(2 * k + 1) % AtLook<KB>::N]) : x.t[k], scale);
 }
 
 // Element n of a value piece of the tokens with words w0 and w1, as an fp16 pair. e and o are
@@ -298,24 +323,6 @@ __device__ __forceinline__ uint32_t at_pair_at(uint32_t x, int q, uint32_t lane4
   } else {
     return at_lds(C::TV + ((q == 0 ? x << 2 : x >> (4 * q - 2)) & 0x3cu));
   }
-}
-
-// the larger of each half, as unsigned numbers (scales are not negative)
-__device__ __forceinline__ uint32_t at_max_u16(uint32_t a, uint32_t b) {
-  typedef uint16_t V __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b)));
-}
-__device__ __forceinline__ uint32_t at_mul(uint32_t a, uint32_t b) {
-  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, a) * __builtin_bit_cast(half2_t, b));
-}
-// 2^-e in both halves, -15 <= e <= 14; 2^-15 as the subnormal it is
-__device__ __forceinline__ uint32_t at_pow2(int e) {
-  const uint32_t x = e < 15 ? static_cast<uint32_t>(15 - e) << 10 : 0x0200u;
-  return x | (x << 16);
-}
-__device__ __forceinline__ f32x4_t at_mfma(const uint32_t (&a)[4], const uint32_t (&b)[4], f32x4_t c) {
-  const u32x4_t x{a[0], a[1], a[2], a[3]}, y{b[0], b[1], b[2], b[3]};
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, x), __builtin_bit_cast(f16x8_t, y), c, 0, 0, 0);
 }
 
 // A block's codes and scales as loaded: a quarter row of token l % 16 of each half for the scores,
@@ -717,30 +724,36 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
           key_scales();
         }
 #pragma unroll
-        for (int sb = 0; sb < 2; ++sb) {
+        for (int r = 0; r < R; ++r) s[r][0] = s[r][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        // the next step's table reads are on their way while this one's results are multiplied
+        AtLook<KB> look2[2];
+        at_look_k<C, KB>(x.k[0], 0, lane4, look2[0]);
 #pragma unroll
-          for (int r = 0; r < R; ++r) s[r][sb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int y = 0; y < 2 * NS; ++y) {
+          const int sb = y / NS, st = y % NS;
+          if (y + 1 < 2 * NS) at_look_k<C, KB>(x.k[(y + 1) / NS], (y + 1) % NS, lane4, look2[(y + 1) & 1]);
+          u32x4_t qv[R];
 #pragma unroll
-          for (int st = 0; st < NS; ++st) {
-            uint32_t a[4];
-            at_decode_k<C, KB>(x.k[sb], st, lane4, a);
+          for (int r = 0; r < R; ++r)
+            qv[r] = *reinterpret_cast<const u32x4_t*>(smem + C::QS + (16 * r + col) * C::QP + (D / 2) * h + 16 * st);
+          __builtin_amdgcn_sched_barrier(0);
+          uint32_t a[4];
+          at_pairs_k<KB>(look2[y & 1], kd[sb][C::KS == 2 ? st / (NS / 2) : 0], a);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) a[k] = at_mul(a[k], kd[sb][C::KS == 2 ? st / (NS / 2) : 0]);
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              const u32x4_t qv = *reinterpret_cast<const u32x4_t*>(smem + C::QS + (16 * r + col) * C::QP + (D / 2) * h + 16 * st);
-              const uint32_t qb[4] = {qv.x, qv.y, qv.z, qv.w};
-              s[r][sb] = at_mfma(a, qb, s[r][sb]);
-            }
-            if (R > 1 || (st & 1)) __builtin_amdgcn_sched_barrier(0);
+          for (int r = 0; r < R; ++r) {
+            const uint32_t qb[4] = {qv[r].x, qv[r].y, qv[r].z, qv[r].w};
+            s[r][sb] = at_mfma(a, qb, s[r][sb]);
           }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int sb = 0; sb < 2; ++sb)
           if ((x.bad >> sb) & 1u) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
               for (int i = 0; i < 4; ++i) s[r][sb][i] = __builtin_nanf("");
           }
-        }
       };
       auto softmax = [&](int blk, f32x4_t (&s)[R][2], uint32_t (&pb)[R][4]) {
         // masks
@@ -857,61 +870,51 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
             else x.v[i][1] = (x.v[i][0] >> 24) | (x.v[i][1] << 8);
           }
         }
+        constexpr int HALVES = VB == 8 ? 1 : C::VW, PN = CH / HALVES;  // words of a piece, elements of a word
+        uint32_t ev[HALVES][4], od[HALVES][4];
+        if constexpr (VB < 8) {
 #pragma unroll
-        for (int half = 0; half < (VB == 8 ? 1 : C::VW); ++half) {
-          constexpr int PN = VB == 8 ? CH : CH / C::VW;
-          uint32_t ev[4], od[4];
-          if constexpr (VB < 8) {
+          for (int y = 0; y < HALVES; ++y)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) at_pair<VB>(x.v[2 * i][half], x.v[2 * i + 1][half], ev[i], od[i]);
+            for (int i = 0; i < 4; ++i) at_pair<VB>(x.v[2 * i][y], x.v[2 * i + 1][y], ev[y][i], od[y][i]);
+        }
+        // element n of the eight tokens: the table reads, one element ahead of the products
+        constexpr int NT = VB == 8 ? 8 : 4;
+        auto look_v = [&](int n, uint32_t (&tb)[NT]) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            if constexpr (VB == 8) tb[i] = at_lds(at_byte<128>(x.v[i][n >> 2], n & 3, lane4));
+            else tb[i] = at_pair_at<C, VB>((n & 1) ? od[n / PN][i] : ev[n / PN][i], (n % PN) >> 1, lane4);
           }
+        };
+        constexpr int STEP = NT == 8 ? 1 : 2;  // elements of a step: eight table reads
+        uint32_t tb[2][STEP][NT];
 #pragma unroll
-          for (int n = 0; n < PN; ++n) {
+        for (int y = 0; y < STEP; ++y) look_v(y, tb[0][y]);
+#pragma unroll
+        for (int n = 0; n < CH; n += STEP) {
+          if (n + STEP < CH) {
+#pragma unroll
+            for (int y = 0; y < STEP; ++y) look_v(n + STEP + y, tb[((n / STEP) + 1) & 1][y]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int y = 0; y < STEP; ++y) {
             uint32_t a[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              uint32_t y;
-              if constexpr (VB == 8) {
-                const uint32_t y0 = at_lds(at_byte<128>(x.v[2 * i][n >> 2], n & 3, lane4));
-                const uint32_t y1 = at_lds(at_byte<128>(x.v[2 * i + 1][n >> 2], n & 3, lane4));
-                y = at_pack(y0, y1);
-              } else {
-                y = at_pair_at<C, VB>((n & 1) ? od[i] : ev[i], n >> 1, lane4);
-              }
-              a[i] = at_mul(y, vs[i]);
+              const uint32_t* z = tb[(n / STEP) & 1][y];
+              a[i] = at_mul(VB == 8 ? at_pack(z[(2 * i) % NT], z[(2 * i + 1) % NT]) : z[i], vs[i]);
             }
 #pragma unroll
-            for (int r = 0; r < R; ++r) o[r][half * PN + n] = at_mfma(a, pb[r], o[r][half * PN + n]);
-            if (n & 1) __builtin_amdgcn_sched_barrier(0);
+            for (int r = 0; r < R; ++r) o[r][n + y] = at_mfma(a, pb[r], o[r][n + y]);
           }
+          __builtin_amdgcn_sched_barrier(0);
         }
       };
 
       bool first = true;
-      if constexpr (R == 1) {
-        // the next block's codes are loaded while this one is used
-        auto step = [&](AtBlock<C>& cur, AtBlock<C>& nxt) {
-          if (blk + W < k1) {
-            locate(nxt);
-            load_k(nxt);
-            load_v(nxt);
-            if (blk + 2 * W < k1) look(blk + 2 * W);
-          }
-          __builtin_amdgcn_sched_barrier(0);
-          f32x4_t s[R][2];
-          uint32_t pb[R][4];
-          scores(cur, first, s);
-          softmax(blk, s, pb);
-          values(cur, blk, first, s, pb);
-          first = false;
-          blk += W;
-        };
-        while (blk < k1) {
-          step(buf[0], buf[1]);
-          if (blk >= k1) break;
-          step(buf[1], buf[0]);
-        }
-      } else {
+      {
         // the registers hold one block: its keys' make room for the next keys after the scores, its
         // values' after the sums
         for (; blk < k1; blk += W) {
