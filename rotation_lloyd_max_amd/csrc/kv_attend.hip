@@ -17,9 +17,9 @@ constexpr size_t kMetaBytes = sizeof(AttendMeta) * kAtMaxGrid;
 // 16-row blocks of a tile, and the workgroups of a launch.
 int tile_blocks(int D, int share, int B, int64_t M) {
   const int64_t rows = (M * share + B - 1) / B;  // query rows per key head and sequence
-  return rows <= 16 ? 1 : D == 256 ? 2 : 4;
+  return rows <= 16 ? 1 : D == 256 ? 2 : 3;
 }
-int workgroups(int D, int R) { return (R == 1 && D <= 128 ? 3 : 2) * kAtCus; }
+int workgroups(int D, int R) { return (R == 1 && D <= 128 ? 3 : R > 1 && D == 256 ? 1 : 2) * kAtCus; }
 
 // What the join needs of the arguments.
 struct JoinParams {
@@ -66,16 +66,22 @@ __global__ __launch_bounds__(256) void k_attend_join(JoinParams p) {
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) l += __shfl_xor(l, x);
   wave_lds_sync();
+  // sixteen parts' loads at a time (past the last one: that one again, times zero)
   float v[EL] = {};
-  const float* s = base + slot + r * D + d0;
+  for (int i0 = 0; i0 < n; i0 += 16) {
+    float x[16][EL];
 #pragma unroll
-  for (int e = 0; e < EL; ++e) v[e] = wt[wave][0] * s[e];
-  s = base + r * D + d0;
-#pragma unroll 8
-  for (int i = 1; i < n; ++i) {
-    const float f = wt[wave][i];
+    for (int k = 0; k < 16; ++k) {
+      const float* s = part(i0 + k < n ? i0 + k : n - 1) + r * D + d0;
 #pragma unroll
-    for (int e = 0; e < EL; ++e) v[e] = __builtin_fmaf(f, s[2 * i * slot + e], v[e]);
+      for (int e = 0; e < EL; ++e) x[k][e] = s[e];
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float f = i0 + k < n ? wt[wave][i0 + k] : 0.f;
+#pragma unroll
+      for (int e = 0; e < EL; ++e) v[e] = __builtin_fmaf(f, x[k][e], v[e]);
+    }
   }
   at_finish<D>(&p, v, l, static_cast<int64_t>(m.row0) + tk, m.head0 + hd, sg, lane);
 }

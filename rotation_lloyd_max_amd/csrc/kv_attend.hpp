@@ -37,7 +37,8 @@ namespace tq {
 constexpr int kAtCus = 256;
 constexpr int kAtMaxGrid = 3 * kAtCus;  // workgroups of a launch, at most
 constexpr int kAtUnit = 256;            // a unit's set-up in tokens of work
-constexpr int kAtMinShare = 384;        // least work of a share
+constexpr int kAtMinShare = 512;        // least work of a share
+constexpr int kAtMinBlocks = 4;         // least blocks of a part: one per wave
 constexpr float kAtLazy = 8.f;          // log2 of how far a score may pass the reference
 constexpr float kAtNone = -3e38f;       // reference of a row that has seen nothing
 
@@ -90,7 +91,7 @@ struct AtCfg {
   static constexpr int KW = (KROW / 4 + 3) / 4;               // words of a quarter key row
   static constexpr int KS = D == 256 ? 2 : 1;                 // key scales of a quarter row, at most
   static constexpr int VW = (VB * CH + 31) / 32;              // words of a value piece
-  static constexpr int WGS = R == 1 && D <= 128 ? 3 : 2;      // workgroups per CU
+  static constexpr int WGS = R == 1 && D <= 128 ? 3 : R > 1 && D == 256 ? 1 : 2;  // workgroups per CU
   static constexpr int GRID = WGS * kAtCus;
   // LDS; the joined sums take the place of q
   static constexpr int WIDE = (KWIDE || VWIDE) ? 32768 : 0;
@@ -132,9 +133,16 @@ typedef const __attribute__((address_space(1))) char* AtPtr;
 __device__ __forceinline__ AtPtr at_base(const void* base, int64_t bytes) {
   return (AtPtr)(at_uniform(reinterpret_cast<int64_t>(base) + bytes));
 }
+// (constants go to `base`, where they become the load's immediate offset)
 template <typename T>
 __device__ __forceinline__ T at_get(AtPtr base, uint32_t off) {
   return *(const __attribute__((address_space(1))) T*)(base + off);
+}
+// x as a value the compiler knows nothing of: what is computed from it is not kept from one place
+// to another
+__device__ __forceinline__ int at_fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
 }
 // a load at any byte address
 template <typename T>
@@ -150,6 +158,14 @@ __device__ __forceinline__ int at_div(int x, int d, uint32_t mul) {
   uint32_t y = mul ? __umulhi(u, mul) : u;
   y -= static_cast<uint64_t>(y) * d > u ? 1u : 0u;
   return static_cast<int>(y);
+}
+
+// ceil(x / d) for 0 < x < 2^27, d >= 1: an fp32 quotient, at most one off, put right
+__device__ __forceinline__ int at_ceil_div(int x, int d) {
+  int y = static_cast<int>(static_cast<float>(x) * __builtin_amdgcn_rcpf(static_cast<float>(d)));
+  y -= static_cast<int64_t>(y) * d >= x ? 1 : 0;
+  y += static_cast<int64_t>(y + 1) * d <= x - 1 ? 1 : 0;
+  return y + 1;
 }
 
 // Normalises, rotates back and stores one output row held as in kv_wave_transform; sg: the lane's
@@ -180,6 +196,7 @@ struct AtSeq {
   int row0, n, len, tiles;
   int flat;          // 1: every tile reads the whole length (trees; more queries than tokens)
   int64_t per_head;  // cost of all tiles of one head
+  __device__ __forceinline__ int blocks() const { return len > 1 ? (len + 31) >> 5 : 1; }  // of a tile, if flat or alone
 };
 
 __device__ __forceinline__ int64_t at_before(const AtSeq& s, int a, int t) {  // cost of tiles < t, t < tiles
@@ -228,18 +245,27 @@ struct AtInt {
   static constexpr int value = V;
 };
 // Inclusive sum over the lanes of a wave (row shifts, then the rows' last lanes broadcast).
-__device__ __forceinline__ int64_t at_scan(int64_t x) {
-  auto step = [&](auto ctrl, auto rows) {
-    const int lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(x), decltype(ctrl)::value, decltype(rows)::value, 0xf, false);
-    const int hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(x >> 32), decltype(ctrl)::value, decltype(rows)::value, 0xf, false);
-    x += static_cast<int64_t>(hi) << 32 | static_cast<uint32_t>(lo);
-  };
-  step(AtInt<0x111>{}, AtInt<0xf>{});
-  step(AtInt<0x112>{}, AtInt<0xf>{});
-  step(AtInt<0x114>{}, AtInt<0xf>{});
-  step(AtInt<0x118>{}, AtInt<0xf>{});
-  step(AtInt<0x142>{}, AtInt<0xa>{});
-  step(AtInt<0x143>{}, AtInt<0xc>{});
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int at_shift(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float at_shift(float x) {
+  return __int_as_float(at_shift<CTRL, ROWS>(__float_as_int(x)));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t at_shift(int64_t x) {
+  return static_cast<int64_t>(at_shift<CTRL, ROWS>(static_cast<int>(x >> 32))) << 32 |
+         static_cast<uint32_t>(at_shift<CTRL, ROWS>(static_cast<int>(x)));
+}
+template <typename T>
+__device__ __forceinline__ T at_scan(T x) {
+  x += at_shift<0x111, 0xf>(x);
+  x += at_shift<0x112, 0xf>(x);
+  x += at_shift<0x114, 0xf>(x);
+  x += at_shift<0x118, 0xf>(x);
+  x += at_shift<0x142, 0xa>(x);
+  x += at_shift<0x143, 0xc>(x);
   return x;
 }
 __device__ __forceinline__ int64_t at_lane(int64_t x, int lane) {
@@ -329,12 +355,12 @@ __device__ __forceinline__ uint32_t at_pair_at(uint32_t x, int q, uint32_t lane4
 // a piece of eight tokens' rows for the sums.
 template <typename C>
 struct AtBlock {
-  uint32_t k[2][C::KW], v[8][C::VW], ks[2][C::KS], vs[4];
+  uint32_t k[2][C::KW], v[8][C::VW], ks[2][C::KS], vs[8];  // vs: see load_v and pair_scales
   uint32_t bad;  // uniform; bit x: the page of half x is none
 };
 
 template <int KB, int VB, int D, int R>
-__global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS)) void k_attend(AttendParams) {
+__global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS * AtCfg<KB, VB, D, R>::W / 4)) void k_attend(AttendParams) {
   using C = AtCfg<KB, VB, D, R>;
   constexpr int W = C::W, T = C::T, ROWS = C::ROWS, NS = C::NS, CH = C::CH, EL = D / 64;
   extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -350,8 +376,6 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
   const int b0 = lane * per;
   AtRaw raw0{0, 0, 0};
   if (b0 < p->B) raw0 = at_raw(p, b0);
-  const int ch = kv_chunk(lane), d0 = ch * EL;
-  const uint32_t ksg = p->ksigns[d0 >> 5] >> (d0 & 31), vsg = p->vsigns[d0 >> 5] >> (d0 & 31);
 
   // centroid tables, while those loads are on their way. A wave's entries are uniform: scalar
   // loads of the arguments, two 128-byte rows per store.
@@ -380,65 +404,73 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
   if (tid == 0) p->meta[wg].parts = 0;
   const AtSeq seq0 = at_seq(p, raw0);
   const int b1 = b0 + per < p->B ? b0 + per : p->B;
-  // cost and units of the lane's sequences; even: every tile of a head costs the same
-  int64_t sum = 0, units = 0;
+  // units and blocks of the lane's sequences; even: every tile of a head costs the same
+  int units = 0;
+  float blocks = 0.f;
   bool even = true;
   for (int b = b0; b < b1; ++b) {
     const AtSeq x = b == b0 ? seq0 : at_seq(p, at_raw(p, b));
-    sum += x.per_head * hu_n;
-    units += static_cast<int64_t>(x.tiles) * hu_n;
+    const int u = x.tiles * hu_n;
+    units = units + u < C::GRID ? units + u : C::GRID;
+    blocks += static_cast<float>(u) * static_cast<float>(x.blocks());
     even = even && (x.flat || x.tiles <= 1);
   }
-  int64_t incl = at_scan(sum);
-  int64_t total = at_lane(incl, 63);
-  const int64_t all_units = at_lane(at_scan(units), 63);
-  // with few units, each is cut into parts of about q of work, one part per workgroup:
-  // q = total / (GRID - units) gives at most GRID parts. Otherwise the line is cut every q.
+  const int all_units = __builtin_amdgcn_readlane(at_scan(units), 63);
+  // With few units, each is cut into parts of at most `chunk` blocks, one part per workgroup:
+  // sum ceil(blocks / chunk) <= sum blocks / chunk + units <= GRID (the sum in fp32 is rounded up).
+  // Otherwise the line is cut every q.
   const bool own = !__any(!even) && all_units <= C::GRID / 2;
-  int64_t q = own ? static_cast<int64_t>(static_cast<double>(total) / static_cast<double>(C::GRID - all_units)) + 1
-                  : total / C::GRID + 1;
-  q = at_uniform(q < kAtMinShare ? kAtMinShare : q);
-  const int q32 = static_cast<int>(q < 0x7fffffff ? q : 0x7fffffff);
-  auto parts_of = [&](const AtSeq& x) {  // of a unit of an even sequence
-    const int c = (x.len > 1 ? x.len : 1) + kAtUnit;
-    int y = static_cast<int>(static_cast<float>(c) / static_cast<float>(q32));
-    while (static_cast<int64_t>(y) * q32 < c) ++y;
-    return y;
-  };
-  if (own) {  // the same scan in parts
-    sum = 0;
+  int chunk = 0;
+  int64_t q = 0, w0, w1, excl;
+  int src;
+  if (own) {
+    const float all = at_scan(blocks) * (1.f + 0x1p-16f) / static_cast<float>(C::GRID - all_units);
+    chunk = static_cast<int>(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(all), 63))) + 1;
+    chunk = chunk < kAtMinBlocks ? kAtMinBlocks : chunk;
+    int parts = 0;
     for (int b = b0; b < b1; ++b) {
       const AtSeq x = b == b0 ? seq0 : at_seq(p, at_raw(p, b));
-      if (x.tiles > 0) sum += static_cast<int64_t>(x.tiles) * hu_n * parts_of(x);
+      parts += x.tiles * hu_n * at_ceil_div(x.blocks(), chunk);
     }
-    incl = at_scan(sum);
-    total = at_lane(incl, 63);
+    const int incl = at_scan(parts);
+    w0 = wg;
+    w1 = wg + 1;
+    if (wg >= __builtin_amdgcn_readlane(incl, 63)) return;
+    src = __builtin_ctzll(__ballot(incl > wg));
+    excl = __builtin_amdgcn_readlane(incl - parts, src);
+  } else {
+    int64_t sum = 0;
+    for (int b = b0; b < b1; ++b) sum += (b == b0 ? seq0 : at_seq(p, at_raw(p, b))).per_head * hu_n;
+    const int64_t incl = at_scan(sum), total = at_lane(incl, 63);
+    q = total / C::GRID + 1;
+    q = q < kAtMinShare ? kAtMinShare : q;
+    w0 = q * wg;
+    w1 = w0 + q < total ? w0 + q : total;
+    if (w0 >= total) return;
+    src = __builtin_ctzll(__ballot(incl > w0));
+    excl = at_lane(incl - sum, src);
   }
-  const int64_t w0 = own ? wg : q * wg;
-  const int64_t w1 = own ? w0 + 1 : w0 + q < total ? w0 + q : total;
-  if (w0 >= total) return;
-  // the lane that holds w0, then the sequence among its own
-  const int src = __builtin_ctzll(__ballot(incl > w0));
-  int64_t rem = at_uniform(w0 - at_lane(incl - sum, src));
+  // the sequence, among those of the lane that holds w0
+  int64_t rem = at_uniform(w0 - excl);
   int b = src * per;
   AtSeq sq = at_seq(p, AtRaw{__builtin_amdgcn_readlane(raw0.len, src), __builtin_amdgcn_readlane(raw0.lo, src),
                              __builtin_amdgcn_readlane(raw0.hi, src)});
   auto work_of = [&](const AtSeq& x) {
-    return x.tiles == 0 ? int64_t{0} : own ? static_cast<int64_t>(x.tiles) * hu_n * parts_of(x) : x.per_head * hu_n;
+    return own ? static_cast<int64_t>(x.tiles * hu_n * at_ceil_div(x.blocks(), chunk)) : x.per_head * hu_n;
   };
-  for (int64_t x = work_of(sq); rem >= x; x = work_of(sq)) {
-    rem = at_uniform(rem - x);
-    ++b;
-    sq = at_seq(p, at_uniform(at_raw(p, b)));
-  }
+  if (per > 1)
+    for (int64_t x = work_of(sq); rem >= x; x = work_of(sq)) {
+      rem = at_uniform(rem - x);
+      ++b;
+      sq = at_seq(p, at_uniform(at_raw(p, b)));
+    }
   int hu, t, part = 0, np = 1;
   int64_t u0 = 0;  // the unit's begin on the line
   if (own) {
-    np = at_uniform(parts_of(sq));
-    const int r32 = static_cast<int>(rem);  // below GRID
-    const int unit = r32 / np;
-    part = r32 - unit * np;
-    hu = unit / sq.tiles;
+    np = at_uniform(at_ceil_div(sq.blocks(), chunk));
+    const int unit = at_uniform(at_ceil_div(static_cast<int>(rem) + 1, np) - 1);
+    part = static_cast<int>(rem) - unit * np;
+    hu = sq.tiles == 1 ? unit : at_ceil_div(unit + 1, sq.tiles) - 1;
     t = unit - hu * sq.tiles;
   } else {
     // rem < 2^53, so the quotient in fp64 is at most one off
@@ -457,7 +489,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
   }
 
   const uint32_t koff = col * C::KROW + (C::KROW / 4) * h;
-  const uint32_t voff = 4 * h * C::VROW + (VB * CH * col) / 8;
+  const uint32_t voff = 4 * h * C::VROW + (VB * CH * col) / 8, vback = voff - (col == 15 ? 1 : 0);
   // scales of the quarter row's first and (D = 256) second half, and of the value piece
   const uint32_t ksoff = ((col << p->lg_gk) + ((D / 4 * h) >> p->lg_kg)) * 2;
   const uint32_t ksoff2 = ((col << p->lg_gk) + ((D / 4 * h + D / 8) >> p->lg_kg)) * 2;
@@ -480,8 +512,9 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
     const int nblk = (reads + 31) >> 5;
     int k0, k1;
     if (own) {
-      k0 = static_cast<int>(static_cast<int64_t>(nblk) * part / np);
-      k1 = static_cast<int>(static_cast<int64_t>(nblk) * (part + 1) / np);
+      const int each = at_ceil_div(nblk, np);  // evenly; the last part may be short or empty
+      k0 = part * each < nblk ? part * each : nblk;
+      k1 = k0 + each < nblk ? k0 + each : nblk;
     } else {
       const int64_t x0 = w - u0 - kAtUnit, x1 = w1 - u0 - kAtUnit < reads ? w1 - u0 - kAtUnit : reads;
       k0 = x0 <= 0 ? 0 : static_cast<int>((x0 + 31) >> 5);
@@ -537,21 +570,21 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
           constexpr int L = C::KW % 4 == 0 ? 4 : C::KW % 3 == 0 ? 3 : C::KW % 2 == 0 ? 2 : 1;  // words of a load
           if constexpr (C::KROW % 16 != 0) {  // six bytes
             x.k[sb][0] = at_load<uint32_t>(kc, koff);
-            x.k[sb][1] = at_load<uint16_t>(kc, koff + 4);
+            x.k[sb][1] = at_load<uint16_t>(kc + 4, koff);
           } else {
 #pragma unroll
             for (int k = 0; k < C::KW; k += L) {
               if constexpr (L == 4) {
-                const u32x4_t y = at_get<u32x4_t>(kc, koff + 4 * k);
+                const u32x4_t y = at_get<u32x4_t>(kc + 4 * k, koff);
                 x.k[sb][k] = y.x; x.k[sb][k + 1] = y.y; x.k[sb][k + 2] = y.z; x.k[sb][k + 3] = y.w;
               } else if constexpr (L == 3) {
-                const u32x3_t y = at_get<u32x3_t>(kc, koff + 4 * k);
+                const u32x3_t y = at_get<u32x3_t>(kc + 4 * k, koff);
                 x.k[sb][k] = y.x; x.k[sb][k + 1] = y.y; x.k[sb][k + 2] = y.z;
               } else if constexpr (L == 2) {
-                const u32x2_t y = at_get<u32x2_t>(kc, koff + 4 * k);
+                const u32x2_t y = at_get<u32x2_t>(kc + 4 * k, koff);
                 x.k[sb][k] = y.x; x.k[sb][k + 1] = y.y;
               } else {
-                x.k[sb][k] = at_get<uint32_t>(kc, koff + 4 * k);
+                x.k[sb][k] = at_get<uint32_t>(kc + 4 * k, koff);
               }
             }
           }
@@ -561,117 +594,145 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
         }
       };
       auto load_v = [&](AtBlock<C>& x) {
-#pragma unroll
-        for (int sb = 0; sb < 2; ++sb) {
+        auto one = [&](auto half) {
+          constexpr int sb = decltype(half)::value;
           const AtPtr vc = at_base(vcodes, row_of[sb] * C::VROW);
           const AtPtr sp = at_base(vscales, row_of[sb] << (lgv + 1));
 #pragma unroll
           for (int i = 4 * sb; i < 4 * sb + 4; ++i) {
-            const uint32_t off = voff + (i & 3) * C::VROW;
+            const AtPtr vr = vc + (i & 3) * C::VROW;
             if constexpr (VB == 3) {
               // a piece of 12, 24 or 48 bits; of 24, the row's last one is read one byte earlier,
               // inside the row (shifted down where it is used)
               if constexpr (CH == 4) {
-                x.v[i][0] = at_load<uint16_t>(vc, off);
+                x.v[i][0] = at_load<uint16_t>(vr, voff);
               } else if constexpr (CH == 8) {
-                x.v[i][0] = at_load<uint32_t>(vc, off - (col == 15 ? 1 : 0));
+                x.v[i][0] = at_load<uint32_t>(vr, vback);
               } else {
-                x.v[i][0] = at_load<uint32_t>(vc, off);
-                x.v[i][1] = at_load<uint16_t>(vc, off + 4);
+                x.v[i][0] = at_load<uint32_t>(vr, voff);
+                x.v[i][1] = at_load<uint16_t>(vr + 4, voff);
               }
             } else if constexpr (VB * CH == 8) {
-              x.v[i][0] = at_get<uint8_t>(vc, off);
+              x.v[i][0] = at_get<uint8_t>(vr, voff);
             } else if constexpr (VB * CH == 16) {
-              x.v[i][0] = at_get<uint16_t>(vc, off);
+              x.v[i][0] = at_get<uint16_t>(vr, voff);
             } else if constexpr (C::VW == 4) {
-              const u32x4_t y = at_get<u32x4_t>(vc, off);
+              const u32x4_t y = at_get<u32x4_t>(vr, voff);
               x.v[i][0] = y.x; x.v[i][1] = y.y; x.v[i][2] = y.z; x.v[i][3] = y.w;
             } else if constexpr (C::VW == 2) {
-              const u32x2_t y = at_get<u32x2_t>(vc, off);
+              const u32x2_t y = at_get<u32x2_t>(vr, voff);
               x.v[i][0] = y.x; x.v[i][1] = y.y;
             } else {
-              x.v[i][0] = at_get<uint32_t>(vc, off);
+              x.v[i][0] = at_get<uint32_t>(vr, voff);
             }
           }
-          // scales of the piece's group for the four tokens, in pairs
+          // scales of the four tokens: all groups' of up to two, else of the piece's group alone;
+          // nothing is done to them here, which would wait for the loads
+          uint32_t y0, y1, y2 = 0, y3 = 0;
           if (lgv == 0) {
             const u32x2_t y = at_get<u32x2_t>(sp, 8 * h);
-            x.vs[2 * sb] = y.x;
-            x.vs[2 * sb + 1] = y.y;
+            y0 = y.x; y1 = y.y;
+          } else if (lgv == 1) {
+            typedef uint32_t U4 __attribute__((ext_vector_type(4), aligned(8)));
+            const U4 y = at_get<U4>(sp, 16 * h);
+            y0 = y.x; y1 = y.y; y2 = y.z; y3 = y.w;
           } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t off = vsoff + ((2 * i) << (lgv + 1));
-              x.vs[2 * sb + i] = at_get<uint16_t>(sp, off) | static_cast<uint32_t>(at_get<uint16_t>(sp, off + (1 << (lgv + 1)))) << 16;
-            }
+            y0 = at_get<uint16_t>(sp, vsoff);
+            y1 = at_get<uint16_t>(sp + (2 << lgv), vsoff);
+            y2 = at_get<uint16_t>(sp + (4 << lgv), vsoff);
+            y3 = at_get<uint16_t>(sp + (6 << lgv), vsoff);
           }
+          x.vs[4 * sb] = y0; x.vs[4 * sb + 1] = y1; x.vs[4 * sb + 2] = y2; x.vs[4 * sb + 3] = y3;
+        };
+        one(AtInt<0>{});
+        one(AtInt<1>{});
+      };
+      // the scales of the piece's group, tokens 2 i and 2 i + 1 in a word
+      const uint32_t vsel = ((col * CH) >> p->lg_vg) & 1 ? 0x07060302u : 0x05040100u;
+      auto pair_scales = [&](const AtBlock<C>& x, uint32_t (&o)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t pair = x.vs[4 * (i >> 1) + (i & 1)];
+          const uint32_t a = x.vs[4 * (i >> 1) + 2 * (i & 1)], c = x.vs[4 * (i >> 1) + 2 * (i & 1) + 1];
+          o[i] = lgv == 0 ? pair : __builtin_amdgcn_perm(c, a, lgv == 1 ? vsel : 0x05040100u);
         }
       };
-      AtBlock<C> buf[2] = {};
+      // ---- q: rotated, scaled by a power of two to fp16's upper range, into LDS ----
+      constexpr int RW = ROWS / W < 4 ? ROWS / W : 4;  // rows of a wave at a time
+      const int qlane = at_fresh(threadIdx.x & 63), qch = kv_chunk(qlane), qd0 = qch * EL;
+      const uint32_t hb_mul = p->hb_mul;
+      const float qc1 = p->c1;
+      uint16_t qraw[RW][EL];
+      auto q_row = [&](int r, int& tk, int& hd) {  // whether row r of the tile is a query's
+        tk = (static_cast<uint32_t>(r) * hb_mul) >> 16;
+        hd = r - tk * hb;
+        return tk < ntok && hd < nh;
+      };
+      auto load_q = [&](int r0) {
+#pragma unroll
+        for (int x = 0; x < RW; ++x) {
+          int tk, hd;
+          const bool ok = q_row(r0 + x, tk, hd);
+          const uint16_t* src = p->q + (static_cast<int64_t>(sq.row0) + tok0 + (ok ? tk : 0)) * p->q_stride +
+                                static_cast<int64_t>(head0 + (ok ? hd : 0)) * D + qd0;
+          __builtin_memcpy(qraw[x], __builtin_assume_aligned(src, 2 * EL), 2 * EL);
+        }
+      };
+      load_q(wave * (ROWS / W));
+      const uint32_t ksg = (p->ksigns[qd0 >> 5] >> (qd0 & 31)) ^ (p->negate ? 0xffffffffu : 0u);
+
+      AtBlock<C> blk0 = {};
       int blk = k0 + wave;
       if (blk < k1) {
         look(blk);
-        locate(buf[0]);
-        load_k(buf[0]);
-        load_v(buf[0]);
+        locate(blk0);
+        load_k(blk0);
+        load_v(blk0);
         if (blk + W < k1) look(blk + W);
       }
 
-      // ---- q: rotated, scaled by a power of two to fp16's upper range, into LDS ----
+      const int qdt = p->qdt;
+      const bool masked = p->tree != nullptr;
       __syncthreads();  // the last unit's readers of this memory are done
-      {
-        constexpr int RW = ROWS / W < 4 ? ROWS / W : 4;  // rows of a wave at a time
-        const uint32_t neg = p->negate ? 0xffffffffu : 0u, hb_mul = p->hb_mul;
-        const float c1 = p->c1;
-        const int qdt = p->qdt;
 #pragma unroll 1
-        for (int r0 = wave * (ROWS / W); r0 < (wave + 1) * (ROWS / W); r0 += RW) {
-          float v[RW][EL];
-          uint16_t raw[RW][EL];
-          bool ok[RW];
+      for (int r0 = wave * (ROWS / W); r0 < (wave + 1) * (ROWS / W); r0 += RW) {
+        if (r0 != wave * (ROWS / W)) load_q(r0);
+        float v[RW][EL];
 #pragma unroll
-          for (int x = 0; x < RW; ++x) {
-            const int tk = (static_cast<uint32_t>(r0 + x) * hb_mul) >> 16, hd = r0 + x - tk * hb;
-            ok[x] = tk < ntok && hd < nh && c1 != 0.f;
-            const uint16_t* src = p->q + (static_cast<int64_t>(sq.row0) + tok0 + (ok[x] ? tk : 0)) * p->q_stride +
-                                  static_cast<int64_t>(head0 + (ok[x] ? hd : 0)) * D + d0;
-            __builtin_memcpy(raw[x], __builtin_assume_aligned(src, 2 * EL), 2 * EL);
+        for (int x = 0; x < RW; ++x) {
+          int tk, hd;
+          const bool ok = q_row(r0 + x, tk, hd), use = ok && qc1 != 0.f;
+          float mx = 0.f;
+#pragma unroll
+          for (int e = 0; e < EL; ++e) {
+            const float y = qdt == 1 ? bf16_bits_to_float(qraw[x][e]) : half_bits_to_float(qraw[x][e]);
+            v[x][e] = !use ? 0.f : (ksg >> e) & 1u ? -y : y;
           }
+          kv_wave_transform<EL>(v[x], qch);
 #pragma unroll
-          for (int x = 0; x < RW; ++x) {
-            float mx = 0.f;
+          for (int e = 0; e < EL; ++e) mx = fmaxf(mx, fabsf(v[x][e]));
+          mx = kv_wave_max(mx);
+          // the largest magnitude comes to [2^13, 2^14): exponent 127 + 13 of the scaled value
+          const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
+          int k = mx > 0.f && ex < 255 ? 140 - ex : 0;
+          k = k > 100 ? 100 : k;
+          const float f = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+          _Float16 y[EL];
 #pragma unroll
-            for (int e = 0; e < EL; ++e) {
-              const float y = qdt == 1 ? bf16_bits_to_float(raw[x][e]) : half_bits_to_float(raw[x][e]);
-              v[x][e] = !ok[x] ? 0.f : (((ksg ^ neg) >> e) & 1u) ? -y : y;
-            }
-            kv_wave_transform<EL>(v[x], ch);
-#pragma unroll
-            for (int e = 0; e < EL; ++e) mx = fmaxf(mx, fabsf(v[x][e]));
-            mx = kv_wave_max(mx);
-            // the largest magnitude comes to [2^13, 2^14): exponent 127 + 13 of the scaled value
-            const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
-            int k = mx > 0.f && ex < 255 ? 140 - ex : 0;
-            k = k > 100 ? 100 : k;
-            const float f = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-            _Float16 y[EL];
-#pragma unroll
-            for (int e = 0; e < EL; ++e) y[e] = static_cast<_Float16>(v[x][e] * f);
-            __builtin_memcpy(__builtin_assume_aligned(smem + C::QS + (r0 + x) * C::QP + 2 * d0, 2 * EL), y, 2 * EL);
-            if (lane == 0) {
-              const int r = r0 + x, tk = (static_cast<uint32_t>(r) * hb_mul) >> 16, hd = r - tk * hb;
-              *reinterpret_cast<float*>(smem + C::C1 + 4 * r) =
-                  c1 == 0.f ? 1.f : c1 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-              int lim = p->tree ? before : before + tok0 + tk + 1;
-              lim = lim < 0 ? 0 : lim;
-              *reinterpret_cast<int*>(smem + C::LIM + 4 * r) = !(tk < ntok && hd < nh) || lim > len ? len : lim;
-            }
+          for (int e = 0; e < EL; ++e) y[e] = static_cast<_Float16>(v[x][e] * f);
+          __builtin_memcpy(__builtin_assume_aligned(smem + C::QS + (r0 + x) * C::QP + 2 * qd0, 2 * EL), y, 2 * EL);
+          if (qlane == 0) {
+            *reinterpret_cast<float*>(smem + C::C1 + 4 * (r0 + x)) =
+                qc1 == 0.f ? 1.f : qc1 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+            int lim = masked ? before : before + tok0 + tk + 1;
+            lim = lim < 0 ? 0 : lim;
+            *reinterpret_cast<int*>(smem + C::LIM + 4 * (r0 + x)) = !ok || lim > len ? len : lim;
           }
         }
       }
       __syncthreads();
       // from this token on some row's mask may cut
-      int cut = p->tree ? before : before + tok0 + 1;
+      int cut = masked ? before : before + tok0 + 1;
       cut = cut < 0 ? 0 : cut;
       const uint32_t* const tree = p->tree;
 
@@ -726,19 +787,21 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
 #pragma unroll
         for (int r = 0; r < R; ++r) s[r][0] = s[r][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         // the next step's table reads are on their way while this one's results are multiplied
-        AtLook<KB> look2[2];
-        at_look_k<C, KB>(x.k[0], 0, lane4, look2[0]);
+        constexpr int PF = 1;
+        AtLook<KB> ring[PF + 1];
+#pragma unroll
+        for (int y = 0; y < PF; ++y) at_look_k<C, KB>(x.k[y / NS], y % NS, lane4, ring[y]);
 #pragma unroll
         for (int y = 0; y < 2 * NS; ++y) {
           const int sb = y / NS, st = y % NS;
-          if (y + 1 < 2 * NS) at_look_k<C, KB>(x.k[(y + 1) / NS], (y + 1) % NS, lane4, look2[(y + 1) & 1]);
+          if (y + PF < 2 * NS) at_look_k<C, KB>(x.k[(y + PF) / NS], (y + PF) % NS, lane4, ring[(y + PF) % (PF + 1)]);
           u32x4_t qv[R];
 #pragma unroll
           for (int r = 0; r < R; ++r)
             qv[r] = *reinterpret_cast<const u32x4_t*>(smem + C::QS + (16 * r + col) * C::QP + (D / 2) * h + 16 * st);
           __builtin_amdgcn_sched_barrier(0);
           uint32_t a[4];
-          at_pairs_k<KB>(look2[y & 1], kd[sb][C::KS == 2 ? st / (NS / 2) : 0], a);
+          at_pairs_k<KB>(ring[y % (PF + 1)], kd[sb][C::KS == 2 ? st / (NS / 2) : 0], a);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const uint32_t qb[4] = {qv[r].x, qv[r].y, qv[r].z, qv[r].w};
@@ -757,8 +820,8 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
       };
       auto softmax = [&](int blk, f32x4_t (&s)[R][2], uint32_t (&pb)[R][4]) {
         // masks
-        const int j0 = blk * 32 + 4 * h;
         if (blk * 32 + 32 > cut) {
+          const int lane = at_fresh(threadIdx.x & 63), col = lane & 15, j0 = blk * 32 + 4 * (lane >> 4);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const int row = 16 * r + col, lim = *reinterpret_cast<const int*>(smem + C::LIM + 4 * row);
@@ -816,20 +879,22 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
       };
       auto values = [&](AtBlock<C>& x, int blk, bool first, const f32x4_t (&s)[R][2], const uint32_t (&pb)[R][4]) {
         // scales: dead tokens and bad pages to zero, held times 2^-vexp
-        const int j0 = blk * 32 + 4 * h;
+        uint32_t raw[4];
+        pair_scales(x, raw);
         if (blk * 32 + 32 > len || x.bad) {
+          const int j0 = blk * 32 + 4 * (at_fresh(threadIdx.x & 63) >> 4);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int j = j0 + 16 * (i >> 1) + 2 * (i & 1);
             const bool dead = (x.bad >> (i >> 1)) & 1u;
-            x.vs[i] &= (dead || j >= len ? 0u : 0xffffu) | (dead || j + 1 >= len ? 0u : 0xffff0000u);
+            raw[i] &= (dead || j >= len ? 0u : 0xffffu) | (dead || j + 1 >= len ? 0u : 0xffff0000u);
           }
         }
         uint32_t vs[4];
         uint32_t big = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          vs[i] = at_mul(x.vs[i], at_pow2(vexp));
+          vs[i] = at_mul(raw[i], at_pow2(vexp));
           big = at_max_u16(vs[i], big);
         }
         big = big > (big << 16) ? big : big << 16;
@@ -837,11 +902,11 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
           float top = 0.f;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint32_t bits = (x.vs[i >> 1] >> (16 * (i & 1))) & 0xffffu;
+            const uint32_t bits = (raw[i >> 1] >> (16 * (i & 1))) & 0xffffu;
             const uint64_t who = __ballot((bits & 0x7c00u) == 0x7c00u);
             if ((who >> (16 * h)) & 0xffffu) {
               // this token's value is no number: rows that see it become NaN, others stay
-              x.vs[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
+              raw[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
 #pragma unroll
               for (int r = 0; r < R; ++r)
                 if (s[r][i >> 2][i & 3] != -__builtin_inff()) l[r] = __builtin_nanf("");
@@ -860,7 +925,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
               for (int n = 0; n < CH; ++n) o[r][n] *= f;
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) vs[i] = at_mul(x.vs[i], at_pow2(vexp));
+          for (int i = 0; i < 4; ++i) vs[i] = at_mul(raw[i], at_pow2(vexp));
         }
         if constexpr (VB == 3) {
 #pragma unroll
@@ -888,14 +953,17 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
           }
         };
         constexpr int STEP = NT == 8 ? 1 : 2;  // elements of a step: eight table reads
-        uint32_t tb[2][STEP][NT];
+        constexpr int SV = CH / STEP, PV = SV > 1 ? 1 : 0;
+        uint32_t tb[PV + 1][STEP][NT];
 #pragma unroll
-        for (int y = 0; y < STEP; ++y) look_v(y, tb[0][y]);
+        for (int z = 0; z < PV; ++z)
+#pragma unroll
+          for (int y = 0; y < STEP; ++y) look_v(z * STEP + y, tb[z][y]);
 #pragma unroll
         for (int n = 0; n < CH; n += STEP) {
-          if (n + STEP < CH) {
+          if (n + PV * STEP < CH) {
 #pragma unroll
-            for (int y = 0; y < STEP; ++y) look_v(n + STEP + y, tb[((n / STEP) + 1) & 1][y]);
+            for (int y = 0; y < STEP; ++y) look_v(n + PV * STEP + y, tb[(n / STEP + PV) % (PV + 1)][y]);
           }
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -903,7 +971,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
             uint32_t a[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint32_t* z = tb[(n / STEP) & 1][y];
+              const uint32_t* z = tb[(n / STEP) % (PV + 1)][y];
               a[i] = at_mul(VB == 8 ? at_pack(z[(2 * i) % NT], z[(2 * i + 1) % NT]) : z[i], vs[i]);
             }
 #pragma unroll
@@ -919,7 +987,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
         // values' after the sums
         for (; blk < k1; blk += W) {
           const bool more = blk + W < k1;
-          AtBlock<C>& x = buf[0];
+          AtBlock<C>& x = blk0;
           f32x4_t s[R][2];
           uint32_t pb[R][4];
           const uint32_t bad = x.bad;
@@ -941,6 +1009,10 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
 
       // ---- join the waves ----
       p = at_again(p);
+      {
+      const int tid = at_fresh(threadIdx.x), lane = tid & 63, col = lane & 15, h = lane >> 4;
+      const int d0 = kv_chunk(lane) * EL;
+      const uint32_t vsg = p->vsigns[d0 >> 5] >> (d0 & 31);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float x, y;
@@ -1026,12 +1098,13 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
         // the workgroups that go on with this unit: its other parts, or the shares of the line
         // that hold the begin of one of its blocks
         AttendMeta m{};
-        m.parts = own ? np - 1 : static_cast<int>((u0 + kAtUnit + static_cast<int64_t>(nblk - 1) * 32) / q) - wg;
+        m.parts = own ? at_ceil_div(nblk, at_ceil_div(nblk, np)) - 1 : static_cast<int>((u0 + kAtUnit + static_cast<int64_t>(nblk - 1) * 32) / q) - wg;
         m.row0 = sq.row0 + tok0;
         m.nrows = ntok;
         m.head0 = head0;
         m.nh = nh;
         p->meta[wg] = m;
+      }
       }
     }
     // ---- next unit ----
@@ -1065,8 +1138,8 @@ hipError_t at_launch(const AttendParams& p, hipStream_t s) {
 template <int KB, int VB>
 hipError_t at_launch_d(const AttendParams& p, int D, int R, hipStream_t s) {
   switch (D) {
-    case 64: return R == 1 ? at_launch<KB, VB, 64, 1>(p, s) : at_launch<KB, VB, 64, 4>(p, s);
-    case 128: return R == 1 ? at_launch<KB, VB, 128, 1>(p, s) : at_launch<KB, VB, 128, 4>(p, s);
+    case 64: return R == 1 ? at_launch<KB, VB, 64, 1>(p, s) : at_launch<KB, VB, 64, 3>(p, s);
+    case 128: return R == 1 ? at_launch<KB, VB, 128, 1>(p, s) : at_launch<KB, VB, 128, 3>(p, s);
     default: return R == 1 ? at_launch<KB, VB, 256, 1>(p, s) : at_launch<KB, VB, 256, 2>(p, s);
   }
 }
