@@ -174,6 +174,7 @@ template <int D, typename P>
 __device__ __forceinline__ void at_finish(P p, float (&v)[D / 64], float l, int64_t m, int head, uint32_t sg, int lane) {
   constexpr int EL = D / 64;
   const float f = p->inv_sqrt_d / l;
+  sg ^= 0u - kv_sign(kv_chunk(lane));
 #pragma unroll
   for (int e = 0; e < EL; ++e) v[e] = l == 0.f ? 0.f : v[e] * f;
   const int c = kv_chunk(lane);
@@ -679,7 +680,8 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
         }
       };
       load_q(wave * (ROWS / W));
-      const uint32_t ksg = (p->ksigns[qd0 >> 5] >> (qd0 & 31)) ^ (p->negate ? 0xffffffffu : 0u);
+      const uint32_t ksg = p->ksigns[qd0 >> 5] >> (qd0 & 31);
+      const bool qneg = (kv_sign(qch) != 0) != (p->negate != 0);  // the transform's sign, and the scale's
 
       AtBlock<C> blk0 = {};
       int blk = k0 + wave;
@@ -716,7 +718,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
           const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
           int k = mx > 0.f && ex < 255 ? 140 - ex : 0;
           k = k > 100 ? 100 : k;
-          const float f = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+          const float f = __uint_as_float(static_cast<uint32_t>(127 + k) << 23 | (qneg ? 0x80000000u : 0u));
           _Float16 y[EL];
 #pragma unroll
           for (int e = 0; e < EL; ++e) y[e] = static_cast<_Float16>(v[x][e] * f);

@@ -62,22 +62,41 @@ __device__ __forceinline__ double kv_flip(double x, uint32_t m) {
   return __hiloint2double(__double2hiint(x) ^ static_cast<int>(m), __double2loint(x));
 }
 
-// One stage across lanes: the lower chunk keeps the sum, the upper lower - upper.
+// One stage across lanes. B < 4: own + k partner with k = 1 in the lower chunk and -1 in the upper,
+// which there is -(lower - upper): one fused operation (with the lane move as its DPP operand in
+// fp32) instead of a sign change and an addition. Both partners of every later stage carry the
+// same sign, so it stays a factor of the lane: kv_sign. B >= 4: the sum in the lower chunk, lower -
+// upper in the upper.
 template <int B, int N, typename T>
 __device__ __forceinline__ void kv_stage(T (&v)[N], int c) {
-  const uint32_t m = (c >> B) & 1 ? 0x80000000u : 0u;
+  const T k = (c >> B) & 1 ? static_cast<T>(-1) : static_cast<T>(1);
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     if constexpr (B < 4) {
-      const T o = kv_swap<B>(v[j]);
-      v[j] = o + kv_flip(v[j], m);
+      v[j] = __builtin_fma(kv_swap<B>(v[j]), k, v[j]);
     } else {
       T lower, upper;
       kv_both<B>(v[j], lower, upper);
-      v[j] = lower + kv_flip(upper, m);
+      v[j] = __builtin_fma(upper, k, lower);
     }
   }
 }
+template <int B, int N>
+__device__ __forceinline__ void kv_stage(float (&v)[N], int c) {
+  const float k = (c >> B) & 1 ? -1.f : 1.f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    if constexpr (B < 4) {
+      v[j] = __builtin_fmaf(kv_swap<B>(v[j]), k, v[j]);
+    } else {
+      float lower, upper;
+      kv_both<B>(v[j], lower, upper);
+      v[j] = __builtin_fmaf(upper, k, lower);
+    }
+  }
+}
+// 1 where the transforms below leave the lane's values negated.
+__device__ __forceinline__ uint32_t kv_sign(int c) { return __builtin_popcount(c & 15) & 1; }
 
 // The maximum over the wave, in every lane.
 __device__ __forceinline__ float kv_wave_max(float x) {
@@ -92,7 +111,7 @@ __device__ __forceinline__ float kv_wave_max(float x) {
 }
 
 // The unnormalized Sylvester transform of a row of 64 N elements on a whole wave, lane L holding
-// elements N kv_chunk(L) + j.
+// elements N kv_chunk(L) + j; negated where kv_sign says so.
 template <int N>
 __device__ __forceinline__ void kv_wave_transform(float (&v)[N], int c) {
 #pragma unroll
@@ -112,7 +131,7 @@ __device__ __forceinline__ void kv_wave_transform(float (&v)[N], int c) {
   kv_stage<5>(v, c);
 }
 
-// The unnormalized Sylvester transform of the row.
+// The unnormalized Sylvester transform of a row on D / 8 lanes; negated where kv_sign says so.
 template <int D, typename T>
 __device__ __forceinline__ void kv_transform(T (&v)[8], int c) {
 #pragma unroll

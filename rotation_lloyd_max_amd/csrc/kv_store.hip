@@ -169,7 +169,7 @@ __global__ __launch_bounds__(256) void k_kv_store(StoreParams p) {
       if (lg_gl >= 3) sq += kv_swap<2>(sq);
       if (lg_gl >= 4) sq += kv_swap<3>(sq);
       const double rr = __builtin_sqrt(sq / (8 << lg_gl));
-      const double rinv = rr > 0.0 ? 1.0 / rr : 0.0;
+      const double rinv = kv_flip(rr > 0.0 ? 1.0 / rr : 0.0, kv_sign(c) << 31);
       uint32_t code[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {

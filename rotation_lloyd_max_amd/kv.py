@@ -52,10 +52,20 @@ def _call(device, fn, *args):
     if device.type != "cuda":
         raise ValueError(f"the tensors must be on a GPU, not on {device}")
     if device.index == torch.cuda.current_device():
-        _tq._check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+        _tq._check(fn(*args, _stream(device)))
     else:
         with torch.cuda.device(device):
-            _tq._check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+            _tq._check(fn(*args, _stream(device)))
+
+
+# the current stream's handle; torch's own short cut where it has it (2 us less than by the Stream
+# object, a sixth of a small call)
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    def _stream(device):
+        return torch._C._cuda_getCurrentRawStream(device.index)
+else:
+    def _stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
 
 
 def _as(t, dtype, device, name, shape=None):
