@@ -23,10 +23,11 @@ namespace {
 constexpr int kStoreBuckets = 320;  // buckets of 1/64 up to 5.0; the last one is open
 
 // One half's decision data: positive thresholds (binary32 bits, the last one a sentinel no key
-// exceeds) and per bucket the number of thresholds below it.
+// exceeds) and the buckets that hold one, as bits: the thresholds below bucket b are as many as the
+// bits below b.
 struct SnapTable {
   uint32_t thr[128];
-  uint8_t base[kStoreBuckets];
+  uint32_t held[kStoreBuckets / 32];
 };
 
 struct StoreHalf {
@@ -121,10 +122,6 @@ __global__ __launch_bounds__(256) void k_kv_store(StoreParams p) {
   __shared__ double2 cs[2][D / 2];
   const int part = blockIdx.y;
   const StoreHalf& hf = p.half[part];
-  for (int b = threadIdx.x; b < kStoreBuckets; b += blockDim.x) {
-    const uint32_t base = hf.snap.base[b];
-    tab[b] = u32x2_t{hf.snap.thr[base], base};
-  }
   const int c = kv_chunk(threadIdx.x & (LR - 1)), d0 = 8 * c;
   const uint32_t sg = (hf.signs[d0 >> 5] >> (d0 & 31)) & 0xffu;
   const int rows_per_pass = blockDim.x >> LGR;
@@ -133,6 +130,16 @@ __global__ __launch_bounds__(256) void k_kv_store(StoreParams p) {
   const int cpos = hf.levels / 2;
   const bool turn = part == 0 && p.inv_freq;
   int flip = 0;
+  for (int b = threadIdx.x; b < kStoreBuckets; b += blockDim.x) {
+    uint32_t base = 0;
+#pragma unroll
+    for (int k = 0; k < kStoreBuckets / 32; ++k) {
+      const int n = b - 32 * k;  // bits of this word below b
+      const uint32_t m = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+      base += __builtin_popcount(hf.snap.held[k] & m);
+    }
+    tab[b] = u32x2_t{hf.snap.thr[base], base};
+  }
   __syncthreads();
   for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
     const int64_t slot = p.slots[t];
@@ -157,7 +164,11 @@ __global__ __launch_bounds__(256) void k_kv_store(StoreParams p) {
       const char* row = hf.x + (t * hf.ts + h * hf.hs) * (DT == 0 ? 4 : 2);
       double v[8];
       store_load<DT, VEC>(row, d0, v);
-      if (turn) store_turn<DT, VEC>(row, d0, p.rot, p.interleaved, cs[flip], v);
+      if (turn) {
+        int dt = d0;  // the angles are read again for each row: held over the rows they took 100 registers
+        asm volatile("" : "+v"(dt));
+        store_turn<DT, VEC>(row, dt, p.rot, p.interleaved, cs[flip], v);
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = kv_flip(v[e], ((sg >> e) & 1u) << 31);
       kv_transform<D>(v, c);
@@ -238,14 +249,13 @@ void init_snap() {
     ok = ok && positive_threshold_bits(levels[i], bits);
     for (int k = 0; k < 128; ++k) t.thr[k] = k < n ? bits[k] : 0xffffffffu;
     for (int b = 0; b < kStoreBuckets; ++b) {
-      int below = 0, in = 0;
+      int in = 0;
       for (int k = 0; k < n; ++k) {
-        const float x = __builtin_bit_cast(float, bits[k]);
-        below += x * 64.f < b ? 1 : 0;
-        in += x * 64.f >= b && (b + 1 == kStoreBuckets || x * 64.f < b + 1) ? 1 : 0;
+        const float x = __builtin_bit_cast(float, bits[k]) * 64.f;
+        in += x >= b && (b + 1 == kStoreBuckets || x < b + 1) ? 1 : 0;
       }
-      ok = ok && in <= 1;
-      t.base[b] = static_cast<uint8_t>(below);
+      ok = ok && in <= 1 && !(in && b + 1 == kStoreBuckets);
+      if (in) t.held[b >> 5] |= 1u << (b & 31);
     }
   }
   g_snap_ok = ok;
@@ -280,7 +290,7 @@ hipError_t launch_kv_store(const KvCacheArgs& c, const void* k, const void* v, i
   p.inv_sqrt_d = 1.0 / __builtin_sqrt(static_cast<double>(c.D));
   int threads = (c.heads * (c.D / 8) + 63) & ~63;
   if (threads > 256) threads = 256;
-  const dim3 grid(static_cast<uint32_t>(tokens < 1024 ? tokens : 1024), 2);
+  const dim3 grid(static_cast<uint32_t>(tokens < 2048 ? tokens : 2048), 2);
   switch (dt) {
     case 0: store_run_d<0>(p, c.D, vec, grid, threads, s); break;
     case 1: store_run_d<1>(p, c.D, vec, grid, threads, s); break;
