@@ -922,11 +922,15 @@ int tq_kv_attend(const tq_kv_cache* cache, const void* q, tq_dtype q_dtype, int3
     return fail(TQ_ERR_ARG, "tree_words must be in [1, 65536] with a tree and 0 without");
   if (static_cast<int64_t>(table_width) * a.c.page > 0x7fffffffll - 65536)
     return fail(TQ_ERR_ARG, "table_width * page_tokens must be below 2^31 - 65536");
+  // what the schedule counts: units in 32 bits, tokens read by all of them below 2^53
+  const int64_t heads_of_rows = (M + B) * q_heads, tokens = static_cast<int64_t>(table_width) * a.c.page + 256;
+  if (heads_of_rows > 0x7fffffffll || heads_of_rows > (1ll << 53) / tokens)
+    return fail(TQ_ERR_ARG, "(M + B) * q_heads must be below 2^31, and 2^53 with the table's tokens");
+  if (!q_offsets && (B == 0 ? M > 0 : M % B != 0))
+    return fail(TQ_ERR_ARG, "without q_offsets B must divide M");
   if (B == 0 || M == 0) return TQ_OK;
   if (!q || !out || !kv_lens || (table_width > 0 && !page_table))
     return fail(TQ_ERR_ARG, "q, out, kv_lens and page_table must be non-NULL");
-  if (!q_offsets && M % B != 0)
-    return fail(TQ_ERR_ARG, "without q_offsets B must divide M");
   if (!std::isfinite(scale)) return fail(TQ_ERR_ARG, "scale must be finite");
   if (!aligned(q, 16) || q_token_stride % 8 != 0 || !aligned(out, 16))
     return fail(TQ_ERR_ALIGN, "q and its rows, and out, must be 16-byte aligned");

@@ -117,7 +117,7 @@ def _head_strides(t, name):
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
     s = t.stride()
-    if s[2] != 1 and t.shape[2] > 1:
+    if s[2] != 1 and t.shape[2] > 1 and t.numel():  # (an empty tensor's strides may be anything)
         raise ValueError(f"the elements of a head of {name} must be contiguous")
     return s[0], s[1]
 
@@ -257,13 +257,14 @@ def kv_attend(cache, q, kv_lens, page_table, q_offsets=None, tree=None, scale=No
     them its queries' own; q_offsets [B + 1] bounds the sequences' rows of q (None: M / B rows
     each). Causal, or with tree (int32 words [M, words]) bit j of a row's mask for each of the
     sequence's own tokens j. scale: 1 / sqrt(head_dim) by default. Returns [M, q_heads,
-    head_dim] in out_dtype (q's by default)."""
+    head_dim] in out_dtype (q's by default); rows behind q_offsets[B] are not written (without
+    out= they hold whatever the memory held)."""
     dev = cache.device
     if q.dim() != 3 or q.shape[2] != cache.head_dim:
         raise ValueError(f"q must be [M, q_heads, {cache.head_dim}]")
     M, H, D = q.shape
     stride = q.stride()
-    if stride[2] != 1 or (H > 1 and stride[1] != D):
+    if M and (stride[2] != 1 or (H > 1 and stride[1] != D)):
         raise ValueError("the heads of a query row must be contiguous")
     if q.device != dev:
         raise ValueError(f"q is on {q.device}, the cache on {dev}")

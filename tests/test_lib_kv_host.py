@@ -119,7 +119,9 @@ def test_load_refusals(kw, status):
     (dict(width=1 << 26), ERR_ARG), (dict(words=1), ERR_ARG), (dict(tree=256), ERR_ARG), (dict(scale=math.inf), ERR_ARG),
     (dict(scale=math.nan), ERR_ARG), (dict(q=None), ERR_ARG), (dict(out=None), ERR_ARG), (dict(lens=None), ERR_ARG),
     (dict(table=None), ERR_ARG), (dict(q=264), ERR_ALIGN), (dict(stride=4100), ERR_ALIGN), (dict(out=8), ERR_ALIGN),
-    (dict(lens=2), ERR_ALIGN), (dict(table=2), ERR_ALIGN), (dict(off=2), ERR_ALIGN), (dict(tree=2, words=1), ERR_ALIGN)])
+    (dict(lens=2), ERR_ALIGN), (dict(table=2), ERR_ALIGN), (dict(off=2), ERR_ALIGN), (dict(tree=2, words=1), ERR_ALIGN),
+    (dict(B=0, M=4, off=None), ERR_ARG), (dict(qh=1024, M=1 << 22, off=256), ERR_ARG),
+    (dict(qh=64, M=1 << 18, off=256, width=1 << 24), ERR_ARG)])
 def test_attend_refusals(kw, status):
     assert attend(cache(), **kw) == status, tq.lib().tq_last_error()
 
