@@ -1,25 +1,25 @@
 // Attention over the paged compressed cache: dispatch, workspace, and the join of units that
 // several workgroups share (the kernels are in kv_attend.hpp).
-#include "encode_lane.hpp"
-#include "kv_attend.hpp"
+#include "kv_attend_wide.hpp"
 
 namespace tq {
 
-extern template hipError_t at_launch_k<2>(const AttendParams& p, int vbits, int D, int R, hipStream_t s);
-extern template hipError_t at_launch_k<3>(const AttendParams& p, int vbits, int D, int R, hipStream_t s);
-extern template hipError_t at_launch_k<4>(const AttendParams& p, int vbits, int D, int R, hipStream_t s);
-extern template hipError_t at_launch_k<8>(const AttendParams& p, int vbits, int D, int R, hipStream_t s);
+extern template hipError_t at_launch_k<2>(const AttendParams& p, int vbits, int D, int rows, hipStream_t s);
+extern template hipError_t at_launch_k<3>(const AttendParams& p, int vbits, int D, int rows, hipStream_t s);
+extern template hipError_t at_launch_k<4>(const AttendParams& p, int vbits, int D, int rows, hipStream_t s);
+extern template hipError_t at_launch_k<8>(const AttendParams& p, int vbits, int D, int rows, hipStream_t s);
 
 namespace {
 
 constexpr size_t kMetaBytes = sizeof(AttendMeta) * kAtMaxGrid;
 
-// 16-row blocks of a tile, and the workgroups of a launch.
-int tile_blocks(int D, int share, int B, int64_t M) {
-  const int64_t rows = (M * share + B - 1) / B;  // query rows per key head and sequence
-  return rows <= 16 ? 1 : D == 256 ? 2 : 3;
+// Query rows of a tile, and the workgroups of a launch. Up to 16 rows per key head and sequence: the
+// kernel whose waves share the rows and split the tokens. More: the one whose waves split the rows.
+int tile_rows(int D, int share, int B, int64_t M) {
+  const int64_t rows = (M * share + B - 1) / B;
+  return rows <= 16 ? 16 : rows <= 128 || D == 256 ? 128 : 256;
 }
-int workgroups(int D, int R) { return (R == 1 && D <= 128 ? 3 : R > 1 && D == 256 ? 1 : 2) * kAtCus; }
+int workgroups(int D, int rows) { return (rows > 16 ? 1 : D <= 128 ? 3 : 2) * kAtCus; }
 
 // What the join needs of the arguments.
 struct JoinParams {
@@ -92,9 +92,8 @@ uint32_t div_mul(uint32_t d) { return d == 1 ? 0 : static_cast<uint32_t>((0x1000
 
 size_t kv_attend_workspace(const KvCacheArgs& c, int q_heads, int B, int64_t M) {
   if (B == 0 || M == 0) return 0;
-  const int R = tile_blocks(c.D, q_heads / c.heads, B, M);
-  const size_t rows = 16 * R;
-  return kMetaBytes + 2 * workgroups(c.D, R) * rows * (c.D + 2) * sizeof(float);
+  const int rows = tile_rows(c.D, q_heads / c.heads, B, M);
+  return kMetaBytes + 2 * static_cast<size_t>(workgroups(c.D, rows)) * rows * (c.D + 2) * sizeof(float);
 }
 
 hipError_t launch_kv_attend(const AttendArgs& a, hipStream_t s) {
@@ -113,11 +112,11 @@ hipError_t launch_kv_attend(const AttendArgs& a, hipStream_t s) {
   p.lg_kg = __builtin_ctz(a.c.k.group); p.lg_vg = __builtin_ctz(a.c.v.group);
   p.lg_gk = __builtin_ctz(D / a.c.k.group); p.lg_gv = __builtin_ctz(D / a.c.v.group);
   p.share = a.q_heads / a.c.heads;
-  const int R = tile_blocks(D, p.share, a.B, a.M), rows = 16 * R;
+  const int rows = tile_rows(D, p.share, a.B, a.M);
   p.hb = p.share < rows ? p.share : rows;
   p.nhb = (p.share + p.hb - 1) / p.hb;
   p.a_tok = rows / p.hb;
-  p.hb_mul = (65536 + p.hb - 1) / p.hb;  // rows below 64: the product is exact
+  p.hb_mul = (65536 + p.hb - 1) / p.hb;  // r hb < 2^16 for the rows r: the product is exact
   p.a_mul = div_mul(p.a_tok);
   p.hu_n = a.c.heads * p.nhb;
   p.cap = a.table_width * a.c.page;
@@ -134,14 +133,14 @@ hipError_t launch_kv_attend(const AttendArgs& a, hipStream_t s) {
   }
   hipError_t e;
   switch (a.c.k.bits) {
-    case 2: e = at_launch_k<2>(p, a.c.v.bits, D, R, s); break;
-    case 3: e = at_launch_k<3>(p, a.c.v.bits, D, R, s); break;
-    case 4: e = at_launch_k<4>(p, a.c.v.bits, D, R, s); break;
-    default: e = at_launch_k<8>(p, a.c.v.bits, D, R, s); break;
+    case 2: e = at_launch_k<2>(p, a.c.v.bits, D, rows, s); break;
+    case 3: e = at_launch_k<3>(p, a.c.v.bits, D, rows, s); break;
+    case 4: e = at_launch_k<4>(p, a.c.v.bits, D, rows, s); break;
+    default: e = at_launch_k<8>(p, a.c.v.bits, D, rows, s); break;
   }
   if (e != hipSuccess) return e;
   JoinParams j{p.meta, p.parts, p.vsigns, p.out, p.q_heads, p.odt, rows, p.hb_mul, p.hb, p.inv_sqrt_d};
-  const dim3 grid(workgroups(D, R), rows / 4);
+  const dim3 grid(workgroups(D, rows), rows / 4);
   if (D == 64) hipLaunchKernelGGL((k_attend_join<64>), grid, dim3(256), 0, s, j);
   else if (D == 128) hipLaunchKernelGGL((k_attend_join<128>), grid, dim3(256), 0, s, j);
   else hipLaunchKernelGGL((k_attend_join<256>), grid, dim3(256), 0, s, j);

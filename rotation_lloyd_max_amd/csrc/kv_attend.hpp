@@ -274,6 +274,258 @@ __device__ __forceinline__ int64_t at_lane(int64_t x, int lane) {
          static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), lane));
 }
 
+// A workgroup's part of the work: the sequence, head and tile it begins with, and what of the line.
+struct AtWork {
+  bool own;          // cut unit by unit: this is part `part` of np; else [w, w1) of the line
+  int b, hu, t, part, np;
+  AtSeq sq;
+  int64_t q, w, w1, u0;  // shares of the line; the unit's begin on it
+  // what steers a wave is the same in all its lanes; said so, it lives in scalar registers
+  __device__ __forceinline__ void uniform() {
+    w = at_uniform(w);
+    u0 = at_uniform(u0);
+    b = at_uniform(b);
+    hu = at_uniform(hu);
+    t = at_uniform(t);
+    sq.row0 = at_uniform(sq.row0);
+    sq.n = at_uniform(sq.n);
+    sq.len = at_uniform(sq.len);
+    sq.tiles = at_uniform(sq.tiles);
+    sq.flat = at_uniform(sq.flat);
+  }
+  // the blocks [k0, k1) of the unit's nblk that are this workgroup's
+  __device__ __forceinline__ void blocks(int reads, int nblk, int& k0, int& k1) const {
+    if (own) {
+      const int each = at_ceil_div(nblk, np);  // evenly; the last part may be short or empty
+      k0 = part * each < nblk ? part * each : nblk;
+      k1 = k0 + each < nblk ? k0 + each : nblk;
+    } else {
+      const int64_t x0 = w - u0 - kAtUnit, x1 = w1 - u0 - kAtUnit < reads ? w1 - u0 - kAtUnit : reads;
+      k0 = x0 <= 0 ? 0 : static_cast<int>((x0 + 31) >> 5);
+      k1 = x1 <= 0 ? 0 : static_cast<int>((x1 + 31) >> 5);
+    }
+    k0 = at_uniform(k0);
+    k1 = at_uniform(k1);
+  }
+  // the workgroups that go on with this unit: its other parts, or the shares of the line that hold
+  // the begin of one of its blocks
+  __device__ __forceinline__ int more(int nblk, int wg) const {
+    return own ? at_ceil_div(nblk, at_ceil_div(nblk, np)) - 1
+               : static_cast<int>((u0 + kAtUnit + static_cast<int64_t>(nblk - 1) * 32) / q) - wg;
+  }
+  // to the next unit, if any of it is this workgroup's
+  __device__ __forceinline__ bool next(AtArgs p, int reads, int hu_n) {
+    if (own) return false;
+    u0 += reads + kAtUnit;
+    w = u0;
+    if (w >= w1) return false;
+    if (++t == sq.tiles) {
+      t = 0;
+      if (++hu == hu_n) {
+        hu = 0;
+        do {
+          ++b;
+          sq = at_seq(p, at_uniform(at_raw(p, b)));
+        } while (sq.tiles == 0);
+      }
+    }
+    return true;
+  }
+};
+
+// Workgroup wg's part of GRID, found by every wave for itself: a scan over the sequences' costs, a
+// lane taking `per` neighbouring ones from b0 on, of which raw0 is the first. False: nothing to do.
+template <int GRID>
+__device__ __forceinline__ bool at_plan(AtArgs p, int wg, int lane, int per, int b0, const AtRaw& raw0, AtWork& o) {
+  const int a_tok = p->a_tok, hu_n = p->hu_n;
+  const AtSeq seq0 = at_seq(p, raw0);
+  const int b1 = b0 + per < p->B ? b0 + per : p->B;
+  // units and blocks of the lane's sequences; even: every tile of a head costs the same
+  int units = 0;
+  float blocks = 0.f;
+  bool even = true;
+  for (int b = b0; b < b1; ++b) {
+    const AtSeq x = b == b0 ? seq0 : at_seq(p, at_raw(p, b));
+    const int u = x.tiles * hu_n;
+    units = units + u < GRID ? units + u : GRID;
+    blocks += static_cast<float>(u) * static_cast<float>(x.blocks());
+    even = even && (x.flat || x.tiles <= 1);
+  }
+  const int all_units = __builtin_amdgcn_readlane(at_scan(units), 63);
+  // With few units, each is cut into parts of at most `chunk` blocks, one part per workgroup:
+  // sum ceil(blocks / chunk) <= sum blocks / chunk + units <= GRID (the sum in fp32 is rounded up).
+  // Otherwise the line is cut every q.
+  o.own = !__any(!even) && all_units <= GRID / 2;
+  const bool own = o.own;
+  int chunk = 0;
+  int64_t q = 0, w0, w1, excl;
+  int src;
+  if (own) {
+    const float all = at_scan(blocks) * (1.f + 0x1p-16f) / static_cast<float>(GRID - all_units);
+    chunk = static_cast<int>(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(all), 63))) + 1;
+    chunk = chunk < kAtMinBlocks ? kAtMinBlocks : chunk;
+    int parts = 0;
+    for (int b = b0; b < b1; ++b) {
+      const AtSeq x = b == b0 ? seq0 : at_seq(p, at_raw(p, b));
+      parts += x.tiles * hu_n * at_ceil_div(x.blocks(), chunk);
+    }
+    const int incl = at_scan(parts);
+    w0 = wg;
+    w1 = wg + 1;
+    if (wg >= __builtin_amdgcn_readlane(incl, 63)) return false;
+    src = __builtin_ctzll(__ballot(incl > wg));
+    excl = __builtin_amdgcn_readlane(incl - parts, src);
+  } else {
+    int64_t sum = 0;
+    for (int b = b0; b < b1; ++b) sum += (b == b0 ? seq0 : at_seq(p, at_raw(p, b))).per_head * hu_n;
+    const int64_t incl = at_scan(sum), total = at_lane(incl, 63);
+    q = total / GRID + 1;
+    q = q < kAtMinShare ? kAtMinShare : q;
+    w0 = q * wg;
+    w1 = w0 + q < total ? w0 + q : total;
+    if (w0 >= total) return false;
+    src = __builtin_ctzll(__ballot(incl > w0));
+    excl = at_lane(incl - sum, src);
+  }
+  // the sequence, among those of the lane that holds w0
+  int64_t rem = at_uniform(w0 - excl);
+  int b = src * per;
+  AtSeq sq = at_seq(p, AtRaw{__builtin_amdgcn_readlane(raw0.len, src), __builtin_amdgcn_readlane(raw0.lo, src),
+                             __builtin_amdgcn_readlane(raw0.hi, src)});
+  auto work_of = [&](const AtSeq& x) {
+    return own ? static_cast<int64_t>(x.tiles * hu_n * at_ceil_div(x.blocks(), chunk)) : x.per_head * hu_n;
+  };
+  if (per > 1)
+    for (int64_t x = work_of(sq); rem >= x; x = work_of(sq)) {
+      rem = at_uniform(rem - x);
+      ++b;
+      sq = at_seq(p, at_uniform(at_raw(p, b)));
+    }
+  int hu, t, part = 0, np = 1;
+  int64_t u0 = 0;  // the unit's begin on the line
+  if (own) {
+    np = at_uniform(at_ceil_div(sq.blocks(), chunk));
+    const int unit = at_uniform(at_ceil_div(static_cast<int>(rem) + 1, np) - 1);
+    part = static_cast<int>(rem) - unit * np;
+    hu = sq.tiles == 1 ? unit : at_ceil_div(unit + 1, sq.tiles) - 1;
+    t = unit - hu * sq.tiles;
+  } else {
+    // rem < 2^53, so the quotient in fp64 is at most one off
+    hu = static_cast<int>(static_cast<double>(rem) / static_cast<double>(sq.per_head));
+    hu -= hu * sq.per_head > rem ? 1 : 0;
+    hu += (hu + 1) * sq.per_head <= rem ? 1 : 0;
+    rem -= hu * sq.per_head;
+    int lo = 0, hi = sq.tiles - 1;  // last tile with at_before <= rem
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (at_before(sq, a_tok, mid) <= rem) lo = mid;
+      else hi = mid - 1;
+    }
+    t = lo;
+    u0 = w0 - (rem - at_before(sq, a_tok, t));
+  }
+  o.q = q; o.w = w0; o.w1 = w1; o.u0 = u0;
+  o.b = b; o.hu = hu; o.t = t; o.part = part; o.np = np;
+  o.sq = sq;
+  return true;
+}
+
+// The centroid tables. A wave's entries are uniform: scalar loads of the arguments, two 128-byte
+// rows per store.
+template <typename C, int KB, int VB>
+__device__ __forceinline__ void at_tables(AtArgs p, char* smem, int tid, int lane, int wave) {
+  if constexpr (C::WIDE > 0) {
+    constexpr int TB = KB == 8 || VB == 8 ? 8 : 4;
+    const __attribute__((address_space(4))) uint16_t* hc = KB == TB ? p->hk : p->hv;
+    constexpr int PW = 256 / C::W;
+#pragma unroll
+    for (int k = 0; k < PW; k += 2) {
+      const int e = wave * PW + k;
+      const uint32_t x = TB == 8 ? hc[e] : (hc[e & 15] | static_cast<uint32_t>(hc[e >> 4]) << 16);
+      const uint32_t y = TB == 8 ? hc[e + 1] : (hc[(e + 1) & 15] | static_cast<uint32_t>(hc[e >> 4]) << 16);
+      *reinterpret_cast<uint32_t*>(smem + 128 * e + 4 * lane) = lane < 32 ? x : y;
+    }
+  }
+  if constexpr (KB < 8 && !C::KWIDE)
+    for (int e = tid; e < (1 << (2 * KB)); e += C::T)
+      *reinterpret_cast<uint32_t*>(smem + C::TK + 4 * e) =
+          p->hk[e & ((1 << KB) - 1)] | static_cast<uint32_t>(p->hk[e >> KB]) << 16;
+  if constexpr (VB < 8 && !C::VWIDE)
+    for (int e = tid; e < (1 << (2 * VB)); e += C::T)
+      *reinterpret_cast<uint32_t*>(smem + C::TV + 4 * e) =
+          p->hv[e & ((1 << VB) - 1)] | static_cast<uint32_t>(p->hv[e >> VB]) << 16;
+
+}
+
+// RW rows of a tile's queries at a time, by a wave: rotated, scaled by a power of two to fp16's
+// upper range, into LDS as rows of QP bytes, with each row's score factor and the token its mask
+// ends at (a tree's: begins at).
+template <int D, int RW>
+struct AtQuery {
+  static constexpr int EL = D / 64;
+  int lane, ch, d0, tok0, ntok, nh, hb, row0, head0;
+  uint32_t hb_mul;
+  uint32_t sg;
+  float c1;
+  uint16_t raw[RW][EL];
+  __device__ __forceinline__ AtQuery(AtArgs p, int row0_, int head0_, int tok0_, int ntok_, int nh_)
+      : lane(at_fresh(threadIdx.x & 63)), ch(kv_chunk(lane)), d0(ch * EL), tok0(tok0_), ntok(ntok_), nh(nh_),
+        hb(p->hb), row0(row0_), head0(head0_), hb_mul(p->hb_mul), sg(p->ksigns[d0 >> 5] >> (d0 & 31)), c1(p->c1) {}
+  // whether row r of the tile is a query's
+  __device__ __forceinline__ bool row(int r, int& tk, int& hd) const {
+    tk = (static_cast<uint32_t>(r) * hb_mul) >> 16;
+    hd = r - tk * hb;
+    return tk < ntok && hd < nh;
+  }
+  __device__ __forceinline__ void load(AtArgs p, int r0) {
+#pragma unroll
+    for (int x = 0; x < RW; ++x) {
+      int tk, hd;
+      const bool ok = row(r0 + x, tk, hd);
+      const uint16_t* src = p->q + (static_cast<int64_t>(row0) + (ok ? tk : 0)) * p->q_stride +
+                            static_cast<int64_t>(head0 + (ok ? hd : 0)) * D + d0;
+      __builtin_memcpy(raw[x], __builtin_assume_aligned(src, 2 * EL), 2 * EL);
+    }
+  }
+  __device__ __forceinline__ void rotate(AtArgs p, char* smem, int r0, int dst, int QP, int C1, int LIM, int before, int len) {
+    const int qdt = p->qdt;
+    const bool neg = (kv_sign(ch) != 0) != (p->negate != 0);  // the transform's sign, and the scale's
+    const bool masked = p->tree != nullptr;
+    float v[RW][EL];
+#pragma unroll
+    for (int x = 0; x < RW; ++x) {
+      int tk, hd;
+      const bool ok = row(r0 + x, tk, hd), use = ok && c1 != 0.f;
+      float mx = 0.f;
+#pragma unroll
+      for (int e = 0; e < EL; ++e) {
+        const float y = qdt == 1 ? bf16_bits_to_float(raw[x][e]) : half_bits_to_float(raw[x][e]);
+        v[x][e] = !use ? 0.f : (sg >> e) & 1u ? -y : y;
+      }
+      kv_wave_transform<EL>(v[x], ch);
+#pragma unroll
+      for (int e = 0; e < EL; ++e) mx = fmaxf(mx, fabsf(v[x][e]));
+      mx = kv_wave_max(mx);
+      // the largest magnitude comes to [2^13, 2^14): exponent 127 + 13 of the scaled value
+      const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
+      int k = mx > 0.f && ex < 255 ? 140 - ex : 0;
+      k = k > 100 ? 100 : k;
+      const float f = __uint_as_float(static_cast<uint32_t>(127 + k) << 23 | (neg ? 0x80000000u : 0u));
+      _Float16 y[EL];
+#pragma unroll
+      for (int e = 0; e < EL; ++e) y[e] = static_cast<_Float16>(v[x][e] * f);
+      __builtin_memcpy(__builtin_assume_aligned(smem + dst + x * QP + 2 * d0, 2 * EL), y, 2 * EL);
+      if (lane == 0) {
+        *reinterpret_cast<float*>(smem + C1 + 4 * (r0 + x)) =
+            c1 == 0.f ? 1.f : c1 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+        int lim = masked ? before : before + tok0 + tk + 1;
+        lim = lim < 0 ? 0 : lim;
+        *reinterpret_cast<int*>(smem + LIM + 4 * (r0 + x)) = !ok || lim > len ? len : lim;
+      }
+    }
+  }
+};
+
 // ---- decoding -----------------------------------------------------------------------------
 // the larger of each half, as unsigned numbers (scales are not negative)
 __device__ __forceinline__ uint32_t at_max_u16(uint32_t a, uint32_t b) {
@@ -371,123 +623,16 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
   const uint32_t lane4 = (lane & 31) * 4;
   const int wg = blockIdx.x;
 
-  // ---- this workgroup's part of the work, found by every wave for itself: a scan over the
-  // sequences' costs, a lane taking `per` neighbouring ones ----
   const int per = (p->B + 63) >> 6;
   const int b0 = lane * per;
   AtRaw raw0{0, 0, 0};
   if (b0 < p->B) raw0 = at_raw(p, b0);
 
-  // centroid tables, while those loads are on their way. A wave's entries are uniform: scalar
-  // loads of the arguments, two 128-byte rows per store.
-  if constexpr (C::WIDE > 0) {
-    constexpr int TB = KB == 8 || VB == 8 ? 8 : 4;
-    const __attribute__((address_space(4))) uint16_t* hc = KB == TB ? p->hk : p->hv;
-    constexpr int PW = 256 / W;
-#pragma unroll
-    for (int k = 0; k < PW; k += 2) {
-      const int e = wave * PW + k;
-      const uint32_t x = TB == 8 ? hc[e] : (hc[e & 15] | static_cast<uint32_t>(hc[e >> 4]) << 16);
-      const uint32_t y = TB == 8 ? hc[e + 1] : (hc[(e + 1) & 15] | static_cast<uint32_t>(hc[e >> 4]) << 16);
-      *reinterpret_cast<uint32_t*>(smem + 128 * e + 4 * lane) = lane < 32 ? x : y;
-    }
-  }
-  if constexpr (KB < 8 && !C::KWIDE)
-    for (int e = tid; e < (1 << (2 * KB)); e += T)
-      *reinterpret_cast<uint32_t*>(smem + C::TK + 4 * e) =
-          p->hk[e & ((1 << KB) - 1)] | static_cast<uint32_t>(p->hk[e >> KB]) << 16;
-  if constexpr (VB < 8 && !C::VWIDE)
-    for (int e = tid; e < (1 << (2 * VB)); e += T)
-      *reinterpret_cast<uint32_t*>(smem + C::TV + 4 * e) =
-          p->hv[e & ((1 << VB) - 1)] | static_cast<uint32_t>(p->hv[e >> VB]) << 16;
-
+  at_tables<C, KB, VB>(p, smem, tid, lane, wave);  // while those loads are on their way
   const int a_tok = p->a_tok, hu_n = p->hu_n;
   if (tid == 0) p->meta[wg].parts = 0;
-  const AtSeq seq0 = at_seq(p, raw0);
-  const int b1 = b0 + per < p->B ? b0 + per : p->B;
-  // units and blocks of the lane's sequences; even: every tile of a head costs the same
-  int units = 0;
-  float blocks = 0.f;
-  bool even = true;
-  for (int b = b0; b < b1; ++b) {
-    const AtSeq x = b == b0 ? seq0 : at_seq(p, at_raw(p, b));
-    const int u = x.tiles * hu_n;
-    units = units + u < C::GRID ? units + u : C::GRID;
-    blocks += static_cast<float>(u) * static_cast<float>(x.blocks());
-    even = even && (x.flat || x.tiles <= 1);
-  }
-  const int all_units = __builtin_amdgcn_readlane(at_scan(units), 63);
-  // With few units, each is cut into parts of at most `chunk` blocks, one part per workgroup:
-  // sum ceil(blocks / chunk) <= sum blocks / chunk + units <= GRID (the sum in fp32 is rounded up).
-  // Otherwise the line is cut every q.
-  const bool own = !__any(!even) && all_units <= C::GRID / 2;
-  int chunk = 0;
-  int64_t q = 0, w0, w1, excl;
-  int src;
-  if (own) {
-    const float all = at_scan(blocks) * (1.f + 0x1p-16f) / static_cast<float>(C::GRID - all_units);
-    chunk = static_cast<int>(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(all), 63))) + 1;
-    chunk = chunk < kAtMinBlocks ? kAtMinBlocks : chunk;
-    int parts = 0;
-    for (int b = b0; b < b1; ++b) {
-      const AtSeq x = b == b0 ? seq0 : at_seq(p, at_raw(p, b));
-      parts += x.tiles * hu_n * at_ceil_div(x.blocks(), chunk);
-    }
-    const int incl = at_scan(parts);
-    w0 = wg;
-    w1 = wg + 1;
-    if (wg >= __builtin_amdgcn_readlane(incl, 63)) return;
-    src = __builtin_ctzll(__ballot(incl > wg));
-    excl = __builtin_amdgcn_readlane(incl - parts, src);
-  } else {
-    int64_t sum = 0;
-    for (int b = b0; b < b1; ++b) sum += (b == b0 ? seq0 : at_seq(p, at_raw(p, b))).per_head * hu_n;
-    const int64_t incl = at_scan(sum), total = at_lane(incl, 63);
-    q = total / C::GRID + 1;
-    q = q < kAtMinShare ? kAtMinShare : q;
-    w0 = q * wg;
-    w1 = w0 + q < total ? w0 + q : total;
-    if (w0 >= total) return;
-    src = __builtin_ctzll(__ballot(incl > w0));
-    excl = at_lane(incl - sum, src);
-  }
-  // the sequence, among those of the lane that holds w0
-  int64_t rem = at_uniform(w0 - excl);
-  int b = src * per;
-  AtSeq sq = at_seq(p, AtRaw{__builtin_amdgcn_readlane(raw0.len, src), __builtin_amdgcn_readlane(raw0.lo, src),
-                             __builtin_amdgcn_readlane(raw0.hi, src)});
-  auto work_of = [&](const AtSeq& x) {
-    return own ? static_cast<int64_t>(x.tiles * hu_n * at_ceil_div(x.blocks(), chunk)) : x.per_head * hu_n;
-  };
-  if (per > 1)
-    for (int64_t x = work_of(sq); rem >= x; x = work_of(sq)) {
-      rem = at_uniform(rem - x);
-      ++b;
-      sq = at_seq(p, at_uniform(at_raw(p, b)));
-    }
-  int hu, t, part = 0, np = 1;
-  int64_t u0 = 0;  // the unit's begin on the line
-  if (own) {
-    np = at_uniform(at_ceil_div(sq.blocks(), chunk));
-    const int unit = at_uniform(at_ceil_div(static_cast<int>(rem) + 1, np) - 1);
-    part = static_cast<int>(rem) - unit * np;
-    hu = sq.tiles == 1 ? unit : at_ceil_div(unit + 1, sq.tiles) - 1;
-    t = unit - hu * sq.tiles;
-  } else {
-    // rem < 2^53, so the quotient in fp64 is at most one off
-    hu = static_cast<int>(static_cast<double>(rem) / static_cast<double>(sq.per_head));
-    hu -= hu * sq.per_head > rem ? 1 : 0;
-    hu += (hu + 1) * sq.per_head <= rem ? 1 : 0;
-    rem -= hu * sq.per_head;
-    int lo = 0, hi = sq.tiles - 1;  // last tile with at_before <= rem
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (at_before(sq, a_tok, mid) <= rem) lo = mid;
-      else hi = mid - 1;
-    }
-    t = lo;
-    u0 = w0 - (rem - at_before(sq, a_tok, t));
-  }
+  AtWork wk;
+  if (!at_plan<C::GRID>(p, wg, lane, per, b0, raw0, wk)) return;
 
   const uint32_t koff = col * C::KROW + (C::KROW / 4) * h;
   const uint32_t voff = 4 * h * C::VROW + (VB * CH * col) / 8, vback = voff - (col == 15 ? 1 : 0);
@@ -496,33 +641,15 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
   const uint32_t ksoff2 = ((col << p->lg_gk) + ((D / 4 * h + D / 8) >> p->lg_kg)) * 2;
   const uint32_t vsoff = ((4 * h << p->lg_gv) + ((col * CH) >> p->lg_vg)) * 2;
 
-  for (int64_t w = w0; w < w1;) {
-    // what steers the wave is the same in all its lanes; said so, it lives in scalar registers
-    w = at_uniform(w);
-    u0 = at_uniform(u0);
-    b = at_uniform(b);
-    hu = at_uniform(hu);
-    t = at_uniform(t);
-    sq.row0 = at_uniform(sq.row0);
-    sq.n = at_uniform(sq.n);
-    sq.len = at_uniform(sq.len);
-    sq.tiles = at_uniform(sq.tiles);
-    sq.flat = at_uniform(sq.flat);
+  while (true) {
+    wk.uniform();
     p = at_again(p);
-    const int reads = at_reads(sq, a_tok, t);
+    const int reads = at_reads(wk.sq, a_tok, wk.t);
     const int nblk = (reads + 31) >> 5;
     int k0, k1;
-    if (own) {
-      const int each = at_ceil_div(nblk, np);  // evenly; the last part may be short or empty
-      k0 = part * each < nblk ? part * each : nblk;
-      k1 = k0 + each < nblk ? k0 + each : nblk;
-    } else {
-      const int64_t x0 = w - u0 - kAtUnit, x1 = w1 - u0 - kAtUnit < reads ? w1 - u0 - kAtUnit : reads;
-      k0 = x0 <= 0 ? 0 : static_cast<int>((x0 + 31) >> 5);
-      k1 = x1 <= 0 ? 0 : static_cast<int>((x1 + 31) >> 5);
-    }
-    k0 = at_uniform(k0);
-    k1 = at_uniform(k1);
+    wk.blocks(reads, nblk, k0, k1);
+    const AtSeq& sq = wk.sq;
+    const int hu = wk.hu, t = wk.t, b = wk.b;
     if (k0 < k1) {
       const int kh = p->nhb == 1 ? hu : hu / p->nhb, hblk = hu - kh * p->nhb;
       const int hb = p->hb, head0 = kh * p->share + hblk * hb;
@@ -660,29 +787,8 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
       };
       // ---- q: rotated, scaled by a power of two to fp16's upper range, into LDS ----
       constexpr int RW = ROWS / W < 4 ? ROWS / W : 4;  // rows of a wave at a time
-      const int qlane = at_fresh(threadIdx.x & 63), qch = kv_chunk(qlane), qd0 = qch * EL;
-      const uint32_t hb_mul = p->hb_mul;
-      const float qc1 = p->c1;
-      uint16_t qraw[RW][EL];
-      auto q_row = [&](int r, int& tk, int& hd) {  // whether row r of the tile is a query's
-        tk = (static_cast<uint32_t>(r) * hb_mul) >> 16;
-        hd = r - tk * hb;
-        return tk < ntok && hd < nh;
-      };
-      auto load_q = [&](int r0) {
-#pragma unroll
-        for (int x = 0; x < RW; ++x) {
-          int tk, hd;
-          const bool ok = q_row(r0 + x, tk, hd);
-          const uint16_t* src = p->q + (static_cast<int64_t>(sq.row0) + tok0 + (ok ? tk : 0)) * p->q_stride +
-                                static_cast<int64_t>(head0 + (ok ? hd : 0)) * D + qd0;
-          __builtin_memcpy(qraw[x], __builtin_assume_aligned(src, 2 * EL), 2 * EL);
-        }
-      };
-      load_q(wave * (ROWS / W));
-      const uint32_t ksg = p->ksigns[qd0 >> 5] >> (qd0 & 31);
-      const bool qneg = (kv_sign(qch) != 0) != (p->negate != 0);  // the transform's sign, and the scale's
-
+      AtQuery<D, RW> qs(p, sq.row0 + tok0, head0, tok0, ntok, nh);
+      qs.load(p, wave * (ROWS / W));
       AtBlock<C> blk0 = {};
       int blk = k0 + wave;
       if (blk < k1) {
@@ -693,44 +799,12 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
         if (blk + W < k1) look(blk + W);
       }
 
-      const int qdt = p->qdt;
       const bool masked = p->tree != nullptr;
       __syncthreads();  // the last unit's readers of this memory are done
 #pragma unroll 1
       for (int r0 = wave * (ROWS / W); r0 < (wave + 1) * (ROWS / W); r0 += RW) {
-        if (r0 != wave * (ROWS / W)) load_q(r0);
-        float v[RW][EL];
-#pragma unroll
-        for (int x = 0; x < RW; ++x) {
-          int tk, hd;
-          const bool ok = q_row(r0 + x, tk, hd), use = ok && qc1 != 0.f;
-          float mx = 0.f;
-#pragma unroll
-          for (int e = 0; e < EL; ++e) {
-            const float y = qdt == 1 ? bf16_bits_to_float(qraw[x][e]) : half_bits_to_float(qraw[x][e]);
-            v[x][e] = !use ? 0.f : (ksg >> e) & 1u ? -y : y;
-          }
-          kv_wave_transform<EL>(v[x], qch);
-#pragma unroll
-          for (int e = 0; e < EL; ++e) mx = fmaxf(mx, fabsf(v[x][e]));
-          mx = kv_wave_max(mx);
-          // the largest magnitude comes to [2^13, 2^14): exponent 127 + 13 of the scaled value
-          const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
-          int k = mx > 0.f && ex < 255 ? 140 - ex : 0;
-          k = k > 100 ? 100 : k;
-          const float f = __uint_as_float(static_cast<uint32_t>(127 + k) << 23 | (qneg ? 0x80000000u : 0u));
-          _Float16 y[EL];
-#pragma unroll
-          for (int e = 0; e < EL; ++e) y[e] = static_cast<_Float16>(v[x][e] * f);
-          __builtin_memcpy(__builtin_assume_aligned(smem + C::QS + (r0 + x) * C::QP + 2 * qd0, 2 * EL), y, 2 * EL);
-          if (qlane == 0) {
-            *reinterpret_cast<float*>(smem + C::C1 + 4 * (r0 + x)) =
-                qc1 == 0.f ? 1.f : qc1 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-            int lim = masked ? before : before + tok0 + tk + 1;
-            lim = lim < 0 ? 0 : lim;
-            *reinterpret_cast<int*>(smem + C::LIM + 4 * (r0 + x)) = !ok || lim > len ? len : lim;
-          }
-        }
+        if (r0 != wave * (ROWS / W)) qs.load(p, r0);
+        qs.rotate(p, smem, r0, C::QS + r0 * C::QP, C::QP, C::C1, C::LIM, before, len);
       }
       __syncthreads();
       // from this token on some row's mask may cut
@@ -1097,10 +1171,8 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
         }
       }
       if (!whole && k0 == 0 && tid == 0) {
-        // the workgroups that go on with this unit: its other parts, or the shares of the line
-        // that hold the begin of one of its blocks
         AttendMeta m{};
-        m.parts = own ? at_ceil_div(nblk, at_ceil_div(nblk, np)) - 1 : static_cast<int>((u0 + kAtUnit + static_cast<int64_t>(nblk - 1) * 32) / q) - wg;
+        m.parts = wk.more(nblk, wg);
         m.row0 = sq.row0 + tok0;
         m.nrows = ntok;
         m.head0 = head0;
@@ -1109,21 +1181,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
       }
       }
     }
-    // ---- next unit ----
-    if (own) break;
-    u0 += reads + kAtUnit;
-    w = u0;
-    if (w >= w1) break;
-    if (++t == sq.tiles) {
-      t = 0;
-      if (++hu == hu_n) {
-        hu = 0;
-        do {
-          ++b;
-          sq = at_seq(p, at_uniform(at_raw(p, b)));
-        } while (sq.tiles == 0);
-      }
-    }
+    if (!wk.next(p, reads, hu_n)) break;
   }
 }
 
@@ -1135,26 +1193,6 @@ hipError_t at_launch(const AttendParams& p, hipStream_t s) {
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((k_attend<KB, VB, D, R>), dim3(C::GRID), dim3(C::T), C::LDS, s, p);
   return hipGetLastError();
-}
-
-template <int KB, int VB>
-hipError_t at_launch_d(const AttendParams& p, int D, int R, hipStream_t s) {
-  switch (D) {
-    case 64: return R == 1 ? at_launch<KB, VB, 64, 1>(p, s) : at_launch<KB, VB, 64, 3>(p, s);
-    case 128: return R == 1 ? at_launch<KB, VB, 128, 1>(p, s) : at_launch<KB, VB, 128, 3>(p, s);
-    default: return R == 1 ? at_launch<KB, VB, 256, 1>(p, s) : at_launch<KB, VB, 256, 2>(p, s);
-  }
-}
-
-// One key format's kernels.
-template <int KB>
-hipError_t at_launch_k(const AttendParams& p, int vbits, int D, int R, hipStream_t s) {
-  switch (vbits) {
-    case 2: return at_launch_d<KB, 2>(p, D, R, s);
-    case 3: return at_launch_d<KB, 3>(p, D, R, s);
-    case 4: return at_launch_d<KB, 4>(p, D, R, s);
-    default: return at_launch_d<KB, 8>(p, D, R, s);
-  }
 }
 
 }  // namespace tq

@@ -1,8 +1,8 @@
 // Attention kernels for keys of 4 bits.
-#include "kv_attend.hpp"
+#include "kv_attend_wide.hpp"
 
 namespace tq {
 
-template hipError_t at_launch_k<4>(const AttendParams& p, int vbits, int D, int R, hipStream_t s);
+template hipError_t at_launch_k<4>(const AttendParams& p, int vbits, int D, int rows, hipStream_t s);
 
 }  // namespace tq

@@ -1,0 +1,546 @@
+// Attention over the paged compressed cache for many query rows per key head (prompt chunks, trees
+// of drafted tokens): the kernel of kv_attend.hpp with its roles exchanged. There each wave decodes
+// its own tokens for all of a tile's rows; here the rows are spread over eight waves and each
+// decoded block serves all of them, through shared memory.
+//
+// A chunk of NB blocks (32 NB tokens) is decoded once, by four waves its keys and by four its
+// values, straight into the order in which the matrix instructions take them: 1 KB pieces, 16 bytes
+// per lane. Two buffers alternate: while a chunk is multiplied the next one is decoded, the
+// waves of keys (0 - 3) multiplying first and those of values (4 - 7) decoding first, so that each
+// SIMD, which holds one of either, has matrix and vector work at the same time. A wave holds 16 R
+// rows: their rotated queries and sums stay in its registers, and no sums are joined across waves.
+//
+// The powers of two by which scales are held are chosen per block from its scales alone, so that
+// the waves that decode parts of it agree without asking each other; they travel with the block.
+#pragma once
+
+#include "encode_lane.hpp"
+#include "kv_attend.hpp"
+
+namespace tq {
+
+template <int KB, int VB, int D, int R>
+struct AwCfg {
+  static constexpr int W = 8;               // waves
+  static constexpr int T = 64 * W;
+  static constexpr int ROWS = 16 * W * R;
+  static constexpr int NS = D / 32;         // 32-element steps of a key row
+  static constexpr int CH = D / 16;         // codes of a lane's piece of a value row
+  static constexpr bool KWIDE = KB == 8 || (KB == 4 && VB != 8);
+  static constexpr bool VWIDE = VB == 8 || (VB == 4 && KB != 8);
+  static constexpr int KROW = D * KB / 8, VROW = D * VB / 8;  // row bytes
+  static constexpr int NB = D == 256 ? 1 : 2;                 // blocks of a chunk
+  static constexpr int KP = 2 / NB, VP = 4 / NB;              // waves of a half block's keys, of a block's values
+  static constexpr int SPP = NS / KP, EPP = CH / VP;          // steps and value elements of such a wave
+  static constexpr int KBYTES = SPP * KB, KW = (KBYTES + 3) / 4;  // its bytes of a quarter key row
+  static constexpr int VBITS = EPP * VB;                          // its bits of a value piece
+  static constexpr int KS = D == 256 ? 2 : 1;                 // key scales of a quarter row, at most
+  static constexpr int GRID = kAtCus;
+  // LDS; the queries on their way in and the sums on their way out take the place of the buffers
+  static constexpr int WIDE = (KWIDE || VWIDE) ? 32768 : 0;
+  static constexpr int TK = WIDE, TV = TK + 1024;
+  static constexpr int C1 = TV + 1024, LIM = C1 + ROWS * 4, HDR = LIM + ROWS * 4;
+  static constexpr int BUF = HDR + 2 * NB * 16;
+  static constexpr int VOFF = NB * 2 * NS * 1024, BYTES = VOFF + NB * CH * 1024;  // of a buffer
+  static constexpr int QP = D * 2 + 16;                       // padded row of q
+  static constexpr int FR = D == 256 ? 8 : 16, FP = D + 1;    // rows of a wave that go out at a time, padded row
+  static constexpr int max3(int a, int b, int c) { return a > b ? (a > c ? a : c) : b > c ? b : c; }
+  static constexpr int LDS = BUF + max3(2 * BYTES, W * 16 * QP, W * FR * FP * 4);
+  static_assert(LDS <= 163840, "LDS of a CU");
+  static_assert(NB * 2 * KP == 4 && NB * VP == 4, "four waves each");
+};
+
+// What a block of a buffer needs besides its values: 2^kexp of its halves' keys, vexp, and the
+// tokens whose value is no number.
+struct AwHeader {
+  float kf[2];
+  int32_t vexp;
+  uint32_t vbad;
+};
+
+// The power of two that brings scales near 1, if one is beyond 2^13, no number, or all are below
+// 2^-4; top: the largest finite one of the lane's. 2^-15 to 2^15.
+__device__ __forceinline__ int aw_exponent(float top) {
+  const int e = static_cast<int>(__float_as_uint(kv_wave_max(top)) >> 23) - 127;
+  return at_uniform(e < -15 ? -15 : e);
+}
+
+template <int KB, int VB, int D, int R>
+__global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(AttendParams) {
+  using C = AwCfg<KB, VB, D, R>;
+  constexpr int W = C::W, NS = C::NS, CH = C::CH, NB = C::NB, EL = D / 64;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  AtArgs p = (AtArgs)__builtin_amdgcn_kernarg_segment_ptr();
+  const int tid = threadIdx.x, lane = tid & 63, wave = at_uniform(tid >> 6);
+  const int col = lane & 15, h = lane >> 4;
+  const int wg = blockIdx.x;
+  const int per = (p->B + 63) >> 6;
+  const int b0 = lane * per;
+  AtRaw raw0{0, 0, 0};
+  if (b0 < p->B) raw0 = at_raw(p, b0);
+  at_tables<C, KB, VB>(p, smem, tid, lane, wave);  // while those loads are on their way
+  const int a_tok = p->a_tok, hu_n = p->hu_n;
+  if (tid == 0) p->meta[wg].parts = 0;
+  AtWork wk;
+  if (!at_plan<C::GRID>(p, wg, lane, per, b0, raw0, wk)) return;
+
+  // this wave's part of a chunk's decoding: waves 0 - 3 keys, 4 - 7 values
+  const bool keys = wave < 4;
+  const int pb = keys ? (wave & 3) / (2 * C::KP) : (wave & 3) / C::VP;  // block of the chunk
+  const int sbk = (wave / C::KP) & 1, kp = wave % C::KP, vp = wave % C::VP;
+  const uint32_t koff = col * C::KROW + (C::KROW / 4) * h + C::KBYTES * kp;
+  // a value piece's part begins at any bit; of 3-bit rows two bytes are read, inside the row
+  const int vbit = VB * (CH * col + C::EPP * vp);
+  const int vbyte = VB == 3 && (vbit >> 3) > C::VROW - 2 ? C::VROW - 2 : vbit >> 3;
+  const int vshift = vbit - 8 * vbyte;
+  const uint32_t voff = 4 * h * C::VROW + vbyte;
+  // scales: of the quarter key row's first and (D = 256) second half, or of the value piece
+  const uint32_t soff = keys ? ((col << p->lg_gk) + ((D / 4 * h) >> p->lg_kg)) * 2
+                             : ((4 * h << p->lg_gv) + ((col * CH) >> p->lg_vg)) * 2;
+  const uint32_t soff2 = ((col << p->lg_gk) + ((D / 4 * h + D / 8) >> p->lg_kg)) * 2;
+
+  while (true) {
+    wk.uniform();
+    p = at_again(p);
+    const int reads = at_reads(wk.sq, a_tok, wk.t);
+    const int nblk = (reads + 31) >> 5;
+    int k0, k1;
+    wk.blocks(reads, nblk, k0, k1);
+    const AtSeq& sq = wk.sq;
+    const int hu = wk.hu, t = wk.t, b = wk.b;
+    if (k0 < k1) {
+      const int kh = p->nhb == 1 ? hu : hu / p->nhb, hblk = hu - kh * p->nhb;
+      const int hb = p->hb, head0 = kh * p->share + hblk * hb;
+      const int nh = p->share - hblk * hb < hb ? p->share - hblk * hb : hb;
+      const int tok0 = t * a_tok;
+      const int ntok = sq.n - tok0 < a_tok ? sq.n - tok0 : a_tok;
+      const int before = sq.len - sq.n;
+      const int len = sq.len;
+
+      // ---- the stream of blocks ----
+      const int page = p->page, pages = p->pages;
+      const uint32_t page16 = p->page16, page_mul = p->page_mul;
+      const uint32_t prow = static_cast<uint32_t>(p->heads) * page;
+      // of this wave's half: codes and scales of the head, bytes of a row, log2 of a row's scales
+      const uint32_t rbytes = keys ? C::KROW : C::VROW;
+      const int lg = keys ? p->lg_gk : p->lg_gv;
+      const char* const codes = reinterpret_cast<const char*>(keys ? p->kcodes : p->vcodes) + static_cast<int64_t>(kh) * page * rbytes;
+      const char* const scales = reinterpret_cast<const char*>(keys ? p->kscales : p->vscales) + ((static_cast<int64_t>(kh) * page) << (lg + 1));
+      typedef const int32_t __attribute__((address_space(4))) * ConstIds;
+      const ConstIds ids = (ConstIds)reinterpret_cast<uintptr_t>(p->page_table + static_cast<int64_t>(b) * p->table_width);
+      // page ids of a block's halves (a half past the end stands for the first one), read a chunk ahead
+      int id[2] = {}, in[2] = {};
+      auto look = [&](int blk) __attribute__((always_inline)) {
+        const int j = blk * 32, j2 = j + 16 < len ? j + 16 : j;
+        const int pi = at_div(j >> 4, page16, page_mul), pi2 = at_div(j2 >> 4, page16, page_mul);
+        in[0] = j - pi * page;
+        in[1] = j2 - pi2 * page;
+        id[0] = len > 0 ? ids[pi] : -1;
+        id[1] = len > 0 ? ids[pi2] : -1;
+      };
+      uint32_t xc[8] = {}, xs[8] = {};  // codes and scales of this wave's part, as loaded
+      uint32_t bad = 0;       // bit y: the page of half y is none
+      auto load = [&]() __attribute__((always_inline)) {
+        int64_t row_of[2];
+        bad = 0;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const bool none = static_cast<uint32_t>(id[y]) >= static_cast<uint32_t>(pages);
+          bad |= none ? 1u << y : 0u;
+          row_of[y] = static_cast<int64_t>(static_cast<uint64_t>(none ? 0u : static_cast<uint32_t>(id[y])) * prow) + in[y];
+        }
+        if (keys) {
+          const int64_t row = sbk ? row_of[1] : row_of[0];
+          const uint32_t ko = at_fresh(koff), so = at_fresh(soff);
+          const AtPtr kc = at_base(codes, row * C::KROW);
+          constexpr int L = C::KW % 4 == 0 ? 4 : C::KW % 3 == 0 ? 3 : C::KW % 2 == 0 ? 2 : 1;  // words of a load
+          if constexpr (C::KBYTES == 6) {
+            xc[0] = at_load<uint32_t>(kc, ko);
+            xc[1] = at_load<uint16_t>(kc + 4, ko);
+          } else {
+#pragma unroll
+            for (int k = 0; k < C::KW; k += L) {
+              if constexpr (L == 4) {
+                const u32x4_t y = at_get<u32x4_t>(kc + 4 * k, ko);
+                xc[k] = y.x; xc[k + 1] = y.y; xc[k + 2] = y.z; xc[k + 3] = y.w;
+              } else if constexpr (L == 3) {
+                const u32x3_t y = at_get<u32x3_t>(kc + 4 * k, ko);
+                xc[k] = y.x; xc[k + 1] = y.y; xc[k + 2] = y.z;
+              } else if constexpr (L == 2) {
+                const u32x2_t y = at_get<u32x2_t>(kc + 4 * k, ko);
+                xc[k] = y.x; xc[k + 1] = y.y;
+              } else {
+                xc[k] = at_get<uint32_t>(kc + 4 * k, ko);
+              }
+            }
+          }
+          const AtPtr sp = at_base(scales, row << (lg + 1));
+          xs[0] = at_get<uint16_t>(sp, so);
+          if constexpr (C::KS == 2) xs[1] = at_get<uint16_t>(sp, at_fresh(soff2));
+        } else {
+          const uint32_t vo = at_fresh(voff), so = at_fresh(soff);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const AtPtr vr = at_base(codes, row_of[i >> 2] * C::VROW) + (i & 3) * C::VROW;
+            if constexpr (VB == 3) xc[i] = at_load<uint16_t>(vr, vo);
+            else if constexpr (C::VBITS <= 8) xc[i] = at_get<uint8_t>(vr, vo);
+            else if constexpr (C::VBITS == 16) xc[i] = at_get<uint16_t>(vr, vo);
+            else xc[i] = at_get<uint32_t>(vr, vo);
+            xs[i] = at_get<uint16_t>(at_base(scales, (row_of[i >> 2] + (i & 3)) << (lg + 1)), so);
+          }
+        }
+      };
+
+      // what was loaded, of block blk, into buffer `buf`
+      auto decode = [&](int buf, int blk) __attribute__((always_inline)) {
+        const int lane = at_fresh(threadIdx.x & 63), h = lane >> 4;
+        const uint32_t lane4 = (lane & 31) * 4;
+        char* const dst = smem + C::BUF + buf * C::BYTES + 16 * lane;
+        AwHeader* const hdr = reinterpret_cast<AwHeader*>(smem + C::HDR) + buf * NB + pb;
+        if (keys) {
+          uint32_t z[C::KS], big = 0;
+#pragma unroll
+          for (int y = 0; y < C::KS; ++y) {
+            z[y] = (bad >> sbk) & 1u ? 0x7e007e00u : xs[y] | (xs[y] << 16);  // scores of a bad page are NaN
+            big = z[y] > big ? z[y] : big;
+          }
+          int e = 0;
+          if (__any(big > 0x7000ffffu) || !__any(big > 0x2c00ffffu)) {
+            float top = 0.f;
+#pragma unroll
+            for (int y = 0; y < C::KS; ++y)
+              if ((z[y] & 0x7c00u) != 0x7c00u) top = fmaxf(top, fabsf(half_bits_to_float(static_cast<uint16_t>(z[y]))));
+            e = aw_exponent(top);
+          }
+          uint32_t scale = at_mul(C::KS == 2 && kp ? z[C::KS - 1] : z[0], at_pow2(e));
+#pragma unroll
+          for (int st = 0; st < C::SPP; ++st) {
+            AtLook<KB> x;
+            at_look_k<C, KB>(xc, st, lane4, x);
+            uint32_t a[4];
+            at_pairs_k<KB>(x, scale, a);
+            *reinterpret_cast<u32x4_t*>(dst + ((pb * 2 + sbk) * NS + kp * C::SPP + st) * 1024) = u32x4_t{a[0], a[1], a[2], a[3]};
+          }
+          if (lane == 0) hdr->kf[sbk] = at_exp2(static_cast<float>(e));
+          return;
+        }
+        uint32_t raw[4], big = 0;  // scales of tokens 2 i and 2 i + 1
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[i] = at_pack(xs[2 * i], xs[2 * i + 1]);
+        if (blk * 32 + 32 > len || bad) {
+          const int j0 = blk * 32 + 4 * h;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = j0 + 16 * (i >> 1) + 2 * (i & 1);
+            const bool dead = (bad >> (i >> 1)) & 1u;
+            raw[i] &= (dead || j >= len ? 0u : 0xffffu) | (dead || j + 1 >= len ? 0u : 0xffff0000u);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) big = at_max_u16(raw[i], big);
+        big = big > (big << 16) ? big : big << 16;
+        int e = 0;
+        uint32_t vbad = 0;
+        if (__any(big > 0x7000ffffu) || !__any(big > 0x2c00ffffu)) {
+          float top = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t bits = (raw[i >> 1] >> (16 * (i & 1))) & 0xffffu;
+            const uint64_t who = __ballot((bits & 0x7c00u) == 0x7c00u);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              if ((who >> (16 * y)) & 0xffffu) vbad |= 1u << (16 * (i >> 2) + 4 * y + (i & 3));
+            if ((who >> (16 * h)) & 0xffffu) raw[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
+            else top = fmaxf(top, fabsf(half_bits_to_float(static_cast<uint16_t>(bits))));
+          }
+          e = aw_exponent(top);
+        }
+        if (lane == 0) {
+          hdr->vexp = e;
+          hdr->vbad = vbad;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[i] = at_mul(raw[i], at_pow2(e));
+        uint32_t ev[4], od[4];
+        if constexpr (VB < 8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) at_pair<VB>(xc[2 * i] >> vshift, xc[2 * i + 1] >> vshift, ev[i], od[i]);
+        }
+#pragma unroll
+        for (int n = 0; n < C::EPP; ++n) {
+          uint32_t a[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t x;
+            if constexpr (VB == 8) x = at_pack(at_lds(at_byte<128>(xc[2 * i], n, lane4)), at_lds(at_byte<128>(xc[2 * i + 1], n, lane4)));
+            else x = at_pair_at<C, VB>((n & 1) ? od[i] : ev[i], n >> 1, lane4);
+            a[i] = at_mul(x, raw[i]);
+          }
+          *reinterpret_cast<u32x4_t*>(dst + C::VOFF + (pb * CH + vp * C::EPP + n) * 1024) = u32x4_t{a[0], a[1], a[2], a[3]};
+        }
+      };
+
+      // ---- q: row group wave + 8 r of the tile to this wave, by way of LDS ----
+      AtQuery<D, 4> qs(p, sq.row0 + tok0, head0, tok0, ntok, nh);
+      qs.load(p, 16 * wave);
+      int blk = k0 + pb;
+      if (blk < k1) {
+        look(blk);
+        load();
+        if (blk + NB < k1) look(blk + NB);
+      }
+      uint32_t q[R][NS][4];
+      float c1[R], mo[R], l[R];  // score factor; reference - 7; sum
+      f32x4_t o[R][CH];
+      __syncthreads();  // the last unit's readers of this memory are done
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int r0 = 16 * (wave + W * r), at = C::BUF + wave * 16 * C::QP;
+        wave_lds_sync();
+#pragma unroll 1
+        for (int y = 0; y < 16; y += 4) {
+          if (r + y) qs.load(p, r0 + y);
+          qs.rotate(p, smem, r0 + y, at + y * C::QP, C::QP, C::C1, C::LIM, before, len);
+        }
+        wave_lds_sync();
+#pragma unroll
+        for (int st = 0; st < NS; ++st) {
+          const u32x4_t x = *reinterpret_cast<const u32x4_t*>(smem + at + col * C::QP + (D / 2) * h + 16 * st);
+          q[r][st][0] = x.x; q[r][st][1] = x.y; q[r][st][2] = x.z; q[r][st][3] = x.w;
+        }
+        c1[r] = *reinterpret_cast<const float*>(smem + C::C1 + 4 * (r0 + col));
+        mo[r] = kAtNone;
+        l[r] = 0.f;
+#pragma unroll
+        for (int n = 0; n < CH; ++n) o[r][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+      __syncthreads();
+      const bool masked = p->tree != nullptr;
+      int cut = masked ? before : before + tok0 + 1;  // from this token on some row's mask may cut
+      cut = cut < 0 ? 0 : cut;
+      const uint32_t* const tree = p->tree;
+      const uint32_t hb_mul = p->hb_mul;
+      const bool live = ((static_cast<uint32_t>(16 * wave) * hb_mul) >> 16) < static_cast<uint32_t>(ntok);
+      int vexp = 0;  // the sums are held times 2^-vexp
+
+      // scores, weights and sums of block x of the chunk at block c
+      auto multiply = [&](int buf, int x, int blk) __attribute__((always_inline)) {
+        const int lane = at_fresh(threadIdx.x & 63), h = lane >> 4;
+        const char* const src = smem + C::BUF + buf * C::BYTES + 16 * lane;
+        const AwHeader* const hdr = reinterpret_cast<const AwHeader*>(smem + C::HDR) + buf * NB + x;
+        f32x4_t s[R][2];
+        float cf[R][2], mx[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) s[r][0] = s[r][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int y = 0; y < 2 * NS; ++y) {
+          const u32x4_t z = *reinterpret_cast<const u32x4_t*>(src + (x * 2 * NS + y) * 1024);
+          const uint32_t a[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+          for (int r = 0; r < R; ++r) s[r][y / NS] = at_mfma(a, q[r][y % NS], s[r][y / NS]);
+          if (y % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int sb = 0; sb < 2; ++sb) cf[r][sb] = c1[r] * hdr->kf[sb];
+        if (blk * 32 + 32 > cut) {
+          const int j0 = blk * 32 + 4 * h;
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const int row = 16 * (wave + W * r) + (lane & 15), lim = *reinterpret_cast<const int*>(smem + C::LIM + 4 * row);
+            const int tk = (static_cast<uint32_t>(row) * p->hb_mul) >> 16;
+            const uint32_t* bits = tree + static_cast<int64_t>(sq.row0 + tok0 + (tk < ntok ? tk : 0)) * p->tree_words;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int j = j0 + 16 * (i >> 2) + (i & 3);
+              bool see = j < lim;
+              if (tree && !see && j < len) {
+                const int z = j - before;
+                if (z >= 0 && z < p->tree_words * 32) see = (bits[z >> 5] >> (z & 31)) & 1u;
+              }
+              s[r][i >> 2][i & 3] = see ? s[r][i >> 2][i & 3] : -__builtin_inff();
+            }
+          }
+        }
+        bool move = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          mx[r] = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])) * cf[r][0],
+                        fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])) * cf[r][1]);
+          move = move || mx[r] > mo[r] + (7.f + kAtLazy);
+        }
+        if (__any(move)) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            float y, z;
+            kv_both<4>(mx[r], y, z);
+            kv_both<5>(fmaxf(y, z), y, z);
+            y = fmaxf(y, z);
+            if (y > mo[r] + (7.f + kAtLazy)) {  // the same in the four lanes of a row
+              const float f = at_exp2(mo[r] + 7.f - y);
+              mo[r] = y - 7.f;
+              l[r] *= f;
+#pragma unroll
+              for (int n = 0; n < CH; ++n) o[r][n] *= f;
+            }
+          }
+        }
+        uint32_t pb_[R][4];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float e[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) e[i] = at_exp2(__builtin_fmaf(s[r][i >> 2][i & 3], cf[r][i >> 2], -mo[r]));
+          l[r] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const half2_t y{static_cast<_Float16>(e[2 * i]), static_cast<_Float16>(e[2 * i + 1])};
+            pb_[r][i] = __builtin_bit_cast(uint32_t, y);
+          }
+        }
+        const int ve = at_uniform(hdr->vexp);
+        const uint32_t vbad = static_cast<uint32_t>(at_uniform(static_cast<int>(hdr->vbad)));
+        if (ve != vexp) {
+          const float f = at_exp2(static_cast<float>(vexp - ve));
+          vexp = ve;
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int n = 0; n < CH; ++n) o[r][n] *= f;
+        }
+        if (vbad) {
+          // tokens whose value is no number: rows that see one become NaN, others stay
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if ((vbad >> (16 * (i >> 2) + 4 * h + (i & 3))) & 1u) {
+#pragma unroll
+              for (int r = 0; r < R; ++r)
+                if (s[r][i >> 2][i & 3] != -__builtin_inff()) l[r] = __builtin_nanf("");
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < CH; ++n) {
+          const u32x4_t z = *reinterpret_cast<const u32x4_t*>(src + C::VOFF + (x * CH + n) * 1024);
+          const uint32_t a[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+          for (int r = 0; r < R; ++r) o[r][n] = at_mfma(a, pb_[r], o[r][n]);
+          if (n % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+
+      // (first round: nothing to multiply yet)
+      int buf = 1;
+      for (int c = k0 - NB; c < k1; c += NB) {
+#pragma unroll 1
+        for (int phase = 0; phase < 2; ++phase) {
+          if ((phase == 0) == keys) {
+            if (live && c >= k0) {
+#pragma unroll 1
+              for (int x = 0; x < NB && c + x < k1; ++x) multiply(buf, x, c + x);
+            }
+          } else if (blk < k1) {
+            decode(buf ^ 1, blk);
+            blk += NB;
+            if (blk < k1) {
+              load();
+              if (blk + NB < k1) look(blk + NB);
+            }
+          }
+        }
+        __syncthreads();
+        buf ^= 1;
+      }
+
+      // ---- out: a wave's rows, transposed by way of LDS ----
+      p = at_again(p);
+      const int lane = at_fresh(threadIdx.x & 63), col = lane & 15, h = lane >> 4;
+      const int d0 = kv_chunk(lane) * EL;
+      const uint32_t vsg = p->vsigns[d0 >> 5] >> (d0 & 31);
+      const bool whole = k0 == 0 && k1 == nblk;
+      float* const slot = p->parts + static_cast<int64_t>(2 * wg + (k0 > 0 ? 0 : 1)) * C::ROWS * (D + 2);
+      float* const red = reinterpret_cast<float*>(smem + C::BUF) + wave * C::FR * C::FP;
+      const float fv = at_exp2(static_cast<float>(vexp));
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float x, y;
+        kv_both<4>(l[r], x, y);
+        kv_both<5>(x + y, x, y);
+        l[r] = x + y;
+#pragma unroll
+        for (int r1 = 0; r1 < 16; r1 += C::FR) {
+          wave_lds_sync();
+          if (col >= r1 && col < r1 + C::FR)
+#pragma unroll
+            for (int n = 0; n < CH; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) red[(col - r1) * C::FP + CH * (4 * h + i) + n] = o[r][n][i] * fv;
+          wave_lds_sync();
+#pragma unroll 1
+          for (int z = r1; z < r1 + C::FR; ++z) {
+            const int row = 16 * (wave + W * r) + z;
+            const int tk = (static_cast<uint32_t>(row) * hb_mul) >> 16, hd = row - tk * hb;
+            if (tk >= ntok || hd >= nh) continue;
+            const float ls = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(l[r]), z));
+            const float top = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mo[r]), z));
+            float v[EL];
+#pragma unroll
+            for (int e = 0; e < EL; ++e) v[e] = red[(z - r1) * C::FP + d0 + e];
+            if (whole) {
+              at_finish<D>(p, v, ls, static_cast<int64_t>(sq.row0) + tok0 + tk, head0 + hd, vsg, lane);
+            } else {
+#pragma unroll
+              for (int e = 0; e < EL; ++e) slot[row * D + d0 + e] = v[e];
+              if (lane == 0) {
+                slot[C::ROWS * D + row] = top;
+                slot[C::ROWS * D + C::ROWS + row] = ls;
+              }
+            }
+          }
+        }
+      }
+      if (!whole && k0 == 0 && threadIdx.x == 0) {
+        AttendMeta m{};
+        m.parts = wk.more(nblk, wg);
+        m.row0 = sq.row0 + tok0;
+        m.nrows = ntok;
+        m.head0 = head0;
+        m.nh = nh;
+        p->meta[wg] = m;
+      }
+    }
+    if (!wk.next(p, reads, hu_n)) break;
+  }
+}
+
+template <int KB, int VB, int D, int R>
+hipError_t aw_launch(const AttendParams& p, hipStream_t s) {
+  using C = AwCfg<KB, VB, D, R>;
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend_wide<KB, VB, D, R>),
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_attend_wide<KB, VB, D, R>), dim3(C::GRID), dim3(C::T), C::LDS, s, p);
+  return hipGetLastError();
+}
+
+template <int KB, int VB>
+hipError_t at_launch_d(const AttendParams& p, int D, int rows, hipStream_t s) {
+  switch (D) {
+    case 64: return rows == 16 ? at_launch<KB, VB, 64, 1>(p, s) : rows == 128 ? aw_launch<KB, VB, 64, 1>(p, s) : aw_launch<KB, VB, 64, 2>(p, s);
+    case 128: return rows == 16 ? at_launch<KB, VB, 128, 1>(p, s) : rows == 128 ? aw_launch<KB, VB, 128, 1>(p, s) : aw_launch<KB, VB, 128, 2>(p, s);
+    default: return rows == 16 ? at_launch<KB, VB, 256, 1>(p, s) : aw_launch<KB, VB, 256, 1>(p, s);
+  }
+}
+
+// One key format's kernels, by the rows of a tile.
+template <int KB>
+hipError_t at_launch_k(const AttendParams& p, int vbits, int D, int rows, hipStream_t s) {
+  switch (vbits) {
+    case 2: return at_launch_d<KB, 2>(p, D, rows, s);
+    case 3: return at_launch_d<KB, 3>(p, D, rows, s);
+    case 4: return at_launch_d<KB, 4>(p, D, rows, s);
+    default: return at_launch_d<KB, 8>(p, D, rows, s);
+  }
+}
+
+}  // namespace tq
