@@ -14,6 +14,8 @@
 // the waves that decode parts of it agree without asking each other; they travel with the block.
 #pragma once
 
+#include <type_traits>
+
 #include "encode_lane.hpp"
 #include "kv_attend.hpp"
 
@@ -34,6 +36,7 @@ struct AwCfg {
   static constexpr int SPP = NS / KP, EPP = CH / VP;          // steps and value elements of such a wave
   static constexpr int KBYTES = SPP * KB, KW = (KBYTES + 3) / 4;  // its bytes of a quarter key row
   static constexpr int VBITS = EPP * VB;                          // its bits of a value piece
+  using Piece = std::conditional_t<VB == 3 || VBITS == 16, uint16_t, std::conditional_t<VBITS <= 8, uint8_t, uint32_t>>;
   static constexpr int KS = D == 256 ? 2 : 1;                 // key scales of a quarter row, at most
   static constexpr int GRID = kAtCus;
   // LDS; the queries on their way in and the sums on their way out take the place of the buffers
@@ -57,6 +60,9 @@ struct AwHeader {
   int32_t vexp;
   uint32_t vbad;
 };
+
+// The lowest n bits; none for n <= 0, all from 32 on.
+__device__ __forceinline__ uint32_t aw_low(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
 // The power of two that brings scales near 1, if one is beyond 2^13, no number, or all are below
 // 2^-4; top: the largest finite one of the lane's. 2^-15 to 2^15.
@@ -138,9 +144,13 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
         id[0] = len > 0 ? ids[pi] : -1;
         id[1] = len > 0 ? ids[pi2] : -1;
       };
-      uint32_t xc[8] = {}, xs[8] = {};  // codes and scales of this wave's part, as loaded
+      // codes and scales of this wave's part, in the types they are loaded as: widened at once, they
+      // would be waited for at once
+      uint32_t kx[8];
+      uint16_t ks[C::KS], vs[8];
+      typename C::Piece vx[8];
       uint32_t bad = 0;       // bit y: the page of half y is none
-      auto load = [&]() __attribute__((always_inline)) {
+      auto load = [&](auto role) __attribute__((always_inline)) {
         int64_t row_of[2];
         bad = 0;
 #pragma unroll
@@ -149,59 +159,61 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
           bad |= none ? 1u << y : 0u;
           row_of[y] = static_cast<int64_t>(static_cast<uint64_t>(none ? 0u : static_cast<uint32_t>(id[y])) * prow) + in[y];
         }
-        if (keys) {
+        if constexpr (decltype(role)::value) {
           const int64_t row = sbk ? row_of[1] : row_of[0];
           const uint32_t ko = at_fresh(koff), so = at_fresh(soff);
           const AtPtr kc = at_base(codes, row * C::KROW);
           constexpr int L = C::KW % 4 == 0 ? 4 : C::KW % 3 == 0 ? 3 : C::KW % 2 == 0 ? 2 : 1;  // words of a load
           if constexpr (C::KBYTES == 6) {
-            xc[0] = at_load<uint32_t>(kc, ko);
-            xc[1] = at_load<uint16_t>(kc + 4, ko);
+            kx[0] = at_load<uint32_t>(kc, ko);
+            kx[1] = at_load<uint16_t>(kc + 4, ko);
           } else {
 #pragma unroll
             for (int k = 0; k < C::KW; k += L) {
               if constexpr (L == 4) {
                 const u32x4_t y = at_get<u32x4_t>(kc + 4 * k, ko);
-                xc[k] = y.x; xc[k + 1] = y.y; xc[k + 2] = y.z; xc[k + 3] = y.w;
+                kx[k] = y.x; kx[k + 1] = y.y; kx[k + 2] = y.z; kx[k + 3] = y.w;
               } else if constexpr (L == 3) {
                 const u32x3_t y = at_get<u32x3_t>(kc + 4 * k, ko);
-                xc[k] = y.x; xc[k + 1] = y.y; xc[k + 2] = y.z;
+                kx[k] = y.x; kx[k + 1] = y.y; kx[k + 2] = y.z;
               } else if constexpr (L == 2) {
                 const u32x2_t y = at_get<u32x2_t>(kc + 4 * k, ko);
-                xc[k] = y.x; xc[k + 1] = y.y;
+                kx[k] = y.x; kx[k + 1] = y.y;
               } else {
-                xc[k] = at_get<uint32_t>(kc + 4 * k, ko);
+                kx[k] = at_get<uint32_t>(kc + 4 * k, ko);
               }
             }
           }
           const AtPtr sp = at_base(scales, row << (lg + 1));
-          xs[0] = at_get<uint16_t>(sp, so);
-          if constexpr (C::KS == 2) xs[1] = at_get<uint16_t>(sp, at_fresh(soff2));
+          ks[0] = at_get<uint16_t>(sp, so);
+          if constexpr (C::KS == 2) ks[1] = at_get<uint16_t>(sp, at_fresh(soff2));
         } else {
           const uint32_t vo = at_fresh(voff), so = at_fresh(soff);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const AtPtr vr = at_base(codes, row_of[i >> 2] * C::VROW) + (i & 3) * C::VROW;
-            if constexpr (VB == 3) xc[i] = at_load<uint16_t>(vr, vo);
-            else if constexpr (C::VBITS <= 8) xc[i] = at_get<uint8_t>(vr, vo);
-            else if constexpr (C::VBITS == 16) xc[i] = at_get<uint16_t>(vr, vo);
-            else xc[i] = at_get<uint32_t>(vr, vo);
-            xs[i] = at_get<uint16_t>(at_base(scales, (row_of[i >> 2] + (i & 3)) << (lg + 1)), so);
+          for (int y = 0; y < 2; ++y) {
+            const AtPtr vc = at_base(codes, row_of[y] * C::VROW), sp = at_base(scales, row_of[y] << (lg + 1));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const AtPtr vr = vc + i * C::VROW;
+              if constexpr (VB == 3) vx[4 * y + i] = at_load<uint16_t>(vr, vo);
+              else vx[4 * y + i] = at_get<typename C::Piece>(vr, vo);
+              vs[4 * y + i] = at_get<uint16_t>(sp + (static_cast<int64_t>(i) << (lg + 1)), so);
+            }
           }
         }
       };
 
       // what was loaded, of block blk, into buffer `buf`
-      auto decode = [&](int buf, int blk) __attribute__((always_inline)) {
+      auto decode = [&](auto role, int buf, int blk) __attribute__((always_inline)) {
         const int lane = at_fresh(threadIdx.x & 63), h = lane >> 4;
         const uint32_t lane4 = (lane & 31) * 4;
         char* const dst = smem + C::BUF + buf * C::BYTES + 16 * lane;
         AwHeader* const hdr = reinterpret_cast<AwHeader*>(smem + C::HDR) + buf * NB + pb;
-        if (keys) {
+        if constexpr (decltype(role)::value) {
           uint32_t z[C::KS], big = 0;
 #pragma unroll
           for (int y = 0; y < C::KS; ++y) {
-            z[y] = (bad >> sbk) & 1u ? 0x7e007e00u : xs[y] | (xs[y] << 16);  // scores of a bad page are NaN
+            z[y] = (bad >> sbk) & 1u ? 0x7e007e00u : ks[y] | (static_cast<uint32_t>(ks[y]) << 16);  // scores of a bad page are NaN
             big = z[y] > big ? z[y] : big;
           }
           int e = 0;
@@ -216,17 +228,16 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
 #pragma unroll
           for (int st = 0; st < C::SPP; ++st) {
             AtLook<KB> x;
-            at_look_k<C, KB>(xc, st, lane4, x);
+            at_look_k<C, KB>(kx, st, lane4, x);
             uint32_t a[4];
             at_pairs_k<KB>(x, scale, a);
             *reinterpret_cast<u32x4_t*>(dst + ((pb * 2 + sbk) * NS + kp * C::SPP + st) * 1024) = u32x4_t{a[0], a[1], a[2], a[3]};
           }
           if (lane == 0) hdr->kf[sbk] = at_exp2(static_cast<float>(e));
-          return;
-        }
+        } else {
         uint32_t raw[4], big = 0;  // scales of tokens 2 i and 2 i + 1
 #pragma unroll
-        for (int i = 0; i < 4; ++i) raw[i] = at_pack(xs[2 * i], xs[2 * i + 1]);
+        for (int i = 0; i < 4; ++i) raw[i] = at_pack(vs[2 * i], vs[2 * i + 1]);
         if (blk * 32 + 32 > len || bad) {
           const int j0 = blk * 32 + 4 * h;
 #pragma unroll
@@ -264,7 +275,7 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
         uint32_t ev[4], od[4];
         if constexpr (VB < 8) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) at_pair<VB>(xc[2 * i] >> vshift, xc[2 * i + 1] >> vshift, ev[i], od[i]);
+          for (int i = 0; i < 4; ++i) at_pair<VB>(vx[2 * i] >> vshift, vx[2 * i + 1] >> vshift, ev[i], od[i]);
         }
 #pragma unroll
         for (int n = 0; n < C::EPP; ++n) {
@@ -272,22 +283,26 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t x;
-            if constexpr (VB == 8) x = at_pack(at_lds(at_byte<128>(xc[2 * i], n, lane4)), at_lds(at_byte<128>(xc[2 * i + 1], n, lane4)));
+            if constexpr (VB == 8) x = at_pack(at_lds(at_byte<128>(vx[2 * i], n, lane4)), at_lds(at_byte<128>(vx[2 * i + 1], n, lane4)));
             else x = at_pair_at<C, VB>((n & 1) ? od[i] : ev[i], n >> 1, lane4);
             a[i] = at_mul(x, raw[i]);
           }
           *reinterpret_cast<u32x4_t*>(dst + C::VOFF + (pb * CH + vp * C::EPP + n) * 1024) = u32x4_t{a[0], a[1], a[2], a[3]};
+        }
         }
       };
 
       // ---- q: row group wave + 8 r of the tile to this wave, by way of LDS ----
       AtQuery<D, 4> qs(p, sq.row0 + tok0, head0, tok0, ntok, nh);
       qs.load(p, 16 * wave);
-      int blk = k0 + pb;
-      if (blk < k1) {
+      // past its last block a wave repeats it, into buffers that nothing reads
+      const auto next_of = [&](int x) { return x + NB < k1 ? x + NB : x; };
+      int blk = k0 + pb < k1 ? k0 + pb : k0;
+      {
         look(blk);
-        load();
-        if (blk + NB < k1) look(blk + NB);
+        if (keys) load(AtInt<1>{});
+        else load(AtInt<0>{});
+        look(next_of(blk));
       }
       uint32_t q[R][NS][4];
       float c1[R], mo[R], l[R];  // score factor; reference - 7; sum
@@ -323,49 +338,65 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
       const bool live = ((static_cast<uint32_t>(16 * wave) * hb_mul) >> 16) < static_cast<uint32_t>(ntok);
       int vexp = 0;  // the sums are held times 2^-vexp
 
-      // scores, weights and sums of block x of the chunk at block c
+      // scores, weights and sums of block x of the chunk. Pieces are read G at a time, a group ahead of
+      // their products.
+      constexpr int G = 2, KG = 2 * NS / G, VG = CH / G;
       auto multiply = [&](int buf, int x, int blk) __attribute__((always_inline)) {
         const int lane = at_fresh(threadIdx.x & 63), h = lane >> 4;
-        const char* const src = smem + C::BUF + buf * C::BYTES + 16 * lane;
+        const char* const ksrc = smem + C::BUF + buf * C::BYTES + 16 * lane + x * 2 * NS * 1024;
+        const char* const vsrc = smem + C::BUF + C::VOFF + buf * C::BYTES + 16 * lane + x * CH * 1024;
         const AwHeader* const hdr = reinterpret_cast<const AwHeader*>(smem + C::HDR) + buf * NB + x;
+        u32x4_t z[2][G];
+        auto read = [&](const char* src, u32x4_t (&o)[G]) __attribute__((always_inline)) {
+#pragma unroll
+          for (int y = 0; y < G; ++y) o[y] = *reinterpret_cast<const u32x4_t*>(src + y * 1024);
+        };
         f32x4_t s[R][2];
-        float cf[R][2], mx[R];
+        read(ksrc, z[0]);
 #pragma unroll
-        for (int r = 0; r < R; ++r) s[r][0] = s[r][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int g = 0; g < KG; ++g) {
+          if (g + 1 < KG) read(ksrc + (g + 1) * G * 1024, z[(g + 1) & 1]);
+          else read(vsrc, z[KG & 1]);
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int y = 0; y < 2 * NS; ++y) {
-          const u32x4_t z = *reinterpret_cast<const u32x4_t*>(src + (x * 2 * NS + y) * 1024);
-          const uint32_t a[4] = {z.x, z.y, z.z, z.w};
+          for (int y = 0; y < G; ++y) {
+            const int n = G * g + y, sb = n / NS, st = n % NS;
+            const u32x4_t w = z[g & 1][y];
+            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int r = 0; r < R; ++r) s[r][y / NS] = at_mfma(a, q[r][y % NS], s[r][y / NS]);
-          if (y % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+            for (int r = 0; r < R; ++r) s[r][sb] = at_mfma(a, q[r][st], st == 0 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : s[r][sb]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int sb = 0; sb < 2; ++sb) cf[r][sb] = c1[r] * hdr->kf[sb];
+        const float2 kf = *reinterpret_cast<const float2*>(hdr->kf);
+        const int ve = at_uniform(hdr->vexp);
+        const uint32_t vbad = static_cast<uint32_t>(at_uniform(static_cast<int>(hdr->vbad)));
         if (blk * 32 + 32 > cut) {
-          const int j0 = blk * 32 + 4 * h;
+          const int j0 = blk * 32;
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            const int row = 16 * (wave + W * r) + (lane & 15), lim = *reinterpret_cast<const int*>(smem + C::LIM + 4 * row);
-            const int tk = (static_cast<uint32_t>(row) * p->hb_mul) >> 16;
-            const uint32_t* bits = tree + static_cast<int64_t>(sq.row0 + tok0 + (tk < ntok ? tk : 0)) * p->tree_words;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int j = j0 + 16 * (i >> 2) + (i & 3);
-              bool see = j < lim;
-              if (tree && !see && j < len) {
-                const int z = j - before;
-                if (z >= 0 && z < p->tree_words * 32) see = (bits[z >> 5] >> (z & 31)) & 1u;
-              }
-              s[r][i >> 2][i & 3] = see ? s[r][i >> 2][i & 3] : -__builtin_inff();
+            const int row = 16 * (wave + W * r) + (lane & 15);
+            // the tokens of the block that the row sees, as bits
+            uint32_t see = aw_low(*reinterpret_cast<const int*>(smem + C::LIM + 4 * row) - j0);
+            if (tree) {
+              const int tk = (static_cast<uint32_t>(row) * p->hb_mul) >> 16, words = p->tree_words;
+              const uint32_t* bits = tree + static_cast<int64_t>(sq.row0 + tok0 + (tk < ntok ? tk : 0)) * words;
+              const int w = (j0 - before) >> 5, sh = (j0 - before) & 31;
+              const uint32_t w0 = w >= 0 && w < words ? bits[w] : 0u, w1 = w >= -1 && w + 1 < words ? bits[w + 1] : 0u;
+              see |= static_cast<uint32_t>((static_cast<uint64_t>(w1) << 32 | w0) >> sh) & aw_low(len - j0);
             }
+            see >>= 4 * h;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              s[r][i >> 2][i & 3] = (see >> (16 * (i >> 2) + (i & 3))) & 1u ? s[r][i >> 2][i & 3] : -__builtin_inff();
           }
         }
+        float cf[R][2], mx[R];
         bool move = false;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+          cf[r][0] = c1[r] * kf.x;
+          cf[r][1] = c1[r] * kf.y;
           mx[r] = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])) * cf[r][0],
                         fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])) * cf[r][1]);
           move = move || mx[r] > mo[r] + (7.f + kAtLazy);
@@ -373,10 +404,10 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
         if (__any(move)) {
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            float y, z;
-            kv_both<4>(mx[r], y, z);
-            kv_both<5>(fmaxf(y, z), y, z);
-            y = fmaxf(y, z);
+            float y, w;
+            kv_both<4>(mx[r], y, w);
+            kv_both<5>(fmaxf(y, w), y, w);
+            y = fmaxf(y, w);
             if (y > mo[r] + (7.f + kAtLazy)) {  // the same in the four lanes of a row
               const float f = at_exp2(mo[r] + 7.f - y);
               mo[r] = y - 7.f;
@@ -386,7 +417,22 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
             }
           }
         }
-        uint32_t pb_[R][4];
+        if (ve != vexp || vbad) {
+          const float f = at_exp2(static_cast<float>(vexp - ve));
+          vexp = ve;
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            // tokens whose value is no number: rows that see one become NaN, others stay
+            float y = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              y = (vbad >> (16 * (i >> 2) + 4 * h + (i & 3))) & 1u && s[r][i >> 2][i & 3] != -__builtin_inff() ? __builtin_nanf("") : y;
+            l[r] += y;
+#pragma unroll
+            for (int n = 0; n < CH; ++n) o[r][n] *= f;
+          }
+        }
+        uint32_t pr[R][4];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           float e[8];
@@ -396,61 +442,49 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const half2_t y{static_cast<_Float16>(e[2 * i]), static_cast<_Float16>(e[2 * i + 1])};
-            pb_[r][i] = __builtin_bit_cast(uint32_t, y);
+            pr[r][i] = __builtin_bit_cast(uint32_t, y);
           }
         }
-        const int ve = at_uniform(hdr->vexp);
-        const uint32_t vbad = static_cast<uint32_t>(at_uniform(static_cast<int>(hdr->vbad)));
-        if (ve != vexp) {
-          const float f = at_exp2(static_cast<float>(vexp - ve));
-          vexp = ve;
 #pragma unroll
-          for (int r = 0; r < R; ++r)
+        for (int g = 0; g < VG; ++g) {
+          if (g + 1 < VG) read(vsrc + (g + 1) * G * 1024, z[(KG + g + 1) & 1]);
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int n = 0; n < CH; ++n) o[r][n] *= f;
-        }
-        if (vbad) {
-          // tokens whose value is no number: rows that see one become NaN, others stay
+          for (int y = 0; y < G; ++y) {
+            const u32x4_t w = z[(KG + g) & 1][y];
+            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if ((vbad >> (16 * (i >> 2) + 4 * h + (i & 3))) & 1u) {
-#pragma unroll
-              for (int r = 0; r < R; ++r)
-                if (s[r][i >> 2][i & 3] != -__builtin_inff()) l[r] = __builtin_nanf("");
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < CH; ++n) {
-          const u32x4_t z = *reinterpret_cast<const u32x4_t*>(src + C::VOFF + (x * CH + n) * 1024);
-          const uint32_t a[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-          for (int r = 0; r < R; ++r) o[r][n] = at_mfma(a, pb_[r], o[r][n]);
-          if (n % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+            for (int r = 0; r < R; ++r) o[r][G * g + y] = at_mfma(a, pr[r], o[r][G * g + y]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
       };
 
-      // (first round: nothing to multiply yet)
-      int buf = 1;
-      for (int c = k0 - NB; c < k1; c += NB) {
-#pragma unroll 1
-        for (int phase = 0; phase < 2; ++phase) {
-          if ((phase == 0) == keys) {
+      // One loop for the waves of keys and one for those of values: with both roles in one, the loads
+      // in flight would be copied, and so waited for, where its paths meet. Each ends its rounds with
+      // the same barriers. (First round: nothing to multiply yet.)
+      auto rounds = [&](auto role) __attribute__((always_inline)) {
+        int buf = 1;
+        for (int c = k0 - NB; c < k1; c += NB) {
+          auto sums = [&]() __attribute__((always_inline)) {
             if (live && c >= k0) {
 #pragma unroll 1
-              for (int x = 0; x < NB && c + x < k1; ++x) multiply(buf, x, c + x);
+              for (int x = 0; x < NB; ++x)
+                if (x == 0 || c + x < k1) multiply(buf, x, c + x);
             }
-          } else if (blk < k1) {
-            decode(buf ^ 1, blk);
-            blk += NB;
-            if (blk < k1) {
-              load();
-              if (blk + NB < k1) look(blk + NB);
-            }
-          }
+          };
+          if constexpr (decltype(role)::value) sums();
+          decode(role, buf ^ 1, blk);
+          blk = next_of(blk);
+          load(role);
+          look(next_of(blk));
+          if constexpr (!decltype(role)::value) sums();
+          __syncthreads();
+          buf ^= 1;
         }
-        __syncthreads();
-        buf ^= 1;
-      }
+      };
+      if (keys) rounds(AtInt<1>{});
+      else rounds(AtInt<0>{});
 
       // ---- out: a wave's rows, transposed by way of LDS ----
       p = at_again(p);
