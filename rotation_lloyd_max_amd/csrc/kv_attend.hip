@@ -51,36 +51,58 @@ __global__ __launch_bounds__(256) void k_attend_join(JoinParams p) {
   const float* const base = p.parts + 2 * static_cast<int64_t>(blockIdx.x) * slot;
   auto part = [&](int i) { return base + (i == 0 ? slot : 2 * i * slot); };
   float top = kAtNone, l = 0.f;
-  for (int i = lane; i < n; i += 64) {
-    const float a = part(i)[p.rows * D + r];
-    wt[wave][i] = a;
-    top = fmaxf(top, a);
-  }
-  top = kv_wave_max(top);
-  for (int i = lane; i < n; i += 64) {
-    const float a = wt[wave][i], b = part(i)[p.rows * D + p.rows + r];
-    const float f = a == kAtNone ? 0.f : at_exp2(a - top);
-    wt[wave][i] = f;
-    l += b != b ? b : b * f;
-  }
-#pragma unroll
-  for (int x = 1; x < 64; x <<= 1) l += __shfl_xor(l, x);
-  wave_lds_sync();
-  // sixteen parts' loads at a time (past the last one: that one again, times zero)
   float v[EL] = {};
-  for (int i0 = 0; i0 < n; i0 += 16) {
-    float x[16][EL];
+  if (n <= 4) {
+    // everything at once (past the last part: that one again, times zero)
+    float x[4][EL], a[4], b[4];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float* s = part(i0 + k < n ? i0 + k : n - 1) + r * D + d0;
+    for (int k = 0; k < 4; ++k) {
+      const float* s = part(k < n ? k : n - 1);
+      a[k] = s[p.rows * D + r];
+      b[k] = s[p.rows * D + p.rows + r];
 #pragma unroll
-      for (int e = 0; e < EL; ++e) x[k][e] = s[e];
+      for (int e = 0; e < EL; ++e) x[k][e] = s[r * D + d0 + e];
     }
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float f = i0 + k < n ? wt[wave][i0 + k] : 0.f;
+    for (int k = 0; k < 4; ++k) top = fmaxf(top, a[k]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = k >= n || a[k] == kAtNone ? 0.f : at_exp2(a[k] - top);
+      l += k >= n ? 0.f : b[k] != b[k] ? b[k] : b[k] * f;
 #pragma unroll
       for (int e = 0; e < EL; ++e) v[e] = __builtin_fmaf(f, x[k][e], v[e]);
+    }
+  } else {
+    for (int i = lane; i < n; i += 64) {
+      const float a = part(i)[p.rows * D + r];
+      wt[wave][i] = a;
+      top = fmaxf(top, a);
+    }
+    top = kv_wave_max(top);
+    for (int i = lane; i < n; i += 64) {
+      const float a = wt[wave][i], b = part(i)[p.rows * D + p.rows + r];
+      const float f = a == kAtNone ? 0.f : at_exp2(a - top);
+      wt[wave][i] = f;
+      l += b != b ? b : b * f;
+    }
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) l += __shfl_xor(l, x);
+    wave_lds_sync();
+    // sixteen parts' loads at a time
+    for (int i0 = 0; i0 < n; i0 += 16) {
+      float x[16][EL];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float* s = part(i0 + k < n ? i0 + k : n - 1) + r * D + d0;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) x[k][e] = s[e];
+      }
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float f = i0 + k < n ? wt[wave][i0 + k] : 0.f;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) v[e] = __builtin_fmaf(f, x[k][e], v[e]);
+      }
     }
   }
   at_finish<D>(&p, v, l, static_cast<int64_t>(m.row0) + tk, m.head0 + hd, sg, lane);
