@@ -79,6 +79,7 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
   AtArgs p = (AtArgs)__builtin_amdgcn_kernarg_segment_ptr();
   const int tid = threadIdx.x, lane = tid & 63, wave = at_uniform(tid >> 6);
   const int col = lane & 15, h = lane >> 4;
+  const uint32_t lane4 = (lane & 31) * 4;
   const int wg = blockIdx.x;
   const int per = (p->B + 63) >> 6;
   const int b0 = lane * per;
@@ -144,19 +145,19 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
         id[0] = len > 0 ? ids[pi] : -1;
         id[1] = len > 0 ? ids[pi2] : -1;
       };
-      // codes and scales of this wave's part, in the types they are loaded as: widened at once, they
+      // codes and scales of this wave's part, of this round's and the next round's block, in the types they are loaded as: widened at once, they
       // would be waited for at once
-      uint32_t kx[8];
-      uint16_t ks[C::KS], vs[8];
-      typename C::Piece vx[8];
-      uint32_t bad = 0;       // bit y: the page of half y is none
+      uint32_t kx[8], kx1[8];
+      uint16_t ks[C::KS], vs[8], ks1[C::KS], vs1[8];
+      typename C::Piece vx[8], vx1[8];
+      uint32_t bad = 0, bad1 = 0;  // bit y: the page of half y is none
       auto load = [&](auto role) __attribute__((always_inline)) {
         int64_t row_of[2];
-        bad = 0;
+        bad1 = 0;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const bool none = static_cast<uint32_t>(id[y]) >= static_cast<uint32_t>(pages);
-          bad |= none ? 1u << y : 0u;
+          bad1 |= none ? 1u << y : 0u;
           row_of[y] = static_cast<int64_t>(static_cast<uint64_t>(none ? 0u : static_cast<uint32_t>(id[y])) * prow) + in[y];
         }
         if constexpr (decltype(role)::value) {
@@ -165,28 +166,28 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
           const AtPtr kc = at_base(codes, row * C::KROW);
           constexpr int L = C::KW % 4 == 0 ? 4 : C::KW % 3 == 0 ? 3 : C::KW % 2 == 0 ? 2 : 1;  // words of a load
           if constexpr (C::KBYTES == 6) {
-            kx[0] = at_load<uint32_t>(kc, ko);
-            kx[1] = at_load<uint16_t>(kc + 4, ko);
+            kx1[0] = at_load<uint32_t>(kc, ko);
+            kx1[1] = at_load<uint16_t>(kc + 4, ko);
           } else {
 #pragma unroll
             for (int k = 0; k < C::KW; k += L) {
               if constexpr (L == 4) {
                 const u32x4_t y = at_get<u32x4_t>(kc + 4 * k, ko);
-                kx[k] = y.x; kx[k + 1] = y.y; kx[k + 2] = y.z; kx[k + 3] = y.w;
+                kx1[k] = y.x; kx1[k + 1] = y.y; kx1[k + 2] = y.z; kx1[k + 3] = y.w;
               } else if constexpr (L == 3) {
                 const u32x3_t y = at_get<u32x3_t>(kc + 4 * k, ko);
-                kx[k] = y.x; kx[k + 1] = y.y; kx[k + 2] = y.z;
+                kx1[k] = y.x; kx1[k + 1] = y.y; kx1[k + 2] = y.z;
               } else if constexpr (L == 2) {
                 const u32x2_t y = at_get<u32x2_t>(kc + 4 * k, ko);
-                kx[k] = y.x; kx[k + 1] = y.y;
+                kx1[k] = y.x; kx1[k + 1] = y.y;
               } else {
-                kx[k] = at_get<uint32_t>(kc + 4 * k, ko);
+                kx1[k] = at_get<uint32_t>(kc + 4 * k, ko);
               }
             }
           }
           const AtPtr sp = at_base(scales, row << (lg + 1));
-          ks[0] = at_get<uint16_t>(sp, so);
-          if constexpr (C::KS == 2) ks[1] = at_get<uint16_t>(sp, at_fresh(soff2));
+          ks1[0] = at_get<uint16_t>(sp, so);
+          if constexpr (C::KS == 2) ks1[1] = at_get<uint16_t>(sp, at_fresh(soff2));
         } else {
           const uint32_t vo = at_fresh(voff), so = at_fresh(soff);
 #pragma unroll
@@ -195,21 +196,39 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const AtPtr vr = vc + i * C::VROW;
-              if constexpr (VB == 3) vx[4 * y + i] = at_load<uint16_t>(vr, vo);
-              else vx[4 * y + i] = at_get<typename C::Piece>(vr, vo);
-              vs[4 * y + i] = at_get<uint16_t>(sp + (static_cast<int64_t>(i) << (lg + 1)), so);
+              if constexpr (VB == 3) vx1[4 * y + i] = at_load<uint16_t>(vr, vo);
+              else vx1[4 * y + i] = at_get<typename C::Piece>(vr, vo);
+              vs1[4 * y + i] = at_get<uint16_t>(sp + (static_cast<int64_t>(i) << (lg + 1)), so);
             }
           }
         }
       };
 
-      // what was loaded, of block blk, into buffer `buf`
-      auto decode = [&](auto role, int buf, int blk) __attribute__((always_inline)) {
+      auto take = [&](auto role) __attribute__((always_inline)) {
+        bad = bad1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if constexpr (decltype(role)::value) {
+            if (i < C::KW) kx[i] = kx1[i];
+            if (i < C::KS) ks[i] = ks1[i];
+          } else {
+            vx[i] = vx1[i];
+            vs[i] = vs1[i];
+          }
+        }
+      };
+      // A round's decoding: what was loaded, of block blk, into buffer `buf`, in STEPS steps (of keys:
+      // 32-element steps; of values: elements) of a table lookup and, later, its use.
+      constexpr int STEPS = C::SPP;
+      static_assert(C::SPP == C::EPP, "as many for either role");
+      uint32_t mul[4], ev[4], od[4], tb[8];  // scales, value pairs of even and odd elements, table words
+      uint32_t dst;                          // LDS address
+      auto prepare = [&](auto role, int buf, int blk) __attribute__((always_inline)) {
         const int lane = at_fresh(threadIdx.x & 63), h = lane >> 4;
-        const uint32_t lane4 = (lane & 31) * 4;
-        char* const dst = smem + C::BUF + buf * C::BYTES + 16 * lane;
         AwHeader* const hdr = reinterpret_cast<AwHeader*>(smem + C::HDR) + buf * NB + pb;
+        dst = C::BUF + buf * C::BYTES + 16 * lane;
         if constexpr (decltype(role)::value) {
+          dst += ((pb * 2 + sbk) * NS + kp * C::SPP) * 1024;
           uint32_t z[C::KS], big = 0;
 #pragma unroll
           for (int y = 0; y < C::KS; ++y) {
@@ -224,72 +243,77 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
               if ((z[y] & 0x7c00u) != 0x7c00u) top = fmaxf(top, fabsf(half_bits_to_float(static_cast<uint16_t>(z[y]))));
             e = aw_exponent(top);
           }
-          uint32_t scale = at_mul(C::KS == 2 && kp ? z[C::KS - 1] : z[0], at_pow2(e));
-#pragma unroll
-          for (int st = 0; st < C::SPP; ++st) {
-            AtLook<KB> x;
-            at_look_k<C, KB>(kx, st, lane4, x);
-            uint32_t a[4];
-            at_pairs_k<KB>(x, scale, a);
-            *reinterpret_cast<u32x4_t*>(dst + ((pb * 2 + sbk) * NS + kp * C::SPP + st) * 1024) = u32x4_t{a[0], a[1], a[2], a[3]};
-          }
+          mul[0] = at_mul(C::KS == 2 && kp ? z[C::KS - 1] : z[0], at_pow2(e));
           if (lane == 0) hdr->kf[sbk] = at_exp2(static_cast<float>(e));
         } else {
-        uint32_t raw[4], big = 0;  // scales of tokens 2 i and 2 i + 1
+          dst += C::VOFF + (pb * CH + vp * C::EPP) * 1024;
+          uint32_t big = 0;  // mul: scales of tokens 2 i and 2 i + 1
 #pragma unroll
-        for (int i = 0; i < 4; ++i) raw[i] = at_pack(vs[2 * i], vs[2 * i + 1]);
-        if (blk * 32 + 32 > len || bad) {
-          const int j0 = blk * 32 + 4 * h;
+          for (int i = 0; i < 4; ++i) mul[i] = at_pack(vs[2 * i], vs[2 * i + 1]);
+          if (blk * 32 + 32 > len || bad) {
+            const int j0 = blk * 32 + 4 * h;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = j0 + 16 * (i >> 1) + 2 * (i & 1);
-            const bool dead = (bad >> (i >> 1)) & 1u;
-            raw[i] &= (dead || j >= len ? 0u : 0xffffu) | (dead || j + 1 >= len ? 0u : 0xffff0000u);
+            for (int i = 0; i < 4; ++i) {
+              const int j = j0 + 16 * (i >> 1) + 2 * (i & 1);
+              const bool dead = (bad >> (i >> 1)) & 1u;
+              mul[i] &= (dead || j >= len ? 0u : 0xffffu) | (dead || j + 1 >= len ? 0u : 0xffff0000u);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) big = at_max_u16(mul[i], big);
+          big = big > (big << 16) ? big : big << 16;
+          int e = 0;
+          uint32_t vbad = 0;
+          if (__any(big > 0x7000ffffu) || !__any(big > 0x2c00ffffu)) {
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t bits = (mul[i >> 1] >> (16 * (i & 1))) & 0xffffu;
+              const uint64_t who = __ballot((bits & 0x7c00u) == 0x7c00u);
+              if (who != 0) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  if ((who >> (16 * y)) & 0xffffu) vbad |= 1u << (16 * (i >> 2) + 4 * y + (i & 3));
+              }
+              const bool drop = (who >> (16 * h)) & 0xffffu;
+              mul[i >> 1] &= !drop ? 0xffffffffu : (i & 1) ? 0x0000ffffu : 0xffff0000u;
+              top = drop ? top : fmaxf(top, fabsf(half_bits_to_float(static_cast<uint16_t>(bits))));
+            }
+            e = aw_exponent(top);
+          }
+          if (lane == 0) {
+            hdr->vexp = e;
+            hdr->vbad = vbad;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mul[i] = at_mul(mul[i], at_pow2(e));
+          if constexpr (VB < 8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) at_pair<VB>(vx[2 * i] >> vshift, vx[2 * i + 1] >> vshift, ev[i], od[i]);
           }
         }
+      };
+      auto look_up = [&](auto role, int n) __attribute__((always_inline)) {
+        if constexpr (decltype(role)::value) {
+          AtLook<KB> x;
+          at_look_k<C, KB>(kx, n, lane4, x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) big = at_max_u16(raw[i], big);
-        big = big > (big << 16) ? big : big << 16;
-        int e = 0;
-        uint32_t vbad = 0;
-        if (__any(big > 0x7000ffffu) || !__any(big > 0x2c00ffffu)) {
-          float top = 0.f;
+          for (int i = 0; i < AtLook<KB>::N; ++i) tb[i] = x.t[i];
+        } else if constexpr (VB == 8) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t bits = (raw[i >> 1] >> (16 * (i & 1))) & 0xffffu;
-            const uint64_t who = __ballot((bits & 0x7c00u) == 0x7c00u);
+          for (int i = 0; i < 8; ++i) tb[i] = at_lds(at_byte<128>(vx[i], n, lane4));
+        } else {
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              if ((who >> (16 * y)) & 0xffffu) vbad |= 1u << (16 * (i >> 2) + 4 * y + (i & 3));
-            if ((who >> (16 * h)) & 0xffffu) raw[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
-            else top = fmaxf(top, fabsf(half_bits_to_float(static_cast<uint16_t>(bits))));
-          }
-          e = aw_exponent(top);
+          for (int i = 0; i < 4; ++i) tb[i] = at_pair_at<C, VB>((n & 1) ? od[i] : ev[i], n >> 1, lane4);
         }
-        if (lane == 0) {
-          hdr->vexp = e;
-          hdr->vbad = vbad;
-        }
+      };
+      auto finish = [&](auto role, int n) __attribute__((always_inline)) {
+        constexpr bool single = decltype(role)::value ? KB == 8 : VB == 8;  // a word per code, not per pair
+        uint32_t a[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) raw[i] = at_mul(raw[i], at_pow2(e));
-        uint32_t ev[4], od[4];
-        if constexpr (VB < 8) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) at_pair<VB>(vx[2 * i] >> vshift, vx[2 * i + 1] >> vshift, ev[i], od[i]);
-        }
-#pragma unroll
-        for (int n = 0; n < C::EPP; ++n) {
-          uint32_t a[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t x;
-            if constexpr (VB == 8) x = at_pack(at_lds(at_byte<128>(vx[2 * i], n, lane4)), at_lds(at_byte<128>(vx[2 * i + 1], n, lane4)));
-            else x = at_pair_at<C, VB>((n & 1) ? od[i] : ev[i], n >> 1, lane4);
-            a[i] = at_mul(x, raw[i]);
-          }
-          *reinterpret_cast<u32x4_t*>(dst + C::VOFF + (pb * CH + vp * C::EPP + n) * 1024) = u32x4_t{a[0], a[1], a[2], a[3]};
-        }
-        }
+        for (int i = 0; i < 4; ++i)
+          a[i] = at_mul(single ? at_pack(tb[2 * i], tb[2 * i + 1]) : tb[i], decltype(role)::value ? mul[0] : mul[i]);
+        *reinterpret_cast<u32x4_t*>(smem + dst + n * 1024) = u32x4_t{a[0], a[1], a[2], a[3]};
       };
 
       // ---- q: row group wave + 8 r of the tile to this wave, by way of LDS ----
@@ -341,7 +365,7 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
       // scores, weights and sums of block x of the chunk. Pieces are read G at a time, a group ahead of
       // their products.
       constexpr int G = 2, KG = 2 * NS / G, VG = CH / G;
-      auto multiply = [&](int buf, int x, int blk) __attribute__((always_inline)) {
+      auto multiply = [&](int buf, int x, int blk, auto side) __attribute__((always_inline)) {
         const int lane = at_fresh(threadIdx.x & 63), h = lane >> 4;
         const char* const ksrc = smem + C::BUF + buf * C::BYTES + 16 * lane + x * 2 * NS * 1024;
         const char* const vsrc = smem + C::BUF + C::VOFF + buf * C::BYTES + 16 * lane + x * CH * 1024;
@@ -357,7 +381,7 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
         for (int g = 0; g < KG; ++g) {
           if (g + 1 < KG) read(ksrc + (g + 1) * G * 1024, z[(g + 1) & 1]);
           else read(vsrc, z[KG & 1]);
-          __builtin_amdgcn_sched_barrier(0);
+          side(g);
 #pragma unroll
           for (int y = 0; y < G; ++y) {
             const int n = G * g + y, sb = n / NS, st = n % NS;
@@ -448,7 +472,7 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
 #pragma unroll
         for (int g = 0; g < VG; ++g) {
           if (g + 1 < VG) read(vsrc + (g + 1) * G * 1024, z[(KG + g + 1) & 1]);
-          __builtin_amdgcn_sched_barrier(0);
+          side(KG + g);
 #pragma unroll
           for (int y = 0; y < G; ++y) {
             const u32x4_t w = z[(KG + g) & 1][y];
@@ -462,23 +486,45 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
 
       // One loop for the waves of keys and one for those of values: with both roles in one, the loads
       // in flight would be copied, and so waited for, where its paths meet. Each ends its rounds with
-      // the same barriers. (First round: nothing to multiply yet.)
+      // the same barriers. A round decodes a chunk while it multiplies the one before, the steps of
+      // one spread over the products of the other.
       auto rounds = [&](auto role) __attribute__((always_inline)) {
-        int buf = 1;
-        for (int c = k0 - NB; c < k1; c += NB) {
-          auto sums = [&]() __attribute__((always_inline)) {
-            if (live && c >= k0) {
-#pragma unroll 1
-              for (int x = 0; x < NB; ++x)
-                if (x == 0 || c + x < k1) multiply(buf, x, c + x);
-            }
-          };
-          if constexpr (decltype(role)::value) sums();
-          decode(role, buf ^ 1, blk);
+        auto begin = [&](int buf) __attribute__((always_inline)) {
+          take(role);
+          const int now = blk;
           blk = next_of(blk);
           load(role);
           look(next_of(blk));
-          if constexpr (!decltype(role)::value) sums();
+          prepare(role, buf, now);
+        };
+        auto plain = [&]() __attribute__((always_inline)) {
+#pragma unroll
+          for (int n = 0; n < STEPS; ++n) {
+            look_up(role, n);
+            finish(role, n);
+          }
+        };
+        begin(0);
+        plain();
+        __syncthreads();
+        int buf = 0;
+        for (int c = k0; c < k1; c += NB) {
+          begin(buf ^ 1);
+          if (live) {
+            constexpr int SB = STEPS / NB, EVERY = (KG + VG) / (2 * SB);
+#pragma unroll
+            for (int x = 0; x < NB; ++x)
+              if (x == 0 || c + x < k1)  // (without it there is no next chunk either)
+                multiply(buf, x, c + x, [&](int slot) __attribute__((always_inline)) {
+                  if (slot % EVERY == 0) {
+                    const int y = slot / EVERY, n = x * SB + (y >> 1);
+                    if (y & 1) finish(role, n);
+                    else look_up(role, n);
+                  }
+                });
+          } else {
+            plain();
+          }
           __syncthreads();
           buf ^= 1;
         }
