@@ -33,6 +33,28 @@ struct JoinParams {
   float inv_sqrt_d;
 };
 
+// Normalises, rotates back and stores one output row held as in kv_wave_transform; sg: the
+// lane's sign bits.
+template <int D, typename P>
+__device__ __forceinline__ void at_finish(P p, float (&v)[D / 64], float l, int64_t m, int head, uint32_t sg, int lane) {
+  constexpr int EL = D / 64;
+  const float f = p->inv_sqrt_d / l;
+  sg ^= 0u - kv_sign(kv_chunk(lane));
+#pragma unroll
+  for (int e = 0; e < EL; ++e) v[e] = l == 0.f ? 0.f : v[e] * f;
+  const int c = kv_chunk(lane);
+  kv_wave_transform<EL>(v, c);
+  const int odt = p->odt;
+  uint16_t* dst = p->out + (m * p->q_heads + head) * D + c * EL;
+  uint16_t x[EL];
+#pragma unroll
+  for (int e = 0; e < EL; ++e) {
+    const float y = (sg >> e) & 1u ? -v[e] : v[e];
+    x[e] = odt == 1 ? float_to_bf16_rne(y) : float_to_half_rne(y);
+  }
+  __builtin_memcpy(__builtin_assume_aligned(dst, 2 * EL), x, 2 * EL);
+}
+
 // One wave per query row of a unit whose parts lie in several workgroups' slots, added in the
 // order of the tokens.
 template <int D>
@@ -54,9 +76,10 @@ __global__ __launch_bounds__(256) void k_attend_join(JoinParams p) {
   float v[EL] = {};
   if (n <= 4) {
     // everything at once (past the last part: that one again, times zero)
-    float x[4][EL], a[4], b[4];
+    constexpr int K = 4;
+    float x[K][EL], a[K], b[K];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < K; ++k) {
       const float* s = part(k < n ? k : n - 1);
       a[k] = s[p.rows * D + r];
       b[k] = s[p.rows * D + p.rows + r];
@@ -64,9 +87,9 @@ __global__ __launch_bounds__(256) void k_attend_join(JoinParams p) {
       for (int e = 0; e < EL; ++e) x[k][e] = s[r * D + d0 + e];
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) top = fmaxf(top, a[k]);
+    for (int k = 0; k < K; ++k) top = fmaxf(top, a[k]);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < K; ++k) {
       const float f = k >= n || a[k] == kAtNone ? 0.f : at_exp2(a[k] - top);
       l += k >= n ? 0.f : b[k] != b[k] ? b[k] : b[k] * f;
 #pragma unroll

@@ -168,28 +168,6 @@ __device__ __forceinline__ int at_ceil_div(int x, int d) {
   return y + 1;
 }
 
-// Normalises, rotates back and stores one output row held as in kv_wave_transform; sg: the lane's
-// sign bits.
-template <int D, typename P>
-__device__ __forceinline__ void at_finish(P p, float (&v)[D / 64], float l, int64_t m, int head, uint32_t sg, int lane) {
-  constexpr int EL = D / 64;
-  const float f = p->inv_sqrt_d / l;
-  sg ^= 0u - kv_sign(kv_chunk(lane));
-#pragma unroll
-  for (int e = 0; e < EL; ++e) v[e] = l == 0.f ? 0.f : v[e] * f;
-  const int c = kv_chunk(lane);
-  kv_wave_transform<EL>(v, c);
-  const int odt = p->odt;
-  uint16_t* dst = p->out + (m * p->q_heads + head) * D + c * EL;
-  uint16_t x[EL];
-#pragma unroll
-  for (int e = 0; e < EL; ++e) {
-    const float y = (sg >> e) & 1u ? -v[e] : v[e];
-    x[e] = odt == 1 ? float_to_bf16_rne(y) : float_to_half_rne(y);
-  }
-  __builtin_memcpy(__builtin_assume_aligned(dst, 2 * EL), x, 2 * EL);
-}
-
 // ---- work ---------------------------------------------------------------------------------
 // One sequence as the schedule sees it. Tile t of a head costs the tokens its last row sees and
 // kAtUnit; block k of it lies kAtUnit + 32 k from the unit's begin on the line.
@@ -457,20 +435,45 @@ __device__ __forceinline__ void at_tables(AtArgs p, char* smem, int tid, int lan
 
 }
 
-// RW rows of a tile's queries at a time, by a wave: rotated, scaled by a power of two to fp16's
-// upper range, into LDS as rows of QP bytes, with each row's score factor and the token its mask
-// ends at (a tree's: begins at).
-template <int D, int RW>
-struct AtQuery {
-  static constexpr int EL = D / 64;
-  int lane, ch, d0, tok0, ntok, nh, hb, row0, head0;
+// Rows of a tile as a wave takes them in and out: N at a time, each on D / 8 lanes, eight elements
+// of a lane (kv_lane.hpp). A row on the whole wave costs four times the instructions: what is done
+// once per row is then done by every lane for one row only.
+template <int D>
+struct AtRows {
+  static constexpr int LR = D / 8, N = 64 / LR;
+  int sub, c;  // the lane's row of the N, its chunk
+  __device__ __forceinline__ AtRows() {
+    const int lane = at_fresh(threadIdx.x & 63);
+    sub = lane / LR;
+    c = kv_chunk(lane & (LR - 1));
+  }
+  __device__ __forceinline__ uint32_t signs(const uint32_t* bits) const { return (bits[c >> 2] >> (8 * (c & 3))) & 0xffu; }
+  __device__ __forceinline__ static float most(float x) {  // the maximum over the row's lanes
+    x = fmaxf(x, kv_swap<0>(x));
+    x = fmaxf(x, kv_swap<1>(x));
+    x = fmaxf(x, kv_swap<2>(x));
+    if constexpr (LR >= 16) x = fmaxf(x, kv_swap<3>(x));
+    if constexpr (LR >= 32) {
+      float a, b;
+      kv_both<4>(x, a, b);
+      x = fmaxf(a, b);
+    }
+    return x;
+  }
+};
+
+// A tile's queries: rotated, scaled by a power of two to fp16's upper range, into LDS as rows of QP
+// bytes, with each row's score factor and the token its mask ends at (a tree's: begins at).
+template <int D>
+struct AtQuery : AtRows<D> {
+  int tok0, ntok, nh, hb, row0, head0;
   uint32_t hb_mul;
   uint32_t sg;
   float c1;
-  uint16_t raw[RW][EL];
+  u32x4_t raw;
   __device__ __forceinline__ AtQuery(AtArgs p, int row0_, int head0_, int tok0_, int ntok_, int nh_)
-      : lane(at_fresh(threadIdx.x & 63)), ch(kv_chunk(lane)), d0(ch * EL), tok0(tok0_), ntok(ntok_), nh(nh_),
-        hb(p->hb), row0(row0_), head0(head0_), hb_mul(p->hb_mul), sg(p->ksigns[d0 >> 5] >> (d0 & 31)), c1(p->c1) {}
+      : tok0(tok0_), ntok(ntok_), nh(nh_), hb(p->hb), row0(row0_), head0(head0_), hb_mul(p->hb_mul),
+        sg(this->signs(p->ksigns)), c1(p->c1) {}
   // whether row r of the tile is a query's
   __device__ __forceinline__ bool row(int r, int& tk, int& hd) const {
     tk = (static_cast<uint32_t>(r) * hb_mul) >> 16;
@@ -478,53 +481,82 @@ struct AtQuery {
     return tk < ntok && hd < nh;
   }
   __device__ __forceinline__ void load(AtArgs p, int r0) {
-#pragma unroll
-    for (int x = 0; x < RW; ++x) {
-      int tk, hd;
-      const bool ok = row(r0 + x, tk, hd);
-      const uint16_t* src = p->q + (static_cast<int64_t>(row0) + (ok ? tk : 0)) * p->q_stride +
-                            static_cast<int64_t>(head0 + (ok ? hd : 0)) * D + d0;
-      __builtin_memcpy(raw[x], __builtin_assume_aligned(src, 2 * EL), 2 * EL);
-    }
+    int tk, hd;
+    const bool ok = row(r0 + this->sub, tk, hd);
+    raw = *reinterpret_cast<const u32x4_t*>(p->q + (static_cast<int64_t>(row0) + (ok ? tk : 0)) * p->q_stride +
+                                            static_cast<int64_t>(head0 + (ok ? hd : 0)) * D + 8 * this->c);
   }
-  __device__ __forceinline__ void rotate(AtArgs p, char* smem, int r0, int dst, int QP, int C1, int LIM, int before, int len) {
-    const int qdt = p->qdt;
-    const bool neg = (kv_sign(ch) != 0) != (p->negate != 0);  // the transform's sign, and the scale's
-    const bool masked = p->tree != nullptr;
-    float v[RW][EL];
+  // the rows loaded last, rows r0 on; those from `next` on are loaded meanwhile (next < 0: none)
+  __device__ __forceinline__ void rotate(AtArgs p, char* smem, int r0, int dst, int QP, int C1, int LIM, int before, int len, int next) {
+    const int c = this->c, r = r0 + this->sub, qdt = p->qdt;
+    int tk, hd;
+    const bool ok = row(r, tk, hd), use = ok && c1 != 0.f;
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    float v[8], mx = 0.f;
 #pragma unroll
-    for (int x = 0; x < RW; ++x) {
-      int tk, hd;
-      const bool ok = row(r0 + x, tk, hd), use = ok && c1 != 0.f;
-      float mx = 0.f;
+    for (int e = 0; e < 8; ++e) {
+      const uint16_t x = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+      const float y = qdt == 1 ? bf16_bits_to_float(x) : half_bits_to_float(x);
+      v[e] = !use ? 0.f : (sg >> e) & 1u ? -y : y;
+    }
+    if (next >= 0) load(p, next);
+    kv_transform<D>(v, c);
 #pragma unroll
-      for (int e = 0; e < EL; ++e) {
-        const float y = qdt == 1 ? bf16_bits_to_float(raw[x][e]) : half_bits_to_float(raw[x][e]);
-        v[x][e] = !use ? 0.f : (sg >> e) & 1u ? -y : y;
-      }
-      kv_wave_transform<EL>(v[x], ch);
+    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[e]));
+    mx = this->most(mx);
+    // the largest magnitude comes to [2^13, 2^14): exponent 127 + 13 of the scaled value
+    const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
+    int k = mx > 0.f && ex < 255 ? 140 - ex : 0;
+    k = k > 100 ? 100 : k;
+    const bool neg = (kv_sign(c) != 0) != (p->negate != 0);  // the transform's sign, and the scale's
+    const float f = __uint_as_float(static_cast<uint32_t>(127 + k) << 23 | (neg ? 0x80000000u : 0u));
+    uint32_t y[4];
 #pragma unroll
-      for (int e = 0; e < EL; ++e) mx = fmaxf(mx, fabsf(v[x][e]));
-      mx = kv_wave_max(mx);
-      // the largest magnitude comes to [2^13, 2^14): exponent 127 + 13 of the scaled value
-      const int ex = static_cast<int>(__float_as_uint(mx) >> 23);
-      int k = mx > 0.f && ex < 255 ? 140 - ex : 0;
-      k = k > 100 ? 100 : k;
-      const float f = __uint_as_float(static_cast<uint32_t>(127 + k) << 23 | (neg ? 0x80000000u : 0u));
-      _Float16 y[EL];
-#pragma unroll
-      for (int e = 0; e < EL; ++e) y[e] = static_cast<_Float16>(v[x][e] * f);
-      __builtin_memcpy(__builtin_assume_aligned(smem + dst + x * QP + 2 * d0, 2 * EL), y, 2 * EL);
-      if (lane == 0) {
-        *reinterpret_cast<float*>(smem + C1 + 4 * (r0 + x)) =
-            c1 == 0.f ? 1.f : c1 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-        int lim = masked ? before : before + tok0 + tk + 1;
-        lim = lim < 0 ? 0 : lim;
-        *reinterpret_cast<int*>(smem + LIM + 4 * (r0 + x)) = !ok || lim > len ? len : lim;
-      }
+    for (int e = 0; e < 4; ++e) {
+      const half2_t x{static_cast<_Float16>(v[2 * e] * f), static_cast<_Float16>(v[2 * e + 1] * f)};
+      y[e] = __builtin_bit_cast(uint32_t, x);
+    }
+    *reinterpret_cast<u32x4_t*>(smem + dst + this->sub * QP + 16 * c) = u32x4_t{y[0], y[1], y[2], y[3]};
+    if (c == 0) {
+      *reinterpret_cast<float*>(smem + C1 + 4 * r) = c1 == 0.f ? 1.f : c1 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+      int lim = p->tree ? before : before + tok0 + tk + 1;
+      lim = lim < 0 ? 0 : lim;
+      *reinterpret_cast<int*>(smem + LIM + 4 * r) = !ok || lim > len ? len : lim;
     }
   }
 };
+
+// The lane's part v of a row's sums, l the sum of its weights: normalised, rotated back and (if ok)
+// stored.
+template <int D>
+__device__ __forceinline__ void at_store(AtArgs p, float (&v)[8], float l, int64_t m, int head, uint32_t sg, int c, bool ok) {
+  const float f = p->inv_sqrt_d / l;
+  sg ^= 0u - kv_sign(c);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = l == 0.f ? 0.f : v[e] * f;
+  kv_transform<D>(v, c);
+  const int odt = p->odt;
+  uint32_t x[4];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float y = (sg >> e) & 1u ? -v[e] : v[e];
+    const uint32_t b = odt == 1 ? float_to_bf16_rne(y) : float_to_half_rne(y);
+    x[e >> 1] = e & 1 ? x[e >> 1] | b << 16 : b;
+  }
+  if (ok) *reinterpret_cast<u32x4_t*>(p->out + (m * p->q_heads + head) * D + 8 * c) = u32x4_t{x[0], x[1], x[2], x[3]};
+}
+
+// The lane's part of a row's sums into a slot of the workspace: [rows][D] sums, references, weights.
+template <int D>
+__device__ __forceinline__ void at_put(float* slot, int rows, int r, int c, const float (&v)[8], float top, float l) {
+  f32x4_t* const dst = reinterpret_cast<f32x4_t*>(slot + r * D + 8 * c);
+  dst[0] = f32x4_t{v[0], v[1], v[2], v[3]};
+  dst[1] = f32x4_t{v[4], v[5], v[6], v[7]};
+  if (c == 0) {
+    slot[rows * D + r] = top;
+    slot[rows * D + rows + r] = l;
+  }
+}
 
 // ---- decoding -----------------------------------------------------------------------------
 // the larger of each half, as unsigned numbers (scales are not negative)
@@ -615,7 +647,7 @@ struct AtBlock {
 template <int KB, int VB, int D, int R>
 __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS * AtCfg<KB, VB, D, R>::W / 4)) void k_attend(AttendParams) {
   using C = AtCfg<KB, VB, D, R>;
-  constexpr int W = C::W, T = C::T, ROWS = C::ROWS, NS = C::NS, CH = C::CH, EL = D / 64;
+  constexpr int W = C::W, T = C::T, ROWS = C::ROWS, NS = C::NS, CH = C::CH;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   AtArgs p = (AtArgs)__builtin_amdgcn_kernarg_segment_ptr();
   const int tid = threadIdx.x, lane = tid & 63, wave = at_uniform(tid >> 6);
@@ -786,9 +818,9 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
         }
       };
       // ---- q: rotated, scaled by a power of two to fp16's upper range, into LDS ----
-      constexpr int RW = ROWS / W < 4 ? ROWS / W : 4;  // rows of a wave at a time
-      AtQuery<D, RW> qs(p, sq.row0 + tok0, head0, tok0, ntok, nh);
-      qs.load(p, wave * (ROWS / W));
+      AtQuery<D> qs(p, sq.row0 + tok0, head0, tok0, ntok, nh);
+      constexpr int RN = AtRows<D>::N;  // rows of a wave at a time
+      if (wave * RN < ROWS) qs.load(p, wave * RN);
       AtBlock<C> blk0 = {};
       int blk = k0 + wave;
       if (blk < k1) {
@@ -802,10 +834,8 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
       const bool masked = p->tree != nullptr;
       __syncthreads();  // the last unit's readers of this memory are done
 #pragma unroll 1
-      for (int r0 = wave * (ROWS / W); r0 < (wave + 1) * (ROWS / W); r0 += RW) {
-        if (r0 != wave * (ROWS / W)) qs.load(p, r0);
-        qs.rotate(p, smem, r0, C::QS + r0 * C::QP, C::QP, C::C1, C::LIM, before, len);
-      }
+      for (int r0 = wave * RN; r0 < ROWS; r0 += W * RN)
+        qs.rotate(p, smem, r0, C::QS + r0 * C::QP, C::QP, C::C1, C::LIM, before, len, r0 + W * RN < ROWS ? r0 + W * RN : -1);
       __syncthreads();
       // from this token on some row's mask may cut
       int cut = masked ? before : before + tok0 + 1;
@@ -1087,8 +1117,6 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
       p = at_again(p);
       {
       const int tid = at_fresh(threadIdx.x), lane = tid & 63, col = lane & 15, h = lane >> 4;
-      const int d0 = kv_chunk(lane) * EL;
-      const uint32_t vsg = p->vsigns[d0 >> 5] >> (d0 & 31);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float x, y;
@@ -1142,10 +1170,13 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
       __syncthreads();
       const bool whole = k0 == 0 && k1 == nblk;
       float* slot = p->parts + static_cast<int64_t>(2 * wg + (k0 > 0 ? 0 : 1)) * ROWS * (D + 2);
+      const AtRows<D> rows;
+      const uint32_t vsg = rows.signs(p->vsigns);
 #pragma unroll 1
-      for (int r = wave; r < ROWS; r += W) {
+      for (int r0 = wave * RN; r0 < ROWS; r0 += W * RN) {
+        const int r = r0 + rows.sub;
         const int tk = (static_cast<uint32_t>(r) * p->hb_mul) >> 16, hd = r - tk * hb;
-        if (tk >= ntok || hd >= nh) continue;
+        const bool ok = tk < ntok && hd < nh;
         float2 ml[W];
         float top = kAtNone, ls = 0.f;
 #pragma unroll
@@ -1156,18 +1187,13 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
 #pragma unroll
         for (int x = 0; x < W; ++x)  // a wave that saw nothing adds nothing, unless its sum is no number
           ls += ml[x].x == kAtNone ? (ml[x].y != ml[x].y ? ml[x].y : 0.f) : ml[x].y * at_exp2(ml[x].x - top);
-        float v[EL];
+        float v[8];
 #pragma unroll
-        for (int e = 0; e < EL; ++e) v[e] = red[r * C::FP + d0 + e];
+        for (int e = 0; e < 8; ++e) v[e] = red[r * C::FP + 8 * rows.c + e];
         if (whole) {
-          at_finish<D>(p, v, ls, static_cast<int64_t>(sq.row0) + tok0 + tk, head0 + hd, vsg, lane);
-        } else {
-#pragma unroll
-          for (int e = 0; e < EL; ++e) slot[r * D + d0 + e] = v[e];
-          if (lane == 0) {
-            slot[ROWS * D + r] = top;
-            slot[ROWS * D + ROWS + r] = ls;
-          }
+          at_store<D>(p, v, ls, static_cast<int64_t>(sq.row0) + tok0 + tk, head0 + hd, vsg, rows.c, ok);
+        } else if (ok) {
+          at_put<D>(slot, C::ROWS, r, rows.c, v, top, ls);
         }
       }
       if (!whole && k0 == 0 && tid == 0) {

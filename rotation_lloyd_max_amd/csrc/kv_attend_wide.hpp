@@ -74,7 +74,7 @@ __device__ __forceinline__ int aw_exponent(float top) {
 template <int KB, int VB, int D, int R>
 __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(AttendParams) {
   using C = AwCfg<KB, VB, D, R>;
-  constexpr int W = C::W, NS = C::NS, CH = C::CH, NB = C::NB, EL = D / 64;
+  constexpr int W = C::W, NS = C::NS, CH = C::CH, NB = C::NB;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   AtArgs p = (AtArgs)__builtin_amdgcn_kernarg_segment_ptr();
   const int tid = threadIdx.x, lane = tid & 63, wave = at_uniform(tid >> 6);
@@ -317,8 +317,9 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
       };
 
       // ---- q: row group wave + 8 r of the tile to this wave, by way of LDS ----
-      AtQuery<D, 4> qs(p, sq.row0 + tok0, head0, tok0, ntok, nh);
+      AtQuery<D> qs(p, sq.row0 + tok0, head0, tok0, ntok, nh);
       qs.load(p, 16 * wave);
+      constexpr int RN = AtRows<D>::N;  // rows of a wave at a time
       // past its last block a wave repeats it, into buffers that nothing reads
       const auto next_of = [&](int x) { return x + NB < k1 ? x + NB : x; };
       int blk = k0 + pb < k1 ? k0 + pb : k0;
@@ -337,10 +338,9 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
         const int r0 = 16 * (wave + W * r), at = C::BUF + wave * 16 * C::QP;
         wave_lds_sync();
 #pragma unroll 1
-        for (int y = 0; y < 16; y += 4) {
-          if (r + y) qs.load(p, r0 + y);
-          qs.rotate(p, smem, r0 + y, at + y * C::QP, C::QP, C::C1, C::LIM, before, len);
-        }
+        for (int y = 0; y < 16; y += RN)
+          qs.rotate(p, smem, r0 + y, at + y * C::QP, C::QP, C::C1, C::LIM, before, len,
+                    y + RN < 16 ? r0 + y + RN : r + 1 < R ? r0 + 16 * W : -1);
         wave_lds_sync();
 #pragma unroll
         for (int st = 0; st < NS; ++st) {
@@ -362,30 +362,33 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
       const bool live = ((static_cast<uint32_t>(16 * wave) * hb_mul) >> 16) < static_cast<uint32_t>(ntok);
       int vexp = 0;  // the sums are held times 2^-vexp
 
-      // scores, weights and sums of block x of the chunk. Pieces are read G at a time, a group ahead of
-      // their products.
-      constexpr int G = 2, KG = 2 * NS / G, VG = CH / G;
+      // Scores, weights and sums of block x of the chunk. Pieces are read G at a time, AHEAD groups before
+      // their products; z holds those on their way.
+      constexpr int G = 2, KG = 2 * NS / G, VG = CH / G, BG = KG + VG, AHEAD = 1;
+      u32x4_t z[AHEAD + 1][G];
+      auto read = [&](const char* src, int g) __attribute__((always_inline)) {  // group g of the chunk's NB * BG
+        if (g >= NB * BG) return;
+        const int x = g / BG, k = g % BG, at = (k < KG ? x * KG + k : NB * KG + x * VG + k - KG) * G;
+#pragma unroll
+        for (int y = 0; y < G; ++y) z[g % (AHEAD + 1)][y] = *reinterpret_cast<const u32x4_t*>(src + (at + y) * 1024);
+      };
       auto multiply = [&](int buf, int x, int blk, auto side) __attribute__((always_inline)) {
         const int lane = at_fresh(threadIdx.x & 63), h = lane >> 4;
-        const char* const ksrc = smem + C::BUF + buf * C::BYTES + 16 * lane + x * 2 * NS * 1024;
-        const char* const vsrc = smem + C::BUF + C::VOFF + buf * C::BYTES + 16 * lane + x * CH * 1024;
+        const char* const src = smem + C::BUF + buf * C::BYTES + 16 * lane;
         const AwHeader* const hdr = reinterpret_cast<const AwHeader*>(smem + C::HDR) + buf * NB + x;
-        u32x4_t z[2][G];
-        auto read = [&](const char* src, u32x4_t (&o)[G]) __attribute__((always_inline)) {
-#pragma unroll
-          for (int y = 0; y < G; ++y) o[y] = *reinterpret_cast<const u32x4_t*>(src + y * 1024);
-        };
         f32x4_t s[R][2];
-        read(ksrc, z[0]);
+        if (x == 0) {
+#pragma unroll
+          for (int g = 0; g < AHEAD; ++g) read(src, g);
+        }
 #pragma unroll
         for (int g = 0; g < KG; ++g) {
-          if (g + 1 < KG) read(ksrc + (g + 1) * G * 1024, z[(g + 1) & 1]);
-          else read(vsrc, z[KG & 1]);
+          read(src, x * BG + g + AHEAD);
           side(g);
 #pragma unroll
           for (int y = 0; y < G; ++y) {
             const int n = G * g + y, sb = n / NS, st = n % NS;
-            const u32x4_t w = z[g & 1][y];
+            const u32x4_t w = z[(x * BG + g) % (AHEAD + 1)][y];
             const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int r = 0; r < R; ++r) s[r][sb] = at_mfma(a, q[r][st], st == 0 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : s[r][sb]);
@@ -471,11 +474,11 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
         }
 #pragma unroll
         for (int g = 0; g < VG; ++g) {
-          if (g + 1 < VG) read(vsrc + (g + 1) * G * 1024, z[(KG + g + 1) & 1]);
+          read(src, x * BG + KG + g + AHEAD);
           side(KG + g);
 #pragma unroll
           for (int y = 0; y < G; ++y) {
-            const u32x4_t w = z[(KG + g) & 1][y];
+            const u32x4_t w = z[(x * BG + KG + g) % (AHEAD + 1)][y];
             const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int r = 0; r < R; ++r) o[r][G * g + y] = at_mfma(a, pr[r], o[r][G * g + y]);
@@ -511,7 +514,7 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
         for (int c = k0; c < k1; c += NB) {
           begin(buf ^ 1);
           if (live) {
-            constexpr int SB = STEPS / NB, EVERY = (KG + VG) / (2 * SB);
+            constexpr int SB = STEPS / NB, EVERY = BG / (2 * SB);
 #pragma unroll
             for (int x = 0; x < NB; ++x)
               if (x == 0 || c + x < k1)  // (without it there is no next chunk either)
@@ -535,8 +538,8 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
       // ---- out: a wave's rows, transposed by way of LDS ----
       p = at_again(p);
       const int lane = at_fresh(threadIdx.x & 63), col = lane & 15, h = lane >> 4;
-      const int d0 = kv_chunk(lane) * EL;
-      const uint32_t vsg = p->vsigns[d0 >> 5] >> (d0 & 31);
+      const AtRows<D> rows;
+      const uint32_t vsg = rows.signs(p->vsigns);
       const bool whole = k0 == 0 && k1 == nblk;
       float* const slot = p->parts + static_cast<int64_t>(2 * wg + (k0 > 0 ? 0 : 1)) * C::ROWS * (D + 2);
       float* const red = reinterpret_cast<float*>(smem + C::BUF) + wave * C::FR * C::FP;
@@ -557,25 +560,16 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
               for (int i = 0; i < 4; ++i) red[(col - r1) * C::FP + CH * (4 * h + i) + n] = o[r][n][i] * fv;
           wave_lds_sync();
 #pragma unroll 1
-          for (int z = r1; z < r1 + C::FR; ++z) {
-            const int row = 16 * (wave + W * r) + z;
+          for (int z0 = r1; z0 < r1 + C::FR; z0 += RN) {
+            const int z = z0 + rows.sub, row = 16 * (wave + W * r) + z;
             const int tk = (static_cast<uint32_t>(row) * hb_mul) >> 16, hd = row - tk * hb;
-            if (tk >= ntok || hd >= nh) continue;
-            const float ls = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(l[r]), z));
-            const float top = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mo[r]), z));
-            float v[EL];
+            const bool ok = tk < ntok && hd < nh;
+            const float ls = __shfl(l[r], z), top = __shfl(mo[r], z);
+            float v[8];
 #pragma unroll
-            for (int e = 0; e < EL; ++e) v[e] = red[(z - r1) * C::FP + d0 + e];
-            if (whole) {
-              at_finish<D>(p, v, ls, static_cast<int64_t>(sq.row0) + tok0 + tk, head0 + hd, vsg, lane);
-            } else {
-#pragma unroll
-              for (int e = 0; e < EL; ++e) slot[row * D + d0 + e] = v[e];
-              if (lane == 0) {
-                slot[C::ROWS * D + row] = top;
-                slot[C::ROWS * D + C::ROWS + row] = ls;
-              }
-            }
+            for (int e = 0; e < 8; ++e) v[e] = red[(z - r1) * C::FP + 8 * rows.c + e];
+            if (whole) at_store<D>(p, v, ls, static_cast<int64_t>(sq.row0) + tok0 + tk, head0 + hd, vsg, rows.c, ok);
+            else if (ok) at_put<D>(slot, C::ROWS, row, rows.c, v, top, ls);
           }
         }
       }
