@@ -3,7 +3,7 @@
 //     out = R_v^T sum_j p_j v'_j,  p = softmax_j(scale * (R_k q) . k'_j)
 // with k', v' the decoded rows in the rotated bases (R orthonormal: q . k = (R q) . (R k)).
 //
-// Work. A unit is (sequence, key head, tile of up to 16 R query rows that share the head). All
+// Work. A unit is (sequence, key head, tile of up to 16 query rows that share the head). All
 // units lie on one line of work, each as long as the tokens it reads plus a constant for its
 // set-up, cut into shares, one per workgroup: uneven lengths balance, and a few long sequences
 // still fill the chip. With few units each is cut evenly into its own workgroups (AtPlan). A cut
@@ -78,11 +78,11 @@ __device__ __forceinline__ AtArgs at_again(AtArgs p) {
   return p;
 }
 
-template <int KB, int VB, int D, int R>
+template <int KB, int VB, int D>
 struct AtCfg {
   static constexpr int W = 4;               // waves
   static constexpr int T = 64 * W;
-  static constexpr int ROWS = 16 * R;
+  static constexpr int ROWS = 16;
   static constexpr int NS = D / 32;         // 32-element steps of a key row
   static constexpr int CH = D / 16;         // codes of a lane's piece of a value row
   static constexpr bool KWIDE = KB == 8 || (KB == 4 && VB != 8);
@@ -91,7 +91,7 @@ struct AtCfg {
   static constexpr int KW = (KROW / 4 + 3) / 4;               // words of a quarter key row
   static constexpr int KS = D == 256 ? 2 : 1;                 // key scales of a quarter row, at most
   static constexpr int VW = (VB * CH + 31) / 32;              // words of a value piece
-  static constexpr int WGS = R == 1 && D <= 128 ? 3 : R > 1 && D == 256 ? 1 : 2;  // workgroups per CU
+  static constexpr int WGS = D <= 128 ? 3 : 2;  // workgroups per CU
   static constexpr int GRID = WGS * kAtCus;
   // LDS; the joined sums take the place of q
   static constexpr int WIDE = (KWIDE || VWIDE) ? 32768 : 0;
@@ -546,6 +546,23 @@ __device__ __forceinline__ void at_store(AtArgs p, float (&v)[8], float l, int64
   if (ok) *reinterpret_cast<u32x4_t*>(p->out + (m * p->q_heads + head) * D + 8 * c) = u32x4_t{x[0], x[1], x[2], x[3]};
 }
 
+// The lowest n bits; none for n <= 0, all from 32 on.
+__device__ __forceinline__ uint32_t at_low(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+// The tokens j0 .. j0 + 31 that row `row` of the tile sees, as bits: those before lim and, of a tree,
+// those of its mask's words. row0: first query row of the tile, ntok its tokens.
+__device__ __forceinline__ uint32_t at_seen(AtArgs p, int lim, int j0, int before, int len, int row0, int row, int ntok) {
+  uint32_t see = at_low(lim - j0);
+  if (p->tree) {
+    const int tk = (static_cast<uint32_t>(row) * p->hb_mul) >> 16, words = p->tree_words;
+    const uint32_t* bits = p->tree + static_cast<int64_t>(row0 + (tk < ntok ? tk : 0)) * words;
+    const int w = (j0 - before) >> 5, sh = (j0 - before) & 31;
+    const uint32_t w0 = w >= 0 && w < words ? bits[w] : 0u, w1 = w >= -1 && w + 1 < words ? bits[w + 1] : 0u;
+    see |= static_cast<uint32_t>((static_cast<uint64_t>(w1) << 32 | w0) >> sh) & at_low(len - j0);
+  }
+  return see;
+}
+
 // The lane's part of a row's sums into a slot of the workspace: [rows][D] sums, references, weights.
 template <int D>
 __device__ __forceinline__ void at_put(float* slot, int rows, int r, int c, const float (&v)[8], float top, float l) {
@@ -644,9 +661,9 @@ struct AtBlock {
   uint32_t bad;  // uniform; bit x: the page of half x is none
 };
 
-template <int KB, int VB, int D, int R>
-__global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS * AtCfg<KB, VB, D, R>::W / 4)) void k_attend(AttendParams) {
-  using C = AtCfg<KB, VB, D, R>;
+template <int KB, int VB, int D>
+__global__ __launch_bounds__((AtCfg<KB, VB, D>::T), (AtCfg<KB, VB, D>::WGS * AtCfg<KB, VB, D>::W / 4)) void k_attend(AttendParams) {
+  using C = AtCfg<KB, VB, D>;
   constexpr int W = C::W, T = C::T, ROWS = C::ROWS, NS = C::NS, CH = C::CH;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   AtArgs p = (AtArgs)__builtin_amdgcn_kernarg_segment_ptr();
@@ -840,23 +857,17 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
       // from this token on some row's mask may cut
       int cut = masked ? before : before + tok0 + 1;
       cut = cut < 0 ? 0 : cut;
-      const uint32_t* const tree = p->tree;
 
-      float c1[R], mo[R], l[R];  // score factor; reference - 7; sum
-      f32x4_t o[R][CH];
+      float c1 = *reinterpret_cast<const float*>(smem + C::C1 + 4 * col);  // score factor, times 2^kexp
+      float mo = kAtNone, l = 0.f;                                         // reference - 7; sum
+      f32x4_t o[CH];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        c1[r] = *reinterpret_cast<const float*>(smem + C::C1 + 4 * (16 * r + col));  // times 2^kexp
-        mo[r] = kAtNone;
-        l[r] = 0.f;
-#pragma unroll
-        for (int n = 0; n < CH; ++n) o[r][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      }
+      for (int n = 0; n < CH; ++n) o[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       // Scales are held times 2^-kexp and 2^-vexp. They start at 1, are set by the first block if
       // its scales are small (below 2^-4), and grow when one passes 2^13.
       int kexp = 0, vexp = 0;
 
-      auto scores = [&](const AtBlock<C>& x, bool first, f32x4_t (&s)[R][2]) {
+      auto scores = [&](const AtBlock<C>& x, bool first, f32x4_t (&s)[2]) {
         uint32_t kd[2][C::KS];  // scales times 2^-kexp, in both halves
         auto key_scales = [&]() {
           uint32_t big = 0;
@@ -885,13 +896,11 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
           if (ne > kexp || first) {
             const float f = at_exp2(static_cast<float>(ne - kexp));
             kexp = ne;
-#pragma unroll
-            for (int r = 0; r < R; ++r) c1[r] *= f;
+            c1 *= f;
           }
           key_scales();
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r) s[r][0] = s[r][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        s[0] = s[1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         // the next step's table reads are on their way while this one's results are multiplied
         constexpr int PF = 1;
         AtLook<KB> ring[PF + 1];
@@ -901,89 +910,58 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
         for (int y = 0; y < 2 * NS; ++y) {
           const int sb = y / NS, st = y % NS;
           if (y + PF < 2 * NS) at_look_k<C, KB>(x.k[(y + PF) / NS], (y + PF) % NS, lane4, ring[(y + PF) % (PF + 1)]);
-          u32x4_t qv[R];
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-            qv[r] = *reinterpret_cast<const u32x4_t*>(smem + C::QS + (16 * r + col) * C::QP + (D / 2) * h + 16 * st);
+          const u32x4_t qv = *reinterpret_cast<const u32x4_t*>(smem + C::QS + col * C::QP + (D / 2) * h + 16 * st);
           __builtin_amdgcn_sched_barrier(0);
           uint32_t a[4];
           at_pairs_k<KB>(ring[y % (PF + 1)], kd[sb][C::KS == 2 ? st / (NS / 2) : 0], a);
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const uint32_t qb[4] = {qv[r].x, qv[r].y, qv[r].z, qv[r].w};
-            s[r][sb] = at_mfma(a, qb, s[r][sb]);
-          }
+          const uint32_t qb[4] = {qv.x, qv.y, qv.z, qv.w};
+          s[sb] = at_mfma(a, qb, s[sb]);
           __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb)
           if ((x.bad >> sb) & 1u) {
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) s[r][sb][i] = __builtin_nanf("");
+            for (int i = 0; i < 4; ++i) s[sb][i] = __builtin_nanf("");
           }
       };
-      auto softmax = [&](int blk, f32x4_t (&s)[R][2], uint32_t (&pb)[R][4]) {
+      auto softmax = [&](int blk, f32x4_t (&s)[2], uint32_t (&pb)[4]) {
         // masks
         if (blk * 32 + 32 > cut) {
-          const int lane = at_fresh(threadIdx.x & 63), col = lane & 15, j0 = blk * 32 + 4 * (lane >> 4);
+          const int lane = at_fresh(threadIdx.x & 63), col = lane & 15;
+          const uint32_t see = at_seen(p, *reinterpret_cast<const int*>(smem + C::LIM + 4 * col), blk * 32, before, len,
+                                       sq.row0 + tok0, col, ntok) >> (4 * (lane >> 4));
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const int row = 16 * r + col, lim = *reinterpret_cast<const int*>(smem + C::LIM + 4 * row);
-            const int tk = (static_cast<uint32_t>(row) * p->hb_mul) >> 16;
-            const uint32_t* bits = tree + static_cast<int64_t>(sq.row0 + tok0 + (tk < ntok ? tk : 0)) * p->tree_words;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int j = j0 + 16 * (i >> 2) + (i & 3);
-              bool see = j < lim;
-              if (tree && !see && j < len) {
-                const int x = j - before;
-                if (x >= 0 && x < p->tree_words * 32) see = (bits[x >> 5] >> (x & 31)) & 1u;
-              }
-              s[r][i >> 2][i & 3] = see ? s[r][i >> 2][i & 3] : -__builtin_inff();
-            }
-          }
+          for (int i = 0; i < 8; ++i)
+            s[i >> 2][i & 3] = (see >> (16 * (i >> 2) + (i & 3))) & 1u ? s[i >> 2][i & 3] : -__builtin_inff();
         }
         // against a lazily moved reference
-        float mx[R];
-        bool move = false;
+        const float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                               fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3]))) * c1;
+        if (__any(mx > mo + (7.f + kAtLazy))) {
+          float x, y;
+          kv_both<4>(mx, x, y);
+          kv_both<5>(fmaxf(x, y), x, y);
+          x = fmaxf(x, y);
+          if (x > mo + (7.f + kAtLazy)) {  // the same in the four lanes of a row
+            const float f = at_exp2(mo + 7.f - x);
+            mo = x - 7.f;
+            l *= f;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          mx[r] = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
-                        fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3]))) * c1[r];
-          move = move || mx[r] > mo[r] + (7.f + kAtLazy);
-        }
-        if (__any(move)) {
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            float x, y;
-            kv_both<4>(mx[r], x, y);
-            kv_both<5>(fmaxf(x, y), x, y);
-            x = fmaxf(x, y);
-            if (x > mo[r] + (7.f + kAtLazy)) {  // the same in the four lanes of a row
-              const float f = at_exp2(mo[r] + 7.f - x);
-              mo[r] = x - 7.f;
-              l[r] *= f;
-#pragma unroll
-              for (int n = 0; n < CH; ++n) o[r][n] *= f;
-            }
+            for (int n = 0; n < CH; ++n) o[n] *= f;
           }
         }
+        float e[8];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          float e[8];
+        for (int i = 0; i < 8; ++i) e[i] = at_exp2(__builtin_fmaf(s[i >> 2][i & 3], c1, -mo));
+        l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) e[i] = at_exp2(__builtin_fmaf(s[r][i >> 2][i & 3], c1[r], -mo[r]));
-          l[r] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const half2_t x{static_cast<_Float16>(e[2 * i]), static_cast<_Float16>(e[2 * i + 1])};
-            pb[r][i] = __builtin_bit_cast(uint32_t, x);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const half2_t x{static_cast<_Float16>(e[2 * i]), static_cast<_Float16>(e[2 * i + 1])};
+          pb[i] = __builtin_bit_cast(uint32_t, x);
         }
       };
-      auto values = [&](AtBlock<C>& x, int blk, bool first, const f32x4_t (&s)[R][2], const uint32_t (&pb)[R][4]) {
+      auto values = [&](AtBlock<C>& x, int blk, bool first, const f32x4_t (&s)[2], const uint32_t (&pb)[4]) {
         // scales: dead tokens and bad pages to zero, held times 2^-vexp
         uint32_t raw[4];
         pair_scales(x, raw);
@@ -1013,9 +991,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
             if ((who >> (16 * h)) & 0xffffu) {
               // this token's value is no number: rows that see it become NaN, others stay
               raw[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
-#pragma unroll
-              for (int r = 0; r < R; ++r)
-                if (s[r][i >> 2][i & 3] != -__builtin_inff()) l[r] = __builtin_nanf("");
+              if (s[i >> 2][i & 3] != -__builtin_inff()) l = __builtin_nanf("");
             } else {
               top = fmaxf(top, fabsf(half_bits_to_float(static_cast<uint16_t>(bits))));
             }
@@ -1026,9 +1002,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
             const float f = at_exp2(static_cast<float>(vexp - ne));
             vexp = ne;
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-              for (int n = 0; n < CH; ++n) o[r][n] *= f;
+            for (int n = 0; n < CH; ++n) o[n] *= f;
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) vs[i] = at_mul(raw[i], at_pow2(vexp));
@@ -1080,8 +1054,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
               const uint32_t* z = tb[(n / STEP) % (PV + 1)][y];
               a[i] = at_mul(VB == 8 ? at_pack(z[(2 * i) % NT], z[(2 * i + 1) % NT]) : z[i], vs[i]);
             }
-#pragma unroll
-            for (int r = 0; r < R; ++r) o[r][n + y] = at_mfma(a, pb[r], o[r][n + y]);
+            o[n + y] = at_mfma(a, pb, o[n + y]);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -1094,8 +1067,8 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
         for (; blk < k1; blk += W) {
           const bool more = blk + W < k1;
           AtBlock<C>& x = blk0;
-          f32x4_t s[R][2];
-          uint32_t pb[R][4];
+          f32x4_t s[2];
+          uint32_t pb[4];
           const uint32_t bad = x.bad;
           scores(x, first, s);
           if (more) {
@@ -1117,24 +1090,18 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
       p = at_again(p);
       {
       const int tid = at_fresh(threadIdx.x), lane = tid & 63, col = lane & 15, h = lane >> 4;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float x, y;
-        kv_both<4>(l[r], x, y);
-        kv_both<5>(x + y, x, y);
-        l[r] = x + y;
-        if (h == 0)
-          *reinterpret_cast<float2*>(smem + C::ML + 8 * (wave * ROWS + 16 * r + col)) = make_float2(mo[r], l[r]);
-      }
+      float x, y;
+      kv_both<4>(l, x, y);
+      kv_both<5>(x + y, x, y);
+      l = x + y;
+      if (h == 0)
+        *reinterpret_cast<float2*>(smem + C::ML + 8 * (wave * ROWS + col)) = make_float2(mo, l);
       __syncthreads();
-      float f[R];
+      float f;
+      float top = kAtNone;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float top = kAtNone;
-#pragma unroll
-        for (int x = 0; x < W; ++x) top = fmaxf(top, *reinterpret_cast<const float*>(smem + C::ML + 8 * (x * ROWS + 16 * r + col)));
-        f[r] = mo[r] == kAtNone ? 0.f : at_exp2(mo[r] - top + static_cast<float>(vexp));
-      }
+      for (int x = 0; x < W; ++x) top = fmaxf(top, *reinterpret_cast<const float*>(smem + C::ML + 8 * (x * ROWS + col)));
+      f = mo == kAtNone ? 0.f : at_exp2(mo - top + static_cast<float>(vexp));
       constexpr int OUT = C::NL * 16 * ROWS / T;  // sums of a thread per round
       constexpr int RND = CH / C::NL;
       static_assert(C::NL * 16 * ROWS % T == 0, "whole sums per thread");
@@ -1146,10 +1113,8 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
 #pragma unroll
         for (int nl = 0; nl < C::NL; ++nl)
 #pragma unroll
-          for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              red[((wave * C::NL + nl) * 16 + 4 * h + i) * ROWS + 16 * r + col] = o[r][rd * C::NL + nl][i] * f[r];
+          for (int i = 0; i < 4; ++i)
+            red[((wave * C::NL + nl) * 16 + 4 * h + i) * ROWS + col] = o[rd * C::NL + nl][i] * f;
         __syncthreads();
 #pragma unroll
         for (int x = 0; x < OUT; ++x) {
@@ -1211,13 +1176,13 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D, R>::T), (AtCfg<KB, VB, D, R>::WGS
   }
 }
 
-template <int KB, int VB, int D, int R>
+template <int KB, int VB, int D>
 hipError_t at_launch(const AttendParams& p, hipStream_t s) {
-  using C = AtCfg<KB, VB, D, R>;
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend<KB, VB, D, R>),
+  using C = AtCfg<KB, VB, D>;
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend<KB, VB, D>),
                                      hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_attend<KB, VB, D, R>), dim3(C::GRID), dim3(C::T), C::LDS, s, p);
+  hipLaunchKernelGGL((k_attend<KB, VB, D>), dim3(C::GRID), dim3(C::T), C::LDS, s, p);
   return hipGetLastError();
 }
 

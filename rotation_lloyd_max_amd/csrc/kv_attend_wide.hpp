@@ -61,9 +61,6 @@ struct AwHeader {
   uint32_t vbad;
 };
 
-// The lowest n bits; none for n <= 0, all from 32 on.
-__device__ __forceinline__ uint32_t aw_low(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
-
 // The power of two that brings scales near 1, if one is beyond 2^13, no number, or all are below
 // 2^-4; top: the largest finite one of the lane's. 2^-15 to 2^15.
 __device__ __forceinline__ int aw_exponent(float top) {
@@ -357,7 +354,6 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
       const bool masked = p->tree != nullptr;
       int cut = masked ? before : before + tok0 + 1;  // from this token on some row's mask may cut
       cut = cut < 0 ? 0 : cut;
-      const uint32_t* const tree = p->tree;
       const uint32_t hb_mul = p->hb_mul;
       const bool live = ((static_cast<uint32_t>(16 * wave) * hb_mul) >> 16) < static_cast<uint32_t>(ntok);
       int vexp = 0;  // the sums are held times 2^-vexp
@@ -399,20 +395,11 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
         const int ve = at_uniform(hdr->vexp);
         const uint32_t vbad = static_cast<uint32_t>(at_uniform(static_cast<int>(hdr->vbad)));
         if (blk * 32 + 32 > cut) {
-          const int j0 = blk * 32;
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const int row = 16 * (wave + W * r) + (lane & 15);
-            // the tokens of the block that the row sees, as bits
-            uint32_t see = aw_low(*reinterpret_cast<const int*>(smem + C::LIM + 4 * row) - j0);
-            if (tree) {
-              const int tk = (static_cast<uint32_t>(row) * p->hb_mul) >> 16, words = p->tree_words;
-              const uint32_t* bits = tree + static_cast<int64_t>(sq.row0 + tok0 + (tk < ntok ? tk : 0)) * words;
-              const int w = (j0 - before) >> 5, sh = (j0 - before) & 31;
-              const uint32_t w0 = w >= 0 && w < words ? bits[w] : 0u, w1 = w >= -1 && w + 1 < words ? bits[w + 1] : 0u;
-              see |= static_cast<uint32_t>((static_cast<uint64_t>(w1) << 32 | w0) >> sh) & aw_low(len - j0);
-            }
-            see >>= 4 * h;
+            const uint32_t see = at_seen(p, *reinterpret_cast<const int*>(smem + C::LIM + 4 * row), blk * 32, before, len,
+                                         sq.row0 + tok0, row, ntok) >> (4 * h);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               s[r][i >> 2][i & 3] = (see >> (16 * (i >> 2) + (i & 3))) & 1u ? s[r][i >> 2][i & 3] : -__builtin_inff();
@@ -600,9 +587,9 @@ hipError_t aw_launch(const AttendParams& p, hipStream_t s) {
 template <int KB, int VB>
 hipError_t at_launch_d(const AttendParams& p, int D, int rows, hipStream_t s) {
   switch (D) {
-    case 64: return rows == 16 ? at_launch<KB, VB, 64, 1>(p, s) : rows == 128 ? aw_launch<KB, VB, 64, 1>(p, s) : aw_launch<KB, VB, 64, 2>(p, s);
-    case 128: return rows == 16 ? at_launch<KB, VB, 128, 1>(p, s) : rows == 128 ? aw_launch<KB, VB, 128, 1>(p, s) : aw_launch<KB, VB, 128, 2>(p, s);
-    default: return rows == 16 ? at_launch<KB, VB, 256, 1>(p, s) : aw_launch<KB, VB, 256, 1>(p, s);
+    case 64: return rows == 16 ? at_launch<KB, VB, 64>(p, s) : rows == 128 ? aw_launch<KB, VB, 64, 1>(p, s) : aw_launch<KB, VB, 64, 2>(p, s);
+    case 128: return rows == 16 ? at_launch<KB, VB, 128>(p, s) : rows == 128 ? aw_launch<KB, VB, 128, 1>(p, s) : aw_launch<KB, VB, 128, 2>(p, s);
+    default: return rows == 16 ? at_launch<KB, VB, 256>(p, s) : aw_launch<KB, VB, 256, 1>(p, s);
   }
 }
 
