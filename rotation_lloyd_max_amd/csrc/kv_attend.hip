@@ -55,8 +55,10 @@ __device__ __forceinline__ void at_finish(P p, float (&v)[D / 64], float l, int6
   __builtin_memcpy(__builtin_assume_aligned(dst, 2 * EL), x, 2 * EL);
 }
 
-// One wave per query row of a unit whose parts lie in several workgroups' slots, added in the
-// order of the tokens.
+// The query rows of units whose parts lie in several workgroups' slots, the parts added in the order
+// of the tokens. Few parts each: many rows, and what bounds it is the instructions of a row, so a wave
+// takes several (65536 rows of 128: 22 us with a row per wave, 15 us so). Many parts: few rows, one per
+// wave.
 template <int D>
 __global__ __launch_bounds__(256) void k_attend_join(JoinParams p) {
   constexpr int EL = D / 64;
@@ -64,68 +66,78 @@ __global__ __launch_bounds__(256) void k_attend_join(JoinParams p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const AttendMeta m = p.meta[blockIdx.x];
   if (m.parts == 0) return;
-  const int r = blockIdx.y * 4 + wave, tk = (static_cast<uint32_t>(r) * p.hb_mul) >> 16, hd = r - tk * p.hb;
-  if (tk >= m.nrows || hd >= m.nh) return;
-  const int n = m.parts + 1, d0 = kv_chunk(lane) * EL;
-  const uint32_t sg = p.vsigns[d0 >> 5] >> (d0 & 31);
+  const int n = m.parts + 1;
   const int64_t slot = static_cast<int64_t>(p.rows) * (D + 2);
   // part 0 is the second slot of its workgroup, the others the first of theirs
   const float* const base = p.parts + 2 * static_cast<int64_t>(blockIdx.x) * slot;
   auto part = [&](int i) { return base + (i == 0 ? slot : 2 * i * slot); };
-  float top = kAtNone, l = 0.f;
-  float v[EL] = {};
-  if (n <= 4) {
-    // everything at once (past the last part: that one again, times zero)
-    constexpr int K = 4;
-    float x[K][EL], a[K], b[K];
+  // K parts, everything at once (past the last part: that one again, unused)
+  auto few = [&](auto count) {
+    constexpr int K = decltype(count)::value;
+    const AtRows<D> rows;
+    const int r = (blockIdx.y * 4 + wave) * AtRows<D>::N + rows.sub;
+    if (r >= p.rows) return;
+    const int tk = (static_cast<uint32_t>(r) * p.hb_mul) >> 16, hd = r - tk * p.hb;
+    f32x4_t x[K][2];
+    float a[K], b[K], v[8] = {}, top = kAtNone, l = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const float* s = part(k < n ? k : n - 1);
       a[k] = s[p.rows * D + r];
       b[k] = s[p.rows * D + p.rows + r];
 #pragma unroll
-      for (int e = 0; e < EL; ++e) x[k][e] = s[r * D + d0 + e];
+      for (int e = 0; e < 2; ++e) x[k][e] = *reinterpret_cast<const f32x4_t*>(s + r * D + 8 * rows.c + 4 * e);
     }
+    const uint32_t sg = rows.signs(p.vsigns);
 #pragma unroll
     for (int k = 0; k < K; ++k) top = fmaxf(top, a[k]);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const float f = k >= n || a[k] == kAtNone ? 0.f : at_exp2(a[k] - top);
-      l += k >= n ? 0.f : b[k] != b[k] ? b[k] : b[k] * f;
+      if (k >= n) break;
+      const float f = a[k] == kAtNone ? 0.f : at_exp2(a[k] - top);
+      l += b[k] != b[k] ? b[k] : b[k] * f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(f, x[k][e >> 2][e & 3], v[e]);
+    }
+    at_store<D>(&p, v, l, static_cast<int64_t>(m.row0) + tk, m.head0 + hd, sg, rows.c, tk < m.nrows && hd < m.nh);
+  };
+  if (n <= 4) return few(AtInt<4>{});
+  if (n <= 8) return few(AtInt<8>{});
+  const int r = blockIdx.y * 4 + wave, tk = (static_cast<uint32_t>(r) * p.hb_mul) >> 16, hd = r - tk * p.hb;
+  if (tk >= m.nrows || hd >= m.nh) return;
+  const int d0 = kv_chunk(lane) * EL;
+  const uint32_t sg = p.vsigns[d0 >> 5] >> (d0 & 31);
+  float top = kAtNone, l = 0.f;
+  float v[EL] = {};
+  for (int i = lane; i < n; i += 64) {
+    const float a = part(i)[p.rows * D + r];
+    wt[wave][i] = a;
+    top = fmaxf(top, a);
+  }
+  top = kv_wave_max(top);
+  for (int i = lane; i < n; i += 64) {
+    const float a = wt[wave][i], b = part(i)[p.rows * D + p.rows + r];
+    const float f = a == kAtNone ? 0.f : at_exp2(a - top);
+    wt[wave][i] = f;
+    l += b != b ? b : b * f;
+  }
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) l += __shfl_xor(l, x);
+  wave_lds_sync();
+  // sixteen parts' loads at a time
+  for (int i0 = 0; i0 < n; i0 += 16) {
+    float x[16][EL];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float* s = part(i0 + k < n ? i0 + k : n - 1) + r * D + d0;
+#pragma unroll
+      for (int e = 0; e < EL; ++e) x[k][e] = s[e];
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float f = i0 + k < n ? wt[wave][i0 + k] : 0.f;
 #pragma unroll
       for (int e = 0; e < EL; ++e) v[e] = __builtin_fmaf(f, x[k][e], v[e]);
-    }
-  } else {
-    for (int i = lane; i < n; i += 64) {
-      const float a = part(i)[p.rows * D + r];
-      wt[wave][i] = a;
-      top = fmaxf(top, a);
-    }
-    top = kv_wave_max(top);
-    for (int i = lane; i < n; i += 64) {
-      const float a = wt[wave][i], b = part(i)[p.rows * D + p.rows + r];
-      const float f = a == kAtNone ? 0.f : at_exp2(a - top);
-      wt[wave][i] = f;
-      l += b != b ? b : b * f;
-    }
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) l += __shfl_xor(l, x);
-    wave_lds_sync();
-    // sixteen parts' loads at a time
-    for (int i0 = 0; i0 < n; i0 += 16) {
-      float x[16][EL];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float* s = part(i0 + k < n ? i0 + k : n - 1) + r * D + d0;
-#pragma unroll
-        for (int e = 0; e < EL; ++e) x[k][e] = s[e];
-      }
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float f = i0 + k < n ? wt[wave][i0 + k] : 0.f;
-#pragma unroll
-        for (int e = 0; e < EL; ++e) v[e] = __builtin_fmaf(f, x[k][e], v[e]);
-      }
     }
   }
   at_finish<D>(&p, v, l, static_cast<int64_t>(m.row0) + tk, m.head0 + hd, sg, lane);

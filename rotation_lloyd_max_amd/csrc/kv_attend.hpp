@@ -528,8 +528,8 @@ struct AtQuery : AtRows<D> {
 
 // The lane's part v of a row's sums, l the sum of its weights: normalised, rotated back and (if ok)
 // stored.
-template <int D>
-__device__ __forceinline__ void at_store(AtArgs p, float (&v)[8], float l, int64_t m, int head, uint32_t sg, int c, bool ok) {
+template <int D, typename P>
+__device__ __forceinline__ void at_store(P p, float (&v)[8], float l, int64_t m, int head, uint32_t sg, int c, bool ok) {
   const float f = p->inv_sqrt_d / l;
   sg ^= 0u - kv_sign(c);
 #pragma unroll
