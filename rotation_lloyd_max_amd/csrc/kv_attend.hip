@@ -13,11 +13,17 @@ namespace {
 
 constexpr size_t kMetaBytes = sizeof(AttendMeta) * kAtMaxGrid;
 
-// Query rows of a tile, and the workgroups of a launch. Up to 16 rows per key head and sequence: the
-// kernel whose waves share the rows and split the tokens. More: the one whose waves split the rows.
+// Query rows of a tile, and the workgroups of a launch. By the rows that share a key head of a sequence
+// (8 sequences of 4096 tokens, 8 key heads of 128, 8-bit keys, 3-bit values; whole call, us):
+//   rows                              8   32   64  128  132  256  2048 (4 sequences)
+//   tiles of 16: waves share rows,   28   38   57
+//       each decoding its own tokens
+//   tiles of 128: waves split the    50   50   52   66   93   94   294
+//       rows and share each block
+//   tiles of 256                               66   86   85   87   216
 int tile_rows(int D, int share, int B, int64_t M) {
   const int64_t rows = (M * share + B - 1) / B;
-  return rows <= 16 ? 16 : rows <= 128 || D == 256 ? 128 : 256;
+  return rows <= 48 ? 16 : rows <= 128 || D == 256 ? 128 : 256;
 }
 int workgroups(int D, int rows) { return (rows > 16 ? 1 : D <= 128 ? 3 : 2) * kAtCus; }
 

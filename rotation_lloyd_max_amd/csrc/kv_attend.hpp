@@ -3,30 +3,44 @@
 //     out = R_v^T sum_j p_j v'_j,  p = softmax_j(scale * (R_k q) . k'_j)
 // with k', v' the decoded rows in the rotated bases (R orthonormal: q . k = (R q) . (R k)).
 //
-// Work. A unit is (sequence, key head, tile of up to 16 query rows that share the head). All
-// units lie on one line of work, each as long as the tokens it reads plus a constant for its
-// set-up, cut into shares, one per workgroup: uneven lengths balance, and a few long sequences
-// still fill the chip. With few units each is cut evenly into its own workgroups (AtPlan). A cut
-// inside a unit leaves partial sums in the workspace, which k_attend_join adds up in a fixed
-// order. Workgroups are small (four waves), so that two or three share a CU and one's set-up
-// hides behind another's stream.
+// Work. A unit is (sequence, key head, tile of query rows that share the head). All units lie on
+// one line of work, each as long as the tokens it reads plus a constant for its set-up, cut into
+// shares, one per workgroup: uneven lengths balance, and a few long sequences still fill the chip.
+// With few units each is cut evenly into its own workgroups (AtWork). A cut inside a unit leaves
+// partial sums in the workspace, which k_attend_join adds up in a fixed order. The schedule is made
+// on the device, by every workgroup for itself: lengths and offsets may change between replays.
+//
+// This kernel is for few rows (tiles of 16; many: kv_attend_wide.hpp). Workgroups are small (four
+// waves), so that two or three share a CU and one's set-up hides behind another's stream; the waves
+// share the rows and split the tokens.
 //
 // A wave takes blocks of 32 tokens. Scores come as S^T = K Q^T on v_mfma_f32_16x16x32_f16: lane l
 // supplies a quarter row of token l % 16 (elements D / 4 * (l / 16) + ..., one contiguous load and
 // one group scale) and receives, for query row l % 16, the tokens 4 (l / 16) + i: exactly the
-// layout in which P^T is the B operand of O^T += V^T P^T, so probabilities never leave their lane. The V operand wants eight tokens of one element per
-// lane: lane l loads the same piece of eight tokens' rows (D / 16 codes at element D / 16 * (l % 16))
-// and pairs equal positions of two tokens by bit operations. Decoded values are never stored.
+// layout in which P^T is the B operand of O^T += V^T P^T, so probabilities never leave their lane.
+// The V operand wants eight tokens of one element per lane: lane l loads the same piece of eight
+// tokens' rows (D / 16 codes at element D / 16 * (l % 16)) and pairs equal positions of two tokens
+// by bit operations. Decoded values are never stored.
 //
 // Decoding is an LDS table of fp16 centroids. Codes of 8 bits (and pairs of 4-bit codes) use a
 // table with 32 columns, entry e for lane l at 128 e + 4 (l % 32): the lanes that the LDS serves
-// together never meet in a bank, and one v_dot4 makes the address from a byte of the word. Pairs of 3- and 2-bit codes need 64 and 16 entries, which
-// lie in different banks by themselves.
+// together never meet in a bank (2.8 cycles of a CU per wave's read; 4.7 from one copy of 256
+// entries), and one v_dot4 makes the address from a byte of the word. Pairs of 3- and 2-bit codes
+// need 64 and 16 entries, which lie in different banks by themselves (3.4 cycles).
 //
 // Group scales multiply the centroids in fp16, kept in range by powers of two per wave that follow
 // the largest scales met. Softmax in base 2 with a reference that moves only when a score passes it
 // by 2^8 (p then stays within fp16: 2^7 at the reference, at most 2^15), so the running maximum
-// needs neither lane exchange nor rescaling in the common step. Sums are fp32.
+// needs neither lane exchange nor rescaling in the common step. Sums are fp32. What is rounded to
+// fp16 (the rotated q, centroids, their products with scales, p) is what the matrix cores take: half
+// a step each, 2^-11, against 2^-9 of a bf16 output.
+//
+// Measured, 8 key heads of 128 shared by 4 query heads, 8-bit keys and 3-bit values, kernel and join:
+// one token over 337 11.1 + 3.8 us; over 131071 (193 MB) 55.9 + 7.3 us, 3.5 TB/s of the 6.0 that a
+// large read reaches; 32 sequences of 61 to 8191 (82 MB) 36.0 + 4.1 us. What bounds the long ones is
+// the decoding's vector instructions, 364 for a block of 32 tokens (with no table reads 92 % of the
+// time remains, with no loads 85 %); the short ones the chain of memory latencies of schedule, q, page
+// ids, codes and join.
 #pragma once
 
 #include "internal.hpp"
@@ -332,8 +346,10 @@ __device__ __forceinline__ bool at_plan(AtArgs p, int wg, int lane, int per, int
   const int all_units = __builtin_amdgcn_readlane(at_scan(units), 63);
   // With few units, each is cut into parts of at most `chunk` blocks, one part per workgroup:
   // sum ceil(blocks / chunk) <= sum blocks / chunk + units <= GRID (the sum in fp32 is rounded up).
-  // Otherwise the line is cut every q.
-  o.own = !__any(!even) && all_units <= GRID / 2;
+  // Otherwise the line is cut every q. Parts start sooner, shares balance better; whole call with
+  // either, 4096 tokens, units of workgroups: 8 of 768 14 and 20 us, 64 of 768 28 and 31, 256 of 768
+  // 60 and 56; tiles of 128, 32 of 256 44 and 50, 64 of 256 50 and 47.
+  o.own = !__any(!even) && all_units <= GRID / 6;
   const bool own = o.own;
   int chunk = 0;
   int64_t q = 0, w0, w1, excl;

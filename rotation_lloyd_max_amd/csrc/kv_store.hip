@@ -10,6 +10,11 @@
 // waves. The code comes from a bucket table instead of a search: |u| * 64 is exact, each bucket
 // of width 1/64 holds at most one positive threshold (neighbours are more than 1/64 apart even
 // at 256 levels), so one LDS read gives the count below the bucket and the threshold to compare.
+//
+// Bound by vector instructions (fp64 transform of five to eight stages; 2900 wave instructions per
+// 4 x 256 elements of a key or value): 3001 tokens of 4 heads of 256 in fp16, 4 bits, turned (31 MB):
+// 21.7 us, 1.4 TB/s; 16 tokens of 8 heads of 128: 6.0 us, latency. 1024 workgroups a half instead of
+// 2048 23 us; next token's rows loaded ahead spilled and took 59 us.
 #include "kv_lane.hpp"
 
 #include <mutex>
