@@ -143,7 +143,9 @@ def rope(x, positions, rope, transposed=False, out=None):
     dev = x.device
     positions = _as(positions, torch.int32, dev, "positions", (x.shape[0],))
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = torch.empty_like(x)  # (half a microsecond less than torch.empty)
+        if not out.is_contiguous():
+            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
     elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev:
         raise ValueError("out= must have x's shape, dtype and device")
     elif _overlaps_itself(out):
@@ -234,7 +236,10 @@ def kv_load(cache, slots, out_dtype=torch.bfloat16, k_out=None, v_out=None, keys
         if o is not None and o.dtype != out_dtype:
             raise ValueError(f"k_out= and v_out= must be {out_dtype}")
     k = _tq._out(k_out, shape, out_dtype, dev) if keys else None
-    v = _tq._out(v_out, shape, out_dtype, dev) if values else None
+    if values:
+        v = torch.empty_like(k) if keys and k_out is None and v_out is None else _tq._out(v_out, shape, out_dtype, dev)
+    else:
+        v = None
     if out_dtype not in _tq._DT:
         raise TypeError(f"unsupported dtype {out_dtype}")
     _call(dev, _tq.lib().tq_kv_load, cache.desc, slots.data_ptr(), shape[0],
@@ -283,7 +288,10 @@ def kv_attend(cache, q, kv_lens, page_table, q_offsets=None, tree=None, scale=No
         words = tree.shape[1]
         tree = _as(tree, torch.int32, dev, "tree", (M, words))
     if out is None:
-        out = torch.empty((M, H, D), dtype=out_dtype or q.dtype, device=dev)
+        if q.is_contiguous() and (out_dtype is None or out_dtype == q.dtype):
+            out = torch.empty_like(q)
+        else:
+            out = torch.empty((M, H, D), dtype=out_dtype or q.dtype, device=dev)
     else:
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError(f"out= must be {out_dtype}")
