@@ -28,11 +28,11 @@ namespace {
 constexpr int kStoreBuckets = 320;  // buckets of 1/64 up to 5.0; the last one is open
 
 // One half's decision data: positive thresholds (binary32 bits, the last one a sentinel no key
-// exceeds) and the buckets that hold one, as bits: the thresholds below bucket b are as many as the
-// bits below b.
+// exceeds) and the buckets that hold one, as bits, with the number of bits before each word: the
+// thresholds below bucket b are as many as the bits below b.
 struct SnapTable {
   uint32_t thr[128];
-  uint32_t held[kStoreBuckets / 32];
+  uint32_t held[kStoreBuckets / 32], before[kStoreBuckets / 32];
 };
 
 struct StoreHalf {
@@ -135,14 +135,12 @@ __global__ __launch_bounds__(256) void k_kv_store(StoreParams p) {
   const int cpos = hf.levels / 2;
   const bool turn = part == 0 && p.inv_freq;
   int flip = 0;
+  static_assert(kStoreBuckets % 64 == 0, "whole waves");
   for (int b = threadIdx.x; b < kStoreBuckets; b += blockDim.x) {
-    uint32_t base = 0;
-#pragma unroll
-    for (int k = 0; k < kStoreBuckets / 32; ++k) {
-      const int n = b - 32 * k;  // bits of this word below b
-      const uint32_t m = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-      base += __builtin_popcount(hf.snap.held[k] & m);
-    }
+    const int w = __builtin_amdgcn_readfirstlane(b >> 5);  // a wave's buckets: two words
+    const uint32_t held = b & 32 ? hf.snap.held[w + 1] : hf.snap.held[w];
+    const uint32_t before = b & 32 ? hf.snap.before[w + 1] : hf.snap.before[w];
+    const uint32_t base = before + __builtin_popcount(held & ((1u << (b & 31)) - 1u));
     tab[b] = u32x2_t{hf.snap.thr[base], base};
   }
   __syncthreads();
@@ -262,6 +260,7 @@ void init_snap() {
       ok = ok && in <= 1 && !(in && b + 1 == kStoreBuckets);
       if (in) t.held[b >> 5] |= 1u << (b & 31);
     }
+    for (int w = 1; w < kStoreBuckets / 32; ++w) t.before[w] = t.before[w - 1] + __builtin_popcount(t.held[w - 1]);
   }
   g_snap_ok = ok;
 }
