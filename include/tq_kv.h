@@ -124,10 +124,10 @@ int tq_kv_load(const tq_kv_cache *cache, const int64_t *slots, int64_t tokens, v
  * some 2^-11 of the mean size of the values, so fp16 outputs are good to about 7e-4 of their norm
  * and bf16 outputs to their rounding. A token whose scale is NaN makes the rows that see it
  * NaN, and no others. Deterministic.
- * Workspace: tq_kv_attend_workspace(cache, q_heads, B, M) bytes, 256-byte aligned; its contents
- * need not be kept, and two calls that can run at the same time need one each. M is at most
- * 2^24, B at most 65536, (M + B) * q_heads below 2^31, and times (table_width * page_tokens + 256)
- * below 2^53. */
+ * Workspace: tq_kv_attend_workspace(cache, q_heads, B, M) bytes (at most 69 MB, whatever the
+ * lengths), 256-byte aligned; its contents need not be kept, and two calls that can run at the
+ * same time need one each. M is at most 2^24, B at most 65536, (M + B) * q_heads below 2^31, and
+ * times (table_width * page_tokens + 256) below 2^53. */
 int tq_kv_attend(const tq_kv_cache *cache, const void *q, tq_dtype q_dtype, int32_t q_heads,
                  int64_t q_token_stride, int32_t B, const int32_t *q_offsets, int64_t M,
                  const int32_t *kv_lens, const int32_t *page_table, int32_t table_width,

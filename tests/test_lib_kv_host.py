@@ -126,6 +126,13 @@ def test_attend_refusals(kw, status):
     assert attend(cache(), **kw) == status, tq.lib().tq_last_error()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("qh,B,M", [(8, 1, 1), (32, 1, 1), (32, 64, 64), (32, 1, 16), (32, 1, 1 << 20), (1024, 65536, 1 << 20), (8, 0, 0)])
+def test_attend_workspace_is_bounded(D, qh, B, M):
+    n = tq.lib().tq_kv_attend_workspace(cache(dict(K=D, group=32), dict(K=D, group=32)), qh, B, M)
+    assert n <= 69 * 10 ** 6 and (n > 0) == (M > 0)
+
+
 def test_empty_calls_do_nothing():
     c = cache()
     assert store(c, tokens=0, k=None, v=None, slots=None) == 0
