@@ -175,3 +175,42 @@ def test_captured_chunks_replayed():
         for o, t in zip(outs, (None, words)):
             assert torch.equal(o, tq.kv_attend(bt.cache, q, lens, table, q_offsets=off, tree=t)), rep
             o.zero_()
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_sequences_on_the_same_pages(n):
+    # a shared text: the same pages in several sequences' tables, and one page twice in a row of it
+    bt = Batch([160, 160, 96], heads=2, D=64, page=32, kg=32)
+    table = np.array(bt.table)
+    table[1] = table[0]
+    table[2, 2] = table[2, 0]
+    bt.table[:] = table
+    for b, m in ((1, 160), (2, 96)):
+        j = np.arange(m)
+        bt.slots[b] = table[b, j // 32].astype(np.int64) * 32 + j % 32
+    bt.refresh()
+    counts = [n, n, n]
+    q = queries(3 * n, 4, 64, torch.bfloat16)
+    q[n:2 * n] = q[:n]
+    got = run(bt, q, counts)
+    check(got, bt, q, counts, 0.125, only=set(range(0, 3 * n, 7)) | {3 * n - 1})
+    want = got[:n] if n > 1 else got[:1]
+    assert torch.allclose(got[n:2 * n].float(), want.float(), rtol=2.0 ** -6, atol=2.0 ** -6)
+
+
+def test_two_streams_with_their_own_workspaces():
+    bt = Batch([900, 260], heads=2, D=128, page=64)
+    counts = [150, 60]
+    off = torch.tensor([0, 150, 210], dtype=torch.int32, device="cuda")
+    qs = [queries(210, 8, 128, torch.bfloat16, seed=s) for s in range(2)]
+    want = [run(bt, q, counts) for q in qs]
+    lens, table = bt.dev()
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in qs], [[], []]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(tq.kv_attend(bt.cache, qs[i], lens, table, q_offsets=off))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
