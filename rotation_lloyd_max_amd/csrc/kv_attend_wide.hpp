@@ -150,8 +150,8 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
         id[0] = len > 0 ? ids[pi] : -1;
         id[1] = len > 0 ? ids[pi2] : -1;
       };
-      // codes and scales of this wave's part, of this round's and the next round's block, in the types they are loaded as: widened at once, they
-      // would be waited for at once
+      // codes and scales of this wave's part, of the block being decoded and of the next one, in the
+      // types they are loaded as: widened at once, they would be waited for at once
       uint32_t kx[8], kx1[8];
       uint16_t ks[C::KS], vs[8], ks1[C::KS], vs1[8];
       typename C::Piece vx[8], vx1[8];
