@@ -158,6 +158,24 @@ def rope(x, positions, rope, transposed=False, out=None):
     return out
 
 
+def _half(w, name, index):
+    """The descriptor of a cache's half. The library reads and writes E * N rows through its
+    pointers: its tensors must hold them, on the device `index`."""
+    codes, scales, sg, K = w.codes, w.scales, w.signs, w.K
+    n = w.E * w.N * K
+    if (codes.dtype != torch.int32 or codes.numel() * 32 != n * _BITS.get(w.levels, 0)
+            or not codes.is_contiguous()):
+        raise ValueError(f"{name}.codes must be a contiguous int32 tensor of {w.E * w.N} packed rows")
+    if scales.dtype != torch.float16 or scales.numel() * w.group != n or not scales.is_contiguous():
+        raise ValueError(f"{name}.scales must be a contiguous float16 tensor of {w.E * w.N} rows "
+                         "of K / group scales")
+    if sg.dtype != torch.int32 or sg.numel() * 32 < K or not sg.is_contiguous():
+        raise ValueError(f"{name}.signs must hold {K} sign bits")
+    if not codes.get_device() == scales.get_device() == sg.get_device() == index:
+        raise ValueError(f"the tensors of a cache must be on one device ({name} is not on {index})")
+    return _tq._QWeight(codes.data_ptr(), scales.data_ptr(), sg.data_ptr(), w.levels, w.group, K, w.N, w.E)
+
+
 class KVCache:
     """A paged compressed cache: k and v are QWeights of E = pages experts of N = heads *
     page_tokens rows of head_dim K; row h * page_tokens + t of a page is its token t of head h.
@@ -165,26 +183,12 @@ class KVCache:
     and v held when it was made."""
 
     def __init__(self, k, v, heads, page_tokens):
-        # the library reads and writes E * N rows through a half's pointers: its tensors must
-        # hold them, on one device
-        self.device = dev = k.codes.device
+        index = k.codes.get_device()
+        self.desc = _KVCache(_half(k, "k", index), _half(v, "v", index), heads, page_tokens)
+        self.device = k.codes.device
         self._keep = (k.codes, k.scales, k.signs, v.codes, v.scales, v.signs)
-        for name, w in (("k", k), ("v", v)):
-            rows, codes, scales, sg = w.E * w.N, w.codes, w.scales, w.signs
-            if (codes.dtype != torch.int32 or codes.numel() * 32 != rows * w.K * _BITS.get(w.levels, 0)
-                    or not codes.is_contiguous()):
-                raise ValueError(f"{name}.codes must be a contiguous int32 tensor of {rows} packed rows")
-            if (scales.dtype != torch.float16 or scales.numel() * w.group != rows * w.K
-                    or not scales.is_contiguous()):
-                raise ValueError(f"{name}.scales must be a contiguous float16 tensor of {rows} rows "
-                                 "of K / group scales")
-            if sg.dtype != torch.int32 or sg.numel() * 32 < w.K or not sg.is_contiguous():
-                raise ValueError(f"{name}.signs must hold {w.K} sign bits")
-            if codes.device != dev or scales.device != dev or sg.device != dev:
-                raise ValueError(f"the tensors of a cache must be on one device ({name} is not on {dev})")
         self.k, self.v, self.heads, self.page_tokens = k, v, heads, page_tokens
         self.head_dim = k.K
-        self.desc = _KVCache(k.desc(), v.desc(), heads, page_tokens)
 
 
 def kv_cache(pages, heads, head_dim, page_tokens=64, k_levels=256, v_levels=8, k_group=64,
