@@ -887,7 +887,14 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D>::T), (AtCfg<KB, VB, D>::WGS * AtC
       // its scales are small (below 2^-4), and grow when one passes 2^13.
       int kexp = 0, vexp = 0;
 
-      auto scores = [&](const AtBlock<C>& x, bool first, f32x4_t (&s)[2]) {
+      auto scores = [&](AtBlock<C>& x, int blk, bool first, f32x4_t (&s)[2]) {
+        if (blk * 32 + 32 > len) {  // rows behind the last token hold anything: they have no say in the exponent
+          const int j = blk * 32 + (at_fresh(threadIdx.x & 63) & 15);
+#pragma unroll
+          for (int sb = 0; sb < 2; ++sb)
+#pragma unroll
+            for (int y = 0; y < C::KS; ++y) x.ks[sb][y] = j + 16 * sb < len ? x.ks[sb][y] : 0u;
+        }
         uint32_t kd[2][C::KS];  // scales times 2^-kexp, in both halves
         auto key_scales = [&]() {
           uint32_t big = 0;
@@ -1090,7 +1097,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D>::T), (AtCfg<KB, VB, D>::WGS * AtC
           f32x4_t s[2];
           uint32_t pb[4];
           const uint32_t bad = x.bad;
-          scores(x, first, s);
+          scores(x, blk, first, s);
           if (more) {
             locate(x);
             load_k(x);

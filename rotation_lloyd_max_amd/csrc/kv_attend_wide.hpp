@@ -238,6 +238,8 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
 #pragma unroll
           for (int y = 0; y < C::KS; ++y) {
             z[y] = (bad >> sbk) & 1u ? 0x7e007e00u : ks[y] | (static_cast<uint32_t>(ks[y]) << 16);  // scores of a bad page are NaN
+            // rows behind the last token hold anything: they have no say in the exponent
+            if (blk * 32 + 32 > len) z[y] = blk * 32 + 16 * sbk + (lane & 15) < len ? z[y] : 0u;
             big = z[y] > big ? z[y] : big;
           }
           int e = 0;
