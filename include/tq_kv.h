@@ -120,10 +120,13 @@ int tq_kv_load(const tq_kv_cache *cache, const int64_t *slots, int64_t tokens, v
  *   tree         device uint32 [M][tree_words], or NULL
  *   out          device [M][q_heads][K], bf16 or fp16 (its own dtype), contiguous, 16-byte aligned
  * Scores, softmax statistics and sums are fp32; the operands of the matrix cores (rotated
- * q, centroids, p, decoded values) are fp16, scaled so that none overflows: an output is off by
- * some 2^-11 of the mean size of the values, so fp16 outputs are good to about 7e-4 of their norm
- * and bf16 outputs to their rounding. A token whose scale is NaN makes the rows that see it
- * NaN, and no others. Deterministic.
+ * q, centroids, p, decoded values) are fp16, scaled so that none overflows and so that no token's
+ * scales, seen or not, take bits from another's: a token's part of an output is off by some 2^-11
+ * of itself and 2^-32 of the token's value (weights below 2^-21 of the largest lose bits). So fp16
+ * outputs are good to about 7e-4 of their norm and bf16 outputs to their rounding. Rows of the
+ * last page behind kv_lens[b] may hold anything. A token whose scale is NaN makes the rows that
+ * see it NaN, and no others. Deterministic; the last bits of a row depend on the batch it is in
+ * (what else is in it decides where its tokens are cut into parts).
  * Workspace: tq_kv_attend_workspace(cache, q_heads, B, M) bytes (at most 69 MB, whatever the
  * lengths), 256-byte aligned; its contents need not be kept, and two calls that can run at the
  * same time need one each. M is at most 2^24, B at most 65536, (M + B) * q_heads below 2^31, and

@@ -28,12 +28,18 @@
 // entries), and one v_dot4 makes the address from a byte of the word. Pairs of 3- and 2-bit codes
 // need 64 and 16 entries, which lie in different banks by themselves (3.4 cycles).
 //
-// Group scales multiply the centroids in fp16, kept in range by powers of two per wave that follow
-// the largest scales met. Softmax in base 2 with a reference that moves only when a score passes it
-// by 2^8 (p then stays within fp16: 2^7 at the reference, at most 2^15), so the running maximum
-// needs neither lane exchange nor rescaling in the common step. Sums are fp32. What is rounded to
-// fp16 (the rotated q, centroids, their products with scales, p) is what the matrix cores take: half
-// a step each, 2^-11, against 2^-9 of a bf16 output.
+// Group scales multiply the centroids in fp16. Scales from 2^-12 up to 2^13 enter as they are: products
+// stay below fp16's largest, and what its subnormals cut is less than 2^-13 of a scale. In a block that
+// holds another scale each token is held times one of two powers of two, by its own largest scale
+// (kAtLoud). Keys' come off their scores in fp32; a block of such values is multiplied twice, once for the
+// tokens of either kind, with the sums brought to their power of two in between. So no token costs its
+// neighbours bits, seen or not, and in the common step scales cost one comparison.
+//
+// Softmax in base 2 with a reference that moves only when a score passes it by 2^8 (p then stays within
+// fp16: 2^7 at the reference, at most 2^15, so that its subnormals cut 2^-32 of a weight), so the
+// running maximum needs neither lane exchange nor rescaling in the common step. Sums are fp32. What is
+// rounded to fp16 (the rotated q, centroids, their products with scales, p) is what the matrix cores
+// take: half a step each, 2^-11, against 2^-8 of a bf16 output.
 //
 // Measured, 8 key heads of 128 shared by 4 query heads, 8-bit keys and 3-bit values, kernel and join:
 // one token over 337 11.1 + 3.8 us; over 131071 (193 MB) 55.9 + 7.3 us, 3.5 TB/s of the 6.0 that a
@@ -59,6 +65,11 @@ constexpr int kAtMinShare = 512;
 constexpr int kAtMinBlocks = 4;
 constexpr float kAtLazy = 8.f;          // log2 of how far a score may pass the reference
 constexpr float kAtNone = -3e38f;       // reference of a row that has seen nothing
+// fp16 bits of scales: they enter as they are from kAtLow up to below kAtLow + kAtSpan (2^-12, 2^13). In a
+// block with others, tokens whose largest scale is from kAtLoud (2^-4) on are held times 2^-6, the rest
+// times 2^12: both bring every token's largest to 2^-12 .. 2^10.
+constexpr uint32_t kAtLow = 0x0c00, kAtSpan = 0x6400, kAtLoud = 0x2c00;
+constexpr int kAtLoudExp = 6, kAtQuietExp = -12;
 
 struct AttendMeta {                 // of a workgroup whose last unit goes on in the next ones
   int32_t parts;                    // following workgroups that hold a part; 0: nothing to join
@@ -596,19 +607,48 @@ __device__ __forceinline__ void at_put(float* slot, int rows, int r, int c, cons
 }
 
 // ---- decoding -----------------------------------------------------------------------------
-// the larger of each half, as unsigned numbers (scales are not negative)
+// the larger of each half, as unsigned numbers
+typedef uint16_t AtU16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t at_max_u16(uint32_t a, uint32_t b) {
-  typedef uint16_t V __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(AtU16x2, a), __builtin_bit_cast(AtU16x2, b)));
+}
+// how far two scales lie above kAtLow, those below it farthest; in range: less than kAtSpan
+__device__ __forceinline__ uint32_t at_range(uint32_t pair) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(AtU16x2, pair) - __builtin_bit_cast(AtU16x2, kAtLow | kAtLow << 16));
+}
+// whether a scale of any lane's four pairs is out of range (a wave's answer)
+__device__ __forceinline__ bool at_far(const uint32_t (&pair)[4]) {
+  uint32_t big = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) big = at_max_u16(at_range(pair[i]), big);
+  big = big > (big << 16) ? big : big << 16;
+  return __any(big >= (kAtSpan << 16));
+}
+// Which of the 16 tokens of a half block are loud, lane l holding the largest of its scales (without
+// sign) of token l % 16.
+__device__ __forceinline__ uint32_t at_loud(uint32_t largest) {
+  uint64_t who = __ballot(largest >= kAtLoud);
+  who |= who >> 32;
+  return static_cast<uint32_t>(who | who >> 16) & 0xffffu;
+}
+// a if the bit is set, else b, by bit operations (a comparison per bit would take a pair of scalar
+// registers each)
+__device__ __forceinline__ float at_pick(uint32_t bits, int bit, float a, float b) {
+  const uint32_t m = static_cast<uint32_t>(static_cast<int32_t>(bits << (31 - bit)) >> 31);
+  return __uint_as_float((__float_as_uint(a) & m) | (__float_as_uint(b) & ~m));
+}
+// The lane's scores of a half block back from the power of two of their tokens' keys; loud: bits of its
+// 16 tokens.
+__device__ __forceinline__ void at_back(f32x4_t& s, uint32_t loud, int h) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    s[i] *= at_pick(loud >> (4 * h), i, static_cast<float>(1 << kAtLoudExp), 1.f / static_cast<float>(1 << -kAtQuietExp));
 }
 __device__ __forceinline__ uint32_t at_mul(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, a) * __builtin_bit_cast(half2_t, b));
 }
-// 2^-e in both halves, -15 <= e <= 14; 2^-15 as the subnormal it is
-__device__ __forceinline__ uint32_t at_pow2(int e) {
-  const uint32_t x = e < 15 ? static_cast<uint32_t>(15 - e) << 10 : 0x0200u;
-  return x | (x << 16);
-}
+// 2^-e in both halves, -15 <= e <= 14
+__device__ __forceinline__ uint32_t at_pow2(int e) { return static_cast<uint32_t>(15 - e) * 0x04000400u; }
 __device__ __forceinline__ f32x4_t at_mfma(const uint32_t (&a)[4], const uint32_t (&b)[4], f32x4_t c) {
   const u32x4_t x{a[0], a[1], a[2], a[3]}, y{b[0], b[1], b[2], b[3]};
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, x), __builtin_bit_cast(f16x8_t, y), c, 0, 0, 0);
@@ -878,54 +918,43 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D>::T), (AtCfg<KB, VB, D>::WGS * AtC
       int cut = masked ? before : before + tok0 + 1;
       cut = cut < 0 ? 0 : cut;
 
-      float c1 = *reinterpret_cast<const float*>(smem + C::C1 + 4 * col);  // score factor, times 2^kexp
+      const float c1 = *reinterpret_cast<const float*>(smem + C::C1 + 4 * col);  // score factor
+      int oexp = 0;                                                              // the sums are held times 2^-oexp
       float mo = kAtNone, l = 0.f;                                         // reference - 7; sum
       f32x4_t o[CH];
 #pragma unroll
       for (int n = 0; n < CH; ++n) o[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      // Scales are held times 2^-kexp and 2^-vexp. They start at 1, are set by the first block if
-      // its scales are small (below 2^-4), and grow when one passes 2^13.
-      int kexp = 0, vexp = 0;
 
-      auto scores = [&](AtBlock<C>& x, int blk, bool first, f32x4_t (&s)[2]) {
-        if (blk * 32 + 32 > len) {  // rows behind the last token hold anything: they have no say in the exponent
+      auto scores = [&](AtBlock<C>& x, int blk, f32x4_t (&s)[2]) {
+        if (blk * 32 + 32 > len || x.bad) {  // rows that hold no token hold anything: as if 1
           const int j = blk * 32 + (at_fresh(threadIdx.x & 63) & 15);
 #pragma unroll
           for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
-            for (int y = 0; y < C::KS; ++y) x.ks[sb][y] = j + 16 * sb < len ? x.ks[sb][y] : 0u;
-        }
-        uint32_t kd[2][C::KS];  // scales times 2^-kexp, in both halves
-        auto key_scales = [&]() {
-          uint32_t big = 0;
-#pragma unroll
-          for (int sb = 0; sb < 2; ++sb)
-#pragma unroll
-            for (int y = 0; y < C::KS; ++y) {
-              uint32_t z = x.ks[sb][y] | (x.ks[sb][y] << 16);
-              if ((x.bad >> sb) & 1u) z = 0;
-              kd[sb][y] = at_mul(z, at_pow2(kexp));
-              big = kd[sb][y] > big ? kd[sb][y] : big;
-            }
-          return big;
-        };
-        const uint32_t big = key_scales();
-        if (__any(big > 0x7000ffffu) || (first && !__any(big > 0x2c00ffffu))) {  // beyond 2^13, no number, or small
-          float top = 0.f;
-#pragma unroll
-          for (int sb = 0; sb < 2; ++sb)
-#pragma unroll
             for (int y = 0; y < C::KS; ++y)
-              if ((x.ks[sb][y] & 0x7c00u) != 0x7c00u && !((x.bad >> sb) & 1u))
-                top = fmaxf(top, fabsf(half_bits_to_float(static_cast<uint16_t>(x.ks[sb][y]))));
-          int ne = static_cast<int>(__float_as_uint(kv_wave_max(top)) >> 23) - 127;
-          ne = at_uniform(ne < -15 ? -15 : ne);
-          if (ne > kexp || first) {
-            const float f = at_exp2(static_cast<float>(ne - kexp));
-            kexp = ne;
-            c1 *= f;
+              x.ks[sb][y] = j + 16 * sb < len && !((x.bad >> sb) & 1u) ? x.ks[sb][y] : 0x3c00u;
+        }
+        uint32_t kd[2][C::KS];  // scales in both halves
+        uint32_t far = 0;
+#pragma unroll
+        for (int sb = 0; sb < 2; ++sb)
+#pragma unroll
+          for (int y = 0; y < C::KS; ++y) {
+            kd[sb][y] = x.ks[sb][y] | (x.ks[sb][y] << 16);
+            const uint32_t z = x.ks[sb][y] - kAtLow;
+            far = z > far ? z : far;
           }
-          key_scales();
+        const bool apart = __any(far >= kAtSpan);
+        auto loud = [&](int sb) {
+          return at_loud((C::KS == 2 && (x.ks[sb][C::KS - 1] & 0x7fffu) > (x.ks[sb][0] & 0x7fffu) ? x.ks[sb][C::KS - 1] : x.ks[sb][0]) & 0x7fffu);
+        };
+        if (__builtin_expect(apart, 0)) {
+#pragma unroll
+          for (int sb = 0; sb < 2; ++sb) {
+            const uint32_t f = (loud(sb) >> col) & 1u ? at_pow2(kAtLoudExp) : at_pow2(kAtQuietExp);
+#pragma unroll
+            for (int y = 0; y < C::KS; ++y) kd[sb][y] = at_mul(kd[sb][y], f);
+          }
         }
         s[0] = s[1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         // the next step's table reads are on their way while this one's results are multiplied
@@ -945,6 +974,10 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D>::T), (AtCfg<KB, VB, D>::WGS * AtC
           s[sb] = at_mfma(a, qb, s[sb]);
           __builtin_amdgcn_sched_barrier(0);
         }
+        if (__builtin_expect(apart, 0)) {
+          at_back(s[0], loud(0), h);
+          at_back(s[1], loud(1), h);
+        }
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb)
           if ((x.bad >> sb) & 1u) {
@@ -952,16 +985,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D>::T), (AtCfg<KB, VB, D>::WGS * AtC
             for (int i = 0; i < 4; ++i) s[sb][i] = __builtin_nanf("");
           }
       };
-      auto softmax = [&](int blk, f32x4_t (&s)[2], uint32_t (&pb)[4]) {
-        // masks
-        if (blk * 32 + 32 > cut) {
-          const int lane = at_fresh(threadIdx.x & 63), col = lane & 15;
-          const uint32_t see = at_seen(p, *reinterpret_cast<const int*>(smem + C::LIM + 4 * col), blk * 32, before, len,
-                                       sq.row0 + tok0, col, ntok) >> (4 * (lane >> 4));
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            s[i >> 2][i & 3] = (see >> (16 * (i >> 2) + (i & 3))) & 1u ? s[i >> 2][i & 3] : -__builtin_inff();
-        }
+      auto softmax = [&](const f32x4_t (&s)[2], uint32_t (&pb)[4]) {
         // against a lazily moved reference
         const float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
                                fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3]))) * c1;
@@ -988,52 +1012,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D>::T), (AtCfg<KB, VB, D>::WGS * AtC
           pb[i] = __builtin_bit_cast(uint32_t, x);
         }
       };
-      auto values = [&](AtBlock<C>& x, int blk, bool first, const f32x4_t (&s)[2], const uint32_t (&pb)[4]) {
-        // scales: dead tokens and bad pages to zero, held times 2^-vexp
-        uint32_t raw[4];
-        pair_scales(x, raw);
-        if (blk * 32 + 32 > len || x.bad) {
-          const int j0 = blk * 32 + 4 * (at_fresh(threadIdx.x & 63) >> 4);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = j0 + 16 * (i >> 1) + 2 * (i & 1);
-            const bool dead = (x.bad >> (i >> 1)) & 1u;
-            raw[i] &= (dead || j >= len ? 0u : 0xffffu) | (dead || j + 1 >= len ? 0u : 0xffff0000u);
-          }
-        }
-        uint32_t vs[4];
-        uint32_t big = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          vs[i] = at_mul(raw[i], at_pow2(vexp));
-          big = at_max_u16(vs[i], big);
-        }
-        big = big > (big << 16) ? big : big << 16;
-        if (__any(big > 0x7000ffffu) || (first && !__any(big > 0x2c00ffffu))) {
-          float top = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t bits = (raw[i >> 1] >> (16 * (i & 1))) & 0xffffu;
-            const uint64_t who = __ballot((bits & 0x7c00u) == 0x7c00u);
-            if ((who >> (16 * h)) & 0xffffu) {
-              // this token's value is no number: rows that see it become NaN, others stay
-              raw[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
-              if (s[i >> 2][i & 3] != -__builtin_inff()) l = __builtin_nanf("");
-            } else {
-              top = fmaxf(top, fabsf(half_bits_to_float(static_cast<uint16_t>(bits))));
-            }
-          }
-          int ne = static_cast<int>(__float_as_uint(kv_wave_max(top)) >> 23) - 127;
-          ne = at_uniform(ne < -15 ? -15 : ne);
-          if (ne > vexp || first) {
-            const float f = at_exp2(static_cast<float>(vexp - ne));
-            vexp = ne;
-#pragma unroll
-            for (int n = 0; n < CH; ++n) o[n] *= f;
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) vs[i] = at_mul(raw[i], at_pow2(vexp));
-        }
+      auto values = [&](AtBlock<C>& x, const uint32_t (&vs)[4], const uint32_t (&pb)[4]) {
         if constexpr (VB == 3) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -1087,29 +1066,80 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D>::T), (AtCfg<KB, VB, D>::WGS * AtC
         }
       };
 
-      bool first = true;
       {
         // the registers hold one block: its keys' make room for the next keys after the scores, its
         // values' after the sums
-        for (; blk < k1; blk += W) {
+        bool again = false;  // the block comes a second time, see below
+        while (blk < k1) {
           const bool more = blk + W < k1;
           AtBlock<C>& x = blk0;
           f32x4_t s[2];
-          uint32_t pb[4];
+          uint32_t pb[4], vs[4];
           const uint32_t bad = x.bad;
-          scores(x, blk, first, s);
+          scores(x, blk, s);
           if (more) {
             locate(x);
             load_k(x);
             if (blk + 2 * W < k1) look(blk + 2 * W);
           }
-          const uint32_t nbad = x.bad;
-          softmax(blk, s, pb);
-          x.bad = bad;
-          values(x, blk, first, s, pb);
+          uint32_t nbad = x.bad;
+          if (blk * 32 + 32 > cut) {
+            const int lane = at_fresh(threadIdx.x & 63), col = lane & 15;
+            const uint32_t see = at_seen(p, *reinterpret_cast<const int*>(smem + C::LIM + 4 * col), blk * 32, before, len,
+                                         sq.row0 + tok0, col, ntok) >> (4 * (lane >> 4));
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              s[i >> 2][i & 3] = (see >> (16 * (i >> 2) + (i & 3))) & 1u ? s[i >> 2][i & 3] : -__builtin_inff();
+          }
+          pair_scales(x, vs);
+          if (blk * 32 + 32 > len || bad) {  // as if 1: their weights are 0 (or, of a bad page, no numbers)
+            const int j0 = blk * 32 + 4 * (at_fresh(threadIdx.x & 63) >> 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int j = j0 + 16 * (i >> 1) + 2 * (i & 1);
+              const bool dead = (bad >> (i >> 1)) & 1u;
+              const uint32_t none = (dead || j >= len ? 0xffffu : 0u) | (dead || j + 1 >= len ? 0xffff0000u : 0u);
+              vs[i] = (vs[i] & ~none) | (0x3c003c00u & none);
+            }
+          }
+          // A block of values by either power of two is taken twice, for the loud ones and then for the
+          // others, what is not of the kind masked.
+          const bool apart = at_far(vs), once_more = apart && !again;
+          if (__builtin_expect(apart, 0)) {
+            uint32_t f[4] = {};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t bits = (vs[i >> 1] >> (16 * (i & 1))) & 0x7fffu, half = i & 1 ? 0xffff0000u : 0x0000ffffu;
+              const bool none = (__ballot(bits >= 0x7c00u) >> (16 * h)) & 0xffffu, loud = (__ballot(bits >= kAtLoud) >> (16 * h)) & 0xffffu;
+              const float y = s[i >> 2][i & 3];
+              // a token whose value is no number: rows that see it become NaN, others stay
+              l = none && y != -__builtin_inff() ? __builtin_nanf("") : l;
+              vs[i >> 1] &= none ? ~half : 0xffffffffu;
+              f[i >> 1] |= (loud ? at_pow2(kAtLoudExp) : at_pow2(kAtQuietExp)) & half;
+              s[i >> 2][i & 3] = loud != again ? y : -__builtin_inff();
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vs[i] = at_mul(vs[i], f[i]);
+            if (once_more) {  // its keys instead of the next ones; those are looked for again
+              look(blk);
+              locate(x);
+              load_k(x);
+              nbad = x.bad;
+              if (more) look(blk + W);
+            }
+          }
+          if (const int e = !apart ? 0 : again ? kAtQuietExp : kAtLoudExp; __builtin_expect(e != oexp, 0)) {
+            const float f = at_exp2(static_cast<float>(oexp - e));
+            oexp = e;
+#pragma unroll
+            for (int n = 0; n < CH; ++n) o[n] *= f;
+          }
+          softmax(s, pb);
+          values(x, vs, pb);
           x.bad = nbad;
-          if (more) load_v(x);
-          first = false;
+          if (more || once_more) load_v(x);
+          again = once_more;
+          if (!again) blk += W;
         }
       }
 
@@ -1128,7 +1158,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D>::T), (AtCfg<KB, VB, D>::WGS * AtC
       float top = kAtNone;
 #pragma unroll
       for (int x = 0; x < W; ++x) top = fmaxf(top, *reinterpret_cast<const float*>(smem + C::ML + 8 * (x * ROWS + col)));
-      f = mo == kAtNone ? 0.f : at_exp2(mo - top + static_cast<float>(vexp));
+      f = mo == kAtNone ? 0.f : at_exp2(mo - top + static_cast<float>(oexp));
       constexpr int OUT = C::NL * 16 * ROWS / T;  // sums of a thread per round
       constexpr int RND = CH / C::NL;
       static_assert(C::NL * 16 * ROWS % T == 0, "whole sums per thread");

@@ -10,8 +10,8 @@
 // A wave holds 16 R rows: their rotated queries and sums stay in its registers (R = 2 of D = 128: 223
 // of 256), and no sums are joined across waves.
 //
-// The powers of two by which scales are held are chosen per block from its scales alone, so that
-// the waves that decode parts of it agree without asking each other; they travel with the block.
+// The powers of two of a block's tokens (kv_attend.hpp) follow from its scales alone, so that the waves
+// that decode parts of it agree without asking each other; they travel with the block.
 //
 // Measured: two chunks of 2047 tokens over texts of 4095 to 8190, 8 key heads of 128 shared by 4 query
 // heads, 8-bit keys and 3-bit values (300 Gflop): kernel 513 us, join 15 us (traced), 458 us a call in a
@@ -51,7 +51,7 @@ struct AwCfg {
   static constexpr int WIDE = (KWIDE || VWIDE) ? 32768 : 0;
   static constexpr int TK = WIDE, TV = TK + 1024;
   static constexpr int C1 = TV + 1024, LIM = C1 + ROWS * 4, HDR = LIM + ROWS * 4;
-  static constexpr int BUF = HDR + 2 * NB * 16;
+  static constexpr int BUF = HDR + 2 * NB * 32;
   static constexpr int VOFF = NB * 2 * NS * 1024, BYTES = VOFF + NB * CH * 1024;  // of a buffer
   static constexpr int QP = D * 2 + 16;                       // padded row of q
   static constexpr int FR = D == 256 ? 8 : 16, FP = D + 1;    // rows of a wave that go out at a time, padded row
@@ -61,20 +61,13 @@ struct AwCfg {
   static_assert(NB * 2 * KP == 4 && NB * VP == 4, "four waves each");
 };
 
-// What a block of a buffer needs besides its values: 2^kexp of its halves' keys, vexp, and the
-// tokens whose value is no number.
+// What a block of a buffer needs besides its values. Keys and values: whether scales are out of the
+// range that enters as it is, and if so which tokens are loud (kv_attend.hpp); vbad: the tokens whose
+// value is no number.
 struct AwHeader {
-  float kf[2];
-  int32_t vexp;
-  uint32_t vbad;
+  uint32_t k[2];  // of a half: 0, or 1 << 16 and the loud ones of its 16 tokens
+  uint32_t vapart, vloud, vbad, pad[3];
 };
-
-// The power of two that brings scales near 1, if one is beyond 2^13, no number, or all are below
-// 2^-4; top: the largest finite one of the lane's. 2^-15 to 2^15.
-__device__ __forceinline__ int aw_exponent(float top) {
-  const int e = static_cast<int>(__float_as_uint(kv_wave_max(top)) >> 23) - 127;
-  return at_uniform(e < -15 ? -15 : e);
-}
 
 template <int KB, int VB, int D, int R>
 __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(AttendParams) {
@@ -234,66 +227,65 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
         dst = C::BUF + buf * C::BYTES + 16 * lane;
         if constexpr (decltype(role)::value) {
           dst += ((pb * 2 + sbk) * NS + kp * C::SPP) * 1024;
-          uint32_t z[C::KS], big = 0;
+          uint32_t z[C::KS], far = 0, most = 0;
 #pragma unroll
           for (int y = 0; y < C::KS; ++y) {
-            z[y] = (bad >> sbk) & 1u ? 0x7e007e00u : ks[y] | (static_cast<uint32_t>(ks[y]) << 16);  // scores of a bad page are NaN
-            // rows behind the last token hold anything: they have no say in the exponent
-            if (blk * 32 + 32 > len) z[y] = blk * 32 + 16 * sbk + (lane & 15) < len ? z[y] : 0u;
-            big = z[y] > big ? z[y] : big;
+            z[y] = (bad >> sbk) & 1u ? 0x7e00u : ks[y];  // scores of a bad page are NaN
+            // rows that hold no token hold anything: as if 1
+            if (blk * 32 + 32 > len) z[y] = blk * 32 + 16 * sbk + (lane & 15) < len ? z[y] : 0x3c00u;
+            far = z[y] - kAtLow > far ? z[y] - kAtLow : far;
+            most = (z[y] & 0x7fffu) > most ? z[y] & 0x7fffu : most;
           }
-          int e = 0;
-          if (__any(big > 0x7000ffffu) || !__any(big > 0x2c00ffffu)) {
-            float top = 0.f;
-#pragma unroll
-            for (int y = 0; y < C::KS; ++y)
-              if ((z[y] & 0x7c00u) != 0x7c00u) top = fmaxf(top, fabsf(half_bits_to_float(static_cast<uint16_t>(z[y]))));
-            e = aw_exponent(top);
+          mul[0] = C::KS == 2 && kp ? z[C::KS - 1] : z[0];
+          mul[0] |= mul[0] << 16;
+          uint32_t word = 0;
+          if (__any(far >= kAtSpan)) {
+            const uint32_t loud = at_loud(most);
+            mul[0] = at_mul(mul[0], (loud >> (lane & 15)) & 1u ? at_pow2(kAtLoudExp) : at_pow2(kAtQuietExp));
+            word = 0x10000u | loud;
           }
-          mul[0] = at_mul(C::KS == 2 && kp ? z[C::KS - 1] : z[0], at_pow2(e));
-          if (lane == 0) hdr->kf[sbk] = at_exp2(static_cast<float>(e));
+          if (lane == 0) hdr->k[sbk] = word;
         } else {
           dst += C::VOFF + (pb * CH + vp * C::EPP) * 1024;
-          uint32_t big = 0;  // mul: scales of tokens 2 i and 2 i + 1
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mul[i] = at_pack(vs[2 * i], vs[2 * i + 1]);
-          if (blk * 32 + 32 > len || bad) {
+          for (int i = 0; i < 4; ++i) mul[i] = at_pack(vs[2 * i], vs[2 * i + 1]);  // scales of tokens 2 i and 2 i + 1
+          if (blk * 32 + 32 > len || bad) {  // as if 1: their weights are 0 (or, of a bad page, no numbers)
             const int j0 = blk * 32 + 4 * h;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int j = j0 + 16 * (i >> 1) + 2 * (i & 1);
               const bool dead = (bad >> (i >> 1)) & 1u;
-              mul[i] &= (dead || j >= len ? 0u : 0xffffu) | (dead || j + 1 >= len ? 0u : 0xffff0000u);
+              const uint32_t none = (dead || j >= len ? 0xffffu : 0u) | (dead || j + 1 >= len ? 0xffff0000u : 0u);
+              mul[i] = (mul[i] & ~none) | (0x3c003c00u & none);
             }
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) big = at_max_u16(mul[i], big);
-          big = big > (big << 16) ? big : big << 16;
-          int e = 0;
-          uint32_t vbad = 0;
-          if (__any(big > 0x7000ffffu) || !__any(big > 0x2c00ffffu)) {
-            float top = 0.f;
+          uint32_t vapart = 0, vloud = 0, vbad = 0;
+          if (at_far(mul)) {
+            vapart = 1;
+            uint32_t f[4] = {};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const uint32_t bits = (mul[i >> 1] >> (16 * (i & 1))) & 0xffffu;
-              const uint64_t who = __ballot((bits & 0x7c00u) == 0x7c00u);
-              if (who != 0) {
+              const uint32_t bits = (mul[i >> 1] >> (16 * (i & 1))) & 0x7fffu;
+              // the lanes of a token's groups: 16 y to 16 y + 15 of tokens 4 y + (i & 3)
+              const uint64_t none = __ballot(bits >= 0x7c00u), who = __ballot(bits >= kAtLoud);
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                  if ((who >> (16 * y)) & 0xffffu) vbad |= 1u << (16 * (i >> 2) + 4 * y + (i & 3));
+              for (int y = 0; y < 4; ++y) {
+                const uint32_t bit = 1u << (16 * (i >> 2) + 4 * y + (i & 3));
+                if ((none >> (16 * y)) & 0xffffu) vbad |= bit;
+                if ((who >> (16 * y)) & 0xffffu) vloud |= bit;
               }
-              const bool drop = (who >> (16 * h)) & 0xffffu;
-              mul[i >> 1] &= !drop ? 0xffffffffu : (i & 1) ? 0x0000ffffu : 0xffff0000u;
-              top = drop ? top : fmaxf(top, fabsf(half_bits_to_float(static_cast<uint16_t>(bits))));
+              if ((none >> (16 * h)) & 0xffffu) mul[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
+              const uint32_t two = (who >> (16 * h)) & 0xffffu ? at_pow2(kAtLoudExp) : at_pow2(kAtQuietExp);
+              f[i >> 1] |= two & ((i & 1) ? 0xffff0000u : 0x0000ffffu);
             }
-            e = aw_exponent(top);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mul[i] = at_mul(mul[i], f[i]);
           }
           if (lane == 0) {
-            hdr->vexp = e;
+            hdr->vapart = vapart;
+            hdr->vloud = vloud;
             hdr->vbad = vbad;
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mul[i] = at_mul(mul[i], at_pow2(e));
           if constexpr (VB < 8) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) at_pair<VB>(vx[2 * i] >> vshift, vx[2 * i + 1] >> vshift, ev[i], od[i]);
@@ -366,7 +358,9 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
       cut = cut < 0 ? 0 : cut;
       const uint32_t hb_mul = p->hb_mul;
       const bool live = ((static_cast<uint32_t>(16 * wave) * hb_mul) >> 16) < static_cast<uint32_t>(ntok);
-      int vexp = 0;  // the sums are held times 2^-vexp
+
+      int oexp = 0;  // the sums are held times 2^-oexp
+      bool again = false, twice = false;  // see multiply
 
       // Scores, weights and sums of block x of the chunk. Pieces are read G at a time, AHEAD groups before
       // their products; z holds those on their way.
@@ -401,9 +395,8 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
           }
           __builtin_amdgcn_sched_barrier(0);
         }
-        const float2 kf = *reinterpret_cast<const float2*>(hdr->kf);
-        const int ve = at_uniform(hdr->vexp);
-        const uint32_t vbad = static_cast<uint32_t>(at_uniform(static_cast<int>(hdr->vbad)));
+        const u32x4_t hd = *reinterpret_cast<const u32x4_t*>(hdr);
+        const uint32_t apart = static_cast<uint32_t>(at_uniform(static_cast<int>(hd.x | hd.y | hd.z)));
         if (blk * 32 + 32 > cut) {
 #pragma unroll
           for (int r = 0; r < R; ++r) {
@@ -415,14 +408,40 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
               s[r][i >> 2][i & 3] = (see >> (16 * (i >> 2) + (i & 3))) & 1u ? s[r][i >> 2][i & 3] : -__builtin_inff();
           }
         }
-        float cf[R][2], mx[R];
+        if (__builtin_expect((apart | static_cast<uint32_t>(oexp) | (again ? 1u : 0u)) != 0, 0)) {
+          const uint32_t ka = static_cast<uint32_t>(at_uniform(static_cast<int>(hd.x))), kb = static_cast<uint32_t>(at_uniform(static_cast<int>(hd.y)));
+          const bool vapart = at_uniform(static_cast<int>(hd.z)) != 0;
+          // A block of values by either power of two is multiplied twice, for the loud ones and then for the
+          // others, what is not of the kind masked; beside it other blocks have nothing left the second time.
+          const uint2 hv = *reinterpret_cast<const uint2*>(&hdr->vloud);
+          const uint32_t vloud = static_cast<uint32_t>(at_uniform(static_cast<int>(hv.x))), vbad = static_cast<uint32_t>(at_uniform(static_cast<int>(hv.y)));
+          const uint32_t kind = (vapart ? (again ? ~vloud : vloud) : again ? 0u : ~0u) >> (4 * h), none = vapart ? vbad >> (4 * h) : 0u;
+          const int e = !vapart ? 0 : again ? kAtQuietExp : kAtLoudExp;
+          const float f = at_exp2(static_cast<float>(oexp - e));
+          oexp = e;
+          twice = twice || vapart;
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            if (ka) at_back(s[r][0], ka, h);
+            if (kb) at_back(s[r][1], kb, h);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int bit = 16 * (i >> 2) + (i & 3);
+              const float y = s[r][i >> 2][i & 3];
+              // tokens whose value is no number: rows that see one become NaN, others stay
+              l[r] = (none >> bit) & 1u && y != -__builtin_inff() ? __builtin_nanf("") : l[r];
+              s[r][i >> 2][i & 3] = at_pick(kind, bit, y, -__builtin_inff());
+            }
+#pragma unroll
+            for (int n = 0; n < CH; ++n) o[r][n] *= f;
+          }
+        }
+        float mx[R];
         bool move = false;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          cf[r][0] = c1[r] * kf.x;
-          cf[r][1] = c1[r] * kf.y;
-          mx[r] = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])) * cf[r][0],
-                        fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])) * cf[r][1]);
+          mx[r] = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
+                        fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3]))) * c1[r];
           move = move || mx[r] > mo[r] + (7.f + kAtLazy);
         }
         if (__any(move)) {
@@ -441,27 +460,12 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
             }
           }
         }
-        if (ve != vexp || vbad) {
-          const float f = at_exp2(static_cast<float>(vexp - ve));
-          vexp = ve;
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            // tokens whose value is no number: rows that see one become NaN, others stay
-            float y = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              y = (vbad >> (16 * (i >> 2) + 4 * h + (i & 3))) & 1u && s[r][i >> 2][i & 3] != -__builtin_inff() ? __builtin_nanf("") : y;
-            l[r] += y;
-#pragma unroll
-            for (int n = 0; n < CH; ++n) o[r][n] *= f;
-          }
-        }
         uint32_t pr[R][4];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           float e[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) e[i] = at_exp2(__builtin_fmaf(s[r][i >> 2][i & 3], cf[r][i >> 2], -mo[r]));
+          for (int i = 0; i < 8; ++i) e[i] = at_exp2(__builtin_fmaf(s[r][i >> 2][i & 3], c1[r], -mo[r]));
           l[r] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -508,8 +512,9 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
         plain();
         __syncthreads();
         int buf = 0;
-        for (int c = k0; c < k1; c += NB) {
-          begin(buf ^ 1);
+        for (int c = k0; c < k1;) {
+          if (__builtin_expect(!again, 1)) begin(buf ^ 1);
+          twice = false;
           if (live) {
             constexpr int SB = STEPS / NB, EVERY = BG / (2 * SB);
 #pragma unroll
@@ -525,8 +530,11 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
           } else {
             plain();
           }
+          again = twice && !again;
+          if (__builtin_expect(again, 0)) continue;  // the decoding's steps then do again what they did
           __syncthreads();
           buf ^= 1;
+          c += NB;
         }
       };
       if (keys) rounds(AtInt<1>{});
@@ -540,7 +548,7 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
       const bool whole = k0 == 0 && k1 == nblk;
       float* const slot = p->parts + static_cast<int64_t>(2 * wg + (k0 > 0 ? 0 : 1)) * C::ROWS * (D + 2);
       float* const red = reinterpret_cast<float*>(smem + C::BUF) + wave * C::FR * C::FP;
-      const float fv = at_exp2(static_cast<float>(vexp));
+      const float fo = at_exp2(static_cast<float>(oexp));
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float x, y;
@@ -554,7 +562,7 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
 #pragma unroll
             for (int n = 0; n < CH; ++n)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) red[(col - r1) * C::FP + CH * (4 * h + i) + n] = o[r][n][i] * fv;
+              for (int i = 0; i < 4; ++i) red[(col - r1) * C::FP + CH * (4 * h + i) + n] = o[r][n][i] * fo;
           wave_lds_sync();
 #pragma unroll 1
           for (int z0 = r1; z0 < r1 + C::FR; z0 += RN) {
