@@ -64,6 +64,11 @@ constexpr int kAtMinShare = 512;
 // 8 14.8 and 15.5, 16 16.7 and 20.5)
 constexpr int kAtMinBlocks = 4;
 constexpr float kAtLazy = 8.f;          // log2 of how far a score may pass the reference
+// Exponents are one fused operation, score times factor minus reference. The reference was rounded, the
+// fused product is not: from 2^28 on half a step of fp32 between them would take weights out of fp16. From
+// this size on a row's factor is cut to a power of two, whose products are exact. (That scales score
+// differences by up to 2, where the fp16 operands leave the scores themselves off by 2^-11 of 2^25.)
+constexpr float kAtHuge = 0x1p25f;
 constexpr float kAtNone = -3e38f;       // reference of a row that has seen nothing
 // fp16 bits of scales: they enter as they are from kAtLow up to below kAtLow + kAtSpan (2^-12, 2^13). In a
 // block with others, tokens whose largest scale is from kAtLoud (2^-4) on are held times 2^-6, the rest
@@ -172,6 +177,22 @@ __device__ __forceinline__ T at_get(AtPtr base, uint32_t off) {
 __device__ __forceinline__ int at_fresh(int x) {
   asm volatile("" : "+v"(x));
   return x;
+}
+// A row's softmax reference: mo, 7 below the score it was set by, in units of the factor fc; c1 is the
+// row's own factor, which fc is unless the scores are huge.
+__device__ __forceinline__ float at_ratio(float c1) {  // c1 over its power of two
+  return __uint_as_float((__float_as_uint(c1) & 0x007fffffu) | 0x3f800000u);
+}
+__device__ __forceinline__ float at_reference(float c1, float fc, float mo) {  // mo in units of c1
+  return fc == c1 ? mo : mo * at_ratio(c1);
+}
+// To the score x; what was summed so far is to be multiplied by the result.
+__device__ __forceinline__ float at_refer(float x, float c1, float& fc, float& mo) {
+  const float t = x * c1, old = at_reference(c1, fc, mo);
+  const bool huge = fabsf(t) > kAtHuge;
+  fc = huge ? __uint_as_float(__float_as_uint(c1) & 0x7f800000u) : c1;
+  mo = x * fc - 7.f;
+  return at_exp2(fminf(old - (huge ? t - 7.f : mo), 0.f));
 }
 // a load at any byte address
 template <typename T>
@@ -918,9 +939,9 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D>::T), (AtCfg<KB, VB, D>::WGS * AtC
       int cut = masked ? before : before + tok0 + 1;
       cut = cut < 0 ? 0 : cut;
 
-      const float c1 = *reinterpret_cast<const float*>(smem + C::C1 + 4 * col);  // score factor
-      int oexp = 0;                                                              // the sums are held times 2^-oexp
+      float fc = *reinterpret_cast<const float*>(smem + C::C1 + 4 * col);  // score factor
       float mo = kAtNone, l = 0.f;                                         // reference - 7; sum
+      int oexp = 0;                                                        // the sums are held times 2^-oexp
       f32x4_t o[CH];
 #pragma unroll
       for (int n = 0; n < CH; ++n) o[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -988,15 +1009,15 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D>::T), (AtCfg<KB, VB, D>::WGS * AtC
       auto softmax = [&](const f32x4_t (&s)[2], uint32_t (&pb)[4]) {
         // against a lazily moved reference
         const float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                               fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3]))) * c1;
-        if (__any(mx > mo + (7.f + kAtLazy))) {
+                               fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+        if (__any(__builtin_fmaf(mx, fc, -mo) > 7.f + kAtLazy)) {
+          const float c1 = *reinterpret_cast<const float*>(smem + C::C1 + 4 * col);
           float x, y;
           kv_both<4>(mx, x, y);
           kv_both<5>(fmaxf(x, y), x, y);
           x = fmaxf(x, y);
-          if (x > mo + (7.f + kAtLazy)) {  // the same in the four lanes of a row
-            const float f = at_exp2(mo + 7.f - x);
-            mo = x - 7.f;
+          if (__builtin_fmaf(x, fc, -mo) > 7.f + kAtLazy) {  // the same in the four lanes of a row
+            const float f = at_refer(x, c1, fc, mo);
             l *= f;
 #pragma unroll
             for (int n = 0; n < CH; ++n) o[n] *= f;
@@ -1004,7 +1025,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D>::T), (AtCfg<KB, VB, D>::WGS * AtC
         }
         float e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = at_exp2(__builtin_fmaf(s[i >> 2][i & 3], c1, -mo));
+        for (int i = 0; i < 8; ++i) e[i] = at_exp2(__builtin_fmaf(s[i >> 2][i & 3], fc, -mo));
         l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -1151,6 +1172,7 @@ __global__ __launch_bounds__((AtCfg<KB, VB, D>::T), (AtCfg<KB, VB, D>::WGS * AtC
       kv_both<4>(l, x, y);
       kv_both<5>(x + y, x, y);
       l = x + y;
+      mo = at_reference(*reinterpret_cast<const float*>(smem + C::C1 + 4 * col), fc, mo);
       if (h == 0)
         *reinterpret_cast<float2*>(smem + C::ML + 8 * (wave * ROWS + col)) = make_float2(mo, l);
       __syncthreads();

@@ -329,7 +329,7 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
         look(next_of(blk));
       }
       uint32_t q[R][NS][4];
-      float c1[R], mo[R], l[R];  // score factor; reference - 7; sum
+      float fc[R], mo[R], l[R];  // score factor; reference - 7; sum
       f32x4_t o[R][CH];
       __syncthreads();  // the last unit's readers of this memory are done
 #pragma unroll
@@ -346,7 +346,7 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
           const u32x4_t x = *reinterpret_cast<const u32x4_t*>(smem + at + col * C::QP + (D / 2) * h + 16 * st);
           q[r][st][0] = x.x; q[r][st][1] = x.y; q[r][st][2] = x.z; q[r][st][3] = x.w;
         }
-        c1[r] = *reinterpret_cast<const float*>(smem + C::C1 + 4 * (r0 + col));
+        fc[r] = *reinterpret_cast<const float*>(smem + C::C1 + 4 * (r0 + col));
         mo[r] = kAtNone;
         l[r] = 0.f;
 #pragma unroll
@@ -441,19 +441,19 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           mx[r] = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
-                        fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3]))) * c1[r];
-          move = move || mx[r] > mo[r] + (7.f + kAtLazy);
+                        fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])));
+          move = move || __builtin_fmaf(mx[r], fc[r], -mo[r]) > 7.f + kAtLazy;
         }
-        if (__any(move)) {
+        if (__builtin_expect(__any(move), 0)) {
 #pragma unroll
           for (int r = 0; r < R; ++r) {
+            const float c1 = *reinterpret_cast<const float*>(smem + C::C1 + 4 * (16 * (wave + W * r) + (lane & 15)));
             float y, w;
             kv_both<4>(mx[r], y, w);
             kv_both<5>(fmaxf(y, w), y, w);
             y = fmaxf(y, w);
-            if (y > mo[r] + (7.f + kAtLazy)) {  // the same in the four lanes of a row
-              const float f = at_exp2(mo[r] + 7.f - y);
-              mo[r] = y - 7.f;
+            if (__builtin_fmaf(y, fc[r], -mo[r]) > 7.f + kAtLazy) {  // the same in the four lanes of a row
+              const float f = at_refer(y, c1, fc[r], mo[r]);
               l[r] *= f;
 #pragma unroll
               for (int n = 0; n < CH; ++n) o[r][n] *= f;
@@ -465,7 +465,7 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
         for (int r = 0; r < R; ++r) {
           float e[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) e[i] = at_exp2(__builtin_fmaf(s[r][i >> 2][i & 3], c1[r], -mo[r]));
+          for (int i = 0; i < 8; ++i) e[i] = at_exp2(__builtin_fmaf(s[r][i >> 2][i & 3], fc[r], -mo[r]));
           l[r] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -555,6 +555,7 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
         kv_both<4>(l[r], x, y);
         kv_both<5>(x + y, x, y);
         l[r] = x + y;
+        mo[r] = at_reference(*reinterpret_cast<const float*>(smem + C::C1 + 4 * (16 * (wave + W * r) + col)), fc[r], mo[r]);
 #pragma unroll
         for (int r1 = 0; r1 < 16; r1 += C::FR) {
           wave_lds_sync();

@@ -134,7 +134,7 @@ def test_loud_tokens_hidden_by_a_tree_cost_the_others_nothing(D, n, share, low, 
     check_rows(out, bt, q, counts, D ** -0.5, 0, rows, tree)
 
 
-@pytest.mark.parametrize("low,high,size", SPREADS[:2])
+@pytest.mark.parametrize("low,high,size", SPREADS)
 @pytest.mark.parametrize("at", [[3], [70, 71, 200, 333], [LONG - 2]])
 @pytest.mark.parametrize("n,share", ROWS)
 @pytest.mark.parametrize("D", [64, 128, 256])
