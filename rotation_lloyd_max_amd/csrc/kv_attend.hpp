@@ -49,6 +49,7 @@
 // ids, codes and join.
 #pragma once
 
+#include "exact_div.hpp"
 #include "internal.hpp"
 #include "kv_lane.hpp"
 
@@ -210,12 +211,9 @@ __device__ __forceinline__ int at_div(int x, int d, uint32_t mul) {
   return static_cast<int>(y);
 }
 
-// ceil(x / d) for 0 < x < 2^27, d >= 1: an fp32 quotient, at most one off, put right
+// ceil(x / d) for 0 < x <= 2^27, 1 <= d <= 2^27
 __device__ __forceinline__ int at_ceil_div(int x, int d) {
-  int y = static_cast<int>(static_cast<float>(x) * __builtin_amdgcn_rcpf(static_cast<float>(d)));
-  y -= static_cast<int64_t>(y) * d >= x ? 1 : 0;
-  y += static_cast<int64_t>(y + 1) * d <= x - 1 ? 1 : 0;
-  return y + 1;
+  return ceil_div_by(x, d, __builtin_amdgcn_rcpf(static_cast<float>(d)));
 }
 
 // ---- work ---------------------------------------------------------------------------------
