@@ -81,6 +81,12 @@ def _as(t, dtype, device, name, shape=None):
     return t if t.is_contiguous() else t.contiguous()
 
 
+def _no_gradient(name, *tensors):
+    """The library's calls are outside autograd: refuse rather than return a detached result."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(f"{name} records no gradient: call it on detached tensors or under torch.no_grad()")
+
+
 @dataclass
 class Rope:
     """Rotary positions: inv_freq float64 [rot_dim / 2] on the device (radians per position),
@@ -138,7 +144,10 @@ def _overlaps_itself(t):
 def rope(x, positions, rope, transposed=False, out=None):
     """x ([tokens, heads, head_dim], the elements of a head contiguous, any token and head
     strides) with rotary positions applied. out=x turns it in place; another out= must not
-    overlap x. transposed: the negative angle (the gradient of the call)."""
+    overlap x. transposed: the negative angle (the gradient of the call). Not recorded by
+    autograd: refused where x requires grad, unless under torch.no_grad() (as in the forward of an
+    autograd.Function, whose backward is the transposed call)."""
+    _no_gradient("rope", x, out)
     xs = _head_strides(x, "x")
     dev = x.device
     positions = _as(positions, torch.int32, dev, "positions", (x.shape[0],))
@@ -267,7 +276,9 @@ def kv_attend(cache, q, kv_lens, page_table, q_offsets=None, tree=None, scale=No
     each). Causal, or with tree (int32 words [M, words]) bit j of a row's mask for each of the
     sequence's own tokens j. scale: 1 / sqrt(head_dim) by default. Returns [M, q_heads,
     head_dim] in out_dtype (q's by default); rows behind q_offsets[B] are not written (without
-    out= they hold whatever the memory held)."""
+    out= they hold whatever the memory held). Not recorded by autograd: refused where q requires
+    grad, unless under torch.no_grad()."""
+    _no_gradient("kv_attend", q, out)
     dev = cache.device
     if q.dim() != 3 or q.shape[2] != cache.head_dim:
         raise ValueError(f"q must be [M, q_heads, {cache.head_dim}]")
