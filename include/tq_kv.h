@@ -91,8 +91,8 @@ int tq_kv_store(const tq_kv_cache *cache, const void *k, const void *v, tq_dtype
 
 /* Reads tokens back: k_out[t][h] = the dequantized, rotated-back key of slots[t] (v_out the
  * value), device [tokens][heads][K] of `dtype`, contiguous, 16-byte aligned; either may be
- * NULL. A slot outside [0, E * page_tokens) gives NaN rows; slots may repeat. Computed in fp32
- * and rounded once, as tq_kv_fetch. Workspace: none. */
+ * NULL, and they may not overlap. A slot outside [0, E * page_tokens) gives NaN rows; slots
+ * may repeat. Computed in fp32 and rounded once, as tq_kv_fetch. Workspace: none. */
 int tq_kv_load(const tq_kv_cache *cache, const int64_t *slots, int64_t tokens, void *k_out,
                void *v_out, tq_dtype dtype, void *stream);
 
@@ -118,7 +118,8 @@ int tq_kv_load(const tq_kv_cache *cache, const int64_t *slots, int64_t tokens, v
  *   page_table   device int32 [B][table_width]; entries behind a sequence's last page are not
  *                read; a page outside [0, E) makes the rows that see its tokens NaN
  *   tree         device uint32 [M][tree_words], or NULL
- *   out          device [M][q_heads][K], bf16 or fp16 (its own dtype), contiguous, 16-byte aligned
+ *   out          device [M][q_heads][K], bf16 or fp16 (its own dtype), contiguous, 16-byte aligned; it
+ *                may be q (with q's dtype and q_token_stride = q_heads * K), not overlap it otherwise
  * Scores, softmax statistics and sums are fp32; the operands of the matrix cores (rotated
  * q, centroids, p, decoded values) are fp16, scaled so that none overflows and so that no token's
  * scales, seen or not, take bits from another's: a token's part of an output is off by some 2^-11

@@ -141,6 +141,39 @@ def _overlaps_itself(t):
     return inner < d or outer < inner * (count - 1) + d
 
 
+def _span(t):
+    """(first, last + 1) byte that the elements of t lie between."""
+    n = 1 + sum((d - 1) * s for d, s in zip(t.shape, t.stride())) if t.numel() else 0
+    return t.data_ptr(), t.data_ptr() + n * t.element_size()
+
+
+def _apart(a, b):
+    """Whether the memory between a's first and last element and that of b's do not meet."""
+    (a0, a1), (b0, b1) = _span(a), _span(b)
+    return a1 <= b0 or b1 <= a0
+
+
+def _vectors_meet(x, y):
+    """Whether a (token, head) vector of x and one of y, of one shape and type, share a byte."""
+    (n, h, d), size = x.shape, x.element_size()
+    if _apart(x, y):
+        return False
+    width, step, first = d * size, y.data_ptr() - x.data_ptr(), lambda t: tuple(s * size for s in t.stride()[:2])
+    (xt, xh), (yt, yh) = first(x), first(y)
+    if (n == 1 or xt == yt) and (h == 1 or xh == yh):
+        # one grid moved by `step`: the differences of its vectors' places, i tokens and j heads
+        j = step + np.arange(1 - h, h, dtype=np.int64) * xh
+        i = np.clip(-j // xt, 1 - n, n - 1) if xt else np.zeros_like(j)
+        near = np.minimum(np.abs(j + i * xt), np.abs(j + np.minimum(i + 1, n - 1) * xt))
+        return bool((near < width).any())
+    a = np.sort((np.arange(n, dtype=np.int64)[:, None] * xt + np.arange(h, dtype=np.int64) * xh).ravel())
+    b = (step + np.arange(n, dtype=np.int64)[:, None] * yt + np.arange(h, dtype=np.int64) * yh).ravel()
+    k = np.searchsorted(a, b)
+    above = a[np.minimum(k, len(a) - 1)] - b
+    below = b - a[np.maximum(k - 1, 0)]
+    return bool(((np.abs(above) < width) | (np.abs(below) < width)).any())
+
+
 def rope(x, positions, rope, transposed=False, out=None):
     """x ([tokens, heads, head_dim], the elements of a head contiguous, any token and head
     strides) with rotary positions applied. out=x turns it in place; another out= must not
@@ -159,6 +192,8 @@ def rope(x, positions, rope, transposed=False, out=None):
         raise ValueError("out= must have x's shape, dtype and device")
     elif _overlaps_itself(out):
         raise ValueError("out= must not overlap itself")
+    elif (out.data_ptr() != x.data_ptr() or out.stride() != x.stride()) and x.dim() == 3 and _vectors_meet(x, out):
+        raise ValueError("out= must be x itself or not overlap it")
     os_ = _head_strides(out, "out")
     r = rope.desc(dev)
     _call(dev, _tq.lib().tq_rope, x.data_ptr(), _tq._dt(x), x.shape[0], x.shape[1], x.shape[2],
@@ -253,6 +288,8 @@ def kv_load(cache, slots, out_dtype=torch.bfloat16, k_out=None, v_out=None, keys
         v = torch.empty_like(k) if keys and k_out is None and v_out is None else _tq._out(v_out, shape, out_dtype, dev)
     else:
         v = None
+    if k_out is not None and v_out is not None and keys and values and not _apart(k, v):
+        raise ValueError("k_out= and v_out= must not overlap")
     if out_dtype not in _tq._DT:
         raise TypeError(f"unsupported dtype {out_dtype}")
     _call(dev, _tq.lib().tq_kv_load, cache.desc, slots.data_ptr(), shape[0],
@@ -275,7 +312,7 @@ def kv_attend(cache, q, kv_lens, page_table, q_offsets=None, tree=None, scale=No
     them its queries' own; q_offsets [B + 1] bounds the sequences' rows of q (None: M / B rows
     each). Causal, or with tree (int32 words [M, words]) bit j of a row's mask for each of the
     sequence's own tokens j. scale: 1 / sqrt(head_dim) by default. Returns [M, q_heads,
-    head_dim] in out_dtype (q's by default); rows behind q_offsets[B] are not written (without
+    head_dim] in out_dtype (q's by default; out= may be q itself, and must not overlap it otherwise); rows behind q_offsets[B] are not written (without
     out= they hold whatever the memory held). Not recorded by autograd: refused where q requires
     grad, unless under torch.no_grad()."""
     _no_gradient("kv_attend", q, out)
@@ -311,6 +348,9 @@ def kv_attend(cache, q, kv_lens, page_table, q_offsets=None, tree=None, scale=No
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError(f"out= must be {out_dtype}")
         out = _tq._out(out, (M, H, D), out.dtype, dev)
+        same = out.data_ptr() == q.data_ptr() and out.dtype == q.dtype and q.is_contiguous()
+        if not same and not _apart(out, q):
+            raise ValueError("out= must be q itself (contiguous, of its type) or not overlap it")
     nbytes = kv_attend_workspace(cache, H, B, M)
     if ws is None:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None

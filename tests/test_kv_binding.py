@@ -51,3 +51,65 @@ def test_gradients_are_not_lost_in_silence():
 
     with pytest.raises(ValueError, match=NOT_A_GPU):
         Turn.apply(x)
+
+
+def brute_force(x, y):
+    def places(t):
+        f = torch.arange(1 << 14)
+        start = (t.data_ptr() - base.data_ptr()) // base.element_size()
+        return set(f.as_strided(t.shape, t.stride(), start).flatten().tolist())
+    base = x._base if x._base is not None else x
+    return bool(places(x) & places(y))
+
+
+def test_vectors_that_meet_are_found():
+    # every pair of views of one buffer against the sets of their elements
+    import itertools
+    buf = torch.zeros(1 << 14)
+    views = []
+    for n, h, d in ((3, 2, 4), (1, 3, 8), (4, 1, 6)):
+        group = []
+        for ts, hs in ((32, 8), (8, 40), (16, 4), (6, 64), (100, 6), (d, n * d), (0, d)):
+            for off in (0, 1, 3, 4, 8, 12, 20, 31, 64, 130):
+                group.append(buf.as_strided((n, h, d), (ts, hs, 1), off))
+        views.append(group)
+    met = 0
+    for group in views:
+        for x, y in itertools.product(group, group):
+            want = brute_force(x, y)
+            met += want
+            assert tq.kv._vectors_meet(x, y) == want, (x.shape, x.stride(), x.storage_offset(), y.stride(), y.storage_offset())
+    assert 0 < met < sum(len(g) ** 2 for g in views)
+
+
+def test_rope_outputs_that_overlap_the_input_in_part():
+    wide = torch.zeros((5, 12, 64), dtype=torch.bfloat16)
+    x = wide[1:3, 2:6]
+    for bad in (wide[1:3, 3:7], wide[2:4, 2:6], wide[0:2, 4:8], wide.view(-1)[1 * 768 + 2 * 64 + 8:].as_strided((2, 4, 64), (768, 64, 1)),
+                wide.as_strided((2, 4, 64), (64, 768, 1), 768 + 5 * 64)):
+        with pytest.raises(ValueError, match="overlap"):
+            turn(x, out=bad)
+    for good in (x, wide[1:3, 6:10], wide[3:5, 2:6], wide[1:3, 2:6].clone(), wide[0:1].view(-1)[:512].view(2, 4, 64)):
+        with pytest.raises(ValueError, match=NOT_A_GPU):
+            turn(x, out=good)
+
+
+def test_load_outputs_that_overlap():
+    c, slots = cache(), torch.zeros(3, dtype=torch.int64)
+    buf = torch.zeros((6, 2, 64), dtype=torch.bfloat16)
+    for k, v in ((buf[:3], buf[:3]), (buf[:3], buf[2:5])):
+        with pytest.raises(ValueError, match="overlap"):
+            tq.kv_load(c, slots, k_out=k, v_out=v)
+    with pytest.raises(ValueError, match=NOT_A_GPU):
+        tq.kv_load(c, slots, k_out=buf[:3], v_out=buf[3:])
+
+
+def test_attention_outputs_that_overlap_the_queries_in_part():
+    buf = torch.zeros((8, 4, 64), dtype=torch.bfloat16)
+    wide = torch.zeros((3, 8, 64), dtype=torch.bfloat16)
+    for q, out in ((buf[:3], buf[1:4]), (wide[:, :4], wide.view(-1)[:768].view(3, 4, 64)), (buf[:3], buf[:3].view(torch.float16))):
+        with pytest.raises(ValueError, match="overlap"):
+            attend(q, out=out)
+    for q, out in ((buf[:3], buf[:3]), (buf[:3], buf[3:6])):
+        with pytest.raises(ValueError, match=NOT_A_GPU):
+            attend(q, out=out)
