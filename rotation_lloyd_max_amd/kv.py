@@ -69,7 +69,9 @@ else:
 
 
 def _as(t, dtype, device, name, shape=None):
-    """t as a contiguous tensor of dtype on device (the call's index arrays)."""
+    """t as a contiguous tensor of dtype on device (the call's index arrays). Values that dtype does not
+    hold become its nearest: a page or a length far outside stays outside, where plain conversion
+    would wrap it to another page's."""
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
     if shape is not None and tuple(t.shape) != shape:
@@ -77,6 +79,11 @@ def _as(t, dtype, device, name, shape=None):
     if t.dtype != dtype:
         if t.dtype.is_floating_point or t.dtype.is_complex or t.dtype == torch.bool:
             raise TypeError(f"{name} must hold integers, got {t.dtype}")
+        if t.dtype == torch.uint64:     # (from 2^63 on it would turn negative; elementwise calls do not take it)
+            t = t.view(torch.int64)
+            t = torch.where(t < 0, torch.iinfo(torch.int64).max, t)
+        if dtype == torch.int32 and t.dtype in (torch.int64, torch.uint32):
+            t = t.to(torch.int64).clamp(-2 ** 31, 2 ** 31 - 1)
         t = t.to(dtype)
     return t if t.is_contiguous() else t.contiguous()
 

@@ -31,3 +31,19 @@ def test_rope_into_a_neighbouring_slice(dt):
     want[:, 6:10] = tq.rope(wide[:, 2:6].clone(), pos, r)
     tq.rope(wide[:, 2:6], pos, r, out=wide[:, 6:10])
     assert torch.equal(wide, want)
+
+
+def test_wide_index_values_do_not_wrap():
+    # 64-bit pages and lengths: 2^32 + p is no page p, 2^32 + 16 is a length beyond the table
+    bt = Batch([40, 48], heads=1, D=64, page=16, kg=32)
+    q = queries(2, 2, 64, torch.bfloat16)
+    lens, table = (t.to(torch.int64) for t in bt.dev())
+    want = run(bt, q)
+    assert torch.equal(tq.kv_attend(bt.cache, q, lens, table), want)
+    bad = table.clone()
+    bad[0, 1] += 2 ** 32
+    got = tq.kv_attend(bt.cache, q, lens, bad)
+    assert torch.isnan(got[0]).all() and torch.equal(got[1], want[1])
+    far = lens.clone()
+    far[1] = 2 ** 32 + 16
+    assert torch.equal(tq.kv_attend(bt.cache, q, far, table), want)

@@ -113,3 +113,17 @@ def test_attention_outputs_that_overlap_the_queries_in_part():
     for q, out in ((buf[:3], buf[:3]), (buf[:3], buf[3:6])):
         with pytest.raises(ValueError, match=NOT_A_GPU):
             attend(q, out=out)
+
+
+@pytest.mark.parametrize("dt", [torch.int64, torch.uint32, torch.uint64])
+def test_index_values_beyond_their_type_stay_outside(dt):
+    cpu = torch.device("cpu")
+    values = [0, 5, 2 ** 31 - 1, 2 ** 31, 2 ** 32 - 1] + ([2 ** 32 + 3, 2 ** 40] if dt != torch.uint32 else []) + \
+             ([-1, -2 ** 31 - 1, -2 ** 32 + 1] if dt == torch.int64 else []) + ([2 ** 64 - 1] if dt == torch.uint64 else [])
+    t = torch.tensor(values, dtype=dt)
+    got = tq.kv._as(t, torch.int32, cpu, "x", (len(values),))
+    assert got.dtype == torch.int32 and got.tolist() == [max(-2 ** 31, min(2 ** 31 - 1, v)) for v in values]
+    got = tq.kv._as(t, torch.int64, cpu, "x")
+    assert got.dtype == torch.int64 and got.tolist() == [min(2 ** 63 - 1, v) for v in values]
+    small = tq.kv._as(torch.tensor([-3, 7], dtype=torch.int16), torch.int32, cpu, "x")
+    assert small.dtype == torch.int32 and small.tolist() == [-3, 7]
