@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeAngles = 512;  // cosines and sines a workgroup holds
+constexpr int64_t kRopeBlocks = 1 << 23;  // workgroups of a launch, at most: 2^32 threads wrap around
 
 struct RopeParams {
   const char* x;
@@ -25,11 +26,6 @@ struct RopeParams {
   int heads, D, rot, tpb, hpb;         // tokens and heads of a workgroup
   double gain;
   bool transposed, copy;  // copy: elements from rot on are copied (not in place)
-};
-
-template <int DT, int V>
-struct RopeVec {
-  float f[V];
 };
 
 template <int DT, int V>
@@ -153,11 +149,8 @@ hipError_t launch_rope(const void* x, int dt, int64_t tokens, int heads, int D, 
                        int64_t xhs, const RopeArgs& r, bool transposed, void* out, int64_t ots,
                        int64_t ohs, hipStream_t s) {
   RopeParams p{};
-  p.x = static_cast<const char*>(x);
-  p.out = static_cast<char*>(out);
-  p.positions = r.positions;
   p.inv_freq = r.inv_freq;
-  p.tokens = tokens; p.xts = xts; p.xhs = xhs; p.ots = ots; p.ohs = ohs;
+  p.xts = xts; p.xhs = xhs; p.ots = ots; p.ohs = ohs;
   p.heads = heads; p.D = D; p.rot = r.rot;
   p.gain = r.gain;
   p.transposed = transposed;
@@ -175,13 +168,22 @@ hipError_t launch_rope(const void* x, int dt, int64_t tokens, int heads, int D, 
   const int64_t nb = (tokens + tpb - 1) / tpb;
   while (hpb > 4 && nb * ((heads + hpb - 1) / hpb) < 256) hpb = (hpb + 1) / 2;
   p.hpb = hpb;
-  const dim3 grid(static_cast<uint32_t>(nb), (heads + hpb - 1) / hpb);
-  switch (dt) {
-    case 0: rope_run<0>(p, vec, r.interleaved, grid, s); break;
-    case 1: rope_run<1>(p, vec, r.interleaved, grid, s); break;
-    default: rope_run<2>(p, vec, r.interleaved, grid, s); break;
+  const int size = dt == 0 ? 4 : 2;
+  for (int64_t b0 = 0; b0 < nb; b0 += kRopeBlocks) {
+    const int64_t t0 = b0 * tpb, n = nb - b0 < kRopeBlocks ? nb - b0 : kRopeBlocks;
+    p.x = static_cast<const char*>(x) + t0 * xts * size;
+    p.out = static_cast<char*>(out) + t0 * ots * size;
+    p.positions = r.positions + t0;
+    p.tokens = tokens - t0 < n * tpb ? tokens - t0 : n * tpb;
+    const dim3 grid(static_cast<uint32_t>(n), (heads + hpb - 1) / hpb);
+    switch (dt) {
+      case 0: rope_run<0>(p, vec, r.interleaved, grid, s); break;
+      case 1: rope_run<1>(p, vec, r.interleaved, grid, s); break;
+      default: rope_run<2>(p, vec, r.interleaved, grid, s); break;
+    }
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace tq
