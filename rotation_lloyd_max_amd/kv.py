@@ -88,9 +88,9 @@ def _as(t, dtype, device, name, shape=None):
     return t if t.is_contiguous() else t.contiguous()
 
 
-def _no_gradient(name, *tensors):
+def _no_gradient(name):
     """The library's calls are outside autograd: refuse rather than return a detached result."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+    if torch.is_grad_enabled():
         raise ValueError(f"{name} records no gradient: call it on detached tensors or under torch.no_grad()")
 
 
@@ -187,7 +187,8 @@ def rope(x, positions, rope, transposed=False, out=None):
     overlap x. transposed: the negative angle (the gradient of the call). Not recorded by
     autograd: refused where x requires grad, unless under torch.no_grad() (as in the forward of an
     autograd.Function, whose backward is the transposed call)."""
-    _no_gradient("rope", x, out)
+    if x.requires_grad or out is not None and out.requires_grad:
+        _no_gradient("rope")
     xs = _head_strides(x, "x")
     dev = x.device
     positions = _as(positions, torch.int32, dev, "positions", (x.shape[0],))
@@ -195,13 +196,15 @@ def rope(x, positions, rope, transposed=False, out=None):
         out = torch.empty_like(x)  # (half a microsecond less than torch.empty)
         if not out.is_contiguous():
             out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        os_ = out.stride()
     elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev:
         raise ValueError("out= must have x's shape, dtype and device")
     elif _overlaps_itself(out):
         raise ValueError("out= must not overlap itself")
-    elif (out.data_ptr() != x.data_ptr() or out.stride() != x.stride()) and x.dim() == 3 and _vectors_meet(x, out):
+    elif (out.data_ptr() != x.data_ptr() or out.stride() != x.stride()) and _vectors_meet(x, out):
         raise ValueError("out= must be x itself or not overlap it")
-    os_ = _head_strides(out, "out")
+    else:
+        os_ = _head_strides(out, "out")
     r = rope.desc(dev)
     _call(dev, _tq.lib().tq_rope, x.data_ptr(), _tq._dt(x), x.shape[0], x.shape[1], x.shape[2],
           xs[0], xs[1], positions.data_ptr(), r, _TRANSPOSED if transposed else 0, out.data_ptr(),
@@ -322,7 +325,8 @@ def kv_attend(cache, q, kv_lens, page_table, q_offsets=None, tree=None, scale=No
     head_dim] in out_dtype (q's by default; out= may be q itself, and must not overlap it otherwise); rows behind q_offsets[B] are not written (without
     out= they hold whatever the memory held). Not recorded by autograd: refused where q requires
     grad, unless under torch.no_grad()."""
-    _no_gradient("kv_attend", q, out)
+    if q.requires_grad or out is not None and out.requires_grad:
+        _no_gradient("kv_attend")
     dev = cache.device
     if q.dim() != 3 or q.shape[2] != cache.head_dim:
         raise ValueError(f"q must be [M, q_heads, {cache.head_dim}]")
