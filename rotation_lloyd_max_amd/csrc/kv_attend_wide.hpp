@@ -22,6 +22,7 @@
 // 6007: 32.5 + 9.6 us, 28 of them set-up and join.
 #pragma once
 
+#include <cstddef>
 #include <type_traits>
 
 #include "encode_lane.hpp"
@@ -51,7 +52,7 @@ struct AwCfg {
   static constexpr int WIDE = (KWIDE || VWIDE) ? 32768 : 0;
   static constexpr int TK = WIDE, TV = TK + 1024;
   static constexpr int C1 = TV + 1024, LIM = C1 + ROWS * 4, HDR = LIM + ROWS * 4;
-  static constexpr int BUF = HDR + 2 * NB * 32;
+  static constexpr int BUF = HDR + 2 * NB * 32;  // (32: an AwHeader)
   static constexpr int VOFF = NB * 2 * NS * 1024, BYTES = VOFF + NB * CH * 1024;  // of a buffer
   static constexpr int QP = D * 2 + 16;                       // padded row of q
   static constexpr int FR = D == 256 ? 8 : 16, FP = D + 1;    // rows of a wave that go out at a time, padded row
@@ -66,8 +67,9 @@ struct AwCfg {
 // value is no number.
 struct AwHeader {
   uint32_t k[2];  // of a half: 0, or 1 << 16 and the loud ones of its 16 tokens
-  uint32_t vapart, vloud, vbad, pad[3];
+  uint32_t vapart, pad, vloud, vbad, pad2[2];
 };
+static_assert(sizeof(AwHeader) == 32 && offsetof(AwHeader, vloud) % 8 == 0, "as it is read");
 
 template <int KB, int VB, int D, int R>
 __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(AttendParams) {
