@@ -362,7 +362,7 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
       const bool live = ((static_cast<uint32_t>(16 * wave) * hb_mul) >> 16) < static_cast<uint32_t>(ntok);
 
       int oexp = 0;  // the sums are held times 2^-oexp
-      bool again = false, twice = false;  // see multiply
+      uint32_t state = 0;  // 1: a chunk's second time; 2: it needs one; see multiply
 
       // Scores, weights and sums of block x of the chunk. Pieces are read G at a time, AHEAD groups before
       // their products; z holds those on their way.
@@ -410,32 +410,41 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
               s[r][i >> 2][i & 3] = (see >> (16 * (i >> 2) + (i & 3))) & 1u ? s[r][i >> 2][i & 3] : -__builtin_inff();
           }
         }
-        if (__builtin_expect((apart | static_cast<uint32_t>(oexp) | (again ? 1u : 0u)) != 0, 0)) {
+        if (__builtin_expect((apart | static_cast<uint32_t>(oexp) | state) != 0, 0)) {
           const uint32_t ka = static_cast<uint32_t>(at_uniform(static_cast<int>(hd.x))), kb = static_cast<uint32_t>(at_uniform(static_cast<int>(hd.y)));
           const bool vapart = at_uniform(static_cast<int>(hd.z)) != 0;
-          // A block of values by either power of two is multiplied twice, for the loud ones and then for the
-          // others, what is not of the kind masked; beside it other blocks have nothing left the second time.
+          // A block with values of both kinds is multiplied twice, for the loud ones and then for the others,
+          // what is not of the kind masked; beside it other blocks have nothing left the second time.
           const uint2 hv = *reinterpret_cast<const uint2*>(&hdr->vloud);
           const uint32_t vloud = static_cast<uint32_t>(at_uniform(static_cast<int>(hv.x))), vbad = static_cast<uint32_t>(at_uniform(static_cast<int>(hv.y)));
-          const uint32_t kind = (vapart ? (again ? ~vloud : vloud) : again ? 0u : ~0u) >> (4 * h), none = vapart ? vbad >> (4 * h) : 0u;
-          const int e = !vapart ? 0 : again ? kAtQuietExp : kAtLoudExp;
-          const float f = at_exp2(static_cast<float>(oexp - e));
-          oexp = e;
-          twice = twice || vapart;
+          const bool both = vapart && vloud != 0 && vloud != ~0u, again = (state & 1u) != 0;
+          const uint32_t kind = (both ? (again ? ~vloud : vloud) : again ? 0u : ~0u) >> (4 * h), none = vapart ? vbad >> (4 * h) : 0u;
+          state |= both ? 2u : 0u;
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             if (ka) at_back(s[r][0], ka, h);
             if (kb) at_back(s[r][1], kb, h);
+          }
+          if (both || again || (vapart && vbad)) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int bit = 16 * (i >> 2) + (i & 3);
-              const float y = s[r][i >> 2][i & 3];
-              // tokens whose value is no number: rows that see one become NaN, others stay
-              l[r] = (none >> bit) & 1u && y != -__builtin_inff() ? __builtin_nanf("") : l[r];
-              s[r][i >> 2][i & 3] = at_pick(kind, bit, y, -__builtin_inff());
-            }
+            for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int n = 0; n < CH; ++n) o[r][n] *= f;
+              for (int i = 0; i < 8; ++i) {
+                const int bit = 16 * (i >> 2) + (i & 3);
+                const float y = s[r][i >> 2][i & 3];
+                // tokens whose value is no number: rows that see one become NaN, others stay
+                l[r] = (none >> bit) & 1u && y != -__builtin_inff() ? __builtin_nanf("") : l[r];
+                s[r][i >> 2][i & 3] = at_pick(kind, bit, y, -__builtin_inff());
+              }
+          }
+          const int e = !vapart ? 0 : again || !vloud ? kAtQuietExp : kAtLoudExp;
+          if (e != oexp) {
+            const float f = at_exp2(static_cast<float>(oexp - e));
+            oexp = e;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+              for (int n = 0; n < CH; ++n) o[r][n] *= f;
           }
         }
         float mx[R];
@@ -515,8 +524,7 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
         __syncthreads();
         int buf = 0;
         for (int c = k0; c < k1;) {
-          if (__builtin_expect(!again, 1)) begin(buf ^ 1);
-          twice = false;
+          if (__builtin_expect(state == 0, 1)) begin(buf ^ 1);
           if (live) {
             constexpr int SB = STEPS / NB, EVERY = BG / (2 * SB);
 #pragma unroll
@@ -532,8 +540,8 @@ __global__ __launch_bounds__((AwCfg<KB, VB, D, R>::T), 2) void k_attend_wide(Att
           } else {
             plain();
           }
-          again = twice && !again;
-          if (__builtin_expect(again, 0)) continue;  // the decoding's steps then do again what they did
+          state = state == 2u ? 1u : 0u;
+          if (__builtin_expect(state != 0, 0)) continue;  // the decoding's steps then do again what they did
           __syncthreads();
           buf ^= 1;
           c += NB;
