@@ -22,9 +22,10 @@ extern "C" {
  * 2^31 - 1 (the limit of 8192 experts does not apply). page_tokens is a multiple of 16 up to
  * 65536, heads at most 1024. codes are 16-byte aligned and scales 8-byte aligned. A token's
  * place is its slot, page * page_tokens + (index in the page), counted in 64 bits. The row of
- * a slot holds what tq_encode would store for that key or value with the signs of its half,
- * so a cache of up to 8192 pages can also be read by tq_kv_fetch. Both halves may be rotated
- * by different signs. */
+ * a slot holds what tq_encode would store for that key or value with the signs of its half
+ * (of a group with NaN or infinities only the same scale, NaN or 65504; its codes may be
+ * others), so a cache of up to 8192 pages can also be read by tq_kv_fetch. Both halves may be
+ * rotated by different signs. */
 typedef struct {
   tq_qweight k, v;
   int32_t heads, page_tokens;
@@ -50,7 +51,10 @@ typedef struct {
  *   NTK     the frequencies of base * stretch^(rot_dim / (rot_dim - 2))      (rot_dim > 2)
  *   YARN    f_i (g + (1 - g) / stretch), g = clamp((turns - 1) / 31, 0, 1) with turns =
  *           original * f_i / (2 pi), and gain 0.1 ln(stretch) + 1 (Peng et al. 2023; turns
- *           below 1 are interpolated, above 32 kept) */
+ *           below 1 are interpolated, above 32 kept)
+ * YARN's ramp g is linear in the turns, as published. Programs that make it linear in the pair's
+ * index i (in the logarithm of the turns) get other frequencies in between, by up to 2.3 times at
+ * 128 dimensions and stretch 8: for a model trained with those, fill inv_freq by its own rule. */
 enum { TQ_ROPE_NONE = 0, TQ_ROPE_LINEAR = 1, TQ_ROPE_NTK = 2, TQ_ROPE_YARN = 3 };
 
 /* The frequencies into HOST memory inv_freq[rot_dim / 2] (fp64) and the gain (1 but for YARN)
@@ -68,8 +72,9 @@ enum { TQ_ROPE_TRANSPOSED = 1 }; /* turn by the negative angle: the gradient of 
  * (token, head; the elements of a head are contiguous), so a slice of a fused projection's
  * output can be turned where it lies: out may be x itself with the same strides, and may not
  * overlap x otherwise, nor itself. head_dim even, in [2, 1024]; positions device int32 [tokens],
- * any sign. Computed in fp32 with fp32 sines of the reduced fp64 angle, rounded once. x and out need the
- * alignment of their dtype (16-byte loads are used where pointers, strides and sizes allow). */
+ * any sign. Sine and cosine (times the gain) are formed in fp64 and rounded to fp32; the products are
+ * fp32, rounded to the type once. x and out need the alignment of their dtype (16-byte loads are used
+ * where pointers, strides and sizes allow). */
 int tq_rope(const void *x, tq_dtype dtype, int64_t tokens, int32_t heads, int32_t head_dim,
             int64_t x_token_stride, int64_t x_head_stride, const int32_t *positions,
             const tq_rope_params *rope, uint32_t flags, void *out, int64_t out_token_stride,
@@ -124,7 +129,8 @@ int tq_kv_load(const tq_kv_cache *cache, const int64_t *slots, int64_t tokens, v
  * q, centroids, p, decoded values) are fp16, scaled so that none overflows and so that no token's
  * scales, seen or not, take bits from another's: a token's part of an output is off by some 2^-11
  * of itself and 2^-32 of the token's value (weights below 2^-21 of the largest lose bits). So fp16
- * outputs are good to about 7e-4 of their norm and bf16 outputs to their rounding. Rows of the
+ * outputs are good to about 8e-4 of their norm and bf16 outputs to their rounding (the
+ * quantization of an 8-bit cache costs 6e-3; tq_kv_load reads rows in fp32). Rows of the
  * last page behind kv_lens[b] may hold anything. A token whose scale is NaN makes the rows that
  * see it NaN, and no others. Deterministic; the last bits of a row depend on the batch it is in
  * (what else is in it decides where its tokens are cut into parts).

@@ -40,14 +40,17 @@
 // fp16: 2^7 at the reference, at most 2^15, so that its subnormals cut 2^-32 of a weight), so the
 // running maximum needs neither lane exchange nor rescaling in the common step. Sums are fp32. What is
 // rounded to fp16 (the rotated q, centroids, their products with scales, p) is what the matrix cores
-// take: half a step each, 2^-11, against 2^-8 of a bf16 output.
+// take: half a step each, 2^-11, against 2^-8 of a bf16 output and 6e-3 that the quantization of an 8-bit
+// cache costs. (More bits would take fp32 products in the decoding, two vector instructions for one, or
+// twice the matrix products.)
 //
 // Measured, 8 key heads of 128 shared by 4 query heads, 8-bit keys and 3-bit values, kernel and join:
-// one token over 337 11.1 + 3.8 us; over 131071 (193 MB) 55.9 + 7.3 us, 3.5 TB/s of the 6.0 that a
-// large read reaches; 32 sequences of 61 to 8191 (82 MB) 36.0 + 4.1 us. What bounds the long ones is
-// the decoding's vector instructions, 364 for a block of 32 tokens (with no table reads 92 % of the
-// time remains, with no loads 85 %); the short ones the chain of memory latencies of schedule, q, page
-// ids, codes and join.
+// one token over 337 11.1 + 3.6 us; over 131071 (193 MB) 55.0 + 7.3 us, 3.5 TB/s of the 6.0 that a
+// large read reaches; 32 sequences of 61 to 8191 (82 MB) 32.8 + 4.1 us. No one part bounds the long ones:
+// about 370 vector instructions for a block of 32 tokens take half of the cycles, LDS 39 %, a wave waits
+// 45 % of its time (with no table reads 92 % of the time remained, with no loads 85 %): what a wave does
+// for a block follows one another, and three waves per SIMD overlap it in part. The short ones are bound
+// by the chain of memory latencies of schedule, q, page ids, codes and join.
 #pragma once
 
 #include "exact_div.hpp"

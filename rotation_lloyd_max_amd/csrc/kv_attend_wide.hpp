@@ -7,19 +7,19 @@
 // values, straight into the order in which the matrix instructions take them: 1 KB pieces, 16 bytes
 // per lane. Two buffers alternate: while a chunk is multiplied the next one is decoded, the table
 // reads and their use spread over the products, and the one after that is on its way from memory.
-// A wave holds 16 R rows: their rotated queries and sums stay in its registers (R = 2 of D = 128: 223
+// A wave holds 16 R rows: their rotated queries and sums stay in its registers (R = 2 of D = 128: 236
 // of 256), and no sums are joined across waves.
 //
 // The powers of two of a block's tokens (kv_attend.hpp) follow from its scales alone, so that the waves
 // that decode parts of it agree without asking each other; they travel with the block.
 //
 // Measured: two chunks of 2047 tokens over texts of 4095 to 8190, 8 key heads of 128 shared by 4 query
-// heads, 8-bit keys and 3-bit values (300 Gflop): kernel 513 us, join 15 us (traced), 458 us a call in a
-// stream of calls, 655 Tflop/s against 1180 of a large library product in bf16. Of 523 us between
-// events 87 are set-up, join and launch; without the decoding 436 remain, without the softmax 471,
-// without the loads 465, with the products alone 367: bound by the matrix products and the vector
-// instructions that two waves of a SIMD overlap only in part. Four trees of 24 tokens over 1500 to
-// 6007: 32.5 + 9.6 us, 28 of them set-up and join.
+// heads, 8-bit keys and 3-bit values (300 Gflop): 459 us a call in a stream of calls, 655 Tflop/s against
+// 1180 of a large library product in bf16 (traced, which takes longer: kernel 515, join 15). Of a call of
+// 523 us between events 87 were set-up, join and launch; without the decoding 436 remained, without the
+// softmax 471, without the loads 465, with the products alone 367: bound by the matrix products (28 % of
+// the cycles) and the vector instructions (49 %) that two waves of a SIMD overlap only in part. Four trees
+// of 24 tokens over 1500 to 6007: 41 us a call, 28 of them set-up and join.
 #pragma once
 
 #include <cstddef>

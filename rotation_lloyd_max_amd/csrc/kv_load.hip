@@ -6,10 +6,10 @@
 // transform stages in registers and the others with DPP moves, and writes 16 (or 32) bytes;
 // a wave's rows are neighbouring heads of a token, so its store covers consecutive bytes.
 //
-// Bound by its stores and vector instructions: 32768 tokens of 8 heads of 128, 8-bit keys and 3-bit
-// values, to bf16 (183 MB) 47.6 us, 3.8 TB/s of the 5.2 that a large copy reaches (62 us before the
-// next row's codes were loaded a row ahead and divisions left the loop); 301 tokens of 5 heads of 64 to
-// fp32 4.0 us, latency.
+// Bound by vector instructions, 203 for the 64 chunks of a wave (their issue is full): 32768 tokens of 8
+// heads of 128, 8-bit keys and 3-bit values, to bf16 (183 MB) 48 us, 3.8 TB/s of the 5.2 that a large copy
+// reaches (62 us before the next row's codes were loaded a row ahead and divisions left the loop); 301
+// tokens of 5 heads of 64 to fp32 4.0 us, latency.
 #include "internal.hpp"
 #include "kv_lane.hpp"
 

@@ -13,7 +13,7 @@
 //
 // Bound by vector instructions (fp64 transform of five to eight stages; 2900 wave instructions per
 // 4 x 256 elements of a key or value): 3001 tokens of 4 heads of 256 in fp16, 4 bits, turned (31 MB):
-// 21.7 us, 1.4 TB/s; 16 tokens of 8 heads of 128: 6.0 us, latency. 1024 workgroups a half instead of
+// 21.5 us, 1.4 TB/s; 16 tokens of 8 heads of 128: 6.0 us, latency. 1024 workgroups a half instead of
 // 2048 23 us; next token's rows loaded ahead spilled and took 59 us.
 #include "kv_lane.hpp"
 

@@ -3,6 +3,7 @@ values beyond 32 bits. CPU tensors, so that every check is shown to come before 
 
 import os
 
+import numpy as np
 import pytest
 import torch
 
@@ -127,3 +128,18 @@ def test_index_values_beyond_their_type_stay_outside(dt):
     assert got.dtype == torch.int64 and got.tolist() == [min(2 ** 63 - 1, v) for v in values]
     small = tq.kv._as(torch.tensor([-3, 7], dtype=torch.int16), torch.int32, cpu, "x")
     assert small.dtype == torch.int32 and small.tolist() == [-3, 7]
+
+
+@pytest.mark.parametrize("rot,base,stretch,original", [(128, 1e4, 8.0, 4096), (64, 5e5, 32.0, 8192), (96, 1e4, 1.0, 2048), (6, 100.0, 3.5, 50)])
+def test_frequencies_by_their_formulas(rot, base, stretch, original):
+    i = np.arange(0, rot, 2)
+    plain = base ** (-i / rot)
+    turns = original * plain / (2 * np.pi)
+    ramp = np.clip((turns - 1) / 31, 0, 1)          # linear in the turns
+    want = {None: (plain, 1.0), "linear": (plain / stretch, 1.0),
+            "ntk": ((base * stretch ** (rot / (rot - 2))) ** (-i / rot), 1.0),
+            "yarn": (plain * ramp + plain / stretch * (1 - ramp), 0.1 * np.log(stretch) + 1)}
+    for scaling, (f, gain) in want.items():
+        r = tq.rope_frequencies(rot, base=base, scaling=scaling, stretch=stretch, original=original, device="cpu")
+        np.testing.assert_allclose(r.inv_freq.numpy(), f, rtol=1e-13)
+        assert abs(r.gain - gain) < 1e-15 and r.rot_dim == rot
