@@ -150,12 +150,14 @@ def _overlaps_itself(t):
 
 def _span(t):
     """(first, last + 1) byte that the elements of t lie between."""
-    n = 1 + sum((d - 1) * s for d, s in zip(t.shape, t.stride())) if t.numel() else 0
+    n = 1 + sum((d - 1) * s for d, s in zip(t.shape, t.stride()))
     return t.data_ptr(), t.data_ptr() + n * t.element_size()
 
 
 def _apart(a, b):
     """Whether the memory between a's first and last element and that of b's do not meet."""
+    if not a.numel() or not b.numel():
+        return True
     (a0, a1), (b0, b1) = _span(a), _span(b)
     return a1 <= b0 or b1 <= a0
 

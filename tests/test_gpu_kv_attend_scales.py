@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+import rotation_lloyd_max_amd as tq
 from oracle import attention as oat
 from oracle import hadamard as ohd
 from parity import as_f64
@@ -175,3 +176,42 @@ def test_a_value_that_is_no_number_beside_loud_and_quiet_ones(n, share):
         bt.cache.v.scales.copy_(keep)
         same = torch.equal(got[:n - 2], want[:n - 2]) and torch.equal(got[n:], want[n:])
         assert same and torch.isnan(got[n - 2:n]).all(), bits
+
+
+@pytest.mark.parametrize("n,share", ROWS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_of_zeros(D, n, share):
+    # a scale of 0 (a key or value of zeros) alone, beside others, and in a whole cache
+    bt, counts, q = mixed(D, n, share, 0.1, 2.0, D + n)
+    for part, step in ((bt.cache.k, 5), (bt.cache.v, 7)):
+        for j in range(0, LONG, step):
+            s = int(bt.slots[0][j])
+            scales_of(bt, part)[s // bt.page, :, s % bt.page] = 0.0
+    bt.refresh()
+    check_rows(run(bt, q, counts), bt, q, counts, D ** -0.5, 0, [0, n // 2, n - 1])
+    bt.cache.k.scales.zero_()
+    bt.refresh()
+    check_rows(run(bt, q, counts), bt, q, counts, D ** -0.5, 0, [0, n - 1])
+    bt.cache.v.scales.zero_()
+    assert not run(bt, q, counts).any()
+
+
+@pytest.mark.parametrize("n,share", ROWS)
+def test_captured_calls_with_scales_of_every_size(n, share):
+    bt, counts, q = mixed(128, n, share, 1e-7, 5e4, n)
+    bt.cache.k.scales.fill_(0.5)
+    lens, table = bt.dev()
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    tq.kv_attend(bt.cache, q, lens, table, q_offsets=off)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = tq.kv_attend(bt.cache, q, lens, table, q_offsets=off)
+    for rep in range(4):
+        bt.cache.v.scales.mul_(0.25 if rep % 2 else 0.5)
+        q.copy_(queries(*q.shape, torch.bfloat16, seed=rep))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        same = torch.equal(out, tq.kv_attend(bt.cache, q, lens, table, q_offsets=off))
+        assert same and torch.isfinite(out).all(), rep

@@ -90,6 +90,9 @@ def test_rope_outputs_that_overlap_the_input_in_part():
                 wide.as_strided((2, 4, 64), (64, 768, 1), 768 + 5 * 64)):
         with pytest.raises(ValueError, match="overlap"):
             turn(x, out=bad)
+    for n, h in ((0, 4), (2, 0)):       # nothing to write: nothing to meet
+        with pytest.raises(ValueError, match=NOT_A_GPU):
+            turn(wide[1:1 + n, 2:2 + h], out=wide[1:1 + n, 3:3 + h])
     for good in (x, wide[1:3, 6:10], wide[3:5, 2:6], wide[1:3, 2:6].clone(), wide[0:1].view(-1)[:512].view(2, 4, 64)):
         with pytest.raises(ValueError, match=NOT_A_GPU):
             turn(x, out=good)
