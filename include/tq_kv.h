@@ -80,6 +80,19 @@ int tq_rope(const void *x, tq_dtype dtype, int64_t tokens, int32_t heads, int32_
             const tq_rope_params *rope, uint32_t flags, void *out, int64_t out_token_stride,
             int64_t out_head_stride, void *stream);
 
+/* tq_rope with positions of several axes (time, height and width of images and video): pair i turns
+ * by positions[axis[i] * axis_stride + t] * inv_freq[i].
+ *   axis         device uint8 [rot_dim / 2], the axis of each pair; a pair whose axis is not below
+ *                `axes` is not turned (only scaled by the gain)
+ *   positions    device int32, `axes` rows of `tokens` positions, axis_stride elements apart (0: the
+ *                same positions for every axis, as text has them); axes in [1, 255]
+ * Everything else is as in tq_rope, and with one axis so are the results, bit for bit. */
+int tq_rope_axes(const void *x, tq_dtype dtype, int64_t tokens, int32_t heads, int32_t head_dim,
+                 int64_t x_token_stride, int64_t x_head_stride, const int32_t *positions,
+                 int64_t axis_stride, int32_t axes, const uint8_t *axis, const tq_rope_params *rope,
+                 uint32_t flags, void *out, int64_t out_token_stride, int64_t out_head_stride,
+                 void *stream);
+
 /* Writes `tokens` new tokens into the cache: for every token t with a slot in [0, E *
  * page_tokens), each head's key (value) is rotated, quantized and packed into its row, as
  * tq_encode does (fp64 rotation, RMS and, with `rope`, rotary turn; binary32 decision). A
@@ -93,6 +106,14 @@ int tq_kv_store(const tq_kv_cache *cache, const void *k, const void *v, tq_dtype
                 int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
                 int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots,
                 const tq_rope_params *rope, const int32_t *positions, void *stream);
+
+/* tq_kv_store whose keys are turned at positions of several axes: axis, positions, axis_stride and
+ * axes as in tq_rope_axes; rope may not be NULL. */
+int tq_kv_store_axes(const tq_kv_cache *cache, const void *k, const void *v, tq_dtype dtype,
+                     int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                     int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots,
+                     const tq_rope_params *rope, const int32_t *positions, int64_t axis_stride,
+                     int32_t axes, const uint8_t *axis, void *stream);
 
 /* Reads tokens back: k_out[t][h] = the dequantized, rotated-back key of slots[t] (v_out the
  * value), device [tokens][heads][K] of `dtype`, contiguous, 16-byte aligned; either may be

@@ -22,7 +22,8 @@ __all__ = [
     "qmv", "gather_qmv", "multi_gather_qmv", "gather_qmm", "workspace_bytes", "dequant",
     "encode_stream", "multi_gather_qmv_static", "ExpertCache", "kv_fetch", "rotate_dense",
     "encode_dense", "Rope", "rope_frequencies", "rope", "KVCache", "kv_cache", "kv_store",
-    "kv_load", "kv_attend", "kv_attend_workspace",
+    "kv_load", "kv_attend", "kv_attend_workspace", "rope_axes", "KVPool", "kv_pool", "KVPlan", "kv_plan",
+    "kv_keep", "Verified", "verify", "verify_workspace",
     "F32", "BF16", "F16", "X_ROTATED",
 ]
 
@@ -100,7 +101,7 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -m rotation_lloyd_max_amd.build`")
         handle = ctypes.CDLL(LIB_PATH)
-        for name, res, args in SIGNATURES + kv.SIGNATURES:
+        for name, res, args in SIGNATURES + kv.SIGNATURES + step.SIGNATURES:
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args
@@ -558,6 +559,8 @@ class ExpertCache:
         return multi_gather_qmv(self.pool, sid, X, **kw)
 
 
-from . import kv  # noqa: E402  (uses the names above)
+from . import kv, step  # noqa: E402  (use the names above)
 from .kv import (KVCache, Rope, kv_attend, kv_attend_workspace, kv_cache,  # noqa: E402
-                 kv_load, kv_store, rope, rope_frequencies)
+                 kv_load, kv_store, rope, rope_axes, rope_frequencies)
+from .step import (KVPlan, KVPool, Verified, kv_keep, kv_plan, kv_pool,  # noqa: E402
+                   verify, verify_workspace)

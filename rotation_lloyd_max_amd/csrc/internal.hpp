@@ -124,6 +124,9 @@ struct RopeArgs {
   int rot;
   bool interleaved;
   double gain;
+  const uint8_t* axis;  // null: one axis; else the axis of each pair, `axes` rows of positions
+  int64_t axis_stride;
+  int axes;
 };
 hipError_t launch_rope(const void* x, int dt, int64_t tokens, int heads, int D, int64_t xts,
                        int64_t xhs, const RopeArgs& r, bool transposed, void* out, int64_t ots,
@@ -152,6 +155,47 @@ struct AttendArgs {
 };
 size_t kv_attend_workspace(const KvCacheArgs& c, int q_heads, int B, int64_t M);
 hipError_t launch_kv_attend(const AttendArgs& a, hipStream_t s);
+
+// A decoding step (tq_step.h), resolved on the host.
+struct PlanArgs {
+  int32_t *free_pages, *state;
+  int pages, page, B;
+  const int32_t *lens, *counts;
+  int32_t* table;
+  int width;
+  int M;
+  const int32_t* parents;  // null: chains
+  int words;               // of a row's tree mask
+  const int32_t* shift;    // null: none
+  int64_t* slots;
+  int32_t *positions, *q_offsets, *kv_lens, *status;
+  uint32_t* tree;
+  int32_t* left;  // state itself, or another word
+};
+hipError_t launch_kv_plan(const PlanArgs& a, hipStream_t s);
+struct KeepArgs {
+  KvCacheArgs c;  // read where path is not null
+  int32_t *free_pages, *state;
+  int pages, page, B;
+  const int32_t *lens, *q_offsets, *status, *kept, *path;  // q_offsets, status, path may be null
+  const int32_t* table;
+  int width;
+  int32_t *lens_out, *left;
+};
+hipError_t launch_kv_keep(const KeepArgs& a, hipStream_t s);
+struct VerifyArgs {
+  const void *target, *draft;  // draft may be null: point masses
+  int tdt, ddt;
+  int64_t tstride, dstride;  // elements
+  bool tprobs, dprobs;
+  int V, B, M;
+  const int32_t *offsets, *tokens, *parents;  // parents null: chains
+  const float *uniforms, *temperature;        // temperature null: 1
+  int32_t *kept, *out_tokens, *path;
+  void* ws;
+};
+size_t verify_workspace(int V, int B, int M, bool tprobs, bool drafted, bool dprobs);
+hipError_t launch_verify(const VerifyArgs& a, hipStream_t s);
 
 // Up to kMaxSlotIds int32 values passed by value to a kernel (tq_expert_cache_fetch).
 constexpr int kMaxSlotIds = 512;

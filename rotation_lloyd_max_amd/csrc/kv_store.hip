@@ -50,8 +50,10 @@ struct StoreParams {
   const int64_t* slots;
   const int32_t* positions;
   const double* inv_freq;  // null: no rotary positions
+  const uint8_t* axis;     // null: one axis (RopeArgs)
+  int64_t axis_stride;
   int64_t tokens, capacity;
-  int heads, page, rot;
+  int heads, page, rot, axes;
   bool interleaved;
   double gain, inv_sqrt_d;
 };
@@ -151,8 +153,9 @@ __global__ __launch_bounds__(256) void k_kv_store(StoreParams p) {
     const int tok = static_cast<int>(slot - page * p.page);
     if (turn) {
       // two buffers: the next token's angles may be written while this one's are read
-      const double pos = static_cast<double>(p.positions[t]);
       for (int i = threadIdx.x; i < (p.rot >> 1); i += blockDim.x) {
+        const int ax = p.axis ? p.axis[i] : 0;
+        const double pos = static_cast<double>(ax < p.axes ? p.positions[ax * p.axis_stride + t] : 0);
         const double turns = pos * (p.inv_freq[i] * 0.15915494309189533577);
         double s, co;
         sincospi(2.0 * (turns - rint(turns)), &s, &co);
@@ -291,6 +294,7 @@ hipError_t launch_kv_store(const KvCacheArgs& c, const void* k, const void* v, i
   p.heads = c.heads; p.page = c.page;
   p.positions = r.positions; p.inv_freq = r.inv_freq; p.rot = r.rot;
   p.interleaved = r.interleaved; p.gain = r.gain;
+  p.axis = r.axis; p.axis_stride = r.axis_stride; p.axes = r.axis ? r.axes : 1;
   p.inv_sqrt_d = 1.0 / __builtin_sqrt(static_cast<double>(c.D));
   int threads = (c.heads * (c.D / 8) + 63) & ~63;
   if (threads > 256) threads = 256;

@@ -27,6 +27,9 @@ struct RopeParams {
   int64_t tokens, xts, xhs, ots, ohs;  // strides in elements
   int heads, D, rot, tpb, hpb;         // tokens and heads of a workgroup
   double gain;
+  const uint8_t* axis;   // several axes: the axis of each pair, `axes` rows of positions `ps` apart
+  int64_t ps;
+  int axes;
   bool transposed, copy;  // copy: elements from rot on are copied (not in place)
 };
 
@@ -76,7 +79,8 @@ __device__ __forceinline__ void rope_put(char* p, const float (&f)[V]) {
 // VEC: 16-byte accesses. A head is cut into units: V pairs (two accesses) in the half layout, V
 // elements (V / 2 pairs) interleaved, V copied elements behind rot; without VEC a unit is one
 // pair or one copied element.
-template <int DT, bool VEC, bool IL>
+// AX: positions of several axes.
+template <int DT, bool VEC, bool IL, bool AX>
 __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeParams p) {
   constexpr int SZ = DT == 0 ? 4 : 2;
   constexpr int V = VEC ? 16 / SZ : 1;
@@ -88,7 +92,14 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeParams p) {
   const int nh = p.heads - h0 < p.hpb ? p.heads - h0 : p.hpb;
   for (int a = threadIdx.x; a < nt * half; a += kRopeThreads) {
     const int t = a / half, i = a - t * half;
-    const double turns = static_cast<double>(p.positions[t0 + t]) * (p.inv_freq[i] * 0.15915494309189533577);
+    int pos;
+    if constexpr (AX) {
+      const int ax = p.axis[i];
+      pos = ax < p.axes ? p.positions[ax * p.ps + t0 + t] : 0;
+    } else {
+      pos = p.positions[t0 + t];
+    }
+    const double turns = static_cast<double>(pos) * (p.inv_freq[i] * 0.15915494309189533577);
     double sn, cn;
     sincospi(2.0 * (turns - rint(turns)), &sn, &cn);
     cs[a] = make_float2(static_cast<float>(cn * p.gain), static_cast<float>((p.transposed ? -sn : sn) * p.gain));
@@ -135,12 +146,17 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeParams p) {
   }
 }
 
+template <int DT, bool AX>
+void rope_run(const RopeParams& p, bool vec, bool il, dim3 grid, hipStream_t s) {
+  if (vec && il) hipLaunchKernelGGL((k_rope<DT, true, true, AX>), grid, dim3(kRopeThreads), 0, s, p);
+  else if (vec) hipLaunchKernelGGL((k_rope<DT, true, false, AX>), grid, dim3(kRopeThreads), 0, s, p);
+  else if (il) hipLaunchKernelGGL((k_rope<DT, false, true, AX>), grid, dim3(kRopeThreads), 0, s, p);
+  else hipLaunchKernelGGL((k_rope<DT, false, false, AX>), grid, dim3(kRopeThreads), 0, s, p);
+}
 template <int DT>
 void rope_run(const RopeParams& p, bool vec, bool il, dim3 grid, hipStream_t s) {
-  if (vec && il) hipLaunchKernelGGL((k_rope<DT, true, true>), grid, dim3(kRopeThreads), 0, s, p);
-  else if (vec) hipLaunchKernelGGL((k_rope<DT, true, false>), grid, dim3(kRopeThreads), 0, s, p);
-  else if (il) hipLaunchKernelGGL((k_rope<DT, false, true>), grid, dim3(kRopeThreads), 0, s, p);
-  else hipLaunchKernelGGL((k_rope<DT, false, false>), grid, dim3(kRopeThreads), 0, s, p);
+  if (p.axis) rope_run<DT, true>(p, vec, il, grid, s);
+  else rope_run<DT, false>(p, vec, il, grid, s);
 }
 
 }  // namespace
@@ -153,6 +169,7 @@ hipError_t launch_rope(const void* x, int dt, int64_t tokens, int heads, int D, 
   p.xts = xts; p.xhs = xhs; p.ots = ots; p.ohs = ohs;
   p.heads = heads; p.D = D; p.rot = r.rot;
   p.gain = r.gain;
+  p.axis = r.axis; p.ps = r.axis_stride; p.axes = r.axes;
   p.transposed = transposed;
   p.copy = x != out;
   const int V = dt == 0 ? 4 : 8, half = r.rot / 2;

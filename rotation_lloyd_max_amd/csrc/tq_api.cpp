@@ -12,12 +12,14 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <vector>
 
 #include "../../include/tq.h"
 #include "../../include/tq_kv.h"
+#include "../../include/tq_step.h"
 #include "internal.hpp"
 
 namespace tq {
@@ -332,6 +334,16 @@ int check_rope(const tq_rope_params* r, const int32_t* positions, int head_dim, 
   out->rot = r->rot_dim;
   out->interleaved = r->interleaved != 0;
   out->gain = r->gain;
+  return TQ_OK;
+}
+
+int check_axes(const uint8_t* axis, int64_t axis_stride, int32_t axes, RopeArgs* out) {
+  if (!axis) return fail(TQ_ERR_ARG, "axis is NULL");
+  if (axes < 1 || axes > 255) return fail(TQ_ERR_ARG, "axes must be in [1, 255] (got %d)", axes);
+  if (axis_stride < 0) return fail(TQ_ERR_ARG, "axis_stride must be >= 0");
+  out->axis = axis;
+  out->axis_stride = axis_stride;
+  out->axes = axes;
   return TQ_OK;
 }
 
@@ -819,10 +831,12 @@ int tq_rope_frequencies(int32_t rot_dim, double base, int32_t scaling, double st
   return TQ_OK;
 }
 
-int tq_rope(const void* x, tq_dtype dtype, int64_t tokens, int32_t heads, int32_t head_dim,
-            int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions,
-            const tq_rope_params* rope, uint32_t flags, void* out, int64_t out_token_stride,
-            int64_t out_head_stride, void* stream) {
+namespace {
+// tq_rope and tq_rope_axes (r holds the axes of the latter already)
+int rope_call(const char* name, const void* x, tq_dtype dtype, int64_t tokens, int32_t heads, int32_t head_dim,
+              int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions, RopeArgs r,
+              const tq_rope_params* rope, uint32_t flags, void* out, int64_t out_token_stride,
+              int64_t out_head_stride, void* stream) {
   if (!valid_dtype(dtype)) return fail(TQ_ERR_ARG, "bad dtype");
   if (head_dim < 2 || head_dim > 1024 || head_dim % 2 != 0)
     return fail(TQ_ERR_UNSUPPORTED, "head_dim must be even and in [2, 1024] (got %d)", head_dim);
@@ -837,19 +851,18 @@ int tq_rope(const void* x, tq_dtype dtype, int64_t tokens, int32_t heads, int32_
     return fail(TQ_ERR_ARG, "in place, x and out must have the same strides");
   if ((tokens > 1 && out_token_stride == 0) || (heads > 1 && out_head_stride == 0))
     return fail(TQ_ERR_ARG, "out must not overlap itself");
-  RopeArgs r{};
   const int rc = check_rope(rope, positions, head_dim, &r);
   if (rc != TQ_OK) return rc;
   return hip_status(launch_rope(x, dtype, tokens, heads, head_dim, x_token_stride, x_head_stride, r,
                                 (flags & TQ_ROPE_TRANSPOSED) != 0, out, out_token_stride,
                                 out_head_stride, static_cast<hipStream_t>(stream)),
-                    "tq_rope");
+                    name);
 }
 
-int tq_kv_store(const tq_kv_cache* cache, const void* k, const void* v, tq_dtype dtype,
-                int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
-                int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,
-                const tq_rope_params* rope, const int32_t* positions, void* stream) {
+// tq_kv_store and tq_kv_store_axes
+int store_call(const char* name, const tq_kv_cache* cache, const void* k, const void* v, tq_dtype dtype,
+               int64_t tokens, const int64_t (&strides)[4], const int64_t* slots, RopeArgs r,
+               const tq_rope_params* rope, const int32_t* positions, void* stream) {
   KvCacheArgs c{};
   int rc = check_cache(cache, &c);
   if (rc != TQ_OK) return rc;
@@ -859,15 +872,57 @@ int tq_kv_store(const tq_kv_cache* cache, const void* k, const void* v, tq_dtype
   if (!k || !v || !slots) return fail(TQ_ERR_ARG, "k, v and slots must be non-NULL");
   if (!aligned(k, dtype_size(dtype)) || !aligned(v, dtype_size(dtype)) || !aligned(slots, 8))
     return fail(TQ_ERR_ALIGN, "k, v or slots misaligned");
-  RopeArgs r{};
   if (rope) {
     rc = check_rope(rope, positions, c.D, &r);
     if (rc != TQ_OK) return rc;
   }
-  const int64_t strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
   return hip_status(launch_kv_store(c, k, v, dtype, tokens, strides, slots, r,
                                     static_cast<hipStream_t>(stream)),
-                    "tq_kv_store");
+                    name);
+}
+}  // namespace
+
+int tq_rope(const void* x, tq_dtype dtype, int64_t tokens, int32_t heads, int32_t head_dim,
+            int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions,
+            const tq_rope_params* rope, uint32_t flags, void* out, int64_t out_token_stride,
+            int64_t out_head_stride, void* stream) {
+  return rope_call("tq_rope", x, dtype, tokens, heads, head_dim, x_token_stride, x_head_stride, positions,
+                   RopeArgs{}, rope, flags, out, out_token_stride, out_head_stride, stream);
+}
+
+int tq_rope_axes(const void* x, tq_dtype dtype, int64_t tokens, int32_t heads, int32_t head_dim,
+                 int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions,
+                 int64_t axis_stride, int32_t axes, const uint8_t* axis, const tq_rope_params* rope,
+                 uint32_t flags, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                 void* stream) {
+  RopeArgs r{};
+  const int rc = check_axes(axis, axis_stride, axes, &r);
+  if (rc != TQ_OK) return rc;
+  return rope_call("tq_rope_axes", x, dtype, tokens, heads, head_dim, x_token_stride, x_head_stride,
+                   positions, r, rope, flags, out, out_token_stride, out_head_stride, stream);
+}
+
+int tq_kv_store(const tq_kv_cache* cache, const void* k, const void* v, tq_dtype dtype,
+                int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,
+                const tq_rope_params* rope, const int32_t* positions, void* stream) {
+  const int64_t strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
+  return store_call("tq_kv_store", cache, k, v, dtype, tokens, strides, slots, RopeArgs{}, rope, positions,
+                    stream);
+}
+
+int tq_kv_store_axes(const tq_kv_cache* cache, const void* k, const void* v, tq_dtype dtype,
+                     int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                     int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,
+                     const tq_rope_params* rope, const int32_t* positions, int64_t axis_stride,
+                     int32_t axes, const uint8_t* axis, void* stream) {
+  RopeArgs r{};
+  const int rc = check_axes(axis, axis_stride, axes, &r);
+  if (rc != TQ_OK) return rc;
+  if (!rope) return fail(TQ_ERR_ARG, "rope is NULL");
+  const int64_t strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
+  return store_call("tq_kv_store_axes", cache, k, v, dtype, tokens, strides, slots, r, rope, positions,
+                    stream);
 }
 
 int tq_kv_load(const tq_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k_out,
@@ -946,6 +1001,128 @@ int tq_kv_attend(const tq_kv_cache* cache, const void* q, tq_dtype q_dtype, int3
   a.table_width = table_width; a.tree = tree; a.tree_words = tree_words; a.scale = scale;
   a.out = out; a.odt = out_dtype; a.ws = ws;
   return hip_status(launch_kv_attend(a, static_cast<hipStream_t>(stream)), "tq_kv_attend");
+}
+
+namespace {
+int check_pool(const tq_kv_pool* pool, int32_t page_tokens, int32_t B, int32_t table_width) {
+  if (!pool) return fail(TQ_ERR_ARG, "pool is NULL");
+  if (pool->pages < 1 || pool->pages > (1 << 30)) return fail(TQ_ERR_ARG, "pool pages must be in [1, 2^30]");
+  if (!pool->free_pages || !pool->state) return fail(TQ_ERR_ARG, "the pool's free_pages and state must be non-NULL");
+  if (!aligned(pool->free_pages, 4) || !aligned(pool->state, 4))
+    return fail(TQ_ERR_ALIGN, "the pool's free_pages or state misaligned");
+  if (page_tokens < 1 || page_tokens > 65536) return fail(TQ_ERR_ARG, "page_tokens must be in [1, 65536]");
+  if (B < 0 || B > 65536) return fail(TQ_ERR_ARG, "B must be in [0, 65536]");
+  if (table_width < 0 || static_cast<int64_t>(table_width) * page_tokens > 0x7fffffffll - 65536)
+    return fail(TQ_ERR_ARG, "table_width must be >= 0, table_width * page_tokens below 2^31 - 65536");
+  return TQ_OK;
+}
+
+bool all_aligned4(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (p && !aligned(p, 4)) return false;
+  return true;
+}
+}  // namespace
+
+int tq_kv_plan(const tq_kv_pool* pool, int32_t page_tokens, int32_t B, const int32_t* lens,
+               const int32_t* counts, int32_t* page_table, int32_t table_width, int64_t M,
+               const int32_t* parents, const int32_t* shift, int64_t* slots, int32_t* positions,
+               int32_t* q_offsets, int32_t* kv_lens, int32_t* status, uint32_t* tree,
+               int32_t tree_words, int32_t* left, void* stream) {
+  const int rc = check_pool(pool, page_tokens, B, table_width);
+  if (rc != TQ_OK) return rc;
+  if (M < 0 || M > (1 << 24)) return fail(TQ_ERR_ARG, "M must be in [0, 2^24]");
+  if (tree ? tree_words < 1 || tree_words > 65536 : tree_words != 0)
+    return fail(TQ_ERR_ARG, "tree_words must be in [1, 65536] with a tree and 0 without");
+  if (!q_offsets || (B > 0 && (!lens || !counts || !kv_lens || !status || (table_width > 0 && !page_table))) ||
+      (M > 0 && (!slots || !positions)))
+    return fail(TQ_ERR_ARG, "lens, counts, page_table and the outputs must be non-NULL");
+  if (!aligned(slots, 8) || !all_aligned4({lens, counts, page_table, parents, shift, positions, q_offsets,
+                                           kv_lens, status, tree, left}))
+    return fail(TQ_ERR_ALIGN, "slots must be 8-byte, the other arrays 4-byte aligned");
+  PlanArgs a{};
+  a.free_pages = pool->free_pages; a.state = pool->state; a.pages = pool->pages; a.page = page_tokens;
+  a.B = B; a.lens = lens; a.counts = counts; a.table = page_table; a.width = table_width;
+  a.M = static_cast<int>(M); a.parents = parents; a.words = tree_words; a.shift = shift;
+  a.slots = slots; a.positions = positions; a.q_offsets = q_offsets; a.kv_lens = kv_lens;
+  a.status = status; a.tree = tree; a.left = left ? left : pool->state;
+  return hip_status(launch_kv_plan(a, static_cast<hipStream_t>(stream)), "tq_kv_plan");
+}
+
+int tq_kv_keep(const tq_kv_pool* pool, const tq_kv_cache* cache, int32_t page_tokens, int32_t B,
+               const int32_t* lens, const int32_t* q_offsets, const int32_t* status,
+               const int32_t* kept, const int32_t* path, const int32_t* page_table,
+               int32_t table_width, int32_t* lens_out, int32_t* left, void* stream) {
+  int rc = check_pool(pool, page_tokens, B, table_width);
+  if (rc != TQ_OK) return rc;
+  KeepArgs a{};
+  if (path) {
+    rc = check_cache(cache, &a.c);
+    if (rc != TQ_OK) return rc;
+    if (a.c.page != page_tokens || a.c.pages != pool->pages)
+      return fail(TQ_ERR_ARG, "the cache and the pool differ in pages or page_tokens");
+    if (!q_offsets) return fail(TQ_ERR_ARG, "a path needs q_offsets");
+  }
+  if (B == 0 && (!left || left == pool->state)) return TQ_OK;
+  if (B > 0 && (!lens || !kept || !lens_out || (table_width > 0 && !page_table)))
+    return fail(TQ_ERR_ARG, "lens, kept, page_table and lens_out must be non-NULL");
+  if (!all_aligned4({lens, q_offsets, status, kept, path, page_table, lens_out, left}))
+    return fail(TQ_ERR_ALIGN, "the arrays must be 4-byte aligned");
+  a.free_pages = pool->free_pages; a.state = pool->state; a.pages = pool->pages; a.page = page_tokens;
+  a.B = B; a.lens = lens; a.q_offsets = q_offsets; a.status = status; a.kept = kept; a.path = path;
+  a.table = page_table; a.width = table_width; a.lens_out = lens_out;
+  a.left = left ? left : pool->state;
+  return hip_status(launch_kv_keep(a, static_cast<hipStream_t>(stream)), "tq_kv_keep");
+}
+
+namespace {
+int check_verify(int64_t vocab, int32_t B, int64_t M, uint32_t flags) {
+  if (vocab < 1 || vocab > (1 << 28)) return fail(TQ_ERR_ARG, "vocab must be in [1, 2^28]");
+  if (B < 0 || B > 65536) return fail(TQ_ERR_ARG, "B must be in [0, 65536]");
+  if (M < 0 || M > (1 << 24)) return fail(TQ_ERR_ARG, "M must be in [0, 2^24]");
+  if (flags & ~static_cast<uint32_t>(TQ_TARGET_PROBS | TQ_DRAFT_PROBS)) return fail(TQ_ERR_ARG, "unknown flags");
+  return TQ_OK;
+}
+}  // namespace
+
+size_t tq_verify_workspace(int64_t vocab, int32_t B, int64_t M, int32_t drafted, uint32_t flags) {
+  if (check_verify(vocab, B, M, flags) != TQ_OK) return SIZE_MAX;
+  if (drafted != 0 && drafted != 1) {
+    fail(TQ_ERR_ARG, "drafted must be 0 or 1");
+    return SIZE_MAX;
+  }
+  return verify_workspace(static_cast<int>(vocab), B, static_cast<int>(M), (flags & TQ_TARGET_PROBS) != 0,
+                          drafted != 0, (flags & TQ_DRAFT_PROBS) != 0);
+}
+
+int tq_verify(const void* target, tq_dtype target_dtype, int64_t target_stride, const void* draft,
+              tq_dtype draft_dtype, int64_t draft_stride, uint32_t flags, int64_t vocab, int32_t B,
+              const int32_t* offsets, int64_t M, const int32_t* tokens, const int32_t* parents,
+              const float* uniforms, const float* temperature, int32_t* kept, int32_t* out_tokens,
+              int32_t* path, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_verify(vocab, B, M, flags);
+  if (rc != TQ_OK) return rc;
+  if (!valid_dtype(target_dtype) || (draft && !valid_dtype(draft_dtype))) return fail(TQ_ERR_ARG, "bad dtype");
+  if (B == 0) return TQ_OK;
+  if (!offsets || !kept) return fail(TQ_ERR_ARG, "offsets and kept must be non-NULL");
+  if (M > 0 && (!target || !tokens || !uniforms || !out_tokens || !path))
+    return fail(TQ_ERR_ARG, "target, tokens, uniforms, out_tokens and path must be non-NULL");
+  if (!aligned(target, dtype_size(target_dtype)) || (draft && !aligned(draft, dtype_size(draft_dtype))))
+    return fail(TQ_ERR_ALIGN, "target or draft misaligned for its dtype");
+  if (!all_aligned4({offsets, tokens, parents, uniforms, temperature, kept, out_tokens, path}))
+    return fail(TQ_ERR_ALIGN, "the arrays must be 4-byte aligned");
+  VerifyArgs a{};
+  a.target = target; a.draft = draft; a.tdt = target_dtype; a.ddt = draft ? draft_dtype : TQ_F32;
+  a.tstride = target_stride; a.dstride = draft_stride;
+  a.tprobs = (flags & TQ_TARGET_PROBS) != 0; a.dprobs = (flags & TQ_DRAFT_PROBS) != 0;
+  a.V = static_cast<int>(vocab); a.B = B; a.M = static_cast<int>(M);
+  a.offsets = offsets; a.tokens = tokens; a.parents = parents; a.uniforms = uniforms;
+  a.temperature = temperature; a.kept = kept; a.out_tokens = out_tokens; a.path = path; a.ws = ws;
+  const size_t need = verify_workspace(a.V, B, a.M, a.tprobs, draft != nullptr, a.dprobs);
+  if (need > 0 && (!ws || ws_bytes < need))
+    return fail(TQ_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", need, ws_bytes);
+  if (need > 0 && !aligned(ws, 256)) return fail(TQ_ERR_ALIGN, "workspace must be 256-byte aligned");
+  return hip_status(launch_verify(a, static_cast<hipStream_t>(stream)), "tq_verify");
 }
 
 // ---- expert cache ------------------------------------------------------------------------

@@ -40,6 +40,10 @@ SIGNATURES = [
     ("tq_kv_attend", _INT, [_KV, _P, _INT, _I32, _I64, _I32, _P, _I64, _P, _P, _I32, _P, _I32, _F32,
                             _P, _INT, _P, _SZ, _P]),
     ("tq_kv_attend_workspace", _SZ, [_KV, _I32, _I32, _I64]),
+    ("tq_rope_axes", _INT,
+     [_P, _INT, _I64, _I32, _I32, _I64, _I64, _P, _I64, _I32, _P, _RP, _U32, _P, _I64, _I64, _P]),
+    ("tq_kv_store_axes", _INT,
+     [_KV, _P, _P, _INT, _I64, _I64, _I64, _I64, _I64, _P, _RP, _P, _I64, _I32, _P, _P]),
 ]
 
 ROPE_SCALING = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -97,11 +101,14 @@ def _no_gradient(name):
 @dataclass
 class Rope:
     """Rotary positions: inv_freq float64 [rot_dim / 2] on the device (radians per position),
-    pairs (i, i + rot_dim / 2) or, interleaved, (2i, 2i + 1), the turned pair scaled by gain."""
+    pairs (i, i + rot_dim / 2) or, interleaved, (2i, 2i + 1), the turned pair scaled by gain.
+    axis: None, or uint8 [rot_dim / 2] on the device, the axis of each pair for positions of
+    several axes (rope_axes); a pair whose axis the positions do not have is not turned."""
     inv_freq: torch.Tensor
     rot_dim: int
     interleaved: bool = False
     gain: float = 1.0
+    axis: torch.Tensor = None
 
     def desc(self, device):
         f = self.inv_freq
@@ -110,6 +117,20 @@ class Rope:
         if f.device != device:
             raise ValueError(f"inv_freq is on {f.device}, the call runs on {device}")
         return _RopeParams(f.data_ptr(), self.rot_dim, 1 if self.interleaved else 0, self.gain)
+
+    def axes(self, positions, tokens, device):
+        """(positions, axis stride, axes, axis pointer) of a call with several axes: positions
+        [axes, tokens], the axes any distance apart (an expanded tensor: the same for all)."""
+        a = self.axis
+        if a.dtype != torch.uint8 or a.numel() * 2 != self.rot_dim or not a.is_contiguous() or a.device != device:
+            raise ValueError(f"axis must be a contiguous uint8 tensor of rot_dim / 2 elements on {device}")
+        if positions.dim() != 2 or positions.shape[1] != tokens:
+            raise ValueError(f"positions must be [axes, {tokens}], got {tuple(positions.shape)}")
+        if positions.device != device:
+            raise ValueError(f"positions is on {positions.device}, the call runs on {device}")
+        if positions.dtype != torch.int32 or tokens > 1 and positions.stride(1) != 1:
+            positions = _as(positions, torch.int32, device, "positions")
+        return positions, positions.stride(0), positions.shape[0], a.data_ptr()
 
 
 def rope_frequencies(rot_dim, base=10000.0, scaling=None, stretch=1.0, original=4096,
@@ -123,6 +144,35 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=None, stretch=1.0, original=
     _tq._check(_tq.lib().tq_rope_frequencies(rot_dim, base, ROPE_SCALING[scaling], stretch,
                                              original, f.ctypes.data, ctypes.addressof(gain)))
     return Rope(torch.from_numpy(f).to(device), rot_dim, interleaved, gain.value)
+
+
+def rope_axes(sections, base=10000.0, order="blocks", restart=False, scaling=None, stretch=1.0,
+              original=4096, interleaved=False, device="cuda"):
+    """A Rope for positions of several axes (time, height, width): sections[a] pairs turn by axis a.
+    order "blocks": the first sections[0] pairs, then the next; "cycle": the axes take pairs in
+    turn, an axis that has its pairs being passed over. The frequencies run over all pairs as in
+    rope_frequencies(2 * sum(sections), ...) or, restart, over each axis' own (2 * sections[a])."""
+    sections = [int(n) for n in sections]
+    if not 1 <= len(sections) <= 255 or min(sections) < 0 or sum(sections) < 1:
+        raise ValueError("sections must be 1 to 255 numbers of pairs, together at least 1")
+    if order not in ("blocks", "cycle"):
+        raise ValueError("order must be 'blocks' or 'cycle'")
+    axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    if order == "cycle":
+        axis = [a for _, a in sorted((i, a) for a, n in enumerate(sections) for i in range(n))]
+    make = lambda rot: rope_frequencies(rot, base, scaling, stretch, original, device="cpu")  # noqa: E731
+    if restart:
+        own = [make(2 * n) if n else None for n in sections]
+        gain = next(r.gain for r in own if r is not None)
+        inv_freq, seen = torch.empty(len(axis), dtype=torch.float64), [0] * len(sections)
+        for i, a in enumerate(axis):
+            inv_freq[i] = own[a].inv_freq[seen[a]]
+            seen[a] += 1
+    else:
+        whole = make(2 * len(axis))
+        inv_freq, gain = whole.inv_freq, whole.gain
+    return Rope(inv_freq.to(device), 2 * len(axis), interleaved, gain,
+                torch.tensor(axis, dtype=torch.uint8, device=device))
 
 
 def _head_strides(t, name):
@@ -186,14 +236,18 @@ def _vectors_meet(x, y):
 def rope(x, positions, rope, transposed=False, out=None):
     """x ([tokens, heads, head_dim], the elements of a head contiguous, any token and head
     strides) with rotary positions applied. out=x turns it in place; another out= must not
-    overlap x. transposed: the negative angle (the gradient of the call). Not recorded by
+    overlap x. positions: int [tokens], or [axes, tokens] where the rope has several axes.
+    transposed: the negative angle (the gradient of the call). Not recorded by
     autograd: refused where x requires grad, unless under torch.no_grad() (as in the forward of an
     autograd.Function, whose backward is the transposed call)."""
     if x.requires_grad or out is not None and out.requires_grad:
         _no_gradient("rope")
     xs = _head_strides(x, "x")
     dev = x.device
-    positions = _as(positions, torch.int32, dev, "positions", (x.shape[0],))
+    if rope.axis is None:
+        positions = _as(positions, torch.int32, dev, "positions", (x.shape[0],))
+    else:
+        positions, apart, axes, axis = rope.axes(positions, x.shape[0], dev)
     if out is None:
         out = torch.empty_like(x)  # (half a microsecond less than torch.empty)
         if not out.is_contiguous():
@@ -208,6 +262,11 @@ def rope(x, positions, rope, transposed=False, out=None):
     else:
         os_ = _head_strides(out, "out")
     r = rope.desc(dev)
+    if rope.axis is not None:
+        _call(dev, _tq.lib().tq_rope_axes, x.data_ptr(), _tq._dt(x), x.shape[0], x.shape[1], x.shape[2],
+              xs[0], xs[1], positions.data_ptr(), apart, axes, axis, r, _TRANSPOSED if transposed else 0,
+              out.data_ptr(), os_[0], os_[1])
+        return out
     _call(dev, _tq.lib().tq_rope, x.data_ptr(), _tq._dt(x), x.shape[0], x.shape[1], x.shape[2],
           xs[0], xs[1], positions.data_ptr(), r, _TRANSPOSED if transposed else 0, out.data_ptr(),
           os_[0], os_[1])
@@ -265,7 +324,8 @@ def kv_cache(pages, heads, head_dim, page_tokens=64, k_levels=256, v_levels=8, k
 def kv_store(cache, k, v, slots, rope=None, positions=None):
     """Quantize the new tokens' keys and values ([tokens, heads, head_dim], the elements of a
     head contiguous) into their slots of the cache (a slot outside it, such as -1, is skipped;
-    each other one at most once); with rope, the keys are turned at `positions` first."""
+    each other one at most once); with rope, the keys are turned at `positions` first ([tokens], or
+    [axes, tokens] where the rope has several axes)."""
     dev = cache.device
     n = k.shape[0]
     shape = (n, cache.heads, cache.head_dim)
@@ -279,6 +339,12 @@ def kv_store(cache, k, v, slots, rope=None, positions=None):
     if rope is not None:
         if positions is None:
             raise ValueError("rope needs the tokens' positions")
+        if rope.axis is not None:
+            positions, apart, axes, axis = rope.axes(positions, n, dev)
+            _call(dev, _tq.lib().tq_kv_store_axes, cache.desc, k.data_ptr(), v.data_ptr(), _tq._dt(k), n,
+                  ks[0], ks[1], vs[0], vs[1], slots.data_ptr(), rope.desc(dev), positions.data_ptr(), apart,
+                  axes, axis)
+            return
         positions = _as(positions, torch.int32, dev, "positions", (n,))
         r, pos = rope.desc(dev), positions.data_ptr()
     _call(dev, _tq.lib().tq_kv_store, cache.desc, k.data_ptr(), v.data_ptr(), _tq._dt(k), n, ks[0],

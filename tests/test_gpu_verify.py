@@ -1,0 +1,328 @@
+"""Verification of drafted tokens on the GPU against the oracle: whole numbers, equal wherever the oracle's
+decisions are clear.
+
+A decision compares two numbers that the kernel computes in fp64 from sums of up to 2^18 terms: an
+exponential is off by at most 1e-15 of itself plus 2^-52 |t| for its exponent t (in bits, below 1100), a sum
+of n terms by log2(n) + 16 roundings for sums joined pairwise and by n / 256 for a thread's own, all
+2^-53: together below 1e-12 of what is compared. The oracle returns the smallest relative distance of
+its decisions to their borders; where that is below 1e-12 either side is right.
+"""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import rotation_lloyd_max_amd as tq
+from oracle import step as ost
+from parity import as_f64
+
+pytestmark = pytest.mark.gpu
+DTS = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
+CLEAR = 1e-12
+
+
+def case(seed, B, most, V, tdt="bf16", ddt="bf16", kind="logits", tree=False, ragged=True, temperature=None, spread=3.0, noise=0.6,
+         hide=0.0):
+    """Inputs as a program has them: the draft's values are the target's with noise, drafted tokens
+    drawn from its distribution."""
+    g = np.random.default_rng([seed, B, most, V])
+    counts = g.integers(0, most + 1, B) if ragged else np.full(B, most)
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    M = int(offsets[-1])
+    parents = np.concatenate([[0] + [int(g.integers(max(0, i - 4), i)) for i in range(1, c)] if c else [] for c in counts]
+                             or [[]]).astype(np.int64)
+    x = g.standard_normal((M, V)).astype(np.float32) * spread
+    y = x + g.standard_normal((M, V)).astype(np.float32) * noise
+    if hide:
+        gone = g.random((M, V)) < hide
+        gone[np.arange(M), g.integers(0, V, M)] = False
+        x, y = np.where(gone, -np.inf, x).astype(np.float32), np.where(gone, -np.inf, y).astype(np.float32)
+    if kind == "probabilities":
+        x, y = (torch.softmax(torch.from_numpy(z), -1).numpy() if M else z for z in (x, y))
+    t = torch.from_numpy(x).to(DTS[tdt])
+    d = None if ddt is None else torch.from_numpy(y).to(DTS[ddt])
+    tokens = np.zeros(M, np.int64)
+    src = y if d is None else as_f64(d)
+    for b in range(B):
+        for i in range(1, counts[b]):
+            up = offsets[b] + (parents[offsets[b] + i] if tree else i - 1)
+            z = np.log(np.maximum(src[up], 1e-300)) if kind == "probabilities" else src[up] / 1.0
+            tokens[offsets[b] + i] = np.argmax(z + g.gumbel(size=V))
+    u = g.random(M).astype(np.float32)
+    if isinstance(temperature, str):
+        temperature = g.random(B).astype(np.float32) * 0.8 + 0.5
+        temperature[::3] = 0.0
+    return dict(target=t, tokens=tokens, uniforms=u, offsets=offsets, draft=d, parents=parents if tree else None,
+                temperature=temperature, target_kind=kind, draft_kind=kind)
+
+
+def on_gpu(c):
+    put = lambda x, dt: None if x is None else torch.as_tensor(x).to(dt).cuda()  # noqa: E731
+    t = lambda x: None if x is None else x if x.is_cuda else x.cuda()  # noqa: E731
+    return dict(target=t(c["target"]), tokens=put(c["tokens"], torch.int32), uniforms=put(c["uniforms"], torch.float32),
+                offsets=put(c["offsets"], torch.int32), draft=t(c["draft"]), parents=put(c["parents"], torch.int32),
+                temperature=put(c["temperature"], torch.float32), target_kind=c["target_kind"], draft_kind=c["draft_kind"])
+
+
+def reference(c):
+    f = lambda x: None if x is None else as_f64(x)  # noqa: E731
+    return ost.verify(**{**c, "target": f(c["target"]), "draft": f(c["draft"]),
+                         "uniforms": np.asarray(c["uniforms"], np.float32).astype(np.float64),
+                         "temperature": None if c["temperature"] is None else np.asarray(c["temperature"], np.float32)})
+
+
+def check(c, got=None):
+    kept, tokens, path, margin = reference(c)
+    if got is None:
+        got = tq.verify(**on_gpu(c))
+    torch.cuda.synchronize()
+    assert margin > CLEAR, "the inputs of this test leave a decision open"
+    assert np.array_equal(got.kept.cpu().numpy(), kept), (got.kept.tolist(), kept)
+    end = int(c["offsets"][-1])
+    assert np.array_equal(got.path.cpu().numpy()[:end], path[:end])
+    assert np.array_equal(got.tokens.cpu().numpy()[:end], tokens[:end])
+    return got
+
+
+@pytest.mark.parametrize("tdt,ddt", [("bf16", "bf16"), ("fp32", "fp16"), ("fp16", None), ("bf16", "fp32"), ("fp32", None)])
+@pytest.mark.parametrize("kind", ["logits", "probabilities"])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("V", [1, 2, 7, 64, 255, 257, 2049, 10007])
+def test_matches_oracle(tdt, ddt, kind, tree, V):
+    check(case(1, 9, 9, V, tdt, ddt, kind, tree, temperature="mixed"))
+    check(case(2, 5, 13, V, tdt, ddt, kind, tree, noise=2.5))
+
+
+@pytest.mark.parametrize("V", [8191, 8192, 16385, 50257, 131072, 262147])
+@pytest.mark.parametrize("tree,ddt", [(False, "bf16"), (True, "fp16"), (True, None)])
+def test_large_vocabularies(V, tree, ddt):
+    check(case(3, 3, 6, V, "bf16", ddt, "logits", tree, temperature=np.array([0.7, 1.0, 1.3], np.float32)))
+    check(case(4, 1, 1, V, "fp32", ddt, "logits", tree))
+    check(case(5, 2, 5, V, "fp32", ddt, "probabilities", tree, ragged=False))
+
+
+def test_many_sequences_and_long_chains():
+    check(case(6, 300, 4, 500, noise=0.1))
+    check(case(7, 130, 3, 4001, "fp16", None))
+    check(case(8, 2, 300, 300, noise=0.02, ragged=False))
+    check(case(9, 2, 300, 300, "fp32", None, tree=True, ragged=False, spread=12.0))
+    check(case(10, 1, 200, 1000, tree=True, noise=0.05, ragged=False))
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("ddt", ["bf16", None])
+def test_masked_vocabularies(tree, ddt):
+    # logits of -inf nearly everywhere, whole first and last pieces among them
+    check(case(11, 6, 6, 5003, "bf16", ddt, tree=tree, hide=0.99))
+    c = case(12, 4, 5, 40000, "fp32", "fp32" if ddt else None, tree=tree)
+    for t in (c["target"], c["draft"]):
+        if t is not None:
+            t[:, :33000] = -np.inf
+            t[:, 39000:] = -np.inf
+    c["tokens"] = np.where(c["tokens"] < 33000, 33000 + c["tokens"] % 6000, c["tokens"])
+    check(c)
+    c["target"][:, 33000:38999] = -np.inf       # one token is left
+    c["tokens"][1::2] = 38999
+    got = check(c)
+    end, kept = c["offsets"], got.kept.tolist()
+    assert all(got.tokens[end[b] + k - 1].item() == 38999 for b, k in enumerate(kept) if k)
+
+
+def test_values_of_any_size():
+    for dt, big in (("fp32", 3e38), ("bf16", 3e38), ("fp16", 65504.0)):
+        c = case(13, 6, 5, 300, dt, dt, temperature=np.array([1.0, 1e30, 0.3, 1e-3, 100.0, 1.0], np.float32))
+        c["target"][::2, 100:103] = big
+        c["target"][1::2] *= 1000.0
+        c["draft"][::3] *= 500.0
+        c["target"][2] = -c["target"][2].abs() * 100.0 - 5000.0
+        kept, tokens, path, margin = reference(c)
+        got = tq.verify(**on_gpu(c))
+        torch.cuda.synchronize()
+        # three equal largest values: thirds, which u meets only by chance; others as always
+        assert margin > CLEAR and np.array_equal(got.tokens.cpu().numpy(), tokens) and np.array_equal(got.kept.cpu().numpy(), kept)
+
+
+@pytest.mark.parametrize("T", [0.0, -1.0, float("nan"), float("inf"), 1e-38, 1e-44, 1e38])
+def test_temperatures(T):
+    for ddt in ("fp16", None):
+        c = case(14, 5, 6, 777, "fp16", ddt, temperature=np.full(5, T, np.float32), noise=0.2)
+        check(c)
+        c["target"][:, 5:500] = -np.inf
+        check(c)
+    c = case(15, 5, 6, 777, "fp32", "fp32", "probabilities", temperature=np.full(5, T, np.float32))
+    check(c)
+
+
+def test_greedy_takes_the_first_of_equal_values_whatever_the_numbers():
+    c = case(16, 6, 7, 3000, "bf16", "bf16", spread=0.3, temperature=np.zeros(6, np.float32))    # many equal values in bf16
+    c["target"] = torch.round(c["target"].float() * 2).to(torch.bfloat16)
+    for r in range(0, len(c["tokens"]) - 1, 2):
+        c["tokens"][r + 1] = int(np.argmax(as_f64(c["target"])[r]))
+    check(c)
+    for u in (1.0, float("nan"), -3.0):
+        c["uniforms"][:] = u
+        check(c)
+
+
+def test_rows_that_are_no_distribution():
+    for bad in (float("nan"), float("inf")):
+        for where in ("target", "draft"):
+            for place in (0, 1500, 2999):
+                for T in (None, np.array([0.8, 0.0, 1.0, 0.0, 1.2], np.float32)):
+                    c = case(17, 5, 4, 3000, "fp32", "bf16", noise=0.01, ragged=False, temperature=T)
+                    c[where][1::3, place] = bad
+                    check(c)
+    c = case(18, 5, 4, 3000, "fp32", "bf16", noise=0.01, ragged=False)
+    c["target"][5] = -np.inf
+    c["draft"][8] = -np.inf
+    got = check(c)
+    assert (got.tokens == -1).sum() > 0
+    # probabilities: of the row that the new token comes from
+    for bad in (float("nan"), float("inf")):
+        c = case(19, 4, 1, 3000, "fp32", None, "probabilities", ragged=False)
+        c["target"][2, 777] = bad
+        c["target"][3] = 0.0
+        got = check(c)
+        assert got.tokens.tolist()[2:] == [-1, -1]
+
+
+def test_numbers_at_their_ends():
+    c = case(20, 8, 4, 1200, "fp32", "fp32", ragged=False)
+    for u in (0.0, 1.0 - 2.0 ** -24):
+        c["uniforms"][:] = u
+        check(c)
+    # beyond the ends: nothing is accepted, the last token with weight; below: all, the first
+    for kind in ("logits", "probabilities"):
+        c = case(21, 8, 4, 1200, "fp32", "fp32", kind, ragged=False, hide=0.3 if kind == "logits" else 0.0)
+        for u in (1.0, 2.0, float("nan"), -1.0):
+            c["uniforms"][:] = u
+            got = tq.verify(**on_gpu(c))
+            kept, tokens, path, _ = reference(c)
+            torch.cuda.synchronize()
+            assert np.array_equal(got.kept.cpu().numpy(), kept) and np.array_equal(got.path.cpu().numpy(), path)
+
+
+def test_nothing_left_falls_back_to_the_target():
+    # equal distributions whose tokens are turned away by u = 1, and a point mass turned away
+    c = case(22, 4, 2, 50, "fp32", "fp32", ragged=False, noise=0.0)
+    c["uniforms"][1::2] = 1.0
+    check(c)
+    c = case(23, 3, 2, 50, "fp32", None, "probabilities", ragged=False)
+    c["target"][:] = 0.0
+    c["target"][:, 7] = 1.0
+    c["tokens"][:] = 7
+    c["uniforms"][1::2] = 1.0
+    got = check(c)
+    assert got.kept.tolist() == [1, 1, 1] and got.tokens[::2].tolist() == [7, 7, 7]
+
+
+def test_padding_duplicates_and_parents_that_are_none():
+    for ddt in ("bf16", None):
+        c = case(24, 6, 9, 40, "bf16", ddt, tree=True, spread=1.0, ragged=False)
+        c["tokens"][3::5] = -1
+        c["tokens"][4::7] = 40
+        c["tokens"][1::9] = c["tokens"][2::9]
+        c["parents"][2::9] = c["parents"][1::9] = 0
+        c["parents"][5::9] = 7
+        c["parents"][6::9] = -1
+        check(c)
+        c["parents"][:] = 0          # eight children of the root, few tokens: the same one several times
+        check(c)
+
+
+@pytest.mark.parametrize("tdt,ddt", [("bf16", "fp16"), ("fp32", "bf16"), ("fp16", "fp32")])
+def test_strides_and_odd_addresses(tdt, ddt):
+    c = case(25, 5, 5, 4097, tdt, ddt)
+    g = on_gpu(c)
+    for shift in (0, 1, 3):
+        for name in ("target", "draft"):
+            t = c[name]
+            wide = torch.full((t.shape[0], t.shape[1] + 5 + shift), float("nan"), dtype=t.dtype, device="cuda")
+            wide[:, shift:shift + t.shape[1]] = t.cuda()
+            g[name] = wide[:, shift:shift + t.shape[1]]
+        check(c, tq.verify(**g))
+    one = on_gpu(case(26, 3, 1, 1000, tdt, None, ragged=False))
+    one["target"] = one["target"][:1].expand(3, -1)       # one row for every sequence
+    got = tq.verify(**one)
+    assert got.kept.tolist() == [1, 1, 1]
+
+
+def test_rows_behind_the_last_sequence_are_left():
+    c = case(27, 4, 5, 600, ragged=False)
+    g = on_gpu(c)
+    g["offsets"][2:] -= 3
+    M = 20
+    out = [torch.full((n,), 1234, dtype=torch.int32, device="cuda") for n in (4, M, M)]
+    need = tq.verify_workspace(600, 4, M, True)
+    ws = torch.empty(max(1, need), dtype=torch.uint8, device="cuda")
+    rc = tq.lib().tq_verify(g["target"].data_ptr(), tq.BF16, 600, g["draft"].data_ptr(), tq.BF16, 600, 0, 600, 4,
+                            g["offsets"].data_ptr(), M, g["tokens"].data_ptr(), None, g["uniforms"].data_ptr(), None,
+                            out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), ws.data_ptr(), need,
+                            torch.cuda.current_stream().cuda_stream)
+    assert rc == 0, tq.lib().tq_last_error()
+    torch.cuda.synchronize()
+    assert (out[1][17:] == 1234).all() and (out[2][17:] == 1234).all() and not (out[1][:17] == 1234).any()
+    c["offsets"] = g["offsets"].cpu().numpy()
+    kept, tokens, path, _ = reference(c)
+    assert np.array_equal(out[0].cpu().numpy(), kept) and np.array_equal(out[1][:17].cpu().numpy(), tokens[:17])
+
+
+def test_no_rows():
+    e = torch.empty
+    for B in (0, 3):
+        got = tq.verify(e((0, 100), device="cuda"), e(0, dtype=torch.int32, device="cuda"), e(0, device="cuda"),
+                        torch.zeros(B + 1, dtype=torch.int32, device="cuda"))
+        torch.cuda.synchronize()
+        assert got.kept.tolist() == [0] * B
+
+
+def test_repeated_calls_streams_and_graphs():
+    # replays over new inputs, two graphs and eager calls in turn, each with a workspace of its own
+    cs = [case(s, 7, 6, 9001, "bf16", "bf16" if s % 2 else None, tree=s > 29) for s in (28, 29, 30, 31)]
+    gs = [on_gpu(c) for c in cs]
+    want = [check(c) for c in cs]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        other = [tq.verify(**g) for g in gs]
+    st.synchronize()
+    for a, b, c in zip(want, other, cs):
+        end = int(c["offsets"][-1])
+        assert torch.equal(a.kept, b.kept) and torch.equal(a.tokens[:end], b.tokens[:end])
+    graphs, outs = [], []
+    for g in gs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(tq.verify(**g))
+        graphs.append(graph)
+    for turn in range(3):
+        for g in gs:
+            g["uniforms"].copy_(torch.rand_like(g["uniforms"]))
+        for graph, g, o in zip(graphs, gs, outs):
+            graph.replay()
+            eager = tq.verify(**g)
+            torch.cuda.synchronize()
+            end = g["offsets"][-1].item()
+            assert torch.equal(o.kept, eager.kept) and torch.equal(o.tokens[:end], eager.tokens[:end])
+            assert torch.equal(o.path[:end], eager.path[:end])
+
+
+def test_frequencies_follow_the_target():
+    # 4000 sequences over one pair of distributions: counts of the first new token against p, each within
+    # five standard deviations of its binomial count
+    g = np.random.default_rng(33)
+    V, n = 24, 4000
+    x, y = g.standard_normal(V) * 1.5, g.standard_normal(V) * 1.5
+    p, q = (np.exp(z) / np.exp(z).sum() for z in (x, y))
+    for parents, rows in ((None, 2), (np.tile([0, 0, 0, 0], n), 4)):
+        tokens = np.zeros((n, rows), np.int64)
+        tokens[:, 1:] = g.choice(V, (n, rows - 1), p=q)
+        put = lambda z: torch.from_numpy(z.astype(np.float32)).cuda().expand(n * rows, -1)  # noqa: E731
+        got = tq.verify(put(x), torch.from_numpy(tokens.reshape(-1)).cuda(),
+                        torch.from_numpy(g.random(n * rows).astype(np.float32)).cuda(),
+                        torch.arange(0, n * rows + 1, rows, device="cuda"), draft=put(y),
+                        parents=None if parents is None else torch.from_numpy(parents).cuda())
+        first = np.bincount(got.tokens.view(n, rows)[:, 0].cpu().numpy(), minlength=V)
+        assert np.all(np.abs(first - n * p) <= 5 * np.sqrt(n * p * (1 - p)) + 1)
