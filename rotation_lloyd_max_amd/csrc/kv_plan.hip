@@ -84,11 +84,12 @@ __device__ __forceinline__ uint32_t step_free(const int32_t* state, int pages) {
   return n < 0 ? 0 : n < pages ? n : pages;
 }
 
-// Whether this workgroup is the last of the launch to come here.
+// Whether this workgroup is the last of the launch to come here. Nothing passes between them but the order:
+// what the last one overwrites the others have read.
 __device__ __forceinline__ bool step_last(int32_t* state, int& shared) {
   __syncthreads();
   if (threadIdx.x == 0)
-    shared = __hip_atomic_fetch_add(state + 1, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    shared = __hip_atomic_fetch_add(state + 1, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   return shared == static_cast<int>(gridDim.x) - 1;
 }

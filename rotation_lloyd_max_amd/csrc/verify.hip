@@ -21,6 +21,8 @@
 namespace tq {
 namespace {
 
+#define TQ_INLINE __attribute__((always_inline))
+
 constexpr int kVerifyThreads = 256;
 constexpr int kBlockElems = 512;    // a wave's step: 8 elements a lane
 constexpr int kWindow = 256;        // rows whose probabilities are in LDS at a time
@@ -92,11 +94,36 @@ __device__ __forceinline__ void load8_end(const char* row, int i, int V, float n
 #pragma unroll
   for (int k = 0; k < 8; ++k) f[k] = i + k < V ? load_elem<DT>(row, i + k) : none;
 }
+// The same for a type known at run time; one piece of code for all types and ends.
 __device__ __forceinline__ void load8_any(const char* row, int dt, int i, int V, float none, float (&f)[8]) {
-  const bool whole = i + 8 <= V;
-  if (dt == 0) whole ? load8<0>(row, i, f) : load8_end<0>(row, i, V, none, f);
-  else if (dt == 1) whole ? load8<1>(row, i, f) : load8_end<1>(row, i, V, none, f);
-  else whole ? load8<2>(row, i, f) : load8_end<2>(row, i, V, none, f);
+  uint32_t x[8];
+  if (dt == 0 && i + 8 <= V) {
+    const u32x4_a2 a = *reinterpret_cast<const u32x4_a2*>(row + static_cast<int64_t>(i) * 4);
+    const u32x4_a2 b = *reinterpret_cast<const u32x4_a2*>(row + static_cast<int64_t>(i) * 4 + 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[k] = a[k];
+      x[4 + k] = b[k];
+    }
+  } else if (dt == 0) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = reinterpret_cast<const uint32_t*>(row)[i + k < V ? i + k : V - 1];
+  } else if (i + 8 <= V) {
+    const u32x4_a2 a = *reinterpret_cast<const u32x4_a2*>(row + static_cast<int64_t>(i) * 2);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[2 * k] = a[k] & 0xffffu;
+      x[2 * k + 1] = a[k] >> 16;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = reinterpret_cast<const uint16_t*>(row)[i + k < V ? i + k : V - 1];
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    f[k] = dt == 0 ? __uint_as_float(x[k]) : dt == 1 ? __uint_as_float(x[k] << 16) : half_bits_to_float(static_cast<uint16_t>(x[k]));
+    f[k] = i + k < V ? f[k] : none;
+  }
 }
 
 __device__ __forceinline__ void fill_table(double* tab) {
@@ -293,37 +320,50 @@ __global__ __launch_bounds__(kVerifyThreads) void k_verify_stats(VerifyParams p,
 
 // ---- rows as distributions ------------------------------------------------------------------
 
+// Probabilities of a row of logits: 2^((x - ref) c) zinv; zinv NaN: the row is no distribution.
 struct Dist {
-  const char* row;
-  double c, ref, zinv;  // logits: 2^((x - ref) c) zinv; NaN for a row that is none
+  double ref, zinv;
 };
 
-__device__ __forceinline__ double value_of(const Side& s, const Dist& d, int i, const double* tab) {
-  const double x = load_any(d.row, s.dt, i);
+__device__ __forceinline__ double probability(const Side& s, const Dist& d, double c, float x, const double* tab) {
   if (s.probs) return x;
-  const double t = (x - d.ref) * d.c;
-  return (t <= -1000.0 || x == -__builtin_inf() ? 0.0 : add_exp2(t, 0.0, tab)) * d.zinv;
+  const double t = (x - d.ref) * c;
+  return (t <= -1000.0 || x == -__builtin_inff() ? 0.0 : add_exp2(t, 0.0, tab)) * d.zinv;
 }
 
-// Row `row` of one side from its pieces, by `lanes` neighbouring lanes (a power of two).
-__device__ __forceinline__ Dist dist_of(const VerifyParams& p, const Side& s, int row, double c, int lanes, const double* tab) {
-  Dist d;
-  d.row = s.data + row * s.stride;
-  d.c = c;
-  d.ref = 0.0;
-  d.zinv = 1.0;
+// Row `row` of one side from its pieces, by LANES neighbouring lanes.
+template <int LANES>
+__device__ __forceinline__ Dist dist_of(const VerifyParams& p, const Side& s, int row, double c, const double* tab) {
+  Dist d{0.0, 1.0};
   if (s.probs) return d;
+  constexpr int HELD = 4;
   const StatPart* st = s.stat + static_cast<int64_t>(row) * p.parts;
-  const int l = threadIdx.x & (lanes - 1);
-  float top = -__builtin_inff();
-  for (int k = l; k < p.parts; k += lanes) top = __builtin_elementwise_maximum(top, st[k].top);
-  for (int m = lanes >> 1; m; m >>= 1) top = __builtin_elementwise_maximum(top, __shfl_xor(top, m));
+  const int l = threadIdx.x & (LANES - 1);
+  const float inf = __builtin_inff();
+  StatPart held[HELD];
+#pragma unroll
+  for (int k = 0; k < HELD; ++k) {
+    held[k] = StatPart{0.0, -inf, 0};
+    if (l + k * LANES < p.parts) held[k] = st[l + k * LANES];
+  }
+  float top = -inf;
+#pragma unroll
+  for (int k = 0; k < HELD; ++k) top = __builtin_elementwise_maximum(top, held[k].top);
+  for (int k = l + HELD * LANES; k < p.parts; k += LANES) top = __builtin_elementwise_maximum(top, st[k].top);
+#pragma unroll
+  for (int m = LANES >> 1; m; m >>= 1) top = __builtin_elementwise_maximum(top, __shfl_xor(top, m));
   double z = 0.0;
-  for (int k = l; k < p.parts; k += lanes) {
+#pragma unroll
+  for (int k = 0; k < HELD; ++k) {
+    const double f = add_exp2((static_cast<double>(held[k].top) - top) * c, 0.0, tab);
+    z += held[k].z == 0.0 ? 0.0 : held[k].z * f;
+  }
+  for (int k = l + HELD * LANES; k < p.parts; k += LANES) {
     const StatPart q = st[k];
     if (q.z != 0.0) z += q.z * add_exp2((static_cast<double>(q.top) - top) * c, 0.0, tab);
   }
-  for (int m = lanes >> 1; m; m >>= 1) z += __shfl_xor(z, m);
+#pragma unroll
+  for (int m = LANES >> 1; m; m >>= 1) z += __shfl_xor(z, m);
   d.ref = top;
   d.zinv = z > 0.0 && z < __builtin_inf() ? 1.0 / z : __builtin_nan("");
   return d;
@@ -334,59 +374,46 @@ __device__ __forceinline__ int largest_of(const VerifyParams& p, int row) {
   const StatPart* st = p.t.stat + static_cast<int64_t>(row) * p.parts;
   const int lane = threadIdx.x & 63;
   float top = -__builtin_inff();
-  bool bad = false;
-  for (int k = lane; k < p.parts; k += 64) {
-    bad |= st[k].z != 0.0;
-    top = __builtin_elementwise_maximum(top, st[k].top);
-  }
-  top = wave_max(top);
   int at = 0x7fffffff;
-  for (int k = lane; k < p.parts; k += 64)
-    if (st[k].top == top && st[k].at < at) at = st[k].at;
+  bool bad = false;
+  for (int k = lane; k < p.parts; k += 64) {  // (ascending: the first of equal ones stays)
+    const StatPart q = st[k];
+    bad |= q.z != 0.0;
+    if (q.top > top) {
+      top = q.top;
+      at = q.at;
+    }
+  }
+  const float most = wave_max(top);
+  if (top != most) at = 0x7fffffff;
 #pragma unroll
   for (int s = 32; s; s >>= 1) {
     const int o = __shfl_xor(at, s);
     at = o < at ? o : at;
   }
-  if (__ballot(bad) || !(top > (p.t.probs ? 0.f : -__builtin_inff()))) return -1;
-  return at;
+  return __ballot(bad) || !(most > (p.t.probs ? 0.f : -__builtin_inff())) ? -1 : at;
 }
 
 // ---- weights ----------------------------------------------------------------------------------
 
-// What the new token is drawn from (or S is summed over).
+// What the new token is drawn from (or S is summed over): p, or (p - al q)+.
 struct Weights {
+  const char *prow, *qrow;  // qrow null: p
   Dist p, q;
-  double al;        // (p - al q)+ where drafted
-  bool drafted;
-  int ngone;        // tokens taken out of p; more than kGone: look among the rows
+  double c, al;
 };
 
 // w of elements i .. i + 7 (0 behind the row).
 __device__ __forceinline__ void weights8(const VerifyParams& p, const Weights& w, int i, const double* tab, double (&v)[8]) {
   const float none = -__builtin_inff();
-  float f[8];
-  load8_any(w.p.row, p.t.dt, i, p.a.V, p.t.probs ? 0.f : none, f);
+  float f[8], g[8];
+  load8_any(w.prow, p.t.dt, i, p.a.V, p.t.probs ? 0.f : none, f);
+  if (w.qrow) load8_any(w.qrow, p.d.dt, i, p.a.V, p.d.probs ? 0.f : none, g);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if (p.t.probs) {
-      v[k] = f[k];
-    } else {
-      const double t = (f[k] - w.p.ref) * w.p.c;
-      v[k] = t <= -1000.0 || f[k] == none ? 0.0 : add_exp2(t, 0.0, tab) * w.p.zinv;
-    }
-  }
-  if (w.drafted) {
-    load8_any(w.q.row, p.d.dt, i, p.a.V, p.d.probs ? 0.f : none, f);
+  for (int k = 0; k < 8; ++k) v[k] = probability(p.t, w.p, w.c, f[k], tab);
+  if (w.qrow) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      double q = f[k];
-      if (!p.d.probs) {
-        const double t = (f[k] - w.q.ref) * w.q.c;
-        q = t <= -1000.0 || f[k] == none ? 0.0 : add_exp2(t, 0.0, tab) * w.q.zinv;
-      }
-      v[k] = __builtin_fma(-w.al, q, v[k]);
-    }
+    for (int k = 0; k < 8; ++k) v[k] = __builtin_fma(-w.al, probability(p.d, w.q, w.c, g[k], tab), v[k]);
   }
 #pragma unroll
   for (int k = 0; k < 8; ++k) v[k] = v[k] < 0.0 ? 0.0 : v[k];
@@ -396,8 +423,10 @@ __device__ __forceinline__ void weights8(const VerifyParams& p, const Weights& w
 
 struct WalkShared {
   double px[kWindow], qx[kWindow], u[kWindow];
-  int parent[kWindow], token[kWindow], gone[kGone];
-  double tab[kTable], red[64];
+  Dist p[kWindow], q[kWindow];  // of the row's parent
+  int parent[kWindow], token[kWindow];
+  double tab[kTable], red[32];
+  int pick[32];
 };
 
 __device__ __forceinline__ int parent_of(const VerifyArgs& a, int lo, int r) { return a.parents ? a.parents[lo + r] : r - 1; }
@@ -434,14 +463,19 @@ __device__ __forceinline__ Walked walk(const VerifyParams& p, WalkShared& sh, in
     constexpr int LANES = 16;
     for (int r = w0 + static_cast<int>(threadIdx.x) / LANES; r < w1; r += NT / LANES) {
       const int up = parent_of(a, lo, r), x = a.tokens[lo + r];
+      const float u = a.uniforms[lo + r];
       const bool any = r > 0 && up >= 0 && up < r && x >= 0 && x < a.V;
+      Dist t{0.0, 1.0}, q{0.0, 1.0};
       double px = 0.0, qx = 0.0;
       if (any && !greedy) {
-        const Dist t = dist_of(p, p.t, lo + up, c, LANES, sh.tab);
-        px = value_of(p.t, t, x, sh.tab);
+        const float xt = load_any(p.t.data + (lo + up) * p.t.stride, p.t.dt, x);
+        float xd = 0.f;
+        if (drafted) xd = load_any(p.d.data + (lo + up) * p.d.stride, p.d.dt, x);
+        t = dist_of<LANES>(p, p.t, lo + up, c, sh.tab);
+        px = probability(p.t, t, c, xt, sh.tab);
         if (drafted) {
-          const Dist q = dist_of(p, p.d, lo + up, c, LANES, sh.tab);
-          qx = value_of(p.d, q, x, sh.tab);
+          q = dist_of<LANES>(p, p.d, lo + up, c, sh.tab);
+          qx = probability(p.d, q, c, xd, sh.tab);
         }
       }
       if ((threadIdx.x & (LANES - 1)) == 0) {
@@ -449,7 +483,9 @@ __device__ __forceinline__ Walked walk(const VerifyParams& p, WalkShared& sh, in
         sh.token[r - w0] = x;
         sh.px[r - w0] = px;
         sh.qx[r - w0] = qx;
-        sh.u[r - w0] = a.uniforms[lo + r];
+        sh.u[r - w0] = u;
+        sh.p[r - w0] = t;
+        sh.q[r - w0] = q;
       }
     }
     __syncthreads();
@@ -488,7 +524,7 @@ __device__ __forceinline__ Walked walk(const VerifyParams& p, WalkShared& sh, in
         S = 1.0;
         if (greedy) largest = largest_of(p, lo + r);
       } else {
-        ++w.tried;
+        w.tried = r;
         if (drafted) {
           w.al += S;
           if constexpr (SUMS) {
@@ -526,12 +562,14 @@ __global__ __launch_bounds__(kWalkThreads) void k_verify_walk(VerifyParams p) {
   if (hi == lo) return;
   fill_table(sh.tab);
   const double T = temperature_of(a, b);
-  auto sum = [&](int cur, double al) {
+  auto sum = [&](int cur, double al) TQ_INLINE {
     Weights w;
-    w.p = dist_of(p, p.t, lo + cur, scale_of(T), 64, sh.tab);
-    w.q = dist_of(p, p.d, lo + cur, scale_of(T), 64, sh.tab);
+    w.c = scale_of(T);
+    w.prow = p.t.data + (lo + cur) * p.t.stride;
+    w.qrow = p.d.data + (lo + cur) * p.d.stride;
+    w.p = dist_of<64>(p, p.t, lo + cur, w.c, sh.tab);
+    w.q = dist_of<64>(p, p.d, lo + cur, w.c, sh.tab);
     w.al = al;
-    w.drafted = true;
     double s = 0.0, v[8];
     for (int i = threadIdx.x * 8; i < a.V; i += kWalkThreads * 8) {
       weights8(p, w, i, sh.tab, v);
@@ -555,17 +593,18 @@ __global__ __launch_bounds__(kWalkThreads) void k_verify_walk(VerifyParams p) {
 
 // ---- the new token ----------------------------------------------------------------------------
 
-// The first k < count with get(0) + .. + get(k) > u total (the last with get(k) > 0 if there is none), and
-// the sum before it; -1 if the total is not above 0 and finite. By all threads of the workgroup.
-template <typename F>
-__device__ __forceinline__ int locate(WalkShared& sh, int count, F get, double u, double& total, double& before, double& goal) {
+// The first of k0 <= k < k1 with before + get(k0) + .. + get(k) > goal, and what comes before it in
+// `before`; the last with get(k) > 0 and before = infinity if there is none, -1 if none is above 0. By all
+// threads of the workgroup. goal(total): from the sum of all.
+template <typename F, typename G>
+__device__ __forceinline__ int locate(WalkShared& sh, int k0, int k1, F get, G goal_of, double& total, double& before, double& goal) {
   constexpr int NT = kVerifyThreads, W = NT / 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int each = (count + NT - 1) / NT;
-  const int k0 = threadIdx.x * each < count ? threadIdx.x * each : count, k1 = k0 + each < count ? k0 + each : count;
+  const int each = (k1 - k0 + NT - 1) / NT;
+  const int i0 = k0 + static_cast<int>(threadIdx.x) * each < k1 ? k0 + threadIdx.x * each : k1, i1 = i0 + each < k1 ? i0 + each : k1;
   double own = 0.0;
   int last = -1;
-  for (int k = k0; k < k1; ++k) {
+  for (int k = i0; k < i1; ++k) {
     const double x = get(k);
     own += x;
     if (x > 0.0) last = k;
@@ -583,9 +622,8 @@ __device__ __forceinline__ int locate(WalkShared& sh, int count, F get, double u
     const int o = __shfl_xor(last, s);
     last = o > last ? o : last;
   }
-  __syncthreads();
   if (lane == 63) sh.red[wave] = incl;
-  if (lane == 0) sh.gone[wave] = last;
+  if (lane == 0) sh.pick[wave] = last;
   __syncthreads();
   total = 0.0;
   last = -1;
@@ -596,21 +634,19 @@ __device__ __forceinline__ int locate(WalkShared& sh, int count, F get, double u
       incl += total;
     }
     total += sh.red[k];
-    last = sh.gone[k] > last ? sh.gone[k] : last;
+    last = sh.pick[k] > last ? sh.pick[k] : last;
   }
-  goal = (u > 0.0 ? u : 0.0) * total;
-  const uint64_t m = __ballot(incl > goal);
-  __syncthreads();
-  if (lane == 0) sh.gone[wave] = m ? wave * 64 + __builtin_ctzll(m) : NT;
+  goal = goal_of(total);
+  const uint64_t m = __ballot(before + incl > goal);
+  if (lane == 0) sh.pick[W + wave] = m ? wave * 64 + __builtin_ctzll(m) : NT;
   __syncthreads();
   int hit = NT;
 #pragma unroll
-  for (int k = W - 1; k >= 0; --k) hit = sh.gone[k] < NT ? sh.gone[k] : hit;
-  __syncthreads();
+  for (int k = W - 1; k >= 0; --k) hit = sh.pick[W + k] < NT ? sh.pick[W + k] : hit;
   if (static_cast<int>(threadIdx.x) == hit) {
-    int k = k0, found = k0;
-    double run = excl, at = excl;
-    for (; k < k1; ++k) {
+    int found = -1;
+    double run = before + excl, at = run;
+    for (int k = i0; k < i1; ++k) {
       const double x = get(k);
       if (x > 0.0) {  // (rounding may leave the last of the thread's own as the one)
         found = k;
@@ -619,15 +655,14 @@ __device__ __forceinline__ int locate(WalkShared& sh, int count, F get, double u
       }
       run += x;
     }
-    sh.gone[0] = found;
-    sh.red[0] = at;
+    sh.pick[2 * W] = found;
+    sh.red[W] = at;
   }
   __syncthreads();
-  int res = hit < NT ? sh.gone[0] : last;
-  before = hit < NT ? sh.red[0] : __builtin_inf();  // (no border above the goal: take the last there)
-  if (!(total > 0.0) || total == __builtin_inf()) res = -1;
+  const int found = hit < NT ? sh.pick[2 * W] : -1;
+  before = found >= 0 ? sh.red[W] : __builtin_inf();
   __syncthreads();
-  return res;
+  return found >= 0 ? found : last;
 }
 
 // The workgroups of a sequence (`shares` of them) sum w over their blocks; the last finds the token.
@@ -647,7 +682,7 @@ __global__ __launch_bounds__(kVerifyThreads) void k_verify_pick(VerifyParams p) 
     return;
   }
   fill_table(sh.tab);
-  const double T = temperature_of(a, b), c = scale_of(T);
+  const double T = temperature_of(a, b), u = a.uniforms[lo];
   Walked k;
   if constexpr (WALKED) {
     k = p.walked[b];
@@ -661,149 +696,143 @@ __global__ __launch_bounds__(kVerifyThreads) void k_verify_pick(VerifyParams p) 
     if (first && threadIdx.x == 0) *token = at;
     return;
   }
+  const int row = lo + k.cur;
   Weights w;
-  w.p = dist_of(p, p.t, lo + k.cur, c, 64, sh.tab);
+  w.c = scale_of(T);
   w.al = k.al;
-  w.drafted = a.draft && k.al != 0.0;
-  if (w.drafted) w.q = dist_of(p, p.d, lo + k.cur, c, 64, sh.tab);
-  w.ngone = 0;
+  w.prow = p.t.data + row * p.t.stride;
+  w.qrow = a.draft && k.al != 0.0 ? p.d.data + row * p.d.stride : nullptr;
+  if (!WALKED && k.tried && n <= kWindow) {  // (the last child's parent is this row)
+    w.p = sh.p[k.tried];
+    w.q = sh.q[k.tried];
+  } else {
+    w.p = dist_of<64>(p, p.t, row, w.c, sh.tab);
+    w.q = Dist{0.0, 1.0};
+    if (w.qrow) w.q = dist_of<64>(p, p.d, row, w.c, sh.tab);
+  }
+  // tokens that were taken out of p
+  int ngone = 0;
   if (!a.draft && k.tried) {
     for (int r0 = k.cur + 1; r0 < n; r0 += 64) {
       const int r = r0 + lane;
       const bool child = r < n && parent_of(a, lo, r) == k.cur;
       const uint64_t m = __ballot(child);
-      const int at = w.ngone + __popcll(m & ((1ull << lane) - 1));
+      const int at = ngone + __popcll(m & ((1ull << lane) - 1));
       if (wave == 0 && child && at < kGone) s_gone[at] = a.tokens[lo + r];
-      w.ngone += __popcll(m);
+      ngone += __popcll(m);
     }
     __syncthreads();
   }
-  const int blocks = (a.V + kBlockElems - 1) / kBlockElems;
-  const double u = a.uniforms[lo];
-  double* const sums = p.sums + static_cast<int64_t>(b) * blocks;
-  auto weights = [&](int i, double (&v)[8]) {
+  auto weights = [&](int i, double (&v)[8]) TQ_INLINE {
     weights8(p, w, i, sh.tab, v);
-    if (w.ngone) {
-      if (w.ngone <= kGone) {
-        for (int g = 0; g < w.ngone; ++g) {
-          const int x = s_gone[g];
+    // (more of them than LDS holds: looked for among the rows again)
+    const int g0 = ngone <= kGone ? 0 : k.cur + 1, g1 = ngone <= kGone ? ngone : n;
+    for (int g = g0; g < g1; ++g) {
+      const int x = ngone <= kGone ? s_gone[g] : parent_of(a, lo, g) == k.cur ? a.tokens[lo + g] : -1;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = x == i + e ? 0.0 : v[e];
-        }
-      } else {
-        for (int r = k.cur + 1; r < n; ++r) {
-          if (parent_of(a, lo, r) != k.cur) continue;
-          const int x = a.tokens[lo + r];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = x == i + e ? 0.0 : v[e];
-        }
-      }
+      for (int e = 0; e < 8; ++e) v[e] = x == i + e ? 0.0 : v[e];
     }
   };
-  auto block_sum = [&](int block) {  // by a wave
-    double v[8], s = 0.0;
-    const int i = block * kBlockElems + 8 * lane;
-    if (i < a.V) {
-      weights(i, v);
-      s = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+  const int blocks = (a.V + kBlockElems - 1) / kBlockElems;
+  double* const sums = p.sums + static_cast<int64_t>(b) * blocks;
+  // p itself: its pieces are summed already, so only the piece that the token is in is looked into
+  const bool pieces = !p.t.probs && !w.qrow && !ngone;
+  const bool none = w.p.zinv != w.p.zinv || (w.qrow && w.q.zinv != w.q.zinv);  // no distribution
+  if ((pieces || none) && !first) return;
+  int k0 = share * p.share_blocks < blocks ? share * p.share_blocks : blocks;
+  int k1 = k0 + p.share_blocks < blocks ? k0 + p.share_blocks : blocks;
+  double total = 0.0, before = 0.0, goal = 0.0;
+  auto of_total = [&](double s) TQ_INLINE { return (u > 0.0 ? u : 0.0) * s; };
+  bool alone = pieces;  // the other workgroups have ended
+  int at = -1;
+  if (pieces && !none) {
+    const StatPart* st = p.t.stat + static_cast<int64_t>(row) * p.parts;
+    auto piece = [&](int i) TQ_INLINE {
+      const StatPart q = st[i];
+      return q.z == 0.0 ? 0.0 : q.z * add_exp2((static_cast<double>(q.top) - w.p.ref) * w.c, 0.0, sh.tab) * w.p.zinv;
+    };
+    at = locate(sh, 0, p.parts, piece, of_total, total, before, goal);
+    k0 = at * p.part_blocks;
+    k1 = k0 + p.part_blocks < blocks ? k0 + p.part_blocks : blocks;
+    if (before == __builtin_inf()) {  // the last token of that piece
+      before = 0.0;
+      goal = __builtin_inf();
     }
-    return wave_sum(s);
-  };
-  auto sum_blocks = [&](int k0, int k1) {
+  }
+  while (!none) {
     for (int block = k0 + wave; block < k1; block += kVerifyThreads / 64) {
-      const double s = block_sum(block);
+      double v[8], s = 0.0;
+      const int i = block * kBlockElems + 8 * lane;
+      if (i < a.V) {
+        weights(i, v);
+        s = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+      }
+      s = wave_sum(s);
       if (lane == 0) __hip_atomic_store(sums + block, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    __threadfence();
-  };
-  auto put = [&](int at, double before, double goal) {  // the token in block `at`, by the first wave
-    if (wave) return;
-    int res = -1;
-    if (at >= 0) {
-      double v[8], own = 0.0;
-      const int i = at * kBlockElems + 8 * lane;
-      if (i < a.V) weights(i, v);
-      int last = -1;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (i >= a.V) v[e] = 0.0;
-        own += v[e];
-        if (v[e] > 0.0) last = i + e;
-      }
-      double incl = own;
-#pragma unroll
-      for (int s = 1; s < 64; s <<= 1) {
-        const double o = __shfl_up(incl, s);
-        if (lane >= s) incl += o;
-      }
-      double run = before + (incl - own);
-      int hit = 0x7fffffff;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        run += v[e];
-        if (v[e] > 0.0 && run > goal && hit == 0x7fffffff) hit = i + e;
-      }
-#pragma unroll
-      for (int s = 32; s; s >>= 1) {
-        const int o = __shfl_xor(hit, s), l = __shfl_xor(last, s);
-        hit = o < hit ? o : hit;
-        last = l > last ? l : last;
-      }
-      // (none above the goal in the block where its sum passed it: rounding; the last one there)
-      res = hit < 0x7fffffff && before < __builtin_inf() ? hit : last;
-    }
-    if (lane == 0) *token = res;
-  };
-  double total, before, goal;
-  if (w.p.zinv != w.p.zinv || (w.drafted && w.q.zinv != w.q.zinv)) {  // no distribution
-    if (first) put(-1, 0.0, 0.0);
-    return;
-  }
-  if (!p.t.probs && !w.drafted && !w.ngone) {
-    // p itself: its pieces are summed already
-    if (!first) return;
-    const StatPart* st = p.t.stat + static_cast<int64_t>(lo + k.cur) * p.parts;
-    auto piece = [&](int i) {
-      const StatPart q = st[i];
-      return q.z == 0.0 ? 0.0 : q.z * add_exp2((static_cast<double>(q.top) - w.p.ref) * c, 0.0, sh.tab) * w.p.zinv;
-    };
-    const int at = locate(sh, p.parts, piece, u, total, before, goal);
-    if (at < 0) return put(-1, 0.0, 0.0);
-    const int k0 = at * p.part_blocks, k1 = k0 + p.part_blocks < blocks ? k0 + p.part_blocks : blocks;
-    for (int block = k0 + wave; block < k1; block += kVerifyThreads / 64) {
-      const double s = block_sum(block);
-      if (lane == 0) sh.px[block - k0] = s;
-    }
+    // The sums are written through to where every XCD sees them, and read from there: the wave waits
+    // for its stores before it meets the others, and no cache has to be written back (a release fence
+    // does that, for the whole L2: 90 us more in the largest batch).
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    int hit = -1;
-    double run = before, start = before;
-    for (int i = 0; i < k1 - k0; ++i) {
-      if (!(sh.px[i] > 0.0)) continue;
-      hit = i;
-      start = run;
-      if (before < __builtin_inf() && run + sh.px[i] > goal) break;
-      run += sh.px[i];
+    if (!alone) {
+      if (threadIdx.x == 0) s_last = __hip_atomic_fetch_add(p.tickets + b, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __syncthreads();
+      if (s_last != p.shares - 1) return;
+      alone = true;
+      k0 = 0;
+      k1 = blocks;
     }
-    return put(hit < 0 ? -1 : k0 + hit, start, goal);
+    auto get = [&](int i) TQ_INLINE { return __hip_atomic_load(sums + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
+    double part;
+    at = locate(sh, k0, k1, get, [&](double s) TQ_INLINE { return pieces ? goal : of_total(s); }, part, before, goal);
+    if (!pieces) total = part;
+    if (total != 0.0 || (!w.qrow && !ngone)) break;
+    w.qrow = nullptr;  // nothing is left: p itself, by this workgroup
+    ngone = 0;
+    before = 0.0;
   }
-  const int k0 = share * p.share_blocks < blocks ? share * p.share_blocks : blocks;
-  const int k1 = k0 + p.share_blocks < blocks ? k0 + p.share_blocks : blocks;
-  sum_blocks(k0, k1);
-  __syncthreads();
-  if (threadIdx.x == 0) s_last = __hip_atomic_fetch_add(p.tickets + b, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  if (s_last != p.shares - 1) return;
-  __threadfence();
-  auto get = [&](int i) { return __hip_atomic_load(sums + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
-  int at = locate(sh, blocks, get, u, total, before, goal);
-  if (total == 0.0 && (w.drafted || w.ngone)) {  // nothing is left: p itself
-    w.drafted = false;
-    w.ngone = 0;
-    sum_blocks(0, blocks);
-    __syncthreads();
-    at = locate(sh, blocks, get, u, total, before, goal);
+  if (wave) return;
+  // the token in block `at`
+  int res = -1;
+  if (at >= 0 && total > 0.0 && total < __builtin_inf()) {
+    double v[8], own = 0.0;
+    const int i = at * kBlockElems + 8 * lane;
+    int last = -1;
+    if (i < a.V) {
+      weights(i, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.0;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      own += v[e];
+      if (v[e] > 0.0) last = i + e;
+    }
+    double incl = own;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const double o = __shfl_up(incl, s);
+      if (lane >= s) incl += o;
+    }
+    double run = before + (incl - own);
+    int hit = 0x7fffffff;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      run += v[e];
+      if (v[e] > 0.0 && run > goal && hit == 0x7fffffff) hit = i + e;
+    }
+#pragma unroll
+    for (int s = 32; s; s >>= 1) {
+      const int o = __shfl_xor(hit, s), l = __shfl_xor(last, s);
+      hit = o < hit ? o : hit;
+      last = l > last ? l : last;
+    }
+    // (none above the goal in the block where its sum passed it: rounding; the last one there)
+    res = hit < 0x7fffffff && before < __builtin_inf() ? hit : last;
   }
-  put(at, before, goal);
+  if (lane == 0) *token = res;
 }
 
 // The workspace: statistics, then what the workgroups of a sequence share.
