@@ -126,30 +126,64 @@ __device__ __forceinline__ void load8_any(const char* row, int dt, int i, int V,
   }
 }
 
+// 2^(i / 256), the upper word less i << 12: adding j << 12 for any j = 256 k + i leaves 2^(j / 256).
 __device__ __forceinline__ void fill_table(double* tab) {
-  for (int i = threadIdx.x; i < kTable; i += blockDim.x) tab[i] = exp2(i * (1.0 / kTable));
+  for (int i = threadIdx.x; i < kTable; i += blockDim.x) {
+    const double x = exp2(i * (1.0 / kTable));
+    tab[i] = __hiloint2double(__double2hiint(x) - (i << 12), __double2loint(x));
+  }
   __syncthreads();
 }
 
-// s + 2^t for t < 1000, to 2e-14 of 2^t; t below -1000 counts as -1000, NaN too. 2^t = 2^k 2^(i / 256) 2^r,
-// |r| <= 1 / 512: k and i from the low bits of t + 1.5 2^44, 2^r = e^y by the polynomial of degree 3 with
-// the least error on |y| <= h = ln 2 / 512 (y^4 / 24 replaced by its nearest of degree 2, h^2 y^2 - h^4 / 8).
-__device__ __forceinline__ double add_exp2(double t, double s, const double* tab) {
-  constexpr double kMagic = 26388279066624.0;  // 1.5 2^44: steps of 1 / 256
+// Exponentials: 2^t = 2^k 2^(i / 256) 2^r, |r| <= 1 / 512. Adding 1.5 2^44 rounds t to steps of 1 / 256 and leaves
+// 256 k + i in the low word; 2^r = e^y by the polynomial of degree 3 with the least error on |y| <= h =
+// ln 2 / 512 (y^4 / 24 replaced by its nearest of degree 2, h^2 y^2 - h^4 / 8): 2e-14 of 2^t in all.
+constexpr double kMagic = 26388279066624.0;
+__device__ __forceinline__ double add_pow2(double z, double r, double s, const double* tab) {
   constexpr double kLn2 = 0.69314718055994530942, kH = kLn2 / 512;
-  t = __builtin_fmax(t, -1000.0);
-  const double z = t + kMagic;
-  const double r = t - (z - kMagic);
-  const uint32_t i = static_cast<uint32_t>(__double2loint(z));
+  const uint32_t j = static_cast<uint32_t>(__double2loint(z));
   double p = __builtin_fma(r, kLn2 * kLn2 * kLn2 / 6, kLn2 * kLn2 * (0.5 + kH * kH / 24));
   p = __builtin_fma(p, r, kLn2);
   p = __builtin_fma(p, r, 1.0 - kH * kH * kH * kH / 192);
-  const double w = tab[i & (kTable - 1)];
-  return __builtin_fma(__hiloint2double(__double2hiint(w) + ((i & ~(kTable - 1u)) << 12), __double2loint(w)), p, s);
+  u32x2_t w = __builtin_bit_cast(u32x2_t, tab[j & (kTable - 1)]);
+  w.y += j << 12;
+  return __builtin_fma(__builtin_bit_cast(double, w), p, s);
+}
+// s + 2^t for t < 1000; t below -1000 counts as -1000, NaN too.
+__device__ __forceinline__ double add_exp2(double t, double s, const double* tab) {
+  t = __builtin_fmax(t, -1000.0);
+  const double z = t + kMagic;
+  return add_pow2(z, t - (z - kMagic), s, tab);
+}
+
+// 2^((x - ref) c) for many x: with ref c rounded to steps of 1 / 256 (a factor that every x has alike), x c
+// is rounded and its step counted from ref in one fused operation. x is held above `cut`, where the
+// result is about 2^-1000 (NaN stays NaN, and its result is anything). Not `ok`: a scale or a reference for which single precision cannot place the cut
+// (temperatures below 1e-7 or above 1e35 or so).
+struct Exp2Near {
+  double c, magic, base;  // magic = 1.5 2^44 - base; base: ref c, rounded
+  float cut;
+  bool ok;
+};
+__device__ __forceinline__ Exp2Near exp2_near(double ref, double c, double reach) {  // reach = 1000 / c
+  Exp2Near e;
+  e.c = c;
+  const double rc = ref * c;
+  e.base = (rc + kMagic) - kMagic;
+  e.magic = kMagic - e.base;
+  e.cut = static_cast<float>(ref - reach);
+  e.ok = __builtin_fabs(rc) < 0x1p27 && e.cut > -3e38f;
+  return e;
+}
+__device__ __forceinline__ double add_exp2_near(const Exp2Near& e, float x, double s, const double* tab) {
+  const double v = __builtin_elementwise_maximum(x, e.cut);
+  const double z = __builtin_fma(v, e.c, e.magic);
+  return add_pow2(z, __builtin_fma(v, e.c, e.magic - z), s, tab);
 }
 
 __device__ __forceinline__ double temperature_of(const VerifyArgs& a, int b) { return a.temperature ? a.temperature[b] : 1.0; }
 __device__ __forceinline__ double scale_of(double T) { return 1.4426950408889634074 / T; }
+__device__ __forceinline__ double reach_of(double T) { return 693.14718055994530942 * T; }  // 1000 / scale
 
 __device__ __forceinline__ float wave_max(float x) {
 #pragma unroll
@@ -186,51 +220,67 @@ __device__ __forceinline__ void seq_rows(const VerifyArgs& a, int b, int& lo, in
 // ---- statistics of the rows ---------------------------------------------------------------
 
 template <int DT>
-__device__ __forceinline__ StatPart stat_piece(const char* row, int V, int i0, int i1, double c, const double* tab) {
+__device__ __forceinline__ StatPart stat_piece(const char* row, int V, int i0, int i1, double c, double reach, const double* tab) {
   const int lane = threadIdx.x & 63;
   const float inf = __builtin_inff();
-  float f[8], top = -inf, ref = 0.f;
-  double s0 = 0.0, s1 = 0.0, base = 0.0;
-  bool first = true;
-  // relative to the lane's first eight values, which may turn out to be far below the others
-  for (int i = i0 + 8 * lane; i < i1; i += kBlockElems) {
+  float f[8], top = -inf;
+  double s = 0.0, base = 0.0;  // s in units of 2^base
+  auto load = [&](int i) TQ_INLINE {
     if (i + 8 <= V) load8<DT>(row, i, f);
     else load8_end<DT>(row, i, V, -inf, f);
+  };
+  auto largest = [&]() TQ_INLINE {
     float m = __builtin_elementwise_maximum(f[0], f[1]);
 #pragma unroll
-    for (int k = 2; k < 8; k += 2)
-      m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, f[k]), f[k + 1]);
-    top = __builtin_elementwise_maximum(top, m);
-    if (first) {
-      ref = __builtin_fabsf(m) < inf ? m : 0.f;
-      base = ref;
-      first = false;
-    }
+    for (int k = 2; k < 8; k += 2) m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, f[k]), f[k + 1]);
+    return m;
+  };
+  int i = i0 + 8 * lane;
+  bool done = i >= i1;
+  if (!done) {
+    // relative to the lane's first eight values, which may turn out to be far below the others
+    load(i);
+    const float m = largest(), ref = __builtin_fabsf(m) < inf ? m : 0.f;
+    const Exp2Near e = exp2_near(ref, c, reach);
+    double s0 = 0.0, s1 = 0.0;
+    if (e.ok) {
+      for (; i < i1; i += kBlockElems) {
+        load(i);  // (the first ones once more: held over the loop's end they cost a move each)
+        top = __builtin_elementwise_maximum(top, largest());
 #pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      s0 = add_exp2((f[k] - base) * c, s0, tab);
-      s1 = add_exp2((f[k + 1] - base) * c, s1, tab);
+        for (int k = 0; k < 8; k += 2) {
+          s0 = add_exp2_near(e, f[k], s0, tab);
+          s1 = add_exp2_near(e, f[k + 1], s1, tab);
+        }
+      }
+      s = s0 + s1;
+      base = e.base;
+      done = (static_cast<double>(top) - ref) * c < 900.0 && s > 0x1p-900;
     }
   }
-  double s = s0 + s1;
-  if (!((static_cast<double>(top) - base) * c < 900.0) || s < 0x1p-900) {
-    // ... or far above them; or none is finite
+  if (!done) {
+    // ... or far above them, or none is finite, or the temperature is extreme: relative to the largest
+    top = -inf;
+    for (i = i0 + 8 * lane; i < i1; i += kBlockElems) {
+      load(i);
+      top = __builtin_elementwise_maximum(top, largest());
+    }
     s = 0.0;
-    ref = top;
     if (top != top || top == inf) {
       s = __builtin_nan("");
     } else if (top > -inf) {
-      for (int i = i0 + 8 * lane; i < i1; i += kBlockElems) {
-        load8_end<DT>(row, i, V, -inf, f);
+      for (i = i0 + 8 * lane; i < i1; i += kBlockElems) {
+        load(i);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s = add_exp2((f[k] - static_cast<double>(ref)) * c, s, tab);
+        for (int k = 0; k < 8; ++k) s = add_exp2((f[k] - static_cast<double>(top)) * c, s, tab);
       }
     }
+    base = __builtin_nan("");  // (in units of the lane's largest)
   }
   StatPart p;
   p.top = wave_max(top);
   p.at = 0;
-  if (s != 0.0) s *= add_exp2((static_cast<double>(ref) - p.top) * c, 0.0, tab);
+  if (s != 0.0) s *= add_exp2(base == base ? base - p.top * c : (static_cast<double>(top) - p.top) * c, 0.0, tab);
   p.z = wave_sum(s);
   if (p.top != p.top || p.top == inf) p.z = __builtin_nan("");
   return p;
@@ -310,9 +360,9 @@ __global__ __launch_bounds__(kVerifyThreads) void k_verify_stats(VerifyParams p,
     if (greedy) {
       r = s.dt == 0 ? stat_largest<0>(x, a.V, i0, i1) : s.dt == 1 ? stat_largest<1>(x, a.V, i0, i1) : stat_largest<2>(x, a.V, i0, i1);
     } else {
-      const double c = scale_of(T);
-      r = s.dt == 0 ? stat_piece<0>(x, a.V, i0, i1, c, tab) : s.dt == 1 ? stat_piece<1>(x, a.V, i0, i1, c, tab)
-                                                                      : stat_piece<2>(x, a.V, i0, i1, c, tab);
+      const double c = scale_of(T), reach = reach_of(T);
+      r = s.dt == 0 ? stat_piece<0>(x, a.V, i0, i1, c, reach, tab) : s.dt == 1 ? stat_piece<1>(x, a.V, i0, i1, c, reach, tab)
+                                                                             : stat_piece<2>(x, a.V, i0, i1, c, reach, tab);
     }
     if (lane == 0) const_cast<StatPart*>(s.stat)[static_cast<int64_t>(row) * p.parts + part] = r;
   }
@@ -396,27 +446,68 @@ __device__ __forceinline__ int largest_of(const VerifyParams& p, int row) {
 
 // ---- weights ----------------------------------------------------------------------------------
 
-// What the new token is drawn from (or S is summed over): p, or (p - al q)+.
+// Weights up to here count as nothing: masked tokens come out as about 2^-1000, not 0.
+constexpr double kNothing = 1e-280;
+
+// One side of what the new token is drawn from (or S is summed over).
+struct WeightSide {
+  const char* row;  // null: none
+  Dist d;
+  Exp2Near e;
+  double scale;  // probability = 2^(x c - e.base) scale
+};
 struct Weights {
-  const char *prow, *qrow;  // qrow null: p
-  Dist p, q;
-  double c, al;
+  WeightSide p, q;
+  double c, al;  // (p - al q)+
 };
 
-// w of elements i .. i + 7 (0 behind the row).
+// A value that all lanes hold, in scalar registers.
+__device__ __forceinline__ double uniform(double x) {
+  return __hiloint2double(__builtin_amdgcn_readfirstlane(__double2hiint(x)), __builtin_amdgcn_readfirstlane(__double2loint(x)));
+}
+
+__device__ __forceinline__ WeightSide weight_side(const Side& s, int row, const Dist& d, double T, const double* tab) {
+  WeightSide w;
+  const double c = scale_of(T);
+  w.row = s.data + row * s.stride;
+  w.d = Dist{uniform(d.ref), uniform(d.zinv)};
+  w.e = exp2_near(w.d.ref, c, reach_of(T));
+  w.scale = uniform(d.zinv * add_exp2(w.e.base - d.ref * c, 0.0, tab));
+  w.e.c = uniform(c);
+  w.e.base = uniform(w.e.base);
+  w.e.magic = uniform(w.e.magic);
+  w.e.cut = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(w.e.cut)));
+  w.e.ok = __builtin_amdgcn_readfirstlane(w.e.ok);
+  return w;
+}
+
+__device__ __forceinline__ void probabilities8(const Side& s, const WeightSide& w, double c, int i, int V, const double* tab,
+                                               double (&v)[8]) {
+  float f[8];
+  load8_any(w.row, s.dt, i, V, s.probs ? 0.f : -__builtin_inff(), f);
+  if (s.probs) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = f[k];
+  } else if (w.e.ok) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = add_exp2_near(w.e, f[k], 0.0, tab) * w.scale;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = probability(s, w.d, c, f[k], tab);
+  }
+}
+
+// w of elements i .. i + 7 (nothing behind the row).
 __device__ __forceinline__ void weights8(const VerifyParams& p, const Weights& w, int i, const double* tab, double (&v)[8]) {
-  const float none = -__builtin_inff();
-  float f[8], g[8];
-  load8_any(w.prow, p.t.dt, i, p.a.V, p.t.probs ? 0.f : none, f);
-  if (w.qrow) load8_any(w.qrow, p.d.dt, i, p.a.V, p.d.probs ? 0.f : none, g);
+  probabilities8(p.t, w.p, w.c, i, p.a.V, tab, v);
+  if (w.q.row) {
+    double q[8];
+    probabilities8(p.d, w.q, w.c, i, p.a.V, tab, q);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = probability(p.t, w.p, w.c, f[k], tab);
-  if (w.qrow) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = __builtin_fma(-w.al, probability(p.d, w.q, w.c, g[k], tab), v[k]);
+    for (int k = 0; k < 8; ++k) v[k] = __builtin_fma(-w.al, q[k], v[k]);
   }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = v[k] < 0.0 ? 0.0 : v[k];
+  for (int k = 0; k < 8; ++k) v[k] = v[k] <= kNothing ? 0.0 : v[k];  // (NaN stays)
 }
 
 // ---- the walk -----------------------------------------------------------------------------
@@ -565,10 +656,8 @@ __global__ __launch_bounds__(kWalkThreads) void k_verify_walk(VerifyParams p) {
   auto sum = [&](int cur, double al) TQ_INLINE {
     Weights w;
     w.c = scale_of(T);
-    w.prow = p.t.data + (lo + cur) * p.t.stride;
-    w.qrow = p.d.data + (lo + cur) * p.d.stride;
-    w.p = dist_of<64>(p, p.t, lo + cur, w.c, sh.tab);
-    w.q = dist_of<64>(p, p.d, lo + cur, w.c, sh.tab);
+    w.p = weight_side(p.t, lo + cur, dist_of<64>(p, p.t, lo + cur, w.c, sh.tab), T, sh.tab);
+    w.q = weight_side(p.d, lo + cur, dist_of<64>(p, p.d, lo + cur, w.c, sh.tab), T, sh.tab);
     w.al = al;
     double s = 0.0, v[8];
     for (int i = threadIdx.x * 8; i < a.V; i += kWalkThreads * 8) {
@@ -594,7 +683,7 @@ __global__ __launch_bounds__(kWalkThreads) void k_verify_walk(VerifyParams p) {
 // ---- the new token ----------------------------------------------------------------------------
 
 // The first of k0 <= k < k1 with before + get(k0) + .. + get(k) > goal, and what comes before it in
-// `before`; the last with get(k) > 0 and before = infinity if there is none, -1 if none is above 0. By all
+// `before`; the last with get(k) above nothing and before = infinity if there is none, -1 if none is. By all
 // threads of the workgroup. goal(total): from the sum of all.
 template <typename F, typename G>
 __device__ __forceinline__ int locate(WalkShared& sh, int k0, int k1, F get, G goal_of, double& total, double& before, double& goal) {
@@ -682,7 +771,7 @@ __global__ __launch_bounds__(kVerifyThreads) void k_verify_pick(VerifyParams p) 
     return;
   }
   fill_table(sh.tab);
-  const double T = temperature_of(a, b), u = a.uniforms[lo];
+  const double T = uniform(temperature_of(a, b)), u = uniform(a.uniforms[lo]);
   Walked k;
   if constexpr (WALKED) {
     k = p.walked[b];
@@ -690,6 +779,10 @@ __global__ __launch_bounds__(kVerifyThreads) void k_verify_pick(VerifyParams p) 
     k = walk<kVerifyThreads, false>(p, sh, lo, n, T, first, [](int, double) { return 0.0; });
     if (first && threadIdx.x == 0) a.kept[b] = k.kept;
   }
+  k.al = uniform(k.al);
+  k.cur = __builtin_amdgcn_readfirstlane(k.cur);
+  k.kept = __builtin_amdgcn_readfirstlane(k.kept);
+  k.tried = __builtin_amdgcn_readfirstlane(k.tried);
   int32_t* const token = a.out_tokens + lo + k.kept - 1;
   if (!(T > 0.0)) {
     const int at = largest_of(p, lo + k.cur);
@@ -700,16 +793,19 @@ __global__ __launch_bounds__(kVerifyThreads) void k_verify_pick(VerifyParams p) 
   Weights w;
   w.c = scale_of(T);
   w.al = k.al;
-  w.prow = p.t.data + row * p.t.stride;
-  w.qrow = a.draft && k.al != 0.0 ? p.d.data + row * p.d.stride : nullptr;
+  bool drafted = a.draft && k.al != 0.0;
+  Dist dp, dq{0.0, 1.0};
   if (!WALKED && k.tried && n <= kWindow) {  // (the last child's parent is this row)
-    w.p = sh.p[k.tried];
-    w.q = sh.q[k.tried];
+    dp = sh.p[k.tried];
+    dq = sh.q[k.tried];
   } else {
-    w.p = dist_of<64>(p, p.t, row, w.c, sh.tab);
-    w.q = Dist{0.0, 1.0};
-    if (w.qrow) w.q = dist_of<64>(p, p.d, row, w.c, sh.tab);
+    dp = dist_of<64>(p, p.t, row, w.c, sh.tab);
+    if (drafted) dq = dist_of<64>(p, p.d, row, w.c, sh.tab);
   }
+  w.p = weight_side(p.t, row, dp, T, sh.tab);
+  w.q = w.p;
+  if (drafted) w.q = weight_side(p.d, row, dq, T, sh.tab);
+  else w.q.row = nullptr;
   // tokens that were taken out of p
   int ngone = 0;
   if (!a.draft && k.tried) {
@@ -736,8 +832,8 @@ __global__ __launch_bounds__(kVerifyThreads) void k_verify_pick(VerifyParams p) 
   const int blocks = (a.V + kBlockElems - 1) / kBlockElems;
   double* const sums = p.sums + static_cast<int64_t>(b) * blocks;
   // p itself: its pieces are summed already, so only the piece that the token is in is looked into
-  const bool pieces = !p.t.probs && !w.qrow && !ngone;
-  const bool none = w.p.zinv != w.p.zinv || (w.qrow && w.q.zinv != w.q.zinv);  // no distribution
+  const bool pieces = !p.t.probs && !drafted && !ngone;
+  const bool none = dp.zinv != dp.zinv || (drafted && dq.zinv != dq.zinv);  // no distribution
   if ((pieces || none) && !first) return;
   int k0 = share * p.share_blocks < blocks ? share * p.share_blocks : blocks;
   int k1 = k0 + p.share_blocks < blocks ? k0 + p.share_blocks : blocks;
@@ -749,7 +845,7 @@ __global__ __launch_bounds__(kVerifyThreads) void k_verify_pick(VerifyParams p) 
     const StatPart* st = p.t.stat + static_cast<int64_t>(row) * p.parts;
     auto piece = [&](int i) TQ_INLINE {
       const StatPart q = st[i];
-      return q.z == 0.0 ? 0.0 : q.z * add_exp2((static_cast<double>(q.top) - w.p.ref) * w.c, 0.0, sh.tab) * w.p.zinv;
+      return q.z == 0.0 ? 0.0 : q.z * add_exp2((static_cast<double>(q.top) - dp.ref) * w.c, 0.0, sh.tab) * dp.zinv;
     };
     at = locate(sh, 0, p.parts, piece, of_total, total, before, goal);
     k0 = at * p.part_blocks;
@@ -787,8 +883,9 @@ __global__ __launch_bounds__(kVerifyThreads) void k_verify_pick(VerifyParams p) 
     double part;
     at = locate(sh, k0, k1, get, [&](double s) TQ_INLINE { return pieces ? goal : of_total(s); }, part, before, goal);
     if (!pieces) total = part;
-    if (total != 0.0 || (!w.qrow && !ngone)) break;
-    w.qrow = nullptr;  // nothing is left: p itself, by this workgroup
+    if (total != 0.0 || (!drafted && !ngone)) break;
+    drafted = false;
+    w.q.row = nullptr;  // nothing is left: p itself, by this workgroup
     ngone = 0;
     before = 0.0;
   }
