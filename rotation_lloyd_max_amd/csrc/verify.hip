@@ -756,7 +756,7 @@ __device__ __forceinline__ int locate(WalkShared& sh, int k0, int k1, F get, G g
 
 // The workgroups of a sequence (`shares` of them) sum w over their blocks; the last finds the token.
 template <bool WALKED>
-__global__ __launch_bounds__(kVerifyThreads) void k_verify_pick(VerifyParams p) {
+__global__ __launch_bounds__(kVerifyThreads, 4) void k_verify_pick(VerifyParams p) {
   __shared__ WalkShared sh;
   __shared__ int s_gone[kGone], s_last;
   const VerifyArgs& a = p.a;
@@ -855,17 +855,25 @@ __global__ __launch_bounds__(kVerifyThreads) void k_verify_pick(VerifyParams p) 
       goal = __builtin_inf();
     }
   }
-  while (!none) {
-    for (int block = k0 + wave; block < k1; block += kVerifyThreads / 64) {
-      double v[8], s = 0.0;
+  // The same loop sums blocks and, at last, looks at the block that the token is in (`at`): the code is
+  // in the instruction cache then, where a copy of it took 2 us to come.
+  bool found = false;
+  double v[8];
+  for (;;) {
+    for (int block = k0 + wave; block < k1 && !none; block += kVerifyThreads / 64) {
+      double s = 0.0;
       const int i = block * kBlockElems + 8 * lane;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.0;
       if (i < a.V) {
         weights(i, v);
         s = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
       }
+      if (found) break;
       s = wave_sum(s);
       if (lane == 0) __hip_atomic_store(sums + block, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
+    if (found || none) break;
     // The sums are written through to where every XCD sees them, and read from there: the wave waits
     // for its stores before it meets the others, and no cache has to be written back (a release fence
     // does that, for the whole L2: 90 us more in the largest batch).
@@ -883,25 +891,25 @@ __global__ __launch_bounds__(kVerifyThreads) void k_verify_pick(VerifyParams p) 
     double part;
     at = locate(sh, k0, k1, get, [&](double s) TQ_INLINE { return pieces ? goal : of_total(s); }, part, before, goal);
     if (!pieces) total = part;
-    if (total != 0.0 || (!drafted && !ngone)) break;
-    drafted = false;
-    w.q.row = nullptr;  // nothing is left: p itself, by this workgroup
-    ngone = 0;
-    before = 0.0;
+    if (total == 0.0 && (drafted || ngone)) {  // nothing is left: p itself, by this workgroup
+      drafted = false;
+      w.q.row = nullptr;
+      ngone = 0;
+      before = 0.0;
+    } else if (at >= 0 && total > 0.0 && total < __builtin_inf()) {
+      found = true;
+      k0 = at;
+      k1 = at + 1;
+    } else {
+      break;
+    }
   }
   if (wave) return;
-  // the token in block `at`
   int res = -1;
-  if (at >= 0 && total > 0.0 && total < __builtin_inf()) {
-    double v[8], own = 0.0;
+  if (found) {
+    double own = 0.0;
     const int i = at * kBlockElems + 8 * lane;
     int last = -1;
-    if (i < a.V) {
-      weights(i, v);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.0;
-    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       own += v[e];
