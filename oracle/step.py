@@ -102,11 +102,12 @@ def sample(w, u):
 
 def verify(target, tokens, uniforms, offsets, draft=None, parents=None, temperature=None, target_kind="logits",
            draft_kind="logits"):
-    """(kept, tokens, path, margin): margin is the smallest distance of any decision to its border,
-    relative to what is compared."""
+    """(kept, tokens, path, margins [sequences][2]): margins are the smallest distances of a sequence's
+    decisions to their borders, relative to what is compared: of the tests, of the new token."""
     M = len(tokens)
-    kept, out, path, margin = [], np.full(M, -1), np.full(M, -1), 1.0
+    kept, out, path, margins = [], np.full(M, -1), np.full(M, -1), np.ones((len(offsets) - 1, 2))
     for b in range(len(offsets) - 1):
+        margin = margins[b]
         lo, n = int(offsets[b]), int(offsets[b + 1] - offsets[b])
         if n == 0:
             kept.append(0)
@@ -137,7 +138,7 @@ def verify(target, tokens, uniforms, offsets, draft=None, parents=None, temperat
                 # S is what is left of p's sum (1 at first): p / S against q
                 left, right = (u * S * q[x], p[x]) if draft is not None else (u * S, p[x])
                 if left != right:
-                    margin = min(margin, abs(left - right) / max(abs(left), abs(right)))
+                    margin[0] = min(margin[0], abs(left - right) / max(abs(left), abs(right)))
                 if left < right:
                     found = r
                     break
@@ -156,8 +157,7 @@ def verify(target, tokens, uniforms, offsets, draft=None, parents=None, temperat
             new = -1
         else:
             w = np.maximum(p, 0.0)
-            new, m = sample(w if w.sum() > 0 else np.maximum(whole, 0.0), float(uniforms[lo]))
-            margin = min(margin, m)
+            new, margin[1] = sample(w if w.sum() > 0 else np.maximum(whole, 0.0), float(uniforms[lo]))
         out[lo + k - 1] = new
         kept.append(k)
-    return np.array(kept), out, path, margin
+    return np.array(kept), out, path, margins

@@ -7,8 +7,11 @@
 // out of p one by one. Children have larger indices than their parents and are tried in ascending
 // order: one ascending scan of a sequence's rows is the walk.
 //
-// Everything that decides is fp64: the new token is found at u sum(w) in the cumulative sum of w, and
-// each of 10^5 borders in it that is off by 10^-8 gives a neighbour now and then.
+// Where a rounding matters. A test of a drafted token compares two numbers: single precision's errors
+// (1e-7) change it once in millions. The new token is found at u sum(w) in the cumulative sum of w: each of
+// its 10^5 borders that is off by 10^-8 gives a neighbour now and then, so w, its sums and the rows' sums
+// that it is made of are fp64. The rows' sums that the tests need, of all rows, are of exponentials in
+// fp32; the pass that sums w sums the row that it comes from once more, in fp64 (see Sums).
 //
 // Two launches. k_verify_stats: largest value and sum of exponentials of every row of logits that can
 // be looked at, a wave per piece of a row. k_verify_pick: each workgroup of a sequence joins the pieces and
@@ -56,7 +59,8 @@ struct VerifyParams {
   Side t, d;
   int parts, part_blocks;  // pieces of a row of logits, and kBlockElems in each
   int shares, share_blocks;  // the same of k_verify_pick's workgroups
-  double* sums;            // [B][blocks]
+  double* sums;            // [B][blocks][2]: Sums::p and Sums::q of a block
+  double* totals;          // [B][shares * waves][2]: of p and q
   int* tickets;            // [B]
   Walked* walked;          // [B] where k_verify_walk runs
 };
@@ -219,68 +223,67 @@ __device__ __forceinline__ void seq_rows(const VerifyArgs& a, int b, int& lo, in
 
 // ---- statistics of the rows ---------------------------------------------------------------
 
+// Elements [i0, i1) of a row by a wave: fp32 exponentials, eight at a time summed in fp32, then fp64.
 template <int DT>
-__device__ __forceinline__ StatPart stat_piece(const char* row, int V, int i0, int i1, double c, double reach, const double* tab) {
+__device__ __forceinline__ StatPart stat_piece(const char* row, int V, int i0, int i1, double T) {
   const int lane = threadIdx.x & 63;
-  const float inf = __builtin_inff();
-  float f[8], top = -inf;
-  double s = 0.0, base = 0.0;  // s in units of 2^base
+  const float inf = __builtin_inff(), c = static_cast<float>(scale_of(T));
+  const bool usual = c > 1e-30f && c < 1e30f;
+  float f[8], top = -inf, ref = 0.f;
+  double s = 0.0;
   auto load = [&](int i) TQ_INLINE {
     if (i + 8 <= V) load8<DT>(row, i, f);
     else load8_end<DT>(row, i, V, -inf, f);
-  };
-  auto largest = [&]() TQ_INLINE {
     float m = __builtin_elementwise_maximum(f[0], f[1]);
 #pragma unroll
     for (int k = 2; k < 8; k += 2) m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, f[k]), f[k + 1]);
     return m;
   };
-  int i = i0 + 8 * lane;
-  bool done = i >= i1;
-  if (!done) {
-    // relative to the lane's first eight values, which may turn out to be far below the others
-    load(i);
-    const float m = largest(), ref = __builtin_fabsf(m) < inf ? m : 0.f;
-    const Exp2Near e = exp2_near(ref, c, reach);
-    double s0 = 0.0, s1 = 0.0;
-    if (e.ok) {
-      for (; i < i1; i += kBlockElems) {
-        load(i);  // (the first ones once more: held over the loop's end they cost a move each)
-        top = __builtin_elementwise_maximum(top, largest());
+  auto sum8 = [&]() TQ_INLINE {
+    float e[8];
 #pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-          s0 = add_exp2_near(e, f[k], s0, tab);
-          s1 = add_exp2_near(e, f[k + 1], s1, tab);
-        }
-      }
-      s = s0 + s1;
-      base = e.base;
-      done = (static_cast<double>(top) - ref) * c < 900.0 && s > 0x1p-900;
+    for (int k = 0; k < 8; ++k) e[k] = __builtin_amdgcn_exp2f((f[k] - ref) * c);
+    return ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+  };
+  const int first = i0 + 8 * lane;
+  bool done = first >= i1;
+  if (usual && !done) {
+    // relative to the lane's first eight values, which may turn out to be far below the others
+    const float m = load(first);
+    ref = __builtin_fabsf(m) < inf ? m : 0.f;
+    for (int i = first; i < i1; i += kBlockElems) {
+      top = __builtin_elementwise_maximum(top, load(i));
+      s += sum8();
     }
+    done = (top - ref) * c < 100.f && s > 0x1p-100;
   }
   if (!done) {
     // ... or far above them, or none is finite, or the temperature is extreme: relative to the largest
     top = -inf;
-    for (i = i0 + 8 * lane; i < i1; i += kBlockElems) {
-      load(i);
-      top = __builtin_elementwise_maximum(top, largest());
-    }
+    for (int i = first; i < i1; i += kBlockElems) top = __builtin_elementwise_maximum(top, load(i));
+    ref = top;
     s = 0.0;
     if (top != top || top == inf) {
       s = __builtin_nan("");
     } else if (top > -inf) {
-      for (i = i0 + 8 * lane; i < i1; i += kBlockElems) {
+      for (int i = first; i < i1; i += kBlockElems) {
         load(i);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s = add_exp2((f[k] - static_cast<double>(top)) * c, s, tab);
+        if (usual) {
+          s += sum8();
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k) {
+            const float x = load_elem<DT>(row, i + k < V ? i + k : V - 1);
+            s += i + k < V && x > -inf ? exp2((static_cast<double>(x) - top) * scale_of(T)) : 0.0;
+          }
+        }
       }
     }
-    base = __builtin_nan("");  // (in units of the lane's largest)
   }
   StatPart p;
   p.top = wave_max(top);
   p.at = 0;
-  if (s != 0.0) s *= add_exp2(base == base ? base - p.top * c : (static_cast<double>(top) - p.top) * c, 0.0, tab);
+  if (s != 0.0) s *= exp2((static_cast<double>(ref) - p.top) * scale_of(T));
   p.z = wave_sum(s);
   if (p.top != p.top || p.top == inf) p.z = __builtin_nan("");
   return p;
@@ -321,11 +324,9 @@ __device__ __forceinline__ StatPart stat_largest(const char* row, int V, int i0,
 
 // A wave per piece of a row: the target's rows, then (of logits) the draft's.
 __global__ __launch_bounds__(kVerifyThreads) void k_verify_stats(VerifyParams p, int64_t unit0, int64_t units) {
-  __shared__ double tab[kTable];
   const VerifyArgs& a = p.a;
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < a.B; i += kVerifyThreads) p.tickets[i] = 0;
-  fill_table(tab);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int lim = a.offsets[a.B] < a.M ? a.offsets[a.B] : a.M;
   for (int64_t unit = unit0 + static_cast<int64_t>(blockIdx.x) * (kVerifyThreads / 64) + wave; unit < units;
@@ -360,9 +361,7 @@ __global__ __launch_bounds__(kVerifyThreads) void k_verify_stats(VerifyParams p,
     if (greedy) {
       r = s.dt == 0 ? stat_largest<0>(x, a.V, i0, i1) : s.dt == 1 ? stat_largest<1>(x, a.V, i0, i1) : stat_largest<2>(x, a.V, i0, i1);
     } else {
-      const double c = scale_of(T), reach = reach_of(T);
-      r = s.dt == 0 ? stat_piece<0>(x, a.V, i0, i1, c, reach, tab) : s.dt == 1 ? stat_piece<1>(x, a.V, i0, i1, c, reach, tab)
-                                                                             : stat_piece<2>(x, a.V, i0, i1, c, reach, tab);
+      r = s.dt == 0 ? stat_piece<0>(x, a.V, i0, i1, T) : s.dt == 1 ? stat_piece<1>(x, a.V, i0, i1, T) : stat_piece<2>(x, a.V, i0, i1, T);
     }
     if (lane == 0) const_cast<StatPart*>(s.stat)[static_cast<int64_t>(row) * p.parts + part] = r;
   }
@@ -458,7 +457,7 @@ struct WeightSide {
 };
 struct Weights {
   WeightSide p, q;
-  double c, al;  // (p - al q)+
+  double c;
 };
 
 // A value that all lanes hold, in scalar registers.
@@ -497,18 +496,23 @@ __device__ __forceinline__ void probabilities8(const Side& s, const WeightSide& 
   }
 }
 
-// w of elements i .. i + 7 (nothing behind the row).
-__device__ __forceinline__ void weights8(const VerifyParams& p, const Weights& w, int i, const double* tab, double (&v)[8]) {
-  probabilities8(p.t, w.p, w.c, i, p.a.V, tab, v);
-  if (w.q.row) {
-    double q[8];
-    probabilities8(p.d, w.q, w.c, i, p.a.V, tab, q);
+// What w is summed from. Let p~, q~ be a row's probabilities by the rows' sums of k_verify_stats, off by a factor
+// each that is 1 to 1e-6: p = p~ / P, q = q~ / Q with P, Q their sums. (p - a q)+ is summed over the tokens with p~ >
+// a q~ instead of p > a q: the ones on the other side add 1e-6 of themselves. So one pass gives all
+//     p = sum of p~, q = sum of q~ over those tokens, and P, Q:   sum w = p / P - a q / Q.
+struct Sums {
+  double p, q, P, Q;
+  __device__ __forceinline__ void add(const double (&pv)[8], const double (&qv)[8], double al) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = __builtin_fma(-w.al, q[k], v[k]);
+    for (int k = 0; k < 8; ++k) {
+      const double in = __builtin_fma(-al, qv[k], pv[k]) <= 0.0 ? 0.0 : 1.0;  // (NaN goes in)
+      p = __builtin_fma(in, pv[k], p);
+      q = __builtin_fma(in, qv[k], q);
+      P += pv[k];
+      Q += qv[k];
+    }
   }
-#pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = v[k] <= kNothing ? 0.0 : v[k];  // (NaN stays)
-}
+};
 
 // ---- the walk -----------------------------------------------------------------------------
 
@@ -516,7 +520,7 @@ struct WalkShared {
   double px[kWindow], qx[kWindow], u[kWindow];
   Dist p[kWindow], q[kWindow];  // of the row's parent
   int parent[kWindow], token[kWindow];
-  double tab[kTable], red[32];
+  double tab[kTable], red[4 * 16];
   int pick[32];
 };
 
@@ -658,20 +662,34 @@ __global__ __launch_bounds__(kWalkThreads) void k_verify_walk(VerifyParams p) {
     w.c = scale_of(T);
     w.p = weight_side(p.t, lo + cur, dist_of<64>(p, p.t, lo + cur, w.c, sh.tab), T, sh.tab);
     w.q = weight_side(p.d, lo + cur, dist_of<64>(p, p.d, lo + cur, w.c, sh.tab), T, sh.tab);
-    w.al = al;
-    double s = 0.0, v[8];
+    Sums s{};
     for (int i = threadIdx.x * 8; i < a.V; i += kWalkThreads * 8) {
-      weights8(p, w, i, sh.tab, v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s += v[k];
+      double pv[8], qv[8];
+      probabilities8(p.t, w.p, w.c, i, a.V, sh.tab, pv);
+      probabilities8(p.d, w.q, w.c, i, a.V, sh.tab, qv);
+      s.add(pv, qv, al);
     }
-    s = wave_sum(s);
+    s.p = wave_sum(s.p);
+    s.q = wave_sum(s.q);
+    s.P = wave_sum(s.P);
+    s.Q = wave_sum(s.Q);
     __syncthreads();
-    if (lane == 0) sh.red[wave] = s;
+    if (lane == 0) {
+      sh.red[4 * wave] = s.p;
+      sh.red[4 * wave + 1] = s.q;
+      sh.red[4 * wave + 2] = s.P;
+      sh.red[4 * wave + 3] = s.Q;
+    }
     __syncthreads();
-    s = 0.0;
-    for (int k = 0; k < kWalkThreads / 64; ++k) s += sh.red[k];
-    return s;
+    s = Sums{};
+    for (int k = 0; k < kWalkThreads / 64; ++k) {
+      s.p += sh.red[4 * k];
+      s.q += sh.red[4 * k + 1];
+      s.P += sh.red[4 * k + 2];
+      s.Q += sh.red[4 * k + 3];
+    }
+    const double left = s.p * (p.t.probs ? 1.0 : 1.0 / s.P) - al * s.q * (p.d.probs ? 1.0 : 1.0 / s.Q);
+    return left < 0.0 ? 0.0 : left;
   };
   const Walked w = walk<kWalkThreads, true>(p, sh, lo, hi - lo, T, true, sum);
   if (threadIdx.x == 0) {
@@ -682,76 +700,115 @@ __global__ __launch_bounds__(kWalkThreads) void k_verify_walk(VerifyParams p) {
 
 // ---- the new token ----------------------------------------------------------------------------
 
-// The first of k0 <= k < k1 with before + get(k0) + .. + get(k) > goal, and what comes before it in
-// `before`; the last with get(k) above nothing and before = infinity if there is none, -1 if none is. By all
-// threads of the workgroup. goal(total): from the sum of all.
-template <typename F, typename G>
-__device__ __forceinline__ int locate(WalkShared& sh, int k0, int k1, F get, G goal_of, double& total, double& before, double& goal) {
+// The block that the new token is in, from the blocks' sums, by all threads of the workgroup.
+struct Found {
+  int at;          // the first block that takes the cumulative sum above goal; the last with weight if
+                   // there is none (before = infinity then); -1 if nothing is left
+  double total, goal, before;  // sum of all, u of it, sum before the block
+  double rp, rq;   // 1 / P, 1 / Q
+};
+__device__ __forceinline__ Found locate(WalkShared& sh, const double* sums, int blocks, const double* totals, int ntotals, bool drafted,
+                                        bool pn, bool qn, double al, double u) {
   constexpr int NT = kVerifyThreads, W = NT / 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int each = (k1 - k0 + NT - 1) / NT;
-  const int i0 = k0 + static_cast<int>(threadIdx.x) * each < k1 ? k0 + threadIdx.x * each : k1, i1 = i0 + each < k1 ? i0 + each : k1;
-  double own = 0.0;
-  int last = -1;
-  for (int k = i0; k < i1; ++k) {
-    const double x = get(k);
-    own += x;
-    if (x > 0.0) last = k;
+  // (written by other workgroups: read where they were written through to)
+  auto get = [&](const double* x) TQ_INLINE { return __hip_atomic_load(x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
+  const int each = (blocks + NT - 1) / NT;
+  const int k0 = static_cast<int>(threadIdx.x) * each < blocks ? threadIdx.x * each : blocks, k1 = k0 + each < blocks ? k0 + each : blocks;
+  Sums s{};
+  if (drafted)
+    for (int k = threadIdx.x; k < ntotals; k += NT) {
+      s.P += get(totals + 2 * k);
+      s.Q += get(totals + 2 * k + 1);
+    }
+  for (int k = k0; k < k1; ++k) {
+    s.p += get(sums + 2 * k);
+    if (drafted) s.q += get(sums + 2 * k + 1);
   }
-  double incl = own;
+  double ip = s.p, iq = s.q;
 #pragma unroll
-  for (int s = 1; s < 64; s <<= 1) {
-    const double o = __shfl_up(incl, s);
-    if (lane >= s) incl += o;
+  for (int m = 1; m < 64; m <<= 1) {
+    const double o = __shfl_up(ip, m);
+    if (lane >= m) ip += o;
   }
-  double excl = __shfl_up(incl, 1);
-  if (lane == 0) excl = 0.0;
+  if (drafted) {
 #pragma unroll
-  for (int s = 32; s; s >>= 1) {
-    const int o = __shfl_xor(last, s);
-    last = o > last ? o : last;
+    for (int m = 1; m < 64; m <<= 1) {
+      const double o = __shfl_up(iq, m);
+      if (lane >= m) iq += o;
+    }
+    s.P = wave_sum(s.P);
+    s.Q = wave_sum(s.Q);
   }
-  if (lane == 63) sh.red[wave] = incl;
-  if (lane == 0) sh.pick[wave] = last;
+  if (lane == 63) {
+    sh.red[4 * wave] = ip;
+    sh.red[4 * wave + 1] = iq;
+    sh.red[4 * wave + 2] = s.P;
+    sh.red[4 * wave + 3] = s.Q;
+  }
   __syncthreads();
-  total = 0.0;
-  last = -1;
+  Sums all{}, left{};  // of all threads, of the waves before
 #pragma unroll
   for (int k = 0; k < W; ++k) {
-    if (k == wave) {
-      excl += total;
-      incl += total;
-    }
-    total += sh.red[k];
-    last = sh.pick[k] > last ? sh.pick[k] : last;
+    if (k == wave) left = all;
+    all.p += sh.red[4 * k];
+    all.q += sh.red[4 * k + 1];
+    all.P += sh.red[4 * k + 2];
+    all.Q += sh.red[4 * k + 3];
   }
-  goal = goal_of(total);
-  const uint64_t m = __ballot(before + incl > goal);
-  if (lane == 0) sh.pick[W + wave] = m ? wave * 64 + __builtin_ctzll(m) : NT;
+  Found f;
+  f.rp = drafted && pn ? 1.0 / all.P : 1.0;
+  f.rq = drafted && qn ? 1.0 / all.Q : 1.0;
+  auto weight = [&](double p, double q) TQ_INLINE { return p * f.rp - al * (q * f.rq); };
+  f.total = weight(all.p, all.q);
+  f.goal = (u > 0.0 ? u : 0.0) * f.total;
+  // a block's own weight; rounding may leave a block of nothing a little
+  auto block = [&](int k) TQ_INLINE {
+    const double x = weight(get(sums + 2 * k), drafted ? get(sums + 2 * k + 1) : 0.0);
+    return x <= kNothing ? 0.0 : x;
+  };
+  const uint64_t m = __ballot(weight(left.p + ip, left.q + iq) > f.goal);
+  if (lane == 0) sh.pick[wave] = m ? wave * 64 + __builtin_ctzll(m) : NT;
   __syncthreads();
   int hit = NT;
 #pragma unroll
-  for (int k = W - 1; k >= 0; --k) hit = sh.pick[W + k] < NT ? sh.pick[W + k] : hit;
+  for (int k = W - 1; k >= 0; --k) hit = sh.pick[k] < NT ? sh.pick[k] : hit;
   if (static_cast<int>(threadIdx.x) == hit) {
     int found = -1;
-    double run = before + excl, at = run;
-    for (int k = i0; k < i1; ++k) {
-      const double x = get(k);
+    double run = weight(left.p + (ip - s.p), left.q + (iq - s.q)), at = run;
+    for (int k = k0; k < k1; ++k) {
+      const double x = block(k);
       if (x > 0.0) {  // (rounding may leave the last of the thread's own as the one)
         found = k;
         at = run;
-        if (run + x > goal) break;
+        if (run + x > f.goal) break;
       }
       run += x;
     }
-    sh.pick[2 * W] = found;
-    sh.red[W] = at;
+    sh.pick[W] = found;
+    sh.red[4 * W] = at;
   }
   __syncthreads();
-  const int found = hit < NT ? sh.pick[2 * W] : -1;
-  before = found >= 0 ? sh.red[W] : __builtin_inf();
+  f.at = hit < NT ? sh.pick[W] : -1;
+  f.before = sh.red[4 * W];
   __syncthreads();
-  return found >= 0 ? found : last;
+  if (f.at < 0) {
+    f.before = __builtin_inf();
+    int last = -1;
+    for (int k = k0; k < k1; ++k)
+      if (block(k) > 0.0) last = k;
+#pragma unroll
+    for (int k = 32; k; k >>= 1) {
+      const int o = __shfl_xor(last, k);
+      last = o > last ? o : last;
+    }
+    if (lane == 0) sh.pick[wave] = last;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < W; ++k) f.at = sh.pick[k] > f.at ? sh.pick[k] : f.at;
+    __syncthreads();
+  }
+  return f;
 }
 
 // The workgroups of a sequence (`shares` of them) sum w over their blocks; the last finds the token.
@@ -779,7 +836,7 @@ __global__ __launch_bounds__(kVerifyThreads, 4) void k_verify_pick(VerifyParams 
     k = walk<kVerifyThreads, false>(p, sh, lo, n, T, first, [](int, double) { return 0.0; });
     if (first && threadIdx.x == 0) a.kept[b] = k.kept;
   }
-  k.al = uniform(k.al);
+  const double al = uniform(k.al);
   k.cur = __builtin_amdgcn_readfirstlane(k.cur);
   k.kept = __builtin_amdgcn_readfirstlane(k.kept);
   k.tried = __builtin_amdgcn_readfirstlane(k.tried);
@@ -792,8 +849,7 @@ __global__ __launch_bounds__(kVerifyThreads, 4) void k_verify_pick(VerifyParams 
   const int row = lo + k.cur;
   Weights w;
   w.c = scale_of(T);
-  w.al = k.al;
-  bool drafted = a.draft && k.al != 0.0;
+  bool drafted = a.draft && al != 0.0;
   Dist dp, dq{0.0, 1.0};
   if (!WALKED && k.tried && n <= kWindow) {  // (the last child's parent is this row)
     dp = sh.p[k.tried];
@@ -802,10 +858,13 @@ __global__ __launch_bounds__(kVerifyThreads, 4) void k_verify_pick(VerifyParams 
     dp = dist_of<64>(p, p.t, row, w.c, sh.tab);
     if (drafted) dq = dist_of<64>(p, p.d, row, w.c, sh.tab);
   }
+  if (dp.zinv != dp.zinv || (drafted && dq.zinv != dq.zinv)) {  // no distribution
+    if (first && threadIdx.x == 0) *token = -1;
+    return;
+  }
   w.p = weight_side(p.t, row, dp, T, sh.tab);
   w.q = w.p;
   if (drafted) w.q = weight_side(p.d, row, dq, T, sh.tab);
-  else w.q.row = nullptr;
   // tokens that were taken out of p
   int ngone = 0;
   if (!a.draft && k.tried) {
@@ -819,61 +878,59 @@ __global__ __launch_bounds__(kVerifyThreads, 4) void k_verify_pick(VerifyParams 
     }
     __syncthreads();
   }
-  auto weights = [&](int i, double (&v)[8]) TQ_INLINE {
-    weights8(p, w, i, sh.tab, v);
-    // (more of them than LDS holds: looked for among the rows again)
-    const int g0 = ngone <= kGone ? 0 : k.cur + 1, g1 = ngone <= kGone ? ngone : n;
-    for (int g = g0; g < g1; ++g) {
-      const int x = ngone <= kGone ? s_gone[g] : parent_of(a, lo, g) == k.cur ? a.tokens[lo + g] : -1;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = x == i + e ? 0.0 : v[e];
-    }
-  };
-  const int blocks = (a.V + kBlockElems - 1) / kBlockElems;
-  double* const sums = p.sums + static_cast<int64_t>(b) * blocks;
-  // p itself: its pieces are summed already, so only the piece that the token is in is looked into
-  const bool pieces = !p.t.probs && !drafted && !ngone;
-  const bool none = dp.zinv != dp.zinv || (drafted && dq.zinv != dq.zinv);  // no distribution
-  if ((pieces || none) && !first) return;
+  const int blocks = (a.V + kBlockElems - 1) / kBlockElems, ntotals = p.shares * (kVerifyThreads / 64);
+  double* const sums = p.sums + 2 * static_cast<int64_t>(b) * blocks;
+  double* const totals = p.totals + 2 * static_cast<int64_t>(b) * ntotals;
   int k0 = share * p.share_blocks < blocks ? share * p.share_blocks : blocks;
   int k1 = k0 + p.share_blocks < blocks ? k0 + p.share_blocks : blocks;
-  double total = 0.0, before = 0.0, goal = 0.0;
-  auto of_total = [&](double s) TQ_INLINE { return (u > 0.0 ? u : 0.0) * s; };
-  bool alone = pieces;  // the other workgroups have ended
-  int at = -1;
-  if (pieces && !none) {
-    const StatPart* st = p.t.stat + static_cast<int64_t>(row) * p.parts;
-    auto piece = [&](int i) TQ_INLINE {
-      const StatPart q = st[i];
-      return q.z == 0.0 ? 0.0 : q.z * add_exp2((static_cast<double>(q.top) - dp.ref) * w.c, 0.0, sh.tab) * dp.zinv;
-    };
-    at = locate(sh, 0, p.parts, piece, of_total, total, before, goal);
-    k0 = at * p.part_blocks;
-    k1 = k0 + p.part_blocks < blocks ? k0 + p.part_blocks : blocks;
-    if (before == __builtin_inf()) {  // the last token of that piece
-      before = 0.0;
-      goal = __builtin_inf();
-    }
-  }
-  // The same loop sums blocks and, at last, looks at the block that the token is in (`at`): the code is
-  // in the instruction cache then, where a copy of it took 2 us to come.
-  bool found = false;
-  double v[8];
+  // The same loop sums blocks and, at last, looks at the block that the token is in: the code is in the
+  // instruction cache then, where a copy of it took 2 us to come.
+  Found f{-1, 0.0, 0.0, 0.0, 1.0, 1.0};
+  bool alone = false;  // the other workgroups have ended
+  double pv[8], qv[8];
   for (;;) {
-    for (int block = k0 + wave; block < k1 && !none; block += kVerifyThreads / 64) {
-      double s = 0.0;
+    Sums s{};
+    for (int block = k0 + wave; block < k1; block += kVerifyThreads / 64) {
       const int i = block * kBlockElems + 8 * lane;
+      s.p = s.q = 0.0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.0;
+      for (int e = 0; e < 8; ++e) pv[e] = qv[e] = 0.0;
       if (i < a.V) {
-        weights(i, v);
-        s = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        probabilities8(p.t, w.p, w.c, i, a.V, sh.tab, pv);
+        if (drafted) probabilities8(p.d, w.q, w.c, i, a.V, sh.tab, qv);
+        // (more of them than LDS holds: looked for among the rows again)
+        const int g0 = ngone <= kGone ? 0 : k.cur + 1, g1 = ngone <= kGone ? ngone : n;
+        for (int g = g0; g < g1; ++g) {
+          const int x = ngone <= kGone ? s_gone[g] : parent_of(a, lo, g) == k.cur ? a.tokens[lo + g] : -1;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) pv[e] = x == i + e ? 0.0 : pv[e];
+        }
+        if (f.at >= 0) break;
+        if (drafted) {
+          s.add(pv, qv, al);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s.p += pv[e] < 0.0 ? 0.0 : pv[e];
+        }
       }
-      if (found) break;
-      s = wave_sum(s);
-      if (lane == 0) __hip_atomic_store(sums + block, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (f.at >= 0) break;
+      const double ps = wave_sum(s.p);
+      if (lane == 0) __hip_atomic_store(sums + 2 * block, ps <= kNothing ? 0.0 : ps, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (drafted) {
+        const double qs = wave_sum(s.q);
+        if (lane == 0) __hip_atomic_store(sums + 2 * block + 1, qs, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
     }
-    if (found || none) break;
+    if (f.at >= 0) break;
+    if (drafted) {
+      s.P = wave_sum(s.P);
+      s.Q = wave_sum(s.Q);
+      double* const t = totals + 2 * (share * (kVerifyThreads / 64) + wave);
+      if (lane == 0) {
+        __hip_atomic_store(t, s.P, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(t + 1, s.Q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
     // The sums are written through to where every XCD sees them, and read from there: the wave waits
     // for its stores before it meets the others, and no cache has to be written back (a release fence
     // does that, for the whole L2: 90 us more in the largest batch).
@@ -884,66 +941,62 @@ __global__ __launch_bounds__(kVerifyThreads, 4) void k_verify_pick(VerifyParams 
       __syncthreads();
       if (s_last != p.shares - 1) return;
       alone = true;
+    }
+    f = locate(sh, sums, blocks, totals, ntotals, drafted, !p.t.probs, !p.d.probs, al, u);
+    if ((drafted && f.total < 1e-9) || (ngone && f.total == 0.0)) {
+      // nothing is left, or no more than the rounding of the rows' sums: p itself, by this workgroup
+      f.at = -1;
+      drafted = false;
+      ngone = 0;
       k0 = 0;
       k1 = blocks;
+      continue;
     }
-    auto get = [&](int i) TQ_INLINE { return __hip_atomic_load(sums + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
-    double part;
-    at = locate(sh, k0, k1, get, [&](double s) TQ_INLINE { return pieces ? goal : of_total(s); }, part, before, goal);
-    if (!pieces) total = part;
-    if (total == 0.0 && (drafted || ngone)) {  // nothing is left: p itself, by this workgroup
-      drafted = false;
-      w.q.row = nullptr;
-      ngone = 0;
-      before = 0.0;
-    } else if (at >= 0 && total > 0.0 && total < __builtin_inf()) {
-      found = true;
-      k0 = at;
-      k1 = at + 1;
-    } else {
-      break;
+    if (f.at < 0 || !(f.total > 0.0) || f.total == __builtin_inf()) {
+      if (threadIdx.x == 0) *token = -1;
+      return;
     }
+    k0 = f.at;
+    k1 = f.at + 1;
   }
   if (wave) return;
-  int res = -1;
-  if (found) {
-    double own = 0.0;
-    const int i = at * kBlockElems + 8 * lane;
-    int last = -1;
+  double own = 0.0;
+  const int i = f.at * kBlockElems + 8 * lane;
+  int last = -1;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      own += v[e];
-      if (v[e] > 0.0) last = i + e;
-    }
-    double incl = own;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const double o = __shfl_up(incl, s);
-      if (lane >= s) incl += o;
-    }
-    double run = before + (incl - own);
-    int hit = 0x7fffffff;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      run += v[e];
-      if (v[e] > 0.0 && run > goal && hit == 0x7fffffff) hit = i + e;
-    }
-#pragma unroll
-    for (int s = 32; s; s >>= 1) {
-      const int o = __shfl_xor(hit, s), l = __shfl_xor(last, s);
-      hit = o < hit ? o : hit;
-      last = l > last ? l : last;
-    }
-    // (none above the goal in the block where its sum passed it: rounding; the last one there)
-    res = hit < 0x7fffffff && before < __builtin_inf() ? hit : last;
+  for (int e = 0; e < 8; ++e) {
+    const double x = drafted ? pv[e] * f.rp - al * (qv[e] * f.rq) : pv[e];
+    pv[e] = x <= kNothing ? 0.0 : x;
+    own += pv[e];
+    if (pv[e] > 0.0) last = i + e;
   }
-  if (lane == 0) *token = res;
+  double incl = own;
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) {
+    const double o = __shfl_up(incl, s);
+    if (lane >= s) incl += o;
+  }
+  double run = f.before + (incl - own);
+  int hit = 0x7fffffff;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    run += pv[e];
+    if (pv[e] > 0.0 && run > f.goal && hit == 0x7fffffff) hit = i + e;
+  }
+#pragma unroll
+  for (int s = 32; s; s >>= 1) {
+    const int o = __shfl_xor(hit, s), l = __shfl_xor(last, s);
+    hit = o < hit ? o : hit;
+    last = l > last ? l : last;
+  }
+  // (none above the goal in the block where its sum passed it: rounding; the last one there)
+  if (lane == 0) *token = hit < 0x7fffffff && f.before < __builtin_inf() ? hit : last;
 }
 
 // The workspace: statistics, then what the workgroups of a sequence share.
 struct VerifyLayout {
   int parts, part_blocks, shares, share_blocks, blocks;
-  size_t sums, tickets, walked, bytes;  // offsets
+  size_t sums, totals, tickets, walked, bytes;  // offsets
 };
 
 // Pieces of rows: as long as 4096 waves get one each, up to 16 blocks (a wave joins its sum over the lanes
@@ -962,7 +1015,9 @@ VerifyLayout layout(int V, int B, int M, bool tprobs, bool drafted, bool dprobs)
   l.shares = (l.blocks + l.share_blocks - 1) / l.share_blocks;
   size_t at = static_cast<size_t>(M) * (drows ? 2 : 1) * l.parts * sizeof(StatPart);
   l.sums = at;
-  at += static_cast<size_t>(B) * l.blocks * sizeof(double);
+  at += static_cast<size_t>(B) * l.blocks * 2 * sizeof(double);
+  l.totals = at;
+  at += static_cast<size_t>(B) * l.shares * (kVerifyThreads / 64) * 2 * sizeof(double);
   l.walked = at;
   at += static_cast<size_t>(B) * sizeof(Walked);
   l.tickets = at;
@@ -988,6 +1043,7 @@ hipError_t launch_verify(const VerifyArgs& a, hipStream_t s) {
              stat + static_cast<size_t>(a.M) * l.parts};
   p.parts = l.parts; p.part_blocks = l.part_blocks; p.shares = l.shares; p.share_blocks = l.share_blocks;
   p.sums = reinterpret_cast<double*>(ws + l.sums);
+  p.totals = reinterpret_cast<double*>(ws + l.totals);
   p.tickets = reinterpret_cast<int*>(ws + l.tickets);
   p.walked = reinterpret_cast<Walked*>(ws + l.walked);
   if (a.M > 0) {

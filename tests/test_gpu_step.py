@@ -10,6 +10,7 @@ import torch
 import rotation_lloyd_max_amd as tq
 from oracle import step as ost
 from parity import as_f64
+from test_gpu_verify import CLEAR
 
 pytestmark = pytest.mark.gpu
 V, HEADS, SHARE, D, PAGE, WIDTH = 97, 2, 2, 64, 16, 12
@@ -139,9 +140,9 @@ def test_steps(draft, captured):
         total = int(counts.sum())
         assert not np.isnan(as_f64(logits)[:total]).any()
         T = b.temperature.cpu().numpy()
-        kept, new, path, margin = ost.verify(as_f64(logits), tokens, as_f64(b.uniforms), want["q_offsets"],
+        kept, new, path, margins = ost.verify(as_f64(logits), tokens, as_f64(b.uniforms), want["q_offsets"],
                                              as_f64(model.guess)[tokens] if draft else None, parents, T)
-        assert margin > 1e-12
+        assert (margins > CLEAR).all()       # (five sequences, a handful of tests a step)
         assert np.array_equal(got.kept.cpu().numpy(), kept)
         assert np.array_equal(got.tokens.cpu().numpy()[:total], new[:total])
         lens2, free, _ = ost.keep(want["free"], lens, kept, want["table"], PAGE, want["q_offsets"], want["status"])

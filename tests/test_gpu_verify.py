@@ -1,11 +1,17 @@
 """Verification of drafted tokens on the GPU against the oracle: whole numbers, equal wherever the oracle's
 decisions are clear.
 
-A decision compares two numbers that the kernel computes in fp64 from sums of up to 2^18 terms: an
-exponential is off by at most 1e-15 of itself plus 2^-52 |t| for its exponent t (in bits, below 1100), a sum
-of n terms by log2(n) + 16 roundings for sums joined pairwise and by n / 256 for a thread's own, all
-2^-53: together below 1e-12 of what is compared. The oracle returns the smallest relative distance of
-its decisions to their borders; where that is below 1e-12 either side is right.
+A test of a drafted token compares numbers made with fp32 sums of exponentials 2^t, t = (x - ref) c. The
+difference, c and the product are off by half a step (2^-24) each, so t is by 3 2^-24 |t| and 2^t by 3 ln 2 2^-24 |t|;
+2^t itself by a step (2^-23), three fp32 additions by 2^-24 each. The kernel keeps |t| below 100 for what counts: together
+213 2^-24 = 1.3e-5, for p and for q: 2.6e-5 of what is compared.
+
+The new token's border in the cumulative sum is made with fp64: an exponential is off by 2e-14 of itself plus
+2^-52 |t| (t below 1000), sums of n terms by log2(n) + 16 roundings where they are joined pairwise and by n / 256 for
+a thread's own, all 2^-53: together below 1e-12 of the sum of w, divided by how much of p + a q is left in it.
+
+The oracle returns each sequence's smallest relative distances to its borders; below these bounds either
+side is right, and the sequence is not compared.
 """
 
 import ctypes
@@ -20,7 +26,7 @@ from parity import as_f64
 
 pytestmark = pytest.mark.gpu
 DTS = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
-CLEAR = 1e-12
+CLEAR = np.array([2.6e-5, 1e-10])     # (a hundredth of p + a q is left in these tests at least)
 
 
 def case(seed, B, most, V, tdt="bf16", ddt="bf16", kind="logits", tree=False, ragged=True, temperature=None, spread=3.0, noise=0.6,
@@ -73,16 +79,26 @@ def reference(c):
                          "temperature": None if c["temperature"] is None else np.asarray(c["temperature"], np.float32)})
 
 
+def compare(got, want, offsets, share=0.9):
+    """got equal to want for the sequences whose decisions are clear, `share` of them at least."""
+    kept, tokens, path, margins = want
+    clear = (margins > CLEAR).all(1)
+    assert clear.sum() >= share * len(clear) or len(clear) < 3, "the inputs of this test leave decisions open"
+    g = [x.cpu().numpy() for x in got]
+    assert np.array_equal(g[0][clear], kept[clear]), (g[0], kept)
+    rows = np.zeros(len(tokens), bool)
+    for b in np.nonzero(clear)[0]:
+        rows[offsets[b]:offsets[b + 1]] = True
+    assert np.array_equal(g[2][rows], path[rows])
+    assert np.array_equal(g[1][rows], tokens[rows]), (g[1], tokens)
+
+
 def check(c, got=None):
-    kept, tokens, path, margin = reference(c)
+    want = reference(c)
     if got is None:
         got = tq.verify(**on_gpu(c))
     torch.cuda.synchronize()
-    assert margin > CLEAR, "the inputs of this test leave a decision open"
-    assert np.array_equal(got.kept.cpu().numpy(), kept), (got.kept.tolist(), kept)
-    end = int(c["offsets"][-1])
-    assert np.array_equal(got.path.cpu().numpy()[:end], path[:end])
-    assert np.array_equal(got.tokens.cpu().numpy()[:end], tokens[:end])
+    compare(got, want, c["offsets"])
     return got
 
 
@@ -137,11 +153,7 @@ def test_values_of_any_size():
         c["target"][1::2] *= 1000.0
         c["draft"][::3] *= 500.0
         c["target"][2] = -c["target"][2].abs() * 100.0 - 5000.0
-        kept, tokens, path, margin = reference(c)
-        got = tq.verify(**on_gpu(c))
-        torch.cuda.synchronize()
-        # three equal largest values: thirds, which u meets only by chance; others as always
-        assert margin > CLEAR and np.array_equal(got.tokens.cpu().numpy(), tokens) and np.array_equal(got.kept.cpu().numpy(), kept)
+        check(c)     # (three equal largest values: thirds, which u meets only by chance)
 
 
 @pytest.mark.parametrize("T", [0.0, -1.0, float("nan"), float("inf"), 1e-38, 1e-44, 1e38])
