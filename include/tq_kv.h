@@ -86,7 +86,8 @@ int tq_rope(const void *x, tq_dtype dtype, int64_t tokens, int32_t heads, int32_
  *                `axes` is not turned (only scaled by the gain)
  *   positions    device int32, `axes` rows of `tokens` positions, axis_stride elements apart (0: the
  *                same positions for every axis, as text has them); axes in [1, 255]
- * Everything else is as in tq_rope, and with one axis so are the results, bit for bit. */
+ * Everything else is as in tq_rope, and with one axis so are the results of bf16 and fp16, bit for bit;
+ * fp32 vectors are turned in fp64 and rounded once. */
 int tq_rope_axes(const void *x, tq_dtype dtype, int64_t tokens, int32_t heads, int32_t head_dim,
                  int64_t x_token_stride, int64_t x_head_stride, const int32_t *positions,
                  int64_t axis_stride, int32_t axes, const uint8_t *axis, const tq_rope_params *rope,

@@ -1,5 +1,7 @@
 """Rotary positions of several axes on the GPU against the oracle, pair by pair; bounds as derived in
-test_gpu_rope.py (12 2^-24 gain (|a| + |b|) and one rounding). One axis gives tq_rope's bits."""
+test_gpu_rope.py (12 2^-24 gain (|a| + |b|) and one rounding); fp32 vectors are turned in fp64: one rounding
+and 2^-31 gain (|a| + |b|) (the angle of position 2^18 in fp64: two roundings of its turns, 2 2^-53 2^18, times 2 pi: 2^-31).
+One axis gives tq_rope's bits in the 16-bit types."""
 
 import numpy as np
 import pytest
@@ -31,7 +33,8 @@ def check(got, x, pos, r, transposed=False):
     ref, a, h = reference(x, pos, r, transposed), np.abs(as_f64(x)), r.rot_dim // 2
     i, j = (slice(0, r.rot_dim, 2), slice(1, r.rot_dim, 2)) if r.interleaved else (slice(0, h), slice(h, r.rot_dim))
     room = np.zeros_like(a)
-    room[..., i] = room[..., j] = 12 * 2.0 ** -24 * r.gain * (a[..., i] + a[..., j])
+    near = pos.numel() == 0 or int(pos.abs().max()) <= 1 << 18
+    room[..., i] = room[..., j] = (2.0 ** -31 if x.dtype == torch.float32 and near else 12 * 2.0 ** -24) * r.gain * (a[..., i] + a[..., j])
     tiny = 2.0 ** -25 if x.dtype == torch.float16 else 0.0
     bound = room + HALF_STEP[x.dtype] * (np.abs(ref) + room) + tiny
     bound[..., r.rot_dim:] = 0.0
@@ -61,7 +64,7 @@ def test_matches_oracle(dt, interleaved, tokens, heads, D, sections, kw):
         check(got, x, pos, r, transposed)
 
 
-@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("dt", DTS[1:])
 def test_equal_axes_are_one_axis_bit_for_bit(dt):
     r = tq.rope_axes((16, 24, 24))
     x, pos = make(77, 6, 128, 1, dt, seed=1)
