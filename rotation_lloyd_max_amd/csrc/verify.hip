@@ -13,11 +13,13 @@
 // that it is made of are fp64. The rows' sums that the tests need, of all rows, are of exponentials in
 // fp32; the pass that sums w sums the row that it comes from once more, in fp64 (see Sums).
 //
-// Two launches. k_verify_stats: largest value and sum of exponentials of every row of logits that can
-// be looked at, a wave per piece of a row. k_verify_pick: each workgroup of a sequence joins the pieces and
-// walks (all do the same: cheaper than another launch), sums w over its share of the vocabulary, and
-// the one that comes last finds the token. Where siblings are tried against a draft, sums S are needed
-// during the walk: k_verify_walk, a workgroup per sequence, goes first.
+// Launches. k_verify_stats: largest value and sum of exponentials of every row of logits that can be
+// looked at, a wave per piece of a row. k_verify_pick: each workgroup of a sequence joins the pieces and walks
+// (all do the same: cheaper than another launch), sums w over its share of the vocabulary, and the one that
+// comes last finds the token. Where siblings are tried against a draft, S is such a sum too: the last
+// workgroup walks on with it, and the next launch of k_verify_pick sums what the walk needs then. Two more
+// launches follow, in which sequences that are done end at once; what is still open in the last one
+// its last workgroup sums alone (three siblings turned away on one way; two to three in a hundred walks).
 #include "device_common.hpp"
 #include "internal.hpp"
 
@@ -31,6 +33,7 @@ constexpr int kBlockElems = 512;    // a wave's step: 8 elements a lane
 constexpr int kWindow = 256;        // rows whose probabilities are in LDS at a time
 constexpr int kGone = 256;          // tried tokens in LDS
 constexpr int kTable = 256;         // 2^(i / 256)
+constexpr int kPasses = 4;          // launches of k_verify_pick for trees with a draft
 
 // Of a piece of a row, in units of the largest value: z = sum 2^((x - top) c), c = log2(e) / T. Where
 // it holds NaN or +infinity z is NaN. at: the index of its first largest value (greedy rows).
@@ -48,11 +51,46 @@ struct Side {  // target or draft
   const StatPart* stat;  // [rows][parts]
 };
 
-// What the walk found (k_verify_walk to k_verify_pick).
-struct Walked {
-  double al;
-  int cur, kept, tried;
+// What w is summed from. Let p~ = p P, q~ = q Q be a row's values with their own sums P, Q (2^((x - ref) c) of
+// logits; probabilities as they are, P = Q = 1), and rho = a P / Q by the rows' sums of k_verify_stats, which is
+// right to 1e-6. (p - a q)+ is summed over the tokens with p~ > rho q~ instead of p > a q: the ones on the
+// other side add 1e-6 of themselves. So one pass gives all:
+//     p = sum of p~, q = sum of q~ over those tokens, and P, Q:   sum w = p / P - a q / Q.
+struct Sums {
+  double p, q, P, Q;
+  __device__ __forceinline__ void add(const double (&pv)[8], const double (&qv)[8], double rho) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const double in = __builtin_fma(-rho, qv[k], pv[k]) <= 0.0 ? 0.0 : 1.0;  // (NaN goes in)
+      p = __builtin_fma(in, pv[k], p);
+      q = __builtin_fma(in, qv[k], q);
+      P += pv[k];
+      Q += qv[k];
+    }
+  }
 };
+
+// A walk that has come to a row.
+struct Walk {
+  double al, S;
+  int cur, kept, tried;  // tried: the last child of cur that went (0: none)
+  int next;              // the first row that it has not looked at
+};
+// What the walk needs of a row.
+struct Dist {  // probabilities of a row of logits: 2^((x - ref) c) zinv; zinv NaN: the row is no distribution
+  double ref, zinv;
+};
+struct RowInfo {
+  double px, qx, u;   // its token's probabilities under its parent, its number
+  Dist p, q;          // of its parent
+  int parent, token;  // parent -1: a row that is no child of any
+};
+// What one launch of k_verify_pick leaves to the next.
+struct Pending {
+  Walk w;
+  int state;  // kDone, or what has to be summed for cur: kLeft: S, kToken: w
+};
+enum { kDone = 0, kLeft = 1, kToken = 2 };
 
 struct VerifyParams {
   VerifyArgs a;
@@ -60,9 +98,10 @@ struct VerifyParams {
   int parts, part_blocks;  // pieces of a row of logits, and kBlockElems in each
   int shares, share_blocks;  // the same of k_verify_pick's workgroups
   double* sums;            // [B][blocks][2]: Sums::p and Sums::q of a block
-  double* totals;          // [B][shares * waves][2]: of p and q
-  int* tickets;            // [B]
-  Walked* walked;          // [B] where k_verify_walk runs
+  Sums* totals;            // [B][shares * waves]: P and Q; p and q where S is summed
+  int* tickets;            // [kPasses][B]
+  Pending* pending;        // [B], and
+  RowInfo* rows;           // [M], of trees with a draft
 };
 
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
@@ -326,7 +365,7 @@ __device__ __forceinline__ StatPart stat_largest(const char* row, int V, int i0,
 __global__ __launch_bounds__(kVerifyThreads) void k_verify_stats(VerifyParams p, int64_t unit0, int64_t units) {
   const VerifyArgs& a = p.a;
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < a.B; i += kVerifyThreads) p.tickets[i] = 0;
+    for (int i = threadIdx.x; i < kPasses * a.B; i += kVerifyThreads) p.tickets[i] = 0;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int lim = a.offsets[a.B] < a.M ? a.offsets[a.B] : a.M;
   for (int64_t unit = unit0 + static_cast<int64_t>(blockIdx.x) * (kVerifyThreads / 64) + wave; unit < units;
@@ -368,11 +407,6 @@ __global__ __launch_bounds__(kVerifyThreads) void k_verify_stats(VerifyParams p,
 }
 
 // ---- rows as distributions ------------------------------------------------------------------
-
-// Probabilities of a row of logits: 2^((x - ref) c) zinv; zinv NaN: the row is no distribution.
-struct Dist {
-  double ref, zinv;
-};
 
 __device__ __forceinline__ double probability(const Side& s, const Dist& d, double c, float x, const double* tab) {
   if (s.probs) return x;
@@ -448,12 +482,12 @@ __device__ __forceinline__ int largest_of(const VerifyParams& p, int row) {
 // Weights up to here count as nothing: masked tokens come out as about 2^-1000, not 0.
 constexpr double kNothing = 1e-280;
 
-// One side of what the new token is drawn from (or S is summed over).
+// One side of what the new token is drawn from (or S is summed over): values p~ of Sums.
 struct WeightSide {
-  const char* row;  // null: none
+  const char* row;
   Dist d;
   Exp2Near e;
-  double scale;  // probability = 2^(x c - e.base) scale
+  double sum;  // P by k_verify_stats (probabilities: 1)
 };
 struct Weights {
   WeightSide p, q;
@@ -465,13 +499,18 @@ __device__ __forceinline__ double uniform(double x) {
   return __hiloint2double(__builtin_amdgcn_readfirstlane(__double2hiint(x)), __builtin_amdgcn_readfirstlane(__double2loint(x)));
 }
 
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ Walk uniform(const Walk& w) {
+  return Walk{uniform(w.al), uniform(w.S), uniform(w.cur), uniform(w.kept), uniform(w.tried), uniform(w.next)};
+}
+
 __device__ __forceinline__ WeightSide weight_side(const Side& s, int row, const Dist& d, double T, const double* tab) {
   WeightSide w;
   const double c = scale_of(T);
   w.row = s.data + row * s.stride;
   w.d = Dist{uniform(d.ref), uniform(d.zinv)};
   w.e = exp2_near(w.d.ref, c, reach_of(T));
-  w.scale = uniform(d.zinv * add_exp2(w.e.base - d.ref * c, 0.0, tab));
+  w.sum = uniform(s.probs ? 1.0 : 1.0 / (w.e.ok ? d.zinv * add_exp2(w.e.base - d.ref * c, 0.0, tab) : d.zinv));
   w.e.c = uniform(c);
   w.e.base = uniform(w.e.base);
   w.e.magic = uniform(w.e.magic);
@@ -480,7 +519,7 @@ __device__ __forceinline__ WeightSide weight_side(const Side& s, int row, const 
   return w;
 }
 
-__device__ __forceinline__ void probabilities8(const Side& s, const WeightSide& w, double c, int i, int V, const double* tab,
+__device__ __forceinline__ void values8(const Side& s, const WeightSide& w, double c, int i, int V, const double* tab,
                                                double (&v)[8]) {
   float f[8];
   load8_any(w.row, s.dt, i, V, s.probs ? 0.f : -__builtin_inff(), f);
@@ -489,37 +528,19 @@ __device__ __forceinline__ void probabilities8(const Side& s, const WeightSide& 
     for (int k = 0; k < 8; ++k) v[k] = f[k];
   } else if (w.e.ok) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = add_exp2_near(w.e, f[k], 0.0, tab) * w.scale;
+    for (int k = 0; k < 8; ++k) v[k] = add_exp2_near(w.e, f[k], 0.0, tab);
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = probability(s, w.d, c, f[k], tab);
-  }
-}
-
-// What w is summed from. Let p~, q~ be a row's probabilities by the rows' sums of k_verify_stats, off by a factor
-// each that is 1 to 1e-6: p = p~ / P, q = q~ / Q with P, Q their sums. (p - a q)+ is summed over the tokens with p~ >
-// a q~ instead of p > a q: the ones on the other side add 1e-6 of themselves. So one pass gives all
-//     p = sum of p~, q = sum of q~ over those tokens, and P, Q:   sum w = p / P - a q / Q.
-struct Sums {
-  double p, q, P, Q;
-  __device__ __forceinline__ void add(const double (&pv)[8], const double (&qv)[8], double al) {
-#pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const double in = __builtin_fma(-al, qv[k], pv[k]) <= 0.0 ? 0.0 : 1.0;  // (NaN goes in)
-      p = __builtin_fma(in, pv[k], p);
-      q = __builtin_fma(in, qv[k], q);
-      P += pv[k];
-      Q += qv[k];
+      v[k] = f[k] == -__builtin_inff() ? 0.0 : add_exp2((f[k] - w.d.ref) * c, 0.0, tab);
     }
   }
-};
+}
 
 // ---- the walk -----------------------------------------------------------------------------
 
 struct WalkShared {
-  double px[kWindow], qx[kWindow], u[kWindow];
-  Dist p[kWindow], q[kWindow];  // of the row's parent
-  int parent[kWindow], token[kWindow];
+  RowInfo row[kWindow];
   double tab[kTable], red[4 * 16];
   int pick[32];
 };
@@ -533,172 +554,120 @@ __device__ __forceinline__ bool tried_before(const VerifyArgs& a, const WalkShar
   for (int r = cur + 1; r < end && !found; r += 64) {
     const int i = r + lane;
     bool hit = false;
-    if (i < end) hit = n <= kWindow ? sh.parent[i] == cur && sh.token[i] == x : parent_of(a, lo, i) == cur && a.tokens[lo + i] == x;
+    if (i < end) hit = n <= kWindow ? sh.row[i].parent == cur && sh.row[i].token == x : parent_of(a, lo, i) == cur && a.tokens[lo + i] == x;
     found = __ballot(hit) != 0;
   }
   return found;
 }
 
-// The walk of sequence b, by all waves of the workgroup alike; `writes`: this workgroup writes the
-// outputs but the new token. `sum(cur, al)`: S of a row, called by all threads (SUMS only).
-template <int NT, bool SUMS, typename F>
-__device__ __forceinline__ Walked walk(const VerifyParams& p, WalkShared& sh, int lo, int n, double T, bool writes, F sum) {
+// Rows [w0, w1) into LDS: their tokens' probabilities under their parents, 16 lanes a row. kept: where a
+// launch before has left them (load), or where they are left for the next (null: not).
+__device__ __forceinline__ void fill_window(const VerifyParams& p, WalkShared& sh, int lo, int w0, int w1, double T, RowInfo* kept,
+                                            bool load) {
   const VerifyArgs& a = p.a;
-  const int lane = threadIdx.x & 63;
   const bool greedy = !(T > 0.0), drafted = a.draft && !greedy;
   const double c = scale_of(T);
-  Walked w{0.0, 0, 1, 0};
-  double S = 1.0;
-  int largest = greedy ? largest_of(p, lo) : -1;
-  bool over = false;
-  for (int w0 = 0; w0 < n && !over; w0 += kWindow) {
-    const int w1 = n - w0 < kWindow ? n : w0 + kWindow;
-    // the probabilities of the window's tokens under their parents
-    if (w0) __syncthreads();
-    constexpr int LANES = 16;
-    for (int r = w0 + static_cast<int>(threadIdx.x) / LANES; r < w1; r += NT / LANES) {
+  constexpr int LANES = 16;
+  if (load) {
+    for (int r = w0 + static_cast<int>(threadIdx.x); r < w1; r += kVerifyThreads) sh.row[r - w0] = kept[lo + r];
+  } else {
+    for (int r = w0 + static_cast<int>(threadIdx.x) / LANES; r < w1; r += kVerifyThreads / LANES) {
       const int up = parent_of(a, lo, r), x = a.tokens[lo + r];
       const float u = a.uniforms[lo + r];
       const bool any = r > 0 && up >= 0 && up < r && x >= 0 && x < a.V;
-      Dist t{0.0, 1.0}, q{0.0, 1.0};
-      double px = 0.0, qx = 0.0;
+      RowInfo i{0.0, 0.0, u, {0.0, 1.0}, {0.0, 1.0}, any ? up : -1, x};
       if (any && !greedy) {
         const float xt = load_any(p.t.data + (lo + up) * p.t.stride, p.t.dt, x);
         float xd = 0.f;
         if (drafted) xd = load_any(p.d.data + (lo + up) * p.d.stride, p.d.dt, x);
-        t = dist_of<LANES>(p, p.t, lo + up, c, sh.tab);
-        px = probability(p.t, t, c, xt, sh.tab);
+        i.p = dist_of<LANES>(p, p.t, lo + up, c, sh.tab);
+        i.px = probability(p.t, i.p, c, xt, sh.tab);
         if (drafted) {
-          q = dist_of<LANES>(p, p.d, lo + up, c, sh.tab);
-          qx = probability(p.d, q, c, xd, sh.tab);
+          i.q = dist_of<LANES>(p, p.d, lo + up, c, sh.tab);
+          i.qx = probability(p.d, i.q, c, xd, sh.tab);
         }
       }
       if ((threadIdx.x & (LANES - 1)) == 0) {
-        sh.parent[r - w0] = any ? up : -1;
-        sh.token[r - w0] = x;
-        sh.px[r - w0] = px;
-        sh.qx[r - w0] = qx;
-        sh.u[r - w0] = u;
-        sh.p[r - w0] = t;
-        sh.q[r - w0] = q;
-      }
-    }
-    __syncthreads();
-    for (int next = w0;;) {
-      // the next child of cur in the window
-      int r = w1;
-      for (int i = next; i < w1; i += 64) {
-        const uint64_t m = __ballot(i + lane < w1 && sh.parent[i + lane - w0] == w.cur);
-        if (m) {
-          r = i + __builtin_ctzll(m);
-          break;
-        }
-      }
-      if (r >= w1) break;
-      next = r + 1;
-      const int x = sh.token[r - w0];
-      const double u = sh.u[r - w0], px = sh.px[r - w0], qx = sh.qx[r - w0];
-      bool yes, taken = false;
-      if (greedy) {
-        yes = x == largest;
-      } else if (drafted) {
-        yes = u * S * qx < px - w.al * qx;
-      } else {
-        taken = w.tried && tried_before(a, sh, lo, n, w.cur, r, x);
-        yes = u * S < (taken ? 0.0 : px);
-      }
-      if (yes) {
-        if (writes && threadIdx.x == 0) {
-          a.out_tokens[lo + w.kept - 1] = x;
-          a.path[lo + w.kept] = r;
-        }
-        w.cur = r;
-        ++w.kept;
-        w.tried = 0;
-        w.al = 0.0;
-        S = 1.0;
-        if (greedy) largest = largest_of(p, lo + r);
-      } else {
-        w.tried = r;
-        if (drafted) {
-          w.al += S;
-          if constexpr (SUMS) {
-            // (of use only if another child follows)
-            bool more = false;
-            for (int i = r + 1; i < n && !more; i += 64) more = __ballot(i + lane < n && parent_of(a, lo, i + lane) == w.cur) != 0;
-            if (more) S = sum(w.cur, w.al);
-          }
-        } else if (!taken) {
-          S -= px;
-        }
-        if (!a.parents) over = true;
-        if (over) break;
+        sh.row[r - w0] = i;
+        if (kept) kept[lo + r] = i;
       }
     }
   }
-  if (writes) {
-    for (int i = w.kept + threadIdx.x; i < n; i += NT) {
-      a.out_tokens[lo + i] = -1;
-      a.path[lo + i] = -1;
-    }
-    if (threadIdx.x == 0) a.path[lo] = 0;
-  }
-  return w;
+  __syncthreads();
 }
 
-// Rows with siblings tried against a draft: S of the rows on the way takes passes over the vocabulary.
-constexpr int kWalkThreads = 1024;
-__global__ __launch_bounds__(kWalkThreads) void k_verify_walk(VerifyParams p) {
-  __shared__ WalkShared sh;
+// Walks on, all waves of the workgroup alike, until S of cur is needed (true) or no child stays (false).
+// `writes`: this workgroup writes the tokens that stay. held: the window in LDS, -1 for none. later: not the first launch.
+template <bool TREES>
+__device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int lo, int n, double T, bool writes, Walk& w, int& held,
+                                     bool later) {
   const VerifyArgs& a = p.a;
-  const int b = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int lo, hi;
-  seq_rows(a, b, lo, hi);
-  if (hi == lo) return;
-  fill_table(sh.tab);
-  const double T = temperature_of(a, b);
-  auto sum = [&](int cur, double al) TQ_INLINE {
-    Weights w;
-    w.c = scale_of(T);
-    w.p = weight_side(p.t, lo + cur, dist_of<64>(p, p.t, lo + cur, w.c, sh.tab), T, sh.tab);
-    w.q = weight_side(p.d, lo + cur, dist_of<64>(p, p.d, lo + cur, w.c, sh.tab), T, sh.tab);
-    Sums s{};
-    for (int i = threadIdx.x * 8; i < a.V; i += kWalkThreads * 8) {
-      double pv[8], qv[8];
-      probabilities8(p.t, w.p, w.c, i, a.V, sh.tab, pv);
-      probabilities8(p.d, w.q, w.c, i, a.V, sh.tab, qv);
-      s.add(pv, qv, al);
+  const int lane = threadIdx.x & 63;
+  const bool greedy = !(T > 0.0), drafted = a.draft && !greedy;
+  int largest = greedy ? largest_of(p, lo + w.cur) : -1;
+  while (w.next < n) {
+    const int w0 = w.next / kWindow * kWindow, w1 = n - w0 < kWindow ? n : w0 + kWindow;
+    if (held != w0) {
+      if (held >= 0) __syncthreads();
+      fill_window(p, sh, lo, w0, w1, T, TREES && (later || writes) ? p.rows : nullptr, TREES && later);
+      held = w0;
     }
-    s.p = wave_sum(s.p);
-    s.q = wave_sum(s.q);
-    s.P = wave_sum(s.P);
-    s.Q = wave_sum(s.Q);
-    __syncthreads();
-    if (lane == 0) {
-      sh.red[4 * wave] = s.p;
-      sh.red[4 * wave + 1] = s.q;
-      sh.red[4 * wave + 2] = s.P;
-      sh.red[4 * wave + 3] = s.Q;
+    // the next child of cur in the window
+    int r = w1;
+    for (int i = w.next; i < w1; i += 64) {
+      const uint64_t m = __ballot(i + lane < w1 && sh.row[i + lane - w0].parent == w.cur);
+      if (m) {
+        r = i + __builtin_ctzll(m);
+        break;
+      }
     }
-    __syncthreads();
-    s = Sums{};
-    for (int k = 0; k < kWalkThreads / 64; ++k) {
-      s.p += sh.red[4 * k];
-      s.q += sh.red[4 * k + 1];
-      s.P += sh.red[4 * k + 2];
-      s.Q += sh.red[4 * k + 3];
+    w.next = r;
+    if (r == w1) continue;
+    w.next = r + 1;
+    const RowInfo& row = sh.row[r - w0];
+    const int x = row.token;
+    const double u = row.u, px = row.px, qx = row.qx;
+    bool yes, taken = false;
+    if (greedy) {
+      yes = x == largest;
+    } else if (drafted) {
+      yes = u * w.S * qx < px - w.al * qx;
+    } else {
+      taken = w.tried && tried_before(a, sh, lo, n, w.cur, r, x);
+      yes = u * w.S < (taken ? 0.0 : px);
     }
-    const double left = s.p * (p.t.probs ? 1.0 : 1.0 / s.P) - al * s.q * (p.d.probs ? 1.0 : 1.0 / s.Q);
-    return left < 0.0 ? 0.0 : left;
-  };
-  const Walked w = walk<kWalkThreads, true>(p, sh, lo, hi - lo, T, true, sum);
-  if (threadIdx.x == 0) {
-    p.walked[b] = w;
-    a.kept[b] = w.kept;
+    if (yes) {
+      if (writes && threadIdx.x == 0) {
+        a.out_tokens[lo + w.kept - 1] = x;
+        a.path[lo + w.kept] = r;
+      }
+      w = Walk{0.0, 1.0, r, w.kept + 1, 0, r + 1};
+      if (greedy) largest = largest_of(p, lo + r);
+    } else {
+      w.tried = r;
+      if (!a.parents) {  // a chain has no siblings
+        w.al = 1.0;
+        w.next = n;
+      } else if (TREES && drafted) {
+        w.al += w.S;
+        // (S is of use only if another child follows)
+        bool more = false;
+        for (int i = r + 1; i < n && !more; i += 64) more = __ballot(i + lane < n && parent_of(a, lo, i + lane) == w.cur) != 0;
+        if (more) return true;
+      } else if (!taken) {
+        w.S -= px;
+      }
+    }
   }
+  return false;
 }
 
 // ---- the new token ----------------------------------------------------------------------------
+
+// What other workgroups have written, from where it was written through to.
+__device__ __forceinline__ double shared_load(const double* x) {
+  return __hip_atomic_load(x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 
 // The block that the new token is in, from the blocks' sums, by all threads of the workgroup.
 struct Found {
@@ -707,23 +676,21 @@ struct Found {
   double total, goal, before;  // sum of all, u of it, sum before the block
   double rp, rq;   // 1 / P, 1 / Q
 };
-__device__ __forceinline__ Found locate(WalkShared& sh, const double* sums, int blocks, const double* totals, int ntotals, bool drafted,
-                                        bool pn, bool qn, double al, double u) {
+__device__ __forceinline__ Found locate(WalkShared& sh, const double* sums, int blocks, const Sums* totals, int ntotals, bool drafted,
+                                        bool plogits, bool qlogits, double al, double u) {
   constexpr int NT = kVerifyThreads, W = NT / 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  // (written by other workgroups: read where they were written through to)
-  auto get = [&](const double* x) TQ_INLINE { return __hip_atomic_load(x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
   const int each = (blocks + NT - 1) / NT;
   const int k0 = static_cast<int>(threadIdx.x) * each < blocks ? threadIdx.x * each : blocks, k1 = k0 + each < blocks ? k0 + each : blocks;
   Sums s{};
   if (drafted)
     for (int k = threadIdx.x; k < ntotals; k += NT) {
-      s.P += get(totals + 2 * k);
-      s.Q += get(totals + 2 * k + 1);
+      s.P += shared_load(&totals[k].P);
+      s.Q += shared_load(&totals[k].Q);
     }
   for (int k = k0; k < k1; ++k) {
-    s.p += get(sums + 2 * k);
-    if (drafted) s.q += get(sums + 2 * k + 1);
+    s.p += shared_load(sums + 2 * k);
+    if (drafted) s.q += shared_load(sums + 2 * k + 1);
   }
   double ip = s.p, iq = s.q;
 #pragma unroll
@@ -757,14 +724,14 @@ __device__ __forceinline__ Found locate(WalkShared& sh, const double* sums, int 
     all.Q += sh.red[4 * k + 3];
   }
   Found f;
-  f.rp = drafted && pn ? 1.0 / all.P : 1.0;
-  f.rq = drafted && qn ? 1.0 / all.Q : 1.0;
+  f.rp = drafted && plogits ? 1.0 / all.P : 1.0;
+  f.rq = drafted && qlogits ? 1.0 / all.Q : 1.0;
   auto weight = [&](double p, double q) TQ_INLINE { return p * f.rp - al * (q * f.rq); };
   f.total = weight(all.p, all.q);
   f.goal = (u > 0.0 ? u : 0.0) * f.total;
   // a block's own weight; rounding may leave a block of nothing a little
   auto block = [&](int k) TQ_INLINE {
-    const double x = weight(get(sums + 2 * k), drafted ? get(sums + 2 * k + 1) : 0.0);
+    const double x = weight(shared_load(sums + 2 * k), drafted ? shared_load(sums + 2 * k + 1) : 0.0);
     return x <= kNothing ? 0.0 : x;
   };
   const uint64_t m = __ballot(weight(left.p + ip, left.q + iq) > f.goal);
@@ -811,109 +778,159 @@ __device__ __forceinline__ Found locate(WalkShared& sh, const double* sums, int 
   return f;
 }
 
-// The workgroups of a sequence (`shares` of them) sum w over their blocks; the last finds the token.
-template <bool WALKED>
-__global__ __launch_bounds__(kVerifyThreads, 4) void k_verify_pick(VerifyParams p) {
+// The workgroups of a sequence (`shares` of them) sum w over their blocks; the last finds the token, or walks on.
+// TREES: siblings against a draft, several launches (as a branch at run time it spilled registers).
+template <bool TREES>
+__global__ __launch_bounds__(kVerifyThreads, TREES ? 3 : 4) void k_verify_pick(VerifyParams p, int pass, int passes) {
   __shared__ WalkShared sh;
   __shared__ int s_gone[kGone], s_last;
   const VerifyArgs& a = p.a;
   const int b = blockIdx.x / p.shares, share = blockIdx.x - b * p.shares;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const bool first = share == 0;
+  bool writes = share == 0;  // this workgroup writes outputs
   int lo, hi;
   seq_rows(a, b, lo, hi);
   const int n = hi - lo;
   if (n == 0) {
-    if (first && threadIdx.x == 0) a.kept[b] = 0;
+    if (writes && threadIdx.x == 0) a.kept[b] = 0;
     return;
+  }
+  Pending st;
+  if (TREES && pass) {
+    st = p.pending[b];
+    if (st.state == kDone) return;
   }
   fill_table(sh.tab);
   const double T = uniform(temperature_of(a, b)), u = uniform(a.uniforms[lo]);
-  Walked k;
-  if constexpr (WALKED) {
-    k = p.walked[b];
-  } else {
-    k = walk<kVerifyThreads, false>(p, sh, lo, n, T, first, [](int, double) { return 0.0; });
-    if (first && threadIdx.x == 0) a.kept[b] = k.kept;
-  }
-  const double al = uniform(k.al);
-  k.cur = __builtin_amdgcn_readfirstlane(k.cur);
-  k.kept = __builtin_amdgcn_readfirstlane(k.kept);
-  k.tried = __builtin_amdgcn_readfirstlane(k.tried);
-  int32_t* const token = a.out_tokens + lo + k.kept - 1;
-  if (!(T > 0.0)) {
-    const int at = largest_of(p, lo + k.cur);
-    if (first && threadIdx.x == 0) *token = at;
-    return;
-  }
-  const int row = lo + k.cur;
-  Weights w;
-  w.c = scale_of(T);
-  bool drafted = a.draft && al != 0.0;
-  Dist dp, dq{0.0, 1.0};
-  if (!WALKED && k.tried && n <= kWindow) {  // (the last child's parent is this row)
-    dp = sh.p[k.tried];
-    dq = sh.q[k.tried];
-  } else {
-    dp = dist_of<64>(p, p.t, row, w.c, sh.tab);
-    if (drafted) dq = dist_of<64>(p, p.d, row, w.c, sh.tab);
-  }
-  if (dp.zinv != dp.zinv || (drafted && dq.zinv != dq.zinv)) {  // no distribution
-    if (first && threadIdx.x == 0) *token = -1;
-    return;
-  }
-  w.p = weight_side(p.t, row, dp, T, sh.tab);
-  w.q = w.p;
-  if (drafted) w.q = weight_side(p.d, row, dq, T, sh.tab);
-  // tokens that were taken out of p
-  int ngone = 0;
-  if (!a.draft && k.tried) {
-    for (int r0 = k.cur + 1; r0 < n; r0 += 64) {
-      const int r = r0 + lane;
-      const bool child = r < n && parent_of(a, lo, r) == k.cur;
-      const uint64_t m = __ballot(child);
-      const int at = ngone + __popcll(m & ((1ull << lane) - 1));
-      if (wave == 0 && child && at < kGone) s_gone[at] = a.tokens[lo + r];
-      ngone += __popcll(m);
-    }
-    __syncthreads();
+  int held = -1;
+  if (!TREES || !pass) st.w = Walk{0.0, 1.0, 0, 1, 0, 1};
+  if constexpr (!TREES) {
+    walk<false>(p, sh, lo, n, T, writes, st.w, held, false);
+    st.w = uniform(st.w);
+    st.state = kToken;
   }
   const int blocks = (a.V + kBlockElems - 1) / kBlockElems, ntotals = p.shares * (kVerifyThreads / 64);
   double* const sums = p.sums + 2 * static_cast<int64_t>(b) * blocks;
-  double* const totals = p.totals + 2 * static_cast<int64_t>(b) * ntotals;
+  Sums* const totals = p.totals + static_cast<int64_t>(b) * ntotals;
   int k0 = share * p.share_blocks < blocks ? share * p.share_blocks : blocks;
   int k1 = k0 + p.share_blocks < blocks ? k0 + p.share_blocks : blocks;
+  bool alone = false;              // the others have ended
+  bool walks = TREES && !pass, fresh = true;  // to walk on; to begin with the row that the walk has come to
+  bool drafted = false;
+  int ngone = 0;
+  double al = 0.0, rho = 0.0;
+  Weights w;
+  Found f{-1, 0.0, 0.0, 0.0, 1.0, 1.0};
+  double pv[8], qv[8];
+  // Begins with the row that the walk has come to; false: the token needs no sums, and is written.
+  auto begin = [&]() TQ_INLINE {
+    al = st.w.al;
+    int res = -2;  // a token that needs no sums
+    if (st.state == kToken) {
+      if (writes) {
+        for (int i = st.w.kept + threadIdx.x; i < n; i += kVerifyThreads) {
+          a.out_tokens[lo + i] = -1;
+          a.path[lo + i] = -1;
+        }
+        if (threadIdx.x == 0) {
+          a.path[lo] = 0;
+          a.kept[b] = st.w.kept;
+        }
+      }
+      if (!(T > 0.0)) res = largest_of(p, lo + st.w.cur);
+    }
+    const int row = lo + st.w.cur;
+    w.c = scale_of(T);
+    drafted = a.draft && al != 0.0;
+    Dist dp, dq{0.0, 1.0};
+    if (res == -2) {
+      if (st.w.tried && held == 0 && n <= kWindow) {  // (the last child's parent is this row)
+        dp = sh.row[st.w.tried].p;
+        dq = sh.row[st.w.tried].q;
+      } else if (TREES && pass && st.w.tried) {
+        dp = p.rows[lo + st.w.tried].p;
+        dq = p.rows[lo + st.w.tried].q;
+      } else {
+        dp = dist_of<64>(p, p.t, row, w.c, sh.tab);
+        if (drafted) dq = dist_of<64>(p, p.d, row, w.c, sh.tab);
+      }
+      if (st.state == kToken && (dp.zinv != dp.zinv || (drafted && dq.zinv != dq.zinv))) res = -1;  // no distribution
+    }
+    if (res != -2) {
+      if (writes && threadIdx.x == 0) {
+        a.out_tokens[lo + st.w.kept - 1] = res;
+        if (TREES) p.pending[b].state = kDone;
+      }
+      return false;
+    }
+    w.p = weight_side(p.t, row, dp, T, sh.tab);
+    w.q = w.p;
+    if (drafted) w.q = weight_side(p.d, row, dq, T, sh.tab);
+    rho = al * (w.p.sum / w.q.sum);
+    // tokens that were taken out of p
+    ngone = 0;
+    if (!a.draft && st.w.tried) {
+      for (int r0 = st.w.cur + 1; r0 < n; r0 += 64) {
+        const int r = r0 + lane;
+        const bool child = r < n && parent_of(a, lo, r) == st.w.cur;
+        const uint64_t m = __ballot(child);
+        const int at = ngone + __popcll(m & ((1ull << lane) - 1));
+        if (wave == 0 && child && at < kGone) s_gone[at] = a.tokens[lo + r];
+        ngone += __popcll(m);
+      }
+      __syncthreads();
+    }
+    return true;
+  };
+  if constexpr (!TREES)
+    if (!begin()) return;
   // The same loop sums blocks and, at last, looks at the block that the token is in: the code is in the
   // instruction cache then, where a copy of it took 2 us to come.
-  Found f{-1, 0.0, 0.0, 0.0, 1.0, 1.0};
-  bool alone = false;  // the other workgroups have ended
-  double pv[8], qv[8];
   for (;;) {
-    Sums s{};
+    if (TREES && walks) {
+      st.state = walk<true>(p, sh, lo, n, T, writes, st.w, held, pass > 0) ? kLeft : kToken;
+      st.w = uniform(st.w);
+      walks = false;
+      fresh = true;
+      if (alone && pass + 1 < passes) {  // the next launch goes on
+        if (threadIdx.x == 0) p.pending[b] = st;
+        return;
+      }
+    }
+    if (TREES && fresh) {
+      fresh = false;
+      if (!begin()) return;
+    }
+    Sums s{}, all{};
     for (int block = k0 + wave; block < k1; block += kVerifyThreads / 64) {
       const int i = block * kBlockElems + 8 * lane;
       s.p = s.q = 0.0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) pv[e] = qv[e] = 0.0;
       if (i < a.V) {
-        probabilities8(p.t, w.p, w.c, i, a.V, sh.tab, pv);
-        if (drafted) probabilities8(p.d, w.q, w.c, i, a.V, sh.tab, qv);
+        values8(p.t, w.p, w.c, i, a.V, sh.tab, pv);
+        if (drafted) values8(p.d, w.q, w.c, i, a.V, sh.tab, qv);
         // (more of them than LDS holds: looked for among the rows again)
-        const int g0 = ngone <= kGone ? 0 : k.cur + 1, g1 = ngone <= kGone ? ngone : n;
+        const int g0 = ngone <= kGone ? 0 : st.w.cur + 1, g1 = ngone <= kGone ? ngone : n;
         for (int g = g0; g < g1; ++g) {
-          const int x = ngone <= kGone ? s_gone[g] : parent_of(a, lo, g) == k.cur ? a.tokens[lo + g] : -1;
+          const int x = ngone <= kGone ? s_gone[g] : parent_of(a, lo, g) == st.w.cur ? a.tokens[lo + g] : -1;
 #pragma unroll
           for (int e = 0; e < 8; ++e) pv[e] = x == i + e ? 0.0 : pv[e];
         }
         if (f.at >= 0) break;
         if (drafted) {
-          s.add(pv, qv, al);
+          s.add(pv, qv, rho);
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) s.p += pv[e] < 0.0 ? 0.0 : pv[e];
         }
       }
       if (f.at >= 0) break;
+      if (TREES && st.state == kLeft) {
+        all.p += s.p;
+        all.q += s.q;
+        continue;
+      }
       const double ps = wave_sum(s.p);
       if (lane == 0) __hip_atomic_store(sums + 2 * block, ps <= kNothing ? 0.0 : ps, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       if (drafted) {
@@ -923,12 +940,17 @@ __global__ __launch_bounds__(kVerifyThreads, 4) void k_verify_pick(VerifyParams 
     }
     if (f.at >= 0) break;
     if (drafted) {
-      s.P = wave_sum(s.P);
-      s.Q = wave_sum(s.Q);
-      double* const t = totals + 2 * (share * (kVerifyThreads / 64) + wave);
-      if (lane == 0) {
-        __hip_atomic_store(t, s.P, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(t + 1, s.Q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      all = Sums{wave_sum(all.p), wave_sum(all.q), wave_sum(s.P), wave_sum(s.Q)};
+      // (a workgroup alone: the others' are nothing)
+      for (int k = alone ? wave : share * (kVerifyThreads / 64) + wave; k < ntotals; k += kVerifyThreads / 64) {
+        if (lane == 0) {
+          __hip_atomic_store(&totals[k].p, all.p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          __hip_atomic_store(&totals[k].q, all.q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          __hip_atomic_store(&totals[k].P, all.P, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          __hip_atomic_store(&totals[k].Q, all.Q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        all = Sums{};
+        if (!alone) break;
       }
     }
     // The sums are written through to where every XCD sees them, and read from there: the wave waits
@@ -937,10 +959,27 @@ __global__ __launch_bounds__(kVerifyThreads, 4) void k_verify_pick(VerifyParams 
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (!alone) {
-      if (threadIdx.x == 0) s_last = __hip_atomic_fetch_add(p.tickets + b, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (threadIdx.x == 0) s_last = __hip_atomic_fetch_add(p.tickets + pass * a.B + b, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __syncthreads();
       if (s_last != p.shares - 1) return;
-      alone = true;
+      alone = writes = true;
+      k0 = 0;
+      k1 = blocks;
+    }
+    if (TREES && st.state == kLeft) {
+      // S, by every wave for itself
+      Sums t{};
+      for (int k = lane; k < ntotals; k += 64) {
+        t.p += shared_load(&totals[k].p);
+        t.q += shared_load(&totals[k].q);
+        t.P += shared_load(&totals[k].P);
+        t.Q += shared_load(&totals[k].Q);
+      }
+      t = Sums{wave_sum(t.p), wave_sum(t.q), wave_sum(t.P), wave_sum(t.Q)};
+      const double left = (p.t.probs ? t.p : t.p / t.P) - al * (p.d.probs ? t.q : t.q / t.Q);
+      st.w.S = left < 0.0 ? 0.0 : left;
+      walks = true;
+      continue;
     }
     f = locate(sh, sums, blocks, totals, ntotals, drafted, !p.t.probs, !p.d.probs, al, u);
     if ((drafted && f.total < 1e-9) || (ngone && f.total == 0.0)) {
@@ -948,12 +987,11 @@ __global__ __launch_bounds__(kVerifyThreads, 4) void k_verify_pick(VerifyParams 
       f.at = -1;
       drafted = false;
       ngone = 0;
-      k0 = 0;
-      k1 = blocks;
       continue;
     }
+    if (TREES && threadIdx.x == 0) p.pending[b].state = kDone;
     if (f.at < 0 || !(f.total > 0.0) || f.total == __builtin_inf()) {
-      if (threadIdx.x == 0) *token = -1;
+      if (threadIdx.x == 0) a.out_tokens[lo + st.w.kept - 1] = -1;
       return;
     }
     k0 = f.at;
@@ -990,13 +1028,13 @@ __global__ __launch_bounds__(kVerifyThreads, 4) void k_verify_pick(VerifyParams 
     last = l > last ? l : last;
   }
   // (none above the goal in the block where its sum passed it: rounding; the last one there)
-  if (lane == 0) *token = hit < 0x7fffffff && f.before < __builtin_inf() ? hit : last;
+  if (lane == 0) a.out_tokens[lo + st.w.kept - 1] = hit < 0x7fffffff && f.before < __builtin_inf() ? hit : last;
 }
 
 // The workspace: statistics, then what the workgroups of a sequence share.
 struct VerifyLayout {
   int parts, part_blocks, shares, share_blocks, blocks;
-  size_t sums, totals, tickets, walked, bytes;  // offsets
+  size_t sums, totals, tickets, pending, rows, bytes;  // offsets
 };
 
 // Pieces of rows: as long as 4096 waves get one each, up to 16 blocks (a wave joins its sum over the lanes
@@ -1017,11 +1055,13 @@ VerifyLayout layout(int V, int B, int M, bool tprobs, bool drafted, bool dprobs)
   l.sums = at;
   at += static_cast<size_t>(B) * l.blocks * 2 * sizeof(double);
   l.totals = at;
-  at += static_cast<size_t>(B) * l.shares * (kVerifyThreads / 64) * 2 * sizeof(double);
-  l.walked = at;
-  at += static_cast<size_t>(B) * sizeof(Walked);
+  at += static_cast<size_t>(B) * l.shares * (kVerifyThreads / 64) * sizeof(Sums);
+  l.pending = at;
+  at += static_cast<size_t>(B) * sizeof(Pending);
+  l.rows = at;
+  at += drafted ? static_cast<size_t>(M) * sizeof(RowInfo) : 0;
   l.tickets = at;
-  at += static_cast<size_t>(B) * sizeof(int);
+  at += static_cast<size_t>(B) * kPasses * sizeof(int);
   l.bytes = M > 0 && B > 0 ? at : 0;
   return l;
 }
@@ -1043,9 +1083,10 @@ hipError_t launch_verify(const VerifyArgs& a, hipStream_t s) {
              stat + static_cast<size_t>(a.M) * l.parts};
   p.parts = l.parts; p.part_blocks = l.part_blocks; p.shares = l.shares; p.share_blocks = l.share_blocks;
   p.sums = reinterpret_cast<double*>(ws + l.sums);
-  p.totals = reinterpret_cast<double*>(ws + l.totals);
+  p.totals = reinterpret_cast<Sums*>(ws + l.totals);
   p.tickets = reinterpret_cast<int*>(ws + l.tickets);
-  p.walked = reinterpret_cast<Walked*>(ws + l.walked);
+  p.pending = reinterpret_cast<Pending*>(ws + l.pending);
+  p.rows = reinterpret_cast<RowInfo*>(ws + l.rows);
   if (a.M > 0) {
     // (rows of probabilities have statistics only where they may be greedy)
     const int first = a.tprobs && !a.temperature ? a.M : 0, end = a.draft && !a.dprobs ? 2 * a.M : a.M;
@@ -1055,12 +1096,14 @@ hipError_t launch_verify(const VerifyArgs& a, hipStream_t s) {
     hipLaunchKernelGGL(k_verify_stats, dim3(static_cast<uint32_t>(blocks)), dim3(kVerifyThreads), 0, s, p, u0, u1);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  if (a.M > 0 && a.draft && a.parents) {
-    hipLaunchKernelGGL(k_verify_walk, dim3(a.B), dim3(kWalkThreads), 0, s, p);
+  const dim3 grid(a.B * l.shares);
+  if (a.M == 0 || !a.draft || !a.parents) {
+    hipLaunchKernelGGL(k_verify_pick<false>, grid, dim3(kVerifyThreads), 0, s, p, 0, 1);
+    return hipGetLastError();
+  }
+  for (int pass = 0; pass < kPasses; ++pass) {
+    hipLaunchKernelGGL(k_verify_pick<true>, grid, dim3(kVerifyThreads), 0, s, p, pass, kPasses);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_verify_pick<true>, dim3(a.B * l.shares), dim3(kVerifyThreads), 0, s, p);
-  } else {
-    hipLaunchKernelGGL(k_verify_pick<false>, dim3(a.B * l.shares), dim3(kVerifyThreads), 0, s, p);
   }
   return hipGetLastError();
 }
