@@ -33,6 +33,7 @@ constexpr int kBlockElems = 512;    // a wave's step: 8 elements a lane
 constexpr int kWindow = 256;        // rows whose probabilities are in LDS at a time
 constexpr int kGone = 256;          // tried tokens in LDS
 constexpr int kTable = 256;         // 2^(i / 256)
+constexpr int kPieces = 64;         // pieces of a row that 16 lanes hold at once
 constexpr int kPasses = 4;          // launches of k_verify_pick for trees with a draft
 
 // Of a piece of a row, in units of the largest value: z = sum 2^((x - top) c), c = log2(e) / T. Where
@@ -419,7 +420,7 @@ template <int LANES>
 __device__ __forceinline__ Dist dist_of(const VerifyParams& p, const Side& s, int row, double c, const double* tab) {
   Dist d{0.0, 1.0};
   if (s.probs) return d;
-  constexpr int HELD = 4;
+  constexpr int HELD = kPieces / 16;
   const StatPart* st = s.stat + static_cast<int64_t>(row) * p.parts;
   const int l = threadIdx.x & (LANES - 1);
   const float inf = __builtin_inff();
@@ -487,7 +488,7 @@ struct WeightSide {
   const char* row;
   Dist d;
   Exp2Near e;
-  double sum;  // P by k_verify_stats (probabilities: 1)
+  double inv;  // 1 / P by k_verify_stats (probabilities: 1)
 };
 struct Weights {
   WeightSide p, q;
@@ -510,7 +511,7 @@ __device__ __forceinline__ WeightSide weight_side(const Side& s, int row, const 
   w.row = s.data + row * s.stride;
   w.d = Dist{uniform(d.ref), uniform(d.zinv)};
   w.e = exp2_near(w.d.ref, c, reach_of(T));
-  w.sum = uniform(s.probs ? 1.0 : 1.0 / (w.e.ok ? d.zinv * add_exp2(w.e.base - d.ref * c, 0.0, tab) : d.zinv));
+  w.inv = uniform(s.probs ? 1.0 : w.e.ok ? d.zinv * add_exp2(w.e.base - d.ref * c, 0.0, tab) : d.zinv);
   w.e.c = uniform(c);
   w.e.base = uniform(w.e.base);
   w.e.magic = uniform(w.e.magic);
@@ -866,7 +867,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 3 : 4) void k_verify_pick(V
     w.p = weight_side(p.t, row, dp, T, sh.tab);
     w.q = w.p;
     if (drafted) w.q = weight_side(p.d, row, dq, T, sh.tab);
-    rho = al * (w.p.sum / w.q.sum);
+    rho = al * (w.q.inv / w.p.inv);
     // tokens that were taken out of p
     ngone = 0;
     if (!a.draft && st.w.tried) {
@@ -1038,15 +1039,17 @@ struct VerifyLayout {
 };
 
 // Pieces of rows: as long as 4096 waves get one each, up to 16 blocks (a wave joins its sum over the lanes
-// once per piece); workgroups of a sequence: 1024 in all, with a block for each wave at least.
+// once per piece), and of no more than kPieces to a row, which 16 lanes join without a loop (256 of them took
+// the walk of 8 rows 17 us instead of 4); workgroups of a sequence: 1024 in all, with a block for each wave at least.
 VerifyLayout layout(int V, int B, int M, bool tprobs, bool drafted, bool dprobs) {
   VerifyLayout l{};
   l.blocks = (V + kBlockElems - 1) / kBlockElems;
   const bool drows = drafted && !dprobs;
   const int64_t rows = static_cast<int64_t>(M) * ((tprobs ? 0 : 1) + (drows ? 1 : 0));
+  const auto pieces = [&](int part_blocks) { return (l.blocks + part_blocks - 1) / part_blocks; };
   l.part_blocks = 16;
-  while (l.part_blocks > 1 && rows * ((l.blocks + l.part_blocks - 1) / l.part_blocks) < 4096) l.part_blocks >>= 1;
-  l.parts = (l.blocks + l.part_blocks - 1) / l.part_blocks;
+  while (l.part_blocks > 1 && rows * pieces(l.part_blocks) < 4096 && pieces(l.part_blocks / 2) <= kPieces) l.part_blocks /= 2;
+  l.parts = pieces(l.part_blocks);
   int shares = B > 0 ? (1024 + B - 1) / B : 1;
   if (shares > (l.blocks + 3) / 4) shares = (l.blocks + 3) / 4;
   l.share_blocks = (l.blocks + shares - 1) / shares;
