@@ -20,8 +20,8 @@
 // workgroup walks on with it, and the next launch of k_verify_pick sums what the walk needs then. Two more
 // launches follow, in which sequences that are done end at once; what is still open in the last one
 // its last workgroup sums alone (three siblings turned away on one way; two to three in a hundred walks).
-#include "device_common.hpp"
 #include "internal.hpp"
+#include "kv_lane.hpp"
 
 namespace tq {
 namespace {
@@ -229,15 +229,46 @@ __device__ __forceinline__ double temperature_of(const VerifyArgs& a, int b) { r
 __device__ __forceinline__ double scale_of(double T) { return 1.4426950408889634074 / T; }
 __device__ __forceinline__ double reach_of(double T) { return 693.14718055994530942 * T; }  // 1000 / scale
 
+// Over rows of 16 lanes and over the wave, in every lane, by lane moves that need no LDS (kv_lane.hpp); NaN
+// where any is.
+__device__ __forceinline__ float row_max(float x) {
+  x = __builtin_elementwise_maximum(x, kv_swap<0>(x));
+  x = __builtin_elementwise_maximum(x, kv_swap<1>(x));
+  x = __builtin_elementwise_maximum(x, kv_swap<2>(x));
+  return __builtin_elementwise_maximum(x, kv_swap<3>(x));
+}
 __device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-  for (int s = 32; s; s >>= 1) x = __builtin_elementwise_maximum(x, __shfl_xor(x, s));
-  return x;
+  float a, b;
+  kv_both<4>(row_max(x), a, b);
+  kv_both<5>(__builtin_elementwise_maximum(a, b), a, b);
+  return __builtin_elementwise_maximum(a, b);
+}
+__device__ __forceinline__ double row_sum(double x) {
+  x += kv_swap<0>(x);
+  x += kv_swap<1>(x);
+  x += kv_swap<2>(x);
+  return x + kv_swap<3>(x);
 }
 __device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-  for (int s = 32; s; s >>= 1) x += __shfl_xor(x, s);
-  return x;
+  double a, b;
+  kv_both<4>(row_sum(x), a, b);
+  kv_both<5>(a + b, a, b);
+  return a + b;
+}
+// x and all before it, over the wave: within rows of 16 by shifts, then the rows before by broadcasts.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double scan_step(double x) {
+  const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(x), CTRL, ROWS, 0xf, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(x), CTRL, ROWS, 0xf, false);
+  return x + __hiloint2double(hi, lo);
+}
+__device__ __forceinline__ double wave_scan(double x) {
+  x = scan_step<0x111, 0xf>(x);  // row_shr:1, 2, 4, 8
+  x = scan_step<0x112, 0xf>(x);
+  x = scan_step<0x114, 0xf>(x);
+  x = scan_step<0x118, 0xf>(x);
+  x = scan_step<0x142, 0xa>(x);  // lane 15 of rows 0 and 2 to rows 1 and 3
+  return scan_step<0x143, 0xc>(x);  // lane 31 to rows 2 and 3
 }
 
 // The largest b with offsets[b] <= row, by all lanes of a wave.
@@ -420,6 +451,7 @@ template <int LANES>
 __device__ __forceinline__ Dist dist_of(const VerifyParams& p, const Side& s, int row, double c, const double* tab) {
   Dist d{0.0, 1.0};
   if (s.probs) return d;
+  static_assert(LANES == 16 || LANES == 64, "rows of lanes, or the wave");
   constexpr int HELD = kPieces / 16;
   const StatPart* st = s.stat + static_cast<int64_t>(row) * p.parts;
   const int l = threadIdx.x & (LANES - 1);
@@ -434,8 +466,7 @@ __device__ __forceinline__ Dist dist_of(const VerifyParams& p, const Side& s, in
 #pragma unroll
   for (int k = 0; k < HELD; ++k) top = __builtin_elementwise_maximum(top, held[k].top);
   for (int k = l + HELD * LANES; k < p.parts; k += LANES) top = __builtin_elementwise_maximum(top, st[k].top);
-#pragma unroll
-  for (int m = LANES >> 1; m; m >>= 1) top = __builtin_elementwise_maximum(top, __shfl_xor(top, m));
+  top = LANES == 16 ? row_max(top) : wave_max(top);
   double z = 0.0;
 #pragma unroll
   for (int k = 0; k < HELD; ++k) {
@@ -446,8 +477,7 @@ __device__ __forceinline__ Dist dist_of(const VerifyParams& p, const Side& s, in
     const StatPart q = st[k];
     if (q.z != 0.0) z += q.z * add_exp2((static_cast<double>(q.top) - top) * c, 0.0, tab);
   }
-#pragma unroll
-  for (int m = LANES >> 1; m; m >>= 1) z += __shfl_xor(z, m);
+  z = LANES == 16 ? row_sum(z) : wave_sum(z);
   d.ref = top;
   d.zinv = z > 0.0 && z < __builtin_inf() ? 1.0 / z : __builtin_nan("");
   return d;
@@ -693,18 +723,10 @@ __device__ __forceinline__ Found locate(WalkShared& sh, const double* sums, int 
     s.p += shared_load(sums + 2 * k);
     if (drafted) s.q += shared_load(sums + 2 * k + 1);
   }
-  double ip = s.p, iq = s.q;
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const double o = __shfl_up(ip, m);
-    if (lane >= m) ip += o;
-  }
+  const double ip = wave_scan(s.p);
+  double iq = 0.0;
   if (drafted) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const double o = __shfl_up(iq, m);
-      if (lane >= m) iq += o;
-    }
+    iq = wave_scan(s.q);
     s.P = wave_sum(s.P);
     s.Q = wave_sum(s.Q);
   }
@@ -789,19 +811,22 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 3 : 4) void k_verify_pick(V
   const int b = blockIdx.x / p.shares, share = blockIdx.x - b * p.shares;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   bool writes = share == 0;  // this workgroup writes outputs
-  int lo, hi;
-  seq_rows(a, b, lo, hi);
-  const int n = hi - lo;
-  if (n == 0) {
-    if (writes && threadIdx.x == 0) a.kept[b] = 0;
-    return;
-  }
   Pending st;
   if (TREES && pass) {
     st = p.pending[b];
     if (st.state == kDone) return;
   }
-  fill_table(sh.tab);
+  int lo, hi;
+  seq_rows(a, b, lo, hi);
+  fill_table(sh.tab);  // (while the bounds are on their way)
+  const int n = hi - lo;
+  if (n == 0) {
+    if (writes && threadIdx.x == 0) {
+      a.kept[b] = 0;
+      if (TREES) p.pending[b].state = kDone;
+    }
+    return;
+  }
   const double T = uniform(temperature_of(a, b)), u = uniform(a.uniforms[lo]);
   int held = -1;
   if (!TREES || !pass) st.w = Walk{0.0, 1.0, 0, 1, 0, 1};
@@ -1009,13 +1034,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 3 : 4) void k_verify_pick(V
     own += pv[e];
     if (pv[e] > 0.0) last = i + e;
   }
-  double incl = own;
-#pragma unroll
-  for (int s = 1; s < 64; s <<= 1) {
-    const double o = __shfl_up(incl, s);
-    if (lane >= s) incl += o;
-  }
-  double run = f.before + (incl - own);
+  double run = f.before + (wave_scan(own) - own);
   int hit = 0x7fffffff;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
