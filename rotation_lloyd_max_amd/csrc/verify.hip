@@ -76,6 +76,7 @@ struct Walk {
   double al, S;
   int cur, kept, tried;  // tried: the last child of cur that went (0: none)
   int next;              // the first row that it has not looked at
+  int known;             // the rows before it are in VerifyParams::rows (trees with a draft)
 };
 // What the walk needs of a row.
 struct Dist {  // probabilities of a row of logits: 2^((x - ref) c) zinv; zinv NaN: the row is no distribution
@@ -532,7 +533,7 @@ __device__ __forceinline__ double uniform(double x) {
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ Walk uniform(const Walk& w) {
-  return Walk{uniform(w.al), uniform(w.S), uniform(w.cur), uniform(w.kept), uniform(w.tried), uniform(w.next)};
+  return Walk{uniform(w.al), uniform(w.S), uniform(w.cur), uniform(w.kept), uniform(w.tried), uniform(w.next), uniform(w.known)};
 }
 
 __device__ __forceinline__ WeightSide weight_side(const Side& s, int row, const Dist& d, double T, const double* tab) {
@@ -640,8 +641,9 @@ __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int 
     const int w0 = w.next / kWindow * kWindow, w1 = n - w0 < kWindow ? n : w0 + kWindow;
     if (held != w0) {
       if (held >= 0) __syncthreads();
-      fill_window(p, sh, lo, w0, w1, T, TREES && (later || writes) ? p.rows : nullptr, TREES && later);
+      fill_window(p, sh, lo, w0, w1, T, TREES && (later || writes) ? p.rows : nullptr, TREES && later && w0 < w.known);
       held = w0;
+      if (w.known < w1) w.known = w1;
     }
     // the next child of cur in the window
     int r = w1;
@@ -672,7 +674,7 @@ __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int 
         a.out_tokens[lo + w.kept - 1] = x;
         a.path[lo + w.kept] = r;
       }
-      w = Walk{0.0, 1.0, r, w.kept + 1, 0, r + 1};
+      w = Walk{0.0, 1.0, r, w.kept + 1, 0, r + 1, w.known};
       if (greedy) largest = largest_of(p, lo + r);
     } else {
       w.tried = r;
@@ -829,7 +831,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 3 : 4) void k_verify_pick(V
   }
   const double T = uniform(temperature_of(a, b)), u = uniform(a.uniforms[lo]);
   int held = -1;
-  if (!TREES || !pass) st.w = Walk{0.0, 1.0, 0, 1, 0, 1};
+  if (!TREES || !pass) st.w = Walk{0.0, 1.0, 0, 1, 0, 1, 0};
   if constexpr (!TREES) {
     walk<false>(p, sh, lo, n, T, writes, st.w, held, false);
     st.w = uniform(st.w);

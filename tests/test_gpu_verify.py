@@ -338,3 +338,60 @@ def test_frequencies_follow_the_target():
                         parents=None if parents is None else torch.from_numpy(parents).cuda())
         first = np.bincount(got.tokens.view(n, rows)[:, 0].cpu().numpy(), minlength=V)
         assert np.all(np.abs(first - n * p) <= 5 * np.sqrt(n * p * (1 - p)) + 1)
+
+
+@pytest.mark.parametrize("ddt", ["fp32", None])
+def test_broad_trees_of_many_rows(ddt):
+    # three children to a row, 700 rows: accepted rows beyond the first 256, siblings turned away on the way there
+    c = case(34, 16, 700, 60, "fp32", ddt, ragged=False, noise=0.5, spread=1.5 if ddt else 5.0)
+    n = 700
+    up = np.concatenate([[0], (np.arange(1, n) - 1) // 3])
+    c["parents"] = np.tile(up, 16)
+    g = np.random.default_rng(35)
+    src = as_f64(c["target"] if ddt is None else c["draft"])
+    for r in range(16 * n):
+        if r % n:
+            c["tokens"][r] = np.argmax(src[r - r % n + up[r % n]] + g.gumbel(size=60))
+    if ddt is None:
+        c["uniforms"] *= 0.5           # (point masses stay as often as their probability says)
+    got = check(c)
+    path = got.path.view(16, n).cpu().numpy()
+    assert (path.max(1) >= 256).sum() >= 4
+    later = [(path[b, i] - 1) % 3 for b in range(16) for i in range(1, got.kept[b].item())]
+    assert any(later), "no sibling was turned away"
+
+
+@pytest.mark.parametrize("ddt", ["fp32", "bf16", None])
+def test_many_children_of_one_row(ddt):
+    # all rows are the root's children, more than LDS holds, some tokens twice; nearly all are turned away
+    for n, V in ((13, 500), (300, 5000), (700, 20001)):
+        c = case(36, 6, n, V, "fp32", ddt, ragged=False, noise=2.0, spread=1.0)
+        c["parents"] = np.zeros(6 * n, np.int64)
+        g = np.random.default_rng([37, n])
+        src = as_f64(c["target"] if ddt is None else c["draft"])
+        for r in range(6 * n):
+            c["tokens"][r] = np.argmax(src[r - r % n] + g.gumbel(size=V))
+        if ddt is not None:     # the first eight are tokens that the draft likes far more than the target
+            for b in range(6):
+                c["tokens"][b * n + 1:b * n + 9] = np.argsort(as_f64(c["target"])[b * n] - src[b * n])[:8]
+        c["tokens"][3::n] = c["tokens"][2::n]
+        c["uniforms"] = (1.0 - c["uniforms"] * (1e-3 if ddt is None else 0.03)).astype(np.float32)
+        check(c)
+
+
+@pytest.mark.parametrize("T", [1e-44, 1e-6, 1e38, float("inf")])
+def test_siblings_at_extreme_temperatures(T):
+    for tdt in ("fp32", "bf16"):
+        c = case(38, 6, 9, 777, tdt, tdt, tree=True, temperature=np.full(6, T, np.float32), noise=1.0, ragged=False)
+        c["parents"][:] = np.tile([0, 0, 0, 0, 1, 1, 2, 2, 2], 6)
+        check(c)
+        c["target"][:, 5:500] = -np.inf
+        check(c)
+
+
+@pytest.mark.parametrize("tree,ddt", [(False, "bf16"), (True, "fp32"), (True, None)])
+def test_more_pieces_of_a_row_than_lanes_hold(tree, ddt):
+    # above 64 pieces of 8192 tokens
+    for kind in ("logits", "probabilities"):
+        check(case(39, 2, 4, 600001, "fp32", ddt, kind, tree, ragged=False, noise=1.5))
+    check(case(40, 2, 3, 1100000, "bf16", ddt, "logits", tree, ragged=False, temperature=np.array([0.0, 0.9], np.float32)))
