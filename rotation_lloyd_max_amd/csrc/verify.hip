@@ -295,7 +295,8 @@ __device__ __forceinline__ void seq_rows(const VerifyArgs& a, int b, int& lo, in
 
 // ---- statistics of the rows ---------------------------------------------------------------
 
-// Elements [i0, i1) of a row by a wave: fp32 exponentials, eight at a time summed in fp32, then fp64.
+// Elements [i0, i1) of a row by a wave: fp32 exponentials, eight at a time summed in fp32, then fp64. Relative to a
+// value of the piece, not to its largest: that one need not be looked for.
 template <int DT>
 __device__ __forceinline__ StatPart stat_piece(const char* row, int V, int i0, int i1, double T) {
   const int lane = threadIdx.x & 63;
@@ -303,45 +304,69 @@ __device__ __forceinline__ StatPart stat_piece(const char* row, int V, int i0, i
   const bool usual = c > 1e-30f && c < 1e30f;
   float f[8], top = -inf, ref = 0.f;
   double s = 0.0;
-  auto load = [&](int i) TQ_INLINE {
+  auto load = [&](int i, float (&f)[8]) TQ_INLINE {
     if (i + 8 <= V) load8<DT>(row, i, f);
     else load8_end<DT>(row, i, V, -inf, f);
+  };
+  auto most = [&](const float (&f)[8]) TQ_INLINE {
     float m = __builtin_elementwise_maximum(f[0], f[1]);
 #pragma unroll
     for (int k = 2; k < 8; k += 2) m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, f[k]), f[k + 1]);
     return m;
   };
-  auto sum8 = [&]() TQ_INLINE {
-    float e[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) e[k] = __builtin_amdgcn_exp2f((f[k] - ref) * c);
-    return ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-  };
+  auto sum8 = [&](const float (&e)[8]) TQ_INLINE { return ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7])); };
   const int first = i0 + 8 * lane;
   bool done = first >= i1;
   if (usual && !done) {
-    // relative to the lane's first eight values, which may turn out to be far below the others
-    const float m = load(first);
-    ref = __builtin_fabsf(m) < inf ? m : 0.f;
-    for (int i = first; i < i1; i += kBlockElems) {
-      top = __builtin_elementwise_maximum(top, load(i));
-      s += sum8();
+    // relative to the lane's first eight values: x c - base is rounded once, so base may be any value near ref c
+    load(first, f);
+    const float m = most(f);
+    const bool near = __builtin_fabsf(m) * c < 0x1p24f;
+    top = near ? m : 0.f;
+    const float base = top * c;
+    auto sum_near = [&](const float (&f)[8]) TQ_INLINE {
+      float e[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) e[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(f[k], c, -base));
+      return sum8(e);
+    };
+    s = sum_near(f);
+    int i = first + kBlockElems;
+    constexpr int U = 2;
+    for (; i + (U - 1) * kBlockElems + 8 <= i1; i += U * kBlockElems) {
+      float g[U][8];
+#pragma unroll
+      for (int u = 0; u < U; ++u) load8<DT>(row, i + u * kBlockElems, g[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) s += sum_near(g[u]);
     }
-    done = (top - ref) * c < 100.f && s > 0x1p-100;
+    for (; i < i1; i += kBlockElems) {
+      load(i, f);
+      s += sum_near(f);
+    }
+    done = s > 0x1p-100 && s < 0x1p100;
+    // (in units of 2^base: of `top`)
+    if (done) s *= exp2(static_cast<double>(base) - static_cast<double>(top) * c);
+    ref = top;
   }
   if (!done) {
-    // ... or far above them, or none is finite, or the temperature is extreme: relative to the largest
+    // ... or far above them or below, or none is finite, or the temperature is extreme: relative to the largest
     top = -inf;
-    for (int i = first; i < i1; i += kBlockElems) top = __builtin_elementwise_maximum(top, load(i));
+    for (int i = first; i < i1; i += kBlockElems) {
+      load(i, f);
+      top = __builtin_elementwise_maximum(top, most(f));
+    }
     ref = top;
     s = 0.0;
     if (top != top || top == inf) {
       s = __builtin_nan("");
     } else if (top > -inf) {
       for (int i = first; i < i1; i += kBlockElems) {
-        load(i);
+        load(i, f);
         if (usual) {
-          s += sum8();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = __builtin_amdgcn_exp2f((f[k] - ref) * c);
+          s += sum8(f);
         } else {
 #pragma unroll 1
           for (int k = 0; k < 8; ++k) {
@@ -513,6 +538,8 @@ __device__ __forceinline__ int largest_of(const VerifyParams& p, int row) {
 
 // Weights up to here count as nothing: masked tokens come out as about 2^-1000, not 0.
 constexpr double kNothing = 1e-280;
+// So much left of p, or less, is nothing: the roundings of fp64 sums of 10^5 terms are below a tenth of it.
+constexpr double kLittle = 1e-9;
 
 // One side of what the new token is drawn from (or S is summed over): values p~ of Sums.
 struct WeightSide {
@@ -664,7 +691,7 @@ __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int 
     if (greedy) {
       yes = x == largest;
     } else if (drafted) {
-      yes = u * w.S * qx < px - w.al * qx;
+      yes = w.S > 0.0 && u * w.S * qx < px - w.al * qx;  // (nothing left: the difference is rounding)
     } else {
       taken = w.tried && tried_before(a, sh, lo, n, w.cur, r, x);
       yes = u * w.S < (taken ? 0.0 : px);
@@ -1005,12 +1032,12 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 3 : 4) void k_verify_pick(V
       }
       t = Sums{wave_sum(t.p), wave_sum(t.q), wave_sum(t.P), wave_sum(t.Q)};
       const double left = (p.t.probs ? t.p : t.p / t.P) - al * (p.d.probs ? t.q : t.q / t.Q);
-      st.w.S = left < 0.0 ? 0.0 : left;
+      st.w.S = left < kLittle ? 0.0 : left;
       walks = true;
       continue;
     }
     f = locate(sh, sums, blocks, totals, ntotals, drafted, !p.t.probs, !p.d.probs, al, u);
-    if ((drafted && f.total < 1e-9) || (ngone && f.total == 0.0)) {
+    if ((drafted && f.total < kLittle) || (ngone && f.total == 0.0)) {
       // nothing is left, or no more than the rounding of the rows' sums: p itself, by this workgroup
       f.at = -1;
       drafted = false;
