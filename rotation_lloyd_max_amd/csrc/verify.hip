@@ -17,9 +17,16 @@
 // looked at, a wave per piece of a row. k_verify_pick: each workgroup of a sequence joins the pieces and walks
 // (all do the same: cheaper than another launch), sums w over its share of the vocabulary, and the one that
 // comes last finds the token. Where siblings are tried against a draft, S is such a sum too: the last
-// workgroup walks on with it, and the next launch of k_verify_pick sums what the walk needs then. Two more
-// launches follow, in which sequences that are done end at once; what is still open in the last one
-// its last workgroup sums alone (three siblings turned away on one way; two to three in a hundred walks).
+// workgroup walks on with it, and the next launch of k_verify_pick sums what the walk needs then. kPasses - 1 more
+// launches follow, in which sequences that are done end at once; what is still open in the last one its last
+// workgroup sums alone (20 rows of 8 sequences, 60000 tokens: 105 us when the first launch's did so, 57 now).
+//
+// Bounds and figures. 64 sequences of 9 rows, 131072 tokens in bf16, a draft: k_verify_stats reads 285 MB in 54 us,
+// 5.3 TB/s, bound by memory; k_verify_pick, 34 us, reads 64 of these rows again: 6 us for the walk (12 where nine
+// rows stay), 11 for the sums (fp64 operations at 4.7 cycles a wave are 7 of them), 5 for the meeting and the
+// last block; the rest is the slowest sequence. One sequence of 4 rows, 32000 tokens: 4 + 14 us, the latency of
+// some ten loads that wait for each other (1500 cycles each: another launch wrote them, or nobody read them yet)
+// and of fp64 chains in waves that have a SIMD to themselves.
 #include "internal.hpp"
 #include "kv_lane.hpp"
 
@@ -36,8 +43,8 @@ constexpr int kTable = 256;         // 2^(i / 256)
 constexpr int kPieces = 64;         // pieces of a row that 16 lanes hold at once
 constexpr int kPasses = 4;          // launches of k_verify_pick for trees with a draft
 
-// Of a piece of a row, in units of the largest value: z = sum 2^((x - top) c), c = log2(e) / T. Where
-// it holds NaN or +infinity z is NaN. at: the index of its first largest value (greedy rows).
+// Of a piece of a row: z = sum 2^((x - top) c), c = log2(e) / T, top a value with x - top below 100 / c for every
+// x. Where it holds NaN or +infinity z is NaN. Greedy rows: top the largest value, at its first index.
 struct StatPart {
   double z;
   float top;
@@ -139,36 +146,55 @@ __device__ __forceinline__ void load8_end(const char* row, int i, int V, float n
 #pragma unroll
   for (int k = 0; k < 8; ++k) f[k] = i + k < V ? load_elem<DT>(row, i + k) : none;
 }
-// The same for a type known at run time; one piece of code for all types and ends.
-__device__ __forceinline__ void load8_any(const char* row, int dt, int i, int V, float none, float (&f)[8]) {
+// The same for a type known at run time; one piece of code for all types and ends. The loads, and the values.
+struct Raw8 {
   uint32_t x[8];
+};
+__device__ __forceinline__ Raw8 load8_any(const char* row, int dt, int i, int V) {
+  Raw8 r;
   if (dt == 0 && i + 8 <= V) {
     const u32x4_a2 a = *reinterpret_cast<const u32x4_a2*>(row + static_cast<int64_t>(i) * 4);
     const u32x4_a2 b = *reinterpret_cast<const u32x4_a2*>(row + static_cast<int64_t>(i) * 4 + 16);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      x[k] = a[k];
-      x[4 + k] = b[k];
+      r.x[k] = a[k];
+      r.x[4 + k] = b[k];
     }
   } else if (dt == 0) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = reinterpret_cast<const uint32_t*>(row)[i + k < V ? i + k : V - 1];
+    for (int k = 0; k < 8; ++k) r.x[k] = reinterpret_cast<const uint32_t*>(row)[i + k < V ? i + k : V - 1];
   } else if (i + 8 <= V) {
     const u32x4_a2 a = *reinterpret_cast<const u32x4_a2*>(row + static_cast<int64_t>(i) * 2);
 #pragma unroll
+    for (int k = 0; k < 4; ++k) r.x[k] = a[k];
+  } else {
+#pragma unroll
     for (int k = 0; k < 4; ++k) {
-      x[2 * k] = a[k] & 0xffffu;
-      x[2 * k + 1] = a[k] >> 16;
+      const uint16_t* const h = reinterpret_cast<const uint16_t*>(row);
+      r.x[k] = h[i + 2 * k < V ? i + 2 * k : V - 1] | static_cast<uint32_t>(h[i + 2 * k + 1 < V ? i + 2 * k + 1 : V - 1]) << 16;
+    }
+  }
+  return r;
+}
+__device__ __forceinline__ void values_any(const Raw8& r, int dt, int i, int V, float none, float (&f)[8]) {
+  if (dt == 0) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(r.x[k]);
+  } else if (dt == 1) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[2 * k] = __uint_as_float(r.x[k] << 16);
+      f[2 * k + 1] = __uint_as_float(r.x[k] & 0xffff0000u);
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = reinterpret_cast<const uint16_t*>(row)[i + k < V ? i + k : V - 1];
+    for (int k = 0; k < 4; ++k) {
+      f[2 * k] = half_bits_to_float(static_cast<uint16_t>(r.x[k] & 0xffffu));
+      f[2 * k + 1] = half_bits_to_float(static_cast<uint16_t>(r.x[k] >> 16));
+    }
   }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    f[k] = dt == 0 ? __uint_as_float(x[k]) : dt == 1 ? __uint_as_float(x[k] << 16) : half_bits_to_float(static_cast<uint16_t>(x[k]));
-    f[k] = i + k < V ? f[k] : none;
-  }
+  for (int k = 0; k < 8; ++k) f[k] = i + k < V ? f[k] : none;
 }
 
 // 2^(i / 256), the upper word less i << 12: adding j << 12 for any j = 256 k + i leaves 2^(j / 256).
@@ -203,8 +229,8 @@ __device__ __forceinline__ double add_exp2(double t, double s, const double* tab
 
 // 2^((x - ref) c) for many x: with ref c rounded to steps of 1 / 256 (a factor that every x has alike), x c
 // is rounded and its step counted from ref in one fused operation. x is held above `cut`, where the
-// result is about 2^-1000 (NaN stays NaN, and its result is anything). Not `ok`: a scale or a reference for which single precision cannot place the cut
-// (temperatures below 1e-7 or above 1e35 or so).
+// result is about 2^-1000 (NaN stays NaN, and its result is anything). Not `ok`: a scale or a reference for
+// which single precision cannot place the cut (temperatures below 1e-7 or above 1e35 or so).
 struct Exp2Near {
   double c, magic, base;  // magic = 1.5 2^44 - base; base: ref c, rounded
   float cut;
@@ -295,8 +321,10 @@ __device__ __forceinline__ void seq_rows(const VerifyArgs& a, int b, int& lo, in
 
 // ---- statistics of the rows ---------------------------------------------------------------
 
-// Elements [i0, i1) of a row by a wave: fp32 exponentials, eight at a time summed in fp32, then fp64. Relative to a
-// value of the piece, not to its largest: that one need not be looked for.
+// Elements [i0, i1) of a row by a wave: fp32 exponentials (a step off in 2^23, a test compares numbers that are
+// off by 1e-6 then), eight at a time summed in fp32, then fp64. Relative to a value of the piece, not to
+// its largest: that one need not be looked for. Two loads at a time: 54 us for 285 MB; one 56, four 55; with
+// the largest value and (x - ref) c in three roundings 60.
 template <int DT>
 __device__ __forceinline__ StatPart stat_piece(const char* row, int V, int i0, int i1, double T) {
   const int lane = threadIdx.x & 63;
@@ -578,10 +606,10 @@ __device__ __forceinline__ WeightSide weight_side(const Side& s, int row, const 
   return w;
 }
 
-__device__ __forceinline__ void values8(const Side& s, const WeightSide& w, double c, int i, int V, const double* tab,
+__device__ __forceinline__ void values8(const Side& s, const WeightSide& w, const Raw8& raw, double c, int i, int V, const double* tab,
                                                double (&v)[8]) {
   float f[8];
-  load8_any(w.row, s.dt, i, V, s.probs ? 0.f : -__builtin_inff(), f);
+  values_any(raw, s.dt, i, V, s.probs ? 0.f : -__builtin_inff(), f);
   if (s.probs) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = f[k];
@@ -742,13 +770,20 @@ __device__ __forceinline__ Found locate(WalkShared& sh, const double* sums, int 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int each = (blocks + NT - 1) / NT;
   const int k0 = static_cast<int>(threadIdx.x) * each < blocks ? threadIdx.x * each : blocks, k1 = k0 + each < blocks ? k0 + each : blocks;
+  // (all first loads before any wait; a thread with one block does not read it again)
   Sums s{};
-  if (drafted)
-    for (int k = threadIdx.x; k < ntotals; k += NT) {
+  if (k0 < k1) s.p = shared_load(sums + 2 * k0);
+  if (drafted) {
+    const int t = threadIdx.x;
+    if (k0 < k1) s.q = shared_load(sums + 2 * k0 + 1);
+    if (t < ntotals) s.P = shared_load(&totals[t].P);
+    if (t < ntotals) s.Q = shared_load(&totals[t].Q);
+    for (int k = t + NT; k < ntotals; k += NT) {
       s.P += shared_load(&totals[k].P);
       s.Q += shared_load(&totals[k].Q);
     }
-  for (int k = k0; k < k1; ++k) {
+  }
+  for (int k = k0 + 1; k < k1; ++k) {
     s.p += shared_load(sums + 2 * k);
     if (drafted) s.q += shared_load(sums + 2 * k + 1);
   }
@@ -783,7 +818,7 @@ __device__ __forceinline__ Found locate(WalkShared& sh, const double* sums, int 
   f.goal = (u > 0.0 ? u : 0.0) * f.total;
   // a block's own weight; rounding may leave a block of nothing a little
   auto block = [&](int k) TQ_INLINE {
-    const double x = weight(shared_load(sums + 2 * k), drafted ? shared_load(sums + 2 * k + 1) : 0.0);
+    const double x = each == 1 ? weight(s.p, s.q) : weight(shared_load(sums + 2 * k), drafted ? shared_load(sums + 2 * k + 1) : 0.0);
     return x <= kNothing ? 0.0 : x;
   };
   const uint64_t m = __ballot(weight(left.p + ip, left.q + iq) > f.goal);
@@ -831,9 +866,10 @@ __device__ __forceinline__ Found locate(WalkShared& sh, const double* sums, int 
 }
 
 // The workgroups of a sequence (`shares` of them) sum w over their blocks; the last finds the token, or walks on.
-// TREES: siblings against a draft, several launches (as a branch at run time it spilled registers).
+// TREES: siblings against a draft, several launches; as a branch at run time it spilled registers, at three
+// waves a SIMD it does (205 registers wanted: 8 sequences of 20 rows 61 us against 57 a call, 48 of 12 rows 74 either way).
 template <bool TREES>
-__global__ __launch_bounds__(kVerifyThreads, TREES ? 3 : 4) void k_verify_pick(VerifyParams p, int pass, int passes) {
+__global__ __launch_bounds__(kVerifyThreads, TREES ? 2 : 3) void k_verify_pick(VerifyParams p, int pass, int passes) {
   __shared__ WalkShared sh;
   __shared__ int s_gone[kGone], s_last;
   const VerifyArgs& a = p.a;
@@ -846,8 +882,9 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 3 : 4) void k_verify_pick(V
     if (st.state == kDone) return;
   }
   int lo, hi;
+  const float temperature = a.temperature ? a.temperature[b] : 1.f;
   seq_rows(a, b, lo, hi);
-  fill_table(sh.tab);  // (while the bounds are on their way)
+  fill_table(sh.tab);  // (while these are on their way)
   const int n = hi - lo;
   if (n == 0) {
     if (writes && threadIdx.x == 0) {
@@ -856,7 +893,8 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 3 : 4) void k_verify_pick(V
     }
     return;
   }
-  const double T = uniform(temperature_of(a, b)), u = uniform(a.uniforms[lo]);
+  const double T = uniform(static_cast<double>(temperature));
+  const float u = a.uniforms[lo];
   int held = -1;
   if (!TREES || !pass) st.w = Walk{0.0, 1.0, 0, 1, 0, 1, 0};
   if constexpr (!TREES) {
@@ -963,8 +1001,11 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 3 : 4) void k_verify_pick(V
 #pragma unroll
       for (int e = 0; e < 8; ++e) pv[e] = qv[e] = 0.0;
       if (i < a.V) {
-        values8(p.t, w.p, w.c, i, a.V, sh.tab, pv);
-        if (drafted) values8(p.d, w.q, w.c, i, a.V, sh.tab, qv);
+        const Raw8 praw = load8_any(w.p.row, p.t.dt, i, a.V);
+        Raw8 qraw{};
+        if (drafted) qraw = load8_any(w.q.row, p.d.dt, i, a.V);
+        values8(p.t, w.p, praw, w.c, i, a.V, sh.tab, pv);
+        if (drafted) values8(p.d, w.q, qraw, w.c, i, a.V, sh.tab, qv);
         // (more of them than LDS holds: looked for among the rows again)
         const int g0 = ngone <= kGone ? 0 : st.w.cur + 1, g1 = ngone <= kGone ? ngone : n;
         for (int g = g0; g < g1; ++g) {
@@ -1147,7 +1188,13 @@ hipError_t launch_verify(const VerifyArgs& a, hipStream_t s) {
     hipLaunchKernelGGL(k_verify_stats, dim3(static_cast<uint32_t>(blocks)), dim3(kVerifyThreads), 0, s, p, u0, u1);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  const dim3 grid(a.B * l.shares);
+  if (a.draft && a.parents) {  // two workgroups of these to a CU: no more than run at once (48 sequences of 12 rows: 77 -> 74 us)
+    int shares = (512 + a.B - 1) / a.B;
+    if (shares > l.shares) shares = l.shares;
+    p.share_blocks = (l.blocks + shares - 1) / shares;
+    p.shares = (l.blocks + p.share_blocks - 1) / p.share_blocks;
+  }
+  const dim3 grid(a.B * p.shares);
   if (a.M == 0 || !a.draft || !a.parents) {
     hipLaunchKernelGGL(k_verify_pick<false>, grid, dim3(kVerifyThreads), 0, s, p, 0, 1);
     return hipGetLastError();
