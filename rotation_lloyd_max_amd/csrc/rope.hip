@@ -8,7 +8,8 @@
 // heads of a token share them, so a workgroup makes the cosines and sines of its tokens once, in
 // LDS, and its threads then stream the heads: the call is bound by reading x and writing out.
 // 8192 tokens of 32 + 8 heads of 128 in bf16 (168 MB): 28.4 us, 5.9 TB/s, the rate of a copy
-// whose data partly stays in the last cache; one token 2.9 us.
+// whose data partly stays in the last cache; one token 2.9 us. With positions of
+// three axes 29.5 and 2.8 in a stream of launches.
 #include <type_traits>
 
 #include "device_common.hpp"

@@ -167,7 +167,8 @@ def kv_keep(pool, lens, kept, page_table, page_tokens, q_offsets=None, status=No
 class Verified(NamedTuple):
     """What verify found: kept [B] rows of each sequence that stay, the root among them; tokens
     [M], from offsets[b] the drafted tokens that stay and the new one (kept[b] in all), -1 behind
-    them; path [M], from offsets[b] the rows that stay, -1 behind them."""
+    them; path [M], from offsets[b] the rows that stay, -1 behind them. tokens and path behind the
+    last sequence's rows hold anything."""
     kept: torch.Tensor
     tokens: torch.Tensor
     path: torch.Tensor
