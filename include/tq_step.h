@@ -77,6 +77,7 @@ int tq_kv_plan(const tq_kv_pool *pool, int32_t page_tokens, int32_t B, const int
  *                token lens[b] + path[q_offsets[b] + j] are moved to token lens[b] + j, for 0 < j <
  *                kept[b]; the path of tq_verify: path >= j, ascending, below n_b (a row that is not
  *                is not moved; of a path that does not ascend the rows may hold each other's)
+ *   M            elements of path (the step's rows): q_offsets are cut to [0, M]; without a path M is not used
  *   cache        read and written where path is not NULL, else it may be NULL
  *   page_table   device int32 [B][table_width], read; pages outside [0, pages) are not moved
  *   lens_out     device int32 [B], may be lens itself
@@ -84,7 +85,7 @@ int tq_kv_plan(const tq_kv_pool *pool, int32_t page_tokens, int32_t B, const int
  * Limits as for tq_kv_plan. Workspace: none. */
 int tq_kv_keep(const tq_kv_pool *pool, const tq_kv_cache *cache, int32_t page_tokens, int32_t B,
                const int32_t *lens, const int32_t *q_offsets, const int32_t *status,
-               const int32_t *kept, const int32_t *path, const int32_t *page_table,
+               const int32_t *kept, const int32_t *path, int64_t M, const int32_t *page_table,
                int32_t table_width, int32_t *lens_out, int32_t *left, void *stream);
 
 /* flags of tq_verify: the rows are probabilities (not negative), not logits */

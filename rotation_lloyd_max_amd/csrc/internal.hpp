@@ -178,6 +178,7 @@ struct KeepArgs {
   int32_t *free_pages, *state;
   int pages, page, B;
   const int32_t *lens, *q_offsets, *status, *kept, *path;  // q_offsets, status, path may be null
+  int M;  // q_offsets are cut to [0, M]
   const int32_t* table;
   int width;
   int32_t *lens_out, *left;

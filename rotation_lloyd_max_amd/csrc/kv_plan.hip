@@ -252,6 +252,7 @@ __global__ __launch_bounds__(kStepThreads) void k_kv_plan(PlanArgs p, int rows_e
 // A sequence at the end of a step: tokens before it, its rows, those that stay, pages that go back.
 struct KeepSeq {
   uint32_t len, rows, kept, end, from, back;  // back: pages from .. from + back
+  int first;                                  // of the rows, in the step
 };
 __device__ __forceinline__ KeepSeq keep_seq(const KeepArgs& p, int b) {
   KeepSeq s;
@@ -259,8 +260,14 @@ __device__ __forceinline__ KeepSeq keep_seq(const KeepArgs& p, int b) {
   const int len = p.lens[b], kept = p.kept[b];
   s.len = len < 0 ? 0 : len;
   s.len = s.len < cap ? s.len : cap;
-  int rows = p.q_offsets && !(p.status && p.status[b]) ? p.q_offsets[b + 1] - p.q_offsets[b] : 0;
-  rows = rows < 0 ? 0 : rows;
+  int rows = 0;
+  s.first = 0;
+  if (p.q_offsets && !(p.status && p.status[b])) {
+    const int lo = p.q_offsets[b], hi = p.q_offsets[b + 1];
+    s.first = lo < 0 ? 0 : lo < p.M ? lo : p.M;
+    rows = (hi < p.M ? hi : p.M) - s.first;
+    rows = rows < 0 ? 0 : rows;
+  }
   s.rows = static_cast<uint32_t>(rows) < cap - s.len ? rows : cap - s.len;
   s.kept = kept < 0 ? 0 : static_cast<uint32_t>(kept) < s.rows ? kept : s.rows;
   s.end = kept < 0 ? 0 : s.len + s.kept;
@@ -281,7 +288,7 @@ __device__ __forceinline__ void keep_move(const KeepArgs& p, int b, const KeepSe
   const KvHalf& half = value ? p.c.v : p.c.k;
   const int64_t step = scale ? (value ? vs : ks) * 2 : half.wpr * 4;  // bytes of a row
   char* base = scale ? reinterpret_cast<char*>(half.scales) + col * 2 : reinterpret_cast<char*>(half.codes) + col * 8;
-  const int32_t* path = p.path + p.q_offsets[b];
+  const int32_t* path = p.path + s.first;
   const int32_t* table = p.table + static_cast<int64_t>(b) * p.width;
   auto row = [&](uint32_t token) -> int64_t {  // byte offset of its row, -1 outside the cache
     const uint32_t j = token / static_cast<uint32_t>(p.page);

@@ -1051,7 +1051,7 @@ int tq_kv_plan(const tq_kv_pool* pool, int32_t page_tokens, int32_t B, const int
 
 int tq_kv_keep(const tq_kv_pool* pool, const tq_kv_cache* cache, int32_t page_tokens, int32_t B,
                const int32_t* lens, const int32_t* q_offsets, const int32_t* status,
-               const int32_t* kept, const int32_t* path, const int32_t* page_table,
+               const int32_t* kept, const int32_t* path, int64_t M, const int32_t* page_table,
                int32_t table_width, int32_t* lens_out, int32_t* left, void* stream) {
   int rc = check_pool(pool, page_tokens, B, table_width);
   if (rc != TQ_OK) return rc;
@@ -1062,6 +1062,7 @@ int tq_kv_keep(const tq_kv_pool* pool, const tq_kv_cache* cache, int32_t page_to
     if (a.c.page != page_tokens || a.c.pages != pool->pages)
       return fail(TQ_ERR_ARG, "the cache and the pool differ in pages or page_tokens");
     if (!q_offsets) return fail(TQ_ERR_ARG, "a path needs q_offsets");
+    if (M < 0 || M > (1 << 24)) return fail(TQ_ERR_ARG, "M must be in [0, 2^24]");
   }
   if (B == 0 && (!left || left == pool->state)) return TQ_OK;
   if (B > 0 && (!lens || !kept || !lens_out || (table_width > 0 && !page_table)))
@@ -1070,6 +1071,7 @@ int tq_kv_keep(const tq_kv_pool* pool, const tq_kv_cache* cache, int32_t page_to
     return fail(TQ_ERR_ALIGN, "the arrays must be 4-byte aligned");
   a.free_pages = pool->free_pages; a.state = pool->state; a.pages = pool->pages; a.page = page_tokens;
   a.B = B; a.lens = lens; a.q_offsets = q_offsets; a.status = status; a.kept = kept; a.path = path;
+  a.M = path ? static_cast<int>(M) : 0x7fffffff;
   a.table = page_table; a.width = table_width; a.lens_out = lens_out;
   a.left = left ? left : pool->state;
   return hip_status(launch_kv_keep(a, static_cast<hipStream_t>(stream)), "tq_kv_keep");

@@ -27,7 +27,7 @@ _PL = ctypes.POINTER(_KVPool)
 SIGNATURES = [
     ("tq_kv_plan", _INT,
      [_PL, _I32, _I32, _P, _P, _P, _I32, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _P]),
-    ("tq_kv_keep", _INT, [_PL, _KV, _I32, _I32, _P, _P, _P, _P, _P, _P, _I32, _P, _P, _P]),
+    ("tq_kv_keep", _INT, [_PL, _KV, _I32, _I32, _P, _P, _P, _P, _P, _I64, _P, _I32, _P, _P, _P]),
     ("tq_verify", _INT,
      [_P, _INT, _I64, _P, _INT, _I64, _U32, _I64, _I32, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     ("tq_verify_workspace", _SZ, [_I64, _I32, _I64, _I32, _U32]),
@@ -160,7 +160,8 @@ def kv_keep(pool, lens, kept, page_table, page_tokens, q_offsets=None, status=No
     _call(dev, _tq.lib().tq_kv_keep, pool.desc, cache.desc if path is not None else None, page_tokens, B,
           lens.data_ptr(), q_offsets.data_ptr() if q_offsets is not None else None,
           status.data_ptr() if status is not None else None, kept.data_ptr(),
-          path.data_ptr() if path is not None else None, table, width, out.data_ptr(), left)
+          path.data_ptr() if path is not None else None, path.numel() if path is not None else 0, table, width,
+          out.data_ptr(), left)
     return out
 
 

@@ -280,3 +280,18 @@ def test_other_stream_and_int64_arguments():
     st.synchronize()
     assert p.positions.tolist() == [20, 21, 3, 4, 5, 6, 7] and p.slots.tolist()[2:4] == [-1, -1]
     assert pool.state.tolist() == [4, 0]
+
+
+def test_rows_that_the_path_does_not_have_do_not_stay():
+    page, heads = 16, 2
+    cache = filled(4, heads, 64, page, 256, 8, 32, 5)
+    table = np.array([[1, 2], [3, 0]])
+    lens, kept, path = np.array([4, 6]), np.array([3, 9]), np.array([0, 3, 5, 6, 7, 8, 9, 10, 11, 1, 1, 1, 0, 3, 7])
+    want = moved(cache, page, heads, table, lens, np.array([0, 12, 15]), path, [(0, 1), (0, 2)])
+    for offsets in ([0, 12, 24], [-5, 12, 2 ** 31 - 1]):
+        mine = filled(4, heads, 64, page, 256, 8, 32, 5)
+        out = tq.kv_keep(pool_of([], 4), dev(lens), dev(kept), dev(table), page, q_offsets=dev(offsets), path=dev(path), cache=mine)
+        torch.cuda.synchronize()
+        assert out.tolist() == [7, 9]
+        for a, b in zip((mine.k.codes, mine.k.scales, mine.v.codes, mine.v.scales), want):
+            assert torch.equal(a, b)

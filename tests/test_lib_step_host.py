@@ -50,8 +50,8 @@ def plan(p=None, page=64, B=2, lens=256, counts=256, table=256, width=10, M=7, p
                                pos, off, kvl, status, tree, words, left, None)
 
 
-def keep(p=None, c=None, page=64, B=2, lens=256, off=256, status=None, kept=256, path=None, table=256, width=10, out=256, left=None):
-    return tq.lib().tq_kv_keep(p if p is not None else pool(), c, page, B, lens, off, status, kept, path, table, width, out,
+def keep(p=None, c=None, page=64, B=2, lens=256, off=256, status=None, kept=256, path=None, M=7, table=256, width=10, out=256, left=None):
+    return tq.lib().tq_kv_keep(p if p is not None else pool(), c, page, B, lens, off, status, kept, path, M, table, width, out,
                                left, None)
 
 
@@ -80,6 +80,7 @@ def test_plan_refusals(kw, status):
     (dict(kept=None), ERR_ARG), (dict(out=None), ERR_ARG), (dict(kept=258), ERR_ALIGN), (dict(off=258), ERR_ALIGN),
     (dict(status=258), ERR_ALIGN), (dict(out=258), ERR_ALIGN), (dict(path=256), ERR_ARG), (dict(path=256, c=cache(), page=32), ERR_ARG),
     (dict(path=256, c=cache(), p=pool(pages=5)), ERR_ARG), (dict(path=256, c=cache(), off=None), ERR_ARG),
+    (dict(path=256, c=cache(), M=-1), ERR_ARG), (dict(path=256, c=cache(), M=(1 << 24) + 1), ERR_ARG),
     (dict(path=258, c=cache()), ERR_ALIGN)])
 def test_keep_refusals(kw, status):
     assert keep(**kw) == status, tq.lib().tq_last_error()
@@ -93,7 +94,7 @@ def test_moves_refuse_a_bad_cache(bad, status):
 def test_null_pool_and_no_sequences():
     L = tq.lib()
     assert L.tq_kv_plan(None, 64, 2, 256, 256, 256, 10, 7, None, None, 256, 256, 256, 256, 256, None, 0, None, None) == ERR_ARG
-    assert L.tq_kv_keep(None, None, 64, 2, 256, 256, None, 256, None, 256, 10, 256, None, None) == ERR_ARG
+    assert L.tq_kv_keep(None, None, 64, 2, 256, 256, None, 256, None, 0, 256, 10, 256, None, None) == ERR_ARG
     assert keep(B=0, lens=None, kept=None, out=None, table=None) == 0      # (nothing to launch)
 
 
