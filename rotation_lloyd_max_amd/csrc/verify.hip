@@ -700,6 +700,39 @@ __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int 
       held = w0;
       if (w.known < w1) w.known = w1;
     }
+    if (!TREES && !a.parents && !greedy) {
+      // A chain: no test depends on another's, so 64 rows at a time (nine rows that stay one by one: 7 us).
+      for (;;) {
+        const int i = w.next + lane;
+        bool row = false, yes = false;
+        int x = 0;
+        if (i < w1) {
+          const RowInfo& f = sh.row[i - w0];
+          x = f.token;
+          row = f.parent >= 0;
+          yes = row && (drafted ? f.u * f.qx : f.u) < f.px;
+        }
+        const uint64_t m = ~__ballot(yes);
+        const int run = m ? __builtin_ctzll(m) : 64;
+        if (writes && threadIdx.x < 64 && lane < run) {
+          a.out_tokens[lo + w.kept - 1 + lane] = x;
+          a.path[lo + w.kept + lane] = i;
+        }
+        w.kept += run;
+        w.next += run;
+        w.cur = w.next - 1;
+        if (run == 64 && w.next < w1) continue;
+        if (w.next < w1) {
+          if (__ballot(row) >> run & 1) {
+            w.tried = w.next;
+            w.al = 1.0;
+          }
+          w.next = n;
+        }
+        break;
+      }
+      continue;
+    }
     // the next child of cur in the window
     int r = w1;
     for (int i = w.next; i < w1; i += 64) {
@@ -734,7 +767,6 @@ __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int 
     } else {
       w.tried = r;
       if (!a.parents) {  // a chain has no siblings
-        w.al = 1.0;
         w.next = n;
       } else if (TREES && drafted) {
         w.al += w.S;

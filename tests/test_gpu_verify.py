@@ -395,3 +395,27 @@ def test_more_pieces_of_a_row_than_lanes_hold(tree, ddt):
     for kind in ("logits", "probabilities"):
         check(case(39, 2, 4, 600001, "fp32", ddt, kind, tree, ragged=False, noise=1.5))
     check(case(40, 2, 3, 1100000, "bf16", ddt, "logits", tree, ragged=False, temperature=np.array([0.0, 0.9], np.float32)))
+
+
+@pytest.mark.parametrize("ddt", ["fp32", None])
+def test_long_chains_that_end_anywhere(ddt):
+    # 64 rows are looked at at once, 256 are in LDS: all stay, one is turned away or is padding near the ends of these
+    n = 600
+    c = case(41, 12, n, 40, "fp32", ddt, ragged=False, noise=0.0, spread=2.0)
+    c["uniforms"] = (c["uniforms"] * 1e-4).astype(np.float32)
+    src = as_f64(c["target"])
+    c["tokens"] = np.concatenate([[0], np.argmax(src[:-1], 1)])       # the likeliest tokens: all stay
+    if ddt:
+        c["draft"] = c["target"].clone()
+    ends = (0, 1, 63, 64, 65, 127, 255, 256, 257, 511, 598, 599)
+    for b, e in enumerate(ends):
+        row = b * n + e + 1
+        if e + 1 < n:
+            if b % 2:
+                c["tokens"][row] = -1
+            else:
+                c["uniforms"][row] = 1.0
+                if ddt is None:
+                    c["tokens"][row] = np.argmin(src[row - 1])
+    got = check(c)
+    assert got.kept.tolist() == [e + 1 for e in ends]
