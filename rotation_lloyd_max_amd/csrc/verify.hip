@@ -1161,7 +1161,8 @@ struct VerifyLayout {
 
 // Pieces of rows: as long as 4096 waves get one each, up to 16 blocks (a wave joins its sum over the lanes
 // once per piece), and of no more than kPieces to a row, which 16 lanes join without a loop (256 of them took
-// the walk of 8 rows 17 us instead of 4); workgroups of a sequence: 1024 in all, with a block for each wave at least.
+// the walk of 8 rows 17 us instead of 4). Workgroups of a sequence: 768 in all, three to a CU, with a block for each wave
+// at least (200 sequences of 5 rows of 32000: 55.0 us, 58.7 with 1024, 55.9 with 512; 64 of 9 of 131072: 84.5, 84.5, 85.6).
 VerifyLayout layout(int V, int B, int M, bool tprobs, bool drafted, bool dprobs) {
   VerifyLayout l{};
   l.blocks = (V + kBlockElems - 1) / kBlockElems;
@@ -1171,7 +1172,7 @@ VerifyLayout layout(int V, int B, int M, bool tprobs, bool drafted, bool dprobs)
   l.part_blocks = 16;
   while (l.part_blocks > 1 && rows * pieces(l.part_blocks) < 4096 && pieces(l.part_blocks / 2) <= kPieces) l.part_blocks /= 2;
   l.parts = pieces(l.part_blocks);
-  int shares = B > 0 ? (1024 + B - 1) / B : 1;
+  int shares = B > 0 ? (768 + B - 1) / B : 1;
   if (shares > (l.blocks + 3) / 4) shares = (l.blocks + 3) / 4;
   l.share_blocks = (l.blocks + shares - 1) / shares;
   l.shares = (l.blocks + l.share_blocks - 1) / l.share_blocks;
