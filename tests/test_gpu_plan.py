@@ -295,3 +295,26 @@ def test_rows_that_the_path_does_not_have_do_not_stay():
         assert out.tolist() == [7, 9]
         for a, b in zip((mine.k.codes, mine.k.scales, mine.v.codes, mine.v.scales), want):
             assert torch.equal(a, b)
+
+
+def test_moves_in_a_cache_of_gigabytes():
+    page, heads, pages = 64, 8, 70000      # (4.6 GB of key codes)
+    cache = tq.kv_cache(pages, heads, 128, page_tokens=page)
+    table = np.array([[69998, 69999, 3], [1, 40000, 69997]])
+    lens, path, kept = np.array([60, 126]), np.array([0, 2, 5, 6, -1, -1, -1] + [0, 1, 3, 5, 6, -1, -1]), np.array([4, 5])
+    g = torch.Generator(device="cuda").manual_seed(7)
+    for w in (cache.k, cache.v):
+        for t in (w.codes, w.scales):
+            rows = t[table.reshape(-1)]
+            t[table.reshape(-1)] = torch.randint(1, 2 ** 14, rows.shape, generator=g, device="cuda").to(t.dtype)
+    before = [{p: t[p].clone() for p in table.reshape(-1)} for w in (cache.k, cache.v) for t in (w.codes, w.scales)]
+    for b in range(2):
+        for j in range(1, kept[b]):
+            s, d = lens[b] + path[7 * b + j], lens[b] + j
+            for t in before:
+                t[table[b][d // page]][d % page::page] = t[table[b][s // page]][s % page::page].clone()
+    out = tq.kv_keep(pool_of([], pages), dev(lens), dev(kept), dev(table), page, q_offsets=dev([0, 7, 14]), path=dev(path), cache=cache)
+    torch.cuda.synchronize()
+    assert out.tolist() == [64, 131]
+    for t, want in zip((t for w in (cache.k, cache.v) for t in (w.codes, w.scales)), before):
+        assert all(torch.equal(t[p], x) for p, x in want.items())

@@ -419,3 +419,14 @@ def test_long_chains_that_end_anywhere(ddt):
                     c["tokens"][row] = np.argmin(src[row - 1])
     got = check(c)
     assert got.kept.tolist() == [e + 1 for e in ends]
+
+
+def test_rows_gigabytes_apart():
+    c = case(42, 2, 3, 5000, "bf16", "fp32", ragged=False)
+    g = on_gpu(c)
+    for name in ("target", "draft"):
+        t = g[name]
+        wide = torch.empty(5 * (1 << 30) + 5000, dtype=t.dtype, device="cuda").as_strided((6, 5000), (1 << 30, 1))
+        wide.copy_(t)
+        g[name] = wide
+    check(c, tq.verify(**g))
