@@ -4,6 +4,7 @@ marshalling only; like the calls of kv.py these run once per step, so their host
 """
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -175,18 +176,22 @@ class Verified(NamedTuple):
     path: torch.Tensor
 
 
-def verify_workspace(vocab, seqs, rows, drafted=False, target_kind="logits", draft_kind="logits"):
-    """Bytes of workspace verify needs for `rows` rows of `seqs` sequences."""
-    n = _tq.lib().tq_verify_workspace(vocab, seqs, rows, 1 if drafted else 0,
-                                      _KINDS[target_kind] | _KINDS[draft_kind] << 1)
+@functools.lru_cache(maxsize=256)
+def _verify_bytes(vocab, seqs, rows, drafted, flags):
+    n = _tq.lib().tq_verify_workspace(vocab, seqs, rows, drafted, flags)
     if n == _NONE:
         raise _tq.TqError(-1, _tq.lib().tq_last_error().decode())
     return n
 
 
+def verify_workspace(vocab, seqs, rows, drafted=False, target_kind="logits", draft_kind="logits"):
+    """Bytes of workspace verify needs for `rows` rows of `seqs` sequences."""
+    return _verify_bytes(vocab, seqs, rows, 1 if drafted else 0, _KINDS[target_kind] | _KINDS[draft_kind] << 1)
+
+
 def _rows(t, M, V, dev, name):
     """Row stride of a distribution tensor [M, V] whose rows are contiguous."""
-    if t.dim() != 2 or tuple(t.shape) != (M, V):
+    if t.shape != (M, V):
         raise ValueError(f"{name} must be [{M}, {V}], got {tuple(t.shape)}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, the call runs on {dev}")
@@ -226,16 +231,17 @@ def verify(target, tokens, uniforms, offsets, draft=None, parents=None, temperat
         flags = _KINDS[target_kind] | _KINDS[draft_kind] << 1
     except KeyError:
         raise ValueError(f"target_kind and draft_kind must be one of {list(_KINDS)}") from None
-    nbytes = _tq.lib().tq_verify_workspace(V, B, M, 1 if draft is not None else 0, flags)
-    if nbytes == _NONE:
-        raise _tq.TqError(-1, _tq.lib().tq_last_error().decode())
-    if ws is None:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-    elif ws.device != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < nbytes:
+    nbytes = _verify_bytes(V, B, M, 1 if draft is not None else 0, flags)
+    if ws is not None and (ws.device != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < nbytes):
         raise ValueError(f"ws= must be a contiguous tensor of at least {nbytes} bytes on {dev}")
-    out = Verified(*tokens.new_empty((B + 2 * M,)).split_with_sizes((B, M, M)))
+    words = 0
+    if ws is None and nbytes <= 1 << 20:     # in one allocation with the outputs (1 us of 16), which keep it
+        words = nbytes >> 2
+    elif ws is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    whole = tokens.new_empty((words + B + 2 * M,))
+    at = whole.data_ptr() + 4 * words
     _call(dev, _tq.lib().tq_verify, target.data_ptr(), _tq._dt(target), ts, dp, dd, ds, flags, V, B,
           offsets.data_ptr(), M, tokens.data_ptr(), parents.data_ptr() if parents is not None else None, up, tp,
-          out.kept.data_ptr(), out.tokens.data_ptr(), out.path.data_ptr(),
-          ws.data_ptr() if ws is not None else None, nbytes)
-    return out
+          at, at + 4 * B, at + 4 * (B + M), ws.data_ptr() if ws is not None else whole.data_ptr(), nbytes)
+    return Verified(*whole.split_with_sizes((words, B, M, M))[1:])
