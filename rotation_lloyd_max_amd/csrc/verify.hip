@@ -22,11 +22,11 @@
 // workgroup sums alone (20 rows of 8 sequences, 60000 tokens: 105 us when the first launch's did so, 57 now).
 //
 // Bounds and figures. 64 sequences of 9 rows, 131072 tokens in bf16, a draft: k_verify_stats reads 285 MB in 54 us,
-// 5.3 TB/s, bound by memory; k_verify_pick, 34 us, reads 64 of these rows again: 6 us for the walk (12 where nine
-// rows stay), 11 for the sums (fp64 operations at 4.7 cycles a wave are 7 of them), 5 for the meeting and the
-// last block; the rest is the slowest sequence. One sequence of 4 rows, 32000 tokens: 4 + 14 us, the latency of
-// some ten loads that wait for each other (1500 cycles each: another launch wrote them, or nobody read them yet)
-// and of fp64 chains in waves that have a SIMD to themselves.
+// 5.3 TB/s, bound by memory; k_verify_pick, 33 us, reads 64 of these rows again: 5 us for the walk, 1 for the row's
+// constants, 17 for the sums (vector instructions: about 36 for a token of both rows), 5 for the meeting and the last
+// block. One sequence of 4 rows, 32000 tokens: 15.2 us in a stream of launches, 4.6 of them launches and the rows'
+// sums, 3.1 the walk, 0.9, 3.0 the sums, 1.7 until the block is found, 1.8 the token: the latency of some ten loads
+// that wait for each other and of fp64 chains in waves that have a SIMD to themselves.
 #include "internal.hpp"
 #include "kv_lane.hpp"
 
