@@ -318,3 +318,16 @@ def test_moves_in_a_cache_of_gigabytes():
     assert out.tolist() == [64, 131]
     for t, want in zip((t for w in (cache.k, cache.v) for t in (w.codes, w.scales)), before):
         assert all(torch.equal(t[p], x) for p, x in want.items())
+
+
+def test_as_many_sequences_as_there_may_be():
+    g = np.random.default_rng(11)
+    lens, counts = g.integers(0, 50, 65536), g.integers(0, 3, 65536)
+    table, free = setup(g, lens, 16, 300000, 5)
+    want, pool, t, p = check_plan(lens, counts, table, free, int(counts.sum()) + 5, 16, 300000)
+    kept = g.integers(-1, 4, 65536)
+    ends, left, _ = ost.keep(want["free"], lens, kept, want["table"], 16, q_offsets=want["q_offsets"], status=want["status"])
+    out = tq.kv_keep(pool, dev(lens), dev(kept), t, 16, q_offsets=p.q_offsets, status=p.status)
+    torch.cuda.synchronize()
+    assert np.array_equal(out.cpu().numpy(), ends)
+    assert pool.state.tolist() == [len(left), 0] and pool.free[:len(left)].tolist() == left

@@ -430,3 +430,9 @@ def test_rows_gigabytes_apart():
         wide.copy_(t)
         g[name] = wide
     check(c, tq.verify(**g))
+
+
+@pytest.mark.parametrize("ddt", ["bf16", None])
+def test_as_many_sequences_as_there_may_be(ddt):
+    check(case(43, 65536, 2, 5, "bf16", ddt))
+    check(case(44, 3000, 3, 130, "fp16", ddt, tree=True, temperature="mixed"))
