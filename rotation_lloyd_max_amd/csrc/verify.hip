@@ -27,6 +27,8 @@
 // block. One sequence of 4 rows, 32000 tokens: 15.2 us in a stream of launches, 4.6 of them launches and the rows'
 // sums, 3.1 the walk, 0.9, 3.0 the sums, 1.7 until the block is found, 1.8 the token: the latency of some ten loads
 // that wait for each other and of fp64 chains in waves that have a SIMD to themselves.
+#include <type_traits>
+
 #include "internal.hpp"
 #include "kv_lane.hpp"
 
@@ -40,7 +42,7 @@ constexpr int kBlockElems = 512;    // a wave's step: 8 elements a lane
 constexpr int kWindow = 256;        // rows whose probabilities are in LDS at a time
 constexpr int kGone = 256;          // tried tokens in LDS
 constexpr int kTable = 256;         // 2^(i / 256)
-constexpr int kPieces = 64;         // pieces of a row that 16 lanes hold at once
+constexpr int kPieces = 32;         // pieces of a row that the lanes of a row hold at once
 constexpr int kPasses = 4;          // launches of k_verify_pick for trees with a draft
 
 // Of a piece of a row: z = sum 2^((x - top) c), c = log2(e) / T, top a value with x - top below 100 / c for every
@@ -150,7 +152,9 @@ __device__ __forceinline__ void load8_end(const char* row, int i, int V, float n
 struct Raw8 {
   uint32_t x[8];
 };
+template <int DT>
 __device__ __forceinline__ Raw8 load8_any(const char* row, int dt, int i, int V) {
+  if (DT >= 0) dt = DT;
   Raw8 r;
   if (dt == 0 && i + 8 <= V) {
     const u32x4_a2 a = *reinterpret_cast<const u32x4_a2*>(row + static_cast<int64_t>(i) * 4);
@@ -176,7 +180,9 @@ __device__ __forceinline__ Raw8 load8_any(const char* row, int dt, int i, int V)
   }
   return r;
 }
+template <int DT>
 __device__ __forceinline__ void values_any(const Raw8& r, int dt, int i, int V, float none, float (&f)[8]) {
+  if (DT >= 0) dt = DT;
   if (dt == 0) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(r.x[k]);
@@ -256,13 +262,14 @@ __device__ __forceinline__ double temperature_of(const VerifyArgs& a, int b) { r
 __device__ __forceinline__ double scale_of(double T) { return 1.4426950408889634074 / T; }
 __device__ __forceinline__ double reach_of(double T) { return 693.14718055994530942 * T; }  // 1000 / scale
 
-// Over rows of 16 lanes and over the wave, in every lane, by lane moves that need no LDS (kv_lane.hpp); NaN
+// Over rows of 8 or 16 lanes and over the wave, in every lane, by lane moves that need no LDS (kv_lane.hpp); NaN
 // where any is.
+template <int LANES = 16>
 __device__ __forceinline__ float row_max(float x) {
   x = __builtin_elementwise_maximum(x, kv_swap<0>(x));
   x = __builtin_elementwise_maximum(x, kv_swap<1>(x));
   x = __builtin_elementwise_maximum(x, kv_swap<2>(x));
-  return __builtin_elementwise_maximum(x, kv_swap<3>(x));
+  return LANES == 8 ? x : __builtin_elementwise_maximum(x, kv_swap<3>(x));
 }
 __device__ __forceinline__ float wave_max(float x) {
   float a, b;
@@ -270,11 +277,12 @@ __device__ __forceinline__ float wave_max(float x) {
   kv_both<5>(__builtin_elementwise_maximum(a, b), a, b);
   return __builtin_elementwise_maximum(a, b);
 }
+template <int LANES = 16>
 __device__ __forceinline__ double row_sum(double x) {
   x += kv_swap<0>(x);
   x += kv_swap<1>(x);
   x += kv_swap<2>(x);
-  return x + kv_swap<3>(x);
+  return LANES == 8 ? x : x + kv_swap<3>(x);
 }
 __device__ __forceinline__ double wave_sum(double x) {
   double a, b;
@@ -505,8 +513,8 @@ template <int LANES>
 __device__ __forceinline__ Dist dist_of(const VerifyParams& p, const Side& s, int row, double c, const double* tab) {
   Dist d{0.0, 1.0};
   if (s.probs) return d;
-  static_assert(LANES == 16 || LANES == 64, "rows of lanes, or the wave");
-  constexpr int HELD = kPieces / 16;
+  static_assert(LANES == 8 || LANES == 16 || LANES == 64, "rows of lanes, or the wave");
+  constexpr int HELD = kPieces / (LANES == 64 ? 16 : LANES);
   const StatPart* st = s.stat + static_cast<int64_t>(row) * p.parts;
   const int l = threadIdx.x & (LANES - 1);
   const float inf = __builtin_inff();
@@ -520,7 +528,7 @@ __device__ __forceinline__ Dist dist_of(const VerifyParams& p, const Side& s, in
 #pragma unroll
   for (int k = 0; k < HELD; ++k) top = __builtin_elementwise_maximum(top, held[k].top);
   for (int k = l + HELD * LANES; k < p.parts; k += LANES) top = __builtin_elementwise_maximum(top, st[k].top);
-  top = LANES == 16 ? row_max(top) : wave_max(top);
+  top = LANES < 64 ? row_max<LANES>(top) : wave_max(top);
   double z = 0.0;
 #pragma unroll
   for (int k = 0; k < HELD; ++k) {
@@ -531,7 +539,7 @@ __device__ __forceinline__ Dist dist_of(const VerifyParams& p, const Side& s, in
     const StatPart q = st[k];
     if (q.z != 0.0) z += q.z * add_exp2((static_cast<double>(q.top) - top) * c, 0.0, tab);
   }
-  z = LANES == 16 ? row_sum(z) : wave_sum(z);
+  z = LANES < 64 ? row_sum<LANES>(z) : wave_sum(z);
   d.ref = top;
   d.zinv = z > 0.0 && z < __builtin_inf() ? 1.0 / z : __builtin_nan("");
   return d;
@@ -606,10 +614,11 @@ __device__ __forceinline__ WeightSide weight_side(const Side& s, int row, const 
   return w;
 }
 
+template <int DT>
 __device__ __forceinline__ void values8(const Side& s, const WeightSide& w, const Raw8& raw, double c, int i, int V, const double* tab,
                                                double (&v)[8]) {
   float f[8];
-  values_any(raw, s.dt, i, V, s.probs ? 0.f : -__builtin_inff(), f);
+  values_any<DT>(raw, s.dt, i, V, s.probs ? 0.f : -__builtin_inff(), f);
   if (s.probs) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = f[k];
@@ -632,7 +641,8 @@ struct WalkShared {
   int pick[32];
 };
 
-__device__ __forceinline__ int parent_of(const VerifyArgs& a, int lo, int r) { return a.parents ? a.parents[lo + r] : r - 1; }
+template <bool TREE>
+__device__ __forceinline__ int parent_of(const VerifyArgs& a, int lo, int r) { return TREE ? a.parents[lo + r] : r - 1; }
 
 // Whether a child of cur before row `end` has token x, by all lanes of a wave.
 __device__ __forceinline__ bool tried_before(const VerifyArgs& a, const WalkShared& sh, int lo, int n, int cur, int end, int x) {
@@ -641,7 +651,7 @@ __device__ __forceinline__ bool tried_before(const VerifyArgs& a, const WalkShar
   for (int r = cur + 1; r < end && !found; r += 64) {
     const int i = r + lane;
     bool hit = false;
-    if (i < end) hit = n <= kWindow ? sh.row[i].parent == cur && sh.row[i].token == x : parent_of(a, lo, i) == cur && a.tokens[lo + i] == x;
+    if (i < end) hit = n <= kWindow ? sh.row[i].parent == cur && sh.row[i].token == x : parent_of<true>(a, lo, i) == cur && a.tokens[lo + i] == x;
     found = __ballot(hit) != 0;
   }
   return found;
@@ -649,17 +659,18 @@ __device__ __forceinline__ bool tried_before(const VerifyArgs& a, const WalkShar
 
 // Rows [w0, w1) into LDS: their tokens' probabilities under their parents, 16 lanes a row. kept: where a
 // launch before has left them (load), or where they are left for the next (null: not).
+template <bool TREE, bool DRAFT>
 __device__ __forceinline__ void fill_window(const VerifyParams& p, WalkShared& sh, int lo, int w0, int w1, double T, RowInfo* kept,
                                             bool load) {
   const VerifyArgs& a = p.a;
-  const bool greedy = !(T > 0.0), drafted = a.draft && !greedy;
+  const bool greedy = !(T > 0.0), drafted = DRAFT && !greedy;
   const double c = scale_of(T);
-  constexpr int LANES = 16;
+  constexpr int LANES = TREE ? 8 : 16;
   if (load) {
     for (int r = w0 + static_cast<int>(threadIdx.x); r < w1; r += kVerifyThreads) sh.row[r - w0] = kept[lo + r];
   } else {
     for (int r = w0 + static_cast<int>(threadIdx.x) / LANES; r < w1; r += kVerifyThreads / LANES) {
-      const int up = parent_of(a, lo, r), x = a.tokens[lo + r];
+      const int up = parent_of<TREE>(a, lo, r), x = a.tokens[lo + r];
       const float u = a.uniforms[lo + r];
       const bool any = r > 0 && up >= 0 && up < r && x >= 0 && x < a.V;
       RowInfo i{0.0, 0.0, u, {0.0, 1.0}, {0.0, 1.0}, any ? up : -1, x};
@@ -685,22 +696,23 @@ __device__ __forceinline__ void fill_window(const VerifyParams& p, WalkShared& s
 
 // Walks on, all waves of the workgroup alike, until S of cur is needed (true) or no child stays (false).
 // `writes`: this workgroup writes the tokens that stay. held: the window in LDS, -1 for none. later: not the first launch.
-template <bool TREES>
+template <bool TREE, bool DRAFT>
 __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int lo, int n, double T, bool writes, Walk& w, int& held,
                                      bool later) {
+  constexpr bool SUMS = TREE && DRAFT;
   const VerifyArgs& a = p.a;
   const int lane = threadIdx.x & 63;
-  const bool greedy = !(T > 0.0), drafted = a.draft && !greedy;
+  const bool greedy = !(T > 0.0), drafted = DRAFT && !greedy;
   int largest = greedy ? largest_of(p, lo + w.cur) : -1;
   while (w.next < n) {
     const int w0 = w.next / kWindow * kWindow, w1 = n - w0 < kWindow ? n : w0 + kWindow;
     if (held != w0) {
       if (held >= 0) __syncthreads();
-      fill_window(p, sh, lo, w0, w1, T, TREES && (later || writes) ? p.rows : nullptr, TREES && later && w0 < w.known);
+      fill_window<TREE, DRAFT>(p, sh, lo, w0, w1, T, SUMS && (later || writes) ? p.rows : nullptr, SUMS && later && w0 < w.known);
       held = w0;
       if (w.known < w1) w.known = w1;
     }
-    if (!TREES && !a.parents && !greedy) {
+    if (!TREE && !greedy) {
       // A chain: no test depends on another's, so 64 rows at a time (nine rows that stay one by one: 7 us).
       for (;;) {
         const int i = w.next + lane;
@@ -754,7 +766,7 @@ __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int 
     } else if (drafted) {
       yes = w.S > 0.0 && u * w.S * qx < px - w.al * qx;  // (nothing left: the difference is rounding)
     } else {
-      taken = w.tried && tried_before(a, sh, lo, n, w.cur, r, x);
+      taken = TREE && w.tried && tried_before(a, sh, lo, n, w.cur, r, x);
       yes = u * w.S < (taken ? 0.0 : px);
     }
     if (yes) {
@@ -766,13 +778,13 @@ __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int 
       if (greedy) largest = largest_of(p, lo + r);
     } else {
       w.tried = r;
-      if (!a.parents) {  // a chain has no siblings
+      if (!TREE) {  // a chain has no siblings
         w.next = n;
-      } else if (TREES && drafted) {
+      } else if (drafted) {
         w.al += w.S;
         // (S is of use only if another child follows)
         bool more = false;
-        for (int i = r + 1; i < n && !more; i += 64) more = __ballot(i + lane < n && parent_of(a, lo, i + lane) == w.cur) != 0;
+        for (int i = r + 1; i < n && !more; i += 64) more = __ballot(i + lane < n && parent_of<TREE>(a, lo, i + lane) == w.cur) != 0;
         if (more) return true;
       } else if (!taken) {
         w.S -= px;
@@ -796,9 +808,11 @@ struct Found {
   double total, goal, before;  // sum of all, u of it, sum before the block
   double rp, rq;   // 1 / P, 1 / Q
 };
+template <bool DRAFT>
 __device__ __forceinline__ Found locate(WalkShared& sh, const double* sums, int blocks, const Sums* totals, int ntotals, bool drafted,
                                         bool plogits, bool qlogits, double al, double u) {
   constexpr int NT = kVerifyThreads, W = NT / 64;
+  drafted = DRAFT && drafted;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int each = (blocks + NT - 1) / NT;
   const int k0 = static_cast<int>(threadIdx.x) * each < blocks ? threadIdx.x * each : blocks, k1 = k0 + each < blocks ? k0 + each : blocks;
@@ -898,10 +912,14 @@ __device__ __forceinline__ Found locate(WalkShared& sh, const double* sums, int 
 }
 
 // The workgroups of a sequence (`shares` of them) sum w over their blocks; the last finds the token, or walks on.
-// TREES: siblings against a draft, several launches; as a branch at run time it spilled registers, at three
-// waves a SIMD it does (205 registers wanted: 8 sequences of 20 rows 61 us against 57 a call, 48 of 12 rows 74 either way).
-template <bool TREES>
-__global__ __launch_bounds__(kVerifyThreads, TREES ? 2 : 3) void k_verify_pick(VerifyParams p, int pass, int passes) {
+// Trees with a draft take several launches. Chains, trees, drafts and the rows' type (DT, as in load_elem; -1: two
+// of them) are told apart at compile time: a wave that has a SIMD to itself pays for every branch and spilled
+// register (one sequence of 4 rows 14.0 us, 14.9 with all of it in one kernel; 8 trees of 24 rows 20.3, 23.6; 64
+// sequences of 9 rows 80.5, 84.5). Trees with a draft want 200 registers: at three waves a SIMD they spilled (8
+// sequences of 20 rows 61 us a call against 57).
+template <bool TREE, bool DRAFT, int DT>
+__global__ __launch_bounds__(kVerifyThreads, TREE && DRAFT ? 2 : 3) void k_verify_pick(VerifyParams p, int pass, int passes) {
+  constexpr bool SUMS = TREE && DRAFT;
   __shared__ WalkShared sh;
   __shared__ int s_gone[kGone], s_last;
   const VerifyArgs& a = p.a;
@@ -909,7 +927,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 2 : 3) void k_verify_pick(V
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   bool writes = share == 0;  // this workgroup writes outputs
   Pending st;
-  if (TREES && pass) {
+  if (SUMS && pass) {
     st = p.pending[b];
     if (st.state == kDone) return;
   }
@@ -921,16 +939,16 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 2 : 3) void k_verify_pick(V
   if (n == 0) {
     if (writes && threadIdx.x == 0) {
       a.kept[b] = 0;
-      if (TREES) p.pending[b].state = kDone;
+      if (SUMS) p.pending[b].state = kDone;
     }
     return;
   }
   const double T = uniform(static_cast<double>(temperature));
   const float u = a.uniforms[lo];
   int held = -1;
-  if (!TREES || !pass) st.w = Walk{0.0, 1.0, 0, 1, 0, 1, 0};
-  if constexpr (!TREES) {
-    walk<false>(p, sh, lo, n, T, writes, st.w, held, false);
+  if (!SUMS || !pass) st.w = Walk{0.0, 1.0, 0, 1, 0, 1, 0};
+  if constexpr (!SUMS) {
+    walk<TREE, DRAFT>(p, sh, lo, n, T, writes, st.w, held, false);
     st.w = uniform(st.w);
     st.state = kToken;
   }
@@ -940,7 +958,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 2 : 3) void k_verify_pick(V
   int k0 = share * p.share_blocks < blocks ? share * p.share_blocks : blocks;
   int k1 = k0 + p.share_blocks < blocks ? k0 + p.share_blocks : blocks;
   bool alone = false;              // the others have ended
-  bool walks = TREES && !pass, fresh = true;  // to walk on; to begin with the row that the walk has come to
+  bool walks = SUMS && !pass, fresh = true;  // to walk on; to begin with the row that the walk has come to
   bool drafted = false;
   int ngone = 0;
   double al = 0.0, rho = 0.0;
@@ -966,13 +984,13 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 2 : 3) void k_verify_pick(V
     }
     const int row = lo + st.w.cur;
     w.c = scale_of(T);
-    drafted = a.draft && al != 0.0;
+    drafted = DRAFT && al != 0.0;
     Dist dp, dq{0.0, 1.0};
     if (res == -2) {
       if (st.w.tried && held == 0 && n <= kWindow) {  // (the last child's parent is this row)
         dp = sh.row[st.w.tried].p;
         dq = sh.row[st.w.tried].q;
-      } else if (TREES && pass && st.w.tried) {
+      } else if (SUMS && pass && st.w.tried) {
         dp = p.rows[lo + st.w.tried].p;
         dq = p.rows[lo + st.w.tried].q;
       } else {
@@ -984,7 +1002,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 2 : 3) void k_verify_pick(V
     if (res != -2) {
       if (writes && threadIdx.x == 0) {
         a.out_tokens[lo + st.w.kept - 1] = res;
-        if (TREES) p.pending[b].state = kDone;
+        if (SUMS) p.pending[b].state = kDone;
       }
       return false;
     }
@@ -994,10 +1012,10 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 2 : 3) void k_verify_pick(V
     rho = al * (w.q.inv / w.p.inv);
     // tokens that were taken out of p
     ngone = 0;
-    if (!a.draft && st.w.tried) {
+    if (!DRAFT && st.w.tried) {
       for (int r0 = st.w.cur + 1; r0 < n; r0 += 64) {
         const int r = r0 + lane;
-        const bool child = r < n && parent_of(a, lo, r) == st.w.cur;
+        const bool child = r < n && parent_of<TREE>(a, lo, r) == st.w.cur;
         const uint64_t m = __ballot(child);
         const int at = ngone + __popcll(m & ((1ull << lane) - 1));
         if (wave == 0 && child && at < kGone) s_gone[at] = a.tokens[lo + r];
@@ -1007,13 +1025,13 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 2 : 3) void k_verify_pick(V
     }
     return true;
   };
-  if constexpr (!TREES)
+  if constexpr (!SUMS)
     if (!begin()) return;
   // The same loop sums blocks and, at last, looks at the block that the token is in: the code is in the
   // instruction cache then, where a copy of it took 2 us to come.
   for (;;) {
-    if (TREES && walks) {
-      st.state = walk<true>(p, sh, lo, n, T, writes, st.w, held, pass > 0) ? kLeft : kToken;
+    if (SUMS && walks) {
+      st.state = walk<TREE, DRAFT>(p, sh, lo, n, T, writes, st.w, held, pass > 0) ? kLeft : kToken;
       st.w = uniform(st.w);
       walks = false;
       fresh = true;
@@ -1022,7 +1040,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 2 : 3) void k_verify_pick(V
         return;
       }
     }
-    if (TREES && fresh) {
+    if (SUMS && fresh) {
       fresh = false;
       if (!begin()) return;
     }
@@ -1033,15 +1051,15 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 2 : 3) void k_verify_pick(V
 #pragma unroll
       for (int e = 0; e < 8; ++e) pv[e] = qv[e] = 0.0;
       if (i < a.V) {
-        const Raw8 praw = load8_any(w.p.row, p.t.dt, i, a.V);
+        const Raw8 praw = load8_any<DT>(w.p.row, p.t.dt, i, a.V);
         Raw8 qraw{};
-        if (drafted) qraw = load8_any(w.q.row, p.d.dt, i, a.V);
-        values8(p.t, w.p, praw, w.c, i, a.V, sh.tab, pv);
-        if (drafted) values8(p.d, w.q, qraw, w.c, i, a.V, sh.tab, qv);
+        if (drafted) qraw = load8_any<DT>(w.q.row, p.d.dt, i, a.V);
+        values8<DT>(p.t, w.p, praw, w.c, i, a.V, sh.tab, pv);
+        if (drafted) values8<DT>(p.d, w.q, qraw, w.c, i, a.V, sh.tab, qv);
         // (more of them than LDS holds: looked for among the rows again)
         const int g0 = ngone <= kGone ? 0 : st.w.cur + 1, g1 = ngone <= kGone ? ngone : n;
         for (int g = g0; g < g1; ++g) {
-          const int x = ngone <= kGone ? s_gone[g] : parent_of(a, lo, g) == st.w.cur ? a.tokens[lo + g] : -1;
+          const int x = ngone <= kGone ? s_gone[g] : parent_of<TREE>(a, lo, g) == st.w.cur ? a.tokens[lo + g] : -1;
 #pragma unroll
           for (int e = 0; e < 8; ++e) pv[e] = x == i + e ? 0.0 : pv[e];
         }
@@ -1054,7 +1072,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 2 : 3) void k_verify_pick(V
         }
       }
       if (f.at >= 0) break;
-      if (TREES && st.state == kLeft) {
+      if (SUMS && st.state == kLeft) {
         all.p += s.p;
         all.q += s.q;
         continue;
@@ -1094,7 +1112,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 2 : 3) void k_verify_pick(V
       k0 = 0;
       k1 = blocks;
     }
-    if (TREES && st.state == kLeft) {
+    if (SUMS && st.state == kLeft) {
       // S, by every wave for itself
       Sums t{};
       for (int k = lane; k < ntotals; k += 64) {
@@ -1109,7 +1127,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 2 : 3) void k_verify_pick(V
       walks = true;
       continue;
     }
-    f = locate(sh, sums, blocks, totals, ntotals, drafted, !p.t.probs, !p.d.probs, al, u);
+    f = locate<DRAFT>(sh, sums, blocks, totals, ntotals, drafted, !p.t.probs, !p.d.probs, al, u);
     if ((drafted && f.total < kLittle) || (ngone && f.total == 0.0)) {
       // nothing is left, or no more than the rounding of the rows' sums: p itself, by this workgroup
       f.at = -1;
@@ -1117,7 +1135,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREES ? 2 : 3) void k_verify_pick(V
       ngone = 0;
       continue;
     }
-    if (TREES && threadIdx.x == 0) p.pending[b].state = kDone;
+    if (SUMS && threadIdx.x == 0) p.pending[b].state = kDone;
     if (f.at < 0 || !(f.total > 0.0) || f.total == __builtin_inf()) {
       if (threadIdx.x == 0) a.out_tokens[lo + st.w.kept - 1] = -1;
       return;
@@ -1160,7 +1178,7 @@ struct VerifyLayout {
 };
 
 // Pieces of rows: as long as 4096 waves get one each, up to 16 blocks (a wave joins its sum over the lanes
-// once per piece), and of no more than kPieces to a row, which 16 lanes join without a loop (256 of them took
+// once per piece), and of no more than kPieces to a row, which its lanes join without a loop (256 of them took
 // the walk of 8 rows 17 us instead of 4). Workgroups of a sequence: 768 in all, three to a CU, with a block for each wave
 // at least (200 sequences of 5 rows of 32000: 55.0 us, 58.7 with 1024, 55.9 with 512; 64 of 9 of 131072: 84.5, 84.5, 85.6).
 VerifyLayout layout(int V, int B, int M, bool tprobs, bool drafted, bool dprobs) {
@@ -1228,14 +1246,22 @@ hipError_t launch_verify(const VerifyArgs& a, hipStream_t s) {
     p.shares = (l.blocks + p.share_blocks - 1) / p.share_blocks;
   }
   const dim3 grid(a.B * p.shares);
-  if (a.M == 0 || !a.draft || !a.parents) {
-    hipLaunchKernelGGL(k_verify_pick<false>, grid, dim3(kVerifyThreads), 0, s, p, 0, 1);
+  const int dt = a.draft && a.ddt != a.tdt ? -1 : a.tdt;
+  const auto pick = [&](auto tree, auto draft, int pass, int passes) {
+    constexpr bool TREE = decltype(tree)::value, DRAFT = decltype(draft)::value;
+    const dim3 threads(kVerifyThreads);
+    if (dt == 0) hipLaunchKernelGGL((k_verify_pick<TREE, DRAFT, 0>), grid, threads, 0, s, p, pass, passes);
+    else if (dt == 1) hipLaunchKernelGGL((k_verify_pick<TREE, DRAFT, 1>), grid, threads, 0, s, p, pass, passes);
+    else if (dt == 2) hipLaunchKernelGGL((k_verify_pick<TREE, DRAFT, 2>), grid, threads, 0, s, p, pass, passes);
+    else if constexpr (DRAFT) hipLaunchKernelGGL((k_verify_pick<TREE, true, -1>), grid, threads, 0, s, p, pass, passes);
     return hipGetLastError();
-  }
-  for (int pass = 0; pass < kPasses; ++pass) {
-    hipLaunchKernelGGL(k_verify_pick<true>, grid, dim3(kVerifyThreads), 0, s, p, pass, kPasses);
-    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  }
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+  if (!a.parents) return a.draft ? pick(No{}, Yes{}, 0, 1) : pick(No{}, No{}, 0, 1);
+  if (!a.draft || a.M == 0) return pick(Yes{}, No{}, 0, 1);
+  for (int pass = 0; pass < kPasses; ++pass)
+    if (const hipError_t e = pick(Yes{}, Yes{}, pass, kPasses); e != hipSuccess) return e;
   return hipGetLastError();
 }
 
