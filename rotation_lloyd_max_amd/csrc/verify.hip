@@ -657,7 +657,8 @@ __device__ __forceinline__ bool tried_before(const VerifyArgs& a, const WalkShar
   return found;
 }
 
-// Rows [w0, w1) into LDS: their tokens' probabilities under their parents, 16 lanes a row. kept: where a
+// Rows [w0, w1) into LDS: their tokens' probabilities under their parents, some lanes a row (trees, which have
+// more rows, 8: 24 rows in one round; 8 trees of these 21.7 -> 20.6 us). kept: where a
 // launch before has left them (load), or where they are left for the next (null: not).
 template <bool TREE, bool DRAFT>
 __device__ __forceinline__ void fill_window(const VerifyParams& p, WalkShared& sh, int lo, int w0, int w1, double T, RowInfo* kept,
