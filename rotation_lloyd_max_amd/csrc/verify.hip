@@ -19,14 +19,14 @@
 // comes last finds the token. Where siblings are tried against a draft, S is such a sum too: the last
 // workgroup walks on with it, and the next launch of k_verify_pick sums what the walk needs then. kPasses - 1 more
 // launches follow, in which sequences that are done end at once; what is still open in the last one its last
-// workgroup sums alone (20 rows of 8 sequences, 60000 tokens: 105 us when the first launch's did so, 57 now).
+// workgroup sums alone (20 rows of 8 sequences, 60000 tokens: 105 us when the first launch's did so, 52 now).
 //
 // Bounds and figures. 64 sequences of 9 rows, 131072 tokens in bf16, a draft: k_verify_stats reads 285 MB in 54 us,
-// 5.3 TB/s, bound by memory; k_verify_pick, 33 us, reads 64 of these rows again: 5 us for the walk, 1 for the row's
-// constants, 17 for the sums (vector instructions: about 36 for a token of both rows), 5 for the meeting and the last
-// block. One sequence of 4 rows, 32000 tokens: 15.2 us in a stream of launches, 4.6 of them launches and the rows'
-// sums, 3.1 the walk, 0.9, 3.0 the sums, 1.7 until the block is found, 1.8 the token: the latency of some ten loads
-// that wait for each other and of fp64 chains in waves that have a SIMD to themselves.
+// 5.3 TB/s, bound by memory; k_verify_pick, 29 us, reads 64 of these rows again: 5 us for the walk, 1 for the row's
+// constants, 15 for the sums (vector instructions: about 36 for a token of both rows), 5 for the meeting and the last
+// block. One sequence of 4 rows, 32000 tokens: 14.0 us in a stream of launches, 4.6 of them launches and the rows'
+// sums, about 3 the walk, 3 the sums, 1.5 until the block is found, 1.5 the token: the latency of some ten loads that
+// wait for each other and of fp64 chains in waves that have a SIMD to themselves.
 #include <type_traits>
 
 #include "internal.hpp"
@@ -1181,7 +1181,8 @@ struct VerifyLayout {
 // Pieces of rows: as long as 4096 waves get one each, up to 16 blocks (a wave joins its sum over the lanes
 // once per piece), and of no more than kPieces to a row, which its lanes join without a loop (256 of them took
 // the walk of 8 rows 17 us instead of 4). Workgroups of a sequence: 768 in all, three to a CU, with a block for each wave
-// at least (200 sequences of 5 rows of 32000: 55.0 us, 58.7 with 1024, 55.9 with 512; 64 of 9 of 131072: 84.5, 84.5, 85.6).
+// at least (200 sequences of 5 rows of 32000: 55.0 us, 58.7 with 1024, 55.9 with 512; 64 of 9 of 131072: 84.5, 84.5, 85.6;
+// before the kernels were told apart).
 VerifyLayout layout(int V, int B, int M, bool tprobs, bool drafted, bool dprobs) {
   VerifyLayout l{};
   l.blocks = (V + kBlockElems - 1) / kBlockElems;
