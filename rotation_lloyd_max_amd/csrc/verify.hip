@@ -7,11 +7,11 @@
 // out of p one by one. Children have larger indices than their parents and are tried in ascending
 // order: one ascending scan of a sequence's rows is the walk.
 //
-// Where a rounding matters. A test of a drafted token compares two numbers: single precision's errors
-// (1e-7) change it once in millions. The new token is found at u sum(w) in the cumulative sum of w: each of
+// Where a rounding matters. A test of a row's first child compares two numbers: single precision's errors
+// (1e-7) change it once in millions. Later siblings are tested against a small S. The new token is found at u sum(w) in the cumulative sum of w: each of
 // its 10^5 borders that is off by 10^-8 gives a neighbour now and then, so w, its sums and the rows' sums
-// that it is made of are fp64. The rows' sums that the tests need, of all rows, are of exponentials in
-// fp32; the pass that sums w sums the row that it comes from once more, in fp64 (see Sums).
+// that it is made of are fp64. The rows' sums that the first tests need, of all rows, are of exponentials
+// in fp32; the passes that sum S and w sum their row once more, in fp64 (see Sums), and later siblings take that.
 //
 // Launches. k_verify_stats: largest value and sum of exponentials of every row of logits that can be
 // looked at, a wave per piece of a row. k_verify_pick: each workgroup of a sequence joins the pieces and walks
@@ -83,6 +83,7 @@ struct Sums {
 // A walk that has come to a row.
 struct Walk {
   double al, S;
+  double fp, fq;  // 1 / P and 1 / Q of cur by those of k_verify_stats, once its sums are made in fp64 (till then 1)
   int cur, kept, tried;  // tried: the last child of cur that went (0: none)
   int next;              // the first row that it has not looked at
   int known;             // the rows before it are in VerifyParams::rows (trees with a draft)
@@ -574,8 +575,12 @@ __device__ __forceinline__ int largest_of(const VerifyParams& p, int row) {
 
 // Weights up to here count as nothing: masked tokens come out as about 2^-1000, not 0.
 constexpr double kNothing = 1e-280;
-// So much left of p, or less, is nothing: the roundings of fp64 sums of 10^5 terms are below a tenth of it.
-constexpr double kLittle = 1e-9;
+// So much left of p, or less, is nothing: the rounding of the sums of p and of a q, ten times over. Sums of 10^5 terms
+// are off by 10^-15 or so, of logits the exponentials by 2 10^-14 too, and by 2^-52 of the exponent.
+__device__ __forceinline__ double little(bool probs) { return probs ? 1e-14 : 1e-12; }
+// With less left than this the tokens that the rows' fp32 sums put on the wrong side of p = a q (10^-6 of them) may
+// matter: the sums are made once more, with P and Q as they were found (a sequence comes here as often as that).
+constexpr double kAgain = 1e-4;
 
 // One side of what the new token is drawn from (or S is summed over): values p~ of Sums.
 struct WeightSide {
@@ -596,7 +601,7 @@ __device__ __forceinline__ double uniform(double x) {
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ Walk uniform(const Walk& w) {
-  return Walk{uniform(w.al), uniform(w.S), uniform(w.cur), uniform(w.kept), uniform(w.tried), uniform(w.next), uniform(w.known)};
+  return Walk{uniform(w.al), uniform(w.S), uniform(w.fp), uniform(w.fq), uniform(w.cur), uniform(w.kept), uniform(w.tried), uniform(w.next), uniform(w.known)};
 }
 
 __device__ __forceinline__ WeightSide weight_side(const Side& s, int row, const Dist& d, double T, const double* tab) {
@@ -658,7 +663,7 @@ __device__ __forceinline__ bool tried_before(const VerifyArgs& a, const WalkShar
 }
 
 // Rows [w0, w1) into LDS: their tokens' probabilities under their parents, some lanes a row (trees, which have
-// more rows, 8: 24 rows in one round; 8 trees of these 21.7 -> 20.6 us). kept: where a
+// more rows, 8: 24 rows at once; 8 trees of these 21.7 -> 20.6 us). kept: where a
 // launch before has left them (load), or where they are left for the next (null: not).
 template <bool TREE, bool DRAFT>
 __device__ __forceinline__ void fill_window(const VerifyParams& p, WalkShared& sh, int lo, int w0, int w1, double T, RowInfo* kept,
@@ -760,7 +765,8 @@ __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int 
     w.next = r + 1;
     const RowInfo& row = sh.row[r - w0];
     const int x = row.token;
-    const double u = row.u, px = row.px, qx = row.qx;
+    // (where siblings have gone S may be as small as the rows' sums are off)
+    const double u = row.u, px = SUMS ? row.px * w.fp : row.px, qx = SUMS ? row.qx * w.fq : row.qx;
     bool yes, taken = false;
     if (greedy) {
       yes = x == largest;
@@ -775,7 +781,7 @@ __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int 
         a.out_tokens[lo + w.kept - 1] = x;
         a.path[lo + w.kept] = r;
       }
-      w = Walk{0.0, 1.0, r, w.kept + 1, 0, r + 1, w.known};
+      w = Walk{0.0, 1.0, 1.0, 1.0, r, w.kept + 1, 0, r + 1, w.known};
       if (greedy) largest = largest_of(p, lo + r);
     } else {
       w.tried = r;
@@ -944,10 +950,10 @@ __global__ __launch_bounds__(kVerifyThreads, TREE && DRAFT ? 2 : 3) void k_verif
     }
     return;
   }
-  const double T = uniform(static_cast<double>(temperature));
+  const double T = uniform(static_cast<double>(temperature)), nothing = little(p.t.probs && p.d.probs);
   const float u = a.uniforms[lo];
   int held = -1;
-  if (!SUMS || !pass) st.w = Walk{0.0, 1.0, 0, 1, 0, 1, 0};
+  if (!SUMS || !pass) st.w = Walk{0.0, 1.0, 1.0, 1.0, 0, 1, 0, 1, 0};
   if constexpr (!SUMS) {
     walk<TREE, DRAFT>(p, sh, lo, n, T, writes, st.w, held, false);
     st.w = uniform(st.w);
@@ -960,7 +966,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREE && DRAFT ? 2 : 3) void k_verif
   int k1 = k0 + p.share_blocks < blocks ? k0 + p.share_blocks : blocks;
   bool alone = false;              // the others have ended
   bool walks = SUMS && !pass, fresh = true;  // to walk on; to begin with the row that the walk has come to
-  bool drafted = false;
+  bool drafted = false, exact = false;  // exact: rho is made of sums in fp64
   int ngone = 0;
   double al = 0.0, rho = 0.0;
   Weights w;
@@ -1011,6 +1017,8 @@ __global__ __launch_bounds__(kVerifyThreads, TREE && DRAFT ? 2 : 3) void k_verif
     w.q = w.p;
     if (drafted) w.q = weight_side(p.d, row, dq, T, sh.tab);
     rho = al * (w.q.inv / w.p.inv);
+    if (SUMS) rho *= st.w.fq / st.w.fp;
+    exact = (p.t.probs || st.w.fp != 1.0) && (p.d.probs || st.w.fq != 1.0);
     // tokens that were taken out of p
     ngone = 0;
     if (!DRAFT && st.w.tried) {
@@ -1122,14 +1130,28 @@ __global__ __launch_bounds__(kVerifyThreads, TREE && DRAFT ? 2 : 3) void k_verif
         t.P += shared_load(&totals[k].P);
         t.Q += shared_load(&totals[k].Q);
       }
+      __syncthreads();  // (they may be written again)
       t = Sums{wave_sum(t.p), wave_sum(t.q), wave_sum(t.P), wave_sum(t.Q)};
+      if (!p.t.probs) st.w.fp = 1.0 / (t.P * w.p.inv);
+      if (!p.d.probs) st.w.fq = 1.0 / (t.Q * w.q.inv);
       const double left = (p.t.probs ? t.p : t.p / t.P) - al * (p.d.probs ? t.q : t.q / t.Q);
-      st.w.S = left < kLittle ? 0.0 : left;
+      if (left < kAgain && !exact) {
+        exact = true;
+        rho = al * ((w.q.inv * st.w.fq) / (w.p.inv * st.w.fp));
+        continue;
+      }
+      st.w.S = left < nothing ? 0.0 : left;
       walks = true;
       continue;
     }
     f = locate<DRAFT>(sh, sums, blocks, totals, ntotals, drafted, !p.t.probs, !p.d.probs, al, u);
-    if ((drafted && f.total < kLittle) || (ngone && f.total == 0.0)) {
+    if (DRAFT && drafted && f.total < kAgain && !exact) {
+      exact = true;
+      rho = al * (f.rq / f.rp);
+      f.at = -1;
+      continue;
+    }
+    if ((drafted && f.total < nothing) || (ngone && f.total == 0.0)) {
       // nothing is left, or no more than the rounding of the rows' sums: p itself, by this workgroup
       f.at = -1;
       drafted = false;

@@ -436,3 +436,41 @@ def test_rows_gigabytes_apart():
 def test_as_many_sequences_as_there_may_be(ddt):
     check(case(43, 65536, 2, 5, "bf16", ddt))
     check(case(44, 3000, 3, 130, "fp16", ddt, tree=True, temperature="mixed"))
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("kinds", [("logits", "probabilities"), ("probabilities", "logits")])
+@pytest.mark.parametrize("tdt,ddt", [("bf16", "fp32"), ("fp32", "fp32"), ("fp16", "bf16")])
+def test_logits_against_probabilities(tdt, ddt, kinds, tree):
+    for seed, V in ((45, 100), (46, 5000)):
+        c = case(seed, 9, 9, V, tdt, ddt, tree=tree, noise=1.5, temperature="mixed")
+        for name, kind, dt in zip(("target", "draft"), kinds, (tdt, ddt)):
+            c[name + "_kind"] = kind
+            if kind == "probabilities":
+                c[name] = torch.softmax(c[name].float(), -1).to(DTS[dt])
+        check(c)
+
+
+@pytest.mark.parametrize("kind,dt", [("logits", "fp32"), ("logits", "bf16"), ("probabilities", "fp32")])
+@pytest.mark.parametrize("gone", [1, 2, 3, 4, 5])
+def test_little_left_after_siblings_the_draft_would_hardly_draw(kind, dt, gone):
+    # one token has nearly all of p and of q: each other sibling leaves a fortieth of S, 1e-8 after the last
+    B, V, n = 64, 300, gone + 3
+    c = case(47 + gone, B, n, V, "fp32", "fp32", ragged=False, tree=True, spread=0.5, noise=0.1)
+    c["parents"] = np.zeros(B * n, np.int64)
+    c["target"][:, 7], c["draft"][:, 7] = 10.4, 9.6
+    for name in ("target", "draft"):
+        if kind == "probabilities":
+            c[name] = torch.softmax(c[name].double(), -1).float()
+        c[name] = c[name].to(DTS[dt])
+        c[name + "_kind"] = kind
+    p, q = (ost.distribution(as_f64(c[x])[0], kind, 1.0) for x in ("target", "draft"))
+    assert p[7] > q[7] > 0.97
+    for b in range(B):
+        p, q = (ost.distribution(as_f64(c[x])[b * n], kind, 1.0) for x in ("target", "draft"))
+        c["tokens"][b * n + 1:b * n + 1 + gone] = np.argsort(p / q)[:gone]       # none of these stays
+    c["tokens"][1 + gone::n] = 7
+    c["uniforms"][1::n] = 0.999
+    c["uniforms"][1 + gone::n] = np.linspace(0.9, 1.1, B)
+    got = check(c)
+    assert (got.kept == 2).sum() > B // 4 and (got.kept == 1).sum() > B // 16
