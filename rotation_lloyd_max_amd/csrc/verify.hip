@@ -24,7 +24,7 @@
 // Bounds and figures. 64 sequences of 9 rows, 131072 tokens in bf16, a draft: k_verify_stats reads 285 MB in 54 us,
 // 5.3 TB/s, bound by memory; k_verify_pick, 29 us, reads 64 of these rows again: 5 us for the walk, 1 for the row's
 // constants, 15 for the sums (vector instructions: about 36 for a token of both rows), 5 for the meeting and the last
-// block. One sequence of 4 rows, 32000 tokens: 14.0 us in a stream of launches, 4.6 of them launches and the rows'
+// block. One sequence of 4 rows, 32000 tokens: 14.2 us in a stream of launches, 4.6 of them launches and the rows'
 // sums, about 3 the walk, 3 the sums, 1.5 until the block is found, 1.5 the token: the latency of some ten loads that
 // wait for each other and of fp64 chains in waves that have a SIMD to themselves.
 #include <type_traits>
