@@ -98,7 +98,8 @@ enum { TQ_TARGET_PROBS = 1, TQ_DRAFT_PROBS = 2 };
  * the others drafted tokens, row i following row parents[i] < i (NULL: row i - 1). Row r of `target`
  * is the target's distribution of the token after r: softmax(x / temperature[b]), or the values as
  * they are with TQ_TARGET_PROBS. Row r of `draft` is the distribution that the tokens of r's children
- * were drawn from; rows without children are not read. draft NULL: the drafted tokens are fixed (point
+ * were drawn from, softmax(x / temperature[b]) or the values with TQ_DRAFT_PROBS; rows without children
+ * are not read. draft NULL: the drafted tokens are fixed (point
  * masses), such as the target's own most likely ones or tokens looked up in the text.
  * From c = the root on, with p, q of row c, a = 0, S = 1, the children x of c in their order, each
  * with its number u = uniforms[its row] in [0, 1):
@@ -121,10 +122,11 @@ enum { TQ_TARGET_PROBS = 1, TQ_DRAFT_PROBS = 2 };
  * are looked at and are NaN, or whose w sum to infinity or to 0 throughout; greedy: NaN, +infinity or no
  * value above 0 resp. -infinity), none of its children stays and the new token is -1.
  * A row's first child is tested with sums of fp32 exponentials: its u q and p are off by 2.6e-5 of themselves at
- * most, by 1e-6 as a rule, and so is, without a draft, S, which is 1 less the p of the tried, by that much of 1. With a
- * draft S and the tests of later siblings, and always the new token, are made with sums of fp64 exponentials: a border of the cumulative sum of w lies where the definition has it to about 1e-12 of the sum of
- * p + a q. With a draft, sum(w) or S below 1e-12 (both sides probabilities: 1e-14) is nothing left: no sibling stays,
- * the new token is one of p. Weights below 1e-280 of the row's largest are 0. Deterministic.
+ * most, by 1e-6 as a rule, and so is, without a draft, S, which is 1 less the p of the tried, by that much of 1. With
+ * a draft S and the tests of later siblings, and always the new token, are made with sums of fp64 exponentials: a
+ * border of the cumulative sum of w lies where the definition has it to about 1e-12 of the sum of p + a q. With a
+ * draft, sum(w) or S below 1e-12 (both sides probabilities: 1e-14) is nothing left: no sibling stays, the new token
+ * is one of p. Weights below 1e-280 of the row's largest are 0. Deterministic.
  * Workspace: tq_verify_workspace bytes, 256-byte aligned; its contents need not be kept, and two calls
  * that can run at the same time need one each. vocab in [1, 2^28], B at most 65536, M at most 2^24;
  * offsets non-decreasing, offsets[0] = 0, at most M. */
