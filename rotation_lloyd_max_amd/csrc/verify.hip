@@ -1270,7 +1270,8 @@ hipError_t launch_verify(const VerifyArgs& a, hipStream_t s) {
     p.shares = (l.blocks + p.share_blocks - 1) / p.share_blocks;
   }
   const dim3 grid(a.B * p.shares);
-  const int dt = a.draft && a.ddt != a.tdt ? -1 : a.tdt;
+  // (no rows: nothing is read of either, and the kernels without a draft are of one type)
+  const int dt = a.M > 0 && a.draft && a.ddt != a.tdt ? -1 : a.tdt;
   const auto pick = [&](auto tree, auto draft, int pass, int passes) {
     constexpr bool TREE = decltype(tree)::value, DRAFT = decltype(draft)::value;
     const dim3 threads(kVerifyThreads);
@@ -1278,6 +1279,7 @@ hipError_t launch_verify(const VerifyArgs& a, hipStream_t s) {
     else if (dt == 1) hipLaunchKernelGGL((k_verify_pick<TREE, DRAFT, 1>), grid, threads, 0, s, p, pass, passes);
     else if (dt == 2) hipLaunchKernelGGL((k_verify_pick<TREE, DRAFT, 2>), grid, threads, 0, s, p, pass, passes);
     else if constexpr (DRAFT) hipLaunchKernelGGL((k_verify_pick<TREE, true, -1>), grid, threads, 0, s, p, pass, passes);
+    else return hipErrorInvalidValue;
     return hipGetLastError();
   };
   using Yes = std::true_type;
