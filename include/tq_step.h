@@ -119,8 +119,9 @@ enum { TQ_TARGET_PROBS = 1, TQ_DRAFT_PROBS = 2 };
  *   path         [M]  from offsets[b]: the rows that stay in the sequence, 0 first; -1 behind them
  * Rows behind offsets[B] are left as they were. Logits of -infinity are probabilities of 0. Where a row
  * of c's makes no distribution (logits with NaN, +infinity or nothing but -infinity; probabilities that
- * are looked at and are NaN, or whose w sum to infinity or to 0 throughout; greedy: NaN, +infinity or no
- * value above 0 resp. -infinity), none of its children stays and the new token is -1.
+ * are looked at, a child's when it is tested and all of the row when S or w is summed, and are NaN or infinity;
+ * a target's that are 0 throughout; greedy: NaN, +infinity or no value above 0 resp. -infinity), none of its
+ * children stays (but one that stayed before the value was looked at) and the new token is -1.
  * A row's first child is tested with sums of fp32 exponentials: its u q and p are off by 2.6e-5 of themselves at
  * most, by 1e-6 as a rule, and so is, without a draft, S, which is 1 less the p of the tried, by that much of 1. With
  * a draft S and the tests of later siblings, and always the new token, are made with sums of fp64 exponentials: a

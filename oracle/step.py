@@ -135,6 +135,9 @@ def verify(target, tokens, uniforms, offsets, draft=None, parents=None, temperat
                     if q is None:
                         bad = True
                         continue
+                if not np.isfinite(p[x]) or (q is not None and not np.isfinite(q[x])):
+                    bad = True  # (probabilities: of logits all are finite)
+                    continue
                 # S is what is left of p's sum (1 at first): p / S against q
                 left, right = (u * S * q[x], p[x]) if draft is not None else (u * S, p[x])
                 if left != right:
@@ -154,6 +157,8 @@ def verify(target, tokens, uniforms, offsets, draft=None, parents=None, temperat
             out[lo + k - 1], path[lo + k] = tokens[lo + found], found
             at, k = found, k + 1
         if bad:
+            new = -1
+        elif q is not None and not np.isfinite(q).all():
             new = -1
         else:
             w = np.maximum(p, 0.0)

@@ -686,6 +686,7 @@ __device__ __forceinline__ void fill_window(const VerifyParams& p, WalkShared& s
         if (drafted) xd = load_any(p.d.data + (lo + up) * p.d.stride, p.d.dt, x);
         i.p = dist_of<LANES>(p, p.t, lo + up, c, sh.tab);
         i.px = probability(p.t, i.p, c, xt, sh.tab);
+        if (!(i.px < __builtin_inf())) i.px = __builtin_nan("");  // no distribution: it stays under no number
         if (drafted) {
           i.q = dist_of<LANES>(p, p.d, lo + up, c, sh.tab);
           i.qx = probability(p.d, i.q, c, xd, sh.tab);
@@ -744,6 +745,7 @@ __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int 
           if (__ballot(row) >> run & 1) {
             w.tried = w.next;
             w.al = 1.0;
+            if (!DRAFT) w.S -= sh.row[w.next - w0].px;
           }
           w.next = n;
         }
@@ -1004,7 +1006,8 @@ __global__ __launch_bounds__(kVerifyThreads, TREE && DRAFT ? 2 : 3) void k_verif
         dp = dist_of<64>(p, p.t, row, w.c, sh.tab);
         if (drafted) dq = dist_of<64>(p, p.d, row, w.c, sh.tab);
       }
-      if (st.state == kToken && (dp.zinv != dp.zinv || (drafted && dq.zinv != dq.zinv))) res = -1;  // no distribution
+      // no distribution: of logits, or a tried token's probability (with a draft w has it too)
+      if (st.state == kToken && (dp.zinv != dp.zinv || (drafted && dq.zinv != dq.zinv) || (!DRAFT && st.w.S != st.w.S))) res = -1;
     }
     if (res != -2) {
       if (writes && threadIdx.x == 0) {

@@ -25,3 +25,58 @@ def test_a_step_of_no_rows_keeps_nothing(tdt, ddt, tree):
     torch.cuda.synchronize()
     assert rc == 0 and kept.tolist() == [0, 0, 0]
     assert out.tolist() == path.tolist() == [1234, 1234]
+
+
+def steady(n, drafted, tree):
+    """A sequence of n rows of even probabilities over 50 tokens, row i drafting token i % 50; 0.01 as its number
+    lets a row stay, 1.0 turns it away (and a draft's too, whose probabilities are the same)."""
+    even = torch.full((n, 50), 0.02)
+    return dict(target=even, tokens=np.arange(n) % 50, uniforms=np.full(n, 0.01, np.float32), offsets=np.array([0, n]),
+                draft=even.clone() if drafted else None, parents=np.maximum(np.arange(n) - 1, 0) if tree else None, temperature=None,
+                target_kind="probabilities", draft_kind="probabilities")
+
+
+def answers(c):
+    got = tq.verify(**on_gpu(c))
+    kept, tokens, path, _ = reference(c)
+    torch.cuda.synchronize()
+    assert got.kept.tolist() == kept.tolist() and got.path.tolist() == path.tolist()
+    assert got.tokens.tolist() == tokens.tolist()
+    k = got.kept.item()
+    return k, got.tokens[k - 1].item()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("drafted", [False, True])
+@pytest.mark.parametrize("tree", [False, True])
+def test_a_drafted_tokens_probability_is_none(bad, drafted, tree):
+    # the row makes no distribution: its child does not stay, whatever its number, and the new token is -1
+    for n, row in ((2, 0), (6, 3), (70, 64), (300, 254), (300, 255), (300, 256), (300, 280)):
+        for name in ("target", "draft") if drafted else ("target",):
+            for u in (0.01, 0.0, 1.0):
+                c = steady(n, drafted, tree)
+                c[name][row, (row + 1) % 50] = bad
+                c["uniforms"][row + 1] = u
+                assert answers(c) == (row + 1, -1)
+    # at a token that nobody looks at
+    c = steady(6, drafted, tree)
+    c["target"][2, 9] = bad
+    k, new = answers(c)
+    assert k == 6 and new >= 0
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("drafted", [False, True])
+def test_one_of_several_siblings_probability_is_none(bad, drafted):
+    for place in range(4):
+        c = steady(5, drafted, True)
+        c["parents"] = np.zeros(5, np.int64)
+        c["target"][0, 1 + place] = bad
+        c["uniforms"][1:] = 1.0
+        assert answers(c) == (1, -1)       # all are turned away, the bad one among them
+        if place:
+            c["uniforms"][1] = 0.01
+            assert answers(c)[0] == 2      # the first stays: the others are not looked at
+        c["uniforms"][1:] = 1.0
+        c["uniforms"][4] = 0.0             # the last would stay
+        assert answers(c) == (1, -1)
