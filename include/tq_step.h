@@ -123,7 +123,7 @@ enum { TQ_TARGET_PROBS = 1, TQ_DRAFT_PROBS = 2 };
  * a target's that are 0 throughout; greedy: NaN, +infinity or no value above 0 resp. -infinity), none of its
  * children stays (but one that stayed before the value was looked at) and the new token is -1.
  * A row's first child is tested with sums of fp32 exponentials: its u q and p are off by 2.6e-5 of themselves at
- * most, by 1e-6 as a rule, and so is, without a draft, S, which is 1 less the p of the tried, by that much of 1. With
+ * most, by 1e-6 as a rule; in trees without a draft, tests that these sums leave open are made with fp64 ones. With
  * a draft S and the tests of later siblings, and always the new token, are made with sums of fp64 exponentials: a
  * border of the cumulative sum of w lies where the definition has it to about 1e-12 of the sum of p + a q. With a
  * draft, sum(w) or S below 1e-12 (both sides probabilities: 1e-14) is nothing left: no sibling stays, the new token

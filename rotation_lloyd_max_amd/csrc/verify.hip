@@ -82,7 +82,7 @@ struct Sums {
 
 // A walk that has come to a row.
 struct Walk {
-  double al, S;
+  double al, S;   // (without a draft al is the p of those that went, by the sums of k_verify_stats)
   double fp, fq;  // 1 / P and 1 / Q of cur by those of k_verify_stats, once its sums are made in fp64 (till then 1)
   int cur, kept, tried;  // tried: the last child of cur that went (0: none)
   int next;              // the first row that it has not looked at
@@ -582,6 +582,10 @@ __device__ __forceinline__ double little(bool probs) { return probs ? 1e-14 : 1e
 // matter: the sums are made once more, with P and Q as they were found (a sequence comes here as often as that).
 constexpr double kAgain = 1e-4;
 
+// So close, relative to what they are made of, two numbers may be for the rows' fp32 sums to tell them apart (2.6e-5
+// for both sides together).
+constexpr double kNear = 3e-5;
+
 // One side of what the new token is drawn from (or S is summed over): values p~ of Sums.
 struct WeightSide {
   const char* row;
@@ -701,9 +705,28 @@ __device__ __forceinline__ void fill_window(const VerifyParams& p, WalkShared& s
   __syncthreads();
 }
 
+// 1 / P of a row of logits by a sum of fp64 exponentials, relative to that of k_verify_stats; by all threads of the
+// workgroup. For a test that the rows' fp32 sums cannot decide: one in some 10^4, and where siblings that went have left
+// little of p.
+template <int DT>
+__device__ __forceinline__ double row_factor(const Side& s, int row, const Dist& d, double T, int V, WalkShared& sh) {
+  const WeightSide w = weight_side(s, row, d, T, sh.tab);
+  double sum = 0.0, v[8];
+  for (int i = 8 * static_cast<int>(threadIdx.x); i < V; i += 8 * kVerifyThreads) {
+    values8<DT>(s, w, load8_any<DT>(w.row, s.dt, i, V), w.e.c, i, V, sh.tab, v);
+    sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+  }
+  sum = wave_sum(sum);
+  if ((threadIdx.x & 63) == 0) sh.red[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  sum = (sh.red[0] + sh.red[1]) + (sh.red[2] + sh.red[3]);
+  __syncthreads();
+  return 1.0 / (sum * w.inv);
+}
+
 // Walks on, all waves of the workgroup alike, until S of cur is needed (true) or no child stays (false).
 // `writes`: this workgroup writes the tokens that stay. held: the window in LDS, -1 for none. later: not the first launch.
-template <bool TREE, bool DRAFT>
+template <bool TREE, bool DRAFT, int DT>
 __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int lo, int n, double T, bool writes, Walk& w, int& held,
                                      bool later) {
   constexpr bool SUMS = TREE && DRAFT;
@@ -768,7 +791,8 @@ __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int 
     const RowInfo& row = sh.row[r - w0];
     const int x = row.token;
     // (where siblings have gone S may be as small as the rows' sums are off)
-    const double u = row.u, px = SUMS ? row.px * w.fp : row.px, qx = SUMS ? row.qx * w.fq : row.qx;
+    const double u = row.u, qx = SUMS ? row.qx * w.fq : row.qx;
+    double px = row.px * w.fp;
     bool yes, taken = false;
     if (greedy) {
       yes = x == largest;
@@ -776,7 +800,12 @@ __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int 
       yes = w.S > 0.0 && u * w.S * qx < px - w.al * qx;  // (nothing left: the difference is rounding)
     } else {
       taken = TREE && w.tried && tried_before(a, sh, lo, n, w.cur, r, x);
-      yes = u * w.S < (taken ? 0.0 : px);
+      if (!p.t.probs && w.fp == 1.0 && !taken && __builtin_fabs(u * w.S - px) < kNear * (u * w.al + px)) {
+        w.fp = row_factor<DT>(p.t, lo + w.cur, row.p, T, a.V, sh);
+        px = row.px * w.fp;
+        w.S = 1.0 - w.al * w.fp;
+      }
+      yes = !taken && u * w.S < px;
     }
     if (yes) {
       if (writes && threadIdx.x == 0) {
@@ -797,6 +826,7 @@ __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int 
         if (more) return true;
       } else if (!taken) {
         w.S -= px;
+        w.al += row.px;
       }
     }
   }
@@ -957,7 +987,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREE && DRAFT ? 2 : 3) void k_verif
   int held = -1;
   if (!SUMS || !pass) st.w = Walk{0.0, 1.0, 1.0, 1.0, 0, 1, 0, 1, 0};
   if constexpr (!SUMS) {
-    walk<TREE, DRAFT>(p, sh, lo, n, T, writes, st.w, held, false);
+    walk<TREE, DRAFT, DT>(p, sh, lo, n, T, writes, st.w, held, false);
     st.w = uniform(st.w);
     st.state = kToken;
   }
@@ -976,7 +1006,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREE && DRAFT ? 2 : 3) void k_verif
   double pv[8], qv[8];
   // Begins with the row that the walk has come to; false: the token needs no sums, and is written.
   auto begin = [&]() TQ_INLINE {
-    al = st.w.al;
+    al = DRAFT ? st.w.al : 0.0;
     int res = -2;  // a token that needs no sums
     if (st.state == kToken) {
       if (writes) {
@@ -1043,7 +1073,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREE && DRAFT ? 2 : 3) void k_verif
   // instruction cache then, where a copy of it took 2 us to come.
   for (;;) {
     if (SUMS && walks) {
-      st.state = walk<TREE, DRAFT>(p, sh, lo, n, T, writes, st.w, held, pass > 0) ? kLeft : kToken;
+      st.state = walk<TREE, DRAFT, DT>(p, sh, lo, n, T, writes, st.w, held, pass > 0) ? kLeft : kToken;
       st.w = uniform(st.w);
       walks = false;
       fresh = true;
