@@ -122,12 +122,10 @@ enum { TQ_TARGET_PROBS = 1, TQ_DRAFT_PROBS = 2 };
  * are looked at, a child's when it is tested and all of the row when S or w is summed, and are NaN or infinity;
  * a target's that are 0 throughout; greedy: NaN, +infinity or no value above 0 resp. -infinity), none of its
  * children stays (but one that stayed before the value was looked at) and the new token is -1.
- * A row's first child is tested with sums of fp32 exponentials: its u q and p are off by 2.6e-5 of themselves at
- * most, by 1e-6 as a rule; in trees without a draft, tests that these sums leave open are made with fp64 ones. With
- * a draft S and the tests of later siblings, and always the new token, are made with sums of fp64 exponentials: a
- * border of the cumulative sum of w lies where the definition has it to about 1e-12 of the sum of p + a q. With a
- * draft, sum(w) or S below 1e-12 (both sides probabilities: 1e-14) is nothing left: no sibling stays, the new token
- * is one of p. Weights below 1e-280 of the row's largest are 0. Deterministic.
+ * Tests are as with sums of fp64 exponentials: u S q and p - a q (u S and p) are told apart where they differ by more
+ * than about 1e-12 of what they are made of. A border of the cumulative sum of w lies where the definition has it to
+ * about 1e-12 of the sum of p + a q. With a draft, sum(w) or S below 1e-12 (both sides probabilities: 1e-14) is nothing
+ * left: no sibling stays, the new token is one of p. Weights below 1e-280 of the row's largest are 0. Deterministic.
  * Workspace: tq_verify_workspace bytes, 256-byte aligned; its contents need not be kept, and two calls
  * that can run at the same time need one each. vocab in [1, 2^28], B at most 65536, M at most 2^24;
  * offsets non-decreasing, offsets[0] = 0, at most M. */

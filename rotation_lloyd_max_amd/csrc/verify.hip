@@ -8,7 +8,7 @@
 // order: one ascending scan of a sequence's rows is the walk.
 //
 // Where a rounding matters. A test of a row's first child compares two numbers: single precision's errors
-// (1e-7) change it once in millions. Later siblings are tested against a small S. The new token is found at u sum(w) in the cumulative sum of w: each of
+// (1e-6) matter where they are that close, and then the row is summed in fp64 (row_factors). Later siblings are tested against a small S. The new token is found at u sum(w) in the cumulative sum of w: each of
 // its 10^5 borders that is off by 10^-8 gives a neighbour now and then, so w, its sums and the rows' sums
 // that it is made of are fp64. The rows' sums that the first tests need, of all rows, are of exponentials
 // in fp32; the passes that sum S and w sum their row once more, in fp64 (see Sums), and later siblings take that.
@@ -586,6 +586,11 @@ constexpr double kAgain = 1e-4;
 // for both sides together).
 constexpr double kNear = 3e-5;
 
+__device__ __forceinline__ bool near_border(double l, double r) {  // (single precision is enough to see it)
+  const float x = static_cast<float>(l), y = static_cast<float>(r);
+  return __builtin_fabsf(x - y) < static_cast<float>(kNear) * (x + y);
+}
+
 // One side of what the new token is drawn from (or S is summed over): values p~ of Sums.
 struct WeightSide {
   const char* row;
@@ -705,23 +710,33 @@ __device__ __forceinline__ void fill_window(const VerifyParams& p, WalkShared& s
   __syncthreads();
 }
 
-// 1 / P of a row of logits by a sum of fp64 exponentials, relative to that of k_verify_stats; by all threads of the
-// workgroup. For a test that the rows' fp32 sums cannot decide: one in some 10^4, and where siblings that went have left
-// little of p.
-template <int DT>
-__device__ __forceinline__ double row_factor(const Side& s, int row, const Dist& d, double T, int V, WalkShared& sh) {
-  const WeightSide w = weight_side(s, row, d, T, sh.tab);
-  double sum = 0.0, v[8];
-  for (int i = 8 * static_cast<int>(threadIdx.x); i < V; i += 8 * kVerifyThreads) {
-    values8<DT>(s, w, load8_any<DT>(w.row, s.dt, i, V), w.e.c, i, V, sh.tab, v);
-    sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+// 1 / P and 1 / Q of the row that `r` follows by sums of fp64 exponentials, relative to those of k_verify_stats; by all
+// threads of the workgroup. For a test that the rows' fp32 sums cannot decide: one in some 10^4, and where siblings
+// that went have left little of p.
+template <bool DRAFT, int DT>
+__device__ __forceinline__ void row_factors(const VerifyParams& p, WalkShared& sh, int row, const RowInfo& r, double T, double& fp,
+                                            double& fq) {
+  fp = fq = 1.0;
+#pragma unroll 1
+  for (int side = 0; side < (DRAFT ? 2 : 1); ++side) {
+    const Side& s = side ? p.d : p.t;
+    if (s.probs) continue;
+    const Dist d = side ? r.q : r.p;
+    const char* const x = s.data + row * s.stride;
+    double sum = 0.0;
+    for (int i = 8 * static_cast<int>(threadIdx.x); i < p.a.V; i += 8 * kVerifyThreads) {
+      float f[8];
+      values_any<DT>(load8_any<DT>(x, s.dt, i, p.a.V), s.dt, i, p.a.V, -__builtin_inff(), f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum = add_exp2((f[k] - d.ref) * scale_of(T), sum, sh.tab);
+    }
+    sum = wave_sum(sum);
+    if ((threadIdx.x & 63) == 0) sh.red[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    sum = (sh.red[0] + sh.red[1]) + (sh.red[2] + sh.red[3]);
+    __syncthreads();
+    (side ? fq : fp) = 1.0 / (sum * d.zinv);
   }
-  sum = wave_sum(sum);
-  if ((threadIdx.x & 63) == 0) sh.red[threadIdx.x >> 6] = sum;
-  __syncthreads();
-  sum = (sh.red[0] + sh.red[1]) + (sh.red[2] + sh.red[3]);
-  __syncthreads();
-  return 1.0 / (sum * w.inv);
 }
 
 // Walks on, all waves of the workgroup alike, until S of cur is needed (true) or no child stays (false).
@@ -733,6 +748,7 @@ __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int 
   const VerifyArgs& a = p.a;
   const int lane = threadIdx.x & 63;
   const bool greedy = !(T > 0.0), drafted = DRAFT && !greedy;
+  const bool sums = !p.t.probs || (drafted && !p.d.probs);  // tests are made with rows' sums
   int largest = greedy ? largest_of(p, lo + w.cur) : -1;
   while (w.next < n) {
     const int w0 = w.next / kWindow * kWindow, w1 = n - w0 < kWindow ? n : w0 + kWindow;
@@ -744,18 +760,33 @@ __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int 
     }
     if (!TREE && !greedy) {
       // A chain: no test depends on another's, so 64 rows at a time (nine rows that stay one by one: 7 us).
-      for (;;) {
+      for (int sure = 0;;) {  // the rows up to `sure` that are near their border have exact numbers
         const int i = w.next + lane;
-        bool row = false, yes = false;
+        bool row = false, yes = false, near = false;
         int x = 0;
         if (i < w1) {
           const RowInfo& f = sh.row[i - w0];
           x = f.token;
           row = f.parent >= 0;
-          yes = row && (drafted ? f.u * f.qx : f.u) < f.px;
+          const double l = drafted ? f.u * f.qx : f.u;
+          yes = row && l < f.px;
+          near = row && i > sure && near_border(l, f.px);
         }
         const uint64_t m = ~__ballot(yes);
         const int run = m ? __builtin_ctzll(m) : 64;
+        const uint64_t open = __ballot(near) & (run < 63 ? (2ull << run) - 1 : ~0ull);
+        if (__builtin_expect(open && sums, 0)) {  // the first of them that the walk comes to
+          sure = w.next + __builtin_ctzll(open);
+          RowInfo& f = sh.row[sure - w0];
+          double fp, fq;
+          row_factors<DRAFT, DT>(p, sh, lo + sure - 1, f, T, fp, fq);
+          if (threadIdx.x == 0) {  // (all waves have read it: row_factors waits for them)
+            f.px *= fp;
+            f.qx *= fq;
+          }
+          __syncthreads();
+          continue;
+        }
         if (writes && threadIdx.x < 64 && lane < run) {
           a.out_tokens[lo + w.kept - 1 + lane] = x;
           a.path[lo + w.kept + lane] = i;
@@ -791,17 +822,22 @@ __device__ __forceinline__ bool walk(const VerifyParams& p, WalkShared& sh, int 
     const RowInfo& row = sh.row[r - w0];
     const int x = row.token;
     // (where siblings have gone S may be as small as the rows' sums are off)
-    const double u = row.u, qx = SUMS ? row.qx * w.fq : row.qx;
-    double px = row.px * w.fp;
+    const double u = row.u;
+    double px = row.px * w.fp, qx = row.qx * w.fq;
     bool yes, taken = false;
     if (greedy) {
       yes = x == largest;
     } else if (drafted) {
+      if (__builtin_expect(sums && w.al == 0.0 && near_border(u * qx, px), 0)) {
+        row_factors<DRAFT, DT>(p, sh, lo + w.cur, row, T, w.fp, w.fq);
+        px = row.px * w.fp;
+        qx = row.qx * w.fq;
+      }
       yes = w.S > 0.0 && u * w.S * qx < px - w.al * qx;  // (nothing left: the difference is rounding)
     } else {
       taken = TREE && w.tried && tried_before(a, sh, lo, n, w.cur, r, x);
-      if (!p.t.probs && w.fp == 1.0 && !taken && __builtin_fabs(u * w.S - px) < kNear * (u * w.al + px)) {
-        w.fp = row_factor<DT>(p.t, lo + w.cur, row.p, T, a.V, sh);
+      if (__builtin_expect(sums && w.fp == 1.0 && !taken && __builtin_fabs(u * w.S - px) < kNear * (u * w.al + px), 0)) {
+        row_factors<DRAFT, DT>(p, sh, lo + w.cur, row, T, w.fp, w.fq);
         px = row.px * w.fp;
         w.S = 1.0 - w.al * w.fp;
       }

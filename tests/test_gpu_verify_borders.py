@@ -61,3 +61,39 @@ def test_little_left_after_fixed_siblings(dt, gone):
             clear += 1
             assert got.kept[b].item() == kept[b], (b, u, S, q)
     assert clear > B // 2
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("tdt,ddt,dkind", [("fp32", "fp32", "logits"), ("bf16", "fp16", "logits"), ("fp32", "bf16", "probabilities"),
+                                           ("bf16", None, "logits")])
+def test_numbers_next_to_the_border_of_their_test(tdt, ddt, dkind, tree):
+    # u is the 32-bit number nearest to p / q (to p without a draft), or a neighbour of it
+    B, V = 1500, 900
+    c = case(70, B, 3, V, tdt, ddt, tree=tree, ragged=False, spread=4.0)
+    c["draft_kind"] = dkind
+    if tree:
+        c["parents"] = np.tile([0, 0, 0], B)
+    p = probabilities(c["target"])[::3]
+    if ddt is None:
+        q = np.ones_like(p)
+    else:
+        if dkind == "probabilities":
+            c["draft"] = torch.softmax(c["draft"].double(), -1).to(DTS[ddt])
+        q = as_f64(c["draft"])[::3] if dkind == "probabilities" else probabilities(c["draft"])[::3]
+    likelier = [np.nonzero((p[b] < q[b]) & (p[b] > 1e-9))[0] for b in range(B)]
+    at = [int(x[b % x.size]) for b, x in enumerate(likelier)]
+    u = np.array([p[b, x] / q[b, x] for b, x in enumerate(at)]).astype(np.float32)
+    u[1::3], u[2::3] = np.nextafter(u[1::3], np.float32(0)), np.nextafter(u[2::3], np.float32(2))
+    c["tokens"][1::3], c["uniforms"][1::3] = at, np.minimum(u, np.float32(1 - 2.0 ** -24))
+    c["uniforms"][2::3] = 1.0 - 2.0 ** -24
+    kept, _, path, _ = reference(c)
+    got = tq.verify(**on_gpu(c))
+    torch.cuda.synchronize()
+    first = got.path.view(B, 3)[:, 1].cpu().numpy() == 1
+    n = 0
+    for b, x in enumerate(at):
+        u = float(c["uniforms"][3 * b + 1])
+        if abs(u * q[b, x] - p[b, x]) > 1e-12 * (u * q[b, x] + p[b, x]):
+            n += 1
+            assert first[b] == (u * q[b, x] < p[b, x]) == (path[3 * b + 1] == 1), (b, u, q[b, x], p[b, x])
+    assert n > B * 0.99
