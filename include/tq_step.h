@@ -124,7 +124,8 @@ enum { TQ_TARGET_PROBS = 1, TQ_DRAFT_PROBS = 2 };
  * children stays (but one that stayed before the value was looked at) and the new token is -1.
  * Tests are as with sums of fp64 exponentials: u S q and p - a q (u S and p) are told apart where they differ by more
  * than about 1e-12 of what they are made of. A border of the cumulative sum of w lies where the definition has it to
- * about 1e-12 of the sum of p + a q. With a draft, sum(w) or S below 1e-12 (both sides probabilities: 1e-14) is nothing
+ * about 1e-12 of the sum of p + a q; where most of p is within 4e-6 of a q, S and the borders are off by 1e-9 of that
+ * sum at most. With a draft, sum(w) or S below 1e-12 (both sides probabilities: 1e-14) is nothing
  * left: no sibling stays, the new token is one of p. Weights below 1e-280 of the row's largest are 0. Deterministic.
  * Workspace: tq_verify_workspace bytes, 256-byte aligned; its contents need not be kept, and two calls
  * that can run at the same time need one each. vocab in [1, 2^28], B at most 65536, M at most 2^24;

@@ -61,24 +61,50 @@ struct Side {  // target or draft
   const StatPart* stat;  // [rows][parts]
 };
 
+// A token may be on the wrong side of p = a q where a q is this close to p by the rows' fp32 sums (if these are off by
+// more, all are), and what is summed over such tokens may be off by so much of the sum of p + a q.
+constexpr double kClose = 0x1p-18, kBorder = 1e-9;
+
 // What w is summed from. Let p~ = p P, q~ = q Q be a row's values with their own sums P, Q (2^((x - ref) c) of
 // logits; probabilities as they are, P = Q = 1), and rho = a P / Q by the rows' sums of k_verify_stats, which is
 // right to 1e-6. (p - a q)+ is summed over the tokens with p~ > rho q~ instead of p > a q: the ones on the
 // other side add 1e-6 of themselves. So one pass gives all:
 //     p = sum of p~, q = sum of q~ over those tokens, and P, Q:   sum w = p / P - a q / Q.
+// Two rows that are alike nearly everywhere may have most of p on the other side. So tokens that may be there are seen
+// (add gives true), and their p is summed: with how far rho was off, known with P and Q, it says whether the pass
+// has to be made again.
 struct Sums {
   double p, q, P, Q;
-  __device__ __forceinline__ void add(const double (&pv)[8], const double (&qv)[8], double rho) {
+  __device__ __forceinline__ bool add(const double (&pv)[8], const double (&qv)[8], double rho) {
+    bool close = false;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const double in = __builtin_fma(-rho, qv[k], pv[k]) <= 0.0 ? 0.0 : 1.0;  // (NaN goes in)
+      const double d = __builtin_fma(-rho, qv[k], pv[k]);
+      const double in = d <= 0.0 ? 0.0 : 1.0;  // (NaN goes in)
+      close |= __builtin_fabs(d) < __builtin_fma(kClose, pv[k], -1e-200);  // (masked tokens, p~ of 1e-301, do not count)
       p = __builtin_fma(in, pv[k], p);
       q = __builtin_fma(in, qv[k], q);
       P += pv[k];
       Q += qv[k];
     }
+    return close;
   }
 };
+__device__ __forceinline__ double close_to_border(const double (&pv)[8], const double (&qv)[8], double rho) {
+  double s = 0.0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s += __builtin_fabs(__builtin_fma(-rho, qv[k], pv[k])) < kClose * pv[k] ? pv[k] : 0.0;
+  return s;
+}
+// Whether too much may be on the wrong side (close to the border, in 2^-30), or rho is off by more than that counts; rp,
+// rq: 1 / P and 1 / Q.
+__device__ __forceinline__ bool border_open(double rho, double al, double rp, double rq, uint64_t close) {
+  const double off = __builtin_fabs(rho * rp - al * rq), whole = al * rq;
+  return off * (static_cast<double>(close) * 0x1p-30 + kBorder / kClose) > kBorder * whole;
+}
+// A sequence's ticket: workgroups that have come in the upper bits, what they have close to the border in the lower
+// (whole numbers: their sum does not depend on the order).
+constexpr uint64_t kArrival = 1ull << 52;
 
 // A walk that has come to a row.
 struct Walk {
@@ -111,7 +137,7 @@ struct VerifyParams {
   int shares, share_blocks;  // the same of k_verify_pick's workgroups
   double* sums;            // [B][blocks][2]: Sums::p and Sums::q of a block
   Sums* totals;            // [B][shares * waves]: P and Q; p and q where S is summed
-  int* tickets;            // [kPasses][B]
+  uint64_t* tickets;       // [kPasses][B]
   Pending* pending;        // [B], and
   RowInfo* rows;           // [M], of trees with a draft
 };
@@ -205,7 +231,8 @@ __device__ __forceinline__ void values_any(const Raw8& r, int dt, int i, int V, 
 }
 
 // 2^(i / 256), the upper word less i << 12: adding j << 12 for any j = 256 k + i leaves 2^(j / 256).
-__device__ __forceinline__ void fill_table(double* tab) {
+__device__ __forceinline__ void fill_table(double* tab, uint64_t* close) {
+  if (threadIdx.x == 0) *close = 0;
   for (int i = threadIdx.x; i < kTable; i += blockDim.x) {
     const double x = exp2(i * (1.0 / kTable));
     tab[i] = __hiloint2double(__double2hiint(x) - (i << 12), __double2loint(x));
@@ -652,6 +679,7 @@ __device__ __forceinline__ void values8(const Side& s, const WeightSide& w, cons
 struct WalkShared {
   RowInfo row[kWindow];
   double tab[kTable], red[4 * 16];
+  uint64_t close;
   int pick[32];
 };
 
@@ -996,7 +1024,8 @@ template <bool TREE, bool DRAFT, int DT>
 __global__ __launch_bounds__(kVerifyThreads, TREE && DRAFT ? 2 : 3) void k_verify_pick(VerifyParams p, int pass, int passes) {
   constexpr bool SUMS = TREE && DRAFT;
   __shared__ WalkShared sh;
-  __shared__ int s_gone[kGone], s_last;
+  __shared__ int s_gone[kGone];
+  __shared__ uint64_t s_ticket;
   const VerifyArgs& a = p.a;
   const int b = blockIdx.x / p.shares, share = blockIdx.x - b * p.shares;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1009,7 +1038,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREE && DRAFT ? 2 : 3) void k_verif
   int lo, hi;
   const float temperature = a.temperature ? a.temperature[b] : 1.f;
   seq_rows(a, b, lo, hi);
-  fill_table(sh.tab);  // (while these are on their way)
+  fill_table(sh.tab, &sh.close);  // (while these are on their way)
   const int n = hi - lo;
   if (n == 0) {
     if (writes && threadIdx.x == 0) {
@@ -1126,6 +1155,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREE && DRAFT ? 2 : 3) void k_verif
     for (int block = k0 + wave; block < k1; block += kVerifyThreads / 64) {
       const int i = block * kBlockElems + 8 * lane;
       s.p = s.q = 0.0;
+      bool close = false;
 #pragma unroll
       for (int e = 0; e < 8; ++e) pv[e] = qv[e] = 0.0;
       if (i < a.V) {
@@ -1143,13 +1173,17 @@ __global__ __launch_bounds__(kVerifyThreads, TREE && DRAFT ? 2 : 3) void k_verif
         }
         if (f.at >= 0) break;
         if (drafted) {
-          s.add(pv, qv, rho);
+          close = s.add(pv, qv, rho);
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) s.p += pv[e] < 0.0 ? 0.0 : pv[e];
         }
       }
       if (f.at >= 0) break;
+      if (DRAFT && __builtin_expect(__ballot(close) != 0, 0)) {
+        const double x = __builtin_fmin(wave_sum(close_to_border(pv, qv, rho)) * w.p.inv, 1.0);
+        if (lane == 0) __hip_atomic_fetch_add(&sh.close, static_cast<uint64_t>(x * 0x1p30) + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+      }
       if (SUMS && st.state == kLeft) {
         all.p += s.p;
         all.q += s.q;
@@ -1183,9 +1217,13 @@ __global__ __launch_bounds__(kVerifyThreads, TREE && DRAFT ? 2 : 3) void k_verif
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (!alone) {
-      if (threadIdx.x == 0) s_last = __hip_atomic_fetch_add(p.tickets + pass * a.B + b, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (threadIdx.x == 0) {
+        const uint64_t mine = kArrival + (DRAFT ? sh.close : 0);
+        s_ticket = mine + __hip_atomic_fetch_add(p.tickets + pass * a.B + b, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (DRAFT) sh.close = s_ticket & (kArrival - 1);
+      }
       __syncthreads();
-      if (s_last != p.shares - 1) return;
+      if (s_ticket / kArrival != static_cast<uint32_t>(p.shares)) return;
       alone = writes = true;
       k0 = 0;
       k1 = blocks;
@@ -1199,12 +1237,15 @@ __global__ __launch_bounds__(kVerifyThreads, TREE && DRAFT ? 2 : 3) void k_verif
         t.P += shared_load(&totals[k].P);
         t.Q += shared_load(&totals[k].Q);
       }
+      const uint64_t close = sh.close;
       __syncthreads();  // (they may be written again)
+      if (threadIdx.x == 0) sh.close = 0;
       t = Sums{wave_sum(t.p), wave_sum(t.q), wave_sum(t.P), wave_sum(t.Q)};
       if (!p.t.probs) st.w.fp = 1.0 / (t.P * w.p.inv);
       if (!p.d.probs) st.w.fq = 1.0 / (t.Q * w.q.inv);
       const double left = (p.t.probs ? t.p : t.p / t.P) - al * (p.d.probs ? t.q : t.q / t.Q);
-      if (left < kAgain && !exact) {
+      __syncthreads();
+      if (!exact && (left < kAgain || border_open(rho, al, st.w.fp * w.p.inv, st.w.fq * w.q.inv, close))) {
         exact = true;
         rho = al * ((w.q.inv * st.w.fq) / (w.p.inv * st.w.fp));
         continue;
@@ -1214,7 +1255,7 @@ __global__ __launch_bounds__(kVerifyThreads, TREE && DRAFT ? 2 : 3) void k_verif
       continue;
     }
     f = locate<DRAFT>(sh, sums, blocks, totals, ntotals, drafted, !p.t.probs, !p.d.probs, al, u);
-    if (DRAFT && drafted && f.total < kAgain && !exact) {
+    if (DRAFT && drafted && !exact && (f.total < kAgain || border_open(rho, al, f.rp, f.rq, sh.close))) {
       exact = true;
       rho = al * (f.rq / f.rp);
       f.at = -1;
@@ -1297,7 +1338,7 @@ VerifyLayout layout(int V, int B, int M, bool tprobs, bool drafted, bool dprobs)
   l.rows = at;
   at += drafted ? static_cast<size_t>(M) * sizeof(RowInfo) : 0;
   l.tickets = at;
-  at += static_cast<size_t>(B) * kPasses * sizeof(int);
+  at += static_cast<size_t>(B) * kPasses * sizeof(uint64_t);
   l.bytes = M > 0 && B > 0 ? at : 0;
   return l;
 }
@@ -1320,7 +1361,7 @@ hipError_t launch_verify(const VerifyArgs& a, hipStream_t s) {
   p.parts = l.parts; p.part_blocks = l.part_blocks; p.shares = l.shares; p.share_blocks = l.share_blocks;
   p.sums = reinterpret_cast<double*>(ws + l.sums);
   p.totals = reinterpret_cast<Sums*>(ws + l.totals);
-  p.tickets = reinterpret_cast<int*>(ws + l.tickets);
+  p.tickets = reinterpret_cast<uint64_t*>(ws + l.tickets);
   p.pending = reinterpret_cast<Pending*>(ws + l.pending);
   p.rows = reinterpret_cast<RowInfo*>(ws + l.rows);
   if (a.M > 0) {

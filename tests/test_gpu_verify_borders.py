@@ -97,3 +97,43 @@ def test_numbers_next_to_the_border_of_their_test(tdt, ddt, dkind, tree):
             n += 1
             assert first[b] == (u * q[b, x] < p[b, x]) == (path[3 * b + 1] == 1), (b, u, q[b, x], p[b, x])
     assert n > B * 0.99
+
+
+@pytest.mark.parametrize("parents", [None, [0, 0]])
+def test_rows_that_differ_in_two_tokens(parents):
+    # p and q are alike but for a token that p likes more and one that it likes less, by as much but for 1e-9 to 1e-6
+    # of the whole: the many tokens in between have w = p - q of that much each if p has the smaller sum, else none,
+    # and the new token's number points into the middle of them. A border is right to 1e-9 of the sum of p + q = 2, so
+    # to 2e-9 / S here where p and q are this close throughout: the number has to be further away from every border.
+    B, V, n = 4096, 1100, 2
+    g = np.random.default_rng(90)
+    x = (np.round(g.standard_normal((B, V)) * 2048) / 1024 - 6.0).astype(np.float32)
+    x[:, :512] -= 30.0             # (what the rows' sums are relative to: the sums are off by some 1e-7)
+    x[:, 600:1024] -= 30.0
+    x[:, V - 1] = np.log(0.02 * np.exp(x[:, :V - 2].astype(np.float64)).sum(1))
+    x[:, V - 2], wanted = -7.0, 10.0 ** g.uniform(-8.5, -6, B)
+    y = x + np.float32(5.25)       # (exactly so: the same distribution, of other numbers)
+    y[:, V - 1] -= 1.0
+    # q's sum above p's by `wanted` of it
+    e = lambda z: np.exp(z.astype(np.float64))  # noqa: E731
+    P = e(x).sum(1)
+    y[:, V - 2] = np.log(e(x[:, V - 2]) + e(x[:, V - 1]) - e(y[:, V - 1] - 5.25) + wanted * P) + 5.25
+    p, q = e(x) / P[:, None], e(y) / e(y).sum(1)[:, None]
+    w = np.maximum(p - q, 0.0)
+    c = np.cumsum(w, 1)
+    # halfway to the last token, into the middle of the place of some token before it
+    far = np.argsort(-w[:, :V - 1], 1)[np.arange(B), np.arange(B) % 5]
+    far[(w[np.arange(B), far] == 0.0)] = V - 1
+    u = ((c - 0.5 * w)[np.arange(B), far] / c[:, -1]).astype(np.float32)
+    clear = 0.4 * w[np.arange(B), far] / c[:, -1] > 2e-9 / c[:, -1] + 2.0 ** -24 * u
+    assert clear.sum() > B // 4 and (far[clear] != V - 1).sum() > B // 5
+    rep = lambda z: torch.from_numpy(np.repeat(z, n, 0)).cuda()  # noqa: E731
+    tokens, uniforms = np.full((B, n), V - 2), np.ones((B, n), np.float32)     # (the token of which q has more: turned away)
+    uniforms[:, 0] = u
+    got = tq.verify(rep(x), torch.from_numpy(tokens.ravel()).cuda(), torch.from_numpy(uniforms.ravel()).cuda(),
+                    torch.arange(0, B * n + 1, n, device="cuda"), draft=rep(y),
+                    parents=None if parents is None else torch.tensor(parents * B, device="cuda"))
+    new = got.tokens.view(B, n)[:, 0].cpu().numpy()
+    assert got.kept.tolist() == [1] * B
+    wrong = (new != far) & clear
+    assert not wrong.any(), (int(wrong.sum()), np.nonzero(wrong)[0][:5], wanted[wrong][:5])
