@@ -9,7 +9,7 @@
  *     tq_kv_keep    -> rows of the accepted branch together, new lengths, unused pages given back
  *
  * so one step can be captured into a graph and replayed. The entry points follow the conventions of
- * tq.h. Outputs may not overlap inputs or each other but where it is said.
+ * tq.h. Outputs may not overlap inputs or each other but where it is said (TQ_ERR_ARG).
  */
 #ifndef TQ_STEP_H
 #define TQ_STEP_H

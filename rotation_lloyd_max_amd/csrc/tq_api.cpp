@@ -1017,6 +1017,37 @@ int check_pool(const tq_kv_pool* pool, int32_t page_tokens, int32_t B, int32_t t
   return TQ_OK;
 }
 
+// Memory of a call: `rows` pieces of `bytes`, `stride` bytes apart.
+struct Piece {
+  const char* name;
+  const void* at;
+  int64_t bytes, rows = 1, stride = 0;
+};
+// Whether [lo, hi) shares a byte with p. Addresses are compared as numbers.
+bool meets(int64_t lo, int64_t hi, const Piece& p) {
+  const int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(p.at));
+  if (!p.at || p.bytes <= 0 || p.rows <= 0 || lo >= hi) return false;
+  if (p.rows > 1 && p.stride >= p.bytes) {  // the last row that begins before hi
+    if (at >= hi) return false;
+    const int64_t r = (hi - 1 - at) / p.stride, last = r < p.rows ? r : p.rows - 1;
+    return lo < at + last * p.stride + p.bytes;
+  }
+  const int64_t all = (p.rows - 1) * p.stride;
+  return lo < at + (all > 0 ? all : 0) + p.bytes && hi > at + (all < 0 ? all : 0);
+}
+// Refuses outputs (one piece each) that meet an input or each other.
+int check_apart(std::initializer_list<Piece> outputs, std::initializer_list<Piece> inputs) {
+  for (const Piece* o = outputs.begin(); o != outputs.end(); ++o) {
+    const int64_t lo = static_cast<int64_t>(reinterpret_cast<uintptr_t>(o->at)), hi = lo + o->bytes;
+    if (!o->at || o->bytes <= 0) continue;
+    for (const Piece& i : inputs)
+      if (meets(lo, hi, i)) return fail(TQ_ERR_ARG, "%s and %s overlap", o->name, i.name);
+    for (const Piece* p = o + 1; p != outputs.end(); ++p)
+      if (meets(lo, hi, *p)) return fail(TQ_ERR_ARG, "%s and %s overlap", o->name, p->name);
+  }
+  return TQ_OK;
+}
+
 bool all_aligned4(std::initializer_list<const void*> ps) {
   for (const void* p : ps)
     if (p && !aligned(p, 4)) return false;
@@ -1029,7 +1060,7 @@ int tq_kv_plan(const tq_kv_pool* pool, int32_t page_tokens, int32_t B, const int
                const int32_t* parents, const int32_t* shift, int64_t* slots, int32_t* positions,
                int32_t* q_offsets, int32_t* kv_lens, int32_t* status, uint32_t* tree,
                int32_t tree_words, int32_t* left, void* stream) {
-  const int rc = check_pool(pool, page_tokens, B, table_width);
+  int rc = check_pool(pool, page_tokens, B, table_width);
   if (rc != TQ_OK) return rc;
   if (M < 0 || M > (1 << 24)) return fail(TQ_ERR_ARG, "M must be in [0, 2^24]");
   if (tree ? tree_words < 1 || tree_words > 65536 : tree_words != 0)
@@ -1040,6 +1071,14 @@ int tq_kv_plan(const tq_kv_pool* pool, int32_t page_tokens, int32_t B, const int
   if (!aligned(slots, 8) || !all_aligned4({lens, counts, page_table, parents, shift, positions, q_offsets,
                                            kv_lens, status, tree, left}))
     return fail(TQ_ERR_ALIGN, "slots must be 8-byte, the other arrays 4-byte aligned");
+  const int64_t per = 4 * static_cast<int64_t>(B), table_bytes = per * table_width;
+  rc = check_apart({{"page_table", page_table, table_bytes}, {"slots", slots, 8 * M}, {"positions", positions, 4 * M},
+                    {"q_offsets", q_offsets, per + 4}, {"kv_lens", kv_lens, per}, {"status", status, per},
+                    {"tree", tree, 4 * M * tree_words}, {"left", left == pool->state ? nullptr : left, 4},
+                    {"the pool's state", pool->state, 8}},
+                   {{"lens", lens, per}, {"counts", counts, per}, {"parents", parents, 4 * M}, {"shift", shift, per},
+                    {"the pool's free_pages", pool->free_pages, 4 * static_cast<int64_t>(pool->pages)}});
+  if (rc != TQ_OK) return rc;
   PlanArgs a{};
   a.free_pages = pool->free_pages; a.state = pool->state; a.pages = pool->pages; a.page = page_tokens;
   a.B = B; a.lens = lens; a.counts = counts; a.table = page_table; a.width = table_width;
@@ -1069,6 +1108,18 @@ int tq_kv_keep(const tq_kv_pool* pool, const tq_kv_cache* cache, int32_t page_to
     return fail(TQ_ERR_ARG, "lens, kept, page_table and lens_out must be non-NULL");
   if (!all_aligned4({lens, q_offsets, status, kept, path, page_table, lens_out, left}))
     return fail(TQ_ERR_ALIGN, "the arrays must be 4-byte aligned");
+  const int64_t per = 4 * static_cast<int64_t>(B), cache_rows = path ? a.c.pages * a.c.heads * a.c.page : 0;
+  const auto codes = [&](const KvHalf& h) { return cache_rows * h.wpr * 4; };
+  const auto scales = [&](const KvHalf& h) { return cache_rows * (a.c.D / (path ? h.group : 1)) * 2; };
+  rc = check_apart({{"lens_out", lens_out, per}, {"left", left == pool->state ? nullptr : left, 4},
+                    {"the pool's free_pages", pool->free_pages, 4 * static_cast<int64_t>(pool->pages)},
+                    {"the pool's state", pool->state, 8}, {"the cache's key codes", a.c.k.codes, codes(a.c.k)},
+                    {"the cache's key scales", a.c.k.scales, scales(a.c.k)},
+                    {"the cache's value codes", a.c.v.codes, codes(a.c.v)},
+                    {"the cache's value scales", a.c.v.scales, scales(a.c.v)}},
+                   {{"lens", lens_out == lens ? nullptr : lens, per}, {"q_offsets", q_offsets, per + 4}, {"status", status, per},
+                    {"kept", kept, per}, {"path", path, 4 * M}, {"page_table", page_table, per * table_width}});
+  if (rc != TQ_OK) return rc;
   a.free_pages = pool->free_pages; a.state = pool->state; a.pages = pool->pages; a.page = page_tokens;
   a.B = B; a.lens = lens; a.q_offsets = q_offsets; a.status = status; a.kept = kept; a.path = path;
   a.M = path ? static_cast<int>(M) : 0x7fffffff;
@@ -1102,7 +1153,7 @@ int tq_verify(const void* target, tq_dtype target_dtype, int64_t target_stride, 
               const int32_t* offsets, int64_t M, const int32_t* tokens, const int32_t* parents,
               const float* uniforms, const float* temperature, int32_t* kept, int32_t* out_tokens,
               int32_t* path, void* ws, size_t ws_bytes, void* stream) {
-  const int rc = check_verify(vocab, B, M, flags);
+  int rc = check_verify(vocab, B, M, flags);
   if (rc != TQ_OK) return rc;
   if (!valid_dtype(target_dtype) || (draft && !valid_dtype(draft_dtype))) return fail(TQ_ERR_ARG, "bad dtype");
   if (B == 0) return TQ_OK;
@@ -1124,6 +1175,13 @@ int tq_verify(const void* target, tq_dtype target_dtype, int64_t target_stride, 
   if (need > 0 && (!ws || ws_bytes < need))
     return fail(TQ_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", need, ws_bytes);
   if (need > 0 && !aligned(ws, 256)) return fail(TQ_ERR_ALIGN, "workspace must be 256-byte aligned");
+  const int64_t per = 4 * static_cast<int64_t>(B), tsize = dtype_size(target_dtype), dsize = draft ? dtype_size(draft_dtype) : 0;
+  rc = check_apart({{"kept", kept, per}, {"out_tokens", out_tokens, 4 * M}, {"path", path, 4 * M},
+                    {"the workspace", ws, static_cast<int64_t>(need)}},
+                   {{"target", target, vocab * tsize, M, target_stride * tsize}, {"draft", draft, vocab * dsize, M, draft_stride * dsize},
+                    {"offsets", offsets, per + 4}, {"tokens", tokens, 4 * M}, {"parents", parents, 4 * M},
+                    {"uniforms", uniforms, 4 * M}, {"temperature", temperature, per}});
+  if (rc != TQ_OK) return rc;
   return hip_status(launch_verify(a, static_cast<hipStream_t>(stream)), "tq_verify");
 }
 
