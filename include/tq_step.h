@@ -44,7 +44,9 @@ enum {
  * behind a sequence that was refused for lack of pages is refused too.
  *   page_table   device int32 [B][table_width], entries of held pages read, of new pages written
  *   parents      device int32 [M], or NULL for chains: row i of a sequence follows its row parents[i]
- *                (in [0, i); another value ends the walk to the root there). Row 0 is the root.
+ *                (in [0, i); another value ends the walk to the root there). Row 0 is the root. Prompts among
+ *                trees are chains of parents; a tree of thousands of rows that does not begin as a chain is made by
+ *                one workgroup from there on (0.1 ms for 4000 rows, 0.6 with their masks)
  *   shift        device int32 [B] or NULL: added to the positions
  * Outputs, device:
  *   slots        int64 [M]   page * page_tokens + place; -1 for rows of refused sequences, rows behind

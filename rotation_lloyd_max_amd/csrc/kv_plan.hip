@@ -32,6 +32,7 @@ constexpr int kStepThreads = 256;
 constexpr int kStepPer = 4;                           // sequences of a thread
 constexpr int kStepTile = kStepThreads * kStepPer;    // sequences in LDS
 constexpr int kStepParents = 2048;                    // parents in LDS
+constexpr uint32_t kStepLong = 256;                   // rows of a tree that are still walked one by one
 constexpr uint32_t kStepCap = (1u << 30) + 1;         // sums stop here, above every limit
 
 __device__ __forceinline__ uint32_t step_add(uint32_t a, uint32_t b) {
@@ -100,6 +101,125 @@ __device__ __forceinline__ bool step_last(int32_t* state, int& shared) {
   return shared == static_cast<int>(gridDim.x) - 1;
 }
 
+// Trees of more than kStepLong rows, whose walks to the root would be as long (time grew with the square of the
+// length). Their first rows, as far as they are a chain, which prompts among trees are throughout, are known without a
+// walk: every workgroup looks how far that is, up to its own rows. The rows behind are made by one workgroup of the
+// sequence, 256 at a time: a row's steps and mask within these by doubling the way to its ancestors, 8 times at most, and
+// the rest from its first ancestor before, which is done. 191 trees of 24 rows and a prompt of 4000, masks of 125 words:
+// 49 us (830 walked); a tree of 4000 rows that each follow the last but one instead, without masks 111 (320), with them
+// 574 (429: the words, 2 MB, are copied by one workgroup).
+struct LongShared {
+  int ptr[kStepThreads], anc[kStepThreads];  // the ancestor 2^k steps up within the 256, -1: none; the first before them, -1: none
+  uint32_t depth[kStepThreads];              // steps to it, or to the root
+  uint32_t mask[kStepThreads][kStepThreads / 32];
+};
+
+// Bits 0 .. last of a mask, word k.
+__device__ __forceinline__ uint32_t step_ones(int64_t last, int k) {
+  return last >= 32ll * k + 31 ? ~0u : last >= 32ll * k ? (2u << (last - 32ll * k)) - 1 : 0;
+}
+
+// The first row in [1, n) that does not follow the one before it; n if there is none. parents: of the sequence.
+__device__ __forceinline__ uint32_t step_chain(const int32_t* parents, uint32_t n, uint32_t& shared) {
+  constexpr uint32_t U = 8;
+  if (threadIdx.x == 0) shared = n;
+  __syncthreads();
+  for (uint32_t t = 1; t < n; t += U * kStepThreads) {
+    uint32_t first = n;
+#pragma unroll
+    for (int u = U - 1; u >= 0; --u) {
+      const uint32_t a = t + u * kStepThreads + threadIdx.x;
+      if (a < n && parents[a] != static_cast<int>(a - 1)) first = a;
+    }
+    if (__syncthreads_or(first < n)) {
+      if (first < n) atomicMin(&shared, first);
+      break;
+    }
+  }
+  __syncthreads();
+  const uint32_t e = shared;
+  __syncthreads();
+  return e;
+}
+
+// Depths and masks of rows e .. n of a sequence whose rows before e are a chain. put(a, depth): slot and position;
+// depth_of(a): of a row before, from its position. tree: of the sequence, null without masks.
+template <class Put, class Depth>
+__device__ __forceinline__ void step_long(const int32_t* parents, uint32_t n, uint32_t e, uint32_t* tree, int words, LongShared& sh,
+                                          Put put, Depth depth_of) {
+  constexpr int W = kStepThreads / 32, U = 4;
+  const int l = threadIdx.x;
+  for (uint32_t t = e & ~(kStepThreads - 1u); t < n; t += kStepThreads) {
+    const uint32_t a = t + l;
+    int ptr = -1, anc = -1;
+    uint32_t depth = 0, mask[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) mask[k] = (l >> 5) == k ? 1u << (l & 31) : 0;
+    if (a < e) {
+      depth = a;
+      anc = static_cast<int>(t) - 1;
+#pragma unroll
+      for (int k = 0; k < W; ++k) mask[k] = step_ones(l, k);
+    } else if (a < n && a > 0) {
+      const int up = parents[a];
+      if (up >= 0 && static_cast<uint32_t>(up) < a) {
+        if (static_cast<uint32_t>(up) >= t) {
+          ptr = up - static_cast<int>(t);
+          depth = 1;
+        } else {
+          anc = up;
+          depth = 1 + (static_cast<uint32_t>(up) < e ? up : depth_of(up));
+        }
+      }
+    }
+    auto share = [&]() {
+      sh.ptr[l] = ptr;
+      sh.anc[l] = anc;
+      sh.depth[l] = depth;
+#pragma unroll
+      for (int k = 0; k < W; ++k) sh.mask[l][k] = mask[k];
+    };
+    share();
+    while (__syncthreads_or(ptr >= 0)) {
+      if (ptr >= 0) {
+        depth += sh.depth[ptr];
+        anc = sh.anc[ptr];
+#pragma unroll
+        for (int k = 0; k < W; ++k) mask[k] |= sh.mask[ptr][k];
+        ptr = sh.ptr[ptr];
+      }
+      __syncthreads();
+      share();
+    }
+    __syncthreads();
+    if (a >= e && a < n) put(a, depth);
+    // the masks, words next to each other by threads next to each other
+    const uint32_t skip = e > t ? e - t : 0, rows = n - t < kStepThreads ? n - t : kStepThreads, base = t >> 5;
+    for (uint32_t x0 = skip * words + l; x0 < rows * words; x0 += U * kStepThreads) {
+      uint32_t v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t x = x0 + u * kStepThreads, row = x / words, k = x - row * words;
+        v[u] = 0;
+        if (row >= rows) continue;
+        if (k >= base) {
+          if (k < base + W) v[u] = sh.mask[row][k - base];
+        } else if (const int up = sh.anc[row]; up >= 0) {
+          v[u] = static_cast<uint32_t>(up) < e ? step_ones(up, k) : tree[static_cast<int64_t>(up) * words + k];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t x = x0 + u * kStepThreads;
+        if (x < rows * words) tree[static_cast<int64_t>(t) * words + x] = v[u];
+      }
+    }
+    __syncthreads();  // (what these rows got is read by the next)
+  }
+}
+
+// TREE: with parents. LONG: more rows than kStepLong, so a tree may be that long.
+template <bool TREE, bool LONG>
 __global__ __launch_bounds__(kStepThreads) void k_kv_plan(PlanArgs p, int rows_each) {
   __shared__ uint32_t s_row[kStepTile + 1], s_new[kStepTile + 1];
   __shared__ int s_len[kStepTile];  // -1: refused
@@ -107,12 +227,20 @@ __global__ __launch_bounds__(kStepThreads) void k_kv_plan(PlanArgs p, int rows_e
   __shared__ uint32_t s_wave[2][kStepThreads / 64];
   __shared__ uint32_t s_granted;
   __shared__ int s_arrived;
+  __shared__ int s_long;  // there are trees of more than kStepLong rows
+  __shared__ uint32_t s_chain;
+  __shared__ LongShared s_tile;
   const uint32_t page = p.page, M = p.M, free_count = step_free(p.state, p.pages);
   const uint32_t cap = page * static_cast<uint32_t>(p.width);
   const uint32_t lo_row = blockIdx.x * rows_each;
   const uint32_t hi_row = lo_row + rows_each < M ? lo_row + rows_each : M;
   uint32_t row0 = 0, new0 = 0, granted = 0;
   if (threadIdx.x == 0) s_granted = 0;
+  if (LONG && threadIdx.x == 0) s_long = 0;
+  // the parents of its rows and of those before, as many as fit, while the lengths are on their way
+  const uint32_t first = hi_row > kStepParents ? hi_row - kStepParents : 0;
+  if (TREE)
+    for (uint32_t r = first + threadIdx.x; r < hi_row; r += kStepThreads) s_parent[r - first] = p.parents[r];
   for (int b0 = 0; b0 < p.B; b0 += kStepTile) {
     const int nb = p.B - b0 < kStepTile ? p.B - b0 : kStepTile;
     uint32_t n[kStepPer], c[kStepPer], w[kStepPer], rows = 0, fresh = 0;
@@ -142,6 +270,7 @@ __global__ __launch_bounds__(kStepThreads) void k_kv_plan(PlanArgs p, int rows_e
         s_new[i] = fresh;
         s_len[i] = status == 0 ? static_cast<int>(n[k]) : -1;
         if (status == 0 && w[k]) granted = last;
+        if (LONG && status == 0 && c[k] > kStepLong) s_long = 1;
         if ((b0 / kStepTile) % gridDim.x == blockIdx.x) {
           p.q_offsets[b0 + i] = rows < M ? rows : M;
           p.kv_lens[b0 + i] = status == 0 ? n[k] + c[k] : 0;
@@ -168,33 +297,37 @@ __global__ __launch_bounds__(kStepThreads) void k_kv_plan(PlanArgs p, int rows_e
     }
     // rows
     const uint32_t lo = s_row[0] < lo_row ? lo_row : s_row[0], hi = s_row[nb] < hi_row ? s_row[nb] : hi_row;
-    uint32_t first = 0;
-    bool near = false;
-    if (p.parents && lo < hi) {  // the parents of these rows' sequences, from the first one's root on
-      first = s_row[step_find(s_row, nb, lo)];
-      near = hi - first <= kStepParents;
-      if (near)
-        for (uint32_t r = first + threadIdx.x; r < hi; r += kStepThreads) s_parent[r - first] = p.parents[r];
-      __syncthreads();
-    }
+    // slot and position of row `own` of sequence i, at `depth`
+    auto put = [&](int i, uint32_t own, uint32_t depth, int number, uint32_t shift) {
+      const uint32_t r = s_row[i] + own, len = s_len[i], token = len + own;
+      p.positions[r] = static_cast<int>(len + depth + shift);
+      p.slots[r] = number >= 0 && number < p.pages ? static_cast<int64_t>(number) * page + token % page : -1;
+    };
+    auto number_of = [&](int i, uint32_t own) {  // of its page
+      const uint32_t len = s_len[i], j = (len + own) / page, held = step_pages(len, page);
+      return j < held ? p.table[static_cast<int64_t>(b0 + i) * p.width + j] : p.free_pages[free_count - 1 - (s_new[i] + (j - held))];
+    };
+    auto shift_of = [&](int i) { return p.shift ? static_cast<uint32_t>(p.shift[b0 + i]) : 0u; };
+    auto is_long = [&](int i) { return s_len[i] >= 0 && s_row[i + 1] - s_row[i] > kStepLong; };
+    const bool longs = LONG && s_long;
     for (uint32_t r = lo + threadIdx.x; r < hi; r += kStepThreads) {
       const int i = step_find(s_row, nb, r), len = s_len[i];
       const uint32_t start = s_row[i], own = r - start;
       uint32_t* mask = p.words ? p.tree + static_cast<int64_t>(r) * p.words : nullptr;
+      if (LONG && __builtin_expect(longs, 0) && is_long(i)) continue;
       if (len < 0) {
         p.slots[r] = -1;
         p.positions[r] = 0;
         for (int k = 0; k < p.words; ++k) mask[k] = 0;
         continue;
       }
-      const uint32_t token = len + own, j = token / page, held = step_pages(len, page);
-      const int64_t at = static_cast<int64_t>(b0 + i) * p.width + j;
-      const int number = j < held ? p.table[at] : p.free_pages[free_count - 1 - (s_new[i] + (j - held))];
-      const uint32_t shift = p.shift ? static_cast<uint32_t>(p.shift[b0 + i]) : 0u;
+      const int number = number_of(i, own);
+      const uint32_t shift = shift_of(i);
       // to the root (while the page's number is on its way): its steps, and a bit for each row on the way (they descend, so a word is done when
       // the next one is below it)
       uint32_t depth = own;
-      if (p.parents) {
+      if (TREE) {
+        const bool near = start >= first;
         depth = 0;
         int k = p.words - 1;
         uint32_t bits = 0;
@@ -218,13 +351,31 @@ __global__ __launch_bounds__(kStepThreads) void k_kv_plan(PlanArgs p, int rows_e
           bits = 0;
         }
       } else {
-        for (int k = 0; k < p.words; ++k) {  // a chain: rows 0 .. own
-          const uint32_t full = own + 1;
-          mask[k] = full >= 32u * (k + 1) ? ~0u : full > 32u * k ? (1u << (full - 32u * k)) - 1 : 0;
-        }
+        for (int k = 0; k < p.words; ++k) mask[k] = step_ones(own, k);  // a chain: rows 0 .. own
       }
-      p.positions[r] = static_cast<int>(len + depth + shift);
-      p.slots[r] = number >= 0 && number < p.pages ? static_cast<int64_t>(number) * page + (token - j * page) : -1;
+      put(i, own, depth, number, shift);
+    }
+    if (LONG && __builtin_expect(longs, 0) && lo < hi) {  // of the trees that are not walked, the rows of this workgroup that begin with a chain
+      for (int i = step_find(s_row, nb, lo); i < nb && s_row[i] < hi; ++i) {
+        if (!is_long(i)) continue;
+        const uint32_t start = s_row[i], end = s_row[i + 1] < hi ? s_row[i + 1] : hi, shift = shift_of(i);
+        const uint32_t e = step_chain(p.parents + start, end - start, s_chain), from = lo > start ? lo - start : 0;
+        for (uint32_t own = from + threadIdx.x; own < e; own += kStepThreads) put(i, own, own, number_of(i, own), shift);
+        const int64_t words = p.words;
+        for (int64_t x = from * words + threadIdx.x; x < e * words; x += kStepThreads)
+          p.tree[start * words + x] = step_ones(x / words, static_cast<int>(x % words));
+      }
+    }
+    if (LONG && __builtin_expect(longs, 0)) {  // and of every one of them that is this workgroup's the rows behind
+      for (int i = 0; i < nb; ++i) {
+        if ((b0 + i) % gridDim.x != blockIdx.x || !is_long(i)) continue;
+        const uint32_t start = s_row[i], n = s_row[i + 1] - start, shift = shift_of(i), base = static_cast<uint32_t>(s_len[i]) + shift;
+        const uint32_t e = step_chain(p.parents + start, n, s_chain);
+        if (e == n) continue;
+        step_long(p.parents + start, n, e, p.words ? p.tree + static_cast<int64_t>(start) * p.words : nullptr, p.words, s_tile,
+                  [&](uint32_t a, uint32_t depth) { put(i, a, depth, number_of(i, a), shift); },
+                  [&](uint32_t a) { return static_cast<uint32_t>(p.positions[start + a]) - base; });
+      }
     }
     __syncthreads();
   }
@@ -385,7 +536,8 @@ hipError_t launch_kv_plan(const PlanArgs& a, hipStream_t s) {
   int blocks = (a.M + kStepThreads - 1) / kStepThreads;
   blocks = blocks < 1 ? 1 : blocks > 256 ? 256 : blocks;
   const int each = (a.M + blocks - 1) / blocks;
-  hipLaunchKernelGGL(k_kv_plan, dim3(blocks), dim3(kStepThreads), 0, s, a, each);
+  const auto plan = !a.parents ? k_kv_plan<false, false> : a.M <= static_cast<int>(kStepLong) ? k_kv_plan<true, false> : k_kv_plan<true, true>;
+  hipLaunchKernelGGL(plan, dim3(blocks), dim3(kStepThreads), 0, s, a, each);
   return hipGetLastError();
 }
 
