@@ -66,7 +66,7 @@ def kv_pool(pages, device="cuda"):
 
 
 class KVPlan(NamedTuple):
-    """A step's tables (see kv_plan)."""
+    """A step's tables (see kv_plan), in one allocation: clone what is kept for long."""
     slots: torch.Tensor
     positions: torch.Tensor
     q_offsets: torch.Tensor
@@ -170,7 +170,8 @@ class Verified(NamedTuple):
     """What verify found: kept [B] rows of each sequence that stay, the root among them; tokens
     [M], from offsets[b] the drafted tokens that stay and the new one (kept[b] in all), -1 behind
     them; path [M], from offsets[b] the rows that stay, -1 behind them. tokens and path behind the
-    last sequence's rows hold anything."""
+    last sequence's rows hold anything. The three share one allocation, up to 64 KiB larger than
+    they are: clone what is kept for long."""
     kept: torch.Tensor
     tokens: torch.Tensor
     path: torch.Tensor
@@ -235,7 +236,7 @@ def verify(target, tokens, uniforms, offsets, draft=None, parents=None, temperat
     if ws is not None and (ws.device != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < nbytes):
         raise ValueError(f"ws= must be a contiguous tensor of at least {nbytes} bytes on {dev}")
     words = 0
-    if ws is None and nbytes <= 1 << 20:     # in one allocation with the outputs (1 us of 16), which keep it
+    if ws is None and nbytes <= 1 << 16:     # in one allocation with the outputs (1 us of 16), which keep it
         words = nbytes >> 2
     elif ws is None:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)

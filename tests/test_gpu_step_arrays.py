@@ -62,3 +62,14 @@ def test_arrays_next_to_each_other_and_between_rows():
     flat = wide.view(-1).view(torch.int32)
     for want, n, r in ((kept, 3, 0), (tokens, M, 5), (path, M, M + 3)):
         assert np.array_equal(flat[128 * r + V:128 * r + V + n].cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("B,rows,vocab", [(1, 4, 32000), (8, 4, 20000), (16, 6, 131072), (64, 2, 131072)])
+def test_what_the_results_of_verify_hold(B, rows, vocab):
+    # programs keep them for many steps: of the workspace they hold 64 KiB at most
+    M = B * rows
+    t = torch.randn((M, vocab), dtype=torch.bfloat16, device="cuda")
+    got = tq.verify(t, torch.zeros(M, dtype=torch.int32, device="cuda"), torch.rand(M, device="cuda"),
+                    torch.arange(0, M + 1, rows, dtype=torch.int32, device="cuda"), draft=t)
+    for x in got:
+        assert x.untyped_storage().nbytes() <= 65536 + 4 * (B + 2 * M)
