@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import rotation_lloyd_max_amd as tq
-from test_gpu_verify import DTS, case, on_gpu, reference
+from test_gpu_verify import CLEAR, DTS, case, on_gpu, reference
 
 pytestmark = pytest.mark.gpu
 CODES = {"fp32": tq.F32, "bf16": tq.BF16, "fp16": tq.F16}
@@ -80,3 +80,19 @@ def test_one_of_several_siblings_probability_is_none(bad, drafted):
         c["uniforms"][1:] = 1.0
         c["uniforms"][4] = 0.0             # the last would stay
         assert answers(c) == (1, -1)
+
+
+@pytest.mark.parametrize("V", [8191, 8192, 16385, 50257])
+@pytest.mark.parametrize("tree,ddt", [(False, "bf16"), (True, "fp16"), (True, None), (False, None)])
+@pytest.mark.parametrize("kind", ["logits", "probabilities"])
+def test_rows_around_the_ends_of_pieces(V, tree, ddt, kind):
+    # every sequence has rows and clear decisions, and all are compared
+    for seed, B, most in ((60, 1, 2), (61, 2, 5), (62, 3, 3)):
+        c = case(seed, B, most, V, "fp32", ddt, kind, tree, ragged=False)
+        assert len(c["tokens"]) == B * most
+        want = reference(c)
+        assert (want[3] > CLEAR).all()
+        got = tq.verify(**on_gpu(c))
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert x.tolist() == y.tolist()
