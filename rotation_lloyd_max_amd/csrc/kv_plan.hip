@@ -19,8 +19,8 @@
 //
 // Bounds and figures. Kilobytes pass (keep's moves aside), so both are bound by a launch and by loads that wait for each
 // other, 0.6 us each: state, lengths, table or list, for trees the parents and then LDS from row to row. In a
-// stream of launches: 16 sequences of one row 5.3 us, 5 prompts of 48,000 rows in all 5.2, 192 trees of 24 rows 9.7 (the
-// page's number is fetched before the way to the root: 9.9 when after); keep 3.6, with 4 rows each of 192 branches
+// stream of launches: 16 sequences of one row 5.3 us, 5 prompts of 48,000 rows in all 5.1, 192 trees of 24 rows 10.0 (the
+// page's number is fetched before the way to the root: 0.2 more when after); keep 3.8, with 4 rows each of 192 branches
 // moved (2.8 MB) 5.5.
 #include "device_common.hpp"
 #include "internal.hpp"

@@ -19,12 +19,13 @@
 // comes last finds the token. Where siblings are tried against a draft, S is such a sum too: the last
 // workgroup walks on with it, and the next launch of k_verify_pick sums what the walk needs then. kPasses - 1 more
 // launches follow, in which sequences that are done end at once; what is still open in the last one its last
-// workgroup sums alone (20 rows of 8 sequences, 60000 tokens: 105 us when the first launch's did so, 52 now).
+// workgroup sums alone (20 rows of 8 sequences, 60000 tokens: 105 us when the first launch's did so, 55 now; each sibling
+// turned away behind the fourth 52 us more, 130 over 131072 tokens).
 //
 // Bounds and figures. 64 sequences of 9 rows, 131072 tokens in bf16, a draft: k_verify_stats reads 285 MB in 54 us,
-// 5.3 TB/s, bound by memory; k_verify_pick, 29 us, reads 64 of these rows again: 5 us for the walk, 1 for the row's
-// constants, 15 for the sums (vector instructions: about 36 for a token of both rows), 5 for the meeting and the last
-// block. One sequence of 4 rows, 32000 tokens: 14.2 us in a stream of launches, 4.6 of them launches and the rows'
+// 5.3 TB/s, bound by memory; k_verify_pick, 30 us, reads 64 of these rows again: 5 us for the walk, 1 for the row's
+// constants, 15 for the sums (8 to 10 of them vector instructions: 32 for a token of both rows, 60 more for 512), 5 for
+// the meeting and the last block. One sequence of 4 rows, 32000 tokens: 14.8 us in a stream of launches, 4.6 of them launches and the rows'
 // sums, about 3 the walk, 3 the sums, 1.5 until the block is found, 1.5 the token: the latency of some ten loads that
 // wait for each other and of fp64 chains in waves that have a SIMD to themselves.
 #include <type_traits>
@@ -739,8 +740,9 @@ __device__ __forceinline__ void fill_window(const VerifyParams& p, WalkShared& s
 }
 
 // 1 / P and 1 / Q of the row that `r` follows by sums of fp64 exponentials, relative to those of k_verify_stats; by all
-// threads of the workgroup. For a test that the rows' fp32 sums cannot decide: one in some 10^4, and where siblings
-// that went have left little of p.
+// threads of the workgroup, in every workgroup of the sequence. For a test that the rows' fp32 sums cannot decide: one
+// in some 10^4 (65 us over 131072 tokens; four loads together instead of one 48, and 0.3 us more where none is made), and
+// where siblings that went have left little of p.
 template <bool DRAFT, int DT>
 __device__ __forceinline__ void row_factors(const VerifyParams& p, WalkShared& sh, int row, const RowInfo& r, double T, double& fp,
                                             double& fq) {
@@ -1018,7 +1020,7 @@ __device__ __forceinline__ Found locate(WalkShared& sh, const double* sums, int 
 // Trees with a draft take several launches. Chains, trees, drafts and the rows' type (DT, as in load_elem; -1: two
 // of them) are told apart at compile time: a wave that has a SIMD to itself pays for every branch and spilled
 // register (one sequence of 4 rows 14.0 us, 14.9 with all of it in one kernel; 8 trees of 24 rows 20.3, 23.6; 64
-// sequences of 9 rows 80.5, 84.5). Trees with a draft want 200 registers: at three waves a SIMD they spilled (8
+// sequences of 9 rows 80.5, 84.5; before tests near their border were made again). Trees with a draft want 200 registers: at three waves a SIMD they spilled (8
 // sequences of 20 rows 61 us a call against 57).
 template <bool TREE, bool DRAFT, int DT>
 __global__ __launch_bounds__(kVerifyThreads, TREE && DRAFT ? 2 : 3) void k_verify_pick(VerifyParams p, int pass, int passes) {
