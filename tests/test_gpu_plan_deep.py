@@ -93,3 +93,30 @@ def test_many_deep_trees():
     table, free = setup(g, lens, 64, 4000, 40)
     t = [shapes(c, g)[("far", "two", "chain")[b % 3]] if c == n else np.zeros(c, int) for b, c in enumerate(counts)]
     check_plan(lens, counts, table, free, int(counts.sum()), 64, 4000, np.concatenate(t).astype(np.int64), 3)
+
+
+def test_deep_trees_captured_and_replayed():
+    # lengths, rows and parents change between the replays
+    B, M, words, page = 6, 5000, 40, 16
+    g = np.random.default_rng(8)
+    pool, table = tq.kv_pool(500), torch.full((B, 400), -1, dtype=torch.int32, device="cuda")
+    z = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    lens, counts, parents, left = z(B), z(B), z(M), z(1)
+    call = lambda: tq.kv_plan(pool, lens, counts, table, M, page, parents=parents, tree_words=words, left=left)  # noqa: E731
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p = call()
+    for turn, (deep, shape) in enumerate(((1300, "far"), (24, "near"), (4000, "chain"), (2000, "two"), (3000, "late"))):
+        n = np.array([5, deep, 0, 24, 300, 9])
+        counts.copy_(dev(n))
+        lens.zero_()
+        parents.zero_()
+        parents[:n.sum()] = dev(np.concatenate([shapes(deep, g)[shape] if x == deep else trees(g, [x]) for x in n]))
+        graph.replay()
+        eager = call()
+        torch.cuda.synchronize()
+        for x, y in zip(p, eager):
+            assert torch.equal(x, y), turn
+        d = depths(parents[5:5 + deep].cpu().numpy())
+        assert np.array_equal(p.positions[5:5 + deep].cpu().numpy(), d) and p.status.tolist() == [0] * B
